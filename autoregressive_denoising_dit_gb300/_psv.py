@@ -29,6 +29,7 @@ PSV_FLAG_LATENCY = 8
 
 PSV_DTYPE_F32 = 0
 PSV_DTYPE_BF16 = 1
+PSV_DTYPE_F16 = 2
 PSV_LOC_HOST = 0
 PSV_LOC_DEVICE = 1
 
@@ -49,9 +50,14 @@ EXPORTS = [
     "psv_set_graphs", "psv_set_profiling", "psv_kernel_times", "psv_debug_tap",
     "psv_debug_read_kv", "psv_attention_scratch_bytes", "psv_attention",
     "psv_attention_noalloc", "psv_attention_noalloc_status", "psv_debug_error_word",
+    "psv_cache_last_error", "psv_rope", "psv_cache_scratch_bytes", "psv_cache_attention",
+    "psv_cache_mass", "psv_cache_evict",
 ]
 
 PSV_ATTN_NOALLOC_SCRATCH_BYTES = 16 << 20
+PSV_CACHE_SCRATCH_HEAD = 256
+PSV_ROPE_PAIRS = 0
+PSV_ROPE_HALVES = 1
 
 
 class ModelDesc(ctypes.Structure):
@@ -82,6 +88,33 @@ class KernelTime(ctypes.Structure):
 
 class AttnProblem(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n", "T", "H", "dh", "L", "k_rows", "vt_cols")]
+
+
+class RopeProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "B", "L", "H", "dh", "n_axes")] + \
+               [("axis_dims", ctypes.c_int32 * 4), ("layout", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("freqs", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3), ("pos_stride", ctypes.c_int64 * 2),
+                ("lens", ctypes.c_void_p)]
+
+
+class CacheProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "B", "Hq", "Hkv", "dh", "Lq", "Lk", "causal")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float)] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "o_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("q_lens", "k_lens", "q_pos", "q_doc")] + \
+               [("q_meta_stride", ctypes.c_int64), ("k_pos", ctypes.c_void_p),
+                ("k_doc", ctypes.c_void_p), ("k_meta_stride", ctypes.c_int64 * 2),
+                ("prefix", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
+
+
+class EvictProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "B", "Hkv", "dh", "L", "budget", "sinks", "recent")] + \
+               [(n, ctypes.c_int64 * 3) for n in ("k_stride", "v_stride", "k_out_stride", "v_out_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("k_lens", "k_pos", "k_doc")] + \
+               [("k_meta_stride", ctypes.c_int64 * 2)] + \
+               [(n, ctypes.c_void_p) for n in ("pos_out", "doc_out", "lens_out")]
 
 
 class PSVError(RuntimeError):
@@ -129,6 +162,12 @@ def lib() -> ctypes.CDLL:
             "psv_attention_noalloc": (i32, [ctypes.POINTER(AttnProblem), vp, vp, vp, vp, vp]),
             "psv_attention_noalloc_status": (i32, [ctypes.POINTER(i32), vp]),
             "psv_debug_error_word": (i32, [vp, ctypes.POINTER(sz)]),
+            "psv_cache_last_error": (ctypes.c_char_p, []),
+            "psv_rope": (i32, [ctypes.POINTER(RopeProblem), vp, vp, vp, vp]),
+            "psv_cache_scratch_bytes": (i32, [ctypes.POINTER(CacheProblem), ctypes.POINTER(sz)]),
+            "psv_cache_attention": (i32, [ctypes.POINTER(CacheProblem), vp, vp, vp, vp, vp, vp, sz, vp]),
+            "psv_cache_mass": (i32, [ctypes.POINTER(CacheProblem), vp, vp, vp, vp, vp, vp, sz, vp]),
+            "psv_cache_evict": (i32, [ctypes.POINTER(EvictProblem), vp, vp, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -353,3 +392,111 @@ def psv_attention_noalloc_status(stream_ptr: int = 0) -> int:
     if r < 0:
         raise PSVError(r, "psv_attention_noalloc_status failed")
     return st.value
+
+
+# ------------------------------------------- operators of a rolling cache
+
+def _strides(given, *shape):
+    """Element strides (batch, row, head) of [B][L][H][dh]: as given, or dense."""
+    if given is None:
+        L, H, dh = shape
+        given = (L * H * dh, H * dh, dh)
+    return (ctypes.c_int64 * 3)(*given)
+
+
+def _cache_check(r: int) -> None:
+    if r < 0:
+        raise PSVError(r, (lib().psv_cache_last_error() or b"").decode())
+
+
+def rope_problem(dtype: int, shape, axis_dims, x_stride=None, out_stride=None, pos_stride=None,
+                 theta: float = 1e4, freqs: np.ndarray | None = None, halves: bool = False,
+                 inverse: bool = False, lens: int = 0) -> RopeProblem:
+    """psv_rope_problem of x [B][L][H][dh]; strides in elements (default: dense),
+    ``freqs`` float64 [sum(axis_dims) / 2], ``lens`` a device pointer."""
+    B, L, H, dh = shape
+    if not 1 <= len(axis_dims) <= 4:
+        raise ValueError("1 to 4 axes")
+    p = RopeProblem(dtype=dtype, B=B, L=L, H=H, dh=dh, n_axes=len(axis_dims),
+                    axis_dims=(ctypes.c_int32 * 4)(*axis_dims),
+                    layout=PSV_ROPE_HALVES if halves else PSV_ROPE_PAIRS, inverse=int(inverse),
+                    theta=theta, x_stride=_strides(x_stride, L, H, dh),
+                    out_stride=_strides(out_stride, L, H, dh), lens=lens or None)
+    p.pos_stride = (ctypes.c_int64 * 2)(*(pos_stride or (L * len(axis_dims), len(axis_dims))))
+    if freqs is not None:
+        f = np.ascontiguousarray(freqs, dtype=np.float64)
+        if f.size != sum(axis_dims) // 2:
+            raise ValueError(f"expected {sum(axis_dims) // 2} frequencies, got {f.size}")
+        p._freqs = f  # keeps the host array alive with the description
+        p.freqs = f.ctypes.data
+    return p
+
+
+def psv_rope(prob: RopeProblem, x_ptr: int, pos_ptr: int, out_ptr: int, stream_ptr: int = 0) -> None:
+    _cache_check(lib().psv_rope(ctypes.byref(prob), x_ptr, pos_ptr, out_ptr, stream_ptr or None))
+
+
+def cache_problem(dtype: int, q_shape, k_shape, q_stride=None, k_stride=None, v_stride=None,
+                  o_stride=None, scale: float = 0.0, softcap: float = 0.0, causal: bool = False,
+                  q_lens: int = 0, k_lens: int = 0, q_pos: int = 0, q_doc: int = 0,
+                  q_meta_stride: int | None = None, k_pos: int = 0, k_doc: int = 0,
+                  k_meta_stride=None, prefix: int = 0, slopes: int = 0) -> CacheProblem:
+    """psv_cache_problem of q [B][Lq][Hq][dh] over a cache [B][Lk][Hkv][dh]; strides in
+    elements (default: dense), lengths, positions, documents, prefixes and slopes as
+    device pointers (0: none)."""
+    B, Lq, Hq, dh = q_shape
+    Bk, Lk, Hkv, dhk = k_shape
+    if Bk != B or dhk != dh:
+        raise ValueError("q and k differ in batch or head width")
+    p = CacheProblem(dtype=dtype, B=B, Hq=Hq, Hkv=Hkv, dh=dh, Lq=Lq, Lk=Lk, causal=int(causal),
+                     scale=scale, softcap=softcap, q_stride=_strides(q_stride, Lq, Hq, dh),
+                     k_stride=_strides(k_stride, Lk, Hkv, dh), v_stride=_strides(v_stride, Lk, Hkv, dh),
+                     o_stride=_strides(o_stride, Lq, Hq, dh), q_lens=q_lens or None,
+                     k_lens=k_lens or None, q_pos=q_pos or None, q_doc=q_doc or None,
+                     k_pos=k_pos or None, k_doc=k_doc or None, prefix=prefix or None,
+                     slopes=slopes or None)
+    p.q_meta_stride = Lq if q_meta_stride is None else q_meta_stride
+    p.k_meta_stride = (ctypes.c_int64 * 2)(*(k_meta_stride or (Hkv * Lk, Lk)))
+    return p
+
+
+def psv_cache_scratch_bytes(prob: CacheProblem) -> int:
+    n = ctypes.c_size_t()
+    _cache_check(lib().psv_cache_scratch_bytes(ctypes.byref(prob), ctypes.byref(n)))
+    return n.value
+
+
+def psv_cache_attention(prob: CacheProblem, q_ptr: int, k_ptr: int, v_ptr: int, o_ptr: int,
+                        lse_ptr: int, scratch_ptr: int, scratch_bytes: int, stream_ptr: int = 0) -> None:
+    _cache_check(lib().psv_cache_attention(ctypes.byref(prob), q_ptr, k_ptr, v_ptr, o_ptr,
+                                           lse_ptr or None, scratch_ptr, scratch_bytes,
+                                           stream_ptr or None))
+
+
+def psv_cache_mass(prob: CacheProblem, q_ptr: int, k_ptr: int, lse_ptr: int, mass_in_ptr: int,
+                   mass_out_ptr: int, scratch_ptr: int, scratch_bytes: int, stream_ptr: int = 0) -> None:
+    _cache_check(lib().psv_cache_mass(ctypes.byref(prob), q_ptr, k_ptr, lse_ptr, mass_in_ptr or None,
+                                      mass_out_ptr, scratch_ptr, scratch_bytes, stream_ptr or None))
+
+
+def evict_problem(dtype: int, shape, budget: int, sinks: int = 0, recent: int = 0, k_stride=None,
+                  v_stride=None, k_out_stride=None, v_out_stride=None, k_lens: int = 0, k_pos: int = 0,
+                  k_doc: int = 0, k_meta_stride=None, pos_out: int = 0, doc_out: int = 0,
+                  lens_out: int = 0) -> EvictProblem:
+    """psv_evict_problem of a cache [B][L][Hkv][dh] cut to ``budget`` rows; strides in
+    elements (default: dense), the rest device pointers (0: none)."""
+    B, L, H, dh = shape
+    p = EvictProblem(dtype=dtype, B=B, Hkv=H, dh=dh, L=L, budget=budget, sinks=sinks, recent=recent,
+                     k_stride=_strides(k_stride, L, H, dh), v_stride=_strides(v_stride, L, H, dh),
+                     k_out_stride=_strides(k_out_stride, budget, H, dh),
+                     v_out_stride=_strides(v_out_stride, budget, H, dh), k_lens=k_lens or None,
+                     k_pos=k_pos or None, k_doc=k_doc or None, pos_out=pos_out or None,
+                     doc_out=doc_out or None, lens_out=lens_out or None)
+    p.k_meta_stride = (ctypes.c_int64 * 2)(*(k_meta_stride or (H * L, L)))
+    return p
+
+
+def psv_cache_evict(prob: EvictProblem, k_ptr: int, v_ptr: int, mass_ptr: int, k_out_ptr: int,
+                    v_out_ptr: int, mass_out_ptr: int, idx_out_ptr: int, stream_ptr: int = 0) -> None:
+    _cache_check(lib().psv_cache_evict(ctypes.byref(prob), k_ptr, v_ptr, mass_ptr, k_out_ptr,
+                                       v_out_ptr, mass_out_ptr, idx_out_ptr, stream_ptr or None))

@@ -1,0 +1,45 @@
+// Internal interface of the rolling-cache operators (public ABI:
+// include/psv.h, "kernel-level operators of a rolling key/value cache").
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace psv {
+
+// Stores `msg` (printf-style) as this thread's last error of the cache calls.
+int cache_fail(int code, const char* fmt, ...);
+
+struct Strides3 {
+  int64_t b, l, h;  // batch, row, head; elements
+};
+
+// psv_cache_problem as the kernels see it, with the tensors of one call.
+struct CacheParams {
+  int B, Hq, Hkv, G, dh, Lq, Lk, causal;
+  float scale, softcap;
+  Strides3 qs, ks, vs, os;
+  const void *q, *k, *v;
+  void* o;
+  float* lse;            // attention: written (or null); mass: read
+  const float* mass_in;  // may be null
+  float* mass_out;
+  const int32_t *q_lens, *k_lens, *q_pos, *q_doc, *k_pos, *k_doc, *prefix;
+  int64_t qm_b, km_b, km_h;
+  const float* slopes;
+  int* err;
+};
+
+__device__ __forceinline__ int cache_k_len(const CacheParams& p, int b) {
+  return p.k_lens ? min(max(p.k_lens[b], 0), p.Lk) : p.Lk;
+}
+__device__ __forceinline__ int cache_q_len(const CacheParams& p, int b) {
+  return p.q_lens ? min(max(p.q_lens[b], 0), p.Lq) : p.Lq;
+}
+
+cudaError_t launch_cache_attention_general(const CacheParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_cache_mass_general(const CacheParams& p, bool bf16, cudaStream_t st);
+
+}  // namespace psv

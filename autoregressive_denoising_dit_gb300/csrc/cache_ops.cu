@@ -1,0 +1,688 @@
+// Entry points of the rolling-cache operators (include/psv.h): argument
+// checks, rotary positions with several axes, and eviction.  The attention
+// over a cache and the attention mass are launched from here.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "../../include/psv.h"
+#include "cache_kernels.h"
+#include "psv_device.cuh"
+#include "psv_kernels.h"
+
+#define PSV_API extern "C" __attribute__((visibility("default")))
+
+namespace psv {
+
+static thread_local char t_cache_error[256];
+
+int cache_fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(t_cache_error, sizeof(t_cache_error), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+}  // namespace psv
+
+using psv::cache_fail;
+using psv::CacheParams;
+using psv::Strides3;
+
+namespace {
+
+int dtype_size(int dtype) {
+  switch (dtype) {
+    case PSV_DTYPE_F32: return 4;
+    case PSV_DTYPE_BF16:
+    case PSV_DTYPE_F16: return 2;
+    default: return 0;
+  }
+}
+
+int cuda_status(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return PSV_OK;
+  return cache_fail(PSV_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// Device memory of the current device (managed memory counts).
+int check_device(const void* ptr, const char* name) {
+  if (!ptr) return cache_fail(PSV_EINVAL, "%s is null", name);
+  cudaPointerAttributes a;
+  cudaError_t e = cudaPointerGetAttributes(&a, ptr);
+  if (e != cudaSuccess) return cuda_status(e, name);
+  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
+    return cache_fail(PSV_EINVAL, "%s is not device memory", name);
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_status(e, "cudaGetDevice");
+  if (a.type == cudaMemoryTypeDevice && a.device != dev)
+    return cache_fail(PSV_EINVAL, "%s is on device %d, the current device is %d", name, a.device, dev);
+  return PSV_OK;
+}
+
+bool stride_ok(const int64_t* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] < 0 || s[i] > (int64_t{1} << 40)) return false;
+  return true;
+}
+
+// Whether the rows of an output [n0][n1][n2][width] are distinct: taken by
+// growing stride, every index steps over all that lies inside it.
+bool rows_distinct(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t width) {
+  int64_t st[3] = {s[0], s[1], s[2]}, n[3] = {n0, n1, n2};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) {
+        const int64_t a = st[i], c = n[i];
+        st[i] = st[j], n[i] = n[j];
+        st[j] = a, n[j] = c;
+      }
+  int64_t span = width;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (st[i] < span) return false;
+    span += st[i] * (n[i] - 1);
+  }
+  return true;
+}
+
+int64_t extent(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t width) {
+  return s[0] * (n0 - 1) + s[1] * (n1 - 1) + s[2] * (n2 - 1) + width;
+}
+
+bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x < y + bbytes && y < x + abytes;
+}
+
+Strides3 strides3(const int64_t* s) { return Strides3{s[0], s[1], s[2]}; }
+
+bool multiple16(const void* ptr, const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int size) {
+  const int64_t n[3] = {n0, n1, n2};
+  if (reinterpret_cast<uintptr_t>(ptr) & 15) return false;
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] * size) % 16 != 0) return false;
+  return true;
+}
+
+// ------------------------------------------------------------------ rope
+
+constexpr int kMaxPairs = 128;
+
+struct RopeParams {
+  const void* x;
+  void* out;
+  const int32_t* pos;
+  const int32_t* lens;
+  Strides3 xs, os;
+  int64_t pos_b, pos_l;
+  int64_t n;             // threads: rows x units x head groups
+  int B, L, H, dh, R;
+  int units;             // units of a head: vectors (PAIRS) or vector pairs (HALVES), then copies
+  int rot_units;         // HALVES: the units that rotate
+  int hpt, hgroups;      // heads per thread
+  int inverse;
+  uint64_t turn[kMaxPairs];  // f_p / 2 pi in 64-bit fixed point: turns per position, mod 1
+  uint8_t axis[kMaxPairs];
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ void from_f(float& y, float x) { y = x; }
+__device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f(__half& y, float x) { y = __float2half_rn(x); }
+
+// N values: 16 bytes as one access, fewer value by value (they need not be
+// aligned to more than one value).
+template <class T, int N>
+struct Vec {
+  static constexpr bool kWide = N * sizeof(T) == 16;
+  alignas(kWide ? 16 : sizeof(T)) T v[N];
+  __device__ __forceinline__ void load(const T* x) {
+    if constexpr (kWide) {
+      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = x[i];
+    }
+  }
+  __device__ __forceinline__ void store(T* x) const {
+    if constexpr (kWide) {
+      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = v[i];
+    }
+  }
+};
+
+// (cos, sin) of pos * f_p.  pos * turn wraps modulo one turn in 64 bits, so
+// the angle is off by at most |pos| 2^-53 f_p whatever the position; of the
+// signed fraction in [-1/2, 1/2) turns 32 bits (1.5e-9 radians) are used.
+__device__ __forceinline__ float2 pair_angle(const RopeParams& p, int pair, int b, int64_t l) {
+  if (2 * pair >= p.R) return make_float2(1.0f, 0.0f);
+  const int pos = p.pos[b * p.pos_b + l * p.pos_l + p.axis[pair]];
+  const uint64_t turns = static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.turn[pair];
+  const float half_turns = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  return make_float2(c, p.inverse ? -s : s);
+}
+
+// A thread holds one unit (VEC values of a head, or for HALVES VEC values and
+// their partners R/2 further on) of a row, computes its angles once and
+// applies them to hpt heads.  Memory-bound: one read and one write of x.
+template <class T, int VEC, bool HALVES>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+  using V = Vec<T, VEC>;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= p.n) return;
+  const int u = static_cast<int>(t % p.units);
+  int64_t r = t / p.units;
+  const int hg = static_cast<int>(r % p.hgroups);
+  r /= p.hgroups;
+  const int b = static_cast<int>(r / p.L);
+  const int64_t l = r % p.L;
+  if (p.lens && l >= p.lens[b]) return;
+  const bool rot = !HALVES || u < p.rot_units;
+  // Values [d0, d0 + VEC); HALVES: partners at d0 + R/2.
+  const int d0 = HALVES && !rot ? p.R + (u - p.rot_units) * VEC : u * VEC;
+  const T* x = static_cast<const T*>(p.x) + b * p.xs.b + l * p.xs.l + d0;
+  T* o = static_cast<T*>(p.out) + b * p.os.b + l * p.os.l + d0;
+  constexpr int PR = HALVES ? VEC : (VEC + 1) / 2;  // pairs of a unit
+  float2 cs[PR];
+#pragma unroll
+  for (int i = 0; i < PR; ++i)
+    cs[i] = pair_angle(p, HALVES ? (rot ? d0 + i : p.R) : d0 / 2 + i, b, l);
+  const int h1 = min(p.H, (hg + 1) * p.hpt);
+  for (int h = hg * p.hpt; h < h1; ++h) {
+    V a;
+    a.load(x + h * p.xs.h);
+    if constexpr (HALVES) {
+      if (rot) {
+        V c;
+        c.load(x + h * p.xs.h + p.R / 2);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float f = to_f(a.v[i]), g = to_f(c.v[i]);
+          from_f(a.v[i], f * cs[i].x - g * cs[i].y);
+          from_f(c.v[i], f * cs[i].y + g * cs[i].x);
+        }
+        c.store(o + h * p.os.h + p.R / 2);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        if (2 * (d0 / 2 + i) < p.R) {  // values behind R are copied bit for bit
+          const float f = to_f(a.v[2 * i]), g = to_f(a.v[2 * i + 1]);
+          from_f(a.v[2 * i], f * cs[i].x - g * cs[i].y);
+          from_f(a.v[2 * i + 1], f * cs[i].y + g * cs[i].x);
+        }
+      }
+    }
+    a.store(o + h * p.os.h);
+  }
+}
+
+// f / 2 pi as 64-bit fixed-point turns modulo one turn.
+uint64_t fixed_turns(double f) {
+  const double hi = 0.15915494309189535, lo = -9.839338337591997e-18;  // 1 / (2 pi)
+  const double t = f * hi;
+  const double e = std::fma(f, hi, -t) + f * lo;
+  const double fr = t - std::floor(t);
+  // fr < 1 holds 53 bits; the remainder e adds the bits behind them.
+  const double scaled = std::ldexp(fr, 64);
+  const uint64_t base = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+  return base + static_cast<uint64_t>(static_cast<int64_t>(std::ldexp(e, 64)));
+}
+
+template <class T, bool HALVES>
+cudaError_t launch_rope_t(RopeParams& p, bool vec, cudaStream_t st) {
+  constexpr int N = 16 / sizeof(T);
+  const int V = vec ? N : (HALVES ? 1 : 2);
+  if (HALVES) {
+    p.rot_units = p.R / 2 / V;
+    p.units = p.rot_units + (p.dh - p.R) / V;
+  } else {
+    p.units = p.dh / V;
+  }
+  p.n = static_cast<int64_t>(p.B) * p.L * p.units * p.hgroups;
+  const int64_t blocks = (p.n + 255) / 256;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  if (vec) rope_kernel<T, N, HALVES><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
+  else rope_kernel<T, HALVES ? 1 : 2, HALVES><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+PSV_API const char* psv_cache_last_error(void) { return psv::t_cache_error; }
+
+PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* pos, void* out,
+                     void* cuda_stream) {
+  if (!p) return cache_fail(PSV_EINVAL, "null problem");
+  const int size = dtype_size(p->dtype);
+  if (!size) return cache_fail(PSV_EINVAL, "unknown dtype %d", p->dtype);
+  if (p->B < 1 || p->L < 1 || p->H < 1) return cache_fail(PSV_EINVAL, "need B, L, H >= 1");
+  if (p->dh < 2 || p->dh > 256 || p->dh % 2) return cache_fail(PSV_EINVAL, "dh %d: even, 2 to 256", p->dh);
+  if (p->n_axes < 1 || p->n_axes > 4) return cache_fail(PSV_EINVAL, "n_axes %d: 1 to 4", p->n_axes);
+  if (p->layout != PSV_ROPE_PAIRS && p->layout != PSV_ROPE_HALVES)
+    return cache_fail(PSV_EINVAL, "unknown layout %d", p->layout);
+  int R = 0;
+  for (int a = 0; a < p->n_axes; ++a) {
+    if (p->axis_dims[a] < 2 || p->axis_dims[a] % 2 || p->axis_dims[a] > 256)
+      return cache_fail(PSV_EINVAL, "axis_dims[%d] = %d: even and positive", a, p->axis_dims[a]);
+    R += p->axis_dims[a];
+  }
+  if (R > p->dh) return cache_fail(PSV_EINVAL, "the axes rotate %d values of dh = %d", R, p->dh);
+  if (!p->freqs && !(std::isfinite(p->theta) && p->theta > 0))
+    return cache_fail(PSV_EINVAL, "theta must be positive and finite");
+  if (!stride_ok(p->x_stride, 3) || !stride_ok(p->out_stride, 3) || !stride_ok(p->pos_stride, 2))
+    return cache_fail(PSV_EINVAL, "strides must lie in [0, 2^40]");
+  if (!rows_distinct(p->out_stride, p->B, p->L, p->H, p->dh))
+    return cache_fail(PSV_EINVAL, "out's rows overlap");
+  RopeParams k{};
+  int pair = 0;
+  for (int a = 0; a < p->n_axes; ++a)
+    for (int j = 0; j < p->axis_dims[a] / 2; ++j, ++pair) {
+      const double f = p->freqs ? p->freqs[pair] : std::pow(p->theta, -2.0 * j / p->axis_dims[a]);
+      if (!std::isfinite(f)) return cache_fail(PSV_EINVAL, "frequency %d is not finite", pair);
+      if (std::fabs(f) > 1e6) return cache_fail(PSV_EINVAL, "frequency %d is over 1e6 radians", pair);
+      k.turn[pair] = fixed_turns(f);
+      k.axis[pair] = static_cast<uint8_t>(a);
+    }
+  if (!x || !pos || !out) return cache_fail(PSV_EINVAL, "null pointer");
+  bool same = x == out;
+  for (int i = 0; i < 3; ++i) same = same && p->x_stride[i] == p->out_stride[i];
+  if (!same && x == out) return cache_fail(PSV_EINVAL, "in place needs equal strides");
+  const uintptr_t mask = static_cast<uintptr_t>(size - 1);
+  if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(out) & mask) ||
+      (reinterpret_cast<uintptr_t>(pos) & 3))
+    return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  if (int r = check_device(x, "x")) return r;
+  if (int r = check_device(pos, "pos")) return r;
+  if (int r = check_device(out, "out")) return r;
+  k.x = x;
+  k.out = out;
+  k.pos = pos;
+  k.lens = p->lens;
+  k.xs = strides3(p->x_stride);
+  k.os = strides3(p->out_stride);
+  k.pos_b = p->pos_stride[0];
+  k.pos_l = p->pos_stride[1];
+  k.B = p->B, k.L = p->L, k.H = p->H, k.dh = p->dh, k.R = R;
+  k.inverse = p->inverse;
+  const int N = 16 / size;
+  const bool halves = p->layout == PSV_ROPE_HALVES;
+  const bool vec = multiple16(x, p->x_stride, p->B, p->L, p->H, size) &&
+                   multiple16(out, p->out_stride, p->B, p->L, p->H, size) && p->dh % N == 0 &&
+                   (!halves || ((R / 2) % N == 0 && (p->dh - R) % N == 0));
+  // Few rows: a thread per head and unit; many: four heads share the angles.
+  const int64_t rows = static_cast<int64_t>(p->B) * p->L;
+  k.hpt = rows * p->H * (p->dh / N) >= (1 << 18) ? 4 : 1;
+  k.hgroups = (p->H + k.hpt - 1) / k.hpt;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e;
+  if (p->dtype == PSV_DTYPE_F32)
+    e = halves ? launch_rope_t<float, true>(k, vec, st) : launch_rope_t<float, false>(k, vec, st);
+  else if (p->dtype == PSV_DTYPE_BF16)
+    e = halves ? launch_rope_t<__nv_bfloat16, true>(k, vec, st) : launch_rope_t<__nv_bfloat16, false>(k, vec, st);
+  else
+    e = halves ? launch_rope_t<__half, true>(k, vec, st) : launch_rope_t<__half, false>(k, vec, st);
+  return cuda_status(e, "rope launch");
+}
+
+// ---------------------------------------------------------------- eviction
+
+namespace {
+
+struct EvictParams {
+  const void *k, *v;
+  const float* mass;
+  void *k_out, *v_out;
+  float* mass_out;
+  int32_t* idx;
+  const int32_t *k_lens, *k_pos, *k_doc;
+  int32_t *pos_out, *doc_out, *lens_out;
+  Strides3 ks, vs, kos, vos;
+  int64_t km_b, km_h;
+  int B, H, dh, L, budget, sinks, recent;
+};
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelSmemKeys = 49152;  // keys held in shared memory (192 KB)
+
+// Order of selection as an unsigned key: protected slots, then NaN, then by
+// value (+0 and -0 are equal).
+__device__ __forceinline__ uint32_t select_key(const EvictParams& p, const float* mass, int j, int n) {
+  if (j < p.sinks || j >= n - p.recent) return 0xffffffffu;
+  const float x = mass[j] + 0.0f;
+  if (x != x) return 0xfffffffeu;
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Exclusive sums of a and b over the block's threads (1024).
+__device__ __forceinline__ void block_scan2(int& a, int& b, int* sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int x = a, y = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int xo = __shfl_up_sync(0xffffffffu, x, o), yo = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x += xo, y += yo;
+  }
+  if (lane == 31) sm[w] = x, sm[32 + w] = y;
+  __syncthreads();
+  if (w == 0) {
+    int s = sm[lane], t = sm[32 + lane];
+    const int s0 = s, t0 = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int so = __shfl_up_sync(0xffffffffu, s, o), to = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) s += so, t += to;
+    }
+    sm[lane] = s - s0, sm[32 + lane] = t - t0;
+  }
+  __syncthreads();
+  a = x - a + sm[w];
+  b = y - b + sm[32 + w];
+}
+
+// One CTA per (sequence, kv head): the budget-th greatest key by radix
+// selection, 8 bits a pass, then the kept slots in order by one scan over
+// contiguous shares of the slots.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[256];
+  __shared__ int scan[64];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need;
+  const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, t = threadIdx.x;
+  const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
+  const int keep = min(n, p.budget);
+  const float* mass = p.mass + (static_cast<int64_t>(b) * p.H + h) * p.L;
+  const bool held = n <= kSelSmemKeys && p.L <= kSelSmemKeys;
+  if (held)
+    for (int j = t; j < n; j += kSelThreads) keys[j] = select_key(p, mass, j, n);
+  if (t == 0) s_prefix = 0, s_need = keep;
+  __syncthreads();
+  auto key_at = [&](int j) { return held ? keys[j] : select_key(p, mass, j, n); };
+  // Keys over the threshold are kept, `need` of those equal to it.
+  uint32_t thr = 0;
+  int need = keep;
+  if (keep < n) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = t; i < 256; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      const uint32_t pre = s_prefix;
+      const uint32_t hi = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+      for (int j = t; j < n; j += kSelThreads) {
+        const uint32_t u = key_at(j);
+        if ((u & hi) == pre) atomicAdd(&hist[(u >> shift) & 255], 1);
+      }
+      __syncthreads();
+      if (t == 0) {
+        int left = s_need, d = 255;
+        while (d > 0 && hist[d] < left) left -= hist[d--];
+        s_prefix = pre | static_cast<uint32_t>(d) << shift;
+        s_need = left;
+      }
+      __syncthreads();
+    }
+    thr = s_prefix;
+    need = s_need;
+  }
+  const int per = (n + kSelThreads - 1) / kSelThreads;
+  const int j0 = min(n, t * per), j1 = min(n, j0 + per);
+  int over = 0, ties = 0;
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t u = key_at(j);
+    over += u > thr;
+    ties += u == thr;
+  }
+  if (keep == n) over += ties, ties = 0;  // everything stays
+  block_scan2(over, ties, scan);
+  const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.budget;
+  const int64_t meta = b * p.km_b + h * p.km_h;
+  int at = over + min(ties, need);
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t u = key_at(j);
+    bool k = keep == n || u > thr;
+    if (!k && u == thr) k = ties++ < need;
+    if (!k) continue;
+    p.idx[row + at] = j;
+    p.mass_out[row + at] = mass[j];
+    if (p.pos_out) p.pos_out[row + at] = p.k_pos ? p.k_pos[meta + j] : j;
+    if (p.doc_out) p.doc_out[row + at] = p.k_doc[meta + j];
+    ++at;
+  }
+  if (h == 0 && t == 0 && p.lens_out) p.lens_out[b] = keep;
+}
+
+// Copies the kept rows: thread = one unit (16 bytes, or one value) of a row
+// of K and of V; consecutive threads write consecutive units of an out row
+// and then the next head.
+template <class U>
+__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, int units, int esize) {
+  const int64_t per_b = static_cast<int64_t>(p.budget) * p.H * units;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= per_b) return;
+  const int b = blockIdx.y;
+  const int u = static_cast<int>(t % units);
+  const int64_t r = t / units;
+  const int h = static_cast<int>(r % p.H);
+  const int64_t row = r / p.H;
+  const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
+  if (row >= min(n, p.budget)) return;
+  const int64_t j = p.idx[(static_cast<int64_t>(b) * p.H + h) * p.budget + row];
+  auto src = [&](const void* base, const Strides3& s) {
+    return reinterpret_cast<const U*>(static_cast<const char*>(base) + (b * s.b + j * s.l + h * s.h) * esize) + u;
+  };
+  auto dst = [&](void* base, const Strides3& s) {
+    return reinterpret_cast<U*>(static_cast<char*>(base) + (b * s.b + row * s.l + h * s.h) * esize) + u;
+  };
+  const U kk = *src(p.k, p.ks), vv = *src(p.v, p.vs);
+  *dst(p.k_out, p.kos) = kk;
+  *dst(p.v_out, p.vos) = vv;
+}
+
+template <class U>
+void launch_gather(const EvictParams& p, int size, cudaStream_t st) {
+  const int units = p.dh * size / static_cast<int>(sizeof(U));
+  const int64_t per_b = static_cast<int64_t>(p.budget) * p.H * units;
+  evict_gather_kernel<U><<<dim3(static_cast<unsigned>((per_b + 255) / 256), p.B), 256, 0, st>>>(p, units, size);
+}
+
+}  // namespace
+
+PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const void* v, const float* mass,
+                            void* k_out, void* v_out, float* mass_out, int32_t* idx_out,
+                            void* cuda_stream) {
+  if (!p) return cache_fail(PSV_EINVAL, "null problem");
+  const int size = dtype_size(p->dtype);
+  if (!size) return cache_fail(PSV_EINVAL, "unknown dtype %d", p->dtype);
+  if (p->B < 1 || p->Hkv < 1 || p->L < 1 || p->dh < 1)
+    return cache_fail(PSV_EINVAL, "need B, Hkv, L, dh >= 1");
+  if (p->B > 65535 || static_cast<int64_t>(p->B) * p->Hkv > 0x7fffffff)
+    return cache_fail(PSV_EINVAL, "too many sequences and heads");
+  if (p->budget < 1 || p->budget > p->L) return cache_fail(PSV_EINVAL, "budget %d: 1 to L = %d", p->budget, p->L);
+  if (p->sinks < 0 || p->recent < 0 || static_cast<int64_t>(p->sinks) + p->recent > p->budget)
+    return cache_fail(PSV_EINVAL, "sinks %d + recent %d do not fit the budget %d", p->sinks, p->recent, p->budget);
+  if (!stride_ok(p->k_stride, 3) || !stride_ok(p->v_stride, 3) || !stride_ok(p->k_out_stride, 3) ||
+      !stride_ok(p->v_out_stride, 3) || !stride_ok(p->k_meta_stride, 2))
+    return cache_fail(PSV_EINVAL, "strides must lie in [0, 2^40]");
+  if (!rows_distinct(p->k_out_stride, p->B, p->budget, p->Hkv, p->dh) ||
+      !rows_distinct(p->v_out_stride, p->B, p->budget, p->Hkv, p->dh))
+    return cache_fail(PSV_EINVAL, "the rows of k_out or v_out overlap");
+  if (p->doc_out && !p->k_doc) return cache_fail(PSV_EINVAL, "doc_out needs k_doc");
+  if (p->lens_out && p->lens_out == p->k_lens) return cache_fail(PSV_EINVAL, "lens_out must not be k_lens");
+  if (static_cast<int64_t>(p->budget) * p->Hkv * p->dh > (int64_t{1} << 38))
+    return cache_fail(PSV_EINVAL, "a sequence's kept rows are over 2^38 values");
+  if (!k || !v || !mass || !k_out || !v_out || !mass_out || !idx_out)
+    return cache_fail(PSV_EINVAL, "null pointer");
+  const void* typed[4] = {k, v, k_out, v_out};
+  for (const void* x : typed)
+    if (reinterpret_cast<uintptr_t>(x) & (size - 1)) return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  if ((reinterpret_cast<uintptr_t>(mass) | reinterpret_cast<uintptr_t>(mass_out) | reinterpret_cast<uintptr_t>(idx_out)) & 3)
+    return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  const int64_t in_k = extent(p->k_stride, p->B, p->L, p->Hkv, p->dh) * size;
+  const int64_t in_v = extent(p->v_stride, p->B, p->L, p->Hkv, p->dh) * size;
+  const int64_t out_k = extent(p->k_out_stride, p->B, p->budget, p->Hkv, p->dh) * size;
+  const int64_t out_v = extent(p->v_out_stride, p->B, p->budget, p->Hkv, p->dh) * size;
+  const int64_t in_m = static_cast<int64_t>(p->B) * p->Hkv * p->L * 4;
+  const int64_t out_m = static_cast<int64_t>(p->B) * p->Hkv * p->budget * 4;
+  if (overlap(k, in_k, k_out, out_k) || overlap(v, in_v, v_out, out_v) || overlap(mass, in_m, mass_out, out_m))
+    return cache_fail(PSV_EINVAL, "out buffers must not overlap their inputs");
+  if (k_out == v_out) return cache_fail(PSV_EINVAL, "k_out and v_out are the same buffer");
+  struct { const void* ptr; const char* name; } ptrs[7] = {{k, "k"}, {v, "v"}, {mass, "mass"}, {k_out, "k_out"},
+      {v_out, "v_out"}, {mass_out, "mass_out"}, {idx_out, "idx_out"}};
+  for (const auto& x : ptrs)
+    if (int r = check_device(x.ptr, x.name)) return r;
+  EvictParams e{};
+  e.k = k, e.v = v, e.mass = mass, e.k_out = k_out, e.v_out = v_out, e.mass_out = mass_out, e.idx = idx_out;
+  e.k_lens = p->k_lens, e.k_pos = p->k_pos, e.k_doc = p->k_doc;
+  e.pos_out = p->pos_out, e.doc_out = p->doc_out, e.lens_out = p->lens_out;
+  e.ks = strides3(p->k_stride), e.vs = strides3(p->v_stride);
+  e.kos = strides3(p->k_out_stride), e.vos = strides3(p->v_out_stride);
+  e.km_b = p->k_meta_stride[0], e.km_h = p->k_meta_stride[1];
+  e.B = p->B, e.H = p->Hkv, e.dh = p->dh, e.L = p->L, e.budget = p->budget;
+  e.sinks = p->sinks, e.recent = p->recent;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const size_t smem = p->L <= kSelSmemKeys ? static_cast<size_t>(p->L) * 4 : 0;
+  static uint64_t set_up = 0;
+  cudaError_t r = psv::once_per_device(&set_up, [](int) {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemKeys * 4);
+  });
+  if (r != cudaSuccess) return cuda_status(r, "eviction set-up");
+  evict_select_kernel<<<p->B * p->Hkv, kSelThreads, smem, st>>>(e);
+  if ((r = cudaGetLastError()) != cudaSuccess) return cuda_status(r, "eviction launch");
+  const bool vec = (static_cast<int64_t>(p->dh) * size) % 16 == 0 &&
+                   multiple16(k, p->k_stride, p->B, p->L, p->Hkv, size) &&
+                   multiple16(v, p->v_stride, p->B, p->L, p->Hkv, size) &&
+                   multiple16(k_out, p->k_out_stride, p->B, p->budget, p->Hkv, size) &&
+                   multiple16(v_out, p->v_out_stride, p->B, p->budget, p->Hkv, size);
+  if (vec) launch_gather<uint4>(e, size, st);
+  else if (size == 4) launch_gather<uint32_t>(e, size, st);
+  else launch_gather<uint16_t>(e, size, st);
+  return cuda_status(cudaGetLastError(), "eviction launch");
+}
+
+// ------------------------------------------------- attention over a cache
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_cache(const psv_cache_problem* p) {
+  if (!p) return cache_fail(PSV_EINVAL, "null problem");
+  if (p->dtype != PSV_DTYPE_BF16 && p->dtype != PSV_DTYPE_F16)
+    return cache_fail(PSV_EINVAL, "dtype %d: bf16 or f16", p->dtype);
+  if (p->B < 1 || p->Hkv < 1 || p->Hq < 1 || p->Hq % p->Hkv)
+    return cache_fail(PSV_EINVAL, "need B >= 1 and Hq (%d) a multiple of Hkv (%d)", p->Hq, p->Hkv);
+  if (p->dh < 1 || p->dh > 256) return cache_fail(PSV_EINVAL, "dh %d: 1 to 256", p->dh);
+  if (p->Lq < 0 || p->Lk < 0 || p->Lq > (1 << 24) || p->Lk > (1 << 28))
+    return cache_fail(PSV_EINVAL, "Lq %d: 0 to 2^24, Lk %d: 0 to 2^28", p->Lq, p->Lk);
+  if (static_cast<int64_t>(p->B) * p->Hq > (1 << 24)) return cache_fail(PSV_EINVAL, "over 2^24 sequences x heads");
+  if (!(std::isfinite(p->scale) && p->scale >= 0)) return cache_fail(PSV_EINVAL, "scale must be finite and not negative");
+  if (!(std::isfinite(p->softcap) && p->softcap >= 0))
+    return cache_fail(PSV_EINVAL, "softcap must be finite and not negative");
+  if (!stride_ok(p->q_stride, 3) || !stride_ok(p->k_stride, 3) || !stride_ok(p->v_stride, 3) ||
+      !stride_ok(p->o_stride, 3) || !stride_ok(&p->q_meta_stride, 1) || !stride_ok(p->k_meta_stride, 2))
+    return cache_fail(PSV_EINVAL, "strides must lie in [0, 2^40]");
+  if (!p->k_doc != !p->q_doc) return cache_fail(PSV_EINVAL, "k_doc and q_doc come together");
+  if (p->prefix && !p->causal) return cache_fail(PSV_EINVAL, "prefix needs causal");
+  return PSV_OK;
+}
+
+int check_scratch(void* scratch, size_t bytes, size_t need) {
+  if (int r = check_device(scratch, "scratch")) return r;
+  if (reinterpret_cast<uintptr_t>(scratch) & 255) return cache_fail(PSV_EINVAL, "scratch must be 256-byte aligned");
+  if (bytes < need) return cache_fail(PSV_EINVAL, "scratch of %zu bytes, %zu needed", bytes, need);
+  return PSV_OK;
+}
+
+CacheParams cache_params(const psv_cache_problem* p, const void* q, const void* k, void* scratch) {
+  CacheParams c{};
+  c.B = p->B, c.Hq = p->Hq, c.Hkv = p->Hkv, c.G = p->Hq / p->Hkv, c.dh = p->dh;
+  c.Lq = p->Lq, c.Lk = p->Lk, c.causal = p->causal != 0;
+  c.scale = p->scale > 0 ? p->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(p->dh)));
+  c.softcap = p->softcap;
+  c.qs = strides3(p->q_stride), c.ks = strides3(p->k_stride);
+  c.vs = strides3(p->v_stride), c.os = strides3(p->o_stride);
+  c.q = q, c.k = k;
+  c.q_lens = p->q_lens, c.k_lens = p->k_lens, c.q_pos = p->q_pos, c.q_doc = p->q_doc;
+  c.k_pos = p->k_pos, c.k_doc = p->k_doc, c.prefix = p->prefix;
+  c.qm_b = p->q_meta_stride, c.km_b = p->k_meta_stride[0], c.km_h = p->k_meta_stride[1];
+  c.slopes = p->slopes;
+  c.err = static_cast<int*>(scratch);
+  return c;
+}
+
+size_t cache_scratch(const psv_cache_problem*) { return up256(PSV_CACHE_SCRATCH_HEAD); }
+
+}  // namespace
+
+PSV_API int psv_cache_scratch_bytes(const psv_cache_problem* p, size_t* bytes) {
+  if (int r = check_cache(p)) return r;
+  if (!bytes) return cache_fail(PSV_EINVAL, "null pointer");
+  *bytes = cache_scratch(p);
+  return PSV_OK;
+}
+
+PSV_API int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k, const void* v,
+                                void* o, float* lse, void* scratch, size_t scratch_bytes,
+                                void* cuda_stream) {
+  if (int r = check_cache(p)) return r;
+  if (p->Lq == 0) return PSV_OK;
+  if (!rows_distinct(p->o_stride, p->B, p->Lq, p->Hq, p->dh)) return cache_fail(PSV_EINVAL, "o's rows overlap");
+  if (!q || !o || !scratch || (p->Lk && (!k || !v))) return cache_fail(PSV_EINVAL, "null pointer");
+  const uintptr_t at = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
+                       reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(o);
+  if ((at & 1) || (reinterpret_cast<uintptr_t>(lse) & 3))
+    return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  if (int r = check_device(q, "q")) return r;
+  if (p->Lk) {
+    if (int r = check_device(k, "k")) return r;
+    if (int r = check_device(v, "v")) return r;
+  }
+  if (int r = check_device(o, "o")) return r;
+  if (lse)
+    if (int r = check_device(lse, "lse")) return r;
+  if (int r = check_scratch(scratch, scratch_bytes, cache_scratch(p))) return r;
+  CacheParams c = cache_params(p, q, k, scratch);
+  c.v = v, c.o = o, c.lse = lse;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  return cuda_status(psv::launch_cache_attention_general(c, p->dtype == PSV_DTYPE_BF16, st), "attention launch");
+}
+
+PSV_API int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, const float* lse,
+                           const float* mass_in, float* mass_out, void* scratch, size_t scratch_bytes,
+                           void* cuda_stream) {
+  if (int r = check_cache(p)) return r;
+  if (p->Lk == 0) return PSV_OK;
+  if (!k || !mass_out || !scratch || (p->Lq && (!q || !lse))) return cache_fail(PSV_EINVAL, "null pointer");
+  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) & 1) ||
+      ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(mass_in) | reinterpret_cast<uintptr_t>(mass_out)) & 3))
+    return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  const int64_t bytes = static_cast<int64_t>(p->B) * p->Hkv * p->Lk * 4;
+  if (mass_in && mass_in != mass_out && overlap(mass_in, bytes, mass_out, bytes))
+    return cache_fail(PSV_EINVAL, "mass_in overlaps mass_out in part");
+  if (p->Lq) {
+    if (int r = check_device(q, "q")) return r;
+    if (int r = check_device(lse, "lse")) return r;
+  }
+  if (int r = check_device(k, "k")) return r;
+  if (mass_in)
+    if (int r = check_device(mass_in, "mass_in")) return r;
+  if (int r = check_device(mass_out, "mass_out")) return r;
+  if (int r = check_scratch(scratch, scratch_bytes, cache_scratch(p))) return r;
+  CacheParams c = cache_params(p, q, k, scratch);
+  c.lse = const_cast<float*>(lse), c.mass_in = mass_in, c.mass_out = mass_out;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  return cuda_status(psv::launch_cache_mass_general(c, p->dtype == PSV_DTYPE_BF16, st), "mass launch");
+}

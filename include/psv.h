@@ -358,6 +358,160 @@ int psv_attention_noalloc(const psv_attn_problem* p, const void* q, const void* 
  * PSV_ECUDA. */
 int psv_attention_noalloc_status(int* status, void* cuda_stream);
 
+/* ---- kernel-level operators of a rolling key/value cache ------------------
+ *
+ * The pages keep the keys and values of the preceding chunks in a rolling
+ * window (AREX article, §难题) and say nothing about positions in space,
+ * masks or what leaves the window.  These calls give a program that drives
+ * its own cache the operators around psv_attention: rotary positions with
+ * several axes, attention over a cache with masks, a score cap and a distance
+ * bias, the attention weight every key received, and the eviction of the keys
+ * that received least.
+ *
+ * Conventions of these calls
+ *   - strides are counted in elements; the innermost index (a head's dh
+ *     values) is contiguous; offsets are 64-bit;
+ *   - every pointer is device memory of the current device unless its line
+ *     says host; work goes to cuda_stream and is asynchronous; nothing is
+ *     allocated and no host memory is read after the call returns, so a call
+ *     can be captured into a CUDA graph;
+ *   - lengths, positions, documents and prefixes are read on the device when
+ *     the kernels run (a captured call sees their values at replay);
+ *   - errors: PSV_EINVAL (shapes, strides, alignment, null or non-device
+ *     pointers), PSV_ECUDA; psv_cache_last_error() names the reason. */
+
+#define PSV_DTYPE_F16 2 /* besides PSV_DTYPE_F32 and PSV_DTYPE_BF16 */
+
+/* Reason of this thread's last failed call of this section ("" if none). */
+const char* psv_cache_last_error(void);
+
+/* Rotary positions with several axes.  x [B][L][H][dh]; the first
+ * R = axis_dims[0] + .. + axis_dims[n_axes-1] values of a head are rotated,
+ * the others copied.  Rotated pair p (0 <= p < R/2) belongs to axis a, whose
+ * pairs are numbered consecutively (axis 0 first), and turns by
+ *   angle = pos[b][l][a] * f_p,  f_p = theta^(-2 j / axis_dims[a])
+ * with j the pair's number within its axis; freqs, where given, holds f_p
+ * itself (any schedule).  (u, w) -> (u cos - w sin, u sin + w cos); inverse
+ * turns by -angle (un-rotates cached keys; also the gradient of the forward
+ * call).  Layout PAIRS: pair p is (2p, 2p+1), as on the wave path; HALVES:
+ * (p, p + R/2).  Angles are reduced in 64-bit fixed point, so positions up to
+ * 2^31 keep f32 accuracy; the rotation is done in f32 and rounded once.
+ * In place (out == x with equal strides) is allowed, other overlap is not.
+ * Rows l >= lens[b] of out are left as they were.
+ * Requirements: dtype F32, BF16 or F16; 1 <= n_axes <= 4; axis_dims even and
+ * positive; R <= dh <= 256; dh even; B, L, H >= 1; strides >= 0, out's rows
+ * distinct.  Bases and strides that are multiples of 16 bytes use 16-byte accesses. */
+#define PSV_ROPE_PAIRS  0
+#define PSV_ROPE_HALVES 1
+typedef struct psv_rope_problem {
+  int32_t dtype, B, L, H, dh;
+  int32_t n_axes, axis_dims[4];
+  int32_t layout, inverse;
+  double theta;
+  const double* freqs;     /* host [R/2], radians per position; NULL: from theta */
+  int64_t x_stride[3];     /* batch, row, head */
+  int64_t out_stride[3];
+  int64_t pos_stride[2];   /* batch (0: shared), row; axes are contiguous */
+  const int32_t* lens;     /* [B] rows in use; NULL: L */
+} psv_rope_problem;
+
+/* pos int32 [B][L][n_axes]. */
+int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* pos, void* out,
+             void* cuda_stream);
+
+/* Attention over a cache.  q, o [B][Lq][Hq][dh]; k, v [B][Lk][Hkv][dh] (values
+ * as written, not transposed); query head h reads key head h / (Hq / Hkv).
+ *   s = scale * q.k;  softcap > 0: s = softcap * tanh(s / softcap);
+ *   slopes: s -= slopes[h] * |q_pos - k_pos|
+ * A row sees key j if j < k_lens[b], q_doc == k_doc (where documents are
+ * given) and, with causal set, k_pos <= q_pos or k_pos < prefix[b].
+ *   o = softmax(s) v over the visible keys;  lse = log sum exp s  [B][Hq][Lq]
+ * A row that sees nothing gets o = 0 and lse = -infinity.  Rows i >= q_lens[b]
+ * of o and lse are left as they were.  Lengths are clamped to [0, Lq] and
+ * [0, Lk].  Default positions: k_pos = j, q_pos = k_len - q_len + i (the rows
+ * are the last ones of the sequence).  Positions lie within +-2^30.
+ * Keys and values behind k_lens[b] may hold anything (NaN too); keys that are
+ * only masked may hold anything finite, their scores are not used.
+ * Products take bf16/f16 operands and accumulate in f32; scores, maxima, sums
+ * and lse are f32; the weights are rounded to the operand type for their
+ * product with v, the output once.  Results do not depend on other sequences
+ * of the batch, and repeat bit for bit.
+ * Requirements: dtype BF16 or F16; B, Hkv >= 1; Hq a multiple of Hkv; Lq, Lk
+ * >= 0; 1 <= dh <= 256; strides >= 0, o's rows distinct; scale >= 0 and
+ * softcap >= 0 finite; k_doc and q_doc both or neither; prefix needs causal.
+ * The tensor-core path takes dh <= 128, dh % 8 == 0, Hq / Hkv <= 128,
+ * bases and strides in multiples of 16 bytes (positive where the extent is
+ * over 1); every other problem runs on a slower general kernel. */
+typedef struct psv_cache_problem {
+  int32_t dtype, B, Hq, Hkv, dh, Lq, Lk;
+  int32_t causal;
+  float scale;              /* 0: 1 / sqrt(dh) */
+  float softcap;            /* 0: none */
+  int64_t q_stride[3];      /* batch, row, head */
+  int64_t k_stride[3], v_stride[3], o_stride[3];
+  const int32_t* q_lens;    /* [B]; NULL: Lq */
+  const int32_t* k_lens;    /* [B]; NULL: Lk */
+  const int32_t* q_pos;     /* [B][Lq]; NULL: see above */
+  const int32_t* q_doc;     /* [B][Lq]; NULL: one document */
+  int64_t q_meta_stride;    /* batch stride of q_pos and q_doc */
+  const int32_t* k_pos;     /* [B][Hkv][Lk]; NULL: j */
+  const int32_t* k_doc;     /* [B][Hkv][Lk] */
+  int64_t k_meta_stride[2]; /* batch and kv-head strides of k_pos and k_doc (0: shared) */
+  const int32_t* prefix;    /* [B]; NULL: 0 */
+  const float* slopes;      /* [Hq]; NULL: no distance bias */
+} psv_cache_problem;
+
+/* Workspace of psv_cache_attention and psv_cache_mass for this problem:
+ * 256-byte aligned device memory whose first PSV_CACHE_SCRATCH_HEAD bytes the
+ * caller zeroes once, before its first use.  It may serve any number of calls
+ * (captured ones too) that do not overlap on the GPU.  The int at its start
+ * becomes nonzero, and stays so, if a device-side wait of a call timed out;
+ * that call's output is not valid, and the workspace is zeroed before reuse. */
+#define PSV_CACHE_SCRATCH_HEAD 256
+int psv_cache_scratch_bytes(const psv_cache_problem* p, size_t* bytes);
+int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k, const void* v,
+                        void* o, float* lse /* may be NULL */, void* scratch, size_t scratch_bytes,
+                        void* cuda_stream);
+
+/* Attention weight that each cached key received, from the rows' lse of
+ * psv_cache_attention on the same problem (v and o are not used):
+ *   mass_out[b][g][j] = mass_in[b][g][j]
+ *                     + sum over rows i < q_lens[b] and heads h of group g of exp(s_ij - lse)
+ * over visible pairs; mass f32 [B][Hkv][Lk]; mass_in may be NULL (zeros) or
+ * mass_out (accumulate in place).  Entries j >= k_lens[b] are left as they
+ * were.  Sums are f32 in a fixed order.  Requirements as above. */
+int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, const float* lse,
+                   const float* mass_in, float* mass_out, void* scratch, size_t scratch_bytes,
+                   void* cuda_stream);
+
+/* Eviction by accumulated weight.  Of the n = k_lens[b] keys of each (sequence,
+ * kv head), min(n, budget) are kept: the first `sinks` slots, the last
+ * `recent` ones, and of the others those with the greatest mass, the lower
+ * slot among equals (NaN counts as the greatest).  Kept keys, values and mass
+ * are written in slot order to other buffers (k_out, v_out [B][budget][Hkv][dh];
+ * mass_out, idx_out, pos_out, doc_out [B][Hkv][budget]); idx_out holds the
+ * slots they came from, lens_out[b] = min(n, budget).  Rows behind lens_out
+ * are left as they were.  pos_out without k_pos receives the slots.  Out
+ * buffers must not overlap any input or one another.
+ * Requirements: dtype F32, BF16 or F16; B, Hkv, L, budget >= 1; budget <= L;
+ * 1 <= dh; sinks, recent >= 0, sinks + recent <= budget; strides >= 0, rows of
+ * k_out and v_out distinct; doc_out needs k_doc. */
+typedef struct psv_evict_problem {
+  int32_t dtype, B, Hkv, dh, L, budget, sinks, recent;
+  int64_t k_stride[3], v_stride[3];         /* batch, row, head */
+  int64_t k_out_stride[3], v_out_stride[3];
+  const int32_t* k_lens;    /* [B]; NULL: L */
+  const int32_t* k_pos;     /* [B][Hkv][L] or NULL */
+  const int32_t* k_doc;     /* [B][Hkv][L] or NULL */
+  int64_t k_meta_stride[2]; /* batch and kv-head strides of k_pos and k_doc (0: shared) */
+  int32_t* pos_out;         /* or NULL */
+  int32_t* doc_out;         /* or NULL */
+  int32_t* lens_out;        /* [B] or NULL; not k_lens */
+} psv_evict_problem;
+
+int psv_cache_evict(const psv_evict_problem* p, const void* k, const void* v, const float* mass,
+                    void* k_out, void* v_out, float* mass_out, int32_t* idx_out, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
