@@ -42,4 +42,11 @@ __device__ __forceinline__ int cache_q_len(const CacheParams& p, int b) {
 cudaError_t launch_cache_attention_general(const CacheParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_cache_mass_general(const CacheParams& p, bool bf16, cudaStream_t st);
 
+// The tensor-core attention: which shapes it takes, which tensors, its
+// workspace (head included), and the launch on `sms` SMs.
+bool cache_attn_tc_shape(const CacheParams& p);
+bool cache_attn_tc_aligned(const CacheParams& p);
+size_t cache_attn_tc_scratch(const CacheParams& p);
+cudaError_t launch_cache_attention_tc(const CacheParams& p, bool bf16, char* scratch, int sms, cudaStream_t st);
+
 }  // namespace psv

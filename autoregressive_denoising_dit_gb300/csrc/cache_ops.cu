@@ -576,8 +576,6 @@ PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const voi
 
 namespace {
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
 int check_cache(const psv_cache_problem* p) {
   if (!p) return cache_fail(PSV_EINVAL, "null problem");
   if (p->dtype != PSV_DTYPE_BF16 && p->dtype != PSV_DTYPE_F16)
@@ -623,7 +621,16 @@ CacheParams cache_params(const psv_cache_problem* p, const void* q, const void* 
   return c;
 }
 
-size_t cache_scratch(const psv_cache_problem*) { return up256(PSV_CACHE_SCRATCH_HEAD); }
+size_t cache_scratch(const psv_cache_problem* p) {
+  const CacheParams c = cache_params(p, nullptr, nullptr, nullptr);
+  return psv::cache_attn_tc_shape(c) ? psv::cache_attn_tc_scratch(c) : PSV_CACHE_SCRATCH_HEAD;
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
 
 }  // namespace
 
@@ -657,6 +664,13 @@ PSV_API int psv_cache_attention(const psv_cache_problem* p, const void* q, const
   CacheParams c = cache_params(p, q, k, scratch);
   c.v = v, c.o = o, c.lse = lse;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (psv::cache_attn_tc_shape(c) && psv::cache_attn_tc_aligned(c)) {
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess)
+      e = psv::launch_cache_attention_tc(c, p->dtype == PSV_DTYPE_BF16, static_cast<char*>(scratch), sms, st);
+    return cuda_status(e, "attention launch");
+  }
   return cuda_status(psv::launch_cache_attention_general(c, p->dtype == PSV_DTYPE_BF16, st), "attention launch");
 }
 

@@ -191,7 +191,7 @@ bool encode_map(CUtensorMapDataType dt, CUtensorMap* map, int rank, void* base,
                 CUtensorMapSwizzle sw) {
   auto enc = get_encoder();
   if (!enc) return false;
-  cuuint32_t es[3] = {1, 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
   CUresult r = enc(map, dt, rank, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -206,6 +206,12 @@ bool psv::encode_bf16_map(CUtensorMap* map, int rank, void* base, const uint64_t
 bool psv::encode_f32_map(CUtensorMap* map, int rank, void* base, const uint64_t* dims,
                          const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
   return encode_map(CU_TENSOR_MAP_DATA_TYPE_FLOAT32, map, rank, base, dims, strides, box, sw);
+}
+
+bool psv::encode_16bit_map(CUtensorMap* map, bool bf16, int rank, void* base, const uint64_t* dims,
+                           const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
+  return encode_map(bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, map, rank, base,
+                    dims, strides, box, sw);
 }
 
 namespace {

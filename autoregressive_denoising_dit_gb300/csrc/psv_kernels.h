@@ -166,6 +166,9 @@ cudaError_t launch_fill_attn_tasks(TaskDev* tasks, int n, int T, int L, cudaStre
 // 1..rank-1); false if the driver entry point or the arguments are rejected.
 bool encode_bf16_map(CUtensorMap* map, int rank, void* base, const uint64_t* dims,
                      const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);
+// The same for bf16 or f16 elements, rank up to 5.
+bool encode_16bit_map(CUtensorMap* map, bool bf16, int rank, void* base, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);
 // The same for f32 elements.
 bool encode_f32_map(CUtensorMap* map, int rank, void* base, const uint64_t* dims,
                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);

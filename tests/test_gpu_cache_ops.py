@@ -38,7 +38,7 @@ def code(P, dtype):
 
 
 def ints(a):
-    return None if a is None else torch.as_tensor(np.ascontiguousarray(a), dtype=torch.int32, device="cuda")
+    return None if a is None else torch.as_tensor(np.array(a, order="C"), dtype=torch.int32, device="cuda")
 
 
 def at(t):
@@ -420,6 +420,28 @@ def test_attention_repeats_and_is_batch_invariant(P):
     one = dict(c, B=1, q=c["q"][2:3], k=c["k"][2:3], v=c["v"][2:3], k_lens=c["k_lens"][2:3].clone())
     o, lse = run_attention(P, one)
     assert torch.equal(o[0], a[2]) and torch.equal(lse[0], la[2])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(Lq=4400, Lk=8800, Hq=24, Hkv=8, dh=128, causal=True, prefix=[880], cap=50.0, dtype="f16"),
+    dict(B=9, Lq=3, Lk=40, Hq=12, Hkv=12, dh=64, k_lens=[40, 1, 0, 7, 33, 39, 12, 40, 3]),
+    dict(B=40, Lq=1, Lk=700, Hq=4, Hkv=4, dh=128, k_lens=list(range(660, 700))),
+], ids=["long", "one-tile-pieces", "shares"])
+def test_attention_many_pieces_many_times(P, kw):
+    """Several work pieces per pair of SMs, launched over and over with and without a gap: the
+    hand-over of pieces between the two SMs never mixes them up."""
+    c = make(**kw)
+    want = run_attention(P, c)
+    prob = problem(P, c)
+    scratch, n = scratch_for(P, prob)
+    o, lse = torch.zeros_like(c["q"]), torch.zeros(c["B"], c["Hq"], c["Lq"], device="cuda")
+    for i in range(300):
+        P.psv_cache_attention(prob, at(c["q"]), at(c["k"]), at(c["v"]), at(o), at(lse), at(scratch), n, stream())
+        if i % 2:
+            torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    no_error(scratch)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
 def test_attention_long_cache_offsets(P):
