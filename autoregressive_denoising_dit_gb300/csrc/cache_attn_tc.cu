@@ -190,6 +190,19 @@ __device__ __forceinline__ void fadd2(float& a0, float& a1, float b0, float b1) 
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
+// (x0, x1) = (x0, x1) * s + (c, c + 1) * bs + as, c a constant.
+__device__ __forceinline__ void bias2(float& x0, float& x1, float s, float c, float bs, float as) {
+  uint64_t x, y, sv, bv, av;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(c), "f"(c + 1.0f));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(sv) : "f"(s));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(bv) : "f"(bs));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(av) : "f"(as));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(bv), "l"(av));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(sv), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (BF16) {
@@ -239,6 +252,19 @@ __device__ __forceinline__ bool mbar_wait_acq_cluster(uint64_t* bar, uint32_t pa
   }
 }
 
+// What a tile of 256 keys and a unit of rows hold, from a small kernel run
+// before the attention where positions or documents are given: tiles that no
+// row of a unit sees are not loaded, tiles that every row sees whole are not
+// masked, and a tile of consecutive positions needs no position per key.
+struct KeyTile {
+  int pos_min, pos_max, doc_min, doc_max;  // over the keys in use (min > max: none)
+  int base;                                // the first key's position
+  int run;                                 // positions are base, base + 1, ..
+};
+struct RowUnit {
+  int pos_max, doc_min, doc_max, pad;
+};
+
 struct TcParams {
   CacheParams c;
   int rows_cta;     // packed rows of a CTA: a multiple of G
@@ -249,6 +275,11 @@ struct TcParams {
   int part_rows;    // rows of a unit in the workspace
   int width;        // columns of a row there (the kernel's DH)
   int meta_vec;     // k_pos and k_doc rows are 16-byte aligned
+  int meta_heads;   // kv heads with k_pos / k_doc rows of their own (1: shared)
+  int tiles;        // key tiles of the buffer
+  const KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
+  const RowUnit* row_units;  // [B][units]
+  float2 cap_c[7];  // coefficients of cap2, each twice
   int* queue;       // next piece, pairs done (zero between launches)
   float* part_o;    // [piece][part_rows][DH], unnormalised
   float2* part_ml;  // [piece][part_rows]: m (log2), l
@@ -287,25 +318,54 @@ __device__ __forceinline__ int unit_limit(const TcParams& p, int b, int unit, in
   return min(k_len, max(max(k_len - q_len + last + 1, prefix), 0));
 }
 
+// Narrows the key tiles [first, last) to those from the first to the last one
+// with a key that some row of the unit sees (by the whole warp).
+__device__ __forceinline__ void seen_tiles(const TcParams& p, int b, int kvh, int unit, int k_len, int& first,
+                                           int& last) {
+  const KeyTile* tiles = p.key_tiles + (static_cast<int64_t>(b) * p.meta_heads + (p.meta_heads > 1 ? kvh : 0)) * p.tiles;
+  const RowUnit u = p.row_units[static_cast<int64_t>(b) * p.units + unit];
+  const int prefix = p.c.prefix ? p.c.prefix[b] : 0;
+  const int plim = max(u.pos_max + 1, prefix);
+  int lo = 0x7fffffff, hi = 0;
+  for (int t = static_cast<int>(lane_id()); t < last; t += 32) {
+    const KeyTile k = tiles[t];
+    const bool docs = !p.c.k_doc || (k.doc_min <= u.doc_max && k.doc_max >= u.doc_min);
+    const bool order = !p.c.causal || k.pos_min < plim;
+    if (docs && order) {
+      lo = min(lo, t);
+      hi = t + 1;
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  first = min(lo, hi);
+  last = hi;
+}
+
 // Whether a key tile ends behind the keys inside the buffer (rows behind the
 // buffer are zero-filled by the tensor map).
 __device__ __forceinline__ bool zero_tile(const TcParams& p, int key0, int k_len) {
   return key0 + KT > k_len && k_len < p.c.Lk;
 }
 
-// tanh on [-1, 1]: x P(x^2), P of degree 6 interpolating tanh(sqrt z) / sqrt z
-// at Chebyshev points of [0, 1] (the nearest singularity, z = -pi^2/4, makes
-// the error 5e-8 with these f32 coefficients).
-__device__ __forceinline__ float tanh_small(float x) {
-  const float z = x * x;
-  float p = 0.001038025133f;
-  p = fmaf(p, z, -0.006194324698f);
-  p = fmaf(p, z, 0.020279707387f);
-  p = fmaf(p, z, -0.053451646119f);
-  p = fmaf(p, z, 0.133250758052f);
-  p = fmaf(p, z, -0.333328276873f);
-  p = fmaf(p, z, 0.999999940395f);
-  return x * p;
+// cap log2(e) tanh(x inv) of a pair with |x inv| <= 1: t P(t^2), t = x inv, P
+// of degree 6 with coefficients c (times cap log2 e), interpolating
+// tanh(sqrt z) / sqrt z at the Chebyshev points of [0, 1]; the nearest
+// singularity, z = -pi^2 / 4, makes the error of tanh 5e-8.  Nine packed
+// instructions a pair, against two for a pair's exp and reciprocal each on the
+// special-function unit and their arithmetic.
+__device__ __forceinline__ void cap2(float& x0, float& x1, float inv, const float2* c) {
+  uint64_t x, iv, z, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(iv) : "f"(inv));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(iv));
+  asm("mul.rn.f32x2 %0, %1, %1;" : "=l"(z) : "l"(x));
+  auto pair = [](const float2& v) { return *reinterpret_cast<const uint64_t*>(&v); };
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(z), "l"(pair(c[6])), "l"(pair(c[5])));
+#pragma unroll
+  for (int k = 4; k >= 0; --k) asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(z), "l"(pair(c[k])));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
 }
 
 // FULL: the score cap, the distance bias, documents and explicit positions;
@@ -369,51 +429,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   const uint32_t pc_empty0 = mapa_shared(pc_empty, 0);
-  // The slot may be rewritten once every reader has released it: the reads
-  // must be done by then, so the release is at the scope of the writer (a
-  // CTA-scope release to the other CTA was measured to overtake them).
   auto take_piece = [&](int i, Piece& pc) -> bool {
     if (!mbar_wait_acq_cluster(&pc_full[i & 1], (i >> 1) & 1, err)) return false;
     pc.a = ld_shared_v4(&pc_slot[2 * (i & 1)]);
     pc.b = ld_shared_v4(&pc_slot[2 * (i & 1) + 1]);
-    mbar_arrive_cluster(pc_empty0 + (i & 1) * 8);
     return pc.a.x >= 0;
   };
+  // A slot may be rewritten once every reader has released it.  The reads must
+  // be done by then, so the release is at cluster scope (a CTA-scope arrive on
+  // the other CTA's barrier was seen to overtake them); as that waits for the
+  // thread's other traffic, readers release late, at the end of their piece.
+  auto release_piece = [&](int i) { mbar_arrive_cluster(pc_empty0 + (i & 1) * 8); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
     if (warp == 3 && leader) {
-      if (lane == 0) {
-        // ---------------- work queue
-        const int pairs = static_cast<int>(gridDim.x >> 1);
-        int k = static_cast<int>(blockIdx.x >> 1);
-        for (int i = 0;; ++i) {
-          Piece pc;
-          for (;; k = pairs + atomicAdd(p.queue, 1)) {
-            if (k >= p.n_pieces) {
-              pc.a = make_int4(-1, 0, 0, 0);
-              pc.b = make_int4(0, 0, 0, 0);
-              break;
-            }
-            pc.a = piece_index(p, k);
-            const int b = pc.a.x / p.c.Hkv;
-            const int nk = cache_k_len(p.c, b), nq = cache_q_len(p.c, b);
-            if (pc.a.y * 2 * p.tok_cta >= nq) continue;  // no rows
-            const int nt = (unit_limit(p, b, pc.a.y, nk, nq) + KT - 1) / KT;
-            const int t0 = static_cast<int>(static_cast<int64_t>(nt) * pc.a.z / p.nsplit);
-            const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (pc.a.z + 1) / p.nsplit);
-            pc.b = make_int4(nk, nq, t0, t1 - t0);
-            break;
-          }
-          if (i >= 2 && !mbar_wait(&pc_empty[i & 1], ((i >> 1) - 1) & 1, err, ERR_ATTN_TIMEOUT)) break;
-          for (uint32_t r = 0; r < 2; ++r) {
-            st_cluster_v4(mapa_shared(&pc_slot[2 * (i & 1)], r), pc.a);
-            st_cluster_v4(mapa_shared(&pc_slot[2 * (i & 1) + 1], r), pc.b);
-          }
-          for (uint32_t r = 0; r < 2; ++r) mbar_arrive_cluster(mapa_shared(&pc_full[i & 1], r));
-          if (pc.a.x < 0) break;
-          k = pairs + atomicAdd(p.queue, 1);
+      // ---------------- work queue (the whole warp scans the key tiles)
+      const int pairs = static_cast<int>(gridDim.x >> 1);
+      int k = static_cast<int>(blockIdx.x >> 1);
+      for (int i = 0;;) {
+        Piece pc;
+        bool rows = true;
+        pc.a = make_int4(-1, 0, 0, 0);
+        pc.b = make_int4(0, 0, 0, 0);
+        if (k < p.n_pieces) {
+          pc.a = piece_index(p, k);
+          const int b = pc.a.x / p.c.Hkv;
+          const int nk = cache_k_len(p.c, b), nq = cache_q_len(p.c, b);
+          rows = pc.a.y * 2 * p.tok_cta < nq;
+          int first = 0, last = (unit_limit(p, b, pc.a.y, nk, nq) + KT - 1) / KT;
+          if (rows && p.key_tiles) seen_tiles(p, b, pc.a.x % p.c.Hkv, pc.a.y, nk, first, last);
+          const int nt = last - first;
+          const int t0 = static_cast<int>(static_cast<int64_t>(nt) * pc.a.z / p.nsplit);
+          const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (pc.a.z + 1) / p.nsplit);
+          pc.b = make_int4(nk, nq, first + t0, t1 - t0);
         }
+        int next = 0;
+        if (lane == 0) {
+          bool ok = true;
+          if (rows) {
+            ok = i < 2 || mbar_wait(&pc_empty[i & 1], ((i >> 1) - 1) & 1, err, ERR_ATTN_TIMEOUT);
+            if (ok) {
+              for (uint32_t r = 0; r < 2; ++r) {
+                st_cluster_v4(mapa_shared(&pc_slot[2 * (i & 1)], r), pc.a);
+                st_cluster_v4(mapa_shared(&pc_slot[2 * (i & 1) + 1], r), pc.b);
+              }
+              for (uint32_t r = 0; r < 2; ++r) mbar_arrive_cluster(mapa_shared(&pc_full[i & 1], r));
+            }
+          }
+          next = ok && pc.a.x >= 0 ? pairs + atomicAdd(p.queue, 1) : -1;
+        }
+        k = __shfl_sync(0xffffffffu, next, 0);
+        if (k < 0) break;
+        if (rows) ++i;
       }
     } else if (warp == 0) {
       if (lane == 0) {
@@ -422,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t k_full0 = mapa_shared(k_full, 0);
         int gk = 0, gq = 0;
         Piece pc;
-        for (int i = 0; take_piece(i, pc); ++i) {
+        for (int i = 0; take_piece(i, pc); release_piece(i), ++i) {
           const int nT = pc.b.w;
           if (nT == 0) continue;
           const int b = pc.a.x / p.c.Hkv, hk = pc.a.x % p.c.Hkv;
@@ -467,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t v_zero0 = mapa_shared(v_zero, rank);
         int gv = 0;
         Piece pc;
-        for (int i = 0; take_piece(i, pc); ++i) {
+        for (int i = 0; take_piece(i, pc); release_piece(i), ++i) {
           const int b = pc.a.x / p.c.Hkv, hk = pc.a.x % p.c.Hkv;
           bool ok = true;
           for (int j = 0; j < pc.b.w; ++j, ++gv) {
@@ -515,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece pc;
       for (int i = 0; ok && take_piece(i, pc); ++i) {
         const int nT = pc.b.w;
+        mbar_arrive_remote(pc_empty0 + (i & 1) * 8);  // this CTA's own slot: CTA scope
         if (nT == 0) continue;
         if (!mbar_wait(q_full, gq & 1, err, ERR_ATTN_TIMEOUT) ||
             !mbar_wait(&k_full[g % KS], (g / KS) & 1, err, ERR_ATTN_TIMEOUT) ||
@@ -599,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int4 pa = ld_shared_v4(sm_piece), pb = ld_shared_v4(sm_piece + 1);
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (pa.x < 0) break;
+      if (warp == 11 && lane == 0) release_piece(i);  // every warp has the copy
       const int b = pa.x / p.c.Hkv, kvh = pa.x % p.c.Hkv;
       const int k_len = pb.x, q_len = pb.y, nT = pb.w;
       // This thread's row.
@@ -617,7 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.c.causal && !(FULL && p.c.k_pos)) klim = min(klim, max(qp + 1, prefix));
       const float slope2 = FULL && p.c.slopes && valid ? p.c.slopes[head] * kLog2e : 0.0f;
       const int64_t meta = FULL ? b * p.c.km_b + kvh * p.c.km_h : 0;
-      const bool masked = FULL && (p.c.k_doc || (p.c.causal && p.c.k_pos));
+      const bool ordered = FULL && p.c.causal && p.c.k_pos;
+      const KeyTile* tiles =
+          p.key_tiles + (static_cast<int64_t>(b) * p.meta_heads + (p.meta_heads > 1 ? kvh : 0)) * p.tiles;
       const int plim = max(qp + 1, prefix);  // positions below it are seen
       float m = -INFINITY, l = 0.0f;  // l: this thread's half of the row sum
       bool ok = true;
@@ -653,27 +725,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < nT; ++j) {
         const int t = g + j;
         const int key0 = (pb.z + j) * KT + hk16 * 128;
-        // Which of the 128 keys this row sees, one bit each (while S is made).
+        // Which of the 128 keys this row sees, one bit each (while S is made),
+        // if some row of the warp sees a part of the tile.
         uint32_t seen[4];
-        if (FULL && masked && active) {
+        bool masked = false;
+        int d0 = qp - key0;  // distance of the first key, where positions run
+        bool run = true;
+        if (FULL && p.key_tiles && active) {
+          const KeyTile kt = tiles[pb.z + j];
+          run = kt.run;
+          if (p.c.k_pos) d0 = qp - kt.base - hk16 * 128;
+          const bool doc_all = !p.c.k_doc || (kt.doc_min == qd && kt.doc_max == qd);
+          const bool pos_all = !ordered || kt.pos_max < plim;
+          masked = __any_sync(0xffffffffu, valid && !(doc_all && pos_all));
+          if (masked) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t bits = 0;
+            for (int w = 0; w < 4; ++w) {
+              uint32_t bits = 0;
 #pragma unroll 2
-            for (int c = 0; c < 32; c += 4) {
-              const int k0 = key0 + 32 * w + c;
-              uint32_t v = 15;
-              if (p.c.k_doc) {
-                const int4 d = ld_meta4(p.c.k_doc + meta, k0, k_len, p.meta_vec);
-                v = (d.x == qd) | (d.y == qd) << 1 | (d.z == qd) << 2 | (d.w == qd) << 3;
+              for (int c = 0; c < 32; c += 4) {
+                const int k0 = key0 + 32 * w + c;
+                uint32_t v = 15;
+                if (p.c.k_doc) {
+                  const int4 d = ld_meta4(p.c.k_doc + meta, k0, k_len, p.meta_vec);
+                  v = (d.x == qd) | (d.y == qd) << 1 | (d.z == qd) << 2 | (d.w == qd) << 3;
+                }
+                if (ordered) {
+                  const int4 x = ld_meta4(p.c.k_pos + meta, k0, k_len, p.meta_vec);
+                  v &= (x.x < plim) | (x.y < plim) << 1 | (x.z < plim) << 2 | (x.w < plim) << 3;
+                }
+                bits |= v << c;
               }
-              if (p.c.causal && p.c.k_pos) {
-                const int4 x = ld_meta4(p.c.k_pos + meta, k0, k_len, p.meta_vec);
-                v &= (x.x < plim) | (x.y < plim) << 1 | (x.z < plim) << 2 | (x.w < plim) << 3;
-              }
-              bits |= v << c;
+              seen[w] = bits;
             }
-            seen[w] = bits;
           }
         }
         if (ok) ok = warp_wait(s_full, t & 1, err);
@@ -708,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 128; c += 2) big = max3(big, fabsf(s[c]), fabsf(s[c + 1]));
             if (__all_sync(0xffffffffu, !valid || big * inv <= 1.0f)) {
 #pragma unroll
-              for (int c = 0; c < 128; ++c) s[c] = tanh_small(s[c] * inv) * c2;
+              for (int c = 0; c < 128; c += 2) cap2(s[c], s[c + 1], inv, p.cap_c);
             } else {
               const float two = 2.0f * kLog2e * inv;
 #pragma unroll
@@ -718,7 +802,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             sl2 = 1.0f;
           }
           if (p.c.slopes) {
-            if (p.c.k_pos) {
+            const float d = static_cast<float>(d0);
+            if (run && __all_sync(0xffffffffu, d0 >= 127 || d0 <= 0)) {
+              // The row lies on one side of all its keys: the bias is linear in c.
+              const float bs = d0 > 0 ? slope2 : -slope2, as = -bs * d;
+#pragma unroll
+              for (int c = 0; c < 128; c += 2) bias2(s[c], s[c + 1], sl2, static_cast<float>(c), bs, as);
+            } else if (run) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], sl2, -slope2 * fabsf(d - static_cast<float>(c)));
+            } else {
 #pragma unroll
               for (int c = 0; c < 128; c += 4) {
                 const int4 kp = ld_meta4(p.c.k_pos + meta, key0 + c, k_len, p.meta_vec);
@@ -727,10 +820,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s[c + 2] = fmaf(s[c + 2], sl2, -slope2 * fabsf(static_cast<float>(qp - kp.z)));
                 s[c + 3] = fmaf(s[c + 3], sl2, -slope2 * fabsf(static_cast<float>(qp - kp.w)));
               }
-            } else {
-              const float d0 = static_cast<float>(qp - key0);
-#pragma unroll
-              for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], sl2, -slope2 * fabsf(d0 - static_cast<float>(c)));
             }
             sl2 = 1.0f;
           }
@@ -887,6 +976,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// KeyTile of every key tile and RowUnit of every unit: one warp each.
+__global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant__ TcParams p, KeyTile* key_tiles,
+                                                          RowUnit* row_units) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = lane_id();
+  int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
+  const int64_t n_tiles = static_cast<int64_t>(p.c.B) * p.meta_heads * p.tiles;
+  int pmin = 0x7fffffff, pmax = -0x7fffffff - 1, dmin = pmin, dmax = pmax;
+  if (w < n_tiles) {
+    const int tile = static_cast<int>(w % p.tiles);
+    const int h = static_cast<int>(w / p.tiles % p.meta_heads), b = static_cast<int>(w / p.tiles / p.meta_heads);
+    const int n = cache_k_len(p.c, b), key0 = tile * KT;
+    const int64_t meta = b * p.c.km_b + h * p.c.km_h;
+    const int base = key0 < n ? (p.c.k_pos ? p.c.k_pos[meta + key0] : key0) : 0;
+    bool run = true;
+    for (int c = lane; c < KT && key0 + c < n; c += 32) {
+      const int pos = p.c.k_pos ? p.c.k_pos[meta + key0 + c] : key0 + c;
+      const int doc = p.c.k_doc ? p.c.k_doc[meta + key0 + c] : 0;
+      pmin = min(pmin, pos), pmax = max(pmax, pos);
+      dmin = min(dmin, doc), dmax = max(dmax, doc);
+      run = run && pos == base + c;
+    }
+    run = __all_sync(0xffffffffu, run);
+    pmin = __reduce_min_sync(0xffffffffu, pmin), pmax = __reduce_max_sync(0xffffffffu, pmax);
+    dmin = __reduce_min_sync(0xffffffffu, dmin), dmax = __reduce_max_sync(0xffffffffu, dmax);
+    if (lane == 0) key_tiles[w] = KeyTile{pmin, pmax, dmin, dmax, base, run};
+    return;
+  }
+  w -= n_tiles;
+  if (w >= static_cast<int64_t>(p.c.B) * p.units) return;
+  const int unit = static_cast<int>(w % p.units), b = static_cast<int>(w / p.units);
+  const int nk = cache_k_len(p.c, b), nq = cache_q_len(p.c, b);
+  for (int i = unit * 2 * p.tok_cta + lane; i < min(nq, (unit + 1) * 2 * p.tok_cta); i += 32) {
+    const int doc = p.c.q_doc ? p.c.q_doc[b * p.c.qm_b + i] : 0;
+    pmax = max(pmax, p.c.q_pos ? p.c.q_pos[b * p.c.qm_b + i] : nk - nq + i);
+    dmin = min(dmin, doc), dmax = max(dmax, doc);
+  }
+  pmax = __reduce_max_sync(0xffffffffu, pmax);
+  dmin = __reduce_min_sync(0xffffffffu, dmin), dmax = __reduce_max_sync(0xffffffffu, dmax);
+  if (lane == 0) row_units[w] = RowUnit{pmax, dmin, dmax, 0};
+}
+
 // Joins the shares of a row: one warp per (sequence, head, token), lanes over
 // the shares for m and l, then over the columns.  Bound by its launch and the
 // reading of nsplit rows of O.
@@ -997,7 +1129,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct TcLayout {
   int width, rows_cta, tok_cta, units, nsplit, part_rows;
   int64_t pieces;
-  size_t part_o, part_ml, total;
+  int tiles, meta_heads;  // of the buffer; 0: no positions or documents
+  size_t part_o, part_ml, key_tiles, row_units, total;
 };
 
 TcLayout tc_layout(const CacheParams& c) {
@@ -1022,6 +1155,14 @@ TcLayout tc_layout(const CacheParams& c) {
     off += up256(static_cast<size_t>(t.pieces) * t.part_rows * t.width * 4);
     t.part_ml = off;
     off += up256(static_cast<size_t>(t.pieces) * t.part_rows * 8);
+  }
+  t.tiles = (c.Lk + KT - 1) / KT;
+  t.meta_heads = c.k_pos || c.k_doc ? (c.km_h == 0 ? 1 : c.Hkv) : 0;
+  if (t.meta_heads) {
+    t.key_tiles = off;
+    off += up256(sizeof(KeyTile) * static_cast<size_t>(c.B) * t.meta_heads * t.tiles);
+    t.row_units = off;
+    off += up256(sizeof(RowUnit) * static_cast<size_t>(c.B) * t.units);
   }
   t.total = off;
   return t;
@@ -1082,12 +1223,34 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
   p.n_pieces = static_cast<int>(t.pieces), p.part_rows = t.part_rows, p.width = t.width;
   p.meta_vec = ((reinterpret_cast<uintptr_t>(c.k_pos) | reinterpret_cast<uintptr_t>(c.k_doc)) & 15) == 0 &&
                c.km_b % 4 == 0 && c.km_h % 4 == 0;
+  constexpr float kTanh[7] = {0.9999999404f, -0.3333282769f, 0.1332507581f, -0.05345164612f, 0.02027970739f, -0.006194324698f, 0.001038025133f};
+  for (int i = 0; i < 7; ++i) p.cap_c[i].x = p.cap_c[i].y = kTanh[i] * c.softcap * kLog2e;
   p.queue = reinterpret_cast<int*>(scratch) + 1;
   p.part_o = reinterpret_cast<float*>(scratch + t.part_o);
   p.part_ml = reinterpret_cast<float2*>(scratch + t.part_ml);
   const int pairs = static_cast<int>(t.pieces < sms / 2 ? t.pieces : sms / 2);
+  cudaError_t e;
+  if (t.meta_heads) {
+    p.meta_heads = t.meta_heads;
+    p.tiles = t.tiles;
+    KeyTile* kt = reinterpret_cast<KeyTile*>(scratch + t.key_tiles);
+    RowUnit* ru = reinterpret_cast<RowUnit*>(scratch + t.row_units);
+    p.key_tiles = kt;
+    p.row_units = ru;
+    const int64_t warps = static_cast<int64_t>(c.B) * (static_cast<int64_t>(t.meta_heads) * t.tiles + t.units);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, cache_tiles_kernel, p, kt, ru)) != cudaSuccess) return e;
+  }
   const bool full = c.softcap > 0 || c.slopes || c.k_doc || c.k_pos || c.q_pos;
-  cudaError_t e = t.width == 64 ? launch_dh<64>(maps, p, bf16, full, pairs, st)
+  e = t.width == 64 ? launch_dh<64>(maps, p, bf16, full, pairs, st)
                                 : launch_dh<128>(maps, p, bf16, full, pairs, st);
   if (e != cudaSuccess || t.nsplit == 1) return e;
   const int64_t rows = static_cast<int64_t>(c.B) * c.Lq * c.Hq;
