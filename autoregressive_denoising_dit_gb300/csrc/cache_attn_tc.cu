@@ -3,6 +3,8 @@
 // the kernel that joins the shares, and the launch.
 #include "cache_attn_tc.cuh"
 
+#include <cmath>
+
 namespace psv {
 
 using namespace cattn;
@@ -37,7 +39,15 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
     sorted = __all_sync(0xffffffffu, sorted);
     pmin = __reduce_min_sync(0xffffffffu, pmin), pmax = __reduce_max_sync(0xffffffffu, pmax);
     dmin = __reduce_min_sync(0xffffffffu, dmin), dmax = __reduce_max_sync(0xffffffffu, dmax);
-    if (lane == 0) key_tiles[w] = KeyTile{pmin, pmax, dmin, dmax, base, run, sorted};
+    int first = 0, other = 0;  // keys of doc_min, keys of neither end
+    for (int c = lane; c < KT && key0 + c < n; c += 32) {
+      const int doc = p.c.k_doc ? p.c.k_doc[meta + key0 + c] : 0;
+      first += doc == dmin;
+      other += doc != dmin && doc != dmax;
+    }
+    first = __reduce_add_sync(0xffffffffu, first);
+    other = __reduce_add_sync(0xffffffffu, other);
+    if (lane == 0) key_tiles[w] = KeyTile{pmin, pmax, dmin, dmax, base, run, sorted, sorted && !other ? first : -1};
     return;
   }
   w -= n_tiles;
@@ -120,6 +130,7 @@ constexpr int kPlanPairs = 76;
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct TcLayout {
+  bool few;  // at most kFewRows rows per kv head
   int width, rows_cta, tok_cta, units, nsplit, part_rows;
   int64_t pieces;
   int tiles, meta_heads;  // of the buffer; 0: no positions or documents
@@ -134,11 +145,14 @@ TcLayout tc_layout(const CacheParams& c) {
   t.units = (c.Lq + 2 * t.tok_cta - 1) / (2 * t.tok_cta);
   const int64_t rows = static_cast<int64_t>(c.Lq) * c.G;
   t.part_rows = static_cast<int>(rows < 2 * t.rows_cta ? rows : 2 * t.rows_cta);
+  t.few = rows <= kFewRows;
   // A share of n tiles reads n * 256 keys of K and V and leaves part_rows rows
   // of f32: at 256 rows as many bytes as one tile, hence five tiles at least.
-  const int tiles = (c.Lk + KT - 1) / KT / (1 + t.part_rows / 64);
+  // Few rows: a share is a CTA of four warps that take 16 keys at a time.
+  const int tiles = t.few ? (c.Lk + 63) / 64 : (c.Lk + KT - 1) / KT / (1 + t.part_rows / 64);
   const int64_t per_seq = static_cast<int64_t>(c.Hkv) * t.units;
-  const int64_t want = per_seq >= kPlanPairs ? 1 : kPlanPairs / per_seq;
+  const int units = t.few ? 2 * kPlanPairs : kPlanPairs;  // SMs, or pairs of them
+  const int64_t want = per_seq >= units ? 1 : units / per_seq;
   t.nsplit = static_cast<int>(want < tiles ? want : tiles);
   if (t.nsplit < 1) t.nsplit = 1;
   t.pieces = static_cast<int64_t>(c.B) * per_seq * t.nsplit;
@@ -150,7 +164,7 @@ TcLayout tc_layout(const CacheParams& c) {
     off += up256(static_cast<size_t>(t.pieces) * t.part_rows * 8);
   }
   t.tiles = (c.Lk + KT - 1) / KT;
-  t.meta_heads = c.k_pos || c.k_doc ? (c.km_h == 0 ? 1 : c.Hkv) : 0;
+  t.meta_heads = !t.few && (c.k_pos || c.k_doc) ? (c.km_h == 0 ? 1 : c.Hkv) : 0;
   if (t.meta_heads) {
     t.key_tiles = off;
     off += up256(sizeof(KeyTile) * static_cast<size_t>(c.B) * t.meta_heads * t.tiles);
@@ -167,9 +181,6 @@ bool map_strides_ok(const Strides3& s, int64_t nb, int64_t nl, int64_t nh) {
     if (n[i] > 1 && (st[i] <= 0 || st[i] % 8 != 0 || st[i] >= (int64_t{1} << 38))) return false;
   return true;
 }
-
-// Byte stride of an index for a tensor map (an index of extent one is never stepped).
-uint64_t map_stride(int64_t s, int64_t n) { return n > 1 ? static_cast<uint64_t>(s) * 2 : 16; }
 
 }  // namespace
 
@@ -188,8 +199,62 @@ bool cache_attn_tc_aligned(const CacheParams& c) {
 
 size_t cache_attn_tc_scratch(const CacheParams& c) { return tc_layout(c).total; }
 
+namespace {
+
+// tanh(sqrt z) / sqrt z interpolated at the Chebyshev points of [0, 1/9] and [0, 1].
+constexpr double kTanh4[4] = {0.9999999761663968, -0.33332645959641233, 0.13302166406252694, -0.04939401888519419};
+constexpr double kTanh7[7] = {0.9999999486455696, -0.3333282797859907, 0.13325076146101278, -0.05345164636973283, 0.02027970828564412, -0.006194324833673898, 0.0010380250967268723};
+
+// Coefficients of cap2 for scores s: cap log2(e) tanh(s inv) = s sum_k c_k s^(2k).
+// A polynomial whose coefficients leave f32's normal range is not used.
+int set_cap_poly(float2* out, const double* c, int n, double inv, double cap2e) {
+  double power = inv;
+  for (int k = 0; k < n; ++k, power *= inv * inv) {
+    const double v = c[k] * power * cap2e;
+    if (std::fabs(v) < 1e-36 || std::fabs(v) > 1e36) return 0;
+    out[k].x = out[k].y = static_cast<float>(v);
+  }
+  return 1;
+}
+
+void set_cap(TcParams& p) {
+  p.cap_small = p.cap_mid = -1.0f;
+  if (!(p.c.softcap > 0)) return;
+  const double inv = static_cast<double>(p.c.scale) / p.c.softcap, cap2e = p.c.softcap * 1.4426950408889634;
+  if (set_cap_poly(p.cap_c4, kTanh4, 4, inv, cap2e)) p.cap_small = static_cast<float>(1.0 / 3.0 / inv);
+  if (set_cap_poly(p.cap_c7, kTanh7, 7, inv, cap2e)) p.cap_mid = static_cast<float>(1.0 / inv);
+}
+
+cudaError_t launch_join(const TcParams& p, bool bf16, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Lq * p.c.Hq;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return bf16 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<true>, p) : cudaLaunchKernelEx(&cfg, cache_join_kernel<false>, p);
+}
+
+}  // namespace
+
 cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scratch, int sms, cudaStream_t st) {
   const TcLayout t = tc_layout(c);
+  TcParams p{};
+  p.c = c;
+  p.rows_cta = t.rows_cta, p.tok_cta = t.tok_cta, p.units = t.units, p.nsplit = t.nsplit;
+  p.n_pieces = static_cast<int>(t.pieces), p.part_rows = t.part_rows, p.width = t.width;
+  p.part_o = reinterpret_cast<float*>(scratch + t.part_o);
+  p.part_ml = reinterpret_cast<float2*>(scratch + t.part_ml);
+  cudaError_t e;
+  if (t.few) {
+    const RowsParams r{c, t.nsplit, t.part_rows, p.part_o, p.part_ml};
+    e = launch_cache_rows(r, bf16, false, st);
+    return e != cudaSuccess || t.nsplit == 1 ? e : launch_join(p, bf16, st);
+  }
   CUtensorMap maps[3];
   bool ok = true;
   {
@@ -210,19 +275,11 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
                            i && vr == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return cudaErrorInvalidValue;
-  TcParams p{};
-  p.c = c;
-  p.rows_cta = t.rows_cta, p.tok_cta = t.tok_cta, p.units = t.units, p.nsplit = t.nsplit;
-  p.n_pieces = static_cast<int>(t.pieces), p.part_rows = t.part_rows, p.width = t.width;
   p.meta_vec = ((reinterpret_cast<uintptr_t>(c.k_pos) | reinterpret_cast<uintptr_t>(c.k_doc)) & 15) == 0 &&
                c.km_b % 4 == 0 && c.km_h % 4 == 0;
-  constexpr float kTanh[7] = {0.9999999404f, -0.3333282769f, 0.1332507581f, -0.05345164612f, 0.02027970739f, -0.006194324698f, 0.001038025133f};
-  for (int i = 0; i < 7; ++i) p.cap_c[i].x = p.cap_c[i].y = kTanh[i] * c.softcap * kLog2e;
+  set_cap(p);
   p.queue = reinterpret_cast<int*>(scratch) + 1;
-  p.part_o = reinterpret_cast<float*>(scratch + t.part_o);
-  p.part_ml = reinterpret_cast<float2*>(scratch + t.part_ml);
   const int pairs = static_cast<int>(t.pieces < sms / 2 ? t.pieces : sms / 2);
-  cudaError_t e;
   if (t.meta_heads) {
     p.meta_heads = t.meta_heads;
     p.tiles = t.tiles;
@@ -247,18 +304,23 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
     e = bf16 ? launch_features<64, true>(maps, p, f, pairs, st) : launch_features<64, false>(maps, p, f, pairs, st);
   else
     e = bf16 ? launch_features<128, true>(maps, p, f, pairs, st) : launch_features<128, false>(maps, p, f, pairs, st);
-  if (e != cudaSuccess || t.nsplit == 1) return e;
-  const int64_t rows = static_cast<int64_t>(c.B) * c.Lq * c.Hq;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return bf16 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<true>, p) : cudaLaunchKernelEx(&cfg, cache_join_kernel<false>, p);
+  return e != cudaSuccess || t.nsplit == 1 ? e : launch_join(p, bf16, st);
+}
+
+bool cache_mass_tc(const CacheParams& c) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(c.q) | reinterpret_cast<uintptr_t>(c.k);
+  return c.dh <= 128 && c.dh % 8 == 0 && c.G <= QT && c.Lq > 0 && (at & 15) == 0 &&
+         map_strides_ok(c.qs, c.B, c.Lq, c.Hq) && map_strides_ok(c.ks, c.B, c.Lk, c.Hkv) &&
+         static_cast<int64_t>(c.Lq) * c.G <= kFewRows;
+}
+
+cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, int sms, cudaStream_t st) {
+  // Keys are independent: shares for two CTAs an SM, of 64 keys at least.
+  const int64_t heads = static_cast<int64_t>(c.B) * c.Hkv, most = (c.Lk + 63) / 64;
+  int64_t n = (4 * static_cast<int64_t>(sms) + heads - 1) / heads;
+  if (n > most) n = most;
+  const RowsParams r{c, static_cast<int>(n), 0, nullptr, nullptr};
+  return launch_cache_rows(r, bf16, true, st);
 }
 
 }  // namespace psv

@@ -258,11 +258,12 @@ __device__ __forceinline__ bool mbar_wait_acq_cluster(uint64_t* bar, uint32_t pa
 // before the attention where positions or documents are given: tiles that no
 // row of a unit sees are not loaded, tiles that every row sees whole are not
 // masked, and a tile of consecutive positions needs no position per key.
-struct KeyTile {
+struct alignas(16) KeyTile {
   int pos_min, pos_max, doc_min, doc_max;  // over the keys in use (min > max: none)
   int base;                                // the first key's position
   int run;                                 // positions are base, base + 1, ..
   int sorted;                              // documents do not decrease
+  int cut;  // the first `cut` keys are of doc_min, the others of doc_max; -1: not so
 };
 struct RowUnit {
   int pos_max, doc_min, doc_max, pad;
@@ -282,7 +283,8 @@ struct TcParams {
   int tiles;        // key tiles of the buffer
   const KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
   const RowUnit* row_units;  // [B][units]
-  float2 cap_c[7];  // coefficients of cap2, each twice
+  float cap_small, cap_mid;       // scores up to which the polynomials hold
+  float2 cap_c4[4], cap_c7[7];    // their coefficients, each twice
   int* queue;       // next piece, pairs done (zero between launches)
   float* part_o;    // [piece][part_rows][DH], unnormalised
   float2* part_ml;  // [piece][part_rows]: m (log2), l
@@ -365,22 +367,21 @@ __device__ __forceinline__ bool zero_tile(const TcParams& p, int key0, int k_len
   return key0 + KT > k_len && k_len < p.c.Lk;
 }
 
-// cap log2(e) tanh(x inv) of a pair with |x inv| <= 1: t P(t^2), t = x inv, P
-// of degree 6 with coefficients c (times cap log2 e), interpolating
-// tanh(sqrt z) / sqrt z at the Chebyshev points of [0, 1]; the nearest
-// singularity, z = -pi^2 / 4, makes the error of tanh 5e-8.  Nine packed
-// instructions a pair, against two for a pair's exp and reciprocal each on the
-// special-function unit and their arithmetic.
-__device__ __forceinline__ void cap2(float& x0, float& x1, float inv, const float2* c) {
-  uint64_t x, iv, z, y;
+// cap log2(e) tanh(s inv) of a pair of scores as s P(s^2), P of degree N - 1
+// with coefficients c (scaled by the powers of inv = scale / cap and by cap
+// log2 e), from interpolating tanh(sqrt z) / sqrt z at Chebyshev points: 4 of
+// [0, 1/9] for |s inv| <= 1/3 (error of tanh 1e-8), 7 of [0, 1] for |s inv|
+// <= 1 (5e-8).  The packed products are bound by the FMA pipe, which is why
+// small scores, the usual ones under a cap, have a short polynomial.
+template <int N>
+__device__ __forceinline__ void cap2(float& x0, float& x1, const float2* c) {
+  uint64_t x, z, y;
   asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(iv) : "f"(inv));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(iv));
   asm("mul.rn.f32x2 %0, %1, %1;" : "=l"(z) : "l"(x));
   auto pair = [](const float2& v) { return *reinterpret_cast<const uint64_t*>(&v); };
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(z), "l"(pair(c[6])), "l"(pair(c[5])));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(z), "l"(pair(c[N - 1])), "l"(pair(c[N - 2])));
 #pragma unroll
-  for (int k = 4; k >= 0; --k) asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(z), "l"(pair(c[k])));
+  for (int k = N - 3; k >= 0; --k) asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(z), "l"(pair(c[k])));
   asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
 }
@@ -710,6 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const KeyTile* tiles =
           p.key_tiles + (static_cast<int64_t>(b) * p.meta_heads + (p.meta_heads > 1 ? kvh : 0)) * p.tiles;
       const int plim = max(qp + 1, prefix);  // positions below it are seen
+      KeyTile kt_next{};
+      if ((F & F_META) && p.key_tiles && nT > 0) kt_next = tiles[pb.z];
       float m = -INFINITY, l = 0.0f;  // l: this thread's half of the row sum
       bool ok = true;
       // Releases the first half of a tile's P (and its V).  In a tile that ends
@@ -751,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int d0 = qp - key0;  // distance of the first key, where positions run
         bool run = true;
         if ((F & F_META) && p.key_tiles && active) {
-          const KeyTile kt = tiles[pb.z + j];
+          const KeyTile kt = kt_next;
+          if (j + 1 < nT) kt_next = tiles[pb.z + j + 1];
           run = kt.run;
           if (p.c.k_pos) d0 = qp - kt.base - hk16 * 128;
           const bool doc_all = !p.c.k_doc || (kt.doc_min == qd && kt.doc_max == qd);
@@ -761,7 +765,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The row's document is one stretch of the tile, and positions that
             // run are seen up to a limit: keys [lo, hi).
             int lo = 0, hi = min(128, k_len - key0);
-            if (p.c.k_doc) {
+            if (p.c.k_doc && kt.cut >= 0) {
+              const int cut = kt.cut - hk16 * 128;
+              if (qd != kt.doc_min) lo = qd == kt.doc_max ? cut : 128;
+              else if (qd != kt.doc_max) hi = min(hi, cut);
+            } else if (p.c.k_doc) {
               const int end = hi;
               lo = first_doc(p.c.k_doc + meta + key0, 0, end, qd);
               hi = qd == 0x7fffffff ? end : first_doc(p.c.k_doc + meta + key0, lo, end, qd + 1);
@@ -821,9 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             float big = 0.0f;
 #pragma unroll
             for (int c = 0; c < 128; c += 2) big = max3(big, fabsf(s[c]), fabsf(s[c + 1]));
-            if (__all_sync(0xffffffffu, !valid || big * inv <= 1.0f)) {
+            if (__all_sync(0xffffffffu, !valid || big <= p.cap_small)) {
 #pragma unroll
-              for (int c = 0; c < 128; c += 2) cap2(s[c], s[c + 1], inv, p.cap_c);
+              for (int c = 0; c < 128; c += 2) cap2<4>(s[c], s[c + 1], p.cap_c4);
+            } else if (__all_sync(0xffffffffu, !valid || big <= p.cap_mid)) {
+#pragma unroll
+              for (int c = 0; c < 128; c += 2) cap2<7>(s[c], s[c + 1], p.cap_c7);
             } else {
               const float two = 2.0f * kLog2e * inv;
 #pragma unroll

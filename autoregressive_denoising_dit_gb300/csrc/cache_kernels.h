@@ -42,11 +42,29 @@ __device__ __forceinline__ int cache_q_len(const CacheParams& p, int b) {
 cudaError_t launch_cache_attention_general(const CacheParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_cache_mass_general(const CacheParams& p, bool bf16, cudaStream_t st);
 
+// Byte stride of an index for a 16-bit tensor map (an index of extent one is never stepped).
+inline uint64_t map_stride(int64_t s, int64_t n) { return n > 1 ? static_cast<uint64_t>(s) * 2 : 16; }
+
+// The kernels for few rows (at most kFewRows per kv head): nsplit shares of
+// the keys, left in part_o [sequence, kv head, share][part_rows][64 or 128]
+// and part_ml (m in log2, l) where there is more than one.
+constexpr int kFewRows = 16;
+struct RowsParams {
+  CacheParams c;
+  int nsplit, part_rows;
+  float* part_o;
+  float2* part_ml;
+};
+cudaError_t launch_cache_rows(const RowsParams& p, bool bf16, bool mass, cudaStream_t st);
+
 // The tensor-core attention: which shapes it takes, which tensors, its
 // workspace (head included), and the launch on `sms` SMs.
 bool cache_attn_tc_shape(const CacheParams& p);
 bool cache_attn_tc_aligned(const CacheParams& p);
 size_t cache_attn_tc_scratch(const CacheParams& p);
 cudaError_t launch_cache_attention_tc(const CacheParams& p, bool bf16, char* scratch, int sms, cudaStream_t st);
+// The same for the mass (q and k only).
+bool cache_mass_tc(const CacheParams& p);
+cudaError_t launch_cache_mass_tc(const CacheParams& p, bool bf16, int sms, cudaStream_t st);
 
 }  // namespace psv

@@ -698,5 +698,11 @@ PSV_API int psv_cache_mass(const psv_cache_problem* p, const void* q, const void
   CacheParams c = cache_params(p, q, k, scratch);
   c.lse = const_cast<float*>(lse), c.mass_in = mass_in, c.mass_out = mass_out;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (psv::cache_mass_tc(c)) {
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = psv::launch_cache_mass_tc(c, p->dtype == PSV_DTYPE_BF16, sms, st);
+    return cuda_status(e, "mass launch");
+  }
   return cuda_status(psv::launch_cache_mass_general(c, p->dtype == PSV_DTYPE_BF16, st), "mass launch");
 }
