@@ -12,8 +12,7 @@ using namespace cattn;
 namespace {
 
 // KeyTile of every key tile and RowUnit of every unit: one warp each.
-__global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant__ TcParams p, KeyTile* key_tiles,
-                                                          RowUnit* row_units) {
+__global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant__ TcParams p) {
   pdl_trigger();
   pdl_wait();
   const int lane = lane_id();
@@ -47,7 +46,7 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
     }
     first = __reduce_add_sync(0xffffffffu, first);
     other = __reduce_add_sync(0xffffffffu, other);
-    if (lane == 0) key_tiles[w] = KeyTile{pmin, pmax, dmin, dmax, base, run, sorted, sorted && !other ? first : -1};
+    if (lane == 0) p.key_tiles[w] = KeyTile{pmin, pmax, dmin, dmax, base, run, sorted, sorted && !other ? first : -1};
     return;
   }
   w -= n_tiles;
@@ -61,7 +60,7 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
   }
   pmax = __reduce_max_sync(0xffffffffu, pmax);
   dmin = __reduce_min_sync(0xffffffffu, dmin), dmax = __reduce_max_sync(0xffffffffu, dmax);
-  if (lane == 0) row_units[w] = RowUnit{pmax, dmin, dmax, 0};
+  if (lane == 0) p.row_units[w] = RowUnit{pmax, dmin, dmax, 0};
 }
 
 // Joins the shares of a row: one warp per (sequence, head, token), lanes over
@@ -241,86 +240,88 @@ cudaError_t launch_join(const TcParams& p, bool bf16, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scratch, int sms, cudaStream_t st) {
+TcParams cattn::plan(const CacheParams& c, char* scratch) {
   const TcLayout t = tc_layout(c);
   TcParams p{};
   p.c = c;
   p.rows_cta = t.rows_cta, p.tok_cta = t.tok_cta, p.units = t.units, p.nsplit = t.nsplit;
   p.n_pieces = static_cast<int>(t.pieces), p.part_rows = t.part_rows, p.width = t.width;
+  p.meta_vec = ((reinterpret_cast<uintptr_t>(c.k_pos) | reinterpret_cast<uintptr_t>(c.k_doc)) & 15) == 0 &&
+               c.km_b % 4 == 0 && c.km_h % 4 == 0;
+  p.tiles = t.tiles;
+  p.meta_heads = t.meta_heads;
+  if (t.meta_heads) {
+    p.key_tiles = reinterpret_cast<KeyTile*>(scratch + t.key_tiles);
+    p.row_units = reinterpret_cast<RowUnit*>(scratch + t.row_units);
+  }
+  set_cap(p);
+  p.queue = reinterpret_cast<int*>(scratch) + 1;
   p.part_o = reinterpret_cast<float*>(scratch + t.part_o);
   p.part_ml = reinterpret_cast<float2*>(scratch + t.part_ml);
-  cudaError_t e;
-  if (t.few) {
-    const RowsParams r{c, t.nsplit, t.part_rows, p.part_o, p.part_ml};
-    e = launch_cache_rows(r, bf16, false, st);
-    return e != cudaSuccess || t.nsplit == 1 ? e : launch_join(p, bf16, st);
-  }
-  CUtensorMap maps[3];
+  return p;
+}
+
+bool cattn::encode_maps(CUtensorMap* maps, const CacheParams& c, const TcParams& p, bool bf16, bool values) {
   bool ok = true;
   {
     const uint64_t dims[4] = {static_cast<uint64_t>(c.dh), static_cast<uint64_t>(c.Hq),
                               static_cast<uint64_t>(c.Lq), static_cast<uint64_t>(c.B)};
     const uint64_t str[3] = {map_stride(c.qs.h, c.Hq), map_stride(c.qs.l, c.Lq), map_stride(c.qs.b, c.B)};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(c.G), static_cast<uint32_t>(t.tok_cta), 1};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(c.G), static_cast<uint32_t>(p.tok_cta), 1};
     ok &= encode_16bit_map(&maps[0], bf16, 4, const_cast<void*>(c.q), dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
   }
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < (values ? 2 : 1); ++i) {
     const Strides3& s = i ? c.vs : c.ks;
     const uint64_t dims[4] = {static_cast<uint64_t>(c.dh), static_cast<uint64_t>(c.Lk),
                               static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(c.B)};
     const uint64_t str[3] = {map_stride(s.l, c.Lk), map_stride(s.h, c.Hkv), map_stride(s.b, c.B)};
-    const uint32_t vr = static_cast<uint32_t>(t.width / 2);
+    const uint32_t vr = static_cast<uint32_t>(p.width / 2);
     const uint32_t box[4] = {i ? vr : 64u, i ? 256u : 128u, 1, 1};
     ok &= encode_16bit_map(&maps[1 + i], bf16, 4, const_cast<void*>(i ? c.v : c.k), dims, str, box,
                            i && vr == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   }
-  if (!ok) return cudaErrorInvalidValue;
-  p.meta_vec = ((reinterpret_cast<uintptr_t>(c.k_pos) | reinterpret_cast<uintptr_t>(c.k_doc)) & 15) == 0 &&
-               c.km_b % 4 == 0 && c.km_h % 4 == 0;
-  set_cap(p);
-  p.queue = reinterpret_cast<int*>(scratch) + 1;
-  const int pairs = static_cast<int>(t.pieces < sms / 2 ? t.pieces : sms / 2);
-  if (t.meta_heads) {
-    p.meta_heads = t.meta_heads;
-    p.tiles = t.tiles;
-    KeyTile* kt = reinterpret_cast<KeyTile*>(scratch + t.key_tiles);
-    RowUnit* ru = reinterpret_cast<RowUnit*>(scratch + t.row_units);
-    p.key_tiles = kt;
-    p.row_units = ru;
-    const int64_t warps = static_cast<int64_t>(c.B) * (static_cast<int64_t>(t.meta_heads) * t.tiles + t.units);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, cache_tiles_kernel, p, kt, ru)) != cudaSuccess) return e;
+  return ok;
+}
+
+cudaError_t cattn::launch_tiles(const TcParams& p, cudaStream_t st) {
+  if (!p.key_tiles) return cudaSuccess;
+  const int64_t warps = static_cast<int64_t>(p.c.B) * (static_cast<int64_t>(p.meta_heads) * p.tiles + p.units);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_tiles_kernel, p);
+}
+
+cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scratch, int sms, cudaStream_t st) {
+  const TcParams p = plan(c, scratch);
+  cudaError_t e;
+  if (static_cast<int64_t>(c.Lq) * c.G <= kFewRows) {
+    const RowsParams r{c, p.nsplit, p.part_rows, p.part_o, p.part_ml};
+    e = launch_cache_rows(r, bf16, false, st);
+    return e != cudaSuccess || p.nsplit == 1 ? e : launch_join(p, bf16, st);
   }
+  CUtensorMap maps[3];
+  if (!encode_maps(maps, c, p, bf16, true)) return cudaErrorInvalidValue;
+  if ((e = launch_tiles(p, st)) != cudaSuccess) return e;
+  const int pairs = p.n_pieces < sms / 2 ? p.n_pieces : sms / 2;
   const int f = (c.softcap > 0 ? F_CAP : 0) | (c.slopes ? F_BIAS : 0) | (c.k_doc || c.k_pos || c.q_pos ? F_META : 0);
-  if (t.width == 64)
+  if (p.width == 64)
     e = bf16 ? launch_features<64, true>(maps, p, f, pairs, st) : launch_features<64, false>(maps, p, f, pairs, st);
   else
     e = bf16 ? launch_features<128, true>(maps, p, f, pairs, st) : launch_features<128, false>(maps, p, f, pairs, st);
-  return e != cudaSuccess || t.nsplit == 1 ? e : launch_join(p, bf16, st);
+  return e != cudaSuccess || p.nsplit == 1 ? e : launch_join(p, bf16, st);
 }
 
 bool cache_mass_tc(const CacheParams& c) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(c.q) | reinterpret_cast<uintptr_t>(c.k);
-  return c.dh <= 128 && c.dh % 8 == 0 && c.G <= QT && c.Lq > 0 && (at & 15) == 0 &&
-         map_strides_ok(c.qs, c.B, c.Lq, c.Hq) && map_strides_ok(c.ks, c.B, c.Lk, c.Hkv) &&
-         static_cast<int64_t>(c.Lq) * c.G <= kFewRows;
-}
-
-cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, int sms, cudaStream_t st) {
-  // Keys are independent: shares for two CTAs an SM, of 64 keys at least.
-  const int64_t heads = static_cast<int64_t>(c.B) * c.Hkv, most = (c.Lk + 63) / 64;
-  int64_t n = (4 * static_cast<int64_t>(sms) + heads - 1) / heads;
-  if (n > most) n = most;
-  const RowsParams r{c, static_cast<int>(n), 0, nullptr, nullptr};
-  return launch_cache_rows(r, bf16, true, st);
+  return cache_attn_tc_shape(c) && static_cast<int64_t>(c.B) * c.Hkv * ((c.Lk + KT - 1) / KT) < (1 << 30) &&
+         (at & 15) == 0 && map_strides_ok(c.qs, c.B, c.Lq, c.Hq) && map_strides_ok(c.ks, c.B, c.Lk, c.Hkv);
 }
 
 }  // namespace psv

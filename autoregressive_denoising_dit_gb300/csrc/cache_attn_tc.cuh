@@ -281,8 +281,8 @@ struct TcParams {
   int meta_vec;     // k_pos and k_doc rows are 16-byte aligned
   int meta_heads;   // kv heads with k_pos / k_doc rows of their own (1: shared)
   int tiles;        // key tiles of the buffer
-  const KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
-  const RowUnit* row_units;  // [B][units]
+  KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
+  RowUnit* row_units;  // [B][units]
   float cap_small, cap_mid;       // scores up to which the polynomials hold
   float2 cap_c4[4], cap_c7[7];    // their coefficients, each twice
   int* queue;       // next piece, pairs done (zero between launches)
@@ -1071,6 +1071,13 @@ cudaError_t launch_features(const CUtensorMap* maps, const TcParams& p, int f, i
     default: return launch_one<DH, BF16, 7>(maps, p, pairs, st);
   }
 }
+
+// The description of a problem for these kernels, its maps (q, k and, with
+// `values`, v), and the kernel that fills key_tiles and row_units where there
+// are positions or documents.
+TcParams plan(const CacheParams& c, char* scratch);
+bool encode_maps(CUtensorMap* maps, const CacheParams& c, const TcParams& p, bool bf16, bool values);
+cudaError_t launch_tiles(const TcParams& p, cudaStream_t st);
 
 extern template cudaError_t launch_features<64, true>(const CUtensorMap*, const TcParams&, int, int, cudaStream_t);
 extern template cudaError_t launch_features<64, false>(const CUtensorMap*, const TcParams&, int, int, cudaStream_t);

@@ -65,6 +65,6 @@ size_t cache_attn_tc_scratch(const CacheParams& p);
 cudaError_t launch_cache_attention_tc(const CacheParams& p, bool bf16, char* scratch, int sms, cudaStream_t st);
 // The same for the mass (q and k only).
 bool cache_mass_tc(const CacheParams& p);
-cudaError_t launch_cache_mass_tc(const CacheParams& p, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_cache_mass_tc(const CacheParams& p, bool bf16, char* scratch, int sms, cudaStream_t st);
 
 }  // namespace psv

@@ -701,7 +701,7 @@ PSV_API int psv_cache_mass(const psv_cache_problem* p, const void* q, const void
   if (psv::cache_mass_tc(c)) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
-    if (e == cudaSuccess) e = psv::launch_cache_mass_tc(c, p->dtype == PSV_DTYPE_BF16, sms, st);
+    if (e == cudaSuccess) e = psv::launch_cache_mass_tc(c, p->dtype == PSV_DTYPE_BF16, static_cast<char*>(scratch), sms, st);
     return cuda_status(e, "mass launch");
   }
   return cuda_status(psv::launch_cache_mass_general(c, p->dtype == PSV_DTYPE_BF16, st), "mass launch");
