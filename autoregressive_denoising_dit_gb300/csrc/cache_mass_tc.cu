@@ -269,7 +269,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 3) {
-    // ---------------- columns of the row tiles (every lane reads the piece)
+    // ---------------- columns of the row tiles (every lane reads the piece).  A
+    // lane notes columns 32 x + lane of both halves; their tokens and heads
+    // within a tile are the same for every tile.
+    int dtok[4], dhead[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = x * 32 + lane;
+      dtok[x] = r < p.rows_cta ? r / p.c.G : 0x40000000;  // never below q_len
+      dhead[x] = r % p.c.G;
+    }
+    const bool given = p.c.q_pos || p.c.q_doc || p.c.slopes;
     int g = 0;
     Piece pc;
     for (int i = 0;; ++i) {
@@ -278,9 +288,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) release_piece(i);
       const int b = pc.a.x / p.c.Hkv, kvh = pc.a.x % p.c.Hkv, nk = pc.b.x, nq = pc.b.y;
       const int prefix = p.c.prefix ? p.c.prefix[b] : 0;
+      const float* lse = p.c.lse + (static_cast<int64_t>(b) * p.c.Hq + kvh * p.c.G) * p.c.Lq;
       bool ok = true;
       for (int j = 0; j < pc.a.w; ++j, ++g) {
         const int st = g % QS;
+        // The reads of lse are on their way while the stage is waited for.
+        const int tok0 = (pc.a.z + j) * 2 * p.tok_cta;
+        float nl[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int tok = tok0 + (x >> 2) * p.tok_cta + dtok[x & 3];
+          nl[x] = tok < nq ? __ldg(lse + static_cast<int64_t>(dhead[x & 3]) * p.c.Lq + tok) : -INFINITY;
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(&c_empty[st], ((g / QS) & 1) ^ 1, err, ERR_ATTN_TIMEOUT))) {
           ok = false;
           break;
@@ -290,26 +309,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pl_min = 0x7fffffff, d_min = 0x7fffffff, d_max = -0x7fffffff - 1;
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const int r = (x & 3) * 32 + lane, half = x >> 2;
-          const int tok = ((pc.a.z + j) * 2 + half) * p.tok_cta + r / p.c.G;
-          const int head = kvh * p.c.G + r % p.c.G;
-          const bool valid = r < p.rows_cta && tok < nq;
-          float nl = -INFINITY, ns = 0.0f;
-          int qp = 0, pl = -0x7fffffff - 1, qd = 0;
-          if (valid) {
-            const float l = p.c.lse[(static_cast<int64_t>(b) * p.c.Hq + head) * p.c.Lq + tok];
-            if (l != -INFINITY) nl = -l * kLog2e;
-            qp = p.c.q_pos ? p.c.q_pos[b * p.c.qm_b + tok] : nk - nq + tok;
-            pl = p.c.causal ? max(qp + 1, prefix) : 0x7fffffff;
+          const int tok = tok0 + (x >> 2) * p.tok_cta + dtok[x & 3];
+          const int at = (x >> 2) * kHalf + (x & 3) * 32 + lane;
+          const bool valid = tok < nq;
+          int qp = nk - nq + tok, qd = 0;
+          float ns = 0.0f;
+          if (given && valid) {
+            if (p.c.q_pos) qp = p.c.q_pos[b * p.c.qm_b + tok];
             if (p.c.q_doc) qd = p.c.q_doc[b * p.c.qm_b + tok];
-            if (p.c.slopes) ns = -p.c.slopes[head] * kLog2e;
+            if (p.c.slopes) ns = -p.c.slopes[kvh * p.c.G + dhead[x & 3]] * kLog2e;
+          }
+          int pl = p.c.causal ? max(qp + 1, prefix) : 0x7fffffff;
+          if (valid) {
             pl_min = min(pl_min, pl);
             d_min = min(d_min, qd), d_max = max(d_max, qd);
-          } else if (r < p.rows_cta && tok < p.c.Lq) {
-            pl_min = -0x7fffffff - 1;  // an unused row may hold NaN: its columns are masked one by one
+          } else {
+            pl = -0x7fffffff - 1;
+            // An unused row may hold NaN: its columns are masked one by one.
+            if (tok < p.c.Lq) pl_min = pl;
           }
-          const int at = half * kHalf + r;
-          col[COL_NLSE * kColWords + at] = nl;
+          col[COL_NLSE * kColWords + at] = nl[x] != -INFINITY ? -nl[x] * kLog2e : -INFINITY;
           icol[COL_PLIM * kColWords + at] = pl;
           if (p.c.slopes) {
             col[COL_NSLOPE * kColWords + at] = ns;
@@ -318,8 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.c.q_doc) icol[COL_DOC * kColWords + at] = qd;
         }
         pl_min = __reduce_min_sync(0xffffffffu, pl_min);
-        d_min = __reduce_min_sync(0xffffffffu, d_min);
-        d_max = __reduce_max_sync(0xffffffffu, d_max);
+        if (p.c.q_doc) {
+          d_min = __reduce_min_sync(0xffffffffu, d_min);
+          d_max = __reduce_max_sync(0xffffffffu, d_max);
+        }
         if (lane == 0) {
           int* stat = icol + COL_ARRAYS * kColWords;
           stat[0] = pl_min, stat[1] = d_min, stat[2] = d_max;
