@@ -147,8 +147,8 @@ TcLayout tc_layout(const CacheParams& c) {
   t.few = rows <= kFewRows;
   // A share of n tiles reads n * 256 keys of K and V and leaves part_rows rows
   // of f32: at 256 rows as many bytes as one tile, hence five tiles at least.
-  // Few rows: a share is a CTA of four warps that take 16 keys at a time.
-  const int tiles = t.few ? (c.Lk + 63) / 64 : (c.Lk + KT - 1) / KT / (1 + t.part_rows / 64);
+  // Few rows: a share is a CTA of four warps that take 32 keys at a time.
+  const int tiles = t.few ? (c.Lk + 127) / 128 : (c.Lk + KT - 1) / KT / (1 + t.part_rows / 64);
   const int64_t per_seq = static_cast<int64_t>(c.Hkv) * t.units;
   const int units = t.few ? 2 * kPlanPairs : kPlanPairs;  // SMs, or pairs of them
   const int64_t want = per_seq >= units ? 1 : units / per_seq;
@@ -302,7 +302,7 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
   const TcParams p = plan(c, scratch);
   cudaError_t e;
   if (static_cast<int64_t>(c.Lq) * c.G <= kFewRows) {
-    const RowsParams r{c, p.nsplit, p.part_rows, p.part_o, p.part_ml};
+    const RowsParams r{c, p.nsplit, p.part_rows, p.n_pieces, sms, p.part_o, p.part_ml};
     e = launch_cache_rows(r, bf16, false, st);
     return e != cudaSuccess || p.nsplit == 1 ? e : launch_join(p, bf16, st);
   }

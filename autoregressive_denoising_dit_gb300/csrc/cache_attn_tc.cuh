@@ -70,8 +70,8 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + kStages * K_BYTES;
   static constexpr int OFF_BAR = OFF_V + kStages * V_BYTES;
   static constexpr int N_BARS = 13 + 5 * kStages;  // an even number
-  // barriers, TMEM address, two published piece slots and the softmax's copy
-  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + 6 * 16;
+  // barriers, TMEM address, two published piece slots and the softmax's copies
+  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + 8 * 16;
   static constexpr int OH = DH / 2;             // O columns per thread
   static constexpr int OC = 32;                 // O columns per TMEM access
 };
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_zero = v_empty + KS;  // [KS] own: a V tile to be zeroed behind the keys landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   int4* pc_slot = reinterpret_cast<int4*>(smem + C::OFF_BAR + C::N_BARS * 8 + 16);  // [2][2]
-  int4* sm_piece = pc_slot + 4;                                                            // [2]
+  int4* sm_piece = pc_slot + 4;                                                            // [2][2]
   static_assert((C::N_BARS * 8) % 16 == 0, "the piece slots are 16-byte aligned");
 
   pdl_trigger();
@@ -680,13 +680,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 4 && lane == 0) {
         Piece pc;
         if (!take_piece(i, pc)) pc.a.x = -1;
-        sm_piece[0] = pc.a;
-        sm_piece[1] = pc.b;
+        sm_piece[2 * (i & 1)] = pc.a;
+        sm_piece[2 * (i & 1) + 1] = pc.b;
       }
-      __syncwarp();  // the barriers and TMEM accesses below are for whole warps
+      __syncwarp();  // the barrier and the TMEM accesses below are for whole warps
+      // (A copy is rewritten two pieces later, behind a barrier that its readers passed.)
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      const int4 pa = ld_shared_v4(sm_piece), pb = ld_shared_v4(sm_piece + 1);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int4 pa = ld_shared_v4(sm_piece + 2 * (i & 1)), pb = ld_shared_v4(sm_piece + 2 * (i & 1) + 1);
       if (pa.x < 0) break;
       if (warp == 11 && lane == 0) release_piece(i);  // every warp has the copy
       const int b = pa.x / p.c.Hkv, kvh = pa.x % p.c.Hkv;

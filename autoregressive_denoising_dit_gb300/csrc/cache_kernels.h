@@ -52,6 +52,7 @@ constexpr int kFewRows = 16;
 struct RowsParams {
   CacheParams c;
   int nsplit, part_rows;
+  int n_pieces, ctas;  // pieces: sequences x kv heads x shares; CTAs at most
   float* part_o;
   float2* part_ml;
 };

@@ -56,7 +56,8 @@ __device__ __forceinline__ void ffma2v(float& x0, float& x1, float s, float b0, 
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
 }
 
-template <int DH, bool BF16>
+// F: F_CAP, F_BIAS (kernels of their own keep the loop within the instruction cache).
+template <int DH, bool BF16, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ TcParams p) {
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   int4* pc_slot = reinterpret_cast<int4*>(smem + C::OFF_BAR + C::N_BARS * 8 + 16);  // [2][3]
   static_assert((C::N_BARS * 8) % 16 == 0, "the piece slots are 16-byte aligned");
-  int4* sm_piece = pc_slot + 6;                                                      // [2]
+  int4* sm_piece = pc_slot + 4;                                                      // [2][2]
 
   pdl_trigger();
   const int warp = warp_id(), lane = lane_id();
@@ -365,13 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 4 && lane == 0) {
         Piece pc;
         if (!take_piece(i, pc)) pc.a.x = -1;
-        sm_piece[0] = pc.a;
-        sm_piece[1] = pc.b;
+        sm_piece[2 * (i & 1)] = pc.a;
+        sm_piece[2 * (i & 1) + 1] = pc.b;
       }
       __syncwarp();
+      // (A copy is rewritten two pieces later, behind a barrier that its readers passed.)
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      const int4 pa = ld_shared_v4(sm_piece), pb = ld_shared_v4(sm_piece + 1);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int4 pa = ld_shared_v4(sm_piece + 2 * (i & 1)), pb = ld_shared_v4(sm_piece + 2 * (i & 1) + 1);
       if (pa.x < 0) break;
       if (warp == 11 && lane == 0) release_piece(i);
       __syncwarp();
@@ -399,17 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool masked = __any_sync(0xffffffffu, valid && !whole);
         const bool unused = stat[0] == -0x7fffffff - 1;
         const uint32_t s_addr = tmem + sb * 256 + lane_off;
-        float s[2][32];
-        tmem_ld32x<128>(s_addr, s[0]);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tmem_wait_ld();
-          if (ch < 3) tmem_ld32x<128>(s_addr + (ch + 1) * 32, s[(ch + 1) & 1]);
-          float* v = s[ch & 1];
+        // 32 columns at a time, the next ones on their way from TMEM meanwhile.
+        auto add_chunk = [&](float* v, int ch) {
           const float* cc = col + half * kHalf + ch * 32;
           const int* ic = reinterpret_cast<const int*>(cc);
           float sc = scale2;
-          if (p.c.softcap > 0) {
+          if constexpr ((F & F_CAP) != 0) {
             const float two = 2.0f * kLog2e * inv;
             float big = 0.0f;
 #pragma unroll
@@ -424,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sc = 1.0f;
           }
-          if (p.c.slopes) {
+          if constexpr ((F & F_BIAS) != 0) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 ns = *reinterpret_cast<const float4*>(cc + COL_NSLOPE * kColWords + e);
@@ -456,6 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             fadd2(acc[(e & 4)], acc[(e & 4) + 1], fast_exp2(v[e]), fast_exp2(v[e + 1]));
             fadd2(acc[(e & 4) + 2], acc[(e & 4) + 3], fast_exp2(v[e + 2]), fast_exp2(v[e + 3]));
           }
+        };
+        float s0[32], s1[32];
+        tmem_ld32x<128>(s_addr, s0);
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ch += 2) {
+          tmem_wait_ld();
+          tmem_ld32x<128>(s_addr + (ch + 1) * 32, s1);
+          add_chunk(s0, ch);
+          tmem_wait_ld();
+          if (ch == 0) tmem_ld32x<128>(s_addr + 64, s0);
+          add_chunk(s1, ch + 1);
         }
         tc_fence_before();
         __syncwarp();
@@ -489,14 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int DH, bool BF16>
+template <int DH, bool BF16, int F>
 cudaError_t launch(const CUtensorMap* maps, const TcParams& p, int pairs, cudaStream_t st) {
   static uint64_t set_up = 0;
   // More than half an SM's shared memory: one CTA per SM, so its TMEM is free.
   const size_t smem = MCfg<DH>::SMEM > 120 * 1024 ? MCfg<DH>::SMEM : 120 * 1024;
   static_assert(MCfg<DH>::SMEM <= 232448, "over the per-block limit");
   cudaError_t e = once_per_device(&set_up, [&](int) {
-    return cudaFuncSetAttribute(cache_mass_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(cache_mass_kernel<DH, BF16, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
@@ -514,18 +521,25 @@ cudaError_t launch(const CUtensorMap* maps, const TcParams& p, int pairs, cudaSt
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, cache_mass_kernel<DH, BF16>, maps[0], maps[1], p);
+  return cudaLaunchKernelEx(&cfg, cache_mass_kernel<DH, BF16, F>, maps[0], maps[1], p);
+}
+
+template <int DH, bool BF16>
+cudaError_t launch_any(const CUtensorMap* maps, const TcParams& p, int pairs, cudaStream_t st) {
+  if (p.c.softcap > 0)
+    return p.c.slopes ? launch<DH, BF16, F_CAP | F_BIAS>(maps, p, pairs, st) : launch<DH, BF16, F_CAP>(maps, p, pairs, st);
+  return p.c.slopes ? launch<DH, BF16, F_BIAS>(maps, p, pairs, st) : launch<DH, BF16, 0>(maps, p, pairs, st);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, char* scratch, int sms, cudaStream_t st) {
   if (static_cast<int64_t>(c.Lq) * c.G <= kFewRows) {
-    // Keys are independent: shares for two CTAs an SM twice over, of 64 keys at least.
-    const int64_t heads = static_cast<int64_t>(c.B) * c.Hkv, most = (c.Lk + 63) / 64;
+    // Keys are independent: about four pieces an SM, of 128 keys at least.
+    const int64_t heads = static_cast<int64_t>(c.B) * c.Hkv, most = (c.Lk + 127) / 128;
     int64_t n = (4 * static_cast<int64_t>(sms) + heads - 1) / heads;
     if (n > most) n = most;
-    const RowsParams r{c, static_cast<int>(n), 0, nullptr, nullptr};
+    const RowsParams r{c, static_cast<int>(n), 0, static_cast<int>(heads * n), sms, nullptr, nullptr};
     return launch_cache_rows(r, bf16, true, st);
   }
   TcParams p = plan(c, scratch);
@@ -536,8 +550,8 @@ cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, char* scratch,
   cudaError_t e = launch_tiles(p, st);
   if (e != cudaSuccess) return e;
   const int pairs = p.n_pieces < sms / 2 ? p.n_pieces : sms / 2;
-  if (p.width == 64) return bf16 ? launch<64, true>(maps, p, pairs, st) : launch<64, false>(maps, p, pairs, st);
-  return bf16 ? launch<128, true>(maps, p, pairs, st) : launch<128, false>(maps, p, pairs, st);
+  if (p.width == 64) return bf16 ? launch_any<64, true>(maps, p, pairs, st) : launch_any<64, false>(maps, p, pairs, st);
+  return bf16 ? launch_any<128, true>(maps, p, pairs, st) : launch_any<128, false>(maps, p, pairs, st);
 }
 
 }  // namespace psv

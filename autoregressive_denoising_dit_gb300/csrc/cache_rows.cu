@@ -2,12 +2,14 @@
 // a draft of tokens, shared heads: at most 16 rows per kv head).
 //
 // Bound by reading K (and V) once: a 16-row tile of mma.sync products costs
-// less than the memory traffic of its keys, and needs no TMEM, no cluster and
-// no block-wide barrier.  A CTA of four warps takes one (sequence, kv head)
-// and an equal share of its keys; a warp owns every fourth tile of 16 keys,
-// brought in by TMA through a ring of its own (kStages tiles in flight), and
-// keeps its own running maximum, sum and output; the four are joined in shared
-// memory at the end, the shares by cache_join_kernel.  Two CTAs an SM.
+// less than the memory traffic of its keys and needs no TMEM and no cluster.
+// Persistent CTAs, one an SM, take pieces (a sequence, a kv head and one of
+// nsplit equal shares of its keys) in turn.  A producer warp brings tiles of 32
+// keys by TMA into a ring of each of the four consumer warps (kStages tiles in
+// flight a ring, across the ends of pieces); a consumer keeps its own running
+// maximum, sum and output over every fourth tile.  The four are joined in
+// shared memory at the end of a piece, the shares by cache_join_kernel.  The
+// next piece's queries are read while the current one runs.
 #include <cuda.h>
 
 #include "../../include/psv.h"
@@ -19,17 +21,23 @@ namespace psv {
 
 namespace {
 
-constexpr int kWarps = 4, kKeys = 16, kStages = 3;
+constexpr int kWarps = 4;  // consumers
+constexpr int kKeys = 32;  // keys of a tile
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 template <int DH, bool MASS>
 struct RCfg {
   static constexpr int NA = DH / 64;
-  static constexpr int ATOM = kKeys * 128;                        // 16 rows of 128 bytes
-  static constexpr int STAGE = NA * ATOM * (MASS ? 1 : 2);        // K, then V
-  static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr size_t SMEM = RING + 1024 + kWarps * kStages * 8;
+  static constexpr int ATOM = kKeys * 128;                  // 32 rows of 128 bytes
+  static constexpr int STAGE = NA * ATOM * (MASS ? 1 : 2);  // K, then V
+  static constexpr int STAGES = MASS ? 6 : 3;
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int OFF_JOIN = RING;                     // [warp][16][DH], then m and l
+  static constexpr int JOIN = MASS ? 0 : kWarps * 16 * (DH + 2) * 4;
+  static constexpr int OFF_BAR = OFF_JOIN + JOIN;
+  static constexpr size_t SMEM = OFF_BAR + kWarps * STAGES * 16;
 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
@@ -93,274 +101,357 @@ struct Row {
   bool valid;
 };
 
-template <int DH, bool BF16, bool MASS>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-    cache_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const __grid_constant__ RowsParams p) {
-  using C = RCfg<DH, MASS>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // swizzled tiles
-  const CacheParams& c = p.c;
-  const int warp = warp_id(), lane = lane_id();
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING) + warp * kStages;
-  uint8_t* ring = smem + warp * kStages * C::STAGE;
-  pdl_trigger();
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
-  pdl_wait();
-  const int share = blockIdx.x % p.nsplit, bh = blockIdx.x / p.nsplit;
-  const int b = bh / c.Hkv, kvh = bh % c.Hkv;
-  const int k_len = cache_k_len(c, b), q_len = cache_q_len(c, b);
-  if (q_len == 0 && !MASS) return;
-  const int rows = q_len * c.G;
-  const int prefix = c.prefix ? c.prefix[b] : 0;
-  const int nt = (k_len + kKeys - 1) / kKeys;
-  const int t0 = static_cast<int>(static_cast<int64_t>(nt) * share / p.nsplit) + warp;
-  const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (share + 1) / p.nsplit);
-  auto load = [&](int t, int st) {  // by one lane
-    uint8_t* dst = ring + st * C::STAGE;
-    mbar_arrive_expect_tx(&full[st], C::STAGE);
-#pragma unroll
-    for (int a = 0; a < C::NA; ++a) {
-      tma_load_4d(dst + a * C::ATOM, &tmK, &full[st], a * 64, t * kKeys, kvh, b);
-      if (!MASS) tma_load_4d(dst + (C::NA + a) * C::ATOM, &tmV, &full[st], a * 64, t * kKeys, kvh, b);
-    }
-  };
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-      if (t0 + i * kWarps < t1) load(t0 + i * kWarps, i);
-  }
-
-  // Q as A fragments: rows lane / 4 and + 8, columns 2 (lane % 4) + {0, 1, 8, 9} of a step of 16.
+// A piece and, for this thread's two rows, their queries as A fragments (rows
+// lane / 4 and + 8; columns 2 (lane % 4) + {0, 1, 8, 9} of a step of 16).
+template <int DH>
+struct Work {
+  int b, kvh, share, k_len, q_len, t0, t1;
   uint32_t qf[DH / 16][4];
   Row row[2];
   float lse2[2];
+};
+
+template <bool MASS>
+__device__ __forceinline__ void piece_tiles(const RowsParams& p, int piece, int& b, int& kvh, int& share, int& k_len,
+                                            int& t0, int& t1) {
+  share = piece % p.nsplit;
+  const int bh = piece / p.nsplit;
+  b = bh / p.c.Hkv, kvh = bh % p.c.Hkv;
+  k_len = cache_k_len(p.c, b);
+  const int nt = (k_len + kKeys - 1) / kKeys;
+  t0 = static_cast<int>(static_cast<int64_t>(nt) * share / p.nsplit);
+  t1 = static_cast<int>(static_cast<int64_t>(nt) * (share + 1) / p.nsplit);
+}
+
+template <int DH, bool MASS>
+__device__ __forceinline__ void load_work(const RowsParams& p, int piece, int lane, Work<DH>& w) {
+  const CacheParams& c = p.c;
+  piece_tiles<MASS>(p, piece, w.b, w.kvh, w.share, w.k_len, w.t0, w.t1);
+  w.q_len = cache_q_len(c, w.b);
+  const int prefix = c.prefix ? c.prefix[w.b] : 0;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int r = lane / 4 + 8 * e, tok = r / c.G, head = kvh * c.G + r % c.G;
-    row[e].valid = r < rows;
-    const uint16_t* q = static_cast<const uint16_t*>(c.q) + b * c.qs.b + tok * c.qs.l + head * c.qs.h;
+    const int r = lane / 4 + 8 * e, tok = r / c.G, head = w.kvh * c.G + r % c.G;
+    Row& row = w.row[e];
+    row.valid = r < w.q_len * c.G;
+    const uint16_t* q = static_cast<const uint16_t*>(c.q) + w.b * c.qs.b + tok * c.qs.l + head * c.qs.h;
 #pragma unroll
     for (int k = 0; k < DH / 16; ++k) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int d = k * 16 + x * 8 + 2 * (lane % 4);
-        qf[k][e + 2 * x] = row[e].valid && d < c.dh ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+        w.qf[k][e + 2 * x] = row.valid && d < c.dh ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
       }
     }
-    row[e].qp = k_len - q_len + tok;
-    row[e].qd = 0;
-    row[e].slope2 = 0.0f;
-    lse2[e] = INFINITY;
-    if (row[e].valid) {
-      if (c.q_pos) row[e].qp = c.q_pos[b * c.qm_b + tok];
-      if (c.q_doc) row[e].qd = c.q_doc[b * c.qm_b + tok];
-      if (c.slopes) row[e].slope2 = c.slopes[head] * kLog2e;
+    row.qp = w.k_len - w.q_len + tok;
+    row.qd = 0;
+    row.slope2 = 0.0f;
+    w.lse2[e] = INFINITY;
+    if (row.valid) {
+      if (c.q_pos) row.qp = c.q_pos[w.b * c.qm_b + tok];
+      if (c.q_doc) row.qd = c.q_doc[w.b * c.qm_b + tok];
+      if (c.slopes) row.slope2 = c.slopes[head] * kLog2e;
       if (MASS) {
-        const float l = c.lse[(static_cast<int64_t>(b) * c.Hq + head) * c.Lq + tok];
-        if (l != -INFINITY) lse2[e] = l * kLog2e;
+        const float l = c.lse[(static_cast<int64_t>(w.b) * c.Hq + head) * c.Lq + tok];
+        if (l != -INFINITY) w.lse2[e] = l * kLog2e;
       }
     }
-    row[e].plim = c.causal ? max(row[e].qp + 1, prefix) : 0x7fffffff;  // positions below it are seen
-    row[e].klim = c.k_pos ? k_len : min(k_len, max(row[e].plim, 0));
+    row.plim = c.causal ? max(row.qp + 1, prefix) : 0x7fffffff;  // positions below it are seen
+    row.klim = c.k_pos ? w.k_len : min(w.k_len, max(row.plim, 0));
   }
-  const float scale2 = c.scale * kLog2e;
-  const int64_t meta = b * c.km_b + kvh * c.km_h;
+}
 
-  float o[MASS ? 1 : DH / 8][4];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  if (!MASS) {
-#pragma unroll
-    for (int n = 0; n < DH / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+template <int DH, bool BF16, bool MASS>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ RowsParams p) {
+  using C = RCfg<DH, MASS>;
+  constexpr int ST = C::STAGES;
+  extern __shared__ uint8_t smem[];
+  const CacheParams& c = p.c;
+  if (smem_u32(smem) & 1023) {  // swizzled tiles
+    if (threadIdx.x == 0) raise_error(c.err, ERR_BOUNDS);
+    return;
   }
+  const int warp = warp_id(), lane = lane_id();
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [warp][ST]
+  uint64_t* empty = full + kWarps * ST;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * kWarps * ST; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tmK);
+    if (!MASS) prefetch_tensormap(&tmV);
+  }
+  __syncthreads();
+  pdl_wait();
+
+  if (warp == kWarps) {
+    // ---------------- producer: one lane
+    if (lane == 0) {
+      uint32_t used[kWarps] = {};  // tiles a ring got
+      bool ok = true;
+      for (int piece = blockIdx.x; piece < p.n_pieces && ok; piece += gridDim.x) {
+        int b, kvh, share, k_len, t0, t1;
+        piece_tiles<MASS>(p, piece, b, kvh, share, k_len, t0, t1);
+        for (int t = t0; t < t1 && ok; t += kWarps) {
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            if (t + w < t1 && ok) {
+              const int st = static_cast<int>(used[w] % ST);
+              uint64_t* bar = &full[w * ST + st];
+              ok = mbar_wait(&empty[w * ST + st], ((used[w] / ST) & 1) ^ 1, c.err, ERR_ATTN_TIMEOUT);
+              if (ok) {
+                uint8_t* dst = smem + (w * ST + st) * C::STAGE;
+                mbar_arrive_expect_tx(bar, C::STAGE);
+#pragma unroll
+                for (int a = 0; a < C::NA; ++a)
+                  tma_load_4d(dst + a * C::ATOM, &tmK, bar, a * 64, (t + w) * kKeys, kvh, b);
+                if (!MASS) {
+#pragma unroll
+                  for (int a = 0; a < C::NA; ++a)
+                    tma_load_4d(dst + (C::NA + a) * C::ATOM, &tmV, bar, a * 64, (t + w) * kKeys, kvh, b);
+                }
+                ++used[w];
+              }
+            }
+          }
+        }
+      }
+      // No copy may be in flight when the CTA exits (bounded; consumers have
+      // waited for all of them unless one gave up).
+      const uint64_t begin = global_timer_ns();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        for (uint32_t k = used[w] > ST ? used[w] - ST : 0; k < used[w]; ++k)
+          while (!mbar_try_wait(&full[w * ST + k % ST], (k / ST) & 1) && global_timer_ns() - begin < kWaitLimitNs) {
+          }
+    }
+    return;
+  }
+
+  // ---------------- consumers
+  const float scale2 = c.scale * kLog2e;
+  uint8_t* ring = smem + warp * ST * C::STAGE;
+  int i = 0;  // tiles of this warp so far
   bool ok = true;
-  int i = 0;
-  for (int t = t0; t < t1; t += kWarps, ++i) {
-    const int st = i % kStages;
-    // Every lane waits: it reads what the TMA wrote.
-    ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / kStages) & 1, c.err, ERR_ATTN_TIMEOUT));
-    if (!ok) break;
-    uint8_t* tile = ring + st * C::STAGE;
-    const int key0 = t * kKeys;
-    float s[2][4];  // keys 8 n + 2 (lane % 4) + {0, 1}, rows lane / 4 and + 8
+  int piece = blockIdx.x;
+  Work<DH> w, next;
+  if (piece < p.n_pieces) load_work<DH, MASS>(p, piece, lane, w);
+  for (; piece < p.n_pieces; piece += gridDim.x) {
+    if (piece + gridDim.x < p.n_pieces) load_work<DH, MASS>(p, piece + gridDim.x, lane, next);
+    const int64_t meta = w.b * c.km_b + w.kvh * c.km_h;
+    const int k_len = w.k_len;
+    float o[MASS ? 1 : DH / 8][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    if (!MASS) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < DH / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-    {
-      const int key = (lane / 16) * 8 + lane % 8;
-      const uint32_t base = smem_u32(tile) + key * 128;
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+    }
+    for (int t = w.t0 + warp; t < w.t1; t += kWarps, ++i) {
+      const int st = i % ST;
+      // Every lane waits: it reads what the TMA wrote.  After a failed wait the
+      // warp only keeps up the barriers below.
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[warp * ST + st], (i / ST) & 1, c.err, ERR_ATTN_TIMEOUT));
+      if (!ok) continue;
+      uint8_t* tile = ring + st * C::STAGE;
+      const int key0 = t * kKeys;
+      float s[4][4];  // keys 8 n + 2 (lane % 4) + {0, 1}, rows lane / 4 and + 8
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
 #pragma unroll
       for (int k = 0; k < DH / 16; ++k) {
         const int chunk = k * 2 + (lane / 8) % 2;
-        uint32_t bf[4];
-        ldmatrix4(bf, base + (chunk / 8) * C::ATOM + (((chunk % 8) ^ (key & 7)) << 4));
-        mma16<BF16>(s[0], qf[k], bf[0], bf[1]);
-        mma16<BF16>(s[1], qf[k], bf[2], bf[3]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int key = 16 * g + (lane / 16) * 8 + lane % 8;
+          uint32_t bf[4];
+          ldmatrix4(bf, smem_u32(tile) + key * 128 + (chunk / 8) * C::ATOM + (((chunk % 8) ^ (key & 7)) << 4));
+          mma16<BF16>(s[2 * g], w.qf[k], bf[0], bf[1]);
+          mma16<BF16>(s[2 * g + 1], w.qf[k], bf[2], bf[3]);
+        }
       }
-    }
-    // Scores in the log2 domain, -inf where the row does not see the key.
+      // Scores in the log2 domain, -inf where the row does not see the key.
+      if (c.softcap > 0) {
+        const float c2 = c.softcap * kLog2e, two = 2.0f * kLog2e * c.scale / c.softcap;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int j = key0 + 8 * n + 2 * (lane % 4) + x;
-        const int jc = min(j, k_len - 1);
-        const int kp = c.k_pos ? c.k_pos[meta + jc] : j;
-        const int kd = c.k_doc ? c.k_doc[meta + jc] : 0;
+          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(-2.0f * c2, fast_rcp(1.0f + fast_exp2(s[n][e] * two)), c2);
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] *= scale2;
+      }
+      if (c.slopes || c.k_pos || c.k_doc) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int j = key0 + 8 * n + 2 * (lane % 4) + x, jc = min(j, k_len - 1);
+            const int kp = c.k_pos ? c.k_pos[meta + jc] : j;
+            const int kd = c.k_doc ? c.k_doc[meta + jc] : 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = s[n][2 * e + x];
+              v -= w.row[e].slope2 * fabsf(static_cast<float>(w.row[e].qp - kp));
+              if (kp >= w.row[e].plim || (c.k_doc && kd != w.row[e].qd)) v = -INFINITY;
+            }
+          }
+        }
+      }
+      if (key0 + kKeys > min(w.row[0].klim, w.row[1].klim)) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + 8 * n + 2 * (lane % 4) + e % 2 >= w.row[e / 2].klim) s[n][e] = -INFINITY;
+      }
+      if constexpr (MASS) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float v = fast_exp2(s[n][x] - w.lse2[0]) + fast_exp2(s[n][2 + x] - w.lse2[1]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            s[n][x] = v;
+          }
+        // Lane 4 n + x of the first 16 writes keys 8 n + 2 x + {0, 1}.
+        float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (lane / 4 == n) v = make_float2(s[n][0], s[n][1]);
+        const int j = key0 + 8 * (lane / 4) + 2 * (lane % 4);
+        if (lane < 16) {
+          const int64_t at = (static_cast<int64_t>(w.b) * c.Hkv + w.kvh) * c.Lk + j;
+          if (j < k_len) c.mass_out[at] = (c.mass_in ? c.mass_in[at] : 0.0f) + v.x;
+          if (j + 1 < k_len) c.mass_out[at + 1] = (c.mass_in ? c.mass_in[at + 1] : 0.0f) + v.y;
+        }
+      } else {
+        uint32_t pf[2][4];
+        float a[2];
+        bool grow = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = s[n][2 * e + x];
-          if (c.softcap > 0) {
-            const float c2 = c.softcap * kLog2e;
-            v = fmaf(-2.0f * c2, fast_rcp(1.0f + fast_exp2(v * (2.0f * kLog2e * c.scale / c.softcap))), c2);
-          } else {
-            v *= scale2;
+          float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+          mx = fmaxf(mx, fmaxf(fmaxf(s[2][2 * e], s[2][2 * e + 1]), fmaxf(s[3][2 * e], s[3][2 * e + 1])));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          a[e] = 1.0f;
+          if (mx > m[e] + kRescaleThreshold) {
+            a[e] = fast_exp2(m[e] - mx);
+            m[e] = mx;
+            grow = true;
           }
-          if (c.slopes) v -= row[e].slope2 * fabsf(static_cast<float>(row[e].qp - kp));
-          const bool sees = j < row[e].klim && kp < row[e].plim && (!c.k_doc || kd == row[e].qd);
-          s[n][2 * e + x] = sees ? v : -INFINITY;
+          const float m0 = m[e] == -INFINITY ? 0.0f : m[e];
+          float sum = 0.0f;
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float x = fast_exp2(s[n][2 * e] - m0), y = fast_exp2(s[n][2 * e + 1] - m0);
+            sum += x + y;
+            pf[n / 2][e + 2 * (n % 2)] = pack2<BF16>(x, y);
+          }
+          l[e] = l[e] * a[e] + sum;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int n = 0; n < DH / 8; ++n) {
+            o[n][0] *= a[0], o[n][1] *= a[0];
+            o[n][2] *= a[1], o[n][3] *= a[1];
+          }
+        }
+        if (key0 + kKeys > k_len) {
+          // Values behind the keys may be NaN: their weight is 0, but 0 * NaN is not.
+          for (int e = (k_len - key0) * 8 + lane; e < kKeys * 8; e += 32)
+#pragma unroll
+            for (int x = 0; x < C::NA; ++x)
+              *reinterpret_cast<uint4*>(tile + (C::NA + x) * C::ATOM + e * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();  // the ring's next copy lands after these
+          __syncwarp();
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int key = 16 * g + (lane / 8 % 2) * 8 + lane % 8;
+          const uint32_t base = smem_u32(tile) + C::NA * C::ATOM + key * 128;
+#pragma unroll
+          for (int n = 0; n < DH / 16; ++n) {
+            const int chunk = n * 2 + lane / 16;
+            uint32_t bf[4];
+            ldmatrix4_t(bf, base + (chunk / 8) * C::ATOM + (((chunk % 8) ^ (key & 7)) << 4));
+            mma16<BF16>(o[2 * n], pf[g], bf[0], bf[1]);
+            mma16<BF16>(o[2 * n + 1], pf[g], bf[2], bf[3]);
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(smem_u32(&empty[warp * ST + st]));
     }
-    if constexpr (MASS) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float w = fast_exp2(s[n][x] - lse2[0]) + fast_exp2(s[n][2 + x] - lse2[1]);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-          const int j = key0 + 8 * n + 2 * (lane % 4) + x;
-          if (lane < 4 && j < k_len) {
-            const int64_t at = (static_cast<int64_t>(b) * c.Hkv + kvh) * c.Lk + j;
-            c.mass_out[at] = (c.mass_in ? c.mass_in[at] : 0.0f) + w;
-          }
-        }
-    } else {
-      uint32_t pf[4];
-      float a[2];
-      bool grow = false;
+    if constexpr (!MASS) {
+      // Join the four warps.
+      float* so = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+      float* sm = so + kWarps * 16 * DH;
+      const int rows = w.q_len * c.G;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        a[e] = 1.0f;
-        if (mx > m[e] + kRescaleThreshold) {
-          a[e] = fast_exp2(m[e] - mx);
-          m[e] = mx;
-          grow = true;
-        }
-        const float m0 = m[e] == -INFINITY ? 0.0f : m[e];
-        float sum = 0.0f;
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        const int r = lane / 4 + 8 * e;
+        if (r < rows) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float x = fast_exp2(s[n][2 * e] - m0), y = fast_exp2(s[n][2 * e + 1] - m0);
-          sum += x + y;
-          pf[e + 2 * n] = pack2<BF16>(x, y);
-        }
-        l[e] = l[e] * a[e] + sum;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int n = 0; n < DH / 8; ++n) {
-          o[n][0] *= a[0], o[n][1] *= a[0];
-          o[n][2] *= a[1], o[n][3] *= a[1];
+          for (int n = 0; n < DH / 8; ++n)
+            *reinterpret_cast<float2*>(so + (warp * 16 + r) * DH + n * 8 + 2 * (lane % 4)) =
+                make_float2(o[n][2 * e], o[n][2 * e + 1]);
+          if (lane % 4 == 0) {
+            sm[(warp * 16 + r) * 2] = m[e];
+            sm[(warp * 16 + r) * 2 + 1] = l[e];
+          }
         }
       }
-      if (key0 + kKeys > k_len) {
-        // Values behind the keys may be NaN: their weight is 0, but 0 * NaN is not.
-        for (int e = (k_len - key0) * 8 + lane; e < kKeys * 8; e += 32)
+      __syncwarp();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      for (int u = threadIdx.x; u < rows * (DH / 4); u += kWarps * 32) {
+        const int r = u / (DH / 4), d = u % (DH / 4) * 4;
+        float mm = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < C::NA; ++x)
-            *reinterpret_cast<uint4*>(tile + (C::NA + x) * C::ATOM + e * 16) = make_uint4(0, 0, 0, 0);
-        __syncwarp();
-      }
-      const int key = (lane / 8 % 2) * 8 + lane % 8;
-      const uint32_t base = smem_u32(tile) + C::NA * C::ATOM + key * 128;
+        for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sm[(x * 16 + r) * 2]);
+        const float m0 = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int n = 0; n < DH / 16; ++n) {
-        const int chunk = n * 2 + lane / 16;
-        uint32_t bf[4];
-        ldmatrix4_t(bf, base + (chunk / 8) * C::ATOM + (((chunk % 8) ^ (key & 7)) << 4));
-        mma16<BF16>(o[2 * n], pf, bf[0], bf[1]);
-        mma16<BF16>(o[2 * n + 1], pf, bf[2], bf[3]);
+        for (int x = 0; x < kWarps; ++x) {
+          const float f = fast_exp2(sm[(x * 16 + r) * 2] - m0);
+          const float4 y = *reinterpret_cast<const float4*>(so + (x * 16 + r) * DH + d);
+          ll = fmaf(f, sm[(x * 16 + r) * 2 + 1], ll);
+          acc.x = fmaf(f, y.x, acc.x);
+          acc.y = fmaf(f, y.y, acc.y);
+          acc.z = fmaf(f, y.z, acc.z);
+          acc.w = fmaf(f, y.w, acc.w);
+        }
+        const int tok = r / c.G, head = w.kvh * c.G + r % c.G;
+        if (p.nsplit > 1) {
+          const int64_t prow = static_cast<int64_t>(piece) * p.part_rows + r;
+          *reinterpret_cast<float4*>(p.part_o + prow * DH + d) = acc;
+          if (d == 0) p.part_ml[prow] = make_float2(mm, ll);
+        } else {
+          const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+          if (d < c.dh)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.o) + w.b * c.os.b + tok * c.os.l + head * c.os.h + d) =
+                make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+          if (d == 0 && c.lse)
+            c.lse[(static_cast<int64_t>(w.b) * c.Hq + head) * c.Lq + tok] =
+                ll > 0.0f ? (mm + fast_log2(ll)) * kLn2 : -INFINITY;
+        }
       }
+      __syncwarp();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
     }
-    __syncwarp();
-    if (lane == 0 && t + kStages * kWarps < t1) load(t + kStages * kWarps, st);
-  }
-  if (!ok) {
-    // No copy of this warp may be left when its shared memory is given up: wait
-    // (bounded) for those issued behind the failed one.
-    const uint64_t begin = global_timer_ns();
-    for (int k = i + 1; k < i + kStages && t0 + k * kWarps < t1; ++k)
-      while (!mbar_try_wait(&full[k % kStages], (k / kStages) & 1) && global_timer_ns() - begin < kWaitLimitNs) {
-      }
-  }
-  if constexpr (!MASS) {
-    // Join the four warps: O [warp][16][DH], then m and l, over the rings.
-    float* so = reinterpret_cast<float*>(smem);
-    float* sm = so + kWarps * 16 * DH;
-    static_assert(kWarps * 16 * (DH + 2) * 4 <= C::RING, "the join fits the rings");
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = lane / 4 + 8 * e;
-#pragma unroll
-      for (int n = 0; n < DH / 8; ++n)
-        *reinterpret_cast<float2*>(so + (warp * 16 + r) * DH + n * 8 + 2 * (lane % 4)) =
-            make_float2(o[n][2 * e], o[n][2 * e + 1]);
-      if (lane % 4 == 0) {
-        sm[(warp * 16 + r) * 2] = m[e];
-        sm[(warp * 16 + r) * 2 + 1] = l[e];
-      }
-    }
-    __syncthreads();
-    for (int u = threadIdx.x; u < rows * (DH / 4); u += kWarps * 32) {
-      const int r = u / (DH / 4), d = u % (DH / 4) * 4;
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm[(w * 16 + r) * 2]);
-      const float m0 = mm == -INFINITY ? 0.0f : mm;
-      float ll = 0.0f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = fast_exp2(sm[(w * 16 + r) * 2] - m0);
-        const float4 x = *reinterpret_cast<const float4*>(so + (w * 16 + r) * DH + d);
-        ll = fmaf(f, sm[(w * 16 + r) * 2 + 1], ll);
-        acc.x = fmaf(f, x.x, acc.x);
-        acc.y = fmaf(f, x.y, acc.y);
-        acc.z = fmaf(f, x.z, acc.z);
-        acc.w = fmaf(f, x.w, acc.w);
-      }
-      const int tok = r / c.G, head = kvh * c.G + r % c.G;
-      if (p.nsplit > 1) {
-        const int64_t prow = (static_cast<int64_t>(bh) * p.nsplit + share) * p.part_rows + r;
-        *reinterpret_cast<float4*>(p.part_o + prow * DH + d) = acc;
-        if (d == 0) p.part_ml[prow] = make_float2(mm, ll);
-      } else {
-        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-        if (d < c.dh)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.o) + b * c.os.b + tok * c.os.l + head * c.os.h + d) =
-              make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-        if (d == 0 && c.lse)
-          c.lse[(static_cast<int64_t>(b) * c.Hq + head) * c.Lq + tok] = ll > 0.0f ? (mm + fast_log2(ll)) * kLn2 : -INFINITY;
-      }
-    }
+    w = next;
   }
 }
 
@@ -368,7 +459,7 @@ template <int DH, bool BF16, bool MASS>
 cudaError_t launch_rows(const CUtensorMap* maps, const RowsParams& p, cudaStream_t st) {
   static uint64_t set_up = 0;
   using C = RCfg<DH, MASS>;
-  static_assert(2 * (C::SMEM + 1024) <= 228 * 1024, "two CTAs an SM");
+  static_assert(C::SMEM <= 232448, "over the per-block limit");
   cudaError_t e = once_per_device(&set_up, [&](int) {
     return cudaFuncSetAttribute(cache_rows_kernel<DH, BF16, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(C::SMEM));
@@ -378,8 +469,8 @@ cudaError_t launch_rows(const CUtensorMap* maps, const RowsParams& p, cudaStream
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv * p.nsplit));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_pieces < p.ctas ? p.n_pieces : p.ctas));
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
