@@ -5,11 +5,13 @@
 // less than the memory traffic of its keys and needs no TMEM and no cluster.
 // Persistent CTAs, one an SM, take pieces (a sequence, a kv head and one of
 // nsplit equal shares of its keys) in turn.  A producer warp brings tiles of 32
-// keys by TMA into a ring of each of the four consumer warps (kStages tiles in
-// flight a ring, across the ends of pieces); a consumer keeps its own running
-// maximum, sum and output over every fourth tile.  The four are joined in
-// shared memory at the end of a piece, the shares by cache_join_kernel.  The
-// next piece's queries are read while the current one runs.
+// keys by TMA into a ring of stages, across the ends of pieces; each of seven
+// consumer warps keeps its own running maximum, sum and output over every
+// seventh tile of a piece (the chain from a tile's scores to its weights takes
+// about 1 us, so fewer warps would bound it, not the memory).  The seven are
+// joined in shared memory at the end of a piece, the shares by
+// cache_join_kernel.  The next piece's queries are read while the current one
+// runs.
 #include <cuda.h>
 
 #include "../../include/psv.h"
@@ -21,7 +23,7 @@ namespace psv {
 
 namespace {
 
-constexpr int kWarps = 4;  // consumers
+constexpr int kWarps = 7;  // consumers (with the producer eight: two an SM quarter, 255 registers each)
 constexpr int kKeys = 32;  // keys of a tile
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -32,12 +34,14 @@ struct RCfg {
   static constexpr int NA = DH / 64;
   static constexpr int ATOM = kKeys * 128;                  // 32 rows of 128 bytes
   static constexpr int STAGE = NA * ATOM * (MASS ? 1 : 2);  // K, then V
-  static constexpr int STAGES = MASS ? 6 : 3;
-  static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int OFF_JOIN = RING;                     // [warp][16][DH], then m and l
-  static constexpr int JOIN = MASS ? 0 : kWarps * 16 * (DH + 2) * 4;
+  static constexpr int JOIN = MASS ? 0 : kWarps * 16 * (DH + 2) * 4;  // [warp][16][DH], then m and l
+  static constexpr int STAGES = MASS ? 2 * kWarps : 10;
+  static constexpr int OFF_JOIN = STAGES * STAGE;
   static constexpr int OFF_BAR = OFF_JOIN + JOIN;
-  static constexpr size_t SMEM = OFF_BAR + kWarps * STAGES * 16;
+  static constexpr size_t SMEM = OFF_BAR + (2 * kWarps + STAGES) * 8;
+  // A warp's tiles are kWarps apart, so that two of them at most are under way:
+  // two barriers a warp tell it of its own tiles, one phase after the other.
+  static_assert(STAGES <= 2 * kWarps, "two tiles of a warp in the ring at most");
 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
@@ -111,6 +115,13 @@ struct Work {
   float lse2[2];
 };
 
+// Of a tile's 32 keys, the one whose summed weight ends up in this lane: the
+// lane's upper three bits choose among the eight keys 8 n + 2 (lane % 4) + x.
+__device__ __forceinline__ int mass_key(int lane) {
+  const int k = lane >> 2;  // bit 2 (lane 16): n's upper bit, bit 1 (8): n's lower bit, bit 0 (4): x
+  return 8 * (k >> 1) + 2 * (lane % 4) + (k & 1);
+}
+
 template <bool MASS>
 __device__ __forceinline__ void piece_tiles(const RowsParams& p, int piece, int& b, int& kvh, int& share, int& k_len,
                                             int& t0, int& t1) {
@@ -174,11 +185,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int warp = warp_id(), lane = lane_id();
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [warp][ST]
-  uint64_t* empty = full + kWarps * ST;
+  // Tile g (counted over the CTA's pieces) goes to stage g % ST and to warp g %
+  // kWarps, whose tiles are told by its two barriers in turn.
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [kWarps][2]
+  uint64_t* empty = full + 2 * kWarps;                              // [ST]
+  auto full_of = [&](uint32_t g) { return &full[2 * (g % kWarps) + (g / kWarps) % 2]; };
+  auto full_parity = [](uint32_t g) { return (g / (2 * kWarps)) & 1; };
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * kWarps * ST; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2 * kWarps + ST; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
     prefetch_tensormap(&tmK);
     if (!MASS) prefetch_tensormap(&tmV);
@@ -189,51 +204,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarps) {
     // ---------------- producer: one lane
     if (lane == 0) {
-      uint32_t used[kWarps] = {};  // tiles a ring got
+      uint32_t g = 0;  // tiles so far
       bool ok = true;
       for (int piece = blockIdx.x; piece < p.n_pieces && ok; piece += gridDim.x) {
         int b, kvh, share, k_len, t0, t1;
         piece_tiles<MASS>(p, piece, b, kvh, share, k_len, t0, t1);
-        for (int t = t0; t < t1 && ok; t += kWarps) {
+        for (int t = t0; t < t1; ++t, ++g) {
+          const uint32_t st = g % ST;
+          if (!(ok = mbar_wait(&empty[st], ((g / ST) & 1) ^ 1, c.err, ERR_ATTN_TIMEOUT))) break;
+          uint8_t* dst = smem + st * C::STAGE;
+          uint64_t* bar = full_of(g);
+          mbar_arrive_expect_tx(bar, C::STAGE);
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            if (t + w < t1 && ok) {
-              const int st = static_cast<int>(used[w] % ST);
-              uint64_t* bar = &full[w * ST + st];
-              ok = mbar_wait(&empty[w * ST + st], ((used[w] / ST) & 1) ^ 1, c.err, ERR_ATTN_TIMEOUT);
-              if (ok) {
-                uint8_t* dst = smem + (w * ST + st) * C::STAGE;
-                mbar_arrive_expect_tx(bar, C::STAGE);
+          for (int a = 0; a < C::NA; ++a) tma_load_4d(dst + a * C::ATOM, &tmK, bar, a * 64, t * kKeys, kvh, b);
+          if (!MASS) {
 #pragma unroll
-                for (int a = 0; a < C::NA; ++a)
-                  tma_load_4d(dst + a * C::ATOM, &tmK, bar, a * 64, (t + w) * kKeys, kvh, b);
-                if (!MASS) {
-#pragma unroll
-                  for (int a = 0; a < C::NA; ++a)
-                    tma_load_4d(dst + (C::NA + a) * C::ATOM, &tmV, bar, a * 64, (t + w) * kKeys, kvh, b);
-                }
-                ++used[w];
-              }
-            }
+            for (int a = 0; a < C::NA; ++a)
+              tma_load_4d(dst + (C::NA + a) * C::ATOM, &tmV, bar, a * 64, t * kKeys, kvh, b);
           }
         }
       }
-      // No copy may be in flight when the CTA exits (bounded; consumers have
+      // No copy may be in flight when the CTA exits (bounded; the consumers have
       // waited for all of them unless one gave up).
       const uint64_t begin = global_timer_ns();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        for (uint32_t k = used[w] > ST ? used[w] - ST : 0; k < used[w]; ++k)
-          while (!mbar_try_wait(&full[w * ST + k % ST], (k / ST) & 1) && global_timer_ns() - begin < kWaitLimitNs) {
-          }
+      for (uint32_t k = g > ST ? g - ST : 0; k < g; ++k)
+        while (!mbar_try_wait(full_of(k), full_parity(k)) && global_timer_ns() - begin < kWaitLimitNs) {
+        }
     }
     return;
   }
 
   // ---------------- consumers
   const float scale2 = c.scale * kLog2e;
-  uint8_t* ring = smem + warp * ST * C::STAGE;
-  int i = 0;  // tiles of this warp so far
+  uint32_t g0 = 0;  // tiles of earlier pieces
   bool ok = true;
   int piece = blockIdx.x;
   Work<DH> w, next;
@@ -250,14 +253,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     }
-    for (int t = w.t0 + warp; t < w.t1; t += kWarps, ++i) {
-      const int st = i % ST;
+    for (uint32_t g = g0 + (warp + kWarps - g0 % kWarps) % kWarps; g < g0 + (w.t1 - w.t0); g += kWarps) {
+      const uint32_t st = g % ST;
+      const int t = w.t0 + static_cast<int>(g - g0);
+      const int key0 = t * kKeys;
+      float old = 0.0f;
+      const int jm = key0 + mass_key(lane);  // MASS: the key that this lane writes
+      const int64_t at = (static_cast<int64_t>(w.b) * c.Hkv + w.kvh) * c.Lk + jm;
+      if (MASS && c.mass_in && jm < k_len) old = c.mass_in[at];
       // Every lane waits: it reads what the TMA wrote.  After a failed wait the
       // warp only keeps up the barriers below.
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[warp * ST + st], (i / ST) & 1, c.err, ERR_ATTN_TIMEOUT));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(full_of(g), full_parity(g), c.err, ERR_ATTN_TIMEOUT));
       if (!ok) continue;
-      uint8_t* tile = ring + st * C::STAGE;
-      const int key0 = t * kKeys;
+      uint8_t* tile = smem + st * C::STAGE;
       float s[4][4];  // keys 8 n + 2 (lane % 4) + {0, 1}, rows lane / 4 and + 8
 #pragma unroll
       for (int n = 0; n < 4; ++n)
@@ -313,26 +321,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (key0 + 8 * n + 2 * (lane % 4) + e % 2 >= w.row[e / 2].klim) s[n][e] = -INFINITY;
       }
       if constexpr (MASS) {
+        // Eight keys a lane (of four lanes), summed over the eight lanes that hold
+        // their rows: each step halves the keys that a lane still carries.
+        float v[8];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float v = fast_exp2(s[n][x] - w.lse2[0]) + fast_exp2(s[n][2 + x] - w.lse2[1]);
+          for (int x = 0; x < 2; ++x)
+            v[2 * n + x] = fast_exp2(s[n][x] - w.lse2[0]) + fast_exp2(s[n][2 + x] - w.lse2[1]);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-            s[n][x] = v;
+        for (int d = 16, cnt = 4; d >= 4; d >>= 1, cnt >>= 1) {
+          const bool up = lane & d;
+#pragma unroll
+          for (int k = 0; k < cnt; ++k) {
+            const float give = up ? v[k] : v[k + cnt], keep = up ? v[k + cnt] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
           }
-        // Lane 4 n + x of the first 16 writes keys 8 n + 2 x + {0, 1}.
-        float2 v = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if (lane / 4 == n) v = make_float2(s[n][0], s[n][1]);
-        const int j = key0 + 8 * (lane / 4) + 2 * (lane % 4);
-        if (lane < 16) {
-          const int64_t at = (static_cast<int64_t>(w.b) * c.Hkv + w.kvh) * c.Lk + j;
-          if (j < k_len) c.mass_out[at] = (c.mass_in ? c.mass_in[at] : 0.0f) + v.x;
-          if (j + 1 < k_len) c.mass_out[at + 1] = (c.mass_in ? c.mass_in[at + 1] : 0.0f) + v.y;
         }
+        if (jm < k_len) c.mass_out[at] = old + v[0];
       } else {
         uint32_t pf[2][4];
         float a[2];
@@ -390,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(smem_u32(&empty[warp * ST + st]));
+      if (lane == 0) mbar_arrive_remote(smem_u32(&empty[st]));
     }
     if constexpr (!MASS) {
-      // Join the four warps.
+      // Join the seven warps.
       float* so = reinterpret_cast<float*>(smem + C::OFF_JOIN);
       float* sm = so + kWarps * 16 * DH;
       const int rows = w.q_len * c.G;
@@ -414,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, 224;" ::: "memory");
       for (int u = threadIdx.x; u < rows * (DH / 4); u += kWarps * 32) {
         const int r = u / (DH / 4), d = u % (DH / 4) * 4;
         float mm = -INFINITY;
@@ -449,8 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, 224;" ::: "memory");
     }
+    g0 += w.t1 - w.t0;
     w = next;
   }
 }
