@@ -32,6 +32,8 @@ int cache_fail(int code, const char* fmt, ...) {
 using psv::cache_fail;
 using psv::CacheParams;
 using psv::Strides3;
+using psv::pdl_trigger;
+using psv::pdl_wait;
 
 namespace {
 
@@ -199,33 +201,43 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
 #pragma unroll
   for (int i = 0; i < PR; ++i)
     cs[i] = pair_angle(p, HALVES ? (rot ? d0 + i : p.R) : d0 / 2 + i, b, l);
+  // kFlight heads' loads are on their way at a time.
+  constexpr int kFlight = HALVES ? 2 : 4;
   const int h1 = min(p.H, (hg + 1) * p.hpt);
-  for (int h = hg * p.hpt; h < h1; ++h) {
-    V a;
-    a.load(x + h * p.xs.h);
-    if constexpr (HALVES) {
-      if (rot) {
-        V c;
-        c.load(x + h * p.xs.h + p.R / 2);
+  for (int h0 = hg * p.hpt; h0 < h1; h0 += kFlight) {
+    V a[kFlight], c[HALVES ? kFlight : 1];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float f = to_f(a.v[i]), g = to_f(c.v[i]);
-          from_f(a.v[i], f * cs[i].x - g * cs[i].y);
-          from_f(c.v[i], f * cs[i].y + g * cs[i].x);
-        }
-        c.store(o + h * p.os.h + p.R / 2);
+    for (int k = 0; k < kFlight; ++k)
+      if (h0 + k < h1) {
+        a[k].load(x + (h0 + k) * p.xs.h);
+        if constexpr (HALVES)
+          if (rot) c[k].load(x + (h0 + k) * p.xs.h + p.R / 2);
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) {
-        if (2 * (d0 / 2 + i) < p.R) {  // values behind R are copied bit for bit
-          const float f = to_f(a.v[2 * i]), g = to_f(a.v[2 * i + 1]);
-          from_f(a.v[2 * i], f * cs[i].x - g * cs[i].y);
-          from_f(a.v[2 * i + 1], f * cs[i].y + g * cs[i].x);
+    for (int k = 0; k < kFlight; ++k) {
+      if (h0 + k >= h1) break;
+      if constexpr (HALVES) {
+        if (rot) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float f = to_f(a[k].v[i]), g = to_f(c[k].v[i]);
+            from_f(a[k].v[i], f * cs[i].x - g * cs[i].y);
+            from_f(c[k].v[i], f * cs[i].y + g * cs[i].x);
+          }
+          c[k].store(o + (h0 + k) * p.os.h + p.R / 2);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+          if (2 * (d0 / 2 + i) < p.R) {  // values behind R are copied bit for bit
+            const float f = to_f(a[k].v[2 * i]), g = to_f(a[k].v[2 * i + 1]);
+            from_f(a[k].v[2 * i], f * cs[i].x - g * cs[i].y);
+            from_f(a[k].v[2 * i + 1], f * cs[i].y + g * cs[i].x);
+          }
         }
       }
+      a[k].store(o + (h0 + k) * p.os.h);
     }
-    a.store(o + h * p.os.h);
   }
 }
 
@@ -322,10 +334,12 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   const bool vec = multiple16(x, p->x_stride, p->B, p->L, p->H, size) &&
                    multiple16(out, p->out_stride, p->B, p->L, p->H, size) && p->dh % N == 0 &&
                    (!halves || ((R / 2) % N == 0 && (p->dh - R) % N == 0));
-  // Few rows: a thread per head and unit; many: four heads share the angles.
-  const int64_t rows = static_cast<int64_t>(p->B) * p->L;
-  k.hpt = rows * p->H * (p->dh / N) >= (1 << 18) ? 4 : 1;
+  // A thread's angles serve as many heads as leave about 512 threads an SM.
+  const int64_t all = static_cast<int64_t>(p->B) * p->L * p->H * (p->dh / (vec ? N : 2));
+  const int64_t hpt = all / (152 * 512);
+  k.hpt = static_cast<int>(hpt < 1 ? 1 : hpt > p->H ? p->H : hpt > 16 ? 16 : hpt);
   k.hgroups = (p->H + k.hpt - 1) / k.hpt;
+  k.hpt = (p->H + k.hgroups - 1) / k.hgroups;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
   if (p->dtype == PSV_DTYPE_F32)
@@ -393,20 +407,105 @@ __device__ __forceinline__ void block_scan2(int& a, int& b, int* sm) {
   b = y - b + sm[32 + w];
 }
 
-// One CTA per (sequence, kv head): the budget-th greatest key by radix
-// selection, 8 bits a pass, then the kept slots in order by one scan over
-// contiguous shares of the slots.
+// What the select kernels write for a kept slot j at place `at` of its row.
+__device__ __forceinline__ void keep_slot(const EvictParams& p, const float* mass, int64_t row, int64_t meta, int at,
+                                          int j) {
+  p.idx[row + at] = j;
+  p.mass_out[row + at] = mass[j];
+  if (p.pos_out) p.pos_out[row + at] = p.k_pos ? p.k_pos[meta + j] : j;
+  if (p.doc_out) p.doc_out[row + at] = p.k_doc[meta + j];
+}
+
+// One CTA per (sequence, kv head) with up to 1024 KPT slots: every thread holds
+// KPT consecutive slots' keys in registers, the keep-th greatest key is found
+// two bits at a time by counting, and one scan gives the kept slots their
+// places.  Bound by latency: 16 rounds of compare, warp sum and barrier.
+template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  __shared__ int scan[64];
+  __shared__ int count[2][4];
+  pdl_trigger();
+  pdl_wait();
+  const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, t = threadIdx.x;
+  const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
+  const int keep = min(n, p.budget);
+  const float* mass = p.mass + (static_cast<int64_t>(b) * p.H + h) * p.L;
+  uint32_t key[KPT];
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) key[i] = t * KPT + i < n ? select_key(p, mass, t * KPT + i, n) : 0u;
+  if (t < 8) count[t / 4][t % 4] = 0;
+  __syncthreads();
+  // thr: the greatest value that at least `keep` keys reach (0 if all stay; no
+  // key of a slot is 0, as only a negative NaN's complement would be).
+  uint32_t thr = 0;
+  int above = 0;  // keys over thr
+  if (keep < n) {
+    for (int shift = 30, r = 0; shift >= 0; shift -= 2, r ^= 1) {
+      int c1 = 0, c2 = 0, c3 = 0;
+      const uint32_t v1 = thr | 1u << shift, v2 = thr | 2u << shift, v3 = thr | 3u << shift;
+#pragma unroll
+      for (int i = 0; i < KPT; ++i) {
+        c1 += key[i] >= v1;
+        c2 += key[i] >= v2;
+        c3 += key[i] >= v3;
+      }
+      c1 = __reduce_add_sync(0xffffffffu, c1);
+      c2 = __reduce_add_sync(0xffffffffu, c2);
+      c3 = __reduce_add_sync(0xffffffffu, c3);
+      if ((t & 31) == 0) {
+        atomicAdd(&count[r][1], c1);
+        atomicAdd(&count[r][2], c2);
+        atomicAdd(&count[r][3], c3);
+      }
+      __syncthreads();
+      c1 = count[r][1], c2 = count[r][2], c3 = count[r][3];
+      if (c3 >= keep) thr = v3;
+      else if (c2 >= keep) thr = v2, above = c3;
+      else if (c1 >= keep) thr = v1, above = c2;
+      else above = c1;
+      if (t < 4) count[r ^ 1][t] = 0;
+      __syncthreads();
+    }
+  }
+  const int need = keep - above;  // of the keys equal to thr
+  int over = 0, ties = 0;
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const bool in = t * KPT + i < n;
+    over += in && (keep == n || key[i] > thr);
+    ties += in && keep < n && key[i] == thr;
+  }
+  block_scan2(over, ties, scan);
+  const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.budget;
+  const int64_t meta = b * p.km_b + h * p.km_h;
+  int at = over + min(ties, need);
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const int j = t * KPT + i;
+    if (j >= n) break;
+    bool k = keep == n || key[i] > thr;
+    if (!k && key[i] == thr) k = ties++ < need;
+    if (k) keep_slot(p, mass, row, meta, at++, j);
+  }
+  if (h == 0 && t == 0 && p.lens_out) p.lens_out[b] = keep;
+}
+
+// The same for any number of slots: radix selection, 8 bits a pass, over keys
+// in shared memory (or read again), then the kept slots in order by one scan
+// over contiguous shares of the slots.
+__global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const EvictParams p) {
   extern __shared__ uint32_t keys[];
   __shared__ int hist[256];
   __shared__ int scan[64];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
+  pdl_trigger();
+  pdl_wait();
   const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, t = threadIdx.x;
   const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
   const int keep = min(n, p.budget);
   const float* mass = p.mass + (static_cast<int64_t>(b) * p.H + h) * p.L;
-  const bool held = n <= kSelSmemKeys && p.L <= kSelSmemKeys;
+  const bool held = p.L <= kSelSmemKeys;
   if (held)
     for (int j = t; j < n; j += kSelThreads) keys[j] = select_key(p, mass, j, n);
   if (t == 0) s_prefix = 0, s_need = keep;
@@ -421,16 +520,39 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       __syncthreads();
       const uint32_t pre = s_prefix;
       const uint32_t hi = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int j = t; j < n; j += kSelThreads) {
-        const uint32_t u = key_at(j);
-        if ((u & hi) == pre) atomicAdd(&hist[(u >> shift) & 255], 1);
+      for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+        const uint32_t u = j0 + t < n ? key_at(j0 + t) : 0u;
+        const bool in = j0 + t < n && (u & hi) == pre;
+        // One addition for the lanes of a warp that share a bin (weights crowd a few).
+        const uint32_t bin = in ? (u >> shift) & 255 : 256u;
+        const uint32_t same = __match_any_sync(0xffffffffu, bin);
+        if (in && (t & 31) == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
       }
       __syncthreads();
-      if (t == 0) {
-        int left = s_need, d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_prefix = pre | static_cast<uint32_t>(d) << shift;
-        s_need = left;
+      if (t < 32) {
+        // Lane l holds bins 8 l .. 8 l + 7, counted from the top.
+        int sum = 0, own[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += own[k] = hist[255 - (8 * t + k)];
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, before, o);
+          if (t >= o) before += x;
+        }
+        before -= sum;
+        const int left = s_need;
+        __syncwarp();
+        if (before < left && before + sum >= left) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (before < left && before + own[k] >= left) {
+              s_prefix = pre | static_cast<uint32_t>(255 - (8 * t + k)) << shift;
+              s_need = left - before;
+            }
+            before += own[k];
+          }
+        }
       }
       __syncthreads();
     }
@@ -442,10 +564,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   int over = 0, ties = 0;
   for (int j = j0; j < j1; ++j) {
     const uint32_t u = key_at(j);
-    over += u > thr;
-    ties += u == thr;
+    over += keep == n || u > thr;
+    ties += keep < n && u == thr;
   }
-  if (keep == n) over += ties, ties = 0;  // everything stays
   block_scan2(over, ties, scan);
   const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.budget;
   const int64_t meta = b * p.km_b + h * p.km_h;
@@ -454,48 +575,87 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     const uint32_t u = key_at(j);
     bool k = keep == n || u > thr;
     if (!k && u == thr) k = ties++ < need;
-    if (!k) continue;
-    p.idx[row + at] = j;
-    p.mass_out[row + at] = mass[j];
-    if (p.pos_out) p.pos_out[row + at] = p.k_pos ? p.k_pos[meta + j] : j;
-    if (p.doc_out) p.doc_out[row + at] = p.k_doc[meta + j];
-    ++at;
+    if (k) keep_slot(p, mass, row, meta, at++, j);
   }
   if (h == 0 && t == 0 && p.lens_out) p.lens_out[b] = keep;
 }
 
-// Copies the kept rows: thread = one unit (16 bytes, or one value) of a row
-// of K and of V; consecutive threads write consecutive units of an out row
-// and then the next head.
-template <class U>
-__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, int units, int esize) {
-  const int64_t per_b = static_cast<int64_t>(p.budget) * p.H * units;
+// Copies the kept rows.  Consecutive threads take consecutive units (16 bytes,
+// or one value) of an out row and then the next head; a thread takes kRows such
+// rows, a grid apart, with all their loads on the way at once.
+template <class U, int kRows>
+__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, int units, int esize, int64_t stride) {
+  pdl_wait();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (t >= per_b) return;
+  if (t >= stride) return;
   const int b = blockIdx.y;
+  const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
   const int u = static_cast<int>(t % units);
   const int64_t r = t / units;
   const int h = static_cast<int>(r % p.H);
-  const int64_t row = r / p.H;
-  const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
-  if (row >= min(n, p.budget)) return;
-  const int64_t j = p.idx[(static_cast<int64_t>(b) * p.H + h) * p.budget + row];
-  auto src = [&](const void* base, const Strides3& s) {
-    return reinterpret_cast<const U*>(static_cast<const char*>(base) + (b * s.b + j * s.l + h * s.h) * esize) + u;
-  };
-  auto dst = [&](void* base, const Strides3& s) {
-    return reinterpret_cast<U*>(static_cast<char*>(base) + (b * s.b + row * s.l + h * s.h) * esize) + u;
-  };
-  const U kk = *src(p.k, p.ks), vv = *src(p.v, p.vs);
-  *dst(p.k_out, p.kos) = kk;
-  *dst(p.v_out, p.vos) = vv;
+  const int64_t row0 = r / p.H, step = stride / units / p.H;
+  const int keep = min(n, p.budget);
+  U kk[kRows], vv[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = row0 + i * step;
+    if (row >= keep) break;
+    const int64_t j = p.idx[(static_cast<int64_t>(b) * p.H + h) * p.budget + row];
+    kk[i] = reinterpret_cast<const U*>(static_cast<const char*>(p.k) + (b * p.ks.b + j * p.ks.l + h * p.ks.h) * esize)[u];
+    vv[i] = reinterpret_cast<const U*>(static_cast<const char*>(p.v) + (b * p.vs.b + j * p.vs.l + h * p.vs.h) * esize)[u];
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = row0 + i * step;
+    if (row >= keep) break;
+    reinterpret_cast<U*>(static_cast<char*>(p.k_out) + (b * p.kos.b + row * p.kos.l + h * p.kos.h) * esize)[u] = kk[i];
+    reinterpret_cast<U*>(static_cast<char*>(p.v_out) + (b * p.vos.b + row * p.vos.l + h * p.vos.h) * esize)[u] = vv[i];
+  }
+}
+
+cudaLaunchConfig_t pdl_config(dim3 grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
 }
 
 template <class U>
-void launch_gather(const EvictParams& p, int size, cudaStream_t st) {
+cudaError_t launch_gather(const EvictParams& p, int size, cudaStream_t st) {
+  constexpr int kRows = 4;
   const int units = p.dh * size / static_cast<int>(sizeof(U));
-  const int64_t per_b = static_cast<int64_t>(p.budget) * p.H * units;
-  evict_gather_kernel<U><<<dim3(static_cast<unsigned>((per_b + 255) / 256), p.B), 256, 0, st>>>(p, units, size);
+  const int64_t stride = static_cast<int64_t>((p.budget + kRows - 1) / kRows) * p.H * units;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>((stride + 255) / 256), p.B), 256, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, evict_gather_kernel<U, kRows>, p, units, size, stride);
+}
+
+template <int KPT>
+cudaError_t launch_select(const EvictParams& p, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3(p.B * p.H), kSelThreads, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, p);
+}
+
+cudaError_t launch_select_any(const EvictParams& p, cudaStream_t st) {
+  if (p.L <= 4 * kSelThreads) return launch_select<4>(p, st);
+  if (p.L <= 8 * kSelThreads) return launch_select<8>(p, st);
+  if (p.L <= 16 * kSelThreads) return launch_select<16>(p, st);
+  static uint64_t set_up = 0;
+  cudaError_t e = psv::once_per_device(&set_up, [](int) {
+    return cudaFuncSetAttribute(evict_select_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemKeys * 4);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  const size_t smem = p.L <= kSelSmemKeys ? static_cast<size_t>(p.L) * 4 : 0;
+  const cudaLaunchConfig_t cfg = pdl_config(dim3(p.B * p.H), kSelThreads, smem, st, attr);
+  return cudaLaunchKernelEx(&cfg, evict_select_long_kernel, p);
 }
 
 }  // namespace
@@ -553,23 +713,16 @@ PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const voi
   e.B = p->B, e.H = p->Hkv, e.dh = p->dh, e.L = p->L, e.budget = p->budget;
   e.sinks = p->sinks, e.recent = p->recent;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const size_t smem = p->L <= kSelSmemKeys ? static_cast<size_t>(p->L) * 4 : 0;
-  static uint64_t set_up = 0;
-  cudaError_t r = psv::once_per_device(&set_up, [](int) {
-    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemKeys * 4);
-  });
-  if (r != cudaSuccess) return cuda_status(r, "eviction set-up");
-  evict_select_kernel<<<p->B * p->Hkv, kSelThreads, smem, st>>>(e);
-  if ((r = cudaGetLastError()) != cudaSuccess) return cuda_status(r, "eviction launch");
+  cudaError_t r = launch_select_any(e, st);
+  if (r != cudaSuccess) return cuda_status(r, "eviction launch");
   const bool vec = (static_cast<int64_t>(p->dh) * size) % 16 == 0 &&
                    multiple16(k, p->k_stride, p->B, p->L, p->Hkv, size) &&
                    multiple16(v, p->v_stride, p->B, p->L, p->Hkv, size) &&
                    multiple16(k_out, p->k_out_stride, p->B, p->budget, p->Hkv, size) &&
                    multiple16(v_out, p->v_out_stride, p->B, p->budget, p->Hkv, size);
-  if (vec) launch_gather<uint4>(e, size, st);
-  else if (size == 4) launch_gather<uint32_t>(e, size, st);
-  else launch_gather<uint16_t>(e, size, st);
-  return cuda_status(cudaGetLastError(), "eviction launch");
+  r = vec ? launch_gather<uint4>(e, size, st)
+          : size == 4 ? launch_gather<uint32_t>(e, size, st) : launch_gather<uint16_t>(e, size, st);
+  return cuda_status(r, "eviction launch");
 }
 
 // ------------------------------------------------- attention over a cache
