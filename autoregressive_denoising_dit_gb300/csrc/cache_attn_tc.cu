@@ -63,54 +63,65 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
   if (lane == 0) p.row_units[w] = RowUnit{pmax, dmin, dmax, 0};
 }
 
-// Joins the shares of a row: one warp per (sequence, head, token), lanes over
-// the shares for m and l, then over the columns.  Bound by its launch and the
-// reading of nsplit rows of O.
+// Joins the shares of a row: one CTA per (sequence, head, token).  Each of its
+// four warps adds up every fourth share, lanes over the columns, four shares'
+// rows on the way at once; the warps' sums are added in order.  Bound by the
+// latency of two dependent reads.
 template <bool BF16>
 __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ TcParams p) {
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);  // (b, tok, head)
-  const int64_t n = static_cast<int64_t>(p.c.B) * p.c.Lq * p.c.Hq;
-  if (row >= n) return;
+  __shared__ float4 s_acc[4][32];
+  __shared__ float s_l[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x;  // (b, tok, head)
   const int head = static_cast<int>(row % p.c.Hq);
   const int tok = static_cast<int>(row / p.c.Hq % p.c.Lq);
   const int b = static_cast<int>(row / p.c.Hq / p.c.Lq);
-  if (tok >= cache_q_len(p.c, b)) return;
   const int kvh = head / p.c.G, unit = tok / (2 * p.tok_cta);
   const int in_unit = tok - unit * 2 * p.tok_cta;
   const int prow = in_unit * p.c.G + head % p.c.G;  // both CTAs' rows in a row
   const int64_t first = ((static_cast<int64_t>(b) * p.c.Hkv + kvh) * p.units + unit) * p.nsplit;
+  const float2* ml = p.part_ml + first * p.part_rows + prow;
+  const float* part = p.part_o + (first * p.part_rows + prow) * p.width + lane * 4;
+  const int64_t step = p.part_rows;  // rows from one share to the next
+  pdl_wait();
+  if (tok >= cache_q_len(p.c, b)) return;
   float m = -INFINITY;
-  for (int s = lane; s < p.nsplit; s += 32) m = fmaxf(m, p.part_ml[(first + s) * p.part_rows + prow].x);
+  for (int s = lane; s < p.nsplit; s += 32) m = fmaxf(m, ml[s * step].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float m0 = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < p.nsplit; s0 += 32) {
-    float w = 0.0f, wl = 0.0f;
-    if (s0 + lane < p.nsplit) {
-      const float2 ml = p.part_ml[(first + s0 + lane) * p.part_rows + prow];
-      if (ml.y > 0.0f) {
-        w = fast_exp2(ml.x - m0);
-        wl = w * ml.y;
-      }
+  const bool in = lane * 4 < p.width;
+  for (int s0 = warp; s0 < p.nsplit; s0 += 16) {
+    float2 w[4];
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int s = s0 + 4 * k;
+      w[k] = s < p.nsplit ? ml[s * step] : make_float2(-INFINITY, 0.0f);
+      x[k] = s < p.nsplit && in ? *reinterpret_cast<const float4*>(part + s * step * p.width)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, o);
-    l += wl;
-    const int cnt = min(32, p.nsplit - s0);
-    for (int s = 0; s < cnt; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (ws == 0.0f || lane * 4 >= p.width) continue;
-      const float4 x =
-          *reinterpret_cast<const float4*>(p.part_o + ((first + s0 + s) * p.part_rows + prow) * p.width + lane * 4);
-      acc.x = fmaf(ws, x.x, acc.x);
-      acc.y = fmaf(ws, x.y, acc.y);
-      acc.z = fmaf(ws, x.z, acc.z);
-      acc.w = fmaf(ws, x.w, acc.w);
+    for (int k = 0; k < 4; ++k) {
+      const float f = fast_exp2(w[k].x - m0);  // 0 for a share that saw nothing (its O is 0)
+      l = fmaf(f, w[k].y, l);
+      acc.x = fmaf(f, x[k].x, acc.x);
+      acc.y = fmaf(f, x[k].y, acc.y);
+      acc.z = fmaf(f, x[k].z, acc.z);
+      acc.w = fmaf(f, x[k].w, acc.w);
     }
+  }
+  s_acc[warp][lane] = acc;
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int k = 1; k < 4; ++k) {
+    const float4 x = s_acc[k][lane];
+    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+    l += s_l[k];
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   if (lane * 4 < p.c.dh) {
@@ -233,7 +244,7 @@ cudaError_t launch_join(const TcParams& p, bool bf16, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cfg.attrs = attr;

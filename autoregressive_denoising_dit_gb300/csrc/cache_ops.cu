@@ -196,16 +196,12 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
   const int d0 = HALVES && !rot ? p.R + (u - p.rot_units) * VEC : u * VEC;
   const T* x = static_cast<const T*>(p.x) + b * p.xs.b + l * p.xs.l + d0;
   T* o = static_cast<T*>(p.out) + b * p.os.b + l * p.os.l + d0;
-  constexpr int PR = HALVES ? VEC : (VEC + 1) / 2;  // pairs of a unit
-  float2 cs[PR];
-#pragma unroll
-  for (int i = 0; i < PR; ++i)
-    cs[i] = pair_angle(p, HALVES ? (rot ? d0 + i : p.R) : d0 / 2 + i, b, l);
-  // kFlight heads' loads are on their way at a time.
-  constexpr int kFlight = HALVES ? 2 : 4;
+  // kFlight heads' loads are on their way at a time, the first ones while the
+  // angles are computed.
+  constexpr int kFlight = 4;
   const int h1 = min(p.H, (hg + 1) * p.hpt);
-  for (int h0 = hg * p.hpt; h0 < h1; h0 += kFlight) {
-    V a[kFlight], c[HALVES ? kFlight : 1];
+  V a[kFlight], c[HALVES ? kFlight : 1];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kFlight; ++k)
       if (h0 + k < h1) {
@@ -213,30 +209,40 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
         if constexpr (HALVES)
           if (rot) c[k].load(x + (h0 + k) * p.xs.h + p.R / 2);
       }
+  };
+  load(hg * p.hpt);
+  constexpr int PR = HALVES ? VEC : (VEC + 1) / 2;  // pairs of a unit
+  float2 cs[PR];
+#pragma unroll
+  for (int i = 0; i < PR; ++i)
+    cs[i] = pair_angle(p, HALVES ? (rot ? d0 + i : p.R) : d0 / 2 + i, b, l);
+  for (int h0 = hg * p.hpt; h0 < h1; h0 += kFlight) {
+    if (h0 != hg * p.hpt) load(h0);
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
-      if (h0 + k >= h1) break;
-      if constexpr (HALVES) {
-        if (rot) {
+      if (h0 + k < h1) {
+        if constexpr (HALVES) {
+          if (rot) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float f = to_f(a[k].v[i]), g = to_f(c[k].v[i]);
-            from_f(a[k].v[i], f * cs[i].x - g * cs[i].y);
-            from_f(c[k].v[i], f * cs[i].y + g * cs[i].x);
+            for (int i = 0; i < VEC; ++i) {
+              const float f = to_f(a[k].v[i]), g = to_f(c[k].v[i]);
+              from_f(a[k].v[i], f * cs[i].x - g * cs[i].y);
+              from_f(c[k].v[i], f * cs[i].y + g * cs[i].x);
+            }
+            c[k].store(o + (h0 + k) * p.os.h + p.R / 2);
           }
-          c[k].store(o + (h0 + k) * p.os.h + p.R / 2);
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-          if (2 * (d0 / 2 + i) < p.R) {  // values behind R are copied bit for bit
-            const float f = to_f(a[k].v[2 * i]), g = to_f(a[k].v[2 * i + 1]);
-            from_f(a[k].v[2 * i], f * cs[i].x - g * cs[i].y);
-            from_f(a[k].v[2 * i + 1], f * cs[i].y + g * cs[i].x);
+          for (int i = 0; i < VEC / 2; ++i) {
+            if (2 * (d0 / 2 + i) < p.R) {  // values behind R are copied bit for bit
+              const float f = to_f(a[k].v[2 * i]), g = to_f(a[k].v[2 * i + 1]);
+              from_f(a[k].v[2 * i], f * cs[i].x - g * cs[i].y);
+              from_f(a[k].v[2 * i + 1], f * cs[i].y + g * cs[i].x);
+            }
           }
         }
+        a[k].store(o + (h0 + k) * p.os.h);
       }
-      a[k].store(o + (h0 + k) * p.os.h);
     }
   }
 }
@@ -299,10 +305,11 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   if (!rows_distinct(p->out_stride, p->B, p->L, p->H, p->dh))
     return cache_fail(PSV_EINVAL, "out's rows overlap");
   RopeParams k{};
+  const double log_theta = p->freqs ? 0.0 : std::log2(p->theta);
   int pair = 0;
   for (int a = 0; a < p->n_axes; ++a)
     for (int j = 0; j < p->axis_dims[a] / 2; ++j, ++pair) {
-      const double f = p->freqs ? p->freqs[pair] : std::pow(p->theta, -2.0 * j / p->axis_dims[a]);
+      const double f = p->freqs ? p->freqs[pair] : std::exp2(log_theta * (-2.0 * j / p->axis_dims[a]));
       if (!std::isfinite(f)) return cache_fail(PSV_EINVAL, "frequency %d is not finite", pair);
       if (std::fabs(f) > 1e6) return cache_fail(PSV_EINVAL, "frequency %d is over 1e6 radians", pair);
       k.turn[pair] = fixed_turns(f);
@@ -334,9 +341,9 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   const bool vec = multiple16(x, p->x_stride, p->B, p->L, p->H, size) &&
                    multiple16(out, p->out_stride, p->B, p->L, p->H, size) && p->dh % N == 0 &&
                    (!halves || ((R / 2) % N == 0 && (p->dh - R) % N == 0));
-  // A thread's angles serve as many heads as leave about 512 threads an SM.
+  // A thread's angles serve as many heads as leave about 1024 threads an SM.
   const int64_t all = static_cast<int64_t>(p->B) * p->L * p->H * (p->dh / (vec ? N : 2));
-  const int64_t hpt = all / (152 * 512);
+  const int64_t hpt = all / (152 * 1024);
   k.hpt = static_cast<int>(hpt < 1 ? 1 : hpt > p->H ? p->H : hpt > 16 ? 16 : hpt);
   k.hgroups = (p->H + k.hpt - 1) / k.hpt;
   k.hpt = (p->H + k.hgroups - 1) / k.hgroups;
@@ -373,15 +380,15 @@ constexpr int kSelSmemKeys = 49152;  // keys held in shared memory (192 KB)
 
 // Order of selection as an unsigned key: protected slots, then NaN, then by
 // value (+0 and -0 are equal).
-__device__ __forceinline__ uint32_t select_key(const EvictParams& p, const float* mass, int j, int n) {
+__device__ __forceinline__ uint32_t select_key(const EvictParams& p, float weight, int j, int n) {
   if (j < p.sinks || j >= n - p.recent) return 0xffffffffu;
-  const float x = mass[j] + 0.0f;
+  const float x = weight + 0.0f;
   if (x != x) return 0xfffffffeu;
   const uint32_t u = __float_as_uint(x);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive sums of a and b over the block's threads (1024).
+// Exclusive sums of a and b over the block's threads.
 __device__ __forceinline__ void block_scan2(int& a, int& b, int* sm) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int x = a, y = b;
@@ -393,7 +400,8 @@ __device__ __forceinline__ void block_scan2(int& a, int& b, int* sm) {
   if (lane == 31) sm[w] = x, sm[32 + w] = y;
   __syncthreads();
   if (w == 0) {
-    int s = sm[lane], t = sm[32 + lane];
+    const bool there = lane < static_cast<int>(blockDim.x >> 5);
+    int s = there ? sm[lane] : 0, t = there ? sm[32 + lane] : 0;
     const int s0 = s, t0 = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -408,37 +416,54 @@ __device__ __forceinline__ void block_scan2(int& a, int& b, int* sm) {
 }
 
 // What the select kernels write for a kept slot j at place `at` of its row.
-__device__ __forceinline__ void keep_slot(const EvictParams& p, const float* mass, int64_t row, int64_t meta, int at,
-                                          int j) {
+__device__ __forceinline__ void keep_slot(const EvictParams& p, float weight, int64_t row, int64_t meta, int at, int j) {
   p.idx[row + at] = j;
-  p.mass_out[row + at] = mass[j];
+  p.mass_out[row + at] = weight;
   if (p.pos_out) p.pos_out[row + at] = p.k_pos ? p.k_pos[meta + j] : j;
   if (p.doc_out) p.doc_out[row + at] = p.k_doc[meta + j];
 }
 
-// One CTA per (sequence, kv head) with up to 1024 KPT slots: every thread holds
+// One CTA per (sequence, kv head) with up to 512 KPT slots: every thread holds
 // KPT consecutive slots' keys in registers, the keep-th greatest key is found
 // two bits at a time by counting, and one scan gives the kept slots their
-// places.  Bound by latency: 16 rounds of compare, warp sum and barrier.
+// places.  Bound by latency: 16 rounds of compare, warp sums and one barrier.
+constexpr int kRegThreads = 512;
+
+// Sum over the warps' counts (lanes 0..15 read one each).
+__device__ __forceinline__ int warps_sum(const int* counts) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, lane < kRegThreads / 32 ? counts[lane] : 0);
+}
+
 template <int KPT>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictParams p, int vec) {
   __shared__ int scan[64];
-  __shared__ int count[2][4];
+  __shared__ int count[2][3][kRegThreads / 32];
   pdl_trigger();
+  const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, t = threadIdx.x, warp = t >> 5;
+  const float* mass = p.mass + (static_cast<int64_t>(b) * p.H + h) * p.L;
   pdl_wait();
-  const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, t = threadIdx.x;
   const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
   const int keep = min(n, p.budget);
-  const float* mass = p.mass + (static_cast<int64_t>(b) * p.H + h) * p.L;
   uint32_t key[KPT];
+  float x[KPT];
 #pragma unroll
-  for (int i = 0; i < KPT; ++i) key[i] = t * KPT + i < n ? select_key(p, mass, t * KPT + i, n) : 0u;
-  if (t < 8) count[t / 4][t % 4] = 0;
-  __syncthreads();
-  // thr: the greatest value that at least `keep` keys reach (0 if all stay; no
-  // key of a slot is 0, as only a negative NaN's complement would be).
+  for (int i = 0; i < KPT; i += 4) {  // rows of L % 4 == 0 are read 16 bytes at a time
+    const int j = t * KPT + i;
+    if (vec && j + 4 <= p.L) {
+      const float4 v = *reinterpret_cast<const float4*>(mass + j);
+      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i + e] = j + e < p.L ? mass[j + e] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) key[i] = t * KPT + i < n ? select_key(p, x[i], t * KPT + i, n) : 0u;
+  // thr: the greatest value that at least `keep` keys reach; above: how many
+  // are over it.  (No slot's key is 0.)
   uint32_t thr = 0;
-  int above = 0;  // keys over thr
+  int above = 0;
   if (keep < n) {
     for (int shift = 30, r = 0; shift >= 0; shift -= 2, r ^= 1) {
       int c1 = 0, c2 = 0, c3 = 0;
@@ -452,19 +477,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       c1 = __reduce_add_sync(0xffffffffu, c1);
       c2 = __reduce_add_sync(0xffffffffu, c2);
       c3 = __reduce_add_sync(0xffffffffu, c3);
-      if ((t & 31) == 0) {
-        atomicAdd(&count[r][1], c1);
-        atomicAdd(&count[r][2], c2);
-        atomicAdd(&count[r][3], c3);
-      }
+      if ((t & 31) == 0) count[r][0][warp] = c1, count[r][1][warp] = c2, count[r][2][warp] = c3;
       __syncthreads();
-      c1 = count[r][1], c2 = count[r][2], c3 = count[r][3];
+      c1 = warps_sum(count[r][0]);
+      c2 = warps_sum(count[r][1]);
+      c3 = warps_sum(count[r][2]);
       if (c3 >= keep) thr = v3;
       else if (c2 >= keep) thr = v2, above = c3;
       else if (c1 >= keep) thr = v1, above = c2;
       else above = c1;
-      if (t < 4) count[r ^ 1][t] = 0;
-      __syncthreads();
+      // (The counts are rewritten two rounds later, behind the next barrier.)
     }
   }
   const int need = keep - above;  // of the keys equal to thr
@@ -482,10 +504,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
     const int j = t * KPT + i;
-    if (j >= n) break;
-    bool k = keep == n || key[i] > thr;
-    if (!k && key[i] == thr) k = ties++ < need;
-    if (k) keep_slot(p, mass, row, meta, at++, j);
+    if (j < n) {
+      bool k = keep == n || key[i] > thr;
+      if (!k && key[i] == thr) k = ties++ < need;
+      if (k) keep_slot(p, x[i], row, meta, at++, j);
+    }
   }
   if (h == 0 && t == 0 && p.lens_out) p.lens_out[b] = keep;
 }
@@ -507,10 +530,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const Ev
   const float* mass = p.mass + (static_cast<int64_t>(b) * p.H + h) * p.L;
   const bool held = p.L <= kSelSmemKeys;
   if (held)
-    for (int j = t; j < n; j += kSelThreads) keys[j] = select_key(p, mass, j, n);
+    for (int j = t; j < n; j += kSelThreads) keys[j] = select_key(p, mass[j], j, n);
   if (t == 0) s_prefix = 0, s_need = keep;
   __syncthreads();
-  auto key_at = [&](int j) { return held ? keys[j] : select_key(p, mass, j, n); };
+  auto key_at = [&](int j) { return held ? keys[j] : select_key(p, mass[j], j, n); };
   // Keys over the threshold are kept, `need` of those equal to it.
   uint32_t thr = 0;
   int need = keep;
@@ -575,7 +598,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const Ev
     const uint32_t u = key_at(j);
     bool k = keep == n || u > thr;
     if (!k && u == thr) k = ties++ < need;
-    if (k) keep_slot(p, mass, row, meta, at++, j);
+    if (k) keep_slot(p, mass[j], row, meta, at++, j);
   }
   if (h == 0 && t == 0 && p.lens_out) p.lens_out[b] = keep;
 }
@@ -639,14 +662,16 @@ cudaError_t launch_gather(const EvictParams& p, int size, cudaStream_t st) {
 template <int KPT>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3(p.B * p.H), kSelThreads, 0, st, attr);
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, p);
+  const cudaLaunchConfig_t cfg = pdl_config(dim3(p.B * p.H), kRegThreads, 0, st, attr);
+  const int vec = p.L % 4 == 0 && (reinterpret_cast<uintptr_t>(p.mass) & 15) == 0;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, p, vec);
 }
 
 cudaError_t launch_select_any(const EvictParams& p, cudaStream_t st) {
-  if (p.L <= 4 * kSelThreads) return launch_select<4>(p, st);
-  if (p.L <= 8 * kSelThreads) return launch_select<8>(p, st);
-  if (p.L <= 16 * kSelThreads) return launch_select<16>(p, st);
+  if (p.L <= 4 * kRegThreads) return launch_select<4>(p, st);
+  if (p.L <= 8 * kRegThreads) return launch_select<8>(p, st);
+  if (p.L <= 16 * kRegThreads) return launch_select<16>(p, st);
+  if (p.L <= 32 * kRegThreads) return launch_select<32>(p, st);
   static uint64_t set_up = 0;
   cudaError_t e = psv::once_per_device(&set_up, [](int) {
     return cudaFuncSetAttribute(evict_select_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemKeys * 4);

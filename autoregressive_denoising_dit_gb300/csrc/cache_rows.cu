@@ -102,17 +102,69 @@ __device__ __forceinline__ float fast_log2(float x) {
 struct Row {
   int qp, qd, klim, plim;
   float slope2;
-  bool valid;
 };
 
 // A piece and, for this thread's two rows, their queries as A fragments (rows
 // lane / 4 and + 8; columns 2 (lane % 4) + {0, 1, 8, 9} of a step of 16).
-template <int DH>
+// fetch() only issues the reads (none depends on another), while the piece
+// before runs; settle() uses them.
+template <int DH, bool MASS>
 struct Work {
-  int b, kvh, share, k_len, q_len, t0, t1;
+  int b, kvh, share, k_len, q_len, t0, t1, prefix;
   uint32_t qf[DH / 16][4];
   Row row[2];
   float lse2[2];
+
+  __device__ __forceinline__ void fetch(const RowsParams& p, int piece, int lane) {
+    const CacheParams& c = p.c;
+    share = piece % p.nsplit;
+    const int bh = piece / p.nsplit;
+    b = bh / c.Hkv, kvh = bh % c.Hkv;
+    k_len = c.k_lens ? c.k_lens[b] : c.Lk;
+    q_len = c.q_lens ? c.q_lens[b] : c.Lq;
+    prefix = c.prefix ? c.prefix[b] : 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = lane / 4 + 8 * e, tok = r / c.G, head = kvh * c.G + r % c.G;
+      const bool there = tok < c.Lq;
+      const uint16_t* q = static_cast<const uint16_t*>(c.q) + b * c.qs.b + tok * c.qs.l + head * c.qs.h;
+#pragma unroll
+      for (int k = 0; k < DH / 16; ++k) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int d = k * 16 + x * 8 + 2 * (lane % 4);
+          qf[k][e + 2 * x] = there && d < c.dh ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+        }
+      }
+      row[e].qp = there && c.q_pos ? c.q_pos[b * c.qm_b + tok] : 0;
+      row[e].qd = there && c.q_doc ? c.q_doc[b * c.qm_b + tok] : 0;
+      row[e].slope2 = there && c.slopes ? c.slopes[head] : 0.0f;
+      lse2[e] = MASS && there ? c.lse[(static_cast<int64_t>(b) * c.Hq + head) * c.Lq + tok] : -INFINITY;
+    }
+  }
+
+  __device__ __forceinline__ void settle(const RowsParams& p, int lane) {
+    const CacheParams& c = p.c;
+    k_len = min(max(k_len, 0), c.Lk);
+    q_len = min(max(q_len, 0), c.Lq);
+    const int nt = (k_len + kKeys - 1) / kKeys;
+    t0 = static_cast<int>(static_cast<int64_t>(nt) * share / p.nsplit);
+    t1 = static_cast<int>(static_cast<int64_t>(nt) * (share + 1) / p.nsplit);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int tok = (lane / 4 + 8 * e) / c.G;
+      const bool valid = tok < q_len;
+      if (!valid) {  // an unused row may hold anything
+#pragma unroll
+        for (int k = 0; k < DH / 16; ++k) qf[k][e] = qf[k][e + 2] = 0u;
+      }
+      if (!c.q_pos) row[e].qp = k_len - q_len + tok;
+      row[e].slope2 *= kLog2e;
+      row[e].plim = c.causal ? max(row[e].qp + 1, prefix) : 0x7fffffff;  // positions below it are seen
+      row[e].klim = c.k_pos ? k_len : min(k_len, max(row[e].plim, 0));
+      lse2[e] = valid && lse2[e] != -INFINITY ? lse2[e] * kLog2e : INFINITY;
+    }
+  }
 };
 
 // Of a tile's 32 keys, the one whose summed weight ends up in this lane: the
@@ -120,56 +172,6 @@ struct Work {
 __device__ __forceinline__ int mass_key(int lane) {
   const int k = lane >> 2;  // bit 2 (lane 16): n's upper bit, bit 1 (8): n's lower bit, bit 0 (4): x
   return 8 * (k >> 1) + 2 * (lane % 4) + (k & 1);
-}
-
-template <bool MASS>
-__device__ __forceinline__ void piece_tiles(const RowsParams& p, int piece, int& b, int& kvh, int& share, int& k_len,
-                                            int& t0, int& t1) {
-  share = piece % p.nsplit;
-  const int bh = piece / p.nsplit;
-  b = bh / p.c.Hkv, kvh = bh % p.c.Hkv;
-  k_len = cache_k_len(p.c, b);
-  const int nt = (k_len + kKeys - 1) / kKeys;
-  t0 = static_cast<int>(static_cast<int64_t>(nt) * share / p.nsplit);
-  t1 = static_cast<int>(static_cast<int64_t>(nt) * (share + 1) / p.nsplit);
-}
-
-template <int DH, bool MASS>
-__device__ __forceinline__ void load_work(const RowsParams& p, int piece, int lane, Work<DH>& w) {
-  const CacheParams& c = p.c;
-  piece_tiles<MASS>(p, piece, w.b, w.kvh, w.share, w.k_len, w.t0, w.t1);
-  w.q_len = cache_q_len(c, w.b);
-  const int prefix = c.prefix ? c.prefix[w.b] : 0;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = lane / 4 + 8 * e, tok = r / c.G, head = w.kvh * c.G + r % c.G;
-    Row& row = w.row[e];
-    row.valid = r < w.q_len * c.G;
-    const uint16_t* q = static_cast<const uint16_t*>(c.q) + w.b * c.qs.b + tok * c.qs.l + head * c.qs.h;
-#pragma unroll
-    for (int k = 0; k < DH / 16; ++k) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int d = k * 16 + x * 8 + 2 * (lane % 4);
-        w.qf[k][e + 2 * x] = row.valid && d < c.dh ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
-      }
-    }
-    row.qp = w.k_len - w.q_len + tok;
-    row.qd = 0;
-    row.slope2 = 0.0f;
-    w.lse2[e] = INFINITY;
-    if (row.valid) {
-      if (c.q_pos) row.qp = c.q_pos[w.b * c.qm_b + tok];
-      if (c.q_doc) row.qd = c.q_doc[w.b * c.qm_b + tok];
-      if (c.slopes) row.slope2 = c.slopes[head] * kLog2e;
-      if (MASS) {
-        const float l = c.lse[(static_cast<int64_t>(w.b) * c.Hq + head) * c.Lq + tok];
-        if (l != -INFINITY) w.lse2[e] = l * kLog2e;
-      }
-    }
-    row.plim = c.causal ? max(row.qp + 1, prefix) : 0x7fffffff;  // positions below it are seen
-    row.klim = c.k_pos ? w.k_len : min(w.k_len, max(row.plim, 0));
-  }
 }
 
 template <int DH, bool BF16, bool MASS>
@@ -206,9 +208,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t g = 0;  // tiles so far
       bool ok = true;
+      auto key_len = [&](int piece) {
+        return c.k_lens && piece < p.n_pieces ? c.k_lens[piece / p.nsplit / c.Hkv] : c.Lk;
+      };
+      int len = key_len(blockIdx.x);
       for (int piece = blockIdx.x; piece < p.n_pieces && ok; piece += gridDim.x) {
-        int b, kvh, share, k_len, t0, t1;
-        piece_tiles<MASS>(p, piece, b, kvh, share, k_len, t0, t1);
+        const int next_len = key_len(piece + gridDim.x);  // read while this piece is loaded
+        const int share = piece % p.nsplit, bh = piece / p.nsplit, b = bh / c.Hkv, kvh = bh % c.Hkv;
+        const int nt = (min(max(len, 0), c.Lk) + kKeys - 1) / kKeys;
+        const int t0 = static_cast<int>(static_cast<int64_t>(nt) * share / p.nsplit);
+        const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (share + 1) / p.nsplit);
+        len = next_len;
         for (int t = t0; t < t1; ++t, ++g) {
           const uint32_t st = g % ST;
           if (!(ok = mbar_wait(&empty[st], ((g / ST) & 1) ^ 1, c.err, ERR_ATTN_TIMEOUT))) break;
@@ -239,10 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t g0 = 0;  // tiles of earlier pieces
   bool ok = true;
   int piece = blockIdx.x;
-  Work<DH> w, next;
-  if (piece < p.n_pieces) load_work<DH, MASS>(p, piece, lane, w);
+  Work<DH, MASS> w, next;
+  if (piece < p.n_pieces) w.fetch(p, piece, lane);
   for (; piece < p.n_pieces; piece += gridDim.x) {
-    if (piece + gridDim.x < p.n_pieces) load_work<DH, MASS>(p, piece + gridDim.x, lane, next);
+    w.settle(p, lane);
+    if (piece + gridDim.x < p.n_pieces) next.fetch(p, piece + gridDim.x, lane);
     const int64_t meta = w.b * c.km_b + w.kvh * c.km_h;
     const int k_len = w.k_len;
     float o[MASS ? 1 : DH / 8][4];
