@@ -161,10 +161,8 @@ TcLayout tc_layout(const CacheParams& c) {
   // Few rows: a share is a CTA of four warps that take 32 keys at a time.
   const int tiles = t.few ? (c.Lk + 127) / 128 : (c.Lk + KT - 1) / KT / (1 + t.part_rows / 64);
   const int64_t per_seq = static_cast<int64_t>(c.Hkv) * t.units;
-  // One share an SM (a pair of SMs) of a sequence, or two where they stay long:
-  // several sequences then fill the SMs evenly.
-  int64_t slots = t.few ? 2 * kPlanPairs : kPlanPairs;
-  if (t.few && static_cast<int64_t>(c.Lk) * per_seq >= 512 * slots) slots *= 2;
+  // One share an SM (a pair of SMs) of a sequence.
+  const int64_t slots = t.few ? 2 * kPlanPairs : kPlanPairs;
   const int64_t want = per_seq >= slots ? 1 : slots / per_seq;
   t.nsplit = static_cast<int>(want < tiles ? want : tiles);
   if (t.nsplit < 1) t.nsplit = 1;

@@ -479,9 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           rows = pc.a.y * 2 * p.tok_cta < nq;
           int first = 0, last = (unit_limit(p, b, pc.a.y, nk, nq) + KT - 1) / KT;
           if (rows && p.key_tiles) seen_tiles(p, b, pc.a.x % p.c.Hkv, pc.a.y, nk, first, last);
-          const int nt = last - first;
-          const int t0 = static_cast<int>(static_cast<int64_t>(nt) * pc.a.z / p.nsplit);
-          const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (pc.a.z + 1) / p.nsplit);
+          // (At most 2^20 tiles and 76 shares.)
+          const uint32_t nt = static_cast<uint32_t>(last - first), n = static_cast<uint32_t>(p.nsplit);
+          const int t0 = static_cast<int>(nt * static_cast<uint32_t>(pc.a.z) / n);
+          const int t1 = static_cast<int>(nt * static_cast<uint32_t>(pc.a.z + 1) / n);
           pc.b = make_int4(nk, nq, first + t0, t1 - t0);
         }
         int next = 0;

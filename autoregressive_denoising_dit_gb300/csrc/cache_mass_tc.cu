@@ -535,10 +535,11 @@ cudaError_t launch_any(const CUtensorMap* maps, const TcParams& p, int pairs, cu
 
 cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, char* scratch, int sms, cudaStream_t st) {
   if (static_cast<int64_t>(c.Lq) * c.G <= kFewRows) {
-    // Keys are independent: about 16 pieces an SM, of 128 keys at least.
+    // Keys are independent: about 8 pieces an SM, of 128 keys at least.
     const int64_t heads = static_cast<int64_t>(c.B) * c.Hkv, most = (c.Lk + 127) / 128;
-    int64_t n = (16 * static_cast<int64_t>(sms) + heads - 1) / heads;
+    int64_t n = (8 * static_cast<int64_t>(sms) + heads - 1) / heads;
     if (n > most) n = most;
+    if (n > 304) n = 304;
     const RowsParams r{c, static_cast<int>(n), 0, static_cast<int>(heads * n), sms, nullptr, nullptr};
     return launch_cache_rows(r, bf16, true, st);
   }

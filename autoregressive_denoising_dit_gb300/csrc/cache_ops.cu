@@ -122,7 +122,7 @@ struct RopeParams {
   const int32_t* lens;
   Strides3 xs, os;
   int64_t pos_b, pos_l;
-  int64_t n;             // threads: rows x units x head groups
+  uint32_t n;            // threads of a sequence: rows x units x head groups
   int B, L, H, dh, R;
   int units;             // units of a head: vectors (PAIRS) or vector pairs (HALVES), then copies
   int rot_units;         // HALVES: the units that rotate
@@ -182,14 +182,14 @@ __device__ __forceinline__ float2 pair_angle(const RopeParams& p, int pair, int 
 template <class T, int VEC, bool HALVES>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
   using V = Vec<T, VEC>;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  // (32-bit divisions: 64-bit ones cost more than the rotation.)
+  const uint32_t t = blockIdx.x * 256 + threadIdx.x;
   if (t >= p.n) return;
-  const int u = static_cast<int>(t % p.units);
-  int64_t r = t / p.units;
-  const int hg = static_cast<int>(r % p.hgroups);
-  r /= p.hgroups;
-  const int b = static_cast<int>(r / p.L);
-  const int64_t l = r % p.L;
+  const uint32_t units = p.units, hgroups = p.hgroups, rest = t / units;
+  const int u = static_cast<int>(t - rest * units);
+  const int hg = static_cast<int>(rest % hgroups);
+  const int b = blockIdx.y;
+  const int64_t l = rest / hgroups;
   if (p.lens && l >= p.lens[b]) return;
   const bool rot = !HALVES || u < p.rot_units;
   // Values [d0, d0 + VEC); HALVES: partners at d0 + R/2.
@@ -269,11 +269,10 @@ cudaError_t launch_rope_t(RopeParams& p, bool vec, cudaStream_t st) {
   } else {
     p.units = p.dh / V;
   }
-  p.n = static_cast<int64_t>(p.B) * p.L * p.units * p.hgroups;
-  const int64_t blocks = (p.n + 255) / 256;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  if (vec) rope_kernel<T, N, HALVES><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
-  else rope_kernel<T, HALVES ? 1 : 2, HALVES><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
+  p.n = static_cast<uint32_t>(p.L) * p.units * p.hgroups;
+  const dim3 grid((p.n + 255) / 256, p.B);
+  if (vec) rope_kernel<T, N, HALVES><<<grid, 256, 0, st>>>(p);
+  else rope_kernel<T, HALVES ? 1 : 2, HALVES><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -287,6 +286,8 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   const int size = dtype_size(p->dtype);
   if (!size) return cache_fail(PSV_EINVAL, "unknown dtype %d", p->dtype);
   if (p->B < 1 || p->L < 1 || p->H < 1) return cache_fail(PSV_EINVAL, "need B, L, H >= 1");
+  if (p->B > 65535 || static_cast<int64_t>(p->L) * p->H * 128 > 0xffffff00ll)
+    return cache_fail(PSV_EINVAL, "B over 65535, or L x H over 2^25");
   if (p->dh < 2 || p->dh > 256 || p->dh % 2) return cache_fail(PSV_EINVAL, "dh %d: even, 2 to 256", p->dh);
   if (p->n_axes < 1 || p->n_axes > 4) return cache_fail(PSV_EINVAL, "n_axes %d: 1 to 4", p->n_axes);
   if (p->layout != PSV_ROPE_PAIRS && p->layout != PSV_ROPE_HALVES)
@@ -341,9 +342,9 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   const bool vec = multiple16(x, p->x_stride, p->B, p->L, p->H, size) &&
                    multiple16(out, p->out_stride, p->B, p->L, p->H, size) && p->dh % N == 0 &&
                    (!halves || ((R / 2) % N == 0 && (p->dh - R) % N == 0));
-  // A thread's angles serve as many heads as leave about 1024 threads an SM.
+  // A thread's angles serve as many heads as leave about 512 threads an SM.
   const int64_t all = static_cast<int64_t>(p->B) * p->L * p->H * (p->dh / (vec ? N : 2));
-  const int64_t hpt = all / (152 * 1024);
+  const int64_t hpt = all / (152 * 512);
   k.hpt = static_cast<int>(hpt < 1 ? 1 : hpt > p->H ? p->H : hpt > 16 ? 16 : hpt);
   k.hgroups = (p->H + k.hpt - 1) / k.hpt;
   k.hpt = (p->H + k.hgroups - 1) / k.hgroups;
@@ -424,24 +425,23 @@ __device__ __forceinline__ void keep_slot(const EvictParams& p, float weight, in
 }
 
 // One CTA per (sequence, kv head) with up to 512 KPT slots: every thread holds
-// KPT consecutive slots' keys in registers, the keep-th greatest key is found
-// two bits at a time by counting, and one scan gives the kept slots their
-// places.  Bound by latency: 16 rounds of compare, warp sums and one barrier.
+// KPT consecutive slots' keys in registers.  The protected slots are set aside;
+// of the others the greatest `left` are found by three histograms of 11 bits
+// in shared memory (the value's sign, exponent and two bits first, so that
+// weights over many octaves spread over the bins), and one scan gives the kept
+// slots their places.  Bound by latency: about five barriers a pass.
 constexpr int kRegThreads = 512;
-
-// Sum over the warps' counts (lanes 0..15 read one each).
-__device__ __forceinline__ int warps_sum(const int* counts) {
-  const int lane = threadIdx.x & 31;
-  return __reduce_add_sync(0xffffffffu, lane < kRegThreads / 32 ? counts[lane] : 0);
-}
 
 template <int KPT>
 __global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictParams p, int vec) {
   __shared__ int scan[64];
-  __shared__ int count[2][3][kRegThreads / 32];
+  __shared__ int hist[2048];
+  __shared__ uint32_t s_thr;
+  __shared__ int s_left;
   pdl_trigger();
-  const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, t = threadIdx.x, warp = t >> 5;
+  const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, t = threadIdx.x;
   const float* mass = p.mass + (static_cast<int64_t>(b) * p.H + h) * p.L;
+  for (int i = t; i < 2048; i += kRegThreads) hist[i] = 0;
   pdl_wait();
   const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
   const int keep = min(n, p.budget);
@@ -460,36 +460,51 @@ __global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictPa
   }
 #pragma unroll
   for (int i = 0; i < KPT; ++i) key[i] = t * KPT + i < n ? select_key(p, x[i], t * KPT + i, n) : 0u;
-  // thr: the greatest value that at least `keep` keys reach; above: how many
-  // are over it.  (No slot's key is 0.)
+  // Keys over thr are kept, `left` of those equal to it.
   uint32_t thr = 0;
-  int above = 0;
+  int left = keep;
   if (keep < n) {
-    for (int shift = 30, r = 0; shift >= 0; shift -= 2, r ^= 1) {
-      int c1 = 0, c2 = 0, c3 = 0;
-      const uint32_t v1 = thr | 1u << shift, v2 = thr | 2u << shift, v3 = thr | 3u << shift;
+    // (sinks + recent <= budget = keep < n: they do not meet.)
+    left = keep - min(p.sinks, n) - p.recent;
+    __syncthreads();
+    for (int shift = 21; left > 0; shift = shift == 21 ? 10 : 0) {
+      const int bits = shift ? 11 : 10;
+      const uint32_t hi = shift == 21 ? 0u : 0xffffffffu << (shift + bits);
 #pragma unroll
       for (int i = 0; i < KPT; ++i) {
-        c1 += key[i] >= v1;
-        c2 += key[i] >= v2;
-        c3 += key[i] >= v3;
+        const int j = t * KPT + i;
+        const bool in = j < n && j >= p.sinks && j < n - p.recent && (key[i] & hi) == thr;
+        if (in) atomicAdd(&hist[(key[i] >> shift) & ((1 << bits) - 1)], 1);
       }
-      c1 = __reduce_add_sync(0xffffffffu, c1);
-      c2 = __reduce_add_sync(0xffffffffu, c2);
-      c3 = __reduce_add_sync(0xffffffffu, c3);
-      if ((t & 31) == 0) count[r][0][warp] = c1, count[r][1][warp] = c2, count[r][2][warp] = c3;
       __syncthreads();
-      c1 = warps_sum(count[r][0]);
-      c2 = warps_sum(count[r][1]);
-      c3 = warps_sum(count[r][2]);
-      if (c3 >= keep) thr = v3;
-      else if (c2 >= keep) thr = v2, above = c3;
-      else if (c1 >= keep) thr = v1, above = c2;
-      else above = c1;
-      // (The counts are rewritten two rounds later, behind the next barrier.)
+      // Thread t holds bins 2047 - 4 t .. 2044 - 4 t (from the top).
+      int own[4], sum = 0, zero = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        own[k] = hist[2047 - 4 * t - k];
+        sum += own[k];
+        hist[2047 - 4 * t - k] = 0;
+      }
+      int before = sum;
+      block_scan2(before, zero, scan);
+      if (before < left && before + sum >= left) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (before < left && before + own[k] >= left) {
+            s_thr = thr | static_cast<uint32_t>(2047 - 4 * t - k) << shift;
+            s_left = left - before;
+          }
+          before += own[k];
+        }
+      }
+      __syncthreads();
+      thr = s_thr;
+      left = s_left;
+      if (shift == 0) break;
     }
+    // With no place left but the protected slots', nothing else is kept.
+    if (keep == min(p.sinks, n) + p.recent) thr = 0xffffffffu, left = keep;
   }
-  const int need = keep - above;  // of the keys equal to thr
   int over = 0, ties = 0;
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
@@ -497,16 +512,17 @@ __global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictPa
     over += in && (keep == n || key[i] > thr);
     ties += in && keep < n && key[i] == thr;
   }
+  __syncthreads();  // scan is used again
   block_scan2(over, ties, scan);
   const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.budget;
   const int64_t meta = b * p.km_b + h * p.km_h;
-  int at = over + min(ties, need);
+  int at = over + min(ties, left);
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
     const int j = t * KPT + i;
     if (j < n) {
       bool k = keep == n || key[i] > thr;
-      if (!k && key[i] == thr) k = ties++ < need;
+      if (!k && key[i] == thr) k = ties++ < left;
       if (k) keep_slot(p, x[i], row, meta, at++, j);
     }
   }
@@ -607,21 +623,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const Ev
 // or one value) of an out row and then the next head; a thread takes kRows such
 // rows, a grid apart, with all their loads on the way at once.
 template <class U, int kRows>
-__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, int units, int esize, int64_t stride) {
-  pdl_wait();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (t >= stride) return;
+__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, uint32_t units, int esize, uint32_t step) {
+  const uint32_t t = blockIdx.x * 256 + threadIdx.x, H = p.H;
+  const uint32_t r = t / units;
+  const int u = static_cast<int>(t - r * units);
+  const int64_t row0 = r / H;
+  const int h = static_cast<int>(r - static_cast<uint32_t>(row0) * H);
   const int b = blockIdx.y;
+  pdl_wait();
+  if (row0 >= step) return;
   const int n = p.k_lens ? min(max(p.k_lens[b], 0), p.L) : p.L;
-  const int u = static_cast<int>(t % units);
-  const int64_t r = t / units;
-  const int h = static_cast<int>(r % p.H);
-  const int64_t row0 = r / p.H, step = stride / units / p.H;
   const int keep = min(n, p.budget);
   U kk[kRows], vv[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int64_t row = row0 + i * step;
+    const int64_t row = row0 + i * static_cast<int64_t>(step);
     if (row >= keep) break;
     const int64_t j = p.idx[(static_cast<int64_t>(b) * p.H + h) * p.budget + row];
     kk[i] = reinterpret_cast<const U*>(static_cast<const char*>(p.k) + (b * p.ks.b + j * p.ks.l + h * p.ks.h) * esize)[u];
@@ -629,7 +645,7 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, 
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int64_t row = row0 + i * step;
+    const int64_t row = row0 + i * static_cast<int64_t>(step);
     if (row >= keep) break;
     reinterpret_cast<U*>(static_cast<char*>(p.k_out) + (b * p.kos.b + row * p.kos.l + h * p.kos.h) * esize)[u] = kk[i];
     reinterpret_cast<U*>(static_cast<char*>(p.v_out) + (b * p.vos.b + row * p.vos.l + h * p.vos.h) * esize)[u] = vv[i];
@@ -653,10 +669,11 @@ template <class U>
 cudaError_t launch_gather(const EvictParams& p, int size, cudaStream_t st) {
   constexpr int kRows = 4;
   const int units = p.dh * size / static_cast<int>(sizeof(U));
-  const int64_t stride = static_cast<int64_t>((p.budget + kRows - 1) / kRows) * p.H * units;
+  const uint32_t step = static_cast<uint32_t>((p.budget + kRows - 1) / kRows);
+  const uint32_t threads = step * p.H * units;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>((stride + 255) / 256), p.B), 256, 0, st, attr);
-  return cudaLaunchKernelEx(&cfg, evict_gather_kernel<U, kRows>, p, units, size, stride);
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((threads + 255) / 256, p.B), 256, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, evict_gather_kernel<U, kRows>, p, static_cast<uint32_t>(units), size, step);
 }
 
 template <int KPT>
@@ -706,8 +723,8 @@ PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const voi
     return cache_fail(PSV_EINVAL, "the rows of k_out or v_out overlap");
   if (p->doc_out && !p->k_doc) return cache_fail(PSV_EINVAL, "doc_out needs k_doc");
   if (p->lens_out && p->lens_out == p->k_lens) return cache_fail(PSV_EINVAL, "lens_out must not be k_lens");
-  if (static_cast<int64_t>(p->budget) * p->Hkv * p->dh > (int64_t{1} << 38))
-    return cache_fail(PSV_EINVAL, "a sequence's kept rows are over 2^38 values");
+  if (static_cast<int64_t>(p->budget) * p->Hkv * p->dh > 0xffffff00ll)
+    return cache_fail(PSV_EINVAL, "a sequence's kept keys are over 2^32 values");
   if (!k || !v || !mass || !k_out || !v_out || !mass_out || !idx_out)
     return cache_fail(PSV_EINVAL, "null pointer");
   const void* typed[4] = {k, v, k_out, v_out};

@@ -104,6 +104,14 @@ struct Row {
   float slope2;
 };
 
+// Key tiles [t0, t1) of a share (at most 2^23 tiles and 304 shares: the
+// product fits 32 bits, whose division is short).
+__device__ __forceinline__ void share_tiles(const RowsParams& p, int k_len, int share, int& t0, int& t1) {
+  const uint32_t nt = static_cast<uint32_t>(k_len + kKeys - 1) / kKeys, n = static_cast<uint32_t>(p.nsplit);
+  t0 = static_cast<int>(nt * static_cast<uint32_t>(share) / n);
+  t1 = static_cast<int>(nt * static_cast<uint32_t>(share + 1) / n);
+}
+
 // A piece and, for this thread's two rows, their queries as A fragments (rows
 // lane / 4 and + 8; columns 2 (lane % 4) + {0, 1, 8, 9} of a step of 16).
 // fetch() only issues the reads (none depends on another), while the piece
@@ -147,9 +155,7 @@ struct Work {
     const CacheParams& c = p.c;
     k_len = min(max(k_len, 0), c.Lk);
     q_len = min(max(q_len, 0), c.Lq);
-    const int nt = (k_len + kKeys - 1) / kKeys;
-    t0 = static_cast<int>(static_cast<int64_t>(nt) * share / p.nsplit);
-    t1 = static_cast<int>(static_cast<int64_t>(nt) * (share + 1) / p.nsplit);
+    share_tiles(p, k_len, share, t0, t1);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int tok = (lane / 4 + 8 * e) / c.G;
@@ -215,9 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int piece = blockIdx.x; piece < p.n_pieces && ok; piece += gridDim.x) {
         const int next_len = key_len(piece + gridDim.x);  // read while this piece is loaded
         const int share = piece % p.nsplit, bh = piece / p.nsplit, b = bh / c.Hkv, kvh = bh % c.Hkv;
-        const int nt = (min(max(len, 0), c.Lk) + kKeys - 1) / kKeys;
-        const int t0 = static_cast<int>(static_cast<int64_t>(nt) * share / p.nsplit);
-        const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (share + 1) / p.nsplit);
+        int t0, t1;
+        share_tiles(p, min(max(len, 0), c.Lk), share, t0, t1);
         len = next_len;
         for (int t = t0; t < t1; ++t, ++g) {
           const uint32_t st = g % ST;
@@ -247,6 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---------------- consumers
   const float scale2 = c.scale * kLog2e;
   uint32_t g0 = 0;  // tiles of earlier pieces
+  const bool two_areas = c.Lq * c.G <= 8;
+  const int jrows = two_areas ? 8 : 16;
+  int n_joined = 0;
   bool ok = true;
   int piece = blockIdx.x;
   Work<DH, MASS> w, next;
@@ -410,9 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_remote(smem_u32(&empty[st]));
     }
     if constexpr (!MASS) {
-      // Join the seven warps.
-      float* so = reinterpret_cast<float*>(smem + C::OFF_JOIN);
-      float* sm = so + kWarps * 16 * DH;
+      // Join the seven warps.  Up to 8 rows there are two join areas, taken in
+      // turn, so that one barrier a piece is enough: an area is written again
+      // two pieces later, behind a barrier that its readers have reached.
+      const int area = two_areas ? n_joined & 1 : 0;
+      ++n_joined;
+      float* so = reinterpret_cast<float*>(smem + C::OFF_JOIN) + area * (C::JOIN / 8);
+      float* sm = so + kWarps * jrows * DH;
       const int rows = w.q_len * c.G;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -422,11 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r < rows) {
 #pragma unroll
           for (int n = 0; n < DH / 8; ++n)
-            *reinterpret_cast<float2*>(so + (warp * 16 + r) * DH + n * 8 + 2 * (lane % 4)) =
+            *reinterpret_cast<float2*>(so + (warp * jrows + r) * DH + n * 8 + 2 * (lane % 4)) =
                 make_float2(o[n][2 * e], o[n][2 * e + 1]);
           if (lane % 4 == 0) {
-            sm[(warp * 16 + r) * 2] = m[e];
-            sm[(warp * 16 + r) * 2 + 1] = l[e];
+            sm[(warp * jrows + r) * 2] = m[e];
+            sm[(warp * jrows + r) * 2 + 1] = l[e];
           }
         }
       }
@@ -436,15 +448,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = u / (DH / 4), d = u % (DH / 4) * 4;
         float mm = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sm[(x * 16 + r) * 2]);
+        for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sm[(x * jrows + r) * 2]);
         const float m0 = mm == -INFINITY ? 0.0f : mm;
         float ll = 0.0f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) {
-          const float f = fast_exp2(sm[(x * 16 + r) * 2] - m0);
-          const float4 y = *reinterpret_cast<const float4*>(so + (x * 16 + r) * DH + d);
-          ll = fmaf(f, sm[(x * 16 + r) * 2 + 1], ll);
+          const float f = fast_exp2(sm[(x * jrows + r) * 2] - m0);
+          const float4 y = *reinterpret_cast<const float4*>(so + (x * jrows + r) * DH + d);
+          ll = fmaf(f, sm[(x * jrows + r) * 2 + 1], ll);
           acc.x = fmaf(f, y.x, acc.x);
           acc.y = fmaf(f, y.y, acc.y);
           acc.z = fmaf(f, y.z, acc.z);
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      asm volatile("bar.sync 1, 224;" ::: "memory");
+      if (!two_areas) asm volatile("bar.sync 1, 224;" ::: "memory");
     }
     g0 += w.t1 - w.t0;
     w = next;
