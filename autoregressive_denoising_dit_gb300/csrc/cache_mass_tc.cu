@@ -15,7 +15,8 @@
 //   warp 1       TMEM allocator (both CTAs) and MMA issuer (even CTA)
 //   warp 2       even CTA: takes pieces from the work queue, publishes them
 //   warp 3       notes the columns of a row tile
-//   warps 4..11  weights: two threads per key (lanes l and l + 16), 128 rows each
+//   warps 4..19  weights: four threads per key (lanes l and l + 16 of two warps),
+//                64 rows each; with eight warps each unit stayed below 45% busy
 #include "cache_attn_tc.cuh"
 
 namespace psv {
@@ -25,6 +26,7 @@ using namespace cattn;
 namespace {
 
 constexpr int QS = 4;          // row-tile stages
+constexpr int kMassThreads = 640, kWeightWarps = 16;
 constexpr int kHalf = 132;     // words between the halves of a column array: other banks
 constexpr int kColWords = 2 * kHalf;
 
@@ -43,7 +45,7 @@ struct MCfg {
   static constexpr int OFF_BAR = OFF_COL + QS * ((COL_BYTES + 127) / 128 * 128);
   static constexpr int COL_STRIDE = (COL_BYTES + 127) / 128 * 128;
   static constexpr int N_BARS = 12 + 4 * QS;
-  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + 8 * 16;
+  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + 8 * 16 + 2 * 128 * 4;
 };
 
 // (x0, x1) * s + (b0, b1).
@@ -58,7 +60,7 @@ __device__ __forceinline__ void ffma2v(float& x0, float& x1, float s, float b0, 
 
 // F: F_CAP, F_BIAS (kernels of their own keep the loop within the instruction cache).
 template <int DH, bool BF16, int F>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kMassThreads, 1)
     cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ TcParams p) {
   using C = MCfg<DH>;
@@ -73,17 +75,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_full = bars + 0;       // [2] even CTA: both K halves landed
   uint64_t* k_empty = bars + 2;      // [2] both: the piece's MMAs are done
   uint64_t* s_full = bars + 4;       // [2] both: S^T of a tile in TMEM
-  uint64_t* s_free = bars + 6;       // [2] even: all 16 weight warps read it
+  uint64_t* s_free = bars + 6;       // [2] even: all 32 weight warps read it
   uint64_t* pc_full = bars + 8;      // [2] both
   uint64_t* pc_empty = bars + 10;    // [2] even
   uint64_t* q_full = bars + 12;      // [QS] even
   uint64_t* q_empty = q_full + QS;   // [QS] both
   uint64_t* c_full = q_empty + QS;   // [QS] own: columns noted
-  uint64_t* c_empty = c_full + QS;   // [QS] own: all 8 weight warps used them
+  uint64_t* c_empty = c_full + QS;   // [QS] own: all 16 weight warps used them
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   int4* pc_slot = reinterpret_cast<int4*>(smem + C::OFF_BAR + C::N_BARS * 8 + 16);  // [2][3]
   static_assert((C::N_BARS * 8) % 16 == 0, "the piece slots are 16-byte aligned");
   int4* sm_piece = pc_slot + 4;                                                      // [2][2]
+  float* part = reinterpret_cast<float*>(sm_piece + 4);                              // [2][128]
 
   pdl_trigger();
   const int warp = warp_id(), lane = lane_id();
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool free16 = i == 6 || i == 7;
       const bool readers = i == 10 || i == 11;
       const bool cols = i >= 12 + 3 * QS;
-      mbar_init(&bars[i], free16 ? 16 : readers ? kPieceReaders : cols ? 8 : 1);
+      mbar_init(&bars[i], free16 ? 2 * kWeightWarps : readers ? kPieceReaders : cols ? kWeightWarps : 1);
     }
     fence_mbar_init();
     prefetch_tensormap(&tmQ);
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.rows_cta < 128) {
     for (int a = 0; a < QS * C::NA; ++a) {
       uint4* z = reinterpret_cast<uint4*>(sQ + a * C::ATOM + p.rows_cta * 128);
-      for (int e = threadIdx.x; e < (128 - p.rows_cta) * 8; e += kThreads) z[e] = make_uint4(0, 0, 0, 0);
+      for (int e = threadIdx.x; e < (128 - p.rows_cta) * 8; e += kMassThreads) z[e] = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
   }
@@ -353,9 +356,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
   } else {
-    // ---------------- weights: warp 4 + 4 h + q serves keys 32 q + 16 h + [0, 16)
-    const int half = lane >> 4;
-    const int rb = (warp & 3) * 32 + ((warp - 4) >> 2) * 16;
+    // ---------------- weights: warps 4 + 4 h + q and 12 + 4 h + q serve keys
+    // 32 q + 16 h + [0, 16), the first columns [0, 64) of each half of a tile,
+    // the second columns [64, 128).
+    const int half = lane >> 4, quarter = (warp - 4) >> 3;
+    const int rb = (warp & 3) * 32 + (((warp - 4) >> 2) & 1) * 16;
     const int r = rb + (lane & 15);
     const uint32_t lane_off = static_cast<uint32_t>(rb) << 16;
     const uint32_t s_free0 = mapa_shared(s_free, 0);
@@ -371,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       // (A copy is rewritten two pieces later, behind a barrier that its readers passed.)
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, 512;" ::: "memory");
       const int4 pa = ld_shared_v4(sm_piece + 2 * (i & 1)), pb = ld_shared_v4(sm_piece + 2 * (i & 1) + 1);
       if (pa.x < 0) break;
-      if (warp == 11 && lane == 0) release_piece(i);
+      if (warp == 19 && lane == 0) release_piece(i);
       __syncwarp();
       const int b = pa.x / p.c.Hkv, kvh = pa.x % p.c.Hkv, nk = pb.x, nT = pa.w;
       const int key = pa.y * KT + rank * 128 + r;
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kd = p.c.k_doc ? p.c.k_doc[meta + kc] : 0;
       const int64_t at = static_cast<int64_t>(pa.x) * p.c.Lk + key;
       float old = 0.0f;
-      if (valid && half == 0 && p.c.mass_in) old = p.c.mass_in[at];
+      if (valid && half == 0 && quarter == 0 && p.c.mass_in) old = p.c.mass_in[at];
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool ok = true;
       for (int j = 0; j < nT; ++j, ++g) {
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool masked = __any_sync(0xffffffffu, valid && !whole);
         const bool unused = stat[0] == -0x7fffffff - 1;
         const uint32_t s_addr = tmem + sb * 256 + lane_off;
-        // 32 columns at a time, the next ones on their way from TMEM meanwhile.
+        // 32 columns at a time.
         auto add_chunk = [&](float* v, int ch) {
           const float* cc = col + half * kHalf + ch * 32;
           const int* ic = reinterpret_cast<const int*>(cc);
@@ -453,16 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             fadd2(acc[(e & 4) + 2], acc[(e & 4) + 3], fast_exp2(v[e + 2]), fast_exp2(v[e + 3]));
           }
         };
-        float s0[32], s1[32];
-        tmem_ld32x<128>(s_addr, s0);
+        float s[32];
 #pragma unroll 1
-        for (int ch = 0; ch < 4; ch += 2) {
+        for (int ch = 2 * quarter; ch < 2 * quarter + 2; ++ch) {
+          tmem_ld32x<128>(s_addr + ch * 32, s);
           tmem_wait_ld();
-          tmem_ld32x<128>(s_addr + (ch + 1) * 32, s1);
-          add_chunk(s0, ch);
-          tmem_wait_ld();
-          if (ch == 0) tmem_ld32x<128>(s_addr + 64, s0);
-          add_chunk(s1, ch + 1);
+          add_chunk(s, ch);
         }
         tc_fence_before();
         __syncwarp();
@@ -474,7 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      if (ok && valid && half == 0) p.c.mass_out[at] = old + sum;
+      // The two warps of a key: the second leaves its sum for the first.
+      float* other = part + (i & 1) * 128;
+      if (quarter == 1 && half == 0) other[r] = sum;
+      __syncwarp();
+      // (The next piece's barrier keeps the two uses of a buffer apart.)
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + ((warp - 4) & 7)) : "memory");
+      if (ok && quarter == 0 && valid && half == 0) p.c.mass_out[at] = old + (sum + other[r]);
       __syncwarp();
     }
   }
@@ -516,7 +523,7 @@ cudaError_t launch(const CUtensorMap* maps, const TcParams& p, int pairs, cudaSt
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kMassThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;

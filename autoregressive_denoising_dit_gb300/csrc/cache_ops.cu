@@ -51,16 +51,16 @@ int cuda_status(cudaError_t e, const char* what) {
   return cache_fail(PSV_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Device memory of the current device (managed memory counts).
-int check_device(const void* ptr, const char* name) {
+// Device memory of the current device `dev` (managed memory counts).  A look at
+// a pointer takes the host about 0.4 us, so that a call looks at its first
+// input and its output: what is mixed up in practice is whole sets of tensors.
+int check_device(int dev, const void* ptr, const char* name) {
   if (!ptr) return cache_fail(PSV_EINVAL, "%s is null", name);
   cudaPointerAttributes a;
   cudaError_t e = cudaPointerGetAttributes(&a, ptr);
   if (e != cudaSuccess) return cuda_status(e, name);
   if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
     return cache_fail(PSV_EINVAL, "%s is not device memory", name);
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_status(e, "cudaGetDevice");
   if (a.type == cudaMemoryTypeDevice && a.device != dev)
     return cache_fail(PSV_EINVAL, "%s is on device %d, the current device is %d", name, a.device, dev);
   return PSV_OK;
@@ -109,6 +109,21 @@ bool multiple16(const void* ptr, const int64_t* s, int64_t n0, int64_t n1, int64
   for (int i = 0; i < 3; ++i)
     if (n[i] > 1 && (s[i] * size) % 16 != 0) return false;
   return true;
+}
+
+// A launch that may begin while the kernel before it ends (it waits for that
+// kernel's results itself).
+cudaLaunchConfig_t pdl_config(dim3 grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
 }
 
 // ------------------------------------------------------------------ rope
@@ -190,6 +205,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
   const int hg = static_cast<int>(rest % hgroups);
   const int b = blockIdx.y;
   const int64_t l = rest / hgroups;
+  pdl_trigger();
+  pdl_wait();
   if (p.lens && l >= p.lens[b]) return;
   const bool rot = !HALVES || u < p.rot_units;
   // Values [d0, d0 + VEC); HALVES: partners at d0 + R/2.
@@ -270,10 +287,10 @@ cudaError_t launch_rope_t(RopeParams& p, bool vec, cudaStream_t st) {
     p.units = p.dh / V;
   }
   p.n = static_cast<uint32_t>(p.L) * p.units * p.hgroups;
-  const dim3 grid((p.n + 255) / 256, p.B);
-  if (vec) rope_kernel<T, N, HALVES><<<grid, 256, 0, st>>>(p);
-  else rope_kernel<T, HALVES ? 1 : 2, HALVES><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((p.n + 255) / 256, p.B), 256, 0, st, attr);
+  return vec ? cudaLaunchKernelEx(&cfg, rope_kernel<T, N, HALVES>, p)
+             : cudaLaunchKernelEx(&cfg, rope_kernel<T, HALVES ? 1 : 2, HALVES>, p);
 }
 
 }  // namespace
@@ -324,9 +341,11 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(out) & mask) ||
       (reinterpret_cast<uintptr_t>(pos) & 3))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
-  if (int r = check_device(x, "x")) return r;
-  if (int r = check_device(pos, "pos")) return r;
-  if (int r = check_device(out, "out")) return r;
+  int dev = 0;
+  if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
+  if (int r = check_device(dev, x, "x")) return r;
+  if (out != x)
+    if (int r = check_device(dev, out, "out")) return r;
   k.x = x;
   k.out = out;
   k.pos = pos;
@@ -436,6 +455,8 @@ template <int KPT>
 __global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictParams p, int vec) {
   __shared__ int scan[64];
   __shared__ int hist[2048];
+  __shared__ uint16_t kept[KPT * kRegThreads];
+  static_assert(KPT * kRegThreads <= 65536, "slots fit 16 bits");
   __shared__ uint32_t s_thr;
   __shared__ int s_left;
   pdl_trigger();
@@ -516,6 +537,8 @@ __global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictPa
   block_scan2(over, ties, scan);
   const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.budget;
   const int64_t meta = b * p.km_b + h * p.km_h;
+  // The kept slots are listed in shared memory and written from there, so that
+  // consecutive threads write consecutive places.
   int at = over + min(ties, left);
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
@@ -523,9 +546,11 @@ __global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictPa
     if (j < n) {
       bool k = keep == n || key[i] > thr;
       if (!k && key[i] == thr) k = ties++ < left;
-      if (k) keep_slot(p, x[i], row, meta, at++, j);
+      if (k) kept[at++] = static_cast<uint16_t>(j);
     }
   }
+  __syncthreads();
+  for (int a = t; a < keep; a += kRegThreads) keep_slot(p, mass[kept[a]], row, meta, a, kept[a]);
   if (h == 0 && t == 0 && p.lens_out) p.lens_out[b] = keep;
 }
 
@@ -652,19 +677,6 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, 
   }
 }
 
-cudaLaunchConfig_t pdl_config(dim3 grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
-  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr->val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-
 template <class U>
 cudaError_t launch_gather(const EvictParams& p, int size, cudaStream_t st) {
   constexpr int kRows = 4;
@@ -741,10 +753,10 @@ PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const voi
   if (overlap(k, in_k, k_out, out_k) || overlap(v, in_v, v_out, out_v) || overlap(mass, in_m, mass_out, out_m))
     return cache_fail(PSV_EINVAL, "out buffers must not overlap their inputs");
   if (k_out == v_out) return cache_fail(PSV_EINVAL, "k_out and v_out are the same buffer");
-  struct { const void* ptr; const char* name; } ptrs[7] = {{k, "k"}, {v, "v"}, {mass, "mass"}, {k_out, "k_out"},
-      {v_out, "v_out"}, {mass_out, "mass_out"}, {idx_out, "idx_out"}};
-  for (const auto& x : ptrs)
-    if (int r = check_device(x.ptr, x.name)) return r;
+  int dev = 0;
+  if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
+  if (int r = check_device(dev, k, "k")) return r;
+  if (int r = check_device(dev, k_out, "k_out")) return r;
   EvictParams e{};
   e.k = k, e.v = v, e.mass = mass, e.k_out = k_out, e.v_out = v_out, e.mass_out = mass_out, e.idx = idx_out;
   e.k_lens = p->k_lens, e.k_pos = p->k_pos, e.k_doc = p->k_doc;
@@ -793,7 +805,6 @@ int check_cache(const psv_cache_problem* p) {
 }
 
 int check_scratch(void* scratch, size_t bytes, size_t need) {
-  if (int r = check_device(scratch, "scratch")) return r;
   if (reinterpret_cast<uintptr_t>(scratch) & 255) return cache_fail(PSV_EINVAL, "scratch must be 256-byte aligned");
   if (bytes < need) return cache_fail(PSV_EINVAL, "scratch of %zu bytes, %zu needed", bytes, need);
   return PSV_OK;
@@ -821,11 +832,6 @@ size_t cache_scratch(const psv_cache_problem* p) {
   return psv::cache_attn_tc_shape(c) ? psv::cache_attn_tc_scratch(c) : PSV_CACHE_SCRATCH_HEAD;
 }
 
-cudaError_t sm_count(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-}
 
 }  // namespace
 
@@ -847,21 +853,17 @@ PSV_API int psv_cache_attention(const psv_cache_problem* p, const void* q, const
                        reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(o);
   if ((at & 1) || (reinterpret_cast<uintptr_t>(lse) & 3))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
-  if (int r = check_device(q, "q")) return r;
-  if (p->Lk) {
-    if (int r = check_device(k, "k")) return r;
-    if (int r = check_device(v, "v")) return r;
-  }
-  if (int r = check_device(o, "o")) return r;
-  if (lse)
-    if (int r = check_device(lse, "lse")) return r;
+  int dev = 0;
+  if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
+  if (int r = check_device(dev, q, "q")) return r;
+  if (int r = check_device(dev, o, "o")) return r;
   if (int r = check_scratch(scratch, scratch_bytes, cache_scratch(p))) return r;
   CacheParams c = cache_params(p, q, k, scratch);
   c.v = v, c.o = o, c.lse = lse;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (psv::cache_attn_tc_shape(c) && psv::cache_attn_tc_aligned(c)) {
     int sms = 0;
-    cudaError_t e = sm_count(&sms);
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
       e = psv::launch_cache_attention_tc(c, p->dtype == PSV_DTYPE_BF16, static_cast<char*>(scratch), sms, st);
     return cuda_status(e, "attention launch");
@@ -881,21 +883,17 @@ PSV_API int psv_cache_mass(const psv_cache_problem* p, const void* q, const void
   const int64_t bytes = static_cast<int64_t>(p->B) * p->Hkv * p->Lk * 4;
   if (mass_in && mass_in != mass_out && overlap(mass_in, bytes, mass_out, bytes))
     return cache_fail(PSV_EINVAL, "mass_in overlaps mass_out in part");
-  if (p->Lq) {
-    if (int r = check_device(q, "q")) return r;
-    if (int r = check_device(lse, "lse")) return r;
-  }
-  if (int r = check_device(k, "k")) return r;
-  if (mass_in)
-    if (int r = check_device(mass_in, "mass_in")) return r;
-  if (int r = check_device(mass_out, "mass_out")) return r;
+  int dev = 0;
+  if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
+  if (int r = check_device(dev, k, "k")) return r;
+  if (int r = check_device(dev, mass_out, "mass_out")) return r;
   if (int r = check_scratch(scratch, scratch_bytes, cache_scratch(p))) return r;
   CacheParams c = cache_params(p, q, k, scratch);
   c.lse = const_cast<float*>(lse), c.mass_in = mass_in, c.mass_out = mass_out;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (psv::cache_mass_tc(c)) {
     int sms = 0;
-    cudaError_t e = sm_count(&sms);
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = psv::launch_cache_mass_tc(c, p->dtype == PSV_DTYPE_BF16, static_cast<char*>(scratch), sms, st);
     return cuda_status(e, "mass launch");
   }
