@@ -299,6 +299,10 @@ __device__ __forceinline__ int4 ld_meta4(const int32_t* m, int j, int k_len, int
                    __ldg(m + min(j + 3, last)));
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // First c in [lo, hi) with d[c] >= doc, else hi (d does not decrease).
 __device__ __forceinline__ int first_doc(const int32_t* d, int lo, int hi, int doc) {
   while (lo < hi) {
@@ -712,8 +716,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const KeyTile* tiles =
           p.key_tiles + (static_cast<int64_t>(b) * p.meta_heads + (p.meta_heads > 1 ? kvh : 0)) * p.tiles;
       const int plim = max(qp + 1, prefix);  // positions below it are seen
-      KeyTile kt_next{};
-      if ((F & F_META) && p.key_tiles && nT > 0) kt_next = tiles[pb.z];
+      // A tile's notes, and its keys' positions and documents, are brought to L1
+      // one tile ahead (held in registers they were spilled, and waited for).
+      auto fetch_meta = [&](int tile) {
+        if (lane == 0) prefetch_l1(tiles + tile);
+        const int j = min(tile * KT + 32 * lane, k_len - 1);
+        if (lane < 8 && p.c.k_doc) prefetch_l1(p.c.k_doc + meta + j);
+        if (lane < 8 && p.c.k_pos) prefetch_l1(p.c.k_pos + meta + j);
+      };
+      if ((F & F_META) && p.key_tiles && nT > 0 && active) fetch_meta(pb.z);
       float m = -INFINITY, l = 0.0f;  // l: this thread's half of the row sum
       bool ok = true;
       // Releases the first half of a tile's P (and its V).  In a tile that ends
@@ -755,8 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int d0 = qp - key0;  // distance of the first key, where positions run
         bool run = true;
         if ((F & F_META) && p.key_tiles && active) {
-          const KeyTile kt = kt_next;
-          if (j + 1 < nT) kt_next = tiles[pb.z + j + 1];
+          const KeyTile kt = tiles[pb.z + j];
+          if (j + 1 < nT) fetch_meta(pb.z + j + 1);
           run = kt.run;
           if (p.c.k_pos) d0 = qp - kt.base - hk16 * 128;
           const bool doc_all = !p.c.k_doc || (kt.doc_min == qd && kt.doc_max == qd);
