@@ -55,12 +55,14 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
   const int nk = cache_k_len(p.c, b), nq = cache_q_len(p.c, b);
   for (int i = unit * 2 * p.tok_cta + lane; i < min(nq, (unit + 1) * 2 * p.tok_cta); i += 32) {
     const int doc = p.c.q_doc ? p.c.q_doc[b * p.c.qm_b + i] : 0;
-    pmax = max(pmax, p.c.q_pos ? p.c.q_pos[b * p.c.qm_b + i] : nk - nq + i);
+    const int pos = p.c.q_pos ? p.c.q_pos[b * p.c.qm_b + i] : nk - nq + i;
+    pmin = min(pmin, pos), pmax = max(pmax, pos);
     dmin = min(dmin, doc), dmax = max(dmax, doc);
   }
+  pmin = __reduce_min_sync(0xffffffffu, pmin);
   pmax = __reduce_max_sync(0xffffffffu, pmax);
   dmin = __reduce_min_sync(0xffffffffu, dmin), dmax = __reduce_max_sync(0xffffffffu, dmax);
-  if (lane == 0) p.row_units[w] = RowUnit{pmax, dmin, dmax, 0};
+  if (lane == 0) p.row_units[w] = RowUnit{pmin, pmax, dmin, dmax};
 }
 
 // Joins the shares of a row: one CTA per (sequence, head, token).  Each of its
@@ -212,8 +214,8 @@ size_t cache_attn_tc_scratch(const CacheParams& c) { return tc_layout(c).total; 
 
 namespace {
 
-// tanh(sqrt z) / sqrt z interpolated at the Chebyshev points of [0, 1/9] and [0, 1].
-constexpr double kTanh4[4] = {0.9999999761663968, -0.33332645959641233, 0.13302166406252694, -0.04939401888519419};
+// tanh(sqrt z) / sqrt z interpolated at the Chebyshev points of [0, 0.18^2] and [0, 1].
+constexpr double kTanh3[3] = {0.9999999437513383, -0.33330206128320755, 0.13074870575291475};
 constexpr double kTanh7[7] = {0.9999999486455696, -0.3333282797859907, 0.13325076146101278, -0.05345164636973283, 0.02027970828564412, -0.006194324833673898, 0.0010380250967268723};
 
 // Coefficients of cap2 for scores s: cap log2(e) tanh(s inv) = s sum_k c_k s^(2k).
@@ -232,7 +234,7 @@ void set_cap(TcParams& p) {
   p.cap_small = p.cap_mid = -1.0f;
   if (!(p.c.softcap > 0)) return;
   const double inv = static_cast<double>(p.c.scale) / p.c.softcap, cap2e = p.c.softcap * 1.4426950408889634;
-  if (set_cap_poly(p.cap_c4, kTanh4, 4, inv, cap2e)) p.cap_small = static_cast<float>(1.0 / 3.0 / inv);
+  if (set_cap_poly(p.cap_c3, kTanh3, 3, inv, cap2e)) p.cap_small = static_cast<float>(0.18 / inv);
   if (set_cap_poly(p.cap_c7, kTanh7, 7, inv, cap2e)) p.cap_mid = static_cast<float>(1.0 / inv);
 }
 

@@ -266,7 +266,7 @@ struct alignas(16) KeyTile {
   int cut;  // the first `cut` keys are of doc_min, the others of doc_max; -1: not so
 };
 struct RowUnit {
-  int pos_max, doc_min, doc_max, pad;
+  int pos_min, pos_max, doc_min, doc_max;
 };
 
 struct TcParams {
@@ -284,7 +284,7 @@ struct TcParams {
   KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
   RowUnit* row_units;  // [B][units]
   float cap_small, cap_mid;       // scores up to which the polynomials hold
-  float2 cap_c4[4], cap_c7[7];    // their coefficients, each twice
+  float2 cap_c3[3], cap_c7[7];    // their coefficients, each twice
   int* queue;       // next piece, pairs done (zero between launches)
   float* part_o;    // [piece][part_rows][DH], unnormalised
   float2* part_ml;  // [piece][part_rows]: m (log2), l
@@ -317,7 +317,8 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// {sequence * Hkv + kv head, unit, share, 0}, x = -1 past the end; and
+// {sequence * Hkv + kv head, unit, share (7 bits) and above it the number of
+// key tiles from w on that every row sees whole, w}, x = -1 past the end; and
 // {k_len, q_len, first key tile, key tiles}.
 struct Piece {
   int4 a, b;
@@ -342,27 +343,39 @@ __device__ __forceinline__ int unit_limit(const TcParams& p, int b, int unit, in
 }
 
 // Narrows the key tiles [first, last) to those from the first to the last one
-// with a key that some row of the unit sees (by the whole warp).
-__device__ __forceinline__ void seen_tiles(const TcParams& p, int b, int kvh, int unit, int k_len, int& first,
-                                           int& last) {
+// with a key that some row of the unit sees, and finds a stretch of tiles that
+// every row sees whole, [whole, whole + count) (by the whole warp).
+__device__ __forceinline__ void seen_tiles(const TcParams& p, int b, int kvh, int unit, int& first, int& last,
+                                           int& whole, int& count) {
   const KeyTile* tiles = p.key_tiles + (static_cast<int64_t>(b) * p.meta_heads + (p.meta_heads > 1 ? kvh : 0)) * p.tiles;
   const RowUnit u = p.row_units[static_cast<int64_t>(b) * p.units + unit];
   const int prefix = p.c.prefix ? p.c.prefix[b] : 0;
-  const int plim = max(u.pos_max + 1, prefix);
-  int lo = 0x7fffffff, hi = 0;
+  const bool ordered = p.c.causal && p.c.k_pos;
+  const int most = max(u.pos_max + 1, prefix), least = max(u.pos_min + 1, prefix);
+  auto is_whole = [&](const KeyTile& k) {
+    return (!p.c.k_doc || (k.doc_min == k.doc_max && u.doc_min == k.doc_min && u.doc_max == k.doc_min)) &&
+           (!ordered || k.pos_max < least);
+  };
+  int lo = 0x7fffffff, hi = 0, w0 = 0x7fffffff, w1 = 0x7fffffff;
   for (int t = static_cast<int>(lane_id()); t < last; t += 32) {
     const KeyTile k = tiles[t];
     const bool docs = !p.c.k_doc || (k.doc_min <= u.doc_max && k.doc_max >= u.doc_min);
-    const bool order = !p.c.causal || k.pos_min < plim;
-    if (docs && order) {
+    if (docs && (!p.c.causal || k.pos_min < most)) {
       lo = min(lo, t);
       hi = t + 1;
+      if (is_whole(k)) w0 = min(w0, t);
     }
   }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
+  w0 = __reduce_min_sync(0xffffffffu, w0);
+  for (int t = static_cast<int>(lane_id()); t < hi; t += 32)
+    if (t > w0 && w1 > t && !is_whole(tiles[t])) w1 = t;
+  w1 = min(__reduce_min_sync(0xffffffffu, w1), hi);
   first = min(lo, hi);
   last = hi;
+  whole = min(w0, hi);
+  count = max(w1 - whole, 0);
 }
 
 // Whether a key tile ends behind the keys inside the buffer (rows behind the
@@ -373,8 +386,8 @@ __device__ __forceinline__ bool zero_tile(const TcParams& p, int key0, int k_len
 
 // cap log2(e) tanh(s inv) of a pair of scores as s P(s^2), P of degree N - 1
 // with coefficients c (scaled by the powers of inv = scale / cap and by cap
-// log2 e), from interpolating tanh(sqrt z) / sqrt z at Chebyshev points: 4 of
-// [0, 1/9] for |s inv| <= 1/3 (error of tanh 1e-8), 7 of [0, 1] for |s inv|
+// log2 e), from interpolating tanh(sqrt z) / sqrt z at Chebyshev points: 3 of
+// [0, 0.0324] for |s inv| <= 0.18 (error of tanh 8e-9), 7 of [0, 1] for |s inv|
 // <= 1 (5e-8).  The packed products are bound by the FMA pipe, which is why
 // small scores, the usual ones under a cap, have a short polynomial.
 template <int N>
@@ -482,12 +495,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nk = cache_k_len(p.c, b), nq = cache_q_len(p.c, b);
           rows = pc.a.y * 2 * p.tok_cta < nq;
           int first = 0, last = (unit_limit(p, b, pc.a.y, nk, nq) + KT - 1) / KT;
-          if (rows && p.key_tiles) seen_tiles(p, b, pc.a.x % p.c.Hkv, pc.a.y, nk, first, last);
+          int whole = 0, count = 0;
+          if (rows && p.key_tiles) seen_tiles(p, b, pc.a.x % p.c.Hkv, pc.a.y, first, last, whole, count);
           // (At most 2^20 tiles and 76 shares.)
           const uint32_t nt = static_cast<uint32_t>(last - first), n = static_cast<uint32_t>(p.nsplit);
           const int t0 = static_cast<int>(nt * static_cast<uint32_t>(pc.a.z) / n);
           const int t1 = static_cast<int>(nt * static_cast<uint32_t>(pc.a.z + 1) / n);
           pc.b = make_int4(nk, nq, first + t0, t1 - t0);
+          pc.a.z |= count << 7;
+          pc.a.w = whole;
         }
         int next = 0;
         if (lane == 0) {
@@ -765,14 +781,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool masked = false;
         int d0 = qp - key0;  // distance of the first key, where positions run
         bool run = true;
-        if ((F & F_META) && p.key_tiles && active) {
+        // (A stretch of tiles is known to be seen whole; only the distance bias
+        // then needs the tile's notes.)
+        const bool whole = static_cast<uint32_t>(pb.z + j - pa.w) < static_cast<uint32_t>(pa.z >> 7);
+        if ((F & F_META) && p.key_tiles && active && ((F & F_BIAS) || !whole)) {
           const KeyTile kt = tiles[pb.z + j];
           if (j + 1 < nT) fetch_meta(pb.z + j + 1);
           run = kt.run;
           if (p.c.k_pos) d0 = qp - kt.base - hk16 * 128;
           const bool doc_all = !p.c.k_doc || (kt.doc_min == qd && kt.doc_max == qd);
           const bool pos_all = !ordered || kt.pos_max < plim;
-          masked = __any_sync(0xffffffffu, valid && !(doc_all && pos_all));
+          masked = !whole && __any_sync(0xffffffffu, valid && !(doc_all && pos_all));
           if (masked && kt.sorted && (run || !ordered)) {
             // The row's document is one stretch of the tile, and positions that
             // run are seen up to a limit: keys [lo, hi).
@@ -843,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 128; c += 2) big = max3(big, fabsf(s[c]), fabsf(s[c + 1]));
             if (__all_sync(0xffffffffu, !valid || big <= p.cap_small)) {
 #pragma unroll
-              for (int c = 0; c < 128; c += 2) cap2<4>(s[c], s[c + 1], p.cap_c4);
+              for (int c = 0; c < 128; c += 2) cap2<3>(s[c], s[c + 1], p.cap_c3);
             } else if (__all_sync(0xffffffffu, !valid || big <= p.cap_mid)) {
 #pragma unroll
               for (int c = 0; c < 128; c += 2) cap2<7>(s[c], s[c + 1], p.cap_c7);
@@ -972,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O is read before this thread writes any P of the next piece, whose
       // first P.V overwrites it.
       const bool split = p.nsplit > 1;
-      const int64_t piece = (static_cast<int64_t>(pa.x) * p.units + pa.y) * p.nsplit + pa.z;
+      const int64_t piece = (static_cast<int64_t>(pa.x) * p.units + pa.y) * p.nsplit + (pa.z & 127);
       const int64_t prow = piece * p.part_rows + rank * p.rows_cta + r;
       using T = uint16_t;
       T* dst = static_cast<T*>(p.c.o) + b * p.c.os.b + tok * p.c.os.l + head * p.c.os.h + hk16 * C::OH;

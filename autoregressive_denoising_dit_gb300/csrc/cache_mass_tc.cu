@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             // (In a tile with unused rows their values must not choose the branch.)
             if (!unused && __all_sync(0xffffffffu, !valid || big <= p.cap_small)) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) cap2<4>(v[e], v[e + 1], p.cap_c4);
+              for (int e = 0; e < 32; e += 2) cap2<3>(v[e], v[e + 1], p.cap_c3);
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] = fmaf(-2.0f * c2, fast_rcp(1.0f + fast_exp2(v[e] * two)), c2);
