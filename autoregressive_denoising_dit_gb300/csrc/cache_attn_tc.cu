@@ -65,6 +65,27 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
   if (lane == 0) p.row_units[w] = RowUnit{pmin, pmax, dmin, dmax};
 }
 
+// A head group's rows' slopes / scale as three values of the operand type whose
+// sum holds 24 bits, in the layout of kLinBytes; and whether they fit it.
+template <bool BF16>
+__global__ void __launch_bounds__(128) cache_lin_kernel(const __grid_constant__ TcParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const int r = threadIdx.x, kvh = blockIdx.x;
+  const float v = r < p.rows_cta ? p.c.slopes[kvh * p.c.G + r % p.c.G] / p.c.scale : 0.0f;
+  // (f16 ends at 65504; in bf16 255 times the value must stay finite.)
+  const int ok = __syncthreads_and(fabsf(v) <= (BF16 ? 1e30f : 6e4f));
+  auto part = [](float x) {
+    if constexpr (BF16) return __bfloat162float(__float2bfloat16_rn(x));
+    else return __half2float(__float2half_rn(x));
+  };
+  const float hi = part(v), mid = part(v - hi), lo = v - hi - mid;
+  uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.lin_q) + kvh * kLinBytes + (r / 8) * 256 + (r % 8) * 16);
+  dst[0] = ok ? make_uint4(pack2<BF16>(hi, mid), pack2<BF16>(lo, 0.0f), 0, 0) : make_uint4(0, 0, 0, 0);
+  dst[8] = make_uint4(0, 0, 0, 0);
+  if (r == 0) p.lin_ok[kvh] = ok;
+}
+
 // Joins the shares of a row: one CTA per (sequence, head, token).  Each of its
 // four warps adds up every fourth share, lanes over the columns, four shares'
 // rows on the way at once; the warps' sums are added in order.  Bound by the
@@ -146,7 +167,8 @@ struct TcLayout {
   int width, rows_cta, tok_cta, units, nsplit, part_rows;
   int64_t pieces;
   int tiles, meta_heads;  // of the buffer; 0: no positions or documents
-  size_t part_o, part_ml, key_tiles, row_units, total;
+  bool lin;  // the distance bias by products (no cap, no positions or documents given)
+  size_t part_o, part_ml, key_tiles, row_units, lin_ok, lin_q, total;
 };
 
 TcLayout tc_layout(const CacheParams& c) {
@@ -183,6 +205,13 @@ TcLayout tc_layout(const CacheParams& c) {
     off += up256(sizeof(KeyTile) * static_cast<size_t>(c.B) * t.meta_heads * t.tiles);
     t.row_units = off;
     off += up256(sizeof(RowUnit) * static_cast<size_t>(c.B) * t.units);
+  }
+  t.lin = !t.few && c.slopes && !(c.softcap > 0) && !c.k_pos && !c.k_doc && !c.q_pos;
+  if (t.lin) {
+    t.lin_ok = off;
+    off += up256(sizeof(int) * static_cast<size_t>(c.Hkv));
+    t.lin_q = off;
+    off += static_cast<size_t>(c.Hkv) * kLinBytes;
   }
   t.total = off;
   return t;
@@ -238,6 +267,19 @@ void set_cap(TcParams& p) {
   if (set_cap_poly(p.cap_c7, kTanh7, 7, inv, cap2e)) p.cap_mid = static_cast<float>(1.0 / inv);
 }
 
+cudaError_t launch_lin(const TcParams& p, bool bf16, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.c.Hkv);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return bf16 ? cudaLaunchKernelEx(&cfg, cache_lin_kernel<true>, p) : cudaLaunchKernelEx(&cfg, cache_lin_kernel<false>, p);
+}
+
 cudaError_t launch_join(const TcParams& p, bool bf16, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Lq * p.c.Hq;
   cudaLaunchConfig_t cfg = {};
@@ -267,6 +309,10 @@ TcParams cattn::plan(const CacheParams& c, char* scratch) {
   if (t.meta_heads) {
     p.key_tiles = reinterpret_cast<KeyTile*>(scratch + t.key_tiles);
     p.row_units = reinterpret_cast<RowUnit*>(scratch + t.row_units);
+  }
+  if (t.lin) {
+    p.lin_ok = reinterpret_cast<int*>(scratch + t.lin_ok);
+    p.lin_q = reinterpret_cast<uint16_t*>(scratch + t.lin_q);
   }
   set_cap(p);
   p.queue = reinterpret_cast<int*>(scratch) + 1;
@@ -320,8 +366,15 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
     e = launch_cache_rows(r, bf16, false, st);
     return e != cudaSuccess || p.nsplit == 1 ? e : launch_join(p, bf16, st);
   }
-  CUtensorMap maps[3];
+  CUtensorMap maps[4];
   if (!encode_maps(maps, c, p, bf16, true)) return cudaErrorInvalidValue;
+  maps[3] = maps[0];
+  if (p.lin_q) {
+    const uint64_t dims[3] = {64, kLinBytes / 128, static_cast<uint64_t>(c.Hkv)}, str[2] = {128, kLinBytes};
+    const uint32_t box[3] = {64, kLinBytes / 128, 1};
+    if (!encode_16bit_map(&maps[3], bf16, 3, p.lin_q, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
+    if ((e = launch_lin(p, bf16, st)) != cudaSuccess) return e;
+  }
   if ((e = launch_tiles(p, st)) != cudaSuccess) return e;
   const int pairs = p.n_pieces < sms / 2 ? p.n_pieces : sms / 2;
   const int f = (c.softcap > 0 ? F_CAP : 0) | (c.slopes ? F_BIAS : 0) | (c.k_doc || c.k_pos || c.q_pos ? F_META : 0);

@@ -52,12 +52,17 @@ constexpr int kThreads = 384;
 constexpr int kStages = 3;
 constexpr int kRegsLow = 64, kRegsHigh = 216;
 constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsHigh;
+// A step of 16 values for 128 rows: 8-row groups of 256 bytes, in each the rows'
+// first 8 values (16 bytes a row), then their second 8 (no swizzle).
+constexpr int kLinBytes = 128 * 32;
 // Readers of a published piece: in both CTAs the Q/K loader, the V loader and
 // one softmax thread; the even CTA's MMA issuer.
 constexpr int kPieceReaders = 7;
 
-template <int DH>
+// LIN: with the products that add the distance bias (see cache_attn_kernel).
+template <int DH, bool LIN>
 struct Cfg {
+  static constexpr int KK = LIN ? 2 : kStages;  // K stages (two measured as fast as three)
   static constexpr int NA = DH / 64;            // 64-wide (128-byte) atoms along dh
   static constexpr int VR = DH / 2;             // V columns held per CTA
   static constexpr int Q_BYTES = QT * DH * 2;
@@ -67,8 +72,9 @@ struct Cfg {
   static constexpr int V_ROW = VR * 2;          // bytes of a V row: 128 or 64 (its swizzle width)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + Q_BYTES;
-  static constexpr int OFF_V = OFF_K + kStages * K_BYTES;
-  static constexpr int OFF_BAR = OFF_V + kStages * V_BYTES;
+  static constexpr int OFF_V = OFF_K + KK * K_BYTES;
+  static constexpr int OFF_LIN = OFF_V + kStages * V_BYTES;  // Q's part, K's part, K's negative part
+  static constexpr int OFF_BAR = OFF_LIN + (LIN ? 3 * kLinBytes : 0);
   static constexpr int N_BARS = 13 + 5 * kStages;  // an even number
   // barriers, TMEM address, two published piece slots and the softmax's copies
   static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + 8 * 16;
@@ -97,6 +103,12 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t smem_addr, uint32_t row_byt
   return umma_desc_kmajor(smem_addr, row_bytes);
 }
 
+// K-major operand in the layout of kLinBytes.
+__device__ __forceinline__ uint64_t desc_lin(uint32_t smem_addr) {
+  return static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 16 |
+         static_cast<uint64_t>(256 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+
 __device__ __forceinline__ void umma_pair_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
                                                  uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -105,6 +117,10 @@ __device__ __forceinline__ void umma_pair_tmem_a(uint32_t tmem_d, uint32_t tmem_
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
       "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_lin(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int z) {
+  tma_load_3d_pair(dst, map, bar_cluster, 0, 0, z);
 }
 
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster,
@@ -283,6 +299,8 @@ struct TcParams {
   int tiles;        // key tiles of the buffer
   KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
   RowUnit* row_units;  // [B][units]
+  int* lin_ok;       // [Hkv]: the head group's slopes fit the operand type
+  uint16_t* lin_q;   // [Hkv][kLinBytes / 2]: the rows' slopes, in three parts
   float cap_small, cap_mid;       // scores up to which the polynomials hold
   float2 cap_c3[3], cap_c7[7];    // their coefficients, each twice
   int* queue;       // next piece, pairs done (zero between launches)
@@ -318,7 +336,8 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 // {sequence * Hkv + kv head, unit, share (7 bits) and above it the number of
-// key tiles from w on that every row sees whole, w}, x = -1 past the end; and
+// key tiles from w on that every row sees whole, w (LIN: whether the tensor
+// cores may add the bias)}, x = -1 past the end; and
 // {k_len, q_len, first key tile, key tiles}.
 struct Piece {
   int4 a, b;
@@ -378,6 +397,16 @@ __device__ __forceinline__ void seen_tiles(const TcParams& p, int b, int kvh, in
   count = max(w1 - whole, 0);
 }
 
+// LIN: 1 if every row of the piece's unit lies at or behind all keys of the
+// tile, -1 if at or before them, 0 otherwise (or if the slopes do not fit).
+__device__ __forceinline__ int tile_side(const TcParams& p, const Piece& pc, int tile) {
+  if (!pc.a.w) return 0;
+  const int unit = 2 * p.tok_cta, first = pc.b.x - pc.b.y + pc.a.y * unit;
+  const int last = pc.b.x - pc.b.y + min(pc.b.y, (pc.a.y + 1) * unit) - 1;
+  if (first >= tile * KT + KT - 1) return 1;
+  return last <= tile * KT ? -1 : 0;
+}
+
 // Whether a key tile ends behind the keys inside the buffer (rows behind the
 // buffer are zero-filled by the tensor map).
 __device__ __forceinline__ bool zero_tile(const TcParams& p, int key0, int k_len) {
@@ -407,12 +436,22 @@ __device__ __forceinline__ void cap2(float& x0, float& x1, const float2* c) {
 // as bits, so that a kernel holds the registers of its own work only: the score
 // cap, the distance bias, documents and explicit positions.
 enum : int { F_CAP = 1, F_BIAS = 2, F_META = 4 };
+//
+// With the bias alone (LIN) the tensor cores add it, as its multiply-adds per
+// score would lengthen the softmax, which paces the kernel: where all rows of a
+// unit lie behind (before) a tile's keys, key c of the tile gets
+// -slope (d0 -+ c) = -+slope d0 +- slope c; the row's slope / scale, in three
+// parts of the operand type (24 bits), times c (0..255, exact) is one more
+// step of 16 products, and -+slope d0 is the same for the whole row.  Only the
+// tiles that a unit's rows lie in are done key by key.
 template <int DH, bool BF16, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
-  using C = Cfg<DH>;
-  constexpr int KS = kStages;
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmL,
+                      const __grid_constant__ TcParams p) {
+  constexpr bool LIN = F == F_BIAS;
+  using C = Cfg<DH, LIN>;
+  constexpr int KS = kStages, KK = C::KK;
   extern __shared__ uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the same in both CTAs: swizzled tiles need it
     if (threadIdx.x == 0) raise_error(p.c.err, ERR_BOUNDS);
@@ -457,6 +496,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
+  }
+  if constexpr (LIN) {
+    // Key c of a tile: c, c, c, 0, ..; and the same negative.
+    for (int i = threadIdx.x; i < 256; i += kThreads) {
+      const int n = i & 127;
+      const float c = static_cast<float>(rank * 128 + n) * (i < 128 ? 1.0f : -1.0f);
+      uint4* dst = reinterpret_cast<uint4*>(smem + C::OFF_LIN + (1 + i / 128) * kLinBytes + (n / 8) * 256 + (n % 8) * 16);
+      dst[0] = make_uint4(pack2<BF16>(c, c), pack2<BF16>(c, 0.0f), 0, 0);
+      dst[8] = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
   tc_fence_before();
@@ -503,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t1 = static_cast<int>(nt * static_cast<uint32_t>(pc.a.z + 1) / n);
           pc.b = make_int4(nk, nq, first + t0, t1 - t0);
           pc.a.z |= count << 7;
-          pc.a.w = whole;
+          pc.a.w = LIN ? p.lin_ok[pc.a.x % p.c.Hkv] : whole;
         }
         int next = 0;
         if (lane == 0) {
@@ -537,15 +587,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int b = pc.a.x / p.c.Hkv, hk = pc.a.x % p.c.Hkv;
           if (gq > 0 && !mbar_wait(q_empty, (gq - 1) & 1, err, ERR_ATTN_TIMEOUT)) break;
           ++gq;
-          if (leader) mbar_arrive_expect_tx(q_full, 2 * p.rows_cta * DH * 2);
+          if (leader) mbar_arrive_expect_tx(q_full, 2 * (p.rows_cta * DH * 2 + (LIN ? kLinBytes : 0)));
+          if constexpr (LIN) tma_load_3d_lin(smem + C::OFF_LIN, &tmL, q_full0, hk);
 #pragma unroll
           for (int a = 0; a < C::NA; ++a)
             tma_load_4d_pair(sQ + a * C::ATOM, &tmQ, q_full0, a * 64, hk * p.c.G,
                              (pc.a.y * 2 + rank) * p.tok_cta, b);
           bool ok = true;
           for (int j = 0; j < nT; ++j, ++gk) {
-            const int st = gk % KS;
-            if (!mbar_wait(&k_empty[st], ((gk / KS) & 1) ^ 1, err, ERR_ATTN_TIMEOUT)) {
+            const int st = gk % KK;
+            if (!mbar_wait(&k_empty[st], ((gk / KK) & 1) ^ 1, err, ERR_ATTN_TIMEOUT)) {
               ok = false;
               break;
             }
@@ -561,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // No copy into or read of this CTA's shared memory may be left when it
         // exits: wait (bounded) until the MMAs released the last stages.
         const uint64_t t0 = global_timer_ns();
-        for (int j = (gk > KS ? gk - KS : 0); j < gk; ++j) {
-          while (!mbar_try_wait(&k_empty[j % KS], (j / KS) & 1) &&
+        for (int j = (gk > KK ? gk - KK : 0); j < gk; ++j) {
+          while (!mbar_try_wait(&k_empty[j % KK], (j / KK) & 1) &&
                  global_timer_ns() - t0 < kWaitLimitNs) {
           }
         }
@@ -609,15 +660,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = umma_desc_kmajor(smem_u32(sQ), 128);
       const uint64_t dk = umma_desc_kmajor(smem_u32(sK), 128);
       const uint64_t dv = desc_mn(smem_u32(sV), C::V_ROW);
-      auto issue_s = [&](int t) {
-        const uint64_t b = dk + static_cast<uint64_t>(((t % KS) * C::K_BYTES) >> 4);
+      const uint64_t dlq = desc_lin(smem_u32(smem + C::OFF_LIN));
+      auto issue_s = [&](int t, int side) {
+        const uint64_t b = dk + static_cast<uint64_t>(((t % KK) * C::K_BYTES) >> 4);
 #pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk) {
           const uint32_t o = ((kk / 4) * C::ATOM + (kk % 4) * 32) >> 4;
           umma_bf16_pair(tmem + COL_S, dq + o, b + o, IDESC_S, kk != 0);
         }
+        if constexpr (LIN) {
+          if (side != 0) umma_bf16_pair(tmem + COL_S, dlq, dlq + ((side > 0 ? 1 : 2) * kLinBytes >> 4), IDESC_S, 1);
+        }
         umma_commit_pair_mc(s_full, 0x3);
-        umma_commit_pair_mc(&k_empty[t % KS], 0x3);
+        umma_commit_pair_mc(&k_empty[t % KK], 0x3);
       };
       int g = 0, gq = 0;
       bool ok = true;
@@ -627,23 +682,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_remote(pc_empty0 + (i & 1) * 8);  // this CTA's own slot: CTA scope
         if (nT == 0) continue;
         if (!mbar_wait(q_full, gq & 1, err, ERR_ATTN_TIMEOUT) ||
-            !mbar_wait(&k_full[g % KS], (g / KS) & 1, err, ERR_ATTN_TIMEOUT) ||
+            !mbar_wait(&k_full[g % KK], (g / KK) & 1, err, ERR_ATTN_TIMEOUT) ||
             (g > 0 && !mbar_wait(s_free, (g - 1) & 1, err, ERR_ATTN_TIMEOUT)))
           break;
         ++gq;
         tc_fence_after();
-        issue_s(g);
+        issue_s(g, LIN ? tile_side(p, pc, pc.b.z) : 0);
         if (nT == 1) umma_commit_pair_mc(q_empty, 0x3);
         for (int j = 0; j < nT; ++j) {
           const int t = g + j;
           if (j + 1 < nT) {
             if (!mbar_wait(s_free, t & 1, err, ERR_ATTN_TIMEOUT) ||
-                !mbar_wait(&k_full[(t + 1) % KS], ((t + 1) / KS) & 1, err, ERR_ATTN_TIMEOUT)) {
+                !mbar_wait(&k_full[(t + 1) % KK], ((t + 1) / KK) & 1, err, ERR_ATTN_TIMEOUT)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            issue_s(t + 1);
+            issue_s(t + 1, LIN ? tile_side(p, pc, pc.b.z + j + 1) : 0);
             if (j + 2 == nT) umma_commit_pair_mc(q_empty, 0x3);
           }
           // In a piece's last tile the acquire at cluster scope pairs with the
@@ -847,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(s_free0);
-        float sl2 = scale2;
+        float sl2 = scale2, off = 0.0f;  // score = s * sl2 + off (log2)
         if constexpr ((F & F_CAP) != 0) {
           {
             const float inv = p.c.scale / p.c.softcap, c2 = p.c.softcap * kLog2e;
@@ -875,8 +930,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             sl2 = 1.0f;
           }
         }
+        const int side = LIN ? tile_side(p, Piece{pa, pb}, pb.z + j) : 0;
+        if constexpr (LIN) {
+          if (side != 0) off = (side > 0 ? -slope2 : slope2) * static_cast<float>(qp - (pb.z + j) * KT);
+        }
         if constexpr ((F & F_BIAS) != 0) {
-          {
+          if (side == 0) {
             const float d = static_cast<float>(d0);
             if (run && __all_sync(0xffffffffu, d0 >= 127 || d0 <= 0)) {
               // The row lies on one side of all its keys: the bias is linear in c.
@@ -924,13 +983,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(mx8[e], s[120 + e]);
         const float mx = fmaxf(max3(mx8[0], mx8[1], mx8[2]),
                                fmaxf(max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float m_tile = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * sl2;
+        const float m_tile = fmaf(fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)), sl2, off);
         const bool grow = m_tile > m + kRescaleThreshold;
         const bool any_grow = __any_sync(0xffffffffu, grow);
         const float m_new = grow ? m_tile : m;
         const float alpha = grow ? fast_exp2(m - m_new) : 1.0f;
         // A row that has seen no key keeps m = -inf; its weights are exp2(-inf).
-        const float negm = m_new == -INFINITY ? 0.0f : -m_new;
+        const float negm = m_new == -INFINITY ? 0.0f : off - m_new;
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         auto exp_chunk = [&](int c, uint32_t* pk) {
 #pragma unroll
@@ -1058,8 +1117,9 @@ cudaError_t launch_one(const CUtensorMap* maps, const TcParams& p, int pairs, cu
   static uint64_t set_up = 0;
   // More than half an SM's shared memory: one CTA per SM, so its 512 TMEM
   // columns are free.
-  const size_t smem = Cfg<DH>::SMEM > 120 * 1024 ? Cfg<DH>::SMEM : 120 * 1024;
-  static_assert(Cfg<DH>::SMEM <= 232448, "over the per-block limit");
+  using C = Cfg<DH, F == F_BIAS>;
+  const size_t smem = C::SMEM > 120 * 1024 ? C::SMEM : 120 * 1024;
+  static_assert(C::SMEM <= 232448, "over the per-block limit");
   cudaError_t e = once_per_device(&set_up, [&](int) {
     // The register split must fit the launch allocation, else the growing
     // warpgroups would wait for registers forever.
@@ -1086,7 +1146,7 @@ cudaError_t launch_one(const CUtensorMap* maps, const TcParams& p, int pairs, cu
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, cache_attn_kernel<DH, BF16, F>, maps[0], maps[1], maps[2], p);
+  return cudaLaunchKernelEx(&cfg, cache_attn_kernel<DH, BF16, F>, maps[0], maps[1], maps[2], maps[3], p);
 }
 
 template <int DH, bool BF16>

@@ -174,7 +174,9 @@ def make(dtype="bf16", B=1, Lq=1, Lk=1, Hq=1, Hkv=1, dh=64, seed=0, causal=False
 
     c = dict(dtype=dtype, B=B, Lq=Lq, Lk=Lk, Hq=Hq, Hkv=Hkv, dh=dh, causal=causal, cap=cap, scale=scale,
              q=rnd(B, Lq, Hq, dh, s=q_scale), k=rnd(B, Lk, Hkv, dh), v=rnd(B, Lk, Hkv, dh))
-    c["slopes"] = (2.0 ** (-8.0 * torch.arange(1, Hq + 1, device="cuda") / Hq)).float() if slopes else None
+    if slopes is True:
+        slopes = 2.0 ** (-8.0 * np.arange(1, Hq + 1) / Hq)
+    c["slopes"] = torch.tensor(slopes, dtype=torch.float32, device="cuda") if slopes is not False else None
     for name, value in dict(prefix=prefix, q_lens=q_lens, k_lens=k_lens, q_pos=q_pos, q_doc=q_doc).items():
         c[name] = ints(value)
     # [B][Lk] metadata is shared by the heads, [B][Hkv][Lk] is not
@@ -315,6 +317,11 @@ ATTN = {
     "large-scores": dict(Lq=60, Lk=900, Hq=2, Hkv=2, dh=64, q_scale=100.0),
     "bias": dict(B=2, Lq=300, Lk=900, Hq=4, Hkv=2, dh=128, slopes=True, k_lens=[900, 400]),
     "bias-causal-cap": dict(B=1, Lq=300, Lk=900, Hq=4, Hkv=4, dh=128, slopes=True, causal=True, cap=50.0, dtype="f16"),
+    "bias-both-sides": dict(B=2, Lq=1100, Lk=1300, Hq=2, Hkv=2, dh=128, slopes=True, k_lens=[1300, 1111]),
+    "bias-both-sides-f16": dict(Lq=900, Lk=900, Hq=6, Hkv=2, dh=64, slopes=True, dtype="f16"),
+    "bias-steep": dict(Lq=600, Lk=800, Hq=4, Hkv=4, dh=64, slopes=[3.0, 1e5, 0.0, 1e-4], dtype="f16"),
+    "bias-signs": dict(Lq=600, Lk=800, Hq=4, Hkv=2, dh=64, slopes=[0.01, -0.01, 1e-7, 0.3], causal=True),
+    "bias-rows": dict(Lq=1, Lk=800, Hq=4, Hkv=4, dh=64, slopes=[0.01, -0.01, 0.0, 1e4]),
     "lens": dict(B=5, Lq=200, Lk=700, Hq=2, Hkv=1, dh=64, k_lens=[0, 1, 256, 699, 5000], q_lens=[200, 1, 0, 129, 4000]),
     "lens-causal": dict(B=5, Lq=200, Lk=700, Hq=2, Hkv=1, dh=64, k_lens=[0, 1, 256, 700, -3], q_lens=[200, 100, 199, 129, 7],
                         causal=True, slopes=True),
