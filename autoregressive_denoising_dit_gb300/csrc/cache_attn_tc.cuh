@@ -82,10 +82,11 @@ struct Cfg {
   static constexpr int OC = 32;                 // O columns per TMEM access
 };
 
+// By the whole warp: every lane polls (one access for all of them); a branch to
+// one lane and a shuffle of its answer cost more than twice as much, and these
+// waits are on the kernels' critical path even where they find the barrier done.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
-  int ok = 0;
-  if (lane_id() == 0) ok = mbar_wait(bar, parity, err, ERR_ATTN_TIMEOUT) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, ERR_ATTN_TIMEOUT));
 }
 
 // Instruction descriptor: f32 accumulate, A and B of the operand type, A
@@ -299,8 +300,10 @@ struct TcParams {
   int tiles;        // key tiles of the buffer
   KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
   RowUnit* row_units;  // [B][units]
-  int* lin_ok;       // [Hkv]: the head group's slopes fit the operand type
-  uint16_t* lin_q;   // [Hkv][kLinBytes / 2]: the rows' slopes, in three parts
+  // [Hkv]: whether a head group's slopes fit the operand type, and the rows'
+  // slopes in three parts (kLinBytes); the mass: the same of -lse by half units.
+  int* lin_ok;
+  uint16_t* lin_q;
   float cap_small, cap_mid;       // scores up to which the polynomials hold
   float2 cap_c3[3], cap_c7[7];    // their coefficients, each twice
   int* queue;       // next piece, pairs done (zero between launches)
@@ -1167,6 +1170,12 @@ cudaError_t launch_features(const CUtensorMap* maps, const TcParams& p, int f, i
 // `values`, v), and the kernel that fills key_tiles and row_units where there
 // are positions or documents.
 TcParams plan(const CacheParams& c, char* scratch);
+// The mass's noted -lse in the workspace: a block per half unit (0: not used).
+struct MassLin {
+  int64_t blocks;
+  size_t ok, q;
+};
+MassLin mass_lin(const CacheParams& c, bool bf16);
 bool encode_maps(CUtensorMap* maps, const CacheParams& c, const TcParams& p, bool bf16, bool values);
 cudaError_t launch_tiles(const TcParams& p, cudaStream_t st);
 
