@@ -168,7 +168,7 @@ struct TcLayout {
   int64_t pieces;
   int tiles, meta_heads;  // of the buffer; 0: no positions or documents
   bool lin;  // the distance bias by products (no cap, no positions or documents given)
-  size_t part_o, part_ml, key_tiles, row_units, lin_ok, lin_q, mass_lin, total;
+  size_t part_o, part_ml, key_tiles, row_units, lin_ok, lin_q, total;
 };
 
 TcLayout tc_layout(const CacheParams& c) {
@@ -212,12 +212,6 @@ TcLayout tc_layout(const CacheParams& c) {
     off += up256(sizeof(int) * static_cast<size_t>(c.Hkv));
     t.lin_q = off;
     off += static_cast<size_t>(c.Hkv) * kLinBytes;
-  }
-  // The mass's part (32 bytes a row).
-  t.mass_lin = off;
-  if (!t.few && !(c.softcap > 0) && !c.slopes) {
-    const size_t blocks = static_cast<size_t>(c.B) * c.Hkv * t.units * 2;
-    off += up256(sizeof(int) * blocks) + blocks * kLinBytes;
   }
   t.total = off;
   return t;
@@ -301,17 +295,6 @@ cudaError_t launch_join(const TcParams& p, bool bf16, cudaStream_t st) {
 }
 
 }  // namespace
-
-MassLin cattn::mass_lin(const CacheParams& c, bool bf16) {
-  const TcLayout t = tc_layout(c);
-  MassLin m{};
-  // (f16's largest value must still make a weight of 0.)
-  if (t.few || c.softcap > 0 || c.slopes || (!bf16 && c.scale < 2e-3f)) return m;
-  m.blocks = static_cast<int64_t>(c.B) * c.Hkv * t.units * 2;
-  m.ok = t.mass_lin;
-  m.q = m.ok + up256(sizeof(int) * static_cast<size_t>(m.blocks));
-  return m;
-}
 
 TcParams cattn::plan(const CacheParams& c, char* scratch) {
   const TcLayout t = tc_layout(c);

@@ -301,7 +301,7 @@ struct TcParams {
   KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
   RowUnit* row_units;  // [B][units]
   // [Hkv]: whether a head group's slopes fit the operand type, and the rows'
-  // slopes in three parts (kLinBytes); the mass: the same of -lse by half units.
+  // slopes in three parts (kLinBytes).
   int* lin_ok;
   uint16_t* lin_q;
   float cap_small, cap_mid;       // scores up to which the polynomials hold
@@ -842,9 +842,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (A stretch of tiles is known to be seen whole; only the distance bias
         // then needs the tile's notes.)
         const bool whole = static_cast<uint32_t>(pb.z + j - pa.w) < static_cast<uint32_t>(pa.z >> 7);
+        if ((F & F_META) && p.key_tiles && active && j + 1 < nT) {
+          const bool next_whole = static_cast<uint32_t>(pb.z + j + 1 - pa.w) < static_cast<uint32_t>(pa.z >> 7);
+          if ((F & F_BIAS) || !next_whole) fetch_meta(pb.z + j + 1);
+        }
         if ((F & F_META) && p.key_tiles && active && ((F & F_BIAS) || !whole)) {
           const KeyTile kt = tiles[pb.z + j];
-          if (j + 1 < nT) fetch_meta(pb.z + j + 1);
           run = kt.run;
           if (p.c.k_pos) d0 = qp - kt.base - hk16 * 128;
           const bool doc_all = !p.c.k_doc || (kt.doc_min == qd && kt.doc_max == qd);
@@ -1170,12 +1173,6 @@ cudaError_t launch_features(const CUtensorMap* maps, const TcParams& p, int f, i
 // `values`, v), and the kernel that fills key_tiles and row_units where there
 // are positions or documents.
 TcParams plan(const CacheParams& c, char* scratch);
-// The mass's noted -lse in the workspace: a block per half unit (0: not used).
-struct MassLin {
-  int64_t blocks;
-  size_t ok, q;
-};
-MassLin mass_lin(const CacheParams& c, bool bf16);
 bool encode_maps(CUtensorMap* maps, const CacheParams& c, const TcParams& p, bool bf16, bool values);
 cudaError_t launch_tiles(const TcParams& p, cudaStream_t st);
 

@@ -7,12 +7,8 @@
 // a tile of 256 keys (128 per CTA) of one (sequence, kv head), which stays in
 // shared memory while the row tiles (256 rows: each CTA holds 128) stream past.
 //   S^T_t = K Q_t^T   M=256, N=256, K=dh, double-buffered in TMEM
-// Without a cap or a bias the tensor cores subtract lse too: a row's -lse /
-// scale, in three parts of the operand type (24 bits) noted by cache_lse_kernel,
-// times one is a further step of 16 products.  Per score one multiplication
-// (scale), one exp2 and one add are left: the MMAs (9 x 136 clocks a tile) and
-// the exponentials (1024) bound it about equally.  Reading -lse per column from
-// shared memory instead took as long as the exponentials again.
+// Per score one multiply-add (scale and -lse), one exp2 and one add: the MMAs
+// (8 x 136 clocks a tile) and the exponentials (1024) bound it about equally.
 // A row's -lse, position limit, document and slope are noted per tile in shared
 // memory by a warp of their own.  Warp roles, 384 threads:
 //   warp 0       TMA: the piece's K tile (2 buffers), the row tiles (4 stages)
@@ -29,7 +25,7 @@ using namespace cattn;
 
 namespace {
 
-constexpr int QS = 3;          // row-tile stages
+constexpr int QS = 4;          // row-tile stages
 constexpr int kMassThreads = 640, kWeightWarps = 16;
 constexpr int kHalf = 132;     // words between the halves of a column array: other banks
 constexpr int kColWords = 2 * kHalf;
@@ -44,9 +40,8 @@ struct MCfg {
   static constexpr int ATOM = 128 * 128;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = OFF_K + 2 * TILE;
-  static constexpr int OFF_LIN = OFF_Q + QS * TILE;  // the keys' ones, then the rows' -lse by stage
-  static constexpr int OFF_COL = OFF_LIN + (1 + QS) * kLinBytes;
-  static constexpr int COL_BYTES = COL_ARRAYS * kColWords * 4 + 32;  // and {limit min, doc min, doc max, lse added by half}
+  static constexpr int OFF_COL = OFF_Q + QS * TILE;
+  static constexpr int COL_BYTES = COL_ARRAYS * kColWords * 4 + 16;  // and {limit min, doc min, doc max, 0}
   static constexpr int OFF_BAR = OFF_COL + QS * ((COL_BYTES + 127) / 128 * 128);
   static constexpr int COL_STRIDE = (COL_BYTES + 127) / 128 * 128;
   static constexpr int N_BARS = 12 + 4 * QS;
@@ -63,50 +58,28 @@ __device__ __forceinline__ void ffma2v(float& x0, float& x1, float s, float b0, 
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
 }
 
-__device__ __forceinline__ void fmul2(float& x0, float& x1, float s) {
-  uint64_t x, sv;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(sv) : "f"(s));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(sv));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
-}
-
-// -lse / scale of 128 rows (a CTA's half of a unit) in three parts of the
-// operand type, in the layout of kLinBytes; a row that is not used or saw
-// nothing gets a value whose weights are 0.  lin_ok: whether they fit the type.
-template <bool BF16>
-__global__ void __launch_bounds__(128) cache_lse_kernel(const __grid_constant__ TcParams p) {
+// mass_out = mass_in (or 0) for the keys in use.
+__global__ void __launch_bounds__(256) mass_copy_kernel(const __grid_constant__ TcParams p) {
   pdl_trigger();
-  const int r = threadIdx.x, block = blockIdx.x, cta = block & 1, unit = (block >> 1) % p.units;
-  const int bh = (block >> 1) / p.units, b = bh / p.c.Hkv, kvh = bh % p.c.Hkv;
-  const int tok = (unit * 2 + cta) * p.tok_cta + r / p.c.G, head = kvh * p.c.G + r % p.c.G;
+  const uint32_t per = (p.c.Lk + 1023) / 1024, bh = blockIdx.x / per;
+  const int j = static_cast<int>(blockIdx.x - bh * per) * 1024 + threadIdx.x;
+  const int64_t row = static_cast<int64_t>(bh) * p.c.Lk;
   pdl_wait();
-  float lse = -INFINITY;
-  if (r < p.rows_cta && tok < cache_q_len(p.c, b)) lse = p.c.lse[(static_cast<int64_t>(b) * p.c.Hq + head) * p.c.Lq + tok];
-  constexpr float kMost = BF16 ? 1e30f : 6e4f;
-  const bool none = lse == -INFINITY;
-  const float v = -lse / p.c.scale;
-  const int ok = __syncthreads_and(none || fabsf(v) <= kMost);
-  auto part = [](float x) {
-    if constexpr (BF16) return __bfloat162float(__float2bfloat16_rn(x));
-    else return __half2float(__float2half_rn(x));
-  };
-  float hi = part(v), mid = part(v - hi), lo = v - hi - mid;
-  if (none) hi = mid = lo = -kMost;
-  uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.lin_q) + static_cast<int64_t>(block) * kLinBytes +
-                                        (r / 8) * 256 + (r % 8) * 16);
-  dst[0] = ok ? make_uint4(pack2<BF16>(hi, mid), pack2<BF16>(lo, 0.0f), 0, 0) : make_uint4(0, 0, 0, 0);
-  dst[8] = make_uint4(0, 0, 0, 0);
-  if (r == 0) p.lin_ok[block] = ok;
+  const int n = cache_k_len(p.c, bh / p.c.Hkv);
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = p.c.mass_in && j + 256 * i < n ? p.c.mass_in[row + j + 256 * i] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j + 256 * i < n) p.c.mass_out[row + j + 256 * i] = x[i];
 }
 
 // F: F_CAP, F_BIAS (kernels of their own keep the loop within the instruction cache).
 template <int DH, bool BF16, int F>
 __global__ void __launch_bounds__(kMassThreads, 1)
     cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmL, const __grid_constant__ TcParams p) {
+                      const __grid_constant__ TcParams p) {
   using C = MCfg<DH>;
-  constexpr bool LIN = F == 0;
   extern __shared__ uint8_t smem[];
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) raise_error(p.c.err, ERR_BOUNDS);
@@ -152,14 +125,6 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     for (int a = 0; a < QS * C::NA; ++a) {
       uint4* z = reinterpret_cast<uint4*>(sQ + a * C::ATOM + p.rows_cta * 128);
       for (int e = threadIdx.x; e < (128 - p.rows_cta) * 8; e += kMassThreads) z[e] = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-  }
-  if constexpr (LIN) {
-    if (threadIdx.x < 128) {  // 1, 1, 1, 0, .. for every key
-      uint4* dst = reinterpret_cast<uint4*>(smem + C::OFF_LIN + (threadIdx.x / 8) * 256 + (threadIdx.x % 8) * 16);
-      dst[0] = make_uint4(pack2<BF16>(1.0f, 1.0f), pack2<BF16>(1.0f, 0.0f), 0, 0);
-      dst[8] = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
   }
@@ -265,10 +230,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(&q_full[st], 2 * (p.rows_cta * DH * 2 + (LIN && p.lin_q ? kLinBytes : 0)));
-          if (LIN && p.lin_q)
-            tma_load_3d_lin(smem + C::OFF_LIN + (1 + st) * kLinBytes, &tmL, q_full0 + st * 8,
-                            (pc.a.x * p.units + pc.a.z + j) * 2 + rank);
+          if (leader) mbar_arrive_expect_tx(&q_full[st], 2 * p.rows_cta * DH * 2);
 #pragma unroll
           for (int a = 0; a < C::NA; ++a)
             tma_load_4d_pair(sQ + st * C::TILE + a * C::ATOM, &tmQ, q_full0 + st * 8, a * 64, kvh * p.c.G,
@@ -294,7 +256,6 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       constexpr uint32_t IDESC = idesc_of<BF16>(256, 256, false);
       const uint64_t dk = umma_desc_kmajor(smem_u32(sK), 128);
       const uint64_t dq = umma_desc_kmajor(smem_u32(sQ), 128);
-      const uint64_t dl = desc_lin(smem_u32(smem + C::OFF_LIN));
       int gk = 0, g = 0;
       bool ok = true;
       Piece pc;
@@ -319,7 +280,6 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             const uint32_t o = ((kk / 4) * C::ATOM + (kk % 4) * 32) >> 4;
             umma_bf16_pair(tmem + sb * 256, a + o, b + o, IDESC, kk != 0);
           }
-          if (LIN && p.lin_q) umma_bf16_pair(tmem + sb * 256, dl, dl + (((1 + st) * kLinBytes) >> 4), IDESC, 1);
           umma_commit_pair_mc(&s_full[sb], 0x3);
           umma_commit_pair_mc(&q_empty[st], 0x3);
         }
@@ -350,27 +310,16 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const int prefix = p.c.prefix ? p.c.prefix[b] : 0;
       const float* lse = p.c.lse + (static_cast<int64_t>(b) * p.c.Hq + kvh * p.c.G) * p.c.Lq;
       bool ok = true;
-      // What a tile needs from memory is read one tile ahead.
-      float nl_next[8];
-      int added_next = 0;  // lane 0, 1: of the halves
-      auto fetch = [&](int j) {
-        const int tok0 = (pc.a.z + j) * 2 * p.tok_cta;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int tok = tok0 + (x >> 2) * p.tok_cta + dtok[x & 3];
-          nl_next[x] = tok < nq ? __ldg(lse + static_cast<int64_t>(dhead[x & 3]) * p.c.Lq + tok) : -INFINITY;
-        }
-        if (LIN && p.lin_q && lane < 2) added_next = __ldg(p.lin_ok + (pc.a.x * p.units + pc.a.z + j) * 2 + lane);
-      };
-      if (pc.a.w > 0) fetch(0);
       for (int j = 0; j < pc.a.w; ++j, ++g) {
         const int st = g % QS;
+        // The reads of lse are on their way while the stage is waited for.
         const int tok0 = (pc.a.z + j) * 2 * p.tok_cta;
         float nl[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) nl[x] = nl_next[x];
-        const int added = added_next;
-        if (j + 1 < pc.a.w) fetch(j + 1);
+        for (int x = 0; x < 8; ++x) {
+          const int tok = tok0 + (x >> 2) * p.tok_cta + dtok[x & 3];
+          nl[x] = tok < nq ? __ldg(lse + static_cast<int64_t>(dhead[x & 3]) * p.c.Lq + tok) : -INFINITY;
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(&c_empty[st], ((g / QS) & 1) ^ 1, err, ERR_ATTN_TIMEOUT))) {
           ok = false;
           break;
@@ -416,7 +365,6 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           int* stat = icol + COL_ARRAYS * kColWords;
           stat[0] = pl_min, stat[1] = d_min, stat[2] = d_max;
         }
-        if (LIN && lane < 2) icol[COL_ARRAYS * kColWords + 3 + lane] = added;
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa_shared(&c_full[st], rank));
         __syncwarp();
@@ -459,8 +407,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const int kp = p.c.k_pos ? p.c.k_pos[meta + kc] : key;
       const int kd = p.c.k_doc ? p.c.k_doc[meta + kc] : 0;
       const int64_t at = static_cast<int64_t>(pa.x) * p.c.Lk + key;
-      float old = 0.0f;
-      if (valid && half == 0 && quarter == 0 && p.c.mass_in) old = p.c.mass_in[at];
+      const bool writes = valid && half == 0 && quarter == 0;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool ok = true;
       if (nT == 0 && warp == 4 && lane == 0) fetch_piece(i + 1);
@@ -468,19 +415,20 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         const int st = g % QS, sb = g & 1;
         if (j + 1 == nT && warp == 4 && lane == 0) fetch_piece(i + 1);
         __syncwarp();
-        if (ok) ok = warp_wait(&c_full[st], (g / QS) & 1, err);
         if (ok) ok = warp_wait(&s_full[sb], (g >> 1) & 1, err);
         if (!ok) continue;
         tc_fence_after();
-        __syncwarp();
-        const float* col = reinterpret_cast<const float*>(smem + C::OFF_COL + st * C::COL_STRIDE);
-        const int* stat = reinterpret_cast<const int*>(col) + COL_ARRAYS * kColWords;
-        const bool whole = kp < stat[0] && (!p.c.k_doc || (stat[1] == kd && stat[2] == kd));
-        const bool masked = __any_sync(0xffffffffu, valid && !whole);
-        const bool unused = stat[0] == -0x7fffffff - 1;
-        const bool added = LIN && stat[3 + half];  // the products hold -lse already
-        const bool all_added = __all_sync(0xffffffffu, added);
         const uint32_t s_addr = tmem + sb * 256 + lane_off;
+        float s[32];
+        tmem_ld32x<128>(s_addr + 64 * quarter, s);
+        ok = warp_wait(&c_full[st], (g / QS) & 1, err);
+        tmem_wait_ld();
+        if (!ok) continue;
+        const float* col = reinterpret_cast<const float*>(smem + C::OFF_COL + st * C::COL_STRIDE);
+        const int4 stat = *reinterpret_cast<const int4*>(col + COL_ARRAYS * kColWords);
+        const bool whole = kp < stat.x && (!p.c.k_doc || (stat.y == kd && stat.z == kd));
+        const bool masked = __any_sync(0xffffffffu, valid && !whole);
+        const bool unused = stat.x == -0x7fffffff - 1;
         // 32 columns at a time.
         auto add_chunk = [&](float* v, int ch) {
           const float* cc = col + half * kHalf + ch * 32;
@@ -525,37 +473,30 @@ __global__ void __launch_bounds__(kMassThreads, 1)
               if (kp >= pl.w || qd.w != kd) v[e + 3] = -INFINITY;
             }
           }
-          if (LIN && all_added) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              fmul2(v[e], v[e + 1], sc);
-              fadd2(acc[e & 6], acc[(e & 6) + 1], fast_exp2(v[e]), fast_exp2(v[e + 1]));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float4 nl = *reinterpret_cast<const float4*>(cc + COL_NLSE * kColWords + e);
-              if (LIN && added) nl = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              ffma2v(v[e], v[e + 1], sc, nl.x, nl.y);
-              ffma2v(v[e + 2], v[e + 3], sc, nl.z, nl.w);
-              fadd2(acc[(e & 4)], acc[(e & 4) + 1], fast_exp2(v[e]), fast_exp2(v[e + 1]));
-              fadd2(acc[(e & 4) + 2], acc[(e & 4) + 3], fast_exp2(v[e + 2]), fast_exp2(v[e + 3]));
-            }
+          for (int e = 0; e < 32; e += 4) {
+            const float4 nl = *reinterpret_cast<const float4*>(cc + COL_NLSE * kColWords + e);
+            ffma2v(v[e], v[e + 1], sc, nl.x, nl.y);
+            ffma2v(v[e + 2], v[e + 3], sc, nl.z, nl.w);
+            fadd2(acc[(e & 4)], acc[(e & 4) + 1], fast_exp2(v[e]), fast_exp2(v[e + 1]));
+            fadd2(acc[(e & 4) + 2], acc[(e & 4) + 3], fast_exp2(v[e + 2]), fast_exp2(v[e + 3]));
           }
         };
-        float s[32];
 #pragma unroll 1
-        for (int ch = 2 * quarter; ch < 2 * quarter + 2; ++ch) {
-          tmem_ld32x<128>(s_addr + ch * 32, s);
-          tmem_wait_ld();
+        for (int ch = 2 * quarter;; ++ch) {
           add_chunk(s, ch);
+          if (ch & 1) break;
+          tmem_ld32x<128>(s_addr + (ch + 1) * 32, s);
+          tmem_wait_ld();
+          // S^T is read: the next but one tile's products wait for it, so it is
+          // given back before the second half of the weights is computed.
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(s_free0 + sb * 8);
+          __syncwarp();
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_remote(s_free0 + sb * 8);
-          mbar_arrive_remote(mapa_shared(&c_empty[st], rank));
-        }
+        if (lane == 0) mbar_arrive_remote(mapa_shared(&c_empty[st], rank));
         __syncwarp();
       }
       float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
@@ -567,7 +508,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       // (Copies of pieces and sums are rewritten two pieces later, behind a barrier
       // that their readers have reached.)
       asm volatile("bar.sync 1, 512;" ::: "memory");
-      if (ok && quarter == 0 && valid && half == 0) p.c.mass_out[at] = old + (sum + other[r]);
+      // mass_out holds the old mass: one addition to each entry, whose order does
+      // not matter, and which needs no answer.
+      if (ok && writes) atomicAdd(p.c.mass_out + at, sum + other[r]);
       __syncwarp();
     }
   }
@@ -614,7 +557,7 @@ cudaError_t launch(const CUtensorMap* maps, const TcParams& p, int pairs, cudaSt
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, cache_mass_kernel<DH, BF16, F>, maps[0], maps[1], maps[2], p);
+  return cudaLaunchKernelEx(&cfg, cache_mass_kernel<DH, BF16, F>, maps[0], maps[1], p);
 }
 
 template <int DH, bool BF16>
@@ -641,28 +584,19 @@ cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, char* scratch,
   p.n_pieces = c.B * c.Hkv * p.tiles;
   CUtensorMap maps[3];
   if (!encode_maps(maps, c, p, bf16, false)) return cudaErrorInvalidValue;
-  maps[2] = maps[0];
   cudaError_t e = launch_tiles(p, st);
   if (e != cudaSuccess) return e;
-  p.lin_ok = nullptr;
-  p.lin_q = nullptr;
-  if (const MassLin lin = mass_lin(c, bf16); lin.blocks) {
-    p.lin_ok = reinterpret_cast<int*>(scratch + lin.ok);
-    p.lin_q = reinterpret_cast<uint16_t*>(scratch + lin.q);
-    const uint64_t dims[3] = {64, kLinBytes / 128, static_cast<uint64_t>(lin.blocks)}, str[2] = {128, kLinBytes};
-    const uint32_t box[3] = {64, kLinBytes / 128, 1};
-    if (!encode_16bit_map(&maps[2], bf16, 3, p.lin_q, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
+  if (c.mass_in != c.mass_out) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(lin.blocks));
-    cfg.blockDim = dim3(128);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(c.B) * c.Hkv * ((c.Lk + 1023) / 1024)));
+    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = bf16 ? cudaLaunchKernelEx(&cfg, cache_lse_kernel<true>, p) : cudaLaunchKernelEx(&cfg, cache_lse_kernel<false>, p);
-    if (e != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, mass_copy_kernel, p)) != cudaSuccess) return e;
   }
   const int pairs = p.n_pieces < sms / 2 ? p.n_pieces : sms / 2;
   if (p.width == 64) return bf16 ? launch_any<64, true>(maps, p, pairs, st) : launch_any<64, false>(maps, p, pairs, st);
