@@ -55,9 +55,10 @@ constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsHigh;
 // A step of 16 values for 128 rows: 8-row groups of 256 bytes, in each the rows'
 // first 8 values (16 bytes a row), then their second 8 (no swizzle).
 constexpr int kLinBytes = 128 * 32;
-// Readers of a published piece: in both CTAs the Q/K loader, the V loader and
-// one softmax thread; the even CTA's MMA issuer.
-constexpr int kPieceReaders = 7;
+// Readers of a published piece: in both CTAs the Q/K loader (which hands it on
+// to its CTA's softmax warps) and the V loader; the even CTA's MMA issuer.
+constexpr int kPieceReaders = 5;
+constexpr int kHanded = 4;  // pieces handed on at a time
 
 // LIN: with the products that add the distance bias (see cache_attn_kernel).
 template <int DH, bool LIN>
@@ -75,9 +76,9 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + KK * K_BYTES;
   static constexpr int OFF_LIN = OFF_V + kStages * V_BYTES;  // Q's part, K's part, K's negative part
   static constexpr int OFF_BAR = OFF_LIN + (LIN ? 3 * kLinBytes : 0);
-  static constexpr int N_BARS = 13 + 5 * kStages;  // an even number
-  // barriers, TMEM address, two published piece slots and the softmax's copies
-  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + 8 * 16;
+  static constexpr int N_BARS = 13 + 5 * kStages + 2 * kHanded;  // an even number
+  // barriers, TMEM address, two published piece slots and the pieces handed on
+  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + (4 + 2 * kHanded) * 16;
   static constexpr int OH = DH / 2;             // O columns per thread
   static constexpr int OC = 32;                 // O columns per TMEM access
 };
@@ -87,6 +88,10 @@ struct Cfg {
 // waits are on the kernels' critical path even where they find the barrier done.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, ERR_ATTN_TIMEOUT));
+}
+
+__device__ __forceinline__ void mbar_arrive_local(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Instruction descriptor: f32 accumulate, A and B of the operand type, A
@@ -478,9 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + KS;  // [KS] even, one arrival per CTA
   uint64_t* v_empty = v_full + KS;  // [KS] both
   uint64_t* v_zero = v_empty + KS;  // [KS] own: a V tile to be zeroed behind the keys landed
+  uint64_t* h_full = bars + 13 + 5 * KS;   // [kHanded] own: a piece handed on to the softmax warps
+  uint64_t* h_empty = h_full + kHanded;    // [kHanded] own: all eight took it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   int4* pc_slot = reinterpret_cast<int4*>(smem + C::OFF_BAR + C::N_BARS * 8 + 16);  // [2][2]
-  int4* sm_piece = pc_slot + 4;                                                            // [2][2]
+  int4* sm_piece = pc_slot + 4;                                                            // [kHanded][2]
   static_assert((C::N_BARS * 8) % 16 == 0, "the piece slots are 16-byte aligned");
 
   pdl_trigger();
@@ -493,7 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool all16 = i == 2 || i == 3 || i == 5;
       const bool readers = i == 10 || i == 11;
       const bool two = i >= 12 + 2 * KS && i < 12 + 3 * KS;  // v_full
-      mbar_init(&bars[i], all16 ? 16 : readers ? kPieceReaders : two ? 2 : 1);
+      const bool taken = i >= 13 + 5 * KS + kHanded;
+      mbar_init(&bars[i], all16 ? 16 : readers ? kPieceReaders : two ? 2 : taken ? 8 : 1);
     }
     fence_mbar_init();
     prefetch_tensormap(&tmQ);
@@ -584,7 +592,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t k_full0 = mapa_shared(k_full, 0);
         int gk = 0, gq = 0;
         Piece pc;
-        for (int i = 0; take_piece(i, pc); release_piece(i), ++i) {
+        for (int i = 0;; release_piece(i), ++i) {
+          const bool more = take_piece(i, pc);
+          // Handed on within the CTA: softmax warps that released slots of the pair
+          // themselves would wait for their stores of O each time.
+          const int s = i % kHanded;
+          if (!mbar_wait(&h_empty[s], ((i / kHanded) & 1) ^ 1, err, ERR_ATTN_TIMEOUT)) break;
+          sm_piece[2 * s] = more ? pc.a : make_int4(-1, 0, 0, 0);
+          sm_piece[2 * s + 1] = pc.b;
+          mbar_arrive_local(&h_full[s]);
+          if (!more) break;
           const int nT = pc.b.w;
           if (nT == 0) continue;
           const int b = pc.a.x / p.c.Hkv, hk = pc.a.x % p.c.Hkv;
@@ -754,20 +771,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     uint32_t gz = 0;
     for (int i = 0;; ++i) {
-      // One thread takes the piece for the CTA's eight softmax warps, so that
-      // all of them run the same pieces and named barriers.
-      if (warp == 4 && lane == 0) {
-        Piece pc;
-        if (!take_piece(i, pc)) pc.a.x = -1;
-        sm_piece[2 * (i & 1)] = pc.a;
-        sm_piece[2 * (i & 1) + 1] = pc.b;
-      }
-      __syncwarp();  // the barrier and the TMEM accesses below are for whole warps
-      // (A copy is rewritten two pieces later, behind a barrier that its readers passed.)
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const int4 pa = ld_shared_v4(sm_piece + 2 * (i & 1)), pb = ld_shared_v4(sm_piece + 2 * (i & 1) + 1);
+      if (!warp_wait(&h_full[i % kHanded], (i / kHanded) & 1, err)) break;
+      __syncwarp();
+      const int4 pa = ld_shared_v4(sm_piece + 2 * (i % kHanded)), pb = ld_shared_v4(sm_piece + 2 * (i % kHanded) + 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(&h_empty[i % kHanded]);
       if (pa.x < 0) break;
-      if (warp == 11 && lane == 0) release_piece(i);  // every warp has the copy
       const int b = pa.x / p.c.Hkv, kvh = pa.x % p.c.Hkv;
       const int k_len = pb.x, q_len = pb.y, nT = pb.w;
       // This thread's row.

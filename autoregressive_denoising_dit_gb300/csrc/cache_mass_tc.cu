@@ -27,6 +27,8 @@ namespace {
 
 constexpr int QS = 4;          // row-tile stages
 constexpr int kMassThreads = 640, kWeightWarps = 16;
+// Readers of a published piece: both loaders (which hand it on) and the MMA issuer.
+constexpr int kMassReaders = 3;
 constexpr int kHalf = 132;     // words between the halves of a column array: other banks
 constexpr int kColWords = 2 * kHalf;
 
@@ -44,8 +46,8 @@ struct MCfg {
   static constexpr int COL_BYTES = COL_ARRAYS * kColWords * 4 + 16;  // and {limit min, doc min, doc max, 0}
   static constexpr int OFF_BAR = OFF_COL + QS * ((COL_BYTES + 127) / 128 * 128);
   static constexpr int COL_STRIDE = (COL_BYTES + 127) / 128 * 128;
-  static constexpr int N_BARS = 12 + 4 * QS;
-  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + 8 * 16 + 2 * 128 * 4;
+  static constexpr int N_BARS = 12 + 4 * QS + 2 * kHanded;
+  static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + (4 + 2 * kHanded) * 16 + 2 * 128 * 4;
 };
 
 // (x0, x1) * s + (b0, b1).
@@ -98,11 +100,13 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   uint64_t* q_empty = q_full + QS;   // [QS] both
   uint64_t* c_full = q_empty + QS;   // [QS] own: columns noted
   uint64_t* c_empty = c_full + QS;   // [QS] own: all 16 weight warps used them
+  uint64_t* h_full = c_empty + QS;       // [kHanded] own: a piece handed on to warps 3 and up
+  uint64_t* h_empty = h_full + kHanded;  // [kHanded] own: all 17 took it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   int4* pc_slot = reinterpret_cast<int4*>(smem + C::OFF_BAR + C::N_BARS * 8 + 16);  // [2][3]
   static_assert((C::N_BARS * 8) % 16 == 0, "the piece slots are 16-byte aligned");
-  int4* sm_piece = pc_slot + 4;                                                      // [2][2]
-  float* part = reinterpret_cast<float*>(sm_piece + 4);                              // [2][128]
+  int4* sm_piece = pc_slot + 4;                                                      // [kHanded][2]
+  float* part = reinterpret_cast<float*>(sm_piece + 2 * kHanded);                    // [2][128]
 
   pdl_trigger();
   const int warp = warp_id(), lane = lane_id();
@@ -113,8 +117,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     for (int i = 0; i < C::N_BARS; ++i) {
       const bool free16 = i == 6 || i == 7;
       const bool readers = i == 10 || i == 11;
-      const bool cols = i >= 12 + 3 * QS;
-      mbar_init(&bars[i], free16 ? 2 * kWeightWarps : readers ? kPieceReaders : cols ? kWeightWarps : 1);
+      const bool cols = i >= 12 + 3 * QS && i < 12 + 4 * QS, taken = i >= 12 + 4 * QS + kHanded;
+      mbar_init(&bars[i], free16 ? 2 * kWeightWarps : readers ? kMassReaders : cols ? kWeightWarps : taken ? kWeightWarps + 1 : 1);
     }
     fence_mbar_init();
     prefetch_tensormap(&tmQ);
@@ -144,6 +148,17 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     return pc.a.x >= 0;
   };
   auto release_piece = [&](int i) { mbar_arrive_cluster(pc_empty0 + (i & 1) * 8); };
+  // By a whole warp: the piece handed on by the CTA's loader; false at the end.
+  auto handed_piece = [&](int i, int4& a, int4& b) -> bool {
+    const int s = i % kHanded;
+    if (!warp_wait(&h_full[s], (i / kHanded) & 1, err)) return false;
+    __syncwarp();
+    a = ld_shared_v4(sm_piece + 2 * s);
+    b = ld_shared_v4(sm_piece + 2 * s + 1);
+    __syncwarp();
+    if (lane == 0) mbar_arrive_local(&h_empty[s]);
+    return a.x >= 0;
+  };
 
   if (warp == 2) {
     if (leader) {
@@ -211,7 +226,14 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const uint32_t q_full0 = mapa_shared(q_full, 0);
       int gk = 0, g = 0;
       Piece pc;
-      for (int i = 0; take_piece(i, pc); release_piece(i), ++i) {
+      for (int i = 0;; release_piece(i), ++i) {
+        const bool more = take_piece(i, pc);
+        const int s = i % kHanded;
+        if (!mbar_wait(&h_empty[s], ((i / kHanded) & 1) ^ 1, err, ERR_ATTN_TIMEOUT)) break;
+        sm_piece[2 * s] = more ? pc.a : make_int4(-1, 0, 0, 0);
+        sm_piece[2 * s + 1] = pc.b;
+        mbar_arrive_local(&h_full[s]);
+        if (!more) break;
         const int nT = pc.a.w;
         if (nT == 0) continue;
         const int b = pc.a.x / p.c.Hkv, kvh = pc.a.x % p.c.Hkv;
@@ -289,7 +311,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       }
     }
   } else if (warp == 3) {
-    // ---------------- columns of the row tiles (every lane reads the piece).  A
+    // ---------------- columns of the row tiles.  A
     // lane notes columns 32 x + lane of both halves; their tokens and heads
     // within a tile are the same for every tile.
     int dtok[4], dhead[4];
@@ -303,9 +325,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     int g = 0;
     Piece pc;
     for (int i = 0;; ++i) {
-      if (!__all_sync(0xffffffffu, take_piece(i, pc))) break;
-      __syncwarp();
-      if (lane == 0) release_piece(i);
+      if (!handed_piece(i, pc.a, pc.b)) break;
       const int b = pc.a.x / p.c.Hkv, kvh = pc.a.x % p.c.Hkv, nk = pc.b.x, nq = pc.b.y;
       const int prefix = p.c.prefix ? p.c.prefix[b] : 0;
       const float* lse = p.c.lse + (static_cast<int64_t>(b) * p.c.Hq + kvh * p.c.G) * p.c.Lq;
@@ -383,23 +403,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     const float scale2 = p.c.scale * kLog2e;
     const float inv = p.c.softcap > 0 ? p.c.scale / p.c.softcap : 0.0f, c2 = p.c.softcap * kLog2e;
     int g = 0;
-    // One thread takes the pieces for the CTA's weight warps, the next one while
-    // the last tile of a piece is worked on; the barrier at the end of a piece
-    // then hands it over, and joins the two warps of a key as well.
-    auto fetch_piece = [&](int i) {
-      Piece pc;
-      if (!take_piece(i, pc)) pc.a.x = -1;
-      sm_piece[2 * (i & 1)] = pc.a;
-      sm_piece[2 * (i & 1) + 1] = pc.b;
-    };
-    if (warp == 4 && lane == 0) fetch_piece(0);
-    __syncwarp();
-    asm volatile("bar.sync 1, 512;" ::: "memory");
     for (int i = 0;; ++i) {
-      const int4 pa = ld_shared_v4(sm_piece + 2 * (i & 1)), pb = ld_shared_v4(sm_piece + 2 * (i & 1) + 1);
-      if (pa.x < 0) break;
-      if (warp == 19 && lane == 0) release_piece(i);
-      __syncwarp();
+      int4 pa, pb;
+      if (!handed_piece(i, pa, pb)) break;
       const int b = pa.x / p.c.Hkv, kvh = pa.x % p.c.Hkv, nk = pb.x, nT = pa.w;
       const int key = pa.y * KT + rank * 128 + r;
       const bool valid = key < nk;
@@ -410,11 +416,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const bool writes = valid && half == 0 && quarter == 0;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool ok = true;
-      if (nT == 0 && warp == 4 && lane == 0) fetch_piece(i + 1);
       for (int j = 0; j < nT; ++j, ++g) {
         const int st = g % QS, sb = g & 1;
-        if (j + 1 == nT && warp == 4 && lane == 0) fetch_piece(i + 1);
-        __syncwarp();
         if (ok) ok = warp_wait(&s_full[sb], (g >> 1) & 1, err);
         if (!ok) continue;
         tc_fence_after();
@@ -505,9 +508,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       float* other = part + (i & 1) * 128;
       if (quarter == 1 && half == 0) other[r] = sum;
       __syncwarp();
-      // (Copies of pieces and sums are rewritten two pieces later, behind a barrier
-      // that their readers have reached.)
-      asm volatile("bar.sync 1, 512;" ::: "memory");
+      // (A buffer of sums is used again two pieces later, behind a barrier that its
+      // reader has reached.)
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + ((warp - 4) & 7)) : "memory");
       // mass_out holds the old mass: one addition to each entry, whose order does
       // not matter, and which needs no answer.
       if (ok && writes) atomicAdd(p.c.mass_out + at, sum + other[r]);
