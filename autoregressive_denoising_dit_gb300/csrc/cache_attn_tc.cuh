@@ -59,11 +59,12 @@ constexpr int kLinBytes = 128 * 32;
 // to its CTA's softmax warps) and the V loader; the even CTA's MMA issuer.
 constexpr int kPieceReaders = 5;
 constexpr int kHanded = 4;  // pieces handed on at a time
+constexpr int kOutRow = 144, kOutBytes = 16 * kOutRow;
 
 // LIN: with the products that add the distance bias (see cache_attn_kernel).
 template <int DH, bool LIN>
 struct Cfg {
-  static constexpr int KK = LIN ? 2 : kStages;  // K stages (two measured as fast as three)
+  static constexpr int KK = 2;                  // K stages (measured as fast as three)
   static constexpr int NA = DH / 64;            // 64-wide (128-byte) atoms along dh
   static constexpr int VR = DH / 2;             // V columns held per CTA
   static constexpr int Q_BYTES = QT * DH * 2;
@@ -75,12 +76,13 @@ struct Cfg {
   static constexpr int OFF_K = OFF_Q + Q_BYTES;
   static constexpr int OFF_V = OFF_K + KK * K_BYTES;
   static constexpr int OFF_LIN = OFF_V + kStages * V_BYTES;  // Q's part, K's part, K's negative part
-  static constexpr int OFF_BAR = OFF_LIN + (LIN ? 3 * kLinBytes : 0);
+  // Per softmax warp 16 rows of 2 * 64 bytes, 16 apart (no bank twice): O on its way out.
+  static constexpr int OFF_OUT = OFF_LIN + (LIN ? 3 * kLinBytes : 0);
+  static constexpr int OFF_BAR = OFF_OUT + 8 * kOutBytes;
   static constexpr int N_BARS = 13 + 5 * kStages + 2 * kHanded;  // an even number
   // barriers, TMEM address, two published piece slots and the pieces handed on
   static constexpr size_t SMEM = OFF_BAR + N_BARS * 8 + 16 + (4 + 2 * kHanded) * 16;
   static constexpr int OH = DH / 2;             // O columns per thread
-  static constexpr int OC = 32;                 // O columns per TMEM access
 };
 
 // By the whole warp: every lane polls (one access for all of them); a branch to
@@ -1054,48 +1056,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(p_full_b0);
       }
+      // A thread's row leaves by way of shared memory, 64 bytes of either half of
+      // its columns at a time, so that four lanes write 64 consecutive bytes
+      // (lanes that wrote rows of their own took 4000 clocks a piece, this 1000).
+      const float lo = __shfl_xor_sync(0xffffffffu, l, 16);
+      l = hk16 == 0 ? l + lo : lo + l;
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const bool split = p.nsplit > 1;
+      const int64_t piece = (static_cast<int64_t>(pa.x) * p.units + pa.y) * p.nsplit + (pa.z & 127);
+      const int64_t prow = piece * p.part_rows + rank * p.rows_cta + r;
+      char* row = split ? reinterpret_cast<char*>(p.part_o + prow * DH)
+                        : reinterpret_cast<char*>(static_cast<uint16_t*>(p.c.o) + b * p.c.os.b + tok * p.c.os.l + head * p.c.os.h);
+      if (!valid) row = nullptr;
+      char* out[4];  // of rows lane / 8 + 4 k
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        out[k] = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), 4 * k + (lane >> 3)));
+      uint8_t* stage = smem + C::OFF_OUT + (warp - 4) * kOutBytes;
+      uint4* mine = reinterpret_cast<uint4*>(stage + (lane & 15) * kOutRow + hk16 * 64);
+      const int half = (lane >> 2) & 1, unit = lane & 3;  // what this lane writes of its four rows
+      const uint4* theirs = reinterpret_cast<const uint4*>(stage + (lane >> 3) * kOutRow + half * 64 + unit * 16);
+      const int width = split ? 2 * C::OH * 4 : p.c.dh * 2;  // bytes of a row (heads may be narrower than DH)
+      auto put = [&](const uint32_t* w, int c) {  // 64 bytes c of this thread's half of its row
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mine[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        __syncwarp();
+        const int at = half * (split ? C::OH * 4 : C::OH * 2) + c * 64 + unit * 16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (out[k] && at < width) *reinterpret_cast<uint4*>(out[k] + at) = theirs[k * (4 * kOutRow / 16)];
+        __syncwarp();
+      };
+      // O is read before this thread writes any P of the next piece, whose
+      // first P.V overwrites it.
       if (ok && nT > 0) {
         ok = warp_wait(o_done, (g + nT - 1) & 1, err);
         if (ok) tc_fence_after();
       }
       g += nT;
       if (!active || !ok) continue;
-      const float lo = __shfl_xor_sync(0xffffffffu, l, 16);
-      l = hk16 == 0 ? l + lo : lo + l;
-      // O is read before this thread writes any P of the next piece, whose
-      // first P.V overwrites it.
-      const bool split = p.nsplit > 1;
-      const int64_t piece = (static_cast<int64_t>(pa.x) * p.units + pa.y) * p.nsplit + (pa.z & 127);
-      const int64_t prow = piece * p.part_rows + rank * p.rows_cta + r;
-      using T = uint16_t;
-      T* dst = static_cast<T*>(p.c.o) + b * p.c.os.b + tok * p.c.os.l + head * p.c.os.h + hk16 * C::OH;
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll 1
-      for (int c = 0; c < C::OH / C::OC; ++c) {
-        float o[C::OC];
-        if (nT > 0) {
-          tmem_ld32x<C::OH>(o_addr + c * C::OC, o);
-          tmem_wait_ld();
-        } else {
+      float o[C::OH];
+      if (nT > 0) {
 #pragma unroll
-          for (int e = 0; e < C::OC; ++e) o[e] = 0.0f;
-        }
-        if (valid && split) {
-          float4* d4 = reinterpret_cast<float4*>(p.part_o + prow * DH + hk16 * C::OH + c * C::OC);
+        for (int c = 0; c < C::OH / 32; ++c) tmem_ld32x<C::OH>(o_addr + c * 32, o + c * 32);
+        tmem_wait_ld();
+      } else {
 #pragma unroll
-          for (int e = 0; e < C::OC / 4; ++e) d4[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else if (valid) {
-          // 16 bytes at a time; heads narrower than DH end at dh (a multiple of 8).
-          uint4* d4 = reinterpret_cast<uint4*>(dst + c * C::OC);
+        for (int e = 0; e < C::OH; ++e) o[e] = 0.0f;
+      }
+      uint32_t w[C::OH];
+      if (split) {
 #pragma unroll
-          for (int e = 0; e < C::OC / 8; ++e) {
-            const float* x = o + 8 * e;
-            if (hk16 * C::OH + c * C::OC + 8 * e < p.c.dh)
-              d4[e] = make_uint4(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv),
-                                 pack2<BF16>(x[4] * inv, x[5] * inv), pack2<BF16>(x[6] * inv, x[7] * inv));
-          }
-        }
-        __syncwarp();
+        for (int e = 0; e < C::OH; ++e) w[e] = __float_as_uint(o[e]);
+#pragma unroll
+        for (int c = 0; c < C::OH / 16; ++c) put(w + 16 * c, c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < C::OH / 2; ++e) w[e] = pack2<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+#pragma unroll
+        for (int c = 0; c < C::OH / 32; ++c) put(w + 16 * c, c);
       }
       if (valid && hk16 == 0) {
         if (split) {
