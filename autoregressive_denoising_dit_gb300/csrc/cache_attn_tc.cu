@@ -65,6 +65,55 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
   if (lane == 0) p.row_units[w] = RowUnit{pmin, pmax, dmin, dmax};
 }
 
+// Units that unit_order is made for: with more there are enough pieces after the
+// longest ones to even out the pairs' times.
+constexpr int kOrderUnits = 512;
+
+// Sorts a sequence's units by the key tiles that they see: rows of two documents
+// see the tiles of both, and such a unit taken last kept its pair at work for
+// TAIL_FIGURE.  One CTA per sequence.
+__global__ void __launch_bounds__(1024) cache_order_kernel(const __grid_constant__ TcParams p) {
+  __shared__ int s_w[kOrderUnits], s_most, s_least;
+  pdl_trigger();
+  const int b = blockIdx.x;
+  if (threadIdx.x == 0) s_most = 0, s_least = 0x7fffffff;
+  __syncthreads();
+  pdl_wait();
+  const int nk = cache_k_len(p.c, b), nq = cache_q_len(p.c, b), n = (nk + KT - 1) / KT;
+  const int prefix = p.c.prefix ? p.c.prefix[b] : 0;
+  const KeyTile* tiles = p.key_tiles + static_cast<int64_t>(b) * p.meta_heads * p.tiles;  // (of the first head)
+  for (int u = warp_id(); u < p.units; u += 32) {
+    const RowUnit ru = p.row_units[static_cast<int64_t>(b) * p.units + u];
+    const int most = max(ru.pos_max + 1, prefix);
+    int w = 0;
+    for (int t = lane_id(); t < n; t += 32) {
+      const KeyTile k = tiles[t];
+      w += (!p.c.k_doc || (k.doc_min <= ru.doc_max && k.doc_max >= ru.doc_min)) && (!p.c.causal || k.pos_min < most);
+    }
+    w = __reduce_add_sync(0xffffffffu, w);
+    if (lane_id() == 0) {
+      const bool rows = u * 2 * p.tok_cta < nq;
+      s_w[u] = rows ? w : 0;
+      if (rows) {
+        atomicMax(&s_most, w);
+        atomicMin(&s_least, w);
+      }
+    }
+  }
+  __syncthreads();
+  int* order = p.unit_order + static_cast<int64_t>(b) * p.units;
+  if (s_most <= s_least + s_least / 4) {
+    if (threadIdx.x == 0) order[0] = -1;
+    return;
+  }
+  for (int u = threadIdx.x; u < p.units; u += 1024) {
+    const int w = s_w[u];
+    int rank = 0;
+    for (int v = 0; v < p.units; ++v) rank += s_w[v] > w || (s_w[v] == w && v < u);
+    order[rank] = u;
+  }
+}
+
 // A head group's rows' slopes / scale as three values of the operand type whose
 // sum holds 24 bits, in the layout of kLinBytes; and whether they fit it.
 template <bool BF16>
@@ -168,7 +217,8 @@ struct TcLayout {
   int64_t pieces;
   int tiles, meta_heads;  // of the buffer; 0: no positions or documents
   bool lin;  // the distance bias by products (no cap, no positions or documents given)
-  size_t part_o, part_ml, key_tiles, row_units, lin_ok, lin_q, total;
+  size_t part_o, part_ml, key_tiles, row_units, unit_order, lin_ok, lin_q, total;
+  int order_heads;  // 0: units in their own order
 };
 
 TcLayout tc_layout(const CacheParams& c) {
@@ -205,6 +255,14 @@ TcLayout tc_layout(const CacheParams& c) {
     off += up256(sizeof(KeyTile) * static_cast<size_t>(c.B) * t.meta_heads * t.tiles);
     t.row_units = off;
     off += up256(sizeof(RowUnit) * static_cast<size_t>(c.B) * t.units);
+    if (t.units > 1 && t.units <= kOrderUnits && c.k_doc && !c.causal) {
+      // Four rounds of the pairs at a time; the keys of more heads than that
+      // would leave L2 before the next unit reads them.
+      t.order_heads = (4 * kPlanPairs + t.units - 1) / t.units;
+      if (t.order_heads > c.Hkv) t.order_heads = c.Hkv;
+      t.unit_order = off;
+      off += up256(sizeof(int) * static_cast<size_t>(c.B) * t.units);
+    }
   }
   t.lin = !t.few && c.slopes && !(c.softcap > 0) && !c.k_pos && !c.k_doc && !c.q_pos;
   if (t.lin) {
@@ -309,6 +367,8 @@ TcParams cattn::plan(const CacheParams& c, char* scratch) {
   if (t.meta_heads) {
     p.key_tiles = reinterpret_cast<KeyTile*>(scratch + t.key_tiles);
     p.row_units = reinterpret_cast<RowUnit*>(scratch + t.row_units);
+    if (t.order_heads) p.unit_order = reinterpret_cast<int*>(scratch + t.unit_order);
+    p.order_heads = t.order_heads;
   }
   if (t.lin) {
     p.lin_ok = reinterpret_cast<int*>(scratch + t.lin_ok);
@@ -358,6 +418,20 @@ cudaError_t cattn::launch_tiles(const TcParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, cache_tiles_kernel, p);
 }
 
+cudaError_t cattn::launch_order(const TcParams& p, cudaStream_t st) {
+  if (!p.unit_order) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_order_kernel, p);
+}
+
 cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scratch, int sms, cudaStream_t st) {
   const TcParams p = plan(c, scratch);
   cudaError_t e;
@@ -375,7 +449,7 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
     if (!encode_16bit_map(&maps[3], bf16, 3, p.lin_q, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
     if ((e = launch_lin(p, bf16, st)) != cudaSuccess) return e;
   }
-  if ((e = launch_tiles(p, st)) != cudaSuccess) return e;
+  if ((e = launch_tiles(p, st)) != cudaSuccess || (e = launch_order(p, st)) != cudaSuccess) return e;
   const int pairs = p.n_pieces < sms / 2 ? p.n_pieces : sms / 2;
   const int f = (c.softcap > 0 ? F_CAP : 0) | (c.slopes ? F_BIAS : 0) | (c.k_doc || c.k_pos || c.q_pos ? F_META : 0);
   if (p.width == 64)

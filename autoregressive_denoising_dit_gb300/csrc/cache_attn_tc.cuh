@@ -307,6 +307,10 @@ struct TcParams {
   int tiles;        // key tiles of the buffer
   KeyTile* key_tiles;  // [B][meta_heads][tiles], with k_pos or k_doc only
   RowUnit* row_units;  // [B][units]
+  // [B][units]: a sequence's units with most key tiles first (unit_order[0] < 0:
+  // they have about as many), for order_heads kv heads at a time; or null.
+  int* unit_order;
+  int order_heads;
   // [Hkv]: whether a head group's slopes fit the operand type, and the rows'
   // slopes in three parts (kLinBytes).
   int* lin_ok;
@@ -356,6 +360,14 @@ struct Piece {
 __device__ __forceinline__ int4 piece_index(const TcParams& p, int k) {
   const int BH = p.c.B * p.c.Hkv;
   const int s = k % p.nsplit, r = k / p.nsplit;
+  if (p.unit_order) {
+    const int per_seq = p.c.Hkv * p.units, b = r / per_seq, q = r % per_seq;
+    const int* order = p.unit_order + static_cast<int64_t>(b) * p.units;
+    if (order[0] < 0) return make_int4(r / p.units, r % p.units, s, 0);
+    const int h0 = q / (p.order_heads * p.units) * p.order_heads, at = q - h0 * p.units;
+    const int heads = min(p.order_heads, p.c.Hkv - h0);
+    return make_int4(b * p.c.Hkv + h0 + at % heads, order[at / heads], s, 0);
+  }
   // Causal: the units with most keys first, so that the last pieces taken are
   // short.  Otherwise the units of one (sequence, kv head) run together and
   // share its keys in L2.
@@ -847,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Which of the 128 keys this row sees, one bit each (while S is made),
         // if some row of the warp sees a part of the tile.
         uint32_t seen[4];
-        bool masked = false;
+        bool masked = false, none = false;  // (none: no row of the warp sees a key of the tile)
         int d0 = qp - key0;  // distance of the first key, where positions run
         bool run = true;
         // (A stretch of tiles is known to be seen whole; only the distance bias
@@ -863,7 +875,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.c.k_pos) d0 = qp - kt.base - hk16 * 128;
           const bool doc_all = !p.c.k_doc || (kt.doc_min == qd && kt.doc_max == qd);
           const bool pos_all = !ordered || kt.pos_max < plim;
-          masked = !whole && __any_sync(0xffffffffu, valid && !(doc_all && pos_all));
+          none = __all_sync(0xffffffffu, !valid || (p.c.k_doc && (qd < kt.doc_min || qd > kt.doc_max)) ||
+                                             (ordered && kt.pos_min >= plim));
+          masked = !whole && !none && __any_sync(0xffffffffu, valid && !(doc_all && pos_all));
           if (masked && kt.sorted && (run || !ordered)) {
             // The row's document is one stretch of the tile, and positions that
             // run are seen up to a limit: keys [lo, hi).
@@ -904,9 +918,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) ok = warp_wait(s_full, t & 1, err);
         if (!ok) continue;
-        if (!active) {  // no row here: only keep the barriers' counts
+        if (!active || ((F & F_META) && none)) {  // only keep the barriers' counts
           if (lane == 0) mbar_arrive_remote(s_free0);
           if (j > 0) ok = warp_wait(o_done, (t - 1) & 1, err);
+          if ((F & F_META) && ok && active) {
+            const uint32_t zero[16] = {};
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st16x<64>(p_addr + 16 * c, zero);
+            tmem_wait_st();
+            tc_fence_before();
+          }
           if (ok) ok = release_p(j, t);
           if (ok && lane == 0) mbar_arrive_remote(p_full_b0);
           continue;
@@ -1203,6 +1225,8 @@ cudaError_t launch_features(const CUtensorMap* maps, const TcParams& p, int f, i
 TcParams plan(const CacheParams& c, char* scratch);
 bool encode_maps(CUtensorMap* maps, const CacheParams& c, const TcParams& p, bool bf16, bool values);
 cudaError_t launch_tiles(const TcParams& p, cudaStream_t st);
+// And the one that fills unit_order from them.
+cudaError_t launch_order(const TcParams& p, cudaStream_t st);
 
 extern template cudaError_t launch_features<64, true>(const CUtensorMap*, const TcParams&, int, int, cudaStream_t);
 extern template cudaError_t launch_features<64, false>(const CUtensorMap*, const TcParams&, int, int, cudaStream_t);
