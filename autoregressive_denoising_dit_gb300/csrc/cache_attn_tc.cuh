@@ -419,14 +419,29 @@ __device__ __forceinline__ void seen_tiles(const TcParams& p, int b, int kvh, in
   count = max(w1 - whole, 0);
 }
 
-// LIN: 1 if every row of the piece's unit lies at or behind all keys of the
-// tile, -1 if at or before them, 0 otherwise (or if the slopes do not fit).
-__device__ __forceinline__ int tile_side(const TcParams& p, const Piece& pc, int tile) {
-  if (!pc.a.w) return 0;
+// LIN: the rows of the piece's unit lie at or behind all keys of tiles up to x,
+// and at or before those of tiles from y on; the other tiles are done key by key
+// (all of them if the slopes do not fit).
+__device__ __forceinline__ int2 lin_tiles(const TcParams& p, const Piece& pc) {
   const int unit = 2 * p.tok_cta, first = pc.b.x - pc.b.y + pc.a.y * unit;
   const int last = pc.b.x - pc.b.y + min(pc.b.y, (pc.a.y + 1) * unit) - 1;
-  if (first >= tile * KT + KT - 1) return 1;
-  return last <= tile * KT ? -1 : 0;
+  static_assert(KT == 256, "the shifts");
+  return pc.a.w ? make_int2((first - (KT - 1)) >> 8, (last + KT - 1) >> 8) : make_int2(-1, 0x7fffffff);
+}
+// Which of the two: 1, -1, or 0 for neither.
+__device__ __forceinline__ int tile_side(int2 lin, int tile) { return tile <= lin.x ? 1 : tile >= lin.y ? -1 : 0; }
+
+// The j-th key tile of a piece.  With a distance bias (and positions that are
+// indexes) the walk starts at the unit's last row and goes down, then from the
+// last tile down to there: the tiles towards the rows have the larger scores,
+// and in ascending order nearly every one of them raised the running maximum
+// and had O rescaled (wave with bias 257 us).
+template <bool ROTATE>
+__device__ __forceinline__ int tile_at(const TcParams& p, const Piece& pc, int j) {
+  if constexpr (!ROTATE) return pc.b.z + j;
+  const int row = pc.b.x - pc.b.y + min(pc.b.y, (pc.a.y + 1) * 2 * p.tok_cta) - 1;  // (may be negative)
+  const int at = min(max(max(row, 0) / KT - pc.b.z, 0), pc.b.w - 1) - j;
+  return at >= 0 ? pc.b.z + at : pc.b.z + pc.b.w + at;
 }
 
 // Whether a key tile ends behind the keys inside the buffer (rows behind the
@@ -471,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmL,
                       const __grid_constant__ TcParams p) {
-  constexpr bool LIN = F == F_BIAS;
+  constexpr bool LIN = F == F_BIAS, ROT = (F & F_BIAS) && !(F & F_META);
   using C = Cfg<DH, LIN>;
   constexpr int KS = kStages, KK = C::KK;
   extern __shared__ uint8_t smem[];
@@ -639,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int a = 0; a < C::NA; ++a)
               tma_load_4d_pair(dst + a * C::ATOM, &tmK, k_full0 + st * 8, a * 64,
-                               (pc.b.z + j) * KT + rank * 128, hk, b);
+                               tile_at<ROT>(p, pc, j) * KT + rank * 128, hk, b);
           }
           if (!ok) break;
         }
@@ -666,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool ok = true;
           for (int j = 0; j < pc.b.w; ++j, ++gv) {
             const int st = gv % KS;
-            const int key0 = (pc.b.z + j) * KT;
+            const int key0 = tile_at<ROT>(p, pc, j) * KT;
             if (!mbar_wait(&v_empty[st], ((gv / KS) & 1) ^ 1, err, ERR_ATTN_TIMEOUT)) {
               ok = false;
               break;
@@ -721,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         ++gq;
         tc_fence_after();
-        issue_s(g, LIN ? tile_side(p, pc, pc.b.z) : 0);
+        const int2 lin = LIN ? lin_tiles(p, pc) : int2{};
+        issue_s(g, LIN ? tile_side(lin, tile_at<ROT>(p, pc, 0)) : 0);
         if (nT == 1) umma_commit_pair_mc(q_empty, 0x3);
         for (int j = 0; j < nT; ++j) {
           const int t = g + j;
@@ -732,13 +748,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
-            issue_s(t + 1, LIN ? tile_side(p, pc, pc.b.z + j + 1) : 0);
+            issue_s(t + 1, LIN ? tile_side(lin, tile_at<ROT>(p, pc, j + 1)) : 0);
             if (j + 2 == nT) umma_commit_pair_mc(q_empty, 0x3);
           }
-          // In a piece's last tile the acquire at cluster scope pairs with the
-          // softmax warps' release after they zeroed rows of V.
-          if (!(j + 1 < nT ? mbar_wait(p_full_a, t & 1, err, ERR_ATTN_TIMEOUT)
-                           : mbar_wait_acq_cluster(p_full_a, t & 1, err)) ||
+          // The acquire at cluster scope pairs with the softmax warps' release after
+          // they zeroed rows of V, in a piece's last tile at most (if not rotated).
+          const bool plain = ROT ? !zero_tile(p, tile_at<ROT>(p, pc, j) * KT, pc.b.x) : j + 1 < nT;
+          if (!(plain ? mbar_wait(p_full_a, t & 1, err, ERR_ATTN_TIMEOUT)
+                      : mbar_wait_acq_cluster(p_full_a, t & 1, err)) ||
               !mbar_wait(&v_full[t % KS], (t / KS) & 1, err, ERR_ATTN_TIMEOUT)) {
             ok = false;
             break;
@@ -822,13 +839,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < 8 && p.c.k_pos) prefetch_l1(p.c.k_pos + meta + j);
       };
       if ((F & F_META) && p.key_tiles && nT > 0 && active) fetch_meta(pb.z);
+      const int2 lin = LIN ? lin_tiles(p, Piece{pa, pb}) : int2{};
       float m = -INFINITY, l = 0.0f;  // l: this thread's half of the row sum
       bool ok = true;
       // Releases the first half of a tile's P (and its V).  In a tile that ends
       // behind the keys the CTA's 256 softmax threads zero those rows of V
       // first: P is 0 there, but 0 times NaN is not.
-      auto release_p = [&](int j, int t) -> bool {
-        const int key0 = (pb.z + j) * KT;
+      auto release_p = [&](int tile, int t) -> bool {
+        const int key0 = tile * KT;
         if (!zero_tile(p, key0, k_len)) {
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(p_full_a0);
@@ -855,7 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (which only skips the work).
       for (int j = 0; j < nT; ++j) {
         const int t = g + j;
-        const int key0 = (pb.z + j) * KT + hk16 * 128;
+        const int tile = tile_at<ROT>(p, Piece{pa, pb}, j);
+        const int key0 = tile * KT + hk16 * 128;
         // Which of the 128 keys this row sees, one bit each (while S is made),
         // if some row of the warp sees a part of the tile.
         uint32_t seen[4];
@@ -864,13 +883,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool run = true;
         // (A stretch of tiles is known to be seen whole; only the distance bias
         // then needs the tile's notes.)
-        const bool whole = static_cast<uint32_t>(pb.z + j - pa.w) < static_cast<uint32_t>(pa.z >> 7);
+        const bool whole = static_cast<uint32_t>(tile - pa.w) < static_cast<uint32_t>(pa.z >> 7);
         if ((F & F_META) && p.key_tiles && active && j + 1 < nT) {
-          const bool next_whole = static_cast<uint32_t>(pb.z + j + 1 - pa.w) < static_cast<uint32_t>(pa.z >> 7);
-          if ((F & F_BIAS) || !next_whole) fetch_meta(pb.z + j + 1);
+          const bool next_whole = static_cast<uint32_t>(tile + 1 - pa.w) < static_cast<uint32_t>(pa.z >> 7);
+          if ((F & F_BIAS) || !next_whole) fetch_meta(tile + 1);
         }
         if ((F & F_META) && p.key_tiles && active && ((F & F_BIAS) || !whole)) {
-          const KeyTile kt = tiles[pb.z + j];
+          const KeyTile kt = tiles[tile];
           run = kt.run;
           if (p.c.k_pos) d0 = qp - kt.base - hk16 * 128;
           const bool doc_all = !p.c.k_doc || (kt.doc_min == qd && kt.doc_max == qd);
@@ -929,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
           }
-          if (ok) ok = release_p(j, t);
+          if (ok) ok = release_p(tile, t);
           if (ok && lane == 0) mbar_arrive_remote(p_full_b0);
           continue;
         }
@@ -969,9 +988,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             sl2 = 1.0f;
           }
         }
-        const int side = LIN ? tile_side(p, Piece{pa, pb}, pb.z + j) : 0;
+        const int side = LIN ? tile_side(lin, tile) : 0;
         if constexpr (LIN) {
-          if (side != 0) off = (side > 0 ? -slope2 : slope2) * static_cast<float>(qp - (pb.z + j) * KT);
+          if (side != 0) off = (side > 0 ? -slope2 : slope2) * static_cast<float>(qp - tile * KT);
         }
         if constexpr ((F & F_BIAS) != 0) {
           if (side == 0) {
@@ -1066,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st16x<64>(p_addr + 16, pk1);
         tmem_wait_st();
         tc_fence_before();
-        ok = release_p(j, t);
+        ok = release_p(tile, t);
         if (!ok) continue;
         exp_chunk(2, pk0);
         tmem_st16x<64>(p_addr + 32, pk0);
