@@ -11,7 +11,8 @@ using namespace cattn;
 
 namespace {
 
-// KeyTile of every key tile and RowUnit of every unit: one warp each.
+// KeyTile of every key tile and RowUnit of every unit: one warp each.  Bound by
+// its launch and the latency of two dependent reads.
 __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant__ TcParams p) {
   pdl_trigger();
   pdl_wait();
@@ -25,24 +26,39 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
     const int n = cache_k_len(p.c, b), key0 = tile * KT;
     const int64_t meta = b * p.c.km_b + h * p.c.km_h;
     const int base = key0 < n ? (p.c.k_pos ? p.c.k_pos[meta + key0] : key0) : 0;
+    // Key c = 32 i + lane: all of a lane's reads are on their way at once.
+    int pos[KT / 32], doc[KT / 32];
+#pragma unroll
+    for (int i = 0; i < KT / 32; ++i) {
+      const int c = 32 * i + lane;
+      const bool in = key0 + c < n;
+      pos[i] = p.c.k_pos && in ? p.c.k_pos[meta + key0 + c] : key0 + c;
+      doc[i] = p.c.k_doc && in ? p.c.k_doc[meta + key0 + c] : 0;
+    }
     bool run = true, sorted = true;
-    for (int c = lane; c < KT && key0 + c < n; c += 32) {
-      const int pos = p.c.k_pos ? p.c.k_pos[meta + key0 + c] : key0 + c;
-      const int doc = p.c.k_doc ? p.c.k_doc[meta + key0 + c] : 0;
-      pmin = min(pmin, pos), pmax = max(pmax, pos);
-      dmin = min(dmin, doc), dmax = max(dmax, doc);
-      run = run && pos == base + c;
-      sorted = sorted && (!p.c.k_doc || c == 0 || p.c.k_doc[meta + key0 + c - 1] <= doc);
+#pragma unroll
+    for (int i = 0; i < KT / 32; ++i) {
+      const int c = 32 * i + lane;
+      int before = __shfl_up_sync(0xffffffffu, doc[i], 1);  // the key before's document
+      const int wrapped = __shfl_sync(0xffffffffu, doc[i ? i - 1 : 0], 31);
+      if (lane == 0) before = wrapped;
+      if (key0 + c < n) {
+        pmin = min(pmin, pos[i]), pmax = max(pmax, pos[i]);
+        dmin = min(dmin, doc[i]), dmax = max(dmax, doc[i]);
+        run = run && pos[i] == base + c;
+        sorted = sorted && (c == 0 || before <= doc[i]);
+      }
     }
     run = __all_sync(0xffffffffu, run);
     sorted = __all_sync(0xffffffffu, sorted);
     pmin = __reduce_min_sync(0xffffffffu, pmin), pmax = __reduce_max_sync(0xffffffffu, pmax);
     dmin = __reduce_min_sync(0xffffffffu, dmin), dmax = __reduce_max_sync(0xffffffffu, dmax);
     int first = 0, other = 0;  // keys of doc_min, keys of neither end
-    for (int c = lane; c < KT && key0 + c < n; c += 32) {
-      const int doc = p.c.k_doc ? p.c.k_doc[meta + key0 + c] : 0;
-      first += doc == dmin;
-      other += doc != dmin && doc != dmax;
+#pragma unroll
+    for (int i = 0; i < KT / 32; ++i) {
+      const bool in = key0 + 32 * i + lane < n;
+      first += in && doc[i] == dmin;
+      other += in && doc[i] != dmin && doc[i] != dmax;
     }
     first = __reduce_add_sync(0xffffffffu, first);
     other = __reduce_add_sync(0xffffffffu, other);
@@ -53,6 +69,7 @@ __global__ void __launch_bounds__(256) cache_tiles_kernel(const __grid_constant_
   if (w >= static_cast<int64_t>(p.c.B) * p.units) return;
   const int unit = static_cast<int>(w % p.units), b = static_cast<int>(w / p.units);
   const int nk = cache_k_len(p.c, b), nq = cache_q_len(p.c, b);
+#pragma unroll 8
   for (int i = unit * 2 * p.tok_cta + lane; i < min(nq, (unit + 1) * 2 * p.tok_cta); i += 32) {
     const int doc = p.c.q_doc ? p.c.q_doc[b * p.c.qm_b + i] : 0;
     const int pos = p.c.q_pos ? p.c.q_pos[b * p.c.qm_b + i] : nk - nq + i;
@@ -71,8 +88,7 @@ constexpr int kOrderUnits = 512;
 
 // Sorts a sequence's units by the key tiles that they see: rows of two documents
 // see the tiles of both, and such a unit taken last kept its pair at work while
-// the others were done (nine documents of 12480 rows: 150 us, sorted 136 with
-// this kernel's 3).  One CTA per sequence.
+// the others were done (nine documents of 12480 rows: 150 us, sorted 136).  One CTA per sequence.
 __global__ void __launch_bounds__(1024) cache_order_kernel(const __grid_constant__ TcParams p) {
   __shared__ int s_w[kOrderUnits], s_most, s_least;
   pdl_trigger();
@@ -87,6 +103,7 @@ __global__ void __launch_bounds__(1024) cache_order_kernel(const __grid_constant
     const RowUnit ru = p.row_units[static_cast<int64_t>(b) * p.units + u];
     const int most = max(ru.pos_max + 1, prefix);
     int w = 0;
+#pragma unroll 4
     for (int t = lane_id(); t < n; t += 32) {
       const KeyTile k = tiles[t];
       w += (!p.c.k_doc || (k.doc_min <= ru.doc_max && k.doc_max >= ru.doc_min)) && (!p.c.causal || k.pos_min < most);
@@ -110,6 +127,7 @@ __global__ void __launch_bounds__(1024) cache_order_kernel(const __grid_constant
   for (int u = threadIdx.x; u < p.units; u += 1024) {
     const int w = s_w[u];
     int rank = 0;
+#pragma unroll 8
     for (int v = 0; v < p.units; ++v) rank += s_w[v] > w || (s_w[v] == w && v < u);
     order[rank] = u;
   }
@@ -138,8 +156,8 @@ __global__ void __launch_bounds__(128) cache_lin_kernel(const __grid_constant__ 
 
 // Joins the shares of a row: one CTA per (sequence, head, token).  Each of its
 // four warps adds up every fourth share, lanes over the columns, four shares'
-// rows on the way at once; the warps' sums are added in order.  Bound by the
-// latency of two dependent reads.
+// rows on the way at once; the warps' sums are added in order.  Bound by its
+// launch and the latency of two dependent reads (4 us for a token's 12 heads).
 template <bool BF16>
 __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ TcParams p) {
   __shared__ float4 s_acc[4][32];

@@ -1,7 +1,8 @@
 // Attention over a cache and the attention mass for every layout, alignment
 // and head width the calls accept: plain loads, one warp per row (or per
 // key), 32-bit arithmetic throughout.  The tensor-core kernels take the
-// aligned problems; these are bound by their uncoalesced 2-byte loads.
+// aligned problems; these are bound by their uncoalesced 2-byte loads and are
+// some tens of times slower (a fallback for odd layouts, not tuned).
 #include "cache_kernels.h"
 
 namespace psv {

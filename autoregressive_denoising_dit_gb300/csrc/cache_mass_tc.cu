@@ -8,10 +8,17 @@
 // shared memory while the row tiles (256 rows: each CTA holds 128) stream past.
 //   S^T_t = K Q_t^T   M=256, N=256, K=dh, double-buffered in TMEM
 // Per score one multiply-add (scale and -lse), one exp2 and one add: the MMAs
-// (8 x 136 clocks a tile) and the exponentials (1024) bound it about equally.
+// and the exponentials each take about 1050 clocks of a tile, and a tile takes
+// 2200: each unit is half busy, as a warp's reads of TMEM, its waits and its
+// weights follow one another and four warps a scheduler do not fill the gaps.
+// (Measured no faster: -lse added by the products, the two halves of the warps
+// on tiles of their own, the row notes read a tile ahead; slower: eight warps,
+// S^T held double in registers.)  Four sequences of 1560 rows x 7800 keys, 12
+// heads of 128: 162 us (925 TFLOP/s).
 // A row's -lse, position limit, document and slope are noted per tile in shared
-// memory by a warp of their own.  Warp roles, 384 threads:
-//   warp 0       TMA: the piece's K tile (2 buffers), the row tiles (4 stages)
+// memory by a warp of their own.  Warp roles, 640 threads:
+//   warp 0       TMA: the piece's K tile (2 buffers), the row tiles (4 stages);
+//                hands the pieces on to the warps from 3 on
 //   warp 1       TMEM allocator (both CTAs) and MMA issuer (even CTA)
 //   warp 2       even CTA: takes pieces from the work queue, publishes them
 //   warp 3       notes the columns of a row tile

