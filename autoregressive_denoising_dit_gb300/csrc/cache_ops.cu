@@ -554,7 +554,27 @@ __global__ void __launch_bounds__(kRegThreads) evict_select_kernel(const EvictPa
     }
   }
   __syncthreads();
-  for (int a = t; a < keep; a += kRegThreads) keep_slot(p, mass[kept[a]], row, meta, a, kept[a]);
+  for (int a0 = t; a0 < keep; a0 += 4 * kRegThreads) {  // four reads on their way at once
+    int j[4], pos[4], doc[4];
+    float w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (a0 + k * kRegThreads >= keep) break;
+      j[k] = kept[a0 + k * kRegThreads];
+      w[k] = mass[j[k]];
+      pos[k] = p.pos_out && p.k_pos ? p.k_pos[meta + j[k]] : j[k];
+      doc[k] = p.doc_out ? p.k_doc[meta + j[k]] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int a = a0 + k * kRegThreads;
+      if (a >= keep) break;
+      p.idx[row + a] = j[k];
+      p.mass_out[row + a] = w[k];
+      if (p.pos_out) p.pos_out[row + a] = pos[k];
+      if (p.doc_out) p.doc_out[row + a] = doc[k];
+    }
+  }
   if (h == 0 && t == 0 && p.lens_out) p.lens_out[b] = keep;
 }
 
@@ -652,7 +672,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const Ev
 // or one value) of an out row and then the next head; a thread takes kRows such
 // rows, a grid apart, with all their loads on the way at once.  Memory-bound:
 // with the selection before it 23 us for 4680 of 7800 slots of 12 heads of 128
-// (58 MB), 336 us for eight sequences of 40 heads (2 GB, 5.9 TB/s).
+// (58 MB), 330 us for eight sequences of 40 heads (2 GB, 6.0 TB/s).
 template <class U, int kRows>
 __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p, uint32_t units, int esize, uint32_t step) {
   const uint32_t t = blockIdx.x * 256 + threadIdx.x, H = p.H;
