@@ -228,6 +228,9 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
 // part's 152 SMs; a constant, so that the bits do not depend on the device).
 constexpr int kPlanPairs = 76;
 
+// Counters in the workspace's head: the ints from kJoinFirst on.
+constexpr int kJoinFirst = 16, kJoinCounters = PSV_CACHE_SCRATCH_HEAD / 4 - kJoinFirst, kJoinShares = 32, kJoinRows = 4;
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct TcLayout {
@@ -451,13 +454,31 @@ cudaError_t cattn::launch_order(const TcParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, cache_order_kernel, p);
 }
 
+namespace {
+
+// Whether the few-row kernel joins the shares itself (to the same bits).  That
+// saves a launch, which is what a short call costs: a token over 1560 keys of 12
+// heads 8.4 us against 10.9, over 3120 9.1 against 10.5.  But one CTA joins a
+// head's shares after the last of them: no gain from 24 MB of keys and values on
+// (7800 keys 14.4 against 13.7), and a loss with more rows (16 rows 14.6 against
+// 10.3) or several pieces a CTA (three tokens 19.1 against 13.0).
+bool joins_within(const TcParams& p, int sms) {
+  const int64_t bytes = static_cast<int64_t>(p.c.B) * p.c.Hkv * p.c.Lk * p.c.dh * 4;
+  return p.nsplit > 1 && p.nsplit <= kJoinShares && p.c.B * p.c.Hkv <= kJoinCounters && p.n_pieces <= sms &&
+         p.c.Lq * p.c.G <= kJoinRows && bytes <= (24 << 20);
+}
+
+}  // namespace
+
 cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scratch, int sms, cudaStream_t st) {
   const TcParams p = plan(c, scratch);
   cudaError_t e;
   if (static_cast<int64_t>(c.Lq) * c.G <= kFewRows) {
-    const RowsParams r{c, p.nsplit, p.part_rows, p.n_pieces, sms, p.part_o, p.part_ml};
+    const bool within = joins_within(p, sms);
+    const RowsParams r{c, p.nsplit, p.part_rows, p.n_pieces, sms, p.part_o, p.part_ml,
+                       within ? reinterpret_cast<int*>(scratch) + kJoinFirst : nullptr};
     e = launch_cache_rows(r, bf16, false, st);
-    return e != cudaSuccess || p.nsplit == 1 ? e : launch_join(p, bf16, st);
+    return e != cudaSuccess || p.nsplit == 1 || within ? e : launch_join(p, bf16, st);
   }
   CUtensorMap maps[4];
   if (!encode_maps(maps, c, p, bf16, true)) return cudaErrorInvalidValue;

@@ -55,6 +55,7 @@ struct RowsParams {
   int n_pieces, ctas;  // pieces: sequences x kv heads x shares; CTAs at most
   float* part_o;
   float2* part_ml;
+  int* joined;  // [sequences x kv heads] shares done, zero between calls; null: another kernel joins them
 };
 cudaError_t launch_cache_rows(const RowsParams& p, bool bf16, bool mass, cudaStream_t st);
 

@@ -586,7 +586,7 @@ cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, char* scratch,
     int64_t n = (8 * static_cast<int64_t>(sms) + heads - 1) / heads;
     if (n > most) n = most;
     if (n > 304) n = 304;
-    const RowsParams r{c, static_cast<int>(n), 0, static_cast<int>(heads * n), sms, nullptr, nullptr};
+    const RowsParams r{c, static_cast<int>(n), 0, static_cast<int>(heads * n), sms, nullptr, nullptr, nullptr};
     return launch_cache_rows(r, bf16, true, st);
   }
   TcParams p = plan(c, scratch);

@@ -9,8 +9,8 @@
 // consumer warps keeps its own running maximum, sum and output over every
 // seventh tile of a piece (the chain from a tile's scores to its weights takes
 // about 1 us, so fewer warps would bound it, not the memory).  The seven are
-// joined in shared memory at the end of a piece, the shares by
-// cache_join_kernel.  The next piece's queries are read while the current one
+// joined in shared memory at the end of a piece, the shares by the CTA that
+// ends the last of them, or where there are many by cache_join_kernel.  The next piece's queries are read while the current one
 // runs.  Measured, heads of 128: eight single tokens over 7800 keys of 12 heads
 // 58.9 us with the join (5.4 TB/s; the pieces are 8% uneven over the SMs), one
 // token over 65536 keys 61.5 us (6.5 TB/s), the mass of eight tokens 31.9 us.
@@ -180,6 +180,57 @@ struct Work {
 __device__ __forceinline__ int mass_key(int lane) {
   const int k = lane >> 2;  // bit 2 (lane 16): n's upper bit, bit 1 (8): n's lower bit, bit 0 (4): x
   return 8 * (k >> 1) + 2 * (lane % 4) + (k & 1);
+}
+
+// Joins the shares of a (sequence, kv head) by all consumers: every fourth share
+// added up in order, then the four sums, as cache_join_kernel does, so that the
+// bits are the same.
+template <int DH, bool BF16>
+__device__ __forceinline__ void join_shares(const RowsParams& p, int b, int kvh, int rows) {
+  const CacheParams& c = p.c;
+  const int64_t first = (static_cast<int64_t>(b) * c.Hkv + kvh) * p.nsplit;
+  for (int u = threadIdx.x; u < rows * (DH / 4); u += kWarps * 32) {
+    const int r = u / (DH / 4), d = u % (DH / 4) * 4;
+    const float2* ml = p.part_ml + first * p.part_rows + r;
+    const float* part = p.part_o + (first * p.part_rows + r) * DH + d;
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, __ldcg(ml + s * p.part_rows).x);
+    const float m0 = m == -INFINITY ? 0.0f : m;
+    float4 acc[4];
+    float l[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) acc[w] = make_float4(0.f, 0.f, 0.f, 0.f), l[w] = 0.0f;
+#pragma unroll 2
+    for (int s0 = 0; s0 < p.nsplit; s0 += 4) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int s = s0 + w;
+        const float2 x = s < p.nsplit ? __ldcg(ml + s * p.part_rows) : make_float2(-INFINITY, 0.0f);
+        const float4 y = s < p.nsplit ? __ldcg(reinterpret_cast<const float4*>(part + static_cast<int64_t>(s) * p.part_rows * DH))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float f = fast_exp2(x.x - m0);
+        l[w] = fmaf(f, x.y, l[w]);
+        acc[w].x = fmaf(f, y.x, acc[w].x);
+        acc[w].y = fmaf(f, y.y, acc[w].y);
+        acc[w].z = fmaf(f, y.z, acc[w].z);
+        acc[w].w = fmaf(f, y.w, acc[w].w);
+      }
+    }
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      acc[0].x += acc[w].x, acc[0].y += acc[w].y, acc[0].z += acc[w].z, acc[0].w += acc[w].w;
+      l[0] += l[w];
+    }
+    const float inv = l[0] > 0.0f ? 1.0f / l[0] : 0.0f;
+    const int tok = r / c.G, head = kvh * c.G + r % c.G;
+    if (d < c.dh)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.o) + b * c.os.b + tok * c.os.l + head * c.os.h + d) =
+          make_uint2(pack2<BF16>(acc[0].x * inv, acc[0].y * inv), pack2<BF16>(acc[0].z * inv, acc[0].w * inv));
+    if (d == 0 && c.lse)
+      c.lse[(static_cast<int64_t>(b) * c.Hq + head) * c.Lq + tok] =
+          l[0] > 0.0f ? (m + fast_log2(l[0])) * kLn2 : -INFINITY;
+  }
 }
 
 template <int DH, bool BF16, bool MASS>
@@ -477,6 +528,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (d == 0 && c.lse)
             c.lse[(static_cast<int64_t>(w.b) * c.Hq + head) * c.Lq + tok] =
                 ll > 0.0f ? (mm + fast_log2(ll)) * kLn2 : -INFINITY;
+        }
+      }
+      if (p.joined) {
+        // The last share of a (sequence, kv head) to be done joins them all, in
+        // their order.
+        __threadfence();
+        asm volatile("bar.sync 1, 224;" ::: "memory");
+        const int bh = w.b * c.Hkv + w.kvh;
+        int last = 0;
+        if (threadIdx.x == 0) {
+          last = atomicAdd(p.joined + bh, 1) == p.nsplit - 1;
+          if (last) atomicExch(p.joined + bh, 0);
+        }
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %0, 0;\n\t"
+            "barrier.cta.red.or.pred q, 1, 224, p;\n\t"
+            "selp.b32 %0, 1, 0, q;\n\t}"
+            : "+r"(last)::"memory");
+        if (last) {
+          __threadfence();
+          join_shares<DH, BF16>(p, w.b, w.kvh, rows);
         }
       }
       __syncwarp();

@@ -429,6 +429,21 @@ def test_attention_repeats_and_is_batch_invariant(P):
     assert torch.equal(o[0], a[2]) and torch.equal(lse[0], la[2])
 
 
+@pytest.mark.parametrize("Lq,G,dh", [(1, 1, 128), (3, 5, 64), (4, 2, 80)])
+def test_tokens_alone_and_in_a_batch(P, Lq, G, dh):
+    """Few rows: the shares of one sequence's few heads are joined elsewhere than those of many, to the same bits."""
+    B, H = 12, 6
+    c = make(B=B, Lq=Lq, Lk=2500, Hq=H * G, Hkv=H, dh=dh, k_lens=[2500 - 190 * b for b in range(B)], slopes=True)
+    o, lse = run_attention(P, c)
+    check_attention(c, o, lse)
+    s, n = scratch_for(P, problem(P, c))
+    for b in (0, 5, 11):
+        one = dict(c, B=1, q=c["q"][b:b + 1], k=c["k"][b:b + 1], v=c["v"][b:b + 1], k_lens=c["k_lens"][b:b + 1].clone())
+        for _ in range(3):  # one workspace for all of them
+            a, la = run_attention(P, one, scratch=s)
+            assert torch.equal(a[0], o[b]) and torch.equal(la[0], lse[b])
+
+
 @pytest.mark.parametrize("kw", [
     dict(Lq=4400, Lk=8800, Hq=24, Hkv=8, dh=128, causal=True, prefix=[880], cap=50.0, dtype="f16"),
     dict(B=9, Lq=3, Lk=40, Hq=12, Hkv=12, dh=64, k_lens=[40, 1, 0, 7, 33, 39, 12, 40, 3]),
