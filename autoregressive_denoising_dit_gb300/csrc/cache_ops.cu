@@ -273,9 +273,9 @@ uint64_t fixed_turns(double f) {
   const double e = std::fma(f, hi, -t) + f * lo;
   const double fr = t - std::floor(t);
   // fr < 1 holds 53 bits; the remainder e adds the bits behind them.
-  const double scaled = std::ldexp(fr, 64);
+  const double scaled = fr * 0x1p64;
   const uint64_t base = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
-  return base + static_cast<uint64_t>(static_cast<int64_t>(std::ldexp(e, 64)));
+  return base + static_cast<uint64_t>(static_cast<int64_t>(e * 0x1p64));
 }
 
 template <class T, bool HALVES>
