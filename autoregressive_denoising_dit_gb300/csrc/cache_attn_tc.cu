@@ -163,35 +163,38 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   __shared__ float4 s_acc[4][32];
   __shared__ float s_l[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;  // (b, tok, head)
+  const int64_t row = blockIdx.x;  // (b, tok, head), of the last unit's tokens only if only that was shared
+  const int tok0 = p.tail_split ? (p.units - 1) * 2 * p.tok_cta : 0, toks = p.c.Lq - tok0;
   const int head = static_cast<int>(row % p.c.Hq);
-  const int tok = static_cast<int>(row / p.c.Hq % p.c.Lq);
-  const int b = static_cast<int>(row / p.c.Hq / p.c.Lq);
+  const int tok = tok0 + static_cast<int>(row / p.c.Hq % toks);
+  const int b = static_cast<int>(row / p.c.Hq / toks);
   const int kvh = head / p.c.G, unit = tok / (2 * p.tok_cta);
   const int in_unit = tok - unit * 2 * p.tok_cta;
   const int prow = in_unit * p.c.G + head % p.c.G;  // both CTAs' rows in a row
-  const int64_t first = ((static_cast<int64_t>(b) * p.c.Hkv + kvh) * p.units + unit) * p.nsplit;
+  const int nsplit = p.tail_split ? p.tail_split : p.nsplit;
+  const int64_t bh = static_cast<int64_t>(b) * p.c.Hkv + kvh;
+  const int64_t first = (p.tail_split ? bh : bh * p.units + unit) * nsplit;
   const float2* ml = p.part_ml + first * p.part_rows + prow;
   const float* part = p.part_o + (first * p.part_rows + prow) * p.width + lane * 4;
   const int64_t step = p.part_rows;  // rows from one share to the next
   pdl_wait();
   if (tok >= cache_q_len(p.c, b)) return;
   float m = -INFINITY;
-  for (int s = lane; s < p.nsplit; s += 32) m = fmaxf(m, ml[s * step].x);
+  for (int s = lane; s < nsplit; s += 32) m = fmaxf(m, ml[s * step].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float m0 = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool in = lane * 4 < p.width;
-  for (int s0 = warp; s0 < p.nsplit; s0 += 16) {
+  for (int s0 = warp; s0 < nsplit; s0 += 16) {
     float2 w[4];
     float4 x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int s = s0 + 4 * k;
-      w[k] = s < p.nsplit ? ml[s * step] : make_float2(-INFINITY, 0.0f);
-      x[k] = s < p.nsplit && in ? *reinterpret_cast<const float4*>(part + s * step * p.width)
+      w[k] = s < nsplit ? ml[s * step] : make_float2(-INFINITY, 0.0f);
+      x[k] = s < nsplit && in ? *reinterpret_cast<const float4*>(part + s * step * p.width)
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
@@ -231,11 +234,14 @@ constexpr int kPlanPairs = 76;
 // Counters in the workspace's head: the ints from kJoinFirst on.
 constexpr int kJoinFirst = 16, kJoinCounters = PSV_CACHE_SCRATCH_HEAD / 4 - kJoinFirst, kJoinShares = 32, kJoinRows = 4;
 
+// Shares of a last unit of few rows.
+constexpr int kTailShares = 4;
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct TcLayout {
   bool few;  // at most kFewRows rows per kv head
-  int width, rows_cta, tok_cta, units, nsplit, part_rows;
+  int width, rows_cta, tok_cta, units, nsplit, tail_split, part_rows;
   int64_t pieces;
   int tiles, meta_heads;  // of the buffer; 0: no positions or documents
   bool lin;  // the distance bias by products (no cap, no positions or documents given)
@@ -263,12 +269,29 @@ TcLayout tc_layout(const CacheParams& c) {
   t.nsplit = static_cast<int>(want < tiles ? want : tiles);
   if (t.nsplit < 1) t.nsplit = 1;
   t.pieces = static_cast<int64_t>(c.B) * per_seq * t.nsplit;
+  int64_t parts = t.nsplit > 1 ? t.pieces : 0;
+  // Units of equal length leave the pairs of SMs uneven, up to a whole unit's time.
+  // A last unit of few rows takes as long as any other, and its shares leave little
+  // to join: taken last they even the pairs out.  (Causal units and those of
+  // documents differ in length, longest first.)  1560 rows x 7800 keys of 12 heads:
+  // one sequence 94 -> 66 us, two 137 -> 119, four 225 -> 211; eight 422 -> 430, as
+  // their keys come from memory again, but a sequence's shares must not depend on
+  // the batch.  From two rounds of units a sequence on little is left to gain, and
+  // more rows would leave as much to join.
+  const int64_t tail_rows = rows - static_cast<int64_t>(t.units - 1) * 2 * t.rows_cta;
+  if (t.nsplit == 1 && !t.few && t.units > 1 && per_seq <= 2 * kPlanPairs && !c.causal && !c.k_doc && tail_rows <= t.rows_cta / 2 &&
+      (c.Lk + KT - 1) / KT >= 4 * kTailShares) {
+    t.tail_split = kTailShares;
+    parts = static_cast<int64_t>(c.B) * c.Hkv * kTailShares;
+    t.pieces += parts - static_cast<int64_t>(c.B) * c.Hkv;
+    t.part_rows = static_cast<int>(tail_rows);
+  }
   size_t off = PSV_CACHE_SCRATCH_HEAD;
-  if (t.nsplit > 1) {
+  if (parts > 0) {
     t.part_o = off;
-    off += up256(static_cast<size_t>(t.pieces) * t.part_rows * t.width * 4);
+    off += up256(static_cast<size_t>(parts) * t.part_rows * t.width * 4);
     t.part_ml = off;
-    off += up256(static_cast<size_t>(t.pieces) * t.part_rows * 8);
+    off += up256(static_cast<size_t>(parts) * t.part_rows * 8);
   }
   t.tiles = (c.Lk + KT - 1) / KT;
   t.meta_heads = !t.few && (c.k_pos || c.k_doc) ? (c.km_h == 0 ? 1 : c.Hkv) : 0;
@@ -361,7 +384,8 @@ cudaError_t launch_lin(const TcParams& p, bool bf16, cudaStream_t st) {
 }
 
 cudaError_t launch_join(const TcParams& p, bool bf16, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Lq * p.c.Hq;
+  const int toks = p.tail_split ? p.c.Lq - (p.units - 1) * 2 * p.tok_cta : p.c.Lq;
+  const int64_t rows = static_cast<int64_t>(p.c.B) * toks * p.c.Hq;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -381,6 +405,7 @@ TcParams cattn::plan(const CacheParams& c, char* scratch) {
   TcParams p{};
   p.c = c;
   p.rows_cta = t.rows_cta, p.tok_cta = t.tok_cta, p.units = t.units, p.nsplit = t.nsplit;
+  p.tail_split = t.tail_split;
   p.n_pieces = static_cast<int>(t.pieces), p.part_rows = t.part_rows, p.width = t.width;
   p.meta_vec = ((reinterpret_cast<uintptr_t>(c.k_pos) | reinterpret_cast<uintptr_t>(c.k_doc)) & 15) == 0 &&
                c.km_b % 4 == 0 && c.km_h % 4 == 0;
@@ -496,7 +521,7 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
     e = bf16 ? launch_features<64, true>(maps, p, f, pairs, st) : launch_features<64, false>(maps, p, f, pairs, st);
   else
     e = bf16 ? launch_features<128, true>(maps, p, f, pairs, st) : launch_features<128, false>(maps, p, f, pairs, st);
-  return e != cudaSuccess || p.nsplit == 1 ? e : launch_join(p, bf16, st);
+  return e != cudaSuccess || (p.nsplit == 1 && !p.tail_split) ? e : launch_join(p, bf16, st);
 }
 
 bool cache_mass_tc(const CacheParams& c) {

@@ -33,9 +33,9 @@
 // piece's notes); issuing the next piece's first S ahead of the last P.V was
 // measured slower (short sequences 80 -> 84 us).
 // Measured, 12 heads of 128, bf16: 12480 rows x 12480 keys 582 us (1640 TFLOP/s),
-// four sequences of 1560 rows x 7800 keys 222 us (1345; 13% of its row tiles are
-// empty), with the distance bias 242, with the cap 306; nine documents of 12480
-// rows 135 us.
+// four sequences of 1560 rows x 7800 keys 211 us (1415; 13% of its row tiles are
+// empty), with the distance bias 226, with the cap 291; nine documents of 12480
+// rows 131 us.
 // Pieces are taken from a device counter (the first of a pair is its own
 // index) that the last pair to finish rewinds.  Shares of a long cache leave
 // O, m and l in a workspace and a second small kernel joins them in a fixed
@@ -310,7 +310,8 @@ struct TcParams {
   int rows_cta;     // packed rows of a CTA: a multiple of G
   int tok_cta;      // tokens of a CTA: rows_cta / G
   int units;        // units of 2 * tok_cta tokens per (sequence, kv head)
-  int nsplit;
+  int nsplit;       // shares of every unit's keys
+  int tail_split;   // shares of the last unit's keys, where only those are shared; or 0
   int n_pieces;
   int part_rows;    // rows of a unit in the workspace
   int width;        // columns of a row there (the kernel's DH)
@@ -371,6 +372,11 @@ struct Piece {
 
 __device__ __forceinline__ int4 piece_index(const TcParams& p, int k) {
   const int BH = p.c.B * p.c.Hkv;
+  if (p.tail_split) {
+    // The last units' shares come last.
+    const int whole = p.units - 1, t = k - BH * whole;
+    return t < 0 ? make_int4(k / whole, k % whole, 0, 0) : make_int4(t / p.tail_split, whole, t % p.tail_split, 0);
+  }
   const int s = k % p.nsplit, r = k / p.nsplit;
   if (p.unit_order) {
     const int per_seq = p.c.Hkv * p.units, b = r / per_seq, q = r % per_seq;
@@ -385,6 +391,11 @@ __device__ __forceinline__ int4 piece_index(const TcParams& p, int k) {
   // share its keys in L2.
   if (p.c.causal) return make_int4(r % BH, p.units - 1 - r / BH, s, 0);
   return make_int4(r / p.units, r % p.units, s, 0);
+}
+
+// Into how many shares a unit's keys are divided.
+__device__ __forceinline__ int unit_shares(const TcParams& p, int unit) {
+  return p.tail_split && unit == p.units - 1 ? p.tail_split : p.nsplit;
 }
 
 // Keys [0, limit) hold every key that some row of the unit sees.
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int whole = 0, count = 0;
           if (rows && p.key_tiles) seen_tiles(p, b, pc.a.x % p.c.Hkv, pc.a.y, first, last, whole, count);
           // (At most 2^20 tiles and 76 shares.)
-          const uint32_t nt = static_cast<uint32_t>(last - first), n = static_cast<uint32_t>(p.nsplit);
+          const uint32_t nt = static_cast<uint32_t>(last - first), n = static_cast<uint32_t>(unit_shares(p, pc.a.y));
           const int t0 = static_cast<int>(nt * static_cast<uint32_t>(pc.a.z) / n);
           const int t1 = static_cast<int>(nt * static_cast<uint32_t>(pc.a.z + 1) / n);
           pc.b = make_int4(nk, nq, first + t0, t1 - t0);
@@ -1115,8 +1126,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lo = __shfl_xor_sync(0xffffffffu, l, 16);
       l = hk16 == 0 ? l + lo : lo + l;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      const bool split = p.nsplit > 1;
-      const int64_t piece = (static_cast<int64_t>(pa.x) * p.units + pa.y) * p.nsplit + (pa.z & 127);
+      const int shares = unit_shares(p, pa.y);
+      const bool split = shares > 1;
+      const int64_t piece =
+          (p.tail_split ? static_cast<int64_t>(pa.x) : static_cast<int64_t>(pa.x) * p.units + pa.y) * shares + (pa.z & 127);
       const int64_t prow = piece * p.part_rows + rank * p.rows_cta + r;
       char* row = split ? reinterpret_cast<char*>(p.part_o + prow * DH)
                         : reinterpret_cast<char*>(static_cast<uint16_t*>(p.c.o) + b * p.c.os.b + tok * p.c.os.l + head * p.c.os.h);

@@ -429,6 +429,24 @@ def test_attention_repeats_and_is_batch_invariant(P):
     assert torch.equal(o[0], a[2]) and torch.equal(lse[0], la[2])
 
 
+@pytest.mark.parametrize("kw", [
+    dict(Lq=300, Hq=20, Hkv=20, dh=32),
+    dict(Lq=270, Hq=20, Hkv=20, dh=64, slopes=True, dtype="f16", q_lens=[270, 257, 256, 3]),
+    dict(Lq=100, Hq=60, Hkv=20, dh=48, cap=20.0),
+    dict(Lq=257, Hq=20, Hkv=20, dh=32, causal=False, k_pos=np.broadcast_to((np.arange(4300) + 999) % 4300, (4, 4300)), slopes=True),
+], ids=["plain", "bias", "groups-cap", "ring"])
+def test_attention_last_unit_in_shares(P, kw):
+    """A last unit of few rows is done in shares of the keys (also empty ones), the same alone as in a batch."""
+    n = [4300, 4100, 700, 0]
+    c = make(B=4, Lk=4300, k_lens=n, **kw)
+    o, lse = run_attention(P, c)
+    check_attention(c, o, lse)
+    for b in (1, 2):
+        one = dict(c, B=1, **{x: c[x][b:b + 1].clone() for x in ("q", "k", "v", "k_lens", "q_lens", "k_pos") if c[x] is not None})
+        a, la = run_attention(P, one)
+        assert torch.equal(a[0], o[b]) and torch.equal(la[0], lse[b])
+
+
 @pytest.mark.parametrize("Lq,G,dh", [(1, 1, 128), (3, 5, 64), (4, 2, 80)])
 def test_tokens_alone_and_in_a_batch(P, Lq, G, dh):
     """Few rows: the shares of one sequence's few heads are joined elsewhere than those of many, to the same bits."""
