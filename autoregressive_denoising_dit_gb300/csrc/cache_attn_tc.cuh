@@ -27,7 +27,7 @@
 //                keys each, through 16-lane TMEM accesses
 // The softmax paces a tile, not the tensor cores: 2500 clocks against 2048 of
 // products (of a tile's clocks, 570 go into the maximum, 1650 into the weights
-// and their way to TMEM), and so do whatever a feature adds to it: the cap 1400
+// and their way to TMEM), and so does what a feature adds to it: the cap 1400
 // clocks (four packed FMA-pipe operations a pair), masks seen key by key 1200.
 // Between pieces 3000 clocks are lost (the last P.V, O's way out, the next
 // piece's notes); issuing the next piece's first S ahead of the last P.V was
