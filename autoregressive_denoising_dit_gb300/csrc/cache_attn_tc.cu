@@ -274,7 +274,7 @@ TcLayout tc_layout(const CacheParams& c) {
   // A last unit of few rows takes as long as any other, and its shares leave little
   // to join: taken last they even the pairs out.  (Causal units and those of
   // documents differ in length, longest first.)  1560 rows x 7800 keys of 12 heads:
-  // one sequence 94 -> 66 us, two 137 -> 119, four 225 -> 211; eight 422 -> 430, as
+  // one sequence 94 -> 66 us, two 137 -> 111, four 225 -> 212; eight 422 -> 430, as
   // their keys come from memory again, but a sequence's shares must not depend on
   // the batch.  From two rounds of units a sequence on little is left to gain, and
   // more rows would leave as much to join.
