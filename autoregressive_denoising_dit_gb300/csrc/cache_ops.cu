@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "../../include/psv.h"
 #include "cache_kernels.h"
@@ -64,6 +65,14 @@ int check_device(int dev, const void* ptr, const char* name) {
   if (a.type == cudaMemoryTypeDevice && a.device != dev)
     return cache_fail(PSV_EINVAL, "%s is on device %d, the current device is %d", name, a.device, dev);
   return PSV_OK;
+}
+
+// Whether every one of these pointers (null ones too) is on four bytes, as the
+// kernels read and write ints and floats there one by one.
+bool on4(std::initializer_list<const void*> ptrs) {
+  uintptr_t at = 0;
+  for (const void* p : ptrs) at |= reinterpret_cast<uintptr_t>(p);
+  return (at & 3) == 0;
 }
 
 bool stride_ok(const int64_t* s, int n) {
@@ -341,8 +350,7 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   for (int i = 0; i < 3; ++i) same = same && p->x_stride[i] == p->out_stride[i];
   if (!same && x == out) return cache_fail(PSV_EINVAL, "in place needs equal strides");
   const uintptr_t mask = static_cast<uintptr_t>(size - 1);
-  if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(out) & mask) ||
-      (reinterpret_cast<uintptr_t>(pos) & 3))
+  if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(out) & mask) || !on4({pos, p->lens}))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
   int dev = 0;
   if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
@@ -768,7 +776,7 @@ PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const voi
   const void* typed[4] = {k, v, k_out, v_out};
   for (const void* x : typed)
     if (reinterpret_cast<uintptr_t>(x) & (size - 1)) return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
-  if ((reinterpret_cast<uintptr_t>(mass) | reinterpret_cast<uintptr_t>(mass_out) | reinterpret_cast<uintptr_t>(idx_out)) & 3)
+  if (!on4({mass, mass_out, idx_out, p->k_lens, p->k_pos, p->k_doc, p->pos_out, p->doc_out, p->lens_out}))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
   const int64_t in_k = extent(p->k_stride, p->B, p->L, p->Hkv, p->dh) * size;
   const int64_t in_v = extent(p->v_stride, p->B, p->L, p->Hkv, p->dh) * size;
@@ -825,6 +833,8 @@ int check_cache(const psv_cache_problem* p) {
   if (!stride_ok(p->q_stride, 3) || !stride_ok(p->k_stride, 3) || !stride_ok(p->v_stride, 3) ||
       !stride_ok(p->o_stride, 3) || !stride_ok(&p->q_meta_stride, 1) || !stride_ok(p->k_meta_stride, 2))
     return cache_fail(PSV_EINVAL, "strides must lie in [0, 2^40]");
+  if (!on4({p->q_lens, p->k_lens, p->q_pos, p->q_doc, p->k_pos, p->k_doc, p->prefix, p->slopes}))
+    return cache_fail(PSV_EINVAL, "lengths, positions, documents, prefixes and slopes must be aligned to 4 bytes");
   if (!p->k_doc != !p->q_doc) return cache_fail(PSV_EINVAL, "k_doc and q_doc come together");
   if (p->prefix && !p->causal) return cache_fail(PSV_EINVAL, "prefix needs causal");
   return PSV_OK;

@@ -376,7 +376,8 @@ int psv_attention_noalloc_status(int* status, void* cuda_stream);
  *     allocated and no host memory is read after the call returns, so a call
  *     can be captured into a CUDA graph;
  *   - lengths, positions, documents and prefixes are read on the device when
- *     the kernels run (a captured call sees their values at replay);
+ *     the kernels run (a captured call sees their values at replay); their
+ *     pointers, as every pointer, are aligned to their type;
  *   - errors: PSV_EINVAL (shapes, strides, alignment, null pointers; host
  *     memory, or another device's, as the first input or the first output),
  *     PSV_ECUDA; psv_cache_last_error() names the reason.  What other pointers

@@ -159,3 +159,19 @@ def test_descriptions_match_the_header():
     for line in out.splitlines():
         c, f, n = line.split()
         assert int(n) == (ctypes.sizeof(names[c]) if f == "size" else getattr(names[c], f).offset), line
+
+
+def test_metadata_off_four_bytes_is_refused():
+    """A kernel would fault on an int or a float off its alignment."""
+    for name in ("q_lens", "k_lens", "q_pos", "k_pos", "prefix", "slopes"):
+        p = changed(cache, causal=1, **{name: A + 2})
+        refused("aligned", P.psv_cache_scratch_bytes, p)
+        refused("aligned", P.psv_cache_attention, p, A, A, A, 2 * A, 0, 3 * A, 1 << 30)
+        refused("aligned", P.psv_cache_mass, p, A, A, A, 0, 2 * A, 3 * A, 1 << 30)
+    for kw in (dict(q_doc=A + 1, k_doc=A), dict(q_doc=A, k_doc=A + 2)):
+        refused("aligned", P.psv_cache_scratch_bytes, changed(cache, **kw))
+    refused("aligned", P.psv_rope, changed(rope, lens=A + 2), A, A, 2 * A)
+    for name in ("k_lens", "k_pos", "pos_out", "lens_out"):
+        refused("aligned", P.psv_cache_evict, changed(evict, **{name: 9 * A + 1}), *(A * k for k in range(1, 8)))
+    for kw in (dict(k_doc=9 * A + 2), dict(k_doc=9 * A, doc_out=8 * A + 2)):
+        refused("aligned", P.psv_cache_evict, changed(evict, **kw), *(A * k for k in range(1, 8)))
