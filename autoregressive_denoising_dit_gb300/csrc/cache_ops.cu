@@ -758,6 +758,8 @@ PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const voi
     return cache_fail(PSV_EINVAL, "need B, Hkv, L, dh >= 1");
   if (p->B > 65535 || static_cast<int64_t>(p->B) * p->Hkv > 0x7fffffff)
     return cache_fail(PSV_EINVAL, "too many sequences and heads");
+  // (The selection steps over the slots in 32 bits, by 1024 at a time and by shares.)
+  if (p->L > (1 << 30)) return cache_fail(PSV_EINVAL, "L %d: at most 2^30 slots", p->L);
   if (p->budget < 1 || p->budget > p->L) return cache_fail(PSV_EINVAL, "budget %d: 1 to L = %d", p->budget, p->L);
   if (p->sinks < 0 || p->recent < 0 || static_cast<int64_t>(p->sinks) + p->recent > p->budget)
     return cache_fail(PSV_EINVAL, "sinks %d + recent %d do not fit the budget %d", p->sinks, p->recent, p->budget);

@@ -501,8 +501,8 @@ int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, con
  * slots they came from, lens_out[b] = min(n, budget).  Rows behind lens_out
  * are left as they were.  pos_out without k_pos receives the slots.  Out
  * buffers must not overlap any input or one another.
- * Requirements: dtype F32, BF16 or F16; B, Hkv, L, budget >= 1; budget <= L;
- * 1 <= dh; sinks, recent >= 0, sinks + recent <= budget; B <= 65535 and budget
+ * Requirements: dtype F32, BF16 or F16; B, Hkv, budget >= 1; 1 <= L <= 2^30;
+ * budget <= L; 1 <= dh; sinks, recent >= 0, sinks + recent <= budget; B <= 65535 and budget
  * x Hkv x dh below 2^32; strides in [0, 2^40], rows of k_out and v_out
  * distinct; doc_out needs k_doc. */
 typedef struct psv_evict_problem {

@@ -175,3 +175,12 @@ def test_metadata_off_four_bytes_is_refused():
         refused("aligned", P.psv_cache_evict, changed(evict, **{name: 9 * A + 1}), *(A * k for k in range(1, 8)))
     for kw in (dict(k_doc=9 * A + 2), dict(k_doc=9 * A, doc_out=8 * A + 2)):
         refused("aligned", P.psv_cache_evict, changed(evict, **kw), *(A * k for k in range(1, 8)))
+
+
+def test_evict_refuses_more_slots_than_it_can_step_over():
+    """Within 1024 slots of 2^31 a 32-bit step passes the end of the numbers and never ends."""
+    def make(n):
+        return P.evict_problem(P.PSV_DTYPE_BF16, (1, n, 1, 1), 1)
+
+    for n in (2**31 - 1, 2**31 - 1024, 2**30 + 1):
+        refused("2^30", P.psv_cache_evict, make(n), *(k << 36 for k in range(1, 8)))
