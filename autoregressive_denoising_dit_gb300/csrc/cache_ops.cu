@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <initializer_list>
+#include <utility>
 
 #include "../../include/psv.h"
 #include "cache_kernels.h"
@@ -101,8 +102,66 @@ bool rows_distinct(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t
   return true;
 }
 
-int64_t extent(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t width) {
-  return s[0] * (n0 - 1) + s[1] * (n1 - 1) + s[2] * (n2 - 1) + width;
+// The bytes of a tensor: rows of `width` bytes, n[d] of them st[d] bytes apart
+// along each of three indexes.
+struct Area {
+  const char* at;
+  int64_t st[3], n[3], width;
+  const char* name;
+};
+
+Area tensor_area(const char* name, const void* at, const int64_t* s, int64_t n0, int64_t n1, int64_t n2,
+                 int64_t width, int size) {
+  return Area{static_cast<const char*>(at), {s[0] * size, s[1] * size, s[2] * size}, {n0, n1, n2}, width * size, name};
+}
+
+// A contiguous one (null: none).
+Area plain_area(const char* name, const void* at, int64_t bytes) {
+  return Area{static_cast<const char*>(at), {0, 0, 0}, {1, 1, 1}, at ? bytes : 0, name};
+}
+
+// Whether two areas, b `d` bytes behind a, may share a byte, from index `level`
+// on.  Where their strides agree and hold what lies inside them, only copies next
+// to each other can meet, so that tensors packed into one buffer are told apart;
+// where they do not agree the whole stretches count.
+bool areas_meet(const Area& a, const Area& b, int64_t d, int level) {
+  int64_t ea = a.width, eb = b.width;
+  for (int i = 2; i > level; --i) ea += a.st[i] * (a.n[i] - 1), eb += b.st[i] * (b.n[i] - 1);
+  if (level == 3) return d < ea && d + eb > 0;
+  const int64_t st = a.st[level], na = a.n[level], nb = b.n[level];
+  if (d >= ea + a.st[level] * (na - 1) || d + eb + b.st[level] * (nb - 1) <= 0) return false;
+  if (na == 1 && nb == 1) return areas_meet(a, b, d, level + 1);
+  if (st != b.st[level] || ea > st || eb > st) return true;
+  const int64_t k0 = d >= 0 ? d / st : -((-d + st - 1) / st);  // copy k of a starts at or before b's first
+  for (int64_t k = k0; k <= k0 + 1; ++k)
+    if (k > -nb && k < na && areas_meet(a, b, d - k * st, level + 1)) return true;
+  return false;
+}
+
+bool areas_meet(Area a, Area b) {
+  if (!a.width || !b.width) return false;
+  for (int i = 0; i < 3; ++i) {
+    if (a.st[i] == 0) a.n[i] = 1;  // (every copy the same)
+    if (b.st[i] == 0) b.n[i] = 1;
+    if (a.n[i] == 1) a.st[i] = b.n[i] == 1 ? 0 : b.st[i];  // an index of extent one is never stepped
+    if (b.n[i] == 1) b.st[i] = a.st[i];
+  }
+  for (Area* x : {&a, &b})  // the largest stride first
+    for (int i = 0; i < 3; ++i)
+      for (int j = i + 1; j < 3; ++j)
+        if (x->st[j] > x->st[i]) std::swap(x->st[i], x->st[j]), std::swap(x->n[i], x->n[j]);
+  return areas_meet(a, b, b.at - a.at, 0);
+}
+
+// Refuses outputs that meet an input or one another.
+int check_areas(std::initializer_list<Area> outs, std::initializer_list<Area> ins) {
+  for (const Area* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Area& i : ins)
+      if (areas_meet(*o, i)) return cache_fail(PSV_EINVAL, "%s overlaps %s", o->name, i.name);
+    for (const Area* p = outs.begin(); p != o; ++p)
+      if (areas_meet(*o, *p)) return cache_fail(PSV_EINVAL, "%s overlaps %s", o->name, p->name);
+  }
+  return PSV_OK;
 }
 
 bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
@@ -352,6 +411,12 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
   const uintptr_t mask = static_cast<uintptr_t>(size - 1);
   if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(out) & mask) || !on4({pos, p->lens}))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  const Area out_area = tensor_area("out", out, p->out_stride, p->B, p->L, p->H, p->dh, size);
+  const int64_t pos_st[3] = {p->pos_stride[0], p->pos_stride[1], 1};
+  if (int r = check_areas({out_area}, {same ? plain_area("x", nullptr, 0)
+                                            : tensor_area("x", x, p->x_stride, p->B, p->L, p->H, p->dh, size),
+                                       tensor_area("pos", pos, pos_st, p->B, p->L, 1, p->n_axes, 4)}))
+    return r;
   int dev = 0;
   if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
   if (int r = check_device(dev, x, "x")) return r;
@@ -780,15 +845,21 @@ PSV_API int psv_cache_evict(const psv_evict_problem* p, const void* k, const voi
     if (reinterpret_cast<uintptr_t>(x) & (size - 1)) return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
   if (!on4({mass, mass_out, idx_out, p->k_lens, p->k_pos, p->k_doc, p->pos_out, p->doc_out, p->lens_out}))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
-  const int64_t in_k = extent(p->k_stride, p->B, p->L, p->Hkv, p->dh) * size;
-  const int64_t in_v = extent(p->v_stride, p->B, p->L, p->Hkv, p->dh) * size;
-  const int64_t out_k = extent(p->k_out_stride, p->B, p->budget, p->Hkv, p->dh) * size;
-  const int64_t out_v = extent(p->v_out_stride, p->B, p->budget, p->Hkv, p->dh) * size;
-  const int64_t in_m = static_cast<int64_t>(p->B) * p->Hkv * p->L * 4;
-  const int64_t out_m = static_cast<int64_t>(p->B) * p->Hkv * p->budget * 4;
-  if (overlap(k, in_k, k_out, out_k) || overlap(v, in_v, v_out, out_v) || overlap(mass, in_m, mass_out, out_m))
-    return cache_fail(PSV_EINVAL, "out buffers must not overlap their inputs");
   if (k_out == v_out) return cache_fail(PSV_EINVAL, "k_out and v_out are the same buffer");
+  const int64_t in_rows = static_cast<int64_t>(p->B) * p->Hkv, meta_st[3] = {p->k_meta_stride[0], p->k_meta_stride[1], 1};
+  auto kept = [&](const char* name, const void* at) { return plain_area(name, at, in_rows * p->budget * 4); };
+  auto meta = [&](const char* name, const void* at) {
+    return at ? tensor_area(name, at, meta_st, p->B, p->Hkv, 1, p->L, 4) : plain_area(name, at, 0);
+  };
+  if (int r = check_areas({tensor_area("k_out", k_out, p->k_out_stride, p->B, p->budget, p->Hkv, p->dh, size),
+                           tensor_area("v_out", v_out, p->v_out_stride, p->B, p->budget, p->Hkv, p->dh, size),
+                           kept("mass_out", mass_out), kept("idx_out", idx_out), kept("pos_out", p->pos_out),
+                           kept("doc_out", p->doc_out), plain_area("lens_out", p->lens_out, p->B * int64_t{4})},
+                          {tensor_area("k", k, p->k_stride, p->B, p->L, p->Hkv, p->dh, size),
+                           tensor_area("v", v, p->v_stride, p->B, p->L, p->Hkv, p->dh, size),
+                           plain_area("mass", mass, in_rows * p->L * 4), plain_area("k_lens", p->k_lens, p->B * int64_t{4}),
+                           meta("k_pos", p->k_pos), meta("k_doc", p->k_doc)}))
+    return r;
   int dev = 0;
   if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
   if (int r = check_device(dev, k, "k")) return r;
@@ -891,6 +962,16 @@ PSV_API int psv_cache_attention(const psv_cache_problem* p, const void* q, const
                        reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(o);
   if ((at & 1) || (reinterpret_cast<uintptr_t>(lse) & 3))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  bool in_place = q == o;  // every row of q is read before the row of o is written
+  for (int i = 0; i < 3; ++i) in_place = in_place && p->q_stride[i] == p->o_stride[i];
+  const Area q_area = tensor_area("q", q, p->q_stride, p->B, p->Lq, p->Hq, p->dh, 2);
+  const Area none = plain_area("", nullptr, 0);
+  if (int r = check_areas(
+          {tensor_area("o", o, p->o_stride, p->B, p->Lq, p->Hq, p->dh, 2),
+           plain_area("lse", lse, static_cast<int64_t>(p->B) * p->Hq * p->Lq * 4)},
+          {in_place ? none : q_area, p->Lk ? tensor_area("k", k, p->k_stride, p->B, p->Lk, p->Hkv, p->dh, 2) : none,
+           p->Lk ? tensor_area("v", v, p->v_stride, p->B, p->Lk, p->Hkv, p->dh, 2) : none}))
+    return r;
   int dev = 0;
   if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
   if (int r = check_device(dev, q, "q")) return r;
@@ -921,6 +1002,12 @@ PSV_API int psv_cache_mass(const psv_cache_problem* p, const void* q, const void
   const int64_t bytes = static_cast<int64_t>(p->B) * p->Hkv * p->Lk * 4;
   if (mass_in && mass_in != mass_out && overlap(mass_in, bytes, mass_out, bytes))
     return cache_fail(PSV_EINVAL, "mass_in overlaps mass_out in part");
+  const Area none = plain_area("", nullptr, 0);
+  if (int r = check_areas({plain_area("mass_out", mass_out, bytes)},
+                          {p->Lq ? tensor_area("q", q, p->q_stride, p->B, p->Lq, p->Hq, p->dh, 2) : none,
+                           tensor_area("k", k, p->k_stride, p->B, p->Lk, p->Hkv, p->dh, 2),
+                           plain_area("lse", lse, static_cast<int64_t>(p->B) * p->Hq * p->Lq * 4)}))
+    return r;
   int dev = 0;
   if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
   if (int r = check_device(dev, k, "k")) return r;

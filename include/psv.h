@@ -381,7 +381,11 @@ int psv_attention_noalloc_status(int* status, void* cuda_stream);
  *   - errors: PSV_EINVAL (shapes, strides, alignment, null pointers; host
  *     memory, or another device's, as the first input or the first output),
  *     PSV_ECUDA; psv_cache_last_error() names the reason.  What other pointers
- *     point to is not looked at. */
+ *     point to is not looked at;
+ *   - outputs that meet an input or one another (as each call says) are refused
+ *     (PSV_EINVAL).  Tensors packed into one buffer, row by row or block by
+ *     block, pass where their strides agree; where they do not, the stretches
+ *     from a tensor's first to its last byte have to be apart. */
 
 #define PSV_DTYPE_F16 2 /* besides PSV_DTYPE_F32 and PSV_DTYPE_BF16 */
 
@@ -399,7 +403,8 @@ const char* psv_cache_last_error(void);
  * call).  Layout PAIRS: pair p is (2p, 2p+1), as on the wave path; HALVES:
  * (p, p + R/2).  Angles are reduced in 64-bit fixed point, so positions up to
  * 2^31 keep f32 accuracy; the rotation is done in f32 and rounded once.
- * In place (out == x with equal strides) is allowed, other overlap is not.
+ * In place (out == x with equal strides) is allowed; an out that meets x
+ * otherwise, or pos, is refused.
  * Rows l >= lens[b] of out are left as they were.
  * Requirements: dtype F32, BF16 or F16; 1 <= n_axes <= 4; axis_dims even and
  * positive; R <= dh <= 256; dh even; 1 <= B <= 65535; L, H >= 1 and L x H
@@ -431,8 +436,9 @@ int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* pos, void*
  *   o = softmax(s) v over the visible keys;  lse = log sum exp s  [B][Hq][Lq]
  * A row that sees nothing gets o = 0 and lse = -infinity.  Rows i >= q_lens[b]
  * of o and lse are left as they were.  Lengths are clamped to [0, Lq] and
- * [0, Lk].  Default positions: k_pos = j, q_pos = k_len - q_len + i (the rows
- * are the last ones of the sequence).  Positions lie within +-2^30.
+ * [0, Lk].  o may be q itself (equal strides); otherwise o and lse meet neither
+ * q, k, v nor one another.  Default positions: k_pos = j, q_pos = k_len - q_len
+ * + i (the rows are the last ones of the sequence).  Positions lie within +-2^30.
  * Keys and values behind k_lens[b] may hold anything (NaN too); keys that are
  * only masked may hold anything finite, their scores are not used.
  * Products take bf16/f16 operands and accumulate in f32; scores, maxima, sums
@@ -485,8 +491,9 @@ int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k
  *   mass_out[b][g][j] = mass_in[b][g][j]
  *                     + sum over rows i < q_lens[b] and heads h of group g of exp(s_ij - lse)
  * over visible pairs; mass f32 [B][Hkv][Lk]; mass_in may be NULL (zeros) or
- * mass_out (accumulate in place).  Entries j >= k_lens[b] are left as they
- * were.  Sums are f32 in a fixed order (repeats are equal bit for bit).
+ * mass_out (accumulate in place); mass_out meets neither q, k nor lse.  Entries
+ * j >= k_lens[b] are left as they were.  Sums are f32 in a fixed order (repeats
+ * are equal bit for bit).
  * Requirements as above. */
 int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, const float* lse,
                    const float* mass_in, float* mass_out, void* scratch, size_t scratch_bytes,
@@ -500,7 +507,8 @@ int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, con
  * mass_out, idx_out, pos_out, doc_out [B][Hkv][budget]); idx_out holds the
  * slots they came from, lens_out[b] = min(n, budget).  Rows behind lens_out
  * are left as they were.  pos_out without k_pos receives the slots.  Out
- * buffers must not overlap any input or one another.
+ * buffers that meet an input or one another are refused (k_out and v_out may be
+ * packed into one buffer).
  * Requirements: dtype F32, BF16 or F16; B, Hkv, budget >= 1; 1 <= L <= 2^30;
  * budget <= L; 1 <= dh; sinks, recent >= 0, sinks + recent <= budget; B <= 65535 and budget
  * x Hkv x dh below 2^32; strides in [0, 2^40], rows of k_out and v_out

@@ -184,3 +184,114 @@ def test_evict_refuses_more_slots_than_it_can_step_over():
 
     for n in (2**31 - 1, 2**31 - 1024, 2**30 + 1):
         refused("2^30", P.psv_cache_evict, make(n), *(k << 36 for k in range(1, 8)))
+
+
+def passes_the_areas(call, *args):
+    """The call gets as far as the device (which is missing, or does not hold these addresses)."""
+    with pytest.raises(P.PSVError) as e:
+        call(*args)
+    assert "overlap" not in str(e.value) and "same buffer" not in str(e.value), str(e.value)
+
+
+def test_evict_outputs_that_meet_anything_are_refused():
+    k = 2 * 50 * 3 * 64 * 2  # bytes of k and of v; of k_out and v_out 15360, of mass 1200, of the lists 480
+    names = ("k", "v", "mass", "k_out", "v_out", "mass_out", "idx_out")
+    where = {n: A * (i + 1) for i, n in enumerate(names)}
+    extra = dict(k_lens=20 * A, k_pos=21 * A, k_doc=22 * A, pos_out=23 * A, doc_out=24 * A, lens_out=25 * A)
+
+    def call(**kw):
+        at = {**where, **extra, **kw}
+        return P.psv_cache_evict, changed(evict, **{n: at[n] for n in extra}), *(at[n] for n in names)
+
+    passes_the_areas(*call())
+    for out, at in (("k_out", "v"), ("v_out", "k"), ("k_out", "mass"), ("mass_out", "v"), ("idx_out", "k"), ("idx_out", "mass"),
+                    ("pos_out", "k_pos"), ("doc_out", "k_doc"), ("pos_out", "mass"), ("lens_out", "k_doc"), ("mass_out", "k_lens")):
+        refused("overlap", *call(**{out: {**where, **extra}[at]}))
+        passes_the_areas(*call(**{out: {**where, **extra}[at] + (1 << 19)}))
+    refused("overlap", *call(k_out=where["v"] + k - 2))
+    passes_the_areas(*call(k_out=where["v"] + k))
+    for a, b in (("v_out", "k_out"), ("mass_out", "k_out"), ("idx_out", "mass_out"), ("pos_out", "idx_out"), ("doc_out", "pos_out"),
+                 ("lens_out", "doc_out")):
+        refused("overlap", *call(**{a: {**where, **extra}[b] + 8}))
+
+
+def test_evict_accepts_packed_buffers():
+    """Keys and values side by side in one buffer, row by row or block by block."""
+    H, dh, L, n = 3, 64, 50, 20
+    rest = (30 * A, 31 * A)
+    for st, step in (((L * H * 2 * dh, H * 2 * dh, 2 * dh), dh),      # [L][H][2][dh]
+                     ((L * 2 * H * dh, 2 * H * dh, dh), H * dh),      # [L][2][H][dh]
+                     ((2 * L * H * dh, H * dh, dh), L * H * dh),      # [2][L][H][dh]
+                     ((2 * H * L * dh, dh, L * dh), H * L * dh)):     # [2][H][L][dh]
+        p = changed(evict, k_stride=st, v_stride=st, k_out_stride=st, v_out_stride=st)
+        passes_the_areas(P.psv_cache_evict, p, A, A + 2 * step, 5 * A, 3 * A, 3 * A + 2 * step, *rest)
+        if step <= H * dh:  # (else k_out, of fewer rows than L, ends before)
+            refused("overlap", P.psv_cache_evict, p, A, A + 2 * step, 5 * A, 3 * A, 3 * A + 2 * step - 2, *rest)
+        refused("overlap", P.psv_cache_evict, p, A, A + 2 * step, 5 * A, A + 2 * step, 3 * A, *rest)
+        # the same buffer's further rows
+        if st[1] >= H * dh:
+            long = tuple([4 * st[0], st[1], st[2]])
+            p = changed(evict, k_stride=long, v_stride=long, k_out_stride=long, v_out_stride=long)
+            at = A + (2 * L if step == L * H * dh else L) * st[1] * 2  # behind k's and v's rows
+            passes_the_areas(P.psv_cache_evict, p, A, A + 2 * step, 5 * A, at, at + 2 * step, *rest)
+            refused("overlap", P.psv_cache_evict, p, A, A + 2 * step, 5 * A, at - 2 * st[1], at + 2 * step, *rest)
+
+
+def test_attention_outputs_that_meet_an_input_are_refused():
+    n = 1 << 30
+    passes_the_areas(P.psv_cache_attention, cache(), A, 2 * A, 3 * A, A, 0, 5 * A, n)  # in place
+    refused("overlap", P.psv_cache_attention, cache(), A, 2 * A, 3 * A, A + 16, 0, 5 * A, n)
+    refused("overlap", P.psv_cache_attention, changed(cache, q_stride=(5 * 400, 400, 64)), A, 2 * A, 3 * A, A, 0, 5 * A, n)
+    refused("overlap", P.psv_cache_attention, cache(), A, 2 * A, 3 * A, 2 * A, 0, 5 * A, n)
+    refused("overlap", P.psv_cache_attention, cache(), A, 2 * A, 3 * A, 3 * A + 35000, 0, 5 * A, n)
+    passes_the_areas(P.psv_cache_attention, cache(), A, 2 * A, 3 * A, 3 * A + 35840, 0, 5 * A, n)
+    for at in (A + 16, 2 * A, 3 * A + 4, 4 * A + 64):
+        refused("lse overlaps", P.psv_cache_attention, cache(), A, 2 * A, 3 * A, 4 * A, at, 5 * A, n)
+    # q, k, v and o of one row side by side: [B][L][6 + 2 + 2 + 6][64]
+    st = (5 * 1024, 1024, 64)
+    p = P.cache_problem(P.PSV_DTYPE_BF16, (2, 5, 6, 64), (2, 5, 2, 64), q_stride=st, k_stride=st, v_stride=st, o_stride=st)
+    passes_the_areas(P.psv_cache_attention, p, A, A + 768, A + 1024, A + 1280, 0, 5 * A, n)
+    refused("o overlaps v", P.psv_cache_attention, p, A, A + 768, A + 1024, A + 1278, 0, 5 * A, n)
+    # one cache for every sequence
+    p = P.cache_problem(P.PSV_DTYPE_BF16, (2, 5, 2, 64), (2, 5, 2, 64), k_stride=(0, 128, 64), v_stride=(0, 128, 64))
+    passes_the_areas(P.psv_cache_attention, p, A, A + 2560, A + 3840, A + 5120, 0, 5 * A, n)
+    refused("o overlaps v", P.psv_cache_attention, p, A, A + 2560, A + 3840, A + 5118, 0, 5 * A, n)
+
+
+def test_mass_and_rope_outputs_that_meet_an_input_are_refused():
+    n = 1 << 30
+    passes_the_areas(P.psv_cache_mass, cache(), A, 2 * A, 3 * A, 4 * A, 4 * A, 5 * A, n)
+    for at in (A, 2 * A, 3 * A):
+        refused("mass_out overlaps", P.psv_cache_mass, cache(), A, 2 * A, 3 * A, 0, at, 5 * A, n)
+    passes_the_areas(P.psv_rope, rope(), A, 2 * A, A)
+    refused("out overlaps x", P.psv_rope, rope(), A, 2 * A, A + 64)
+    refused("out overlaps pos", P.psv_rope, rope(), A, 2 * A, 2 * A - 512)
+    st = (5 * 3 * 192, 3 * 192, 64)  # the queries of a packed projection into the place of its values
+    p = changed(rope, x_stride=st, out_stride=st)
+    passes_the_areas(P.psv_rope, p, A, 2 * A, A + 2 * 384)
+    refused("out overlaps x", P.psv_rope, p, A, 2 * A, A + 2 * 190)
+
+
+def test_areas_against_a_walk_over_all_bytes():
+    """Random small layouts: what meets is refused; what does not passes where the strides agree."""
+    rng = np.random.default_rng(3)
+    met = 0
+    for _ in range(400):
+        B, L, H = (int(x) for x in rng.integers(1, 4, 3))
+        dh, n = 2 * int(rng.integers(1, 3)), int(rng.integers(1, L + 1))
+        order = rng.permutation(3)
+        ext, st, span = (B, L, H), [0, 0, 0], dh * int(rng.integers(1, 4))
+        for d in order:
+            st[d] = span
+            span = st[d] * ext[d] + 2 * int(rng.integers(0, 3))
+        off = 2 * int(rng.integers(-span, span + 2))
+        p = P.evict_problem(P.PSV_DTYPE_BF16, (B, L, H, dh), n, k_stride=st, v_stride=st, k_out_stride=st, v_out_stride=st)
+
+        def cells(at, rows):
+            return {at + b * st[0] + r * st[1] + h * st[2] + e for b in range(B) for r in range(rows) for h in range(H) for e in range(dh)}
+
+        meets = bool(cells(0, L) & cells(off // 2, n))
+        met += meets
+        args = (p, A, 9 * A, 5 * A, A + off // 2 * 2, 7 * A, 30 * A, 31 * A)
+        (refused if meets else passes_the_areas)(*(("k_out overlaps k",) if meets else ()), P.psv_cache_evict, *args)
+    assert 50 < met < 350
