@@ -348,7 +348,10 @@ __device__ __forceinline__ Piece piece_of(int4 pc, int4 pt) {
 
 // The piece slots are written by the even CTA's thread with st.shared::cluster
 // and published with a release.cluster arrive; readers in either CTA wait
-// with an acquire at cluster scope.
+// with an acquire at cluster scope.  Back the same way: readers in the odd CTA
+// release at cluster scope and the writer acquires at cluster scope before it
+// rewrites a slot (an arrive on the other CTA's barrier at CTA scope orders
+// nothing there, and may overtake the reads).
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, int4 v) {
   asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)
@@ -470,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!mbar_wait_acq_cluster(&pc_full[i & 1], (i >> 1) & 1, p.err, ERR_ATTN_TIMEOUT)) return false;
     pc = ld_shared_v4(&pc_slot[2 * (i & 1)]);
     pt = ld_shared_v4(&pc_slot[2 * (i & 1) + 1]);
-    mbar_arrive_remote(pc_empty0 + (i & 1) * 8);
+    if (leader) mbar_arrive_remote(pc_empty0 + (i & 1) * 8);  // own barrier: CTA scope
+    else mbar_arrive_cluster(pc_empty0 + (i & 1) * 8);
     return true;
   };
 
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int4 pc, pt;
           if (leader) {
             const int b = i & 1;
-            if (i >= 2 && !mbar_wait(&pc_empty[b], ((i >> 1) - 1) & 1, p.err, ERR_ATTN_TIMEOUT)) break;
+            if (i >= 2 && !mbar_wait_acq_cluster(&pc_empty[b], ((i >> 1) - 1) & 1, p.err, ERR_ATTN_TIMEOUT)) break;
             pc = decode_piece(atomicAdd(p.counters, 1), p);
             pt = piece_task(pc, p);
             for (uint32_t r = 0; r < 2; ++r) {
