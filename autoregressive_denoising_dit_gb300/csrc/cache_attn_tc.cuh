@@ -275,19 +275,28 @@ __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_acq_cluster(uint64_t* bar, uint32_t parity, int* err) {
+__device__ __forceinline__ bool mbar_wait_acq_cluster(uint64_t* bar, uint32_t parity, int* err,
+                                                      uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait_acq_cluster(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait_acq_cluster(bar, parity)) return true;
     if ((i & 63) == 63) {
       if (error_raised(err)) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
+      if (global_timer_ns() - t0 > limit_ns) {
         raise_error(err, ERR_ATTN_TIMEOUT);
         return false;
       }
     }
   }
+}
+
+// The limit of the queue's wait for a slot: its readers release it at the end of
+// their piece, which may be 2^20 key tiles (or 2^23 row tiles of the mass) long,
+// over 2 s.  A tile takes 1 to 4 us.
+constexpr uint64_t kTileLimitNs = 20000;
+__device__ __forceinline__ uint64_t piece_limit_ns(int tiles0, int tiles1) {
+  return kWaitLimitNs + (static_cast<uint64_t>(tiles0) + static_cast<uint64_t>(tiles1)) * kTileLimitNs;
 }
 
 // What a tile of 256 keys and a unit of rows hold, from a small kernel run
@@ -601,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- work queue (the whole warp scans the key tiles)
       const int pairs = static_cast<int>(gridDim.x >> 1);
       int k = static_cast<int>(blockIdx.x >> 1);
+      int ahead[2] = {0, 0};  // key tiles of the last two pieces published
       for (int i = 0;;) {
         Piece pc;
         bool rows = true;
@@ -626,7 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           bool ok = true;
           if (rows) {
-            if constexpr (!LATE) ok = i < 2 || mbar_wait(&pc_empty[i & 1], ((i >> 1) - 1) & 1, err, ERR_ATTN_TIMEOUT);
+            if constexpr (!LATE)
+              ok = i < 2 || mbar_wait_acq_cluster(&pc_empty[i & 1], ((i >> 1) - 1) & 1, err, piece_limit_ns(ahead[0], ahead[1]));
+            ahead[0] = ahead[1], ahead[1] = pc.b.w;
             if (ok) {
               for (uint32_t r = 0; r < 2; ++r) {
                 st_cluster_v4(mapa_shared(&pc_slot[2 * (i & 1)], r), pc.a);
@@ -634,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               for (uint32_t r = 0; r < 2; ++r) mbar_arrive_cluster(mapa_shared(&pc_full[i & 1], r));
               if (LATE && i >= 1 && pc.a.x >= 0)
-                ok = mbar_wait(&pc_empty[(i + 1) & 1], ((i - 1) >> 1) & 1, err, ERR_ATTN_TIMEOUT);
+                ok = mbar_wait_acq_cluster(&pc_empty[(i + 1) & 1], ((i - 1) >> 1) & 1, err, piece_limit_ns(ahead[0], ahead[1]));
             }
           }
           next = ok && pc.a.x >= 0 ? pairs + atomicAdd(p.queue, 1) : -1;

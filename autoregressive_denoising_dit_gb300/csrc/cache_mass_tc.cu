@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       // ---------------- work queue
       const int pairs = static_cast<int>(gridDim.x >> 1);
       int k = static_cast<int>(blockIdx.x >> 1);
+      int ahead[2] = {0, 0};  // row tiles of the last two pieces published
       for (int i = 0;;) {
         Piece pc;
         bool keys = true;
@@ -210,7 +211,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         if (lane == 0) {
           bool ok = true;
           if (keys) {
-            ok = i < 2 || mbar_wait(&pc_empty[i & 1], ((i >> 1) - 1) & 1, err, ERR_ATTN_TIMEOUT);
+            ok = i < 2 || mbar_wait_acq_cluster(&pc_empty[i & 1], ((i >> 1) - 1) & 1, err, piece_limit_ns(ahead[0], ahead[1]));
+            ahead[0] = ahead[1], ahead[1] = pc.a.w;
             if (ok) {
               for (uint32_t r = 0; r < 2; ++r) {
                 st_cluster_v4(mapa_shared(&pc_slot[2 * (i & 1)], r), pc.a);

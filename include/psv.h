@@ -478,8 +478,9 @@ typedef struct psv_cache_problem {
  * 256-byte aligned device memory whose first PSV_CACHE_SCRATCH_HEAD bytes the
  * caller zeroes once, before its first use.  It may serve any number of calls
  * (captured ones too) that do not overlap on the GPU.  The int at its start
- * becomes nonzero, and stays so, if a device-side wait of a call timed out;
- * that call's output is not valid, and the workspace is zeroed before reuse. */
+ * becomes nonzero, and stays so, if a device-side wait of a call timed out (2 s
+ * without progress); that call's output is not valid, and the workspace is
+ * zeroed before reuse. */
 #define PSV_CACHE_SCRATCH_HEAD 256
 int psv_cache_scratch_bytes(const psv_cache_problem* p, size_t* bytes);
 int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k, const void* v,

@@ -50,3 +50,57 @@ def test_packed_outputs_of_eviction(P):
         for h in range(H):
             w = torch.as_tensor(T.evict_reference(c, b, h), device="cuda")
             assert torch.equal(ko[b, :, h], k[b, w, h]) and torch.equal(vo[b, :, h], v[b, w, h])
+
+
+# ------------------------------------------------------------- long pieces
+
+def test_a_piece_of_over_two_seconds_is_no_timeout(P):
+    """2^28 capped keys in one work item, two of which one pair of SMs does: it takes longer
+    than a wait that makes no progress may."""
+    L, Lq, dh, n = 1 << 28, 76 * 256 + 1, 8, 500
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    k = torch.zeros(1, L, 1, dh, device="cuda", dtype=torch.bfloat16)
+    k[..., 0] = -220.0  # a score of -622 for every row, -60 under the cap: no weight
+    v = torch.zeros_like(k)
+    some = torch.randperm(1 << 20, device="cuda", generator=g)[:n].sort().values * 256 + 77
+    k[0, some, 0] = torch.randn(n, dh, device="cuda", generator=g).to(k.dtype)
+    v[0, some, 0] = torch.randn(n, dh, device="cuda", generator=g).to(k.dtype)
+    q = torch.randn(1, Lq, 1, dh, device="cuda", generator=g).to(k.dtype)
+    q[..., 0] = 8.0
+    c = dict(make(B=1), B=1, Lq=Lq, Lk=L, Hq=1, Hkv=1, dh=dh, q=q, k=k, v=v, cap=60.0)
+    o, lse = run_attention(P, c)
+    few = dict(c, Lk=n, k=k[:, some], v=v[:, some])  # (the others' weight is below 2^28 e^-59)
+    check_attention(few, o, lse)
+
+
+def test_a_mass_piece_of_over_two_seconds_is_no_timeout(P):
+    """2^30 rows for one tile of keys, two of which one pair of SMs does.  The rows overlap in
+    memory: row (i, h) is row i + h of a buffer; 500 of them give weight."""
+    Lq, H, Lk, dh, lse0 = 1 << 24, 64, 76 * 256 + 1, 8, 5.0
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    rows = torch.zeros(Lq + H - 1, dh, device="cuda", dtype=torch.bfloat16)
+    rows[:, 0] = 8.0  # scores of -85: no weight
+    some = torch.randperm(Lq + H - 1, device="cuda", generator=g)[:500].sort().values
+    rows[some] = torch.randn(500, dh, device="cuda", generator=g).to(rows.dtype)
+    rows[some, 0] = 0.0
+    k = torch.randn(1, Lk, 1, dh, device="cuda", generator=g).to(torch.bfloat16)
+    k[..., 0] = -30.0
+    lse = torch.full((1, H, Lq), lse0, device="cuda")
+    out = torch.zeros(1, 1, Lk, device="cuda")
+    prob = P.cache_problem(P.PSV_DTYPE_BF16, (1, Lq, H, dh), k.shape, q_stride=(Lq * dh, dh, dh))
+    n = P.psv_cache_scratch_bytes(prob)
+    s = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    P.psv_cache_mass(prob, at(rows), at(k), at(lse), 0, at(out), at(s), n, stream())
+    torch.cuda.synchronize()
+    T.no_error(s)
+    # how many (i, h) are row r
+    times = torch.minimum(torch.minimum(some + 1, Lq + H - 1 - some), torch.full_like(some, H)).double()
+    x = rows[some].double() @ k[0, :, 0].double().T / dh**0.5
+    want = (torch.exp(x - lse0) * times[:, None]).sum(0)
+    # Of the 32000 weights of a key each of its 32 sums gets about 1000, at most 2^11 (each addition
+    # off by 2^-24 of the sum); a score's products, exp2 and its argument take 2^-17.
+    tol = want * (2.0**-13 + 2.0**-17)
+    d = (out[0, 0].double() - want).abs()
+    assert (d <= tol).all(), float((d / tol).max())
