@@ -3,6 +3,7 @@
 // the kernel that joins the shares, and the launch.
 #include "cache_attn_tc.cuh"
 
+#include <cfloat>
 #include <cmath>
 
 namespace psv {
@@ -351,20 +352,22 @@ constexpr double kTanh3[3] = {0.9999999437513383, -0.33330206128320755, 0.130748
 constexpr double kTanh7[7] = {0.9999999486455696, -0.3333282797859907, 0.13325076146101278, -0.05345164636973283, 0.02027970828564412, -0.006194324833673898, 0.0010380250967268723};
 
 // Coefficients of cap2 for scores s: cap log2(e) tanh(s inv) = s sum_k c_k s^(2k).
-// A polynomial whose coefficients leave f32's normal range is not used.
-int set_cap_poly(float2* out, const double* c, int n, double inv, double cap2e) {
+// A polynomial of which one leaves f32's normal range is not used (the short one
+// from caps of about 1e8 on, the other from 60 at heads of 128).
+bool set_cap_poly(float2* out, const double* c, int n, double inv, double cap2e) {
   double power = inv;
   for (int k = 0; k < n; ++k, power *= inv * inv) {
     const double v = c[k] * power * cap2e;
-    if (std::fabs(v) < 1e-36 || std::fabs(v) > 1e36) return 0;
+    if (std::fabs(v) < FLT_MIN || std::fabs(v) > FLT_MAX) return false;
     out[k].x = out[k].y = static_cast<float>(v);
   }
-  return 1;
+  return true;
 }
 
 void set_cap(TcParams& p) {
   p.cap_small = p.cap_mid = -1.0f;
   if (!(p.c.softcap > 0)) return;
+  set_cap_form(p.cap, p.c.scale, p.c.softcap);
   const double inv = static_cast<double>(p.c.scale) / p.c.softcap, cap2e = p.c.softcap * 1.4426950408889634;
   if (set_cap_poly(p.cap_c3, kTanh3, 3, inv, cap2e)) p.cap_small = static_cast<float>(0.18 / inv);
   if (set_cap_poly(p.cap_c7, kTanh7, 7, inv, cap2e)) p.cap_mid = static_cast<float>(1.0 / inv);
@@ -399,6 +402,15 @@ cudaError_t launch_join(const TcParams& p, bool bf16, cudaStream_t st) {
 }
 
 }  // namespace
+
+void set_cap_form(CapForm& f, float scale, float cap) {
+  const double inv = static_cast<double>(scale) / cap, c2 = cap * 1.4426950408889634, scale2 = scale * 1.4426950408889634;
+  f.inv = static_cast<float>(inv < FLT_MAX ? inv : FLT_MAX);
+  f.c2 = static_cast<float>(c2 < FLT_MAX ? c2 : FLT_MAX);
+  const double two = 2.885390081777927 * inv;
+  f.two = cap <= kCapLow ? static_cast<float>(two < FLT_MAX ? two : FLT_MAX) : 0.0f;
+  for (int k = 0; k < 7; ++k) f.poly[k].x = f.poly[k].y = static_cast<float>(kTanh7[k] * scale2);
+}
 
 TcParams cattn::plan(const CacheParams& c, char* scratch) {
   const TcLayout t = tc_layout(c);
@@ -500,7 +512,7 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
   cudaError_t e;
   if (static_cast<int64_t>(c.Lq) * c.G <= kFewRows) {
     const bool within = joins_within(p, sms);
-    const RowsParams r{c, p.nsplit, p.part_rows, p.n_pieces, sms, p.part_o, p.part_ml,
+    const RowsParams r{c, p.cap, p.nsplit, p.part_rows, p.n_pieces, sms, p.part_o, p.part_ml,
                        within ? reinterpret_cast<int*>(scratch) + kJoinFirst : nullptr};
     e = launch_cache_rows(r, bf16, false, st);
     return e != cudaSuccess || p.nsplit == 1 || within ? e : launch_join(p, bf16, st);
@@ -516,7 +528,7 @@ cudaError_t launch_cache_attention_tc(const CacheParams& c, bool bf16, char* scr
   }
   if ((e = launch_tiles(p, st)) != cudaSuccess || (e = launch_order(p, st)) != cudaSuccess) return e;
   const int pairs = p.n_pieces < sms / 2 ? p.n_pieces : sms / 2;
-  const int f = (c.softcap > 0 ? F_CAP : 0) | (c.slopes ? F_BIAS : 0) | (c.k_doc || c.k_pos || c.q_pos ? F_META : 0);
+  const int f = (c.softcap > 0 ? F_CAP : 0) | (c.softcap > kCapLow ? F_WIDE : 0) | (c.slopes ? F_BIAS : 0) | (c.k_doc || c.k_pos || c.q_pos ? F_META : 0);
   if (p.width == 64)
     e = bf16 ? launch_features<64, true>(maps, p, f, pairs, st) : launch_features<64, false>(maps, p, f, pairs, st);
   else

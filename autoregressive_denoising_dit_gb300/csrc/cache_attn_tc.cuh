@@ -46,6 +46,7 @@
 #include <cuda.h>
 
 #include "../../include/psv.h"
+#include "cache_cap.cuh"
 #include "cache_kernels.h"
 #include "psv_device.cuh"
 #include "psv_kernels.h"
@@ -200,11 +201,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -337,7 +333,8 @@ struct TcParams {
   // slopes in three parts (kLinBytes).
   int* lin_ok;
   uint16_t* lin_q;
-  float cap_small, cap_mid;       // scores up to which the polynomials hold
+  CapForm cap;                    // where c.softcap > 0
+  float cap_small, cap_mid;       // scores up to which cap2's polynomials hold (below 0: none)
   float2 cap_c3[3], cap_c7[7];    // their coefficients, each twice
   int* queue;       // next piece, pairs done (zero between launches)
   float* part_o;    // [piece][part_rows][DH], unnormalised
@@ -485,26 +482,28 @@ __device__ __forceinline__ bool zero_tile(const TcParams& p, int key0, int k_len
 // cap log2(e) tanh(s inv) of a pair of scores as s P(s^2), P of degree N - 1
 // with coefficients c (scaled by the powers of inv = scale / cap and by cap
 // log2 e), from interpolating tanh(sqrt z) / sqrt z at Chebyshev points: 3 of
-// [0, 0.0324] for |s inv| <= 0.18 (error of tanh 8e-9), 7 of [0, 1] for |s inv|
-// <= 1 (5e-8).  The packed products are bound by the FMA pipe, which is why
-// small scores, the usual ones under a cap, have a short polynomial.
+// [0, 0.0324] for |s inv| <= 0.18, 7 of [0, 1] for |s inv| <= 1 (5.6e-8 and 5e-8 of
+// the score).  The packed products are bound by the FMA pipe, which is why scores
+// far below the cap have a short polynomial, and why the cap's powers are in the
+// coefficients where f32 holds them (cap_within takes one product more: four
+// sequences of 1560 rows, heads of 64, cap 20, deviation 4: 399 us, 421 with it).
 template <int N>
 __device__ __forceinline__ void cap2(float& x0, float& x1, const float2* c) {
   uint64_t x, z, y;
   asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
   asm("mul.rn.f32x2 %0, %1, %1;" : "=l"(z) : "l"(x));
-  auto pair = [](const float2& v) { return *reinterpret_cast<const uint64_t*>(&v); };
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(z), "l"(pair(c[N - 1])), "l"(pair(c[N - 2])));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(z), "l"(pair_bits(c[N - 1])), "l"(pair_bits(c[N - 2])));
 #pragma unroll
-  for (int k = N - 3; k >= 0; --k) asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(z), "l"(pair(c[k])));
+  for (int k = N - 3; k >= 0; --k) asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(z), "l"(pair_bits(c[k])));
   asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
 }
 
 // F: what the scores need beside the row's key limit (lengths, causal, prefix),
 // as bits, so that a kernel holds the registers of its own work only: the score
-// cap, the distance bias, documents and explicit positions.
-enum : int { F_CAP = 1, F_BIAS = 2, F_META = 4 };
+// cap, the distance bias, documents and explicit positions, and (with F_CAP) a cap
+// over kCapLow, whose forms beside the usual caps' made both spill.
+enum : int { F_CAP = 1, F_BIAS = 2, F_META = 4, F_WIDE = 8 };
 //
 // With the bias alone (LIN) the tensor cores add it, as its multiply-adds per
 // score would lengthen the softmax, which paces the kernel: where all rows of a
@@ -1004,7 +1003,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sl2 = scale2, off = 0.0f;  // score = s * sl2 + off (log2)
         if constexpr ((F & F_CAP) != 0) {
           {
-            const float inv = p.c.scale / p.c.softcap, c2 = p.c.softcap * kLog2e;
             // What lies behind the keys must not choose the branch.
             if (key0 + 128 > k_len) {
 #pragma unroll
@@ -1017,14 +1015,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__all_sync(0xffffffffu, !valid || big <= p.cap_small)) {
 #pragma unroll
               for (int c = 0; c < 128; c += 2) cap2<3>(s[c], s[c + 1], p.cap_c3);
+            } else if constexpr ((F & F_WIDE) != 0) {
+              if (__all_sync(0xffffffffu, !valid || big * p.cap.inv <= 1.0f)) cap_within<128>(s, p.cap);
+              else cap_any<128>(s, p.cap);
             } else if (__all_sync(0xffffffffu, !valid || big <= p.cap_mid)) {
 #pragma unroll
               for (int c = 0; c < 128; c += 2) cap2<7>(s[c], s[c + 1], p.cap_c7);
             } else {
-              const float two = 2.0f * kLog2e * inv;
-#pragma unroll
-              for (int c = 0; c < 128; ++c)
-                s[c] = fmaf(-2.0f * c2, fast_rcp(1.0f + fast_exp2(s[c] * two)), c2);
+              cap_low<128>(s, p.cap);
             }
             sl2 = 1.0f;
           }
@@ -1277,7 +1275,12 @@ cudaError_t launch_features(const CUtensorMap* maps, const TcParams& p, int f, i
     case 4: return launch_one<DH, BF16, 4>(maps, p, pairs, st);
     case 5: return launch_one<DH, BF16, 5>(maps, p, pairs, st);
     case 6: return launch_one<DH, BF16, 6>(maps, p, pairs, st);
-    default: return launch_one<DH, BF16, 7>(maps, p, pairs, st);
+    case 7: return launch_one<DH, BF16, 7>(maps, p, pairs, st);
+    case 9: return launch_one<DH, BF16, 9>(maps, p, pairs, st);
+    case 11: return launch_one<DH, BF16, 11>(maps, p, pairs, st);
+    case 13: return launch_one<DH, BF16, 13>(maps, p, pairs, st);
+    case 15: return launch_one<DH, BF16, 15>(maps, p, pairs, st);
+    default: return cudaErrorInvalidValue;
   }
 }
 

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "cache_cap.cuh"
+
 namespace psv {
 
 // Stores `msg` (printf-style) as this thread's last error of the cache calls.
@@ -51,6 +53,7 @@ inline uint64_t map_stride(int64_t s, int64_t n) { return n > 1 ? static_cast<ui
 constexpr int kFewRows = 16;
 struct RowsParams {
   CacheParams c;
+  CapForm cap;  // where c.softcap > 0
   int nsplit, part_rows;
   int n_pieces, ctas;  // pieces: sequences x kv heads x shares; CTAs at most
   float* part_o;

@@ -410,7 +410,6 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(rb) << 16;
     const uint32_t s_free0 = mapa_shared(s_free, 0);
     const float scale2 = p.c.scale * kLog2e;
-    const float inv = p.c.softcap > 0 ? p.c.scale / p.c.softcap : 0.0f, c2 = p.c.softcap * kLog2e;
     int g = 0;
     for (int i = 0;; ++i) {
       int4 pa, pb;
@@ -447,17 +446,34 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           const int* ic = reinterpret_cast<const int*>(cc);
           float sc = scale2;
           if constexpr ((F & F_CAP) != 0) {
-            const float two = 2.0f * kLog2e * inv;
+            // (What unused rows hold must not choose the branch.)
+            if (unused) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (ic[COL_PLIM * kColWords + e] == -0x7fffffff - 1) v[e] = 0.0f;
+            }
             float big = 0.0f;
 #pragma unroll
             for (int e = 0; e < 32; e += 2) big = max3(big, fabsf(v[e]), fabsf(v[e + 1]));
-            // (In a tile with unused rows their values must not choose the branch.)
-            if (!unused && __all_sync(0xffffffffu, !valid || big <= p.cap_small)) {
+            if (__all_sync(0xffffffffu, !valid || big <= p.cap_small)) {
 #pragma unroll
               for (int e = 0; e < 32; e += 2) cap2<3>(v[e], v[e + 1], p.cap_c3);
+            } else if (__all_sync(0xffffffffu, !valid || big * p.cap.inv <= 1.0f)) {
+              cap_within<32>(v, p.cap);
             } else {
+              // (A cap over kCapLow that scores pass is rare: its form goes over local
+              // memory, eight scores at a time, which keeps the loop short.)
+              if (p.cap.two > 0.0f) {
+                cap_low<32>(v, p.cap);
+              } else {
+                float t[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = fmaf(-2.0f * c2, fast_rcp(1.0f + fast_exp2(v[e] * two)), c2);
+                for (int e = 0; e < 32; ++e) t[e] = v[e];
+#pragma unroll 1
+                for (int e = 0; e < 32; e += 8) cap_any<8>(t + e, p.cap);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = t[e];
+              }
             }
             sc = 1.0f;
           }
@@ -588,7 +604,9 @@ cudaError_t launch_cache_mass_tc(const CacheParams& c, bool bf16, char* scratch,
     int64_t n = (8 * static_cast<int64_t>(sms) + heads - 1) / heads;
     if (n > most) n = most;
     if (n > 304) n = 304;
-    const RowsParams r{c, static_cast<int>(n), 0, static_cast<int>(heads * n), sms, nullptr, nullptr, nullptr};
+    CapForm cap{};
+    if (c.softcap > 0) set_cap_form(cap, c.scale, c.softcap);
+    const RowsParams r{c, cap, static_cast<int>(n), 0, static_cast<int>(heads * n), sms, nullptr, nullptr, nullptr};
     return launch_cache_rows(r, bf16, true, st);
   }
   TcParams p = plan(c, scratch);

@@ -17,6 +17,7 @@
 #include <cuda.h>
 
 #include "../../include/psv.h"
+#include "cache_cap.cuh"
 #include "cache_kernels.h"
 #include "psv_device.cuh"
 #include "psv_kernels.h"
@@ -88,11 +89,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (BF16) return pack_bf16x2(lo, hi);
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
@@ -357,11 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Scores in the log2 domain, -inf where the row does not see the key.
       if (c.softcap > 0) {
-        const float c2 = c.softcap * kLog2e, two = 2.0f * kLog2e * c.scale / c.softcap;
+        float big = 0.0f;
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(-2.0f * c2, fast_rcp(1.0f + fast_exp2(s[n][e] * two)), c2);
+          for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(s[n][e]));
+        if (__all_sync(0xffffffffu, big * p.cap.inv <= 1.0f)) cap_within<16>(&s[0][0], p.cap);
+        else cap_any<16>(&s[0][0], p.cap);
       } else {
 #pragma unroll
         for (int n = 0; n < 4; ++n)

@@ -442,8 +442,9 @@ int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* pos, void*
  * Keys and values behind k_lens[b] may hold anything (NaN too); keys that are
  * only masked may hold anything finite, their scores are not used.
  * Products take bf16/f16 operands and accumulate in f32; scores, maxima, sums
- * and lse are f32; the weights are rounded to the operand type for their
- * product with v, the output once.  Results do not depend on other sequences
+ * and lse are f32 (the cap's tanh is good to 2^-21 of the capped score, with a
+ * cap of up to 128 to 2^-21 of the cap); the weights are rounded to the operand
+ * type for their product with v, the output once.  Results do not depend on other sequences
  * of the batch, and repeat bit for bit.
  * Requirements: dtype BF16 or F16; B, Hkv >= 1; Hq a multiple of Hkv; B x Hq
  * <= 2^24; 0 <= Lq <= 2^24, 0 <= Lk <= 2^28; 1 <= dh <= 256; strides in [0,

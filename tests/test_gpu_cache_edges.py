@@ -104,3 +104,92 @@ def test_a_mass_piece_of_over_two_seconds_is_no_timeout(P):
     tol = want * (2.0**-13 + 2.0**-17)
     d = (out[0, 0].double() - want).abs()
     assert (d <= tol).all(), float((d / tol).max())
+
+# ------------------------------------------------------------------- caps
+
+def capped_scores(c, b, h):
+    """As the main tests' head_scores, but a cap over 128 costs 2^-21 of the capped score, not of the cap.
+
+    Up to the cap the score is s P(z), z = (s / cap)^2: P is interpolated to 2^-24, z is off by three
+    roundings (2^-22.4, of which P, whose logarithm changes at most a third as fast as z's, takes
+    2^-24), P and its product round four times (2^-22).  Beyond it, t = (1 - a) / (1 + a), a = e^-2x <=
+    0.14: a is off by (2 x + 2) 2^-23, of which t takes 0.28, the reciprocal by 2^-23, and t and its
+    product round four times: 2^-21.2.  Caps up to 128 may take t = 1 - 2 / (1 + e^2x) throughout: e^2x
+    off by (2 |x| + 2) 2^-23, the sum by 2^-24, the reciprocal by 2^-23, 2^-21 of the cap at most.
+    """
+    s, es, ok, nq, nk = T_head_scores(dict(c, cap=0.0, slopes=None), b, h)
+    if c["cap"]:
+        cap = float(np.float32(c["cap"]))
+        s = cap * torch.tanh(s / cap)
+        es = es + 2.0**-21 * (s.abs() if cap > 128 else cap)
+    if c["slopes"] is not None:
+        dev = s.device
+        qp = c["q_pos"][b, :nq].long() if c["q_pos"] is not None else torch.arange(nq, device=dev) + nk - nq
+        kp = c["k_pos"]
+        kp = torch.arange(nk, device=dev) if kp is None else (kp[b, h // (c["Hq"] // c["Hkv"])] if kp.dim() == 3 else kp[b])[:nk].long()
+        far = c["slopes"][h].double() * (qp[:, None] - kp).abs().double()
+        s = s - far
+        es = es + 2.0**-22 * far.abs() + 2.0**-22 * s.abs()
+    return s, es, ok, nq, nk
+
+
+T_head_scores = T.head_scores
+
+CAP_SHAPES = {
+    "token": dict(B=3, Lq=1, Lk=333, Hq=4, Hkv=4, dh=128, k_lens=[333, 1, 70]),
+    "rows": dict(B=2, Lq=5, Lk=700, Hq=6, Hkv=2, dh=64, causal=True, dtype="f16"),
+    "ragged": dict(B=3, Lq=40, Lk=300, Hq=4, Hkv=2, dh=128, q_lens=[40, 17, 1], k_lens=[300, 257, 40]),
+    "many": dict(B=2, Lq=300, Lk=900, Hq=2, Hkv=1, dh=64, causal=True, slopes=True),
+    "wide": dict(B=1, Lq=300, Lk=600, Hq=2, Hkv=2, dh=128, dtype="f16"),
+    "general": dict(B=1, Lq=30, Lk=100, Hq=2, Hkv=1, dh=7, causal=True),
+}
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 2.0, 50.0, 300.0, 1e4, 1e6, 1e8, 1e20, 1e30, 3.4e38])
+@pytest.mark.parametrize("shape", CAP_SHAPES)
+def test_caps(P, monkeypatch, shape, cap):
+    """Scores of deviation 1.5 and 8, and in one head a few far above the cap among small ones."""
+    monkeypatch.setattr(T, "head_scores", capped_scores)
+    for q_scale in (1.5, 8.0):
+        c = make(**CAP_SHAPES[shape], cap=cap, q_scale=q_scale)
+        c["q"][:, ::7, 0] *= 12.0
+        o, lse = run_attention(P, c)
+        check_attention(c, o, lse)
+        mass_in = torch.rand(c["B"], c["Hkv"], c["Lk"], device="cuda")
+        out = torch.full_like(mass_in, 3.0)
+        run_mass(P, c, lse, mass_in, out)
+        check_mass(c, lse, mass_in, out, torch.full_like(out, 3.0))
+
+
+@pytest.mark.parametrize("Lq", [1, 40])
+def test_a_large_cap_beside_far_larger_scores(P, monkeypatch, Lq):
+    """One row's scores pass a cap of 1e6, the others' are small: each row's error follows its own."""
+    monkeypatch.setattr(T, "head_scores", capped_scores)
+    for dh in (64, 128):
+        c = make(B=2, Lq=Lq, Lk=500, Hq=16, Hkv=4, dh=dh, cap=1e6, k_lens=[500, 333])
+        c["q"][:, 0, 1::4] *= 1e6
+        o, lse = run_attention(P, c)
+        check_attention(c, o, lse)
+        out = torch.zeros(2, 4, 500, device="cuda")
+        run_mass(P, c, lse, None, out)
+        check_mass(c, lse, None, out, torch.zeros_like(out))
+
+
+def test_garbage_does_not_choose_how_scores_are_capped(P):
+    """Unused rows and keys behind the lengths, however large, change no bit of the others."""
+    for Lq, dh, cap in ((3, 64, 50.0), (3, 128, 1e6), (300, 128, 50.0), (300, 64, 20.0)):
+        n, nq = [500, 301, 7], [Lq, Lq - 2, 1]
+        c = make(B=3, Lq=Lq, Lk=500, Hq=4, Hkv=2, dh=dh, cap=cap, k_lens=n, q_lens=nq, q_scale=1.0)
+        o, lse = run_attention(P, c)
+        mass = torch.zeros(3, 2, 500, device="cuda")
+        run_mass(P, c, lse, None, mass)
+        for big in (3e38, float("inf"), float("nan"), 40.0):
+            for b in range(3):
+                c["k"][b, n[b]:] = big
+                c["v"][b, n[b]:] = big
+                c["q"][b, nq[b]:] = big
+            got = run_attention(P, c)
+            assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+            again = torch.zeros_like(mass)
+            run_mass(P, c, lse, None, again)
+            assert torch.equal(again, mass)
