@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
                               lane * 4) = v;
   }
   if (lane == 0 && p.c.lse)
-    p.c.lse[(static_cast<int64_t>(b) * p.c.Hq + head) * p.c.Lq + tok] = l > 0.0f ? (m + fast_log2(l)) * kLn2 : -INFINITY;
+    p.c.lse[(static_cast<int64_t>(b) * p.c.Hq + head) * p.c.Lq + tok] = l == 0.0f ? -INFINITY : (m + fast_log2(l)) * kLn2;
 }
 
 // Pairs of SMs that the shares of a sequence are planned for (half of this

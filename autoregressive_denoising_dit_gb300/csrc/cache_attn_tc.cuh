@@ -1203,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_ml[prow] = make_float2(m, l);
         } else if (p.c.lse) {
           p.c.lse[(static_cast<int64_t>(b) * p.c.Hq + head) * p.c.Lq + tok] =
-              l > 0.0f ? (m + fast_log2(l)) * kLn2 : -INFINITY;
+              l == 0.0f ? -INFINITY : (m + fast_log2(l)) * kLn2;  // (NaN stays NaN)
         }
       }
       __syncwarp();

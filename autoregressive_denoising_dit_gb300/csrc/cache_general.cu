@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(kWarps * 32) attention_general_kernel(const Ca
     }
     float mx = s;
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float m_new = fmaxf(m, mx);
-    if (m_new == -INFINITY) continue;
-    const float a = exp2f((m - m_new) * kLog2e), e = sees ? exp2f((s - m_new) * kLog2e) : 0.0f;
+    if (!__any_sync(0xffffffffu, sees)) continue;
+    const float m_new = fmaxf(m, mx), m0 = m_new == -INFINITY ? 0.0f : m_new;  // (-inf: NaN at most so far)
+    const float a = exp2f((m - m0) * kLog2e), e = sees ? exp2f((s - m0) * kLog2e) : 0.0f;
     float sum = e;
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l = l * a + sum;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kWarps * 32) attention_general_kernel(const Ca
 #pragma unroll
   for (int x = 0; x < 8; ++x)
     if (lane + 32 * x < p.dh) put(o + lane + 32 * x, acc[x] * inv);
-  if (lane == 0 && p.lse) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Lq + i] = l > 0 ? m + logf(l) : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Lq + i] = l == 0 ? -INFINITY : m + logf(l);
 }
 
 // One warp per key: lanes take rows in turn, the lanes' sums are joined in a

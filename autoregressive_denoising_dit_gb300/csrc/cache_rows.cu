@@ -225,7 +225,7 @@ __device__ __forceinline__ void join_shares(const RowsParams& p, int b, int kvh,
           make_uint2(pack2<BF16>(acc[0].x * inv, acc[0].y * inv), pack2<BF16>(acc[0].z * inv, acc[0].w * inv));
     if (d == 0 && c.lse)
       c.lse[(static_cast<int64_t>(b) * c.Hq + head) * c.Lq + tok] =
-          l[0] > 0.0f ? (m + fast_log2(l[0])) * kLn2 : -INFINITY;
+          l[0] == 0.0f ? -INFINITY : (m + fast_log2(l[0])) * kLn2;
   }
 }
 
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
           if (d == 0 && c.lse)
             c.lse[(static_cast<int64_t>(w.b) * c.Hq + head) * c.Lq + tok] =
-                ll > 0.0f ? (mm + fast_log2(ll)) * kLn2 : -INFINITY;
+                ll == 0.0f ? -INFINITY : (mm + fast_log2(ll)) * kLn2;
         }
       }
       if (p.joined) {

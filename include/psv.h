@@ -434,11 +434,12 @@ int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* pos, void*
  * A row sees key j if j < k_lens[b], q_doc == k_doc (where documents are
  * given) and, with causal set, k_pos <= q_pos or k_pos < prefix[b].
  *   o = softmax(s) v over the visible keys;  lse = log sum exp s  [B][Hq][Lq]
- * A row that sees nothing gets o = 0 and lse = -infinity.  Rows i >= q_lens[b]
- * of o and lse are left as they were.  Lengths are clamped to [0, Lq] and
- * [0, Lk].  o may be q itself (equal strides); otherwise o and lse meet neither
- * q, k, v nor one another.  Default positions: k_pos = j, q_pos = k_len - q_len
- * + i (the rows are the last ones of the sequence).  Positions lie within +-2^30.
+ * A row that sees nothing gets o = 0 and lse = -infinity; a row that sees a NaN
+ * score gets NaN in o and lse.  Rows i >= q_lens[b] of o and lse are left as they
+ * were.  Lengths are clamped to [0, Lq] and [0, Lk].  o may be q itself (equal strides); otherwise o and lse
+ * meet neither q, k, v nor one another.  Default positions: k_pos = j, q_pos =
+ * k_len - q_len + i (the rows are the last ones of the sequence).  Positions lie
+ * within +-2^30.
  * Keys and values behind k_lens[b] may hold anything (NaN too); keys that are
  * only masked may hold anything finite, their scores are not used.
  * Products take bf16/f16 operands and accumulate in f32; scores, maxima, sums
@@ -492,10 +493,11 @@ int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k
  * psv_cache_attention on the same problem (v and o are not used):
  *   mass_out[b][g][j] = mass_in[b][g][j]
  *                     + sum over rows i < q_lens[b] and heads h of group g of exp(s_ij - lse)
- * over visible pairs; mass f32 [B][Hkv][Lk]; mass_in may be NULL (zeros) or
- * mass_out (accumulate in place); mass_out meets neither q, k nor lse.  Entries
- * j >= k_lens[b] are left as they were.  Sums are f32 in a fixed order (repeats
- * are equal bit for bit).
+ * over visible pairs (a row whose lse is NaN gives NaN to the keys it sees, and
+ * may give it to others of its sequence and kv head); mass f32 [B][Hkv][Lk];
+ * mass_in may be NULL (zeros) or mass_out (accumulate in place); mass_out meets
+ * neither q, k nor lse.  Entries j >= k_lens[b] are left as they were.  Sums are
+ * f32 in a fixed order (repeats are equal bit for bit).
  * Requirements as above. */
 int psv_cache_mass(const psv_cache_problem* p, const void* q, const void* k, const float* lse,
                    const float* mass_in, float* mass_out, void* scratch, size_t scratch_bytes,

@@ -193,3 +193,53 @@ def test_garbage_does_not_choose_how_scores_are_capped(P):
             again = torch.zeros_like(mass)
             run_mass(P, c, lse, None, again)
             assert torch.equal(again, mass)
+
+# -------------------------------------------------------------------- NaN
+
+@pytest.mark.parametrize("kw", [
+    dict(Lq=3, Lk=300, dh=128), dict(Lq=3, Lk=300, dh=64, cap=20.0), dict(Lq=3, Lk=70, dh=7),
+    dict(Lq=60, Lk=300, dh=128), dict(Lq=60, Lk=9000, dh=64), dict(Lq=300, Lk=900, dh=64, slopes=True),
+    dict(Lq=60, Lk=300, dh=128, cap=20.0, dtype="f16"), dict(Lq=60, Lk=90, dh=7, cap=5.0, slopes=True),
+    dict(Lq=1, Lk=9000, dh=128),
+], ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_nan_in_a_query_row_is_not_a_row_that_sees_nothing(P, kw):
+    """Its output, lse and the weights of the keys it sees are NaN; no other row changes, and no
+    weight of another sequence or kv head."""
+    c = make(B=2, Hq=4, Hkv=2, causal=True, **kw)
+    o, lse = run_attention(P, c)
+    mass = torch.zeros(2, 2, c["Lk"], device="cuda")
+    run_mass(P, c, lse, None, mass)
+    i, h = c["Lq"] // 2, 3
+    c["q"][1, i, h, 2] = float("nan")
+    bad, bad_lse = run_attention(P, c)
+    hit = torch.zeros(2, c["Lq"], 4, dtype=torch.bool, device="cuda")
+    hit[1, i, h] = True
+    assert bad[hit].isnan().all() and bad_lse.transpose(1, 2)[hit].isnan().all()
+    assert torch.equal(bad[~hit], o[~hit]) and torch.equal(bad_lse.transpose(1, 2)[~hit], lse.transpose(1, 2)[~hit])
+
+    def check(got):
+        assert got[seen].isnan().all()
+        assert torch.equal(got[0], mass[0]) and torch.equal(got[1, 0], mass[1, 0])
+        rest = ~got[1, 1].isnan()
+        assert torch.equal(got[1, 1][rest], mass[1, 1][rest])
+
+    got = torch.zeros_like(mass)
+    run_mass(P, c, bad_lse, None, got)
+    seen = torch.zeros_like(mass, dtype=torch.bool)
+    seen[1, 1, :c["Lk"] - c["Lq"] + i + 1] = True
+    check(got)
+    # an lse of NaN alone (the row itself is good) says the same
+    c["q"][1, i, h, 2] = 0.25
+    run_mass(P, c, bad_lse, None, got)
+    check(got)
+
+
+@pytest.mark.parametrize("Lq,dh", [(3, 64), (60, 128), (20, 7)])
+def test_nan_in_a_key_that_a_row_sees(P, Lq, dh):
+    doc = (np.arange(300) % 3)[None]
+    c = make(B=1, Lq=Lq, Lk=300, Hq=2, Hkv=1, dh=dh, q_doc=(np.arange(Lq) % 3)[None], k_doc=doc)
+    c["k"][0, 4] = float("nan")  # of document 1
+    o, lse = run_attention(P, c)
+    hit = torch.arange(Lq, device="cuda") % 3 == 1
+    assert o[0, hit].isnan().all() and lse[0][:, hit].isnan().all()
+    assert not o[0, ~hit].isnan().any() and not lse[0][:, ~hit].isnan().any()
