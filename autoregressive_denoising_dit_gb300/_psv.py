@@ -50,7 +50,7 @@ EXPORTS = [
     "psv_set_graphs", "psv_set_profiling", "psv_kernel_times", "psv_debug_tap",
     "psv_debug_read_kv", "psv_attention_scratch_bytes", "psv_attention",
     "psv_attention_noalloc", "psv_attention_noalloc_status", "psv_debug_error_word",
-    "psv_cache_last_error", "psv_rope", "psv_cache_scratch_bytes", "psv_cache_attention",
+    "psv_cache_last_error", "psv_rope", "psv_cache_scratch_bytes", "psv_cache_status", "psv_cache_attention",
     "psv_cache_mass", "psv_cache_evict",
 ]
 
@@ -165,6 +165,7 @@ def lib() -> ctypes.CDLL:
             "psv_cache_last_error": (ctypes.c_char_p, []),
             "psv_rope": (i32, [ctypes.POINTER(RopeProblem), vp, vp, vp, vp]),
             "psv_cache_scratch_bytes": (i32, [ctypes.POINTER(CacheProblem), ctypes.POINTER(sz)]),
+            "psv_cache_status": (i32, [vp, ctypes.POINTER(i32), vp]),
             "psv_cache_attention": (i32, [ctypes.POINTER(CacheProblem), vp, vp, vp, vp, vp, vp, sz, vp]),
             "psv_cache_mass": (i32, [ctypes.POINTER(CacheProblem), vp, vp, vp, vp, vp, vp, sz, vp]),
             "psv_cache_evict": (i32, [ctypes.POINTER(EvictProblem), vp, vp, vp, vp, vp, vp, vp, vp]),
@@ -464,6 +465,14 @@ def psv_cache_scratch_bytes(prob: CacheProblem) -> int:
     n = ctypes.c_size_t()
     _cache_check(lib().psv_cache_scratch_bytes(ctypes.byref(prob), ctypes.byref(n)))
     return n.value
+
+
+def psv_cache_status(scratch_ptr: int, stream_ptr: int = 0) -> int:
+    """0, or nonzero if a device-side wait of a call on this workspace timed out, whose output is
+    then not valid; waits for the stream."""
+    st = ctypes.c_int32()
+    _cache_check(lib().psv_cache_status(scratch_ptr or None, ctypes.byref(st), stream_ptr or None))
+    return st.value
 
 
 def psv_cache_attention(prob: CacheProblem, q_ptr: int, k_ptr: int, v_ptr: int, o_ptr: int,

@@ -951,6 +951,20 @@ PSV_API int psv_cache_scratch_bytes(const psv_cache_problem* p, size_t* bytes) {
   return PSV_OK;
 }
 
+PSV_API int psv_cache_status(const void* scratch, int* status, void* cuda_stream) {
+  if (!scratch || !status) return cache_fail(PSV_EINVAL, "null pointer");
+  if (int r = check_scratch(const_cast<void*>(scratch), 0, 0)) return r;
+  int dev = 0;
+  if (int r = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return r;
+  if (int r = check_device(dev, scratch, "scratch")) return r;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  cudaStreamCaptureStatus capture;
+  if (int r = cuda_status(cudaStreamIsCapturing(st, &capture), "status")) return r;
+  if (capture != cudaStreamCaptureStatusNone) return cache_fail(PSV_EINVAL, "the stream is being captured");
+  if (int r = cuda_status(cudaMemcpyAsync(status, scratch, sizeof(int), cudaMemcpyDeviceToHost, st), "status")) return r;
+  return cuda_status(cudaStreamSynchronize(st), "status");
+}
+
 PSV_API int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k, const void* v,
                                 void* o, float* lse, void* scratch, size_t scratch_bytes,
                                 void* cuda_stream) {

@@ -436,10 +436,10 @@ int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* pos, void*
  *   o = softmax(s) v over the visible keys;  lse = log sum exp s  [B][Hq][Lq]
  * A row that sees nothing gets o = 0 and lse = -infinity; a row that sees a NaN
  * score gets NaN in o and lse.  Rows i >= q_lens[b] of o and lse are left as they
- * were.  Lengths are clamped to [0, Lq] and [0, Lk].  o may be q itself (equal strides); otherwise o and lse
- * meet neither q, k, v nor one another.  Default positions: k_pos = j, q_pos =
- * k_len - q_len + i (the rows are the last ones of the sequence).  Positions lie
- * within +-2^30.
+ * were.  Lengths are clamped to [0, Lq] and [0, Lk].  o may be q itself (equal
+ * strides); otherwise o and lse meet neither q, k, v nor one another.  Default
+ * positions: k_pos = j, q_pos = k_len - q_len + i (the rows are the last ones of
+ * the sequence).  Positions lie within +-2^30.
  * Keys and values behind k_lens[b] may hold anything (NaN too); keys that are
  * only masked may hold anything finite, their scores are not used.
  * Products take bf16/f16 operands and accumulate in f32; scores, maxima, sums
@@ -482,9 +482,16 @@ typedef struct psv_cache_problem {
  * (captured ones too) that do not overlap on the GPU.  The int at its start
  * becomes nonzero, and stays so, if a device-side wait of a call timed out (2 s
  * without progress); that call's output is not valid, and the workspace is
- * zeroed before reuse. */
+ * zeroed before reuse.  The calls return before the GPU has done its work, so
+ * they cannot say so: psv_cache_status does. */
 #define PSV_CACHE_SCRATCH_HEAD 256
 int psv_cache_scratch_bytes(const psv_cache_problem* p, size_t* bytes);
+
+/* Whether a call on this workspace timed out: waits for cuda_stream, then
+ * *status = the workspace's first int.  Not while the stream is captured.
+ * Errors: PSV_EINVAL, PSV_ECUDA. */
+int psv_cache_status(const void* scratch, int* status /* host */, void* cuda_stream);
+
 int psv_cache_attention(const psv_cache_problem* p, const void* q, const void* k, const void* v,
                         void* o, float* lse /* may be NULL */, void* scratch, size_t scratch_bytes,
                         void* cuda_stream);

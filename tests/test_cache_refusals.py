@@ -295,3 +295,9 @@ def test_areas_against_a_walk_over_all_bytes():
         args = (p, A, 9 * A, 5 * A, A + off // 2 * 2, 7 * A, 30 * A, 31 * A)
         (refused if meets else passes_the_areas)(*(("k_out overlaps k",) if meets else ()), P.psv_cache_evict, *args)
     assert 50 < met < 350
+
+
+def test_status_refuses():
+    refused("null", P.psv_cache_status, 0)
+    refused("256", P.psv_cache_status, A + 64)
+    assert P.lib().psv_cache_status(A, None, None) == P.PSV_EINVAL

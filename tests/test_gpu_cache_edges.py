@@ -243,3 +243,37 @@ def test_nan_in_a_key_that_a_row_sees(P, Lq, dh):
     hit = torch.arange(Lq, device="cuda") % 3 == 1
     assert o[0, hit].isnan().all() and lse[0][:, hit].isnan().all()
     assert not o[0, ~hit].isnan().any() and not lse[0][:, ~hit].isnan().any()
+
+
+# ------------------------------------------------------------------ status
+
+def test_status_of_a_workspace(P):
+    """0 after good calls; what a timed-out wait leaves in the first int; not within a capture."""
+    c = make(B=2, Lq=40, Lk=300, Hq=2, Hkv=2, dh=64)
+    prob = T.problem(P, c)
+    scratch, n = T.scratch_for(P, prob)
+    o, lse = torch.empty_like(c["q"]), torch.empty(2, 2, 40, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    P.psv_cache_attention(prob, at(c["q"]), at(c["k"]), at(c["v"]), at(o), at(lse), at(scratch), n, s.cuda_stream)
+    assert P.psv_cache_status(at(scratch), s.cuda_stream) == 0
+    assert P.psv_cache_status(at(scratch)) == 0
+    scratch[:4].view(torch.int32).fill_(3)
+    torch.cuda.synchronize()
+    assert P.psv_cache_status(at(scratch), s.cuda_stream) == 3
+    scratch.zero_()
+    host = torch.zeros(1024, dtype=torch.uint8)
+    with pytest.raises(P.PSVError) as e:
+        P.psv_cache_status((host.data_ptr() + 255) // 256 * 256, s.cuda_stream)
+    assert e.value.code == P.PSV_EINVAL and "device memory" in str(e.value)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        P.psv_cache_attention(prob, at(c["q"]), at(c["k"]), at(c["v"]), at(o), at(lse), at(scratch), n, stream())
+        with pytest.raises(P.PSVError) as e:
+            P.psv_cache_status(at(scratch), stream())
+        assert e.value.code == P.PSV_EINVAL and "captured" in str(e.value)
+    want = o.clone()
+    o.zero_()
+    g.replay()
+    assert P.psv_cache_status(at(scratch), stream()) == 0
+    assert torch.equal(o, want)
