@@ -255,8 +255,9 @@ struct Vec {
 };
 
 // (cos, sin) of pos * f_p.  pos * turn wraps modulo one turn in 64 bits, so
-// the angle is off by at most |pos| 2^-53 f_p whatever the position; of the
-// signed fraction in [-1/2, 1/2) turns 32 bits (1.5e-9 radians) are used.
+// the angle is off by at most |pos| 2^-53 f_p (and 2^-64 turns a position)
+// whatever the position; of the signed fraction in [-1/2, 1/2) turns 24 bits are
+// used (f32's: 9.4e-8 radians at half a turn, less towards zero).
 __device__ __forceinline__ float2 pair_angle(const RopeParams& p, int pair, int b, int64_t l) {
   if (2 * pair >= p.R) return make_float2(1.0f, 0.0f);
   const int pos = p.pos[b * p.pos_b + l * p.pos_l + p.axis[pair]];
@@ -344,6 +345,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
 
 // f / 2 pi as 64-bit fixed-point turns modulo one turn.
 uint64_t fixed_turns(double f) {
+  // (Of a small negative t, t - floor(t) would keep 2^-54 only: 1e-6 radians at 2^31.)
+  if (f < 0) return 0 - fixed_turns(-f);
   const double hi = 0.15915494309189535, lo = -9.839338337591997e-18;  // 1 / (2 pi)
   const double t = f * hi;
   const double e = std::fma(f, hi, -t) + f * lo;

@@ -277,3 +277,22 @@ def test_status_of_a_workspace(P):
     g.replay()
     assert P.psv_cache_status(at(scratch), stream()) == 0
     assert torch.equal(o, want)
+
+# -------------------------------------------------------------------- rope
+
+def test_rope_small_negative_frequencies_far_out(P):
+    """A frequency just below zero turns as exactly as one just above it, up to positions of 2^31."""
+    f = np.geomspace(1e-7, 1.0, 32)
+    x = torch.zeros(1, 500, 1, 64, device="cuda")
+    x[..., 0::2] = 1.0  # every pair becomes (cos, sin) of its angle: no rounding but theirs
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    pos = torch.randint(2**30, 2**31 - 1, (1, 500, 1), device="cuda", generator=g, dtype=torch.int32)
+    # The turns per position are off by 2^-64 (2^-30 radians over 2^31 positions), of an angle 24 bits
+    # are used (2^-23.3 radians), sine and cosine are good to 2 ulp (2^-23).
+    tol = 2.0**-29 + 2.0**-23.3 + 2.0**-23
+    for freqs in (f, -f):
+        out = torch.empty_like(x)
+        P.psv_rope(P.rope_problem(P.PSV_DTYPE_F32, x.shape, (64,), freqs=freqs), at(x), at(pos), at(out), stream())
+        ref, _ = T.rope_reference(x.double(), pos, (64,), freqs=freqs)
+        assert ((out.double() - ref).abs() <= tol).all(), float((out.double() - ref).abs().max())
