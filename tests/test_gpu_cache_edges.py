@@ -296,3 +296,132 @@ def test_rope_small_negative_frequencies_far_out(P):
         P.psv_rope(P.rope_problem(P.PSV_DTYPE_F32, x.shape, (64,), freqs=freqs), at(x), at(pos), at(out), stream())
         ref, _ = T.rope_reference(x.double(), pos, (64,), freqs=freqs)
         assert ((out.double() - ref).abs() <= tol).all(), float((out.double() - ref).abs().max())
+
+# ---------------------------------------- masks and positions on every path
+
+rng = np.random.default_rng(11)
+
+
+def ring(n, turn, B=1):
+    return np.broadcast_to((np.arange(n) + turn) % n, (B, n))
+
+
+def heads(B, H, n):
+    return np.stack([np.stack([rng.permutation(n) for _ in range(H)]) for _ in range(B)])
+
+
+COVER = {
+    # at most 16 rows a kv head
+    "token-ring": dict(B=2, Lq=1, Lk=500, Hq=4, Hkv=2, dh=128, causal=True, k_pos=ring(500, 133, 2), q_pos=[[499], [250]]),
+    "rows-ring-slopes": dict(B=2, Lq=4, Lk=333, Hq=4, Hkv=2, dh=64, causal=True, k_pos=ring(333, 100, 2), slopes=True,
+                             k_lens=[333, 217], dtype="f16"),
+    "rows-per-head": dict(B=2, Lq=3, Lk=500, Hq=6, Hkv=2, dh=80, causal=True, k_pos=heads(2, 2, 500), q_pos=[[3, 499, 200], [0, -4, 77]],
+                          slopes=True),
+    "rows-documents": dict(B=2, Lq=4, Lk=777, Hq=2, Hkv=2, dh=128, q_doc=[[0, 1, 2, 9], [2, 2, 0, 1]], k_doc=docs(2, 777, [1, 300, 640])),
+    "rows-documents-per-head": dict(B=1, Lq=2, Lk=300, Hq=4, Hkv=2, dh=64, q_doc=[[1, 2]], k_doc=rng.integers(0, 4, (1, 2, 300)), cap=20.0),
+    "rows-prefix": dict(B=3, Lq=4, Lk=260, Hq=2, Hkv=1, dh=128, causal=True, prefix=[100, 0, 9999], k_lens=[260, 33, 2], q_lens=[4, 1, 4]),
+    "rows-all": dict(B=2, Lq=2, Lk=400, Hq=8, Hkv=1, dh=128, causal=True, prefix=[50, 7], cap=30.0, slopes=True, k_lens=[400, 399],
+                     k_pos=ring(400, 31, 2), q_doc=[[0, 1], [1, 1]], k_doc=docs(2, 400, [200])),
+    "rows-shares": dict(B=1, Lq=1, Lk=9001, Hq=2, Hkv=1, dh=64, causal=True, k_pos=ring(9001, 77), q_doc=[[1]], k_doc=docs(1, 9001, [4000, 8000])),
+    # many rows, capped, with documents or positions
+    "cap-documents": dict(B=2, Lq=600, Lk=600, Hq=2, Hkv=1, dh=64, cap=20.0, q_doc=docs(2, 600, [1, 100, 357]), k_doc=docs(2, 600, [1, 100, 357])),
+    "cap-documents-wide": dict(B=1, Lq=700, Lk=700, Hq=2, Hkv=2, dh=128, cap=50.0, q_doc=docs(1, 700, [300, 301]), k_doc=docs(1, 700, [300, 301]),
+                               dtype="f16", causal=True),
+    "cap-ring": dict(B=2, Lq=300, Lk=1000, Hq=4, Hkv=2, dh=128, cap=30.0, causal=True, k_pos=ring(1000, 333, 2), k_lens=[1000, 700]),
+    "cap-ring-slopes": dict(B=2, Lq=300, Lk=1000, Hq=4, Hkv=2, dh=128, cap=30.0, causal=True, k_pos=ring(1000, 333, 2), slopes=True),
+    "cap-per-head-slopes": dict(B=1, Lq=260, Lk=700, Hq=4, Hkv=2, dh=64, cap=5.0, causal=True, k_pos=heads(1, 2, 700),
+                                q_pos=rng.integers(-10, 800, (1, 260)), slopes=True, dtype="f16"),
+    "cap-documents-slopes": dict(B=1, Lq=500, Lk=500, Hq=2, Hkv=1, dh=64, cap=10.0, slopes=True, q_doc=rng.integers(0, 3, (1, 500)),
+                                 k_doc=rng.integers(0, 3, (1, 500))),
+    "cap-prefix-lens": dict(B=3, Lq=300, Lk=600, Hq=2, Hkv=2, dh=128, cap=50.0, causal=True, prefix=[100, 0, 600], k_lens=[600, 300, 0],
+                            q_lens=[300, 299, 12]),
+    # the kernels for every layout
+    "general-ring": dict(B=2, Lq=20, Lk=150, Hq=2, Hkv=1, dh=7, causal=True, k_pos=ring(150, 40, 2), slopes=True, k_lens=[150, 99]),
+    "general-per-head": dict(B=1, Lq=9, Lk=100, Hq=4, Hkv=2, dh=256, causal=True, k_pos=heads(1, 2, 100), q_pos=rng.integers(0, 100, (1, 9)), cap=10.0),
+    "general-documents": dict(B=2, Lq=33, Lk=120, Hq=2, Hkv=2, dh=130, q_doc=docs(2, 33, [5, 20]), k_doc=docs(2, 120, [50, 70]), dtype="f16"),
+    "general-prefix": dict(B=2, Lq=40, Lk=90, Hq=2, Hkv=1, dh=36, causal=True, prefix=[60, 0], slopes=True, q_lens=[40, 3]),
+    "general-groups": dict(Lq=2, Lk=60, Hq=160, Hkv=1, dh=64, causal=True, slopes=True),
+}
+
+
+@pytest.mark.parametrize("name", COVER)
+def test_masks_and_positions(P, name):
+    c = make(**COVER[name])
+    o, lse = run_attention(P, c)
+    check_attention(c, o, lse)
+    mass_in = torch.rand(c["B"], c["Hkv"], c["Lk"], device="cuda")
+    out = torch.full_like(mass_in, 3.0)
+    run_mass(P, c, lse, mass_in, out)
+    check_mass(c, lse, mass_in, out, torch.full_like(out, 3.0))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(Lq=1, Hq=4, dh=128), dict(Lq=3, Hq=4, dh=64, cap=20.0), dict(Lq=2, Hq=16, dh=80, slopes=True, dtype="f16"),
+    dict(Lq=1, Hq=2, dh=32, causal=True), dict(Lq=7, Hq=2, dh=36), dict(Lq=100, Hq=4, dh=128), dict(Lq=100, Hq=4, dh=64, cap=20.0),
+    dict(Lq=300, Hq=6, dh=128, slopes=True, causal=True),
+], ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_what_lies_behind_the_lengths_changes_nothing(P, kw):
+    """NaN and infinities behind keys that end anywhere in a tile, and in unused rows: the same bits."""
+    n = [300, 257, 256, 97, 33, 32, 31, 1, 0]
+    Lq = kw["Lq"]
+    nq = [Lq, max(1, Lq - 1), Lq, Lq // 2, Lq, 1, Lq, 0, Lq]
+    c = make(B=len(n), Lk=300, Hkv=2, k_lens=n, q_lens=nq, **kw)
+    o, lse = run_attention(P, c)
+    check_attention(c, o, lse)
+    mass = torch.full((len(n), 2, 300), 2.0, device="cuda")
+    run_mass(P, c, lse, None, mass)
+    check_mass(c, lse, None, mass, torch.full_like(mass, 2.0))
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for b in range(len(n)):
+            c["k"][b, n[b]:] = bad
+            c["v"][b, n[b]:] = bad
+            c["v"][b, n[b]:, :, ::2] = float("nan")
+            c["q"][b, nq[b]:] = bad
+            lse[b, :, nq[b]:] = bad
+        got = run_attention(P, c, lse=torch.where(torch.isfinite(lse) | (lse == -math.inf), lse, torch.full_like(lse, 9.0)))
+        assert torch.equal(got[0], o)
+        for b in range(len(n)):
+            assert torch.equal(got[1][b, :, :nq[b]], lse[b, :, :nq[b]])
+        again = torch.full_like(mass, 2.0)
+        run_mass(P, c, lse, None, again)
+        assert torch.equal(again, mass)
+
+
+# ---------------------------------------------------------------- eviction
+
+EVICT = {
+    "8192": dict(B=1, L=8192, H=1, dh=8, budget=8000, sinks=4, recent=100),
+    "8193": dict(B=2, L=8193, H=1, dh=32, budget=3000, sinks=1, recent=700, lens=[8193, 8192], values="ties"),
+    "12480": dict(B=2, L=12480, H=3, dh=64, budget=9360, sinks=30, recent=1560, lens=[12480, 11000]),
+    "16384": dict(B=1, L=16384, H=2, dh=32, budget=16383, sinks=0, recent=0),
+    "16384-strange": dict(B=1, L=16384, H=1, dh=32, budget=700, sinks=3, recent=60, values="strange"),
+    "16385": dict(B=2, L=16385, H=1, dh=32, budget=5000, sinks=3, recent=60, lens=[16385, 3], values="ties"),
+    "20000": dict(B=2, L=20000, H=2, dh=64, budget=12000, sinks=4, recent=2000, lens=[20000, 12001]),
+    "20002-zeros": dict(B=1, L=20002, H=1, dh=7, budget=9, sinks=4, recent=5, values="zeros"),
+    "49152": dict(B=1, L=49152, H=1, dh=32, budget=30000, sinks=1, recent=1000, values="strange"),
+    "49153": dict(B=1, L=49153, H=1, dh=32, budget=30001, sinks=1, recent=1000, values="ties"),
+    "1023": dict(B=2, L=1023, H=2, dh=64, budget=600, sinks=1, recent=9, lens=[1023, 601], values="ties"),
+    "4097": dict(B=1, L=4097, H=2, dh=128, budget=2049, sinks=1, recent=9),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("name", EVICT)
+def test_evict_sizes(P, monkeypatch, name, dtype):
+    monkeypatch.setitem(T.EVICT, name, EVICT[name])
+    T.test_evict(P, name, dtype)
+
+
+def test_evict_unaligned_mass_of_many_slots(P):
+    """Rows of the mass that do not start on 16 bytes, in the selection with 32 slots a thread."""
+    L, n = 12481, 5000
+    k = torch.randn(1, L, 2, 32, device="cuda").half()
+    mass = torch.rand(2 * L + 1, device="cuda")[1:].view(1, 2, L)
+    ko, vo = (torch.zeros(1, n, 2, 32, device="cuda", dtype=torch.float16) for _ in range(2))
+    mo, idx = torch.zeros(1, 2, n, device="cuda"), torch.zeros(1, 2, n, device="cuda", dtype=torch.int32)
+    prob = P.evict_problem(P.PSV_DTYPE_F16, k.shape, n, 3, 1000)
+    P.psv_cache_evict(prob, at(k), at(k), at(mass), at(ko), at(vo), at(mo), at(idx), stream())
+    for h in range(2):
+        w = torch.as_tensor(T.evict_reference(dict(n=[L], budget=n, sinks=3, recent=1000, mass=mass), 0, h), device="cuda")
+        assert torch.equal(idx[0, h].long(), w) and torch.equal(mo[0, h], mass[0, h, w]) and torch.equal(ko[0, :, h], k[0, w, h])
+        assert torch.equal(vo[0, :, h], ko[0, :, h])
