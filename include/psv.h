@@ -475,8 +475,9 @@ typedef struct psv_cache_problem {
 } psv_cache_problem;
 
 /* Workspace of psv_cache_attention and psv_cache_mass for this problem (its
- * size depends on the shapes, on softcap and on which of the pointers are
- * given; a larger one serves as well):
+ * size depends on the shapes, on softcap, on which of the pointers are given and
+ * on whether k_meta_stride[1] is 0, as the kv heads' notes are then one; a larger
+ * one serves as well):
  * 256-byte aligned device memory whose first PSV_CACHE_SCRATCH_HEAD bytes the
  * caller zeroes once, before its first use.  It may serve any number of calls
  * (captured ones too) that do not overlap on the GPU.  The int at its start

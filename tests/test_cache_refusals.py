@@ -301,3 +301,12 @@ def test_status_refuses():
     refused("null", P.psv_cache_status, 0)
     refused("256", P.psv_cache_status, A + 64)
     assert P.lib().psv_cache_status(A, None, None) == P.PSV_EINVAL
+
+
+def test_workspace_of_shared_and_own_metadata():
+    """A workspace sized for documents that the kv heads share is too small for documents of each head."""
+    def size(**kw):
+        return P.psv_cache_scratch_bytes(P.cache_problem(P.PSV_DTYPE_BF16, (2, 500, 8, 64), (2, 9000, 4, 64), **kw))
+
+    docs = dict(q_doc=A, k_doc=A)
+    assert size() < size(**docs, k_meta_stride=(9000, 0)) < size(**docs, k_meta_stride=(36000, 9000))
