@@ -102,6 +102,12 @@ bool rows_distinct(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t
   return true;
 }
 
+// Whether two tensors at one address have their rows in the same places (an index
+// of extent one is never stepped).
+bool same_rows(const int64_t* a, const int64_t* b, int64_t n0, int64_t n1, int64_t n2) {
+  return (n0 == 1 || a[0] == b[0]) && (n1 == 1 || a[1] == b[1]) && (n2 == 1 || a[2] == b[2]);
+}
+
 // The bytes of a tensor: rows of `width` bytes, n[d] of them st[d] bytes apart
 // along each of three indexes.
 struct Area {
@@ -416,8 +422,7 @@ PSV_API int psv_rope(const psv_rope_problem* p, const void* x, const int32_t* po
       k.axis[pair] = static_cast<uint8_t>(a);
     }
   if (!x || !pos || !out) return cache_fail(PSV_EINVAL, "null pointer");
-  bool same = x == out;
-  for (int i = 0; i < 3; ++i) same = same && p->x_stride[i] == p->out_stride[i];
+  const bool same = x == out && same_rows(p->x_stride, p->out_stride, p->B, p->L, p->H);
   if (!same && x == out) return cache_fail(PSV_EINVAL, "in place needs equal strides");
   const uintptr_t mask = static_cast<uintptr_t>(size - 1);
   if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(out) & mask) || !on4({pos, p->lens}))
@@ -987,8 +992,8 @@ PSV_API int psv_cache_attention(const psv_cache_problem* p, const void* q, const
                        reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(o);
   if ((at & 1) || (reinterpret_cast<uintptr_t>(lse) & 3))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
-  bool in_place = q == o;  // every row of q is read before the row of o is written
-  for (int i = 0; i < 3; ++i) in_place = in_place && p->q_stride[i] == p->o_stride[i];
+  // (Every row of q is read before the row of o is written.)
+  const bool in_place = q == o && same_rows(p->q_stride, p->o_stride, p->B, p->Lq, p->Hq);
   const Area q_area = tensor_area("q", q, p->q_stride, p->B, p->Lq, p->Hq, p->dh, 2);
   const Area none = plain_area("", nullptr, 0);
   if (int r = check_areas(

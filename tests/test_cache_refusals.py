@@ -310,3 +310,14 @@ def test_workspace_of_shared_and_own_metadata():
 
     docs = dict(q_doc=A, k_doc=A)
     assert size() < size(**docs, k_meta_stride=(9000, 0)) < size(**docs, k_meta_stride=(36000, 9000))
+
+
+def test_in_place_with_strides_that_are_never_stepped():
+    """A view's batch stride differs from a dense one's, which does not matter to a batch of one."""
+    p = P.cache_problem(P.PSV_DTYPE_BF16, (1, 5, 6, 64), (1, 70, 2, 64), q_stride=(9999, 384, 64))
+    passes_the_areas(P.psv_cache_attention, p, A, 2 * A, 3 * A, A, 0, 5 * A, 1 << 30)
+    p = P.rope_problem(P.PSV_DTYPE_BF16, (1, 5, 3, 64), (24, 20, 20), x_stride=(7777, 192, 64))
+    with pytest.raises(P.PSVError) as e:
+        P.psv_rope(p, A, 2 * A, A)
+    assert "strides" not in str(e.value) and "overlap" not in str(e.value)
+    refused("equal strides", P.psv_rope, changed(rope, x_stride=(7777, 192, 64)), A, 2 * A, A)
