@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 import test_gpu_cache_ops as T  # noqa: E402
-from test_gpu_cache_ops import P, at, check_attention, check_mass, docs, ints, lens, make, run_attention, run_mass, stream  # noqa: E402,F401
+from test_gpu_cache_ops import P, at, check_attention, check_mass, code, docs, ints, lens, make, run_attention, run_mass, stream  # noqa: E402,F401
 
 
 # ---------------------------------------------------------------- in place
@@ -425,3 +425,94 @@ def test_evict_unaligned_mass_of_many_slots(P):
         w = torch.as_tensor(T.evict_reference(dict(n=[L], budget=n, sinks=3, recent=1000, mass=mass), 0, h), device="cuda")
         assert torch.equal(idx[0, h].long(), w) and torch.equal(mo[0, h], mass[0, h, w]) and torch.equal(ko[0, :, h], k[0, w, h])
         assert torch.equal(vo[0, :, h], ko[0, :, h])
+
+
+# ------------------------------------------------------ captured and replayed
+
+@pytest.mark.parametrize("kw", [
+    dict(B=2, Lq=300, Lk=900, Hq=4, Hkv=2, dh=128, causal=True, slopes=True),
+    dict(B=2, Lq=600, Lk=600, Hq=6, Hkv=3, dh=64, q_doc=docs(2, 600, [40, 41, 300]), k_doc=docs(2, 600, [40, 41, 300])),
+    dict(B=1, Lq=270, Lk=4300, Hq=20, Hkv=20, dh=32),                                            # a last unit in shares
+    dict(B=1, Lq=40, Lk=9000, Hq=2, Hkv=1, dh=128, cap=30.0, slopes=True),                       # shares of the keys
+    dict(B=2, Lq=90, Lk=500, Hq=4, Hkv=2, dh=64, cap=1e5, causal=True, k_pos=ring(500, 99, 2)),  # a wide cap
+    dict(B=2, Lq=9, Lk=200, Hq=2, Hkv=1, dh=7, causal=True),                                     # the general kernels
+], ids=["bias", "documents", "last-unit", "shares", "wide-cap-ring", "general"])
+def test_captured_many_rows(P, kw):
+    """Attention, mass and rope in one graph, and a second graph on the same workspace, replayed in
+    turn with other inputs and lengths: the eager calls' bits."""
+    full = [kw["Lk"]] * kw["B"]
+    c = make(k_lens=full, q_lens=[kw["Lq"]] * kw["B"], **kw)
+    prob = T.problem(P, c)
+    scratch, n = T.scratch_for(P, prob)
+    pos = torch.randint(0, 500, (c["B"], c["Lq"], 1), device="cuda", dtype=torch.int32)
+    dh = c["dh"] // 2 * 2
+    turn = P.rope_problem(code(P, c["dtype"]), (c["B"], c["Lq"], c["Hq"], dh), (dh,)) if dh == c["dh"] else None
+    raw = c["q"].clone()
+
+    def buffers():
+        return torch.zeros_like(c["q"]), torch.zeros(c["B"], c["Hq"], c["Lq"], device="cuda"), torch.zeros(c["B"], c["Hkv"], c["Lk"], device="cuda")
+
+    def calls(o, lse, mass):
+        if turn is not None:
+            P.psv_rope(turn, at(raw), at(pos), at(c["q"]), stream())
+        P.psv_cache_attention(prob, at(c["q"]), at(c["k"]), at(c["v"]), at(o), at(lse), at(scratch), n, stream())
+        P.psv_cache_mass(prob, at(c["q"]), at(c["k"]), at(lse), 0, at(mass), at(scratch), n, stream())
+        P.psv_cache_mass(prob, at(c["q"]), at(c["k"]), at(lse), at(mass), at(mass), at(scratch), n, stream())
+
+    one, two, want = buffers(), buffers(), buffers()
+    calls(*want)
+    torch.cuda.synchronize()
+    graphs = []
+    for out in (one, two):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            calls(*out)
+        graphs.append(g)
+    for step in range(3):
+        c["k_lens"].copy_(torch.tensor([max(0, x - 97 * step * (b + 1)) for b, x in enumerate(full)]))
+        c["q_lens"].copy_(torch.tensor([max(0, c["Lq"] - 31 * step * b) for b in range(c["B"])]))
+        (raw if turn is not None else c["q"]).normal_()
+        pos.random_(0, 10000)
+        for t in (*one, *two, *want):
+            t.zero_()
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+        calls(*want)
+        torch.cuda.synchronize()
+        for got in (one, two):
+            for x, y in zip(got, want):
+                assert torch.equal(x, y)
+    assert P.psv_cache_status(at(scratch), stream()) == 0
+
+
+def test_captured_eviction(P):
+    """A graph of an eviction follows the lengths and weights of its replay."""
+    B, L, H, dh, n = 2, 9000, 2, 64, 4000
+    k, v = (torch.randn(B, L, H, dh, device="cuda").to(torch.bfloat16) for _ in range(2))
+    mass, kl = torch.rand(B, H, L, device="cuda"), ints([L, L])
+
+    def buffers():
+        return [torch.zeros(B, n, H, dh, device="cuda", dtype=torch.bfloat16) for _ in range(2)] + [
+            torch.zeros(B, H, n, device="cuda"), torch.zeros(B, H, n, device="cuda", dtype=torch.int32), ints([0, 0])]
+
+    def call(ko, vo, mo, idx, ln):
+        prob = P.evict_problem(P.PSV_DTYPE_BF16, k.shape, n, 4, 500, k_lens=at(kl), lens_out=at(ln))
+        P.psv_cache_evict(prob, at(k), at(v), at(mass), at(ko), at(vo), at(mo), at(idx), stream())
+
+    got, want = buffers(), buffers()
+    call(*got)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(*got)
+    for new in ([L, L], [3999, 4001], [0, 8999]):
+        kl.copy_(torch.tensor(new))
+        mass.uniform_()
+        for t in got + want:
+            t.zero_()
+        g.replay()
+        call(*want)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
