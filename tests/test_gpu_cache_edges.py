@@ -516,3 +516,92 @@ def test_captured_eviction(P):
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+sys.path.insert(0, {tests!r})
+import torch
+import test_gpu_cache_ops as T
+from autoregressive_denoising_dit_gb300 import _psv as P
+c = T.make(B=2, Lq={Lq}, Lk=3000, Hq=4, Hkv=2, dh={dh}, causal=True, slopes={slopes}, cap={cap}, k_lens=[3000, 40])
+prob = T.problem(P, c)
+scratch, n = T.scratch_for(P, prob)
+x, pos = torch.randn(2, 9, 3, 64, device="cuda"), torch.arange(18, device="cuda", dtype=torch.int32).view(2, 9, 1)
+rope = P.rope_problem(P.PSV_DTYPE_F32, x.shape, (64,))
+ev = P.evict_problem(P.PSV_DTYPE_BF16, c["k"].shape, 700, 4, 100, k_lens=T.at(c["k_lens"]))
+
+def buffers():
+    return (torch.zeros_like(c["q"]), torch.zeros(2, 4, {Lq}, device="cuda"), torch.zeros(2, 2, 3000, device="cuda"), torch.zeros_like(x),
+            torch.zeros(2, 700, 2, {dh}, device="cuda", dtype=torch.bfloat16), torch.zeros(2, 700, 2, {dh}, device="cuda", dtype=torch.bfloat16),
+            torch.zeros(2, 2, 700, device="cuda"), torch.zeros(2, 2, 700, device="cuda", dtype=torch.int32))
+
+def calls(o, lse, mass, y, ko, vo, mo, idx):
+    at, st = T.at, T.stream()
+    P.psv_rope(rope, at(x), at(pos), at(y), st)
+    P.psv_cache_attention(prob, at(c["q"]), at(c["k"]), at(c["v"]), at(o), at(lse), at(scratch), n, st)
+    P.psv_cache_mass(prob, at(c["q"]), at(c["k"]), at(lse), 0, at(mass), at(scratch), n, st)
+    P.psv_cache_evict(ev, at(c["k"]), at(c["v"]), at(mass), at(ko), at(vo), at(mo), at(idx), st)
+
+got, want = buffers(), buffers()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls(*got)
+g.replay()
+calls(*want)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and float(want[1].abs().sum()) > 0
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("kw", [dict(Lq=1, dh=128, slopes=False, cap=0.0), dict(Lq=300, dh=128, slopes=False, cap=0.0),
+                                dict(Lq=300, dh=64, slopes=True, cap=0.0), dict(Lq=90, dh=128, slopes=True, cap=500.0)],
+                         ids=lambda k: f"{k['Lq']}-{k['dh']}-{k['cap']}")
+def test_a_process_may_begin_with_a_capture(kw):
+    """The first calls of a process, before any kernel is loaded, go into a graph."""
+    import os
+    import subprocess
+    import sys
+
+    tests = os.path.dirname(os.path.abspath(__file__))
+    src = FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests, **kw)
+    r = subprocess.run([sys.executable, "-c", src], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-1000:] + r.stderr[-3000:]
+
+
+def test_calls_from_four_threads(P):
+    """Calls at the same time, each thread with its own stream, workspace and outputs; errors stay with their thread."""
+    import threading
+
+    kinds = [dict(B=2, Lq=1, Lk=700, Hq=4, Hkv=2, dh=128), dict(B=1, Lq=300, Lk=900, Hq=2, Hkv=1, dh=64, causal=True),
+             dict(B=1, Lq=40, Lk=5000, Hq=2, Hkv=2, dh=128, slopes=True), dict(B=2, Lq=90, Lk=600, Hq=2, Hkv=1, dh=64, cap=20.0)]
+    cases = [make(seed=i, **kw) for i, kw in enumerate(kinds)]
+    want = [run_attention(P, c) for c in cases]
+    bad = []
+
+    def work(i):
+        try:
+            c, s = cases[i], torch.cuda.Stream()
+            prob = T.problem(P, c)
+            scratch, n = T.scratch_for(P, prob)
+            o, lse = torch.zeros_like(c["q"]), torch.zeros_like(want[i][1])
+            torch.cuda.synchronize()
+            for k in range(200):
+                P.psv_cache_attention(prob, at(c["q"]), at(c["k"]), at(c["v"]), at(o), at(lse), at(scratch), n, s.cuda_stream)
+                if k % 20 == i:
+                    with pytest.raises(P.PSVError, match=f"scratch of {i} bytes"):
+                        P.psv_cache_attention(prob, at(c["q"]), at(c["k"]), at(c["v"]), at(o), at(lse), at(scratch), i, s.cuda_stream)
+            assert P.psv_cache_status(at(scratch), s.cuda_stream) == 0
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+        except BaseException as e:  # noqa: BLE001 (handed to the test's thread)
+            bad.append((i, e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
