@@ -25,17 +25,27 @@
 //   warp 3       even CTA: takes pieces from the work queue, publishes them
 //   warps 4..11  softmax, two threads per query row (lanes l and l + 16), 128
 //                keys each, through 16-lane TMEM accesses
+// The weights are rounded to the operand type for P V: both operands of a product
+// have 16 bits, and f32 weights would take two or three times the products.  That
+// and the output's rounding are what o differs by from 32-bit arithmetic (bf16,
+// relative to 64 bits: 1.8e-3 to 2.3e-3, with f32 weights 1.6e-3 to 1.7e-3; f16
+// 2.9e-4, 2.1e-4); l is the sum of the weights before they are rounded.
 // The softmax paces a tile, not the tensor cores: 2500 clocks against 2048 of
 // products (of a tile's clocks, 570 go into the maximum, 1650 into the weights
 // and their way to TMEM), and so does what a feature adds to it: the cap 1400
 // clocks (four packed FMA-pipe operations a pair), masks seen key by key 1200.
+// It is latency more than issue: two softmax warps a scheduler, each a chain of
+// TMEM reads, the maximum, the weights and their way back, use 39% of the issue
+// slots (with the cap 51%) and 33% of the exponential unit.
 // Between pieces 3000 clocks are lost (the last P.V, O's way out, the next
 // piece's notes); issuing the next piece's first S ahead of the last P.V was
 // measured slower (short sequences 80 -> 84 us).
-// Measured, 12 heads of 128, bf16: 12480 rows x 12480 keys 582 us (1640 TFLOP/s),
-// four sequences of 1560 rows x 7800 keys 211 us (1415; 13% of its row tiles are
-// empty), with the distance bias 226, with the cap 291; nine documents of 12480
-// rows 131 us.
+// Measured, calls on the same inputs one after another, 12 heads of 128, bf16:
+// 12480 rows x 12480 keys 547 to 585 us (1640 to 1750 TFLOP/s, as the power cap
+// allows), four sequences of 1560 rows x 7800 keys 211 us (1415; 13% of its row tiles
+// are empty), with the distance bias 227 (243 where inputs change from call to
+// call), with a cap of 50 285 (scores of deviation 8: 404); nine documents of 12480
+// rows 132 us.
 // Pieces are taken from a device counter (the first of a pair is its own
 // index) that the last pair to finish rewinds.  Shares of a long cache leave
 // O, m and l in a workspace and a second small kernel joins them in a fixed

@@ -1,8 +1,11 @@
 // Attention over a cache and the attention mass for every layout, alignment
 // and head width the calls accept: plain loads, one warp per row (or per
 // key), 32-bit arithmetic throughout.  The tensor-core kernels take the
-// aligned problems; these are bound by their uncoalesced 2-byte loads and are
-// some tens of times slower (a fallback for odd layouts, not tuned).
+// aligned problems; these are bound by their uncoalesced 2-byte loads, which they
+// repeat for every row, and are hundreds of times slower (a fallback for odd
+// layouts, not tuned): eight tokens over 7800 keys of 12 heads of 256 8.5 ms, of
+// 128 in the few-row kernel 67 us; 1560 rows x 1560 keys of 12 heads of 136 8.9 ms,
+// their mass 6.9 ms, of 128 on the tensor cores 30 and 22 us.
 #include "cache_kernels.h"
 
 namespace psv {

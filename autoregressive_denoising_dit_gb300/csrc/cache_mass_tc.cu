@@ -14,7 +14,8 @@
 // (Measured no faster: -lse added by the products, the two halves of the warps
 // on tiles of their own, the row notes read a tile ahead; slower: eight warps,
 // S^T held double in registers.)  Four sequences of 1560 rows x 7800 keys, 12
-// heads of 128: 162 us (925 TFLOP/s).
+// heads of 128: 162 us (925 TFLOP/s), causal 155, with a cap of 50 248 (scores of
+// deviation 8: 330), with the distance bias 283.
 // A row's -lse, position limit, document and slope are noted per tile in shared
 // memory by a warp of their own.  Warp roles, 640 threads:
 //   warp 0       TMA: the piece's K tile (2 buffers), the row tiles (4 stages);

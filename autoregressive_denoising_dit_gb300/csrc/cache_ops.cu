@@ -276,9 +276,10 @@ __device__ __forceinline__ float2 pair_angle(const RopeParams& p, int pair, int 
 
 // A thread holds one unit (VEC values of a head, or for HALVES VEC values and
 // their partners R/2 further on) of a row, computes its angles once and
-// applies them to hpt heads.  Memory-bound: one read and one write of x.  Four
-// sequences of 1560 rows x 12 heads of 128 in bf16 take 12.1 us (launch 4,
-// 38 MB), 12480 rows x 40 heads in f32 93 us (5.5 TB/s).
+// applies them to hpt heads, kFlight at a time.  Memory-bound where large: one
+// read and one write of x (12480 rows x 40 heads of 128 in f32 93 us, 5.5 TB/s).
+// Four sequences of 1560 rows x 12 heads in bf16 (38 MB) take 12.1 us, of which the
+// launch is 4: a thread's 12 heads are three rounds of loads, one after another.
 template <class T, int VEC, bool HALVES>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
   using V = Vec<T, VEC>;

@@ -12,8 +12,8 @@
 // joined in shared memory at the end of a piece, the shares by the CTA that
 // ends the last of them, or where there are many by cache_join_kernel.  The next piece's queries are read while the current one
 // runs.  Measured, heads of 128: eight single tokens over 7800 keys of 12 heads
-// 58.9 us with the join (5.4 TB/s; the pieces are 8% uneven over the SMs), one
-// token over 65536 keys 61.5 us (6.5 TB/s), the mass of eight tokens 31.9 us.
+// 59.2 us with the join (5.4 TB/s; the pieces are 8% uneven over the SMs), one
+// token over 65536 keys 61 us (6.6 TB/s), the mass of eight tokens 31.5 us.
 #include <cuda.h>
 
 #include "../../include/psv.h"

@@ -471,7 +471,7 @@ typedef struct psv_cache_problem {
   const int32_t* k_doc;     /* [B][Hkv][Lk] */
   int64_t k_meta_stride[2]; /* batch and kv-head strides of k_pos and k_doc (0: shared) */
   const int32_t* prefix;    /* [B]; NULL: 0 */
-  const float* slopes;      /* [Hq]; NULL: no distance bias */
+  const float* slopes;      /* [Hq], at most 1e30 in size; NULL: no distance bias */
 } psv_cache_problem;
 
 /* Workspace of psv_cache_attention and psv_cache_mass for this problem (its
