@@ -52,12 +52,18 @@ EXPORTS = [
     "psv_attention_noalloc", "psv_attention_noalloc_status", "psv_debug_error_word",
     "psv_cache_last_error", "psv_rope", "psv_cache_scratch_bytes", "psv_cache_status", "psv_cache_attention",
     "psv_cache_mass", "psv_cache_evict",
+    "psv_page_write", "psv_page_read", "psv_page_scratch_bytes", "psv_page_attention",
 ]
 
 PSV_ATTN_NOALLOC_SCRATCH_BYTES = 16 << 20
 PSV_CACHE_SCRATCH_HEAD = 256
 PSV_ROPE_PAIRS = 0
 PSV_ROPE_HALVES = 1
+PSV_PAGE_BF16 = 1
+PSV_PAGE_F16 = 2
+PSV_PAGE_E4M3 = 3
+PSV_PAGE_I8 = 4
+PSV_PAGE_SCRATCH_HEAD = 8192
 
 
 class ModelDesc(ctypes.Structure):
@@ -117,6 +123,26 @@ class EvictProblem(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("pos_out", "doc_out", "lens_out")]
 
 
+class PageCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("format", "B", "n_pages", "page_size", "max_pages", "Hkv", "dh")] + \
+               [(n, ctypes.c_int64 * 3) for n in ("k_stride", "v_stride", "scale_stride")] + \
+               [("table_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_void_p) for n in ("table", "k_pages", "v_pages", "k_scales", "v_scales")]
+
+
+class PageRows(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("L", ctypes.c_int32)] + \
+               [(n, ctypes.c_int64 * 3) for n in ("k_stride", "v_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("starts", "lens")]
+
+
+class PageQuery(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "Lq", "Hq", "causal", "window", "sinks", "append")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float)] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_stride", "o_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("q_lens", "k_lens")]
+
+
 class PSVError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"libpsv error {code}: {msg}")
@@ -169,6 +195,12 @@ def lib() -> ctypes.CDLL:
             "psv_cache_attention": (i32, [ctypes.POINTER(CacheProblem), vp, vp, vp, vp, vp, vp, sz, vp]),
             "psv_cache_mass": (i32, [ctypes.POINTER(CacheProblem), vp, vp, vp, vp, vp, vp, sz, vp]),
             "psv_cache_evict": (i32, [ctypes.POINTER(EvictProblem), vp, vp, vp, vp, vp, vp, vp, vp]),
+            "psv_page_write": (i32, [ctypes.POINTER(PageCache), ctypes.POINTER(PageRows), vp, vp, vp]),
+            "psv_page_read": (i32, [ctypes.POINTER(PageCache), ctypes.POINTER(PageRows), vp, vp, vp]),
+            "psv_page_scratch_bytes": (i32, [ctypes.POINTER(PageCache), ctypes.POINTER(PageQuery),
+                                             ctypes.POINTER(sz)]),
+            "psv_page_attention": (i32, [ctypes.POINTER(PageCache), ctypes.POINTER(PageQuery), vp, vp, vp, vp,
+                                         sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -509,3 +541,68 @@ def psv_cache_evict(prob: EvictProblem, k_ptr: int, v_ptr: int, mass_ptr: int, k
                     v_out_ptr: int, mass_out_ptr: int, idx_out_ptr: int, stream_ptr: int = 0) -> None:
     _cache_check(lib().psv_cache_evict(ctypes.byref(prob), k_ptr, v_ptr, mass_ptr, k_out_ptr,
                                        v_out_ptr, mass_out_ptr, idx_out_ptr, stream_ptr or None))
+
+
+# ---------------------------------------------- operators of a paged cache
+
+def page_cache(format: int, table_shape, n_pages: int, page_size: int, Hkv: int, dh: int, table: int,
+               k_pages: int, v_pages: int, k_scales: int = 0, v_scales: int = 0, k_stride=None,
+               v_stride=None, scale_stride=None, table_stride: int | None = None) -> PageCache:
+    """psv_page_cache of a table [B][max_pages] over pages [n_pages][Hkv][page_size][dh] with
+    scales [n_pages][Hkv][page_size]; strides (page, row, head) in values (default: dense in
+    that order), the rest device pointers (0: none)."""
+    B, max_pages = table_shape
+    dense = (Hkv * page_size * dh, dh, page_size * dh)
+    c = PageCache(format=format, B=B, n_pages=n_pages, page_size=page_size, max_pages=max_pages, Hkv=Hkv,
+                  dh=dh, k_stride=_strides(k_stride or dense), v_stride=_strides(v_stride or dense),
+                  scale_stride=_strides(scale_stride or (Hkv * page_size, 1, page_size)),
+                  table=table or None, k_pages=k_pages or None, v_pages=v_pages or None,
+                  k_scales=k_scales or None, v_scales=v_scales or None)
+    c.table_stride = max_pages if table_stride is None else table_stride
+    return c
+
+
+def page_rows(dtype: int, shape, k_stride=None, v_stride=None, starts: int = 0, lens: int = 0) -> PageRows:
+    """psv_page_rows of k, v [B][L][Hkv][dh]; strides in elements (default: dense), the rest
+    device pointers (0: none)."""
+    _, L, H, dh = shape
+    return PageRows(dtype=dtype, L=L, k_stride=_strides(k_stride, L, H, dh),
+                    v_stride=_strides(v_stride, L, H, dh), starts=starts or None, lens=lens or None)
+
+
+def page_query(dtype: int, shape, q_stride=None, o_stride=None, causal: bool = False, window: int = 0,
+               sinks: int = 0, scale: float = 0.0, softcap: float = 0.0, q_lens: int = 0, k_lens: int = 0,
+               append: bool = False) -> PageQuery:
+    """psv_page_query of q, o [B][Lq][Hq][dh]; strides in elements (default: dense), lengths
+    device pointers (0: none)."""
+    _, L, H, dh = shape
+    return PageQuery(dtype=dtype, Lq=L, Hq=H, causal=int(causal), window=window, sinks=sinks,
+                     append=int(append), scale=scale, softcap=softcap,
+                     q_stride=_strides(q_stride, L, H, dh), o_stride=_strides(o_stride, L, H, dh),
+                     q_lens=q_lens or None, k_lens=k_lens or None)
+
+
+def psv_page_write(cache: PageCache, rows: PageRows, k_ptr: int, v_ptr: int, stream_ptr: int = 0) -> None:
+    """Quantises rows and writes them into their pages."""
+    _cache_check(lib().psv_page_write(ctypes.byref(cache), ctypes.byref(rows), k_ptr or None, v_ptr or None,
+                                      stream_ptr or None))
+
+
+def psv_page_read(cache: PageCache, rows: PageRows, k_ptr: int, v_ptr: int, stream_ptr: int = 0) -> None:
+    """Reads rows back out of their pages."""
+    _cache_check(lib().psv_page_read(ctypes.byref(cache), ctypes.byref(rows), k_ptr or None, v_ptr or None,
+                                     stream_ptr or None))
+
+
+def psv_page_scratch_bytes(cache: PageCache, query: PageQuery) -> int:
+    n = ctypes.c_size_t()
+    _cache_check(lib().psv_page_scratch_bytes(ctypes.byref(cache), ctypes.byref(query), ctypes.byref(n)))
+    return n.value
+
+
+def psv_page_attention(cache: PageCache, query: PageQuery, q_ptr: int, o_ptr: int, lse_ptr: int,
+                       scratch_ptr: int, scratch_bytes: int, stream_ptr: int = 0) -> None:
+    """Attention of new rows over the pages."""
+    _cache_check(lib().psv_page_attention(ctypes.byref(cache), ctypes.byref(query), q_ptr or None,
+                                          o_ptr or None, lse_ptr or None, scratch_ptr or None, scratch_bytes,
+                                          stream_ptr or None))

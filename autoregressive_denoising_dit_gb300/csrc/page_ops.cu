@@ -1,0 +1,493 @@
+// Entry points of the paged-cache operators (include/psv.h): argument checks,
+// and the kernels that write rows into pages and read them back.  The attention
+// over pages is launched from here.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <type_traits>
+
+#include "cache_check.h"
+#include "page_kernels.h"
+#include "psv_device.cuh"
+#include "psv_kernels.h"
+
+using namespace psv;
+
+namespace {
+
+bool scaled(int format) { return format == PSV_PAGE_E4M3 || format == PSV_PAGE_I8; }
+int page_esize(int format) { return scaled(format) ? 1 : 2; }
+
+// Rows of sequence b: number i of [0, L) at position starts[b] + i.
+struct PageRowsParams {
+  PageCacheDev c;
+  int L, H, dh, lanes;  // lanes of a row (log2): 8 values each
+  FastDiv by_head;
+  Strides3 xs[2];
+  void* x[2];  // k, v
+  const int32_t *starts, *lens;
+};
+
+constexpr float kTiny = 0x1p-100f;  // a row whose largest size is below it is kept as zeros
+
+template <int FMT>
+struct PageFormat {
+  static constexpr bool kScaled = FMT == PSV_PAGE_E4M3 || FMT == PSV_PAGE_I8;
+  static constexpr float kMost = FMT == PSV_PAGE_E4M3 ? 448.0f : 127.0f;
+  static constexpr int kSize = kScaled ? 1 : 2;
+};
+
+// Two values as they are stored, from the lower half on.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  if constexpr (FMT == PSV_PAGE_BF16) return pack_bf16x2(lo, hi);
+  if constexpr (FMT == PSV_PAGE_F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  if constexpr (FMT == PSV_PAGE_E4M3) return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+  if constexpr (FMT == PSV_PAGE_I8)
+    return (static_cast<uint32_t>(__float2int_rn(lo)) & 0xff) | (static_cast<uint32_t>(__float2int_rn(hi)) & 0xff) << 8;
+}
+template <int FMT>
+__device__ __forceinline__ float2 decode2(uint32_t u) {
+  if constexpr (FMT == PSV_PAGE_BF16)
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  if constexpr (FMT == PSV_PAGE_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  if constexpr (FMT == PSV_PAGE_E4M3) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  }
+  if constexpr (FMT == PSV_PAGE_I8)
+    return make_float2(static_cast<float>(static_cast<int8_t>(u)), static_cast<float>(static_cast<int8_t>(u >> 8)));
+}
+
+// Eight values of a program's row, as they are in memory.
+template <class T>
+struct Eight {
+  static constexpr int kFmt = sizeof(T) == 2 ? (std::is_same<T, __half>::value ? PSV_PAGE_F16 : PSV_PAGE_BF16) : 0;
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* x) {
+#pragma unroll
+    for (size_t i = 0; i < sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(x)[i];
+  }
+  __device__ __forceinline__ void load(const T* x, int n) {  // value by value
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) v[i] = x[i];
+      else reinterpret_cast<uint16_t*>(&v[i])[0] = 0, reinterpret_cast<uint16_t*>(&v[i])[sizeof(T) / 2 - 1] = 0;
+    memcpy(u, v, sizeof(v));
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (sizeof(T) == 4) {
+      memcpy(f, u, 32);
+    } else {
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = decode2<kFmt>(w[i]);
+        f[2 * i] = y.x, f[2 * i + 1] = y.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    if constexpr (sizeof(T) == 4) {
+      memcpy(u, f, 32);
+    } else {
+      u[0] = make_uint4(encode2<kFmt>(f[0], f[1]), encode2<kFmt>(f[2], f[3]), encode2<kFmt>(f[4], f[5]),
+                        encode2<kFmt>(f[6], f[7]));
+    }
+  }
+  __device__ __forceinline__ void store(T* x) const {
+#pragma unroll
+    for (size_t i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(x)[i] = u[i];
+  }
+  __device__ __forceinline__ void store(T* x, int n) const {
+    T v[8];
+    memcpy(v, u, sizeof(v));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) x[i] = v[i];
+  }
+};
+
+constexpr int kRowThreads = 256;
+
+// A row (a head of a token) belongs to 2^lanes threads of a warp, eight values
+// each, which find its largest size by shuffles; a thread has kR rows on their
+// way.  grid (rows, sequence, key or value).
+template <class T, int FMT, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_constant__ PageRowsParams p) {
+  using F = PageFormat<FMT>;
+  constexpr int kR = sizeof(T) == 4 ? 2 : 4;
+  const int b = blockIdx.y, kv = blockIdx.z;
+  const int step = kRowThreads >> p.lanes, lane = threadIdx.x & ((1 << p.lanes) - 1), d = lane * 8;
+  const uint32_t r0 = blockIdx.x * static_cast<uint32_t>(step * kR) + (threadIdx.x >> p.lanes);
+  pdl_trigger();
+  pdl_wait();
+  const int n = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
+  const int start = p.starts ? p.starts[b] : 0;
+  const T* x = static_cast<const T*>(p.x[kv]) + b * p.xs[kv].b;
+  Eight<T> in[kR];
+  PageRow at[kR];
+  int head[kR];
+#pragma unroll
+  for (int k = 0; k < kR; ++k) {
+    const uint32_t r = r0 + k * step, i = p.by_head.div(r);
+    head[k] = static_cast<int>(r - i * p.by_head.d);
+    at[k].page = -1;
+    if (i >= static_cast<uint32_t>(n)) continue;
+    if (d < p.dh) {
+      const T* row = x + i * p.xs[kv].l + head[k] * p.xs[kv].h + d;
+      if (VEC) in[k].load(row);
+      else in[k].load(row, p.dh - d);
+    }
+    at[k] = page_row(p.c, b, static_cast<int64_t>(start) + i);
+  }
+  const Strides3& ps = kv ? p.c.vs : p.c.ks;
+  char* pages = static_cast<char*>(kv ? p.c.v : p.c.k);
+#pragma unroll
+  for (int k = 0; k < kR; ++k) {
+    float f[8];
+    if (d < p.dh) in[k].get(f);
+    float turn = 1.0f;
+    if constexpr (F::kScaled) {
+      uint32_t size = 0;  // bits of |x|, by which NaN is above infinity
+      if (d < p.dh)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) size = max(size, __float_as_uint(f[j]) & 0x7fffffffu);
+      for (int o = 1 << p.lanes >> 1; o; o >>= 1) size = max(size, __shfl_xor_sync(0xffffffffu, size, o));
+      const float most = __uint_as_float(size);
+      const bool finite = size < 0x7f800000u, zero = most < kTiny;
+      turn = finite && !zero ? __fdiv_rn(F::kMost, most) : 0.0f;
+      if (lane == 0 && at[k].page >= 0)
+        (kv ? p.c.v_scale : p.c.k_scale)[at[k].page * p.c.ss.b + at[k].row * p.c.ss.l + head[k] * p.c.ss.h] =
+            !finite ? __int_as_float(0x7fc00000) : zero ? 0.0f : __fdiv_rn(most, F::kMost);
+    }
+    if (d >= p.dh || at[k].page < 0) continue;
+    if constexpr (F::kScaled) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = turn > 0.0f ? f[j] * turn : 0.0f;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = encode2<FMT>(f[2 * j], f[2 * j + 1]);
+    char* out = pages + (at[k].page * ps.b + at[k].row * ps.l + head[k] * ps.h + d) * F::kSize;
+    if constexpr (F::kScaled) {
+      const uint2 y = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      if (VEC) *reinterpret_cast<uint2*>(out) = y;
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (d + j < p.dh) out[j] = static_cast<char>((j < 4 ? y.x : y.y) >> 8 * (j % 4));
+    } else {
+      if (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (d + j < p.dh) reinterpret_cast<uint16_t*>(out)[j] = static_cast<uint16_t>(w[j / 2] >> 16 * (j % 2));
+    }
+  }
+}
+
+// The same threads read rows back; positions without a page read as zeros.
+template <class T, int FMT, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) page_read_kernel(const __grid_constant__ PageRowsParams p) {
+  using F = PageFormat<FMT>;
+  constexpr int kR = 4;
+  const int b = blockIdx.y, kv = blockIdx.z;
+  const int step = kRowThreads >> p.lanes, d = (threadIdx.x & ((1 << p.lanes) - 1)) * 8;
+  const uint32_t r0 = blockIdx.x * static_cast<uint32_t>(step * kR) + (threadIdx.x >> p.lanes);
+  pdl_trigger();
+  pdl_wait();
+  if (d >= p.dh) return;
+  const int n = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
+  const int start = p.starts ? p.starts[b] : 0;
+  const Strides3& ps = kv ? p.c.vs : p.c.ks;
+  const char* pages = static_cast<const char*>(kv ? p.c.v : p.c.k);
+  const float* scales = kv ? p.c.v_scale : p.c.k_scale;
+  T* x = static_cast<T*>(p.x[kv]) + b * p.xs[kv].b + d;
+  PageRow at[kR];
+  uint32_t row[kR];
+  int head[kR];
+#pragma unroll
+  for (int k = 0; k < kR; ++k) {
+    const uint32_t r = r0 + k * step;
+    row[k] = p.by_head.div(r);
+    head[k] = static_cast<int>(r - row[k] * p.by_head.d);
+    at[k].page = -1;
+    if (row[k] < static_cast<uint32_t>(n)) at[k] = page_row(p.c, b, static_cast<int64_t>(start) + row[k]);
+  }
+  uint32_t w[kR][4];
+  float s[kR];
+#pragma unroll
+  for (int k = 0; k < kR; ++k) {
+    w[k][0] = w[k][1] = w[k][2] = w[k][3] = 0;
+    s[k] = 0.0f;
+    if (at[k].page < 0) continue;
+    const char* in = pages + (at[k].page * ps.b + at[k].row * ps.l + head[k] * ps.h + d) * F::kSize;
+    if constexpr (F::kScaled) {
+      s[k] = scales[at[k].page * p.c.ss.b + at[k].row * p.c.ss.l + head[k] * p.c.ss.h];
+      if (VEC) {
+        const uint2 y = *reinterpret_cast<const uint2*>(in);
+        w[k][0] = y.x, w[k][2] = y.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (d + j < p.dh) w[k][j / 4 * 2] |= static_cast<uint32_t>(static_cast<uint8_t>(in[j])) << 8 * (j % 4);
+      }
+    } else if (VEC) {
+      const uint4 y = *reinterpret_cast<const uint4*>(in);
+      w[k][0] = y.x, w[k][1] = y.y, w[k][2] = y.z, w[k][3] = y.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (d + j < p.dh)
+          w[k][j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(in)[j]) << 16 * (j % 2);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kR; ++k) {
+    if (row[k] >= static_cast<uint32_t>(n)) continue;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = decode2<FMT>(F::kScaled ? w[k][j / 2 * 2] >> 16 * (j % 2) & 0xffff : w[k][j]);
+      f[2 * j] = F::kScaled ? y.x * s[k] : y.x;
+      f[2 * j + 1] = F::kScaled ? y.y * s[k] : y.y;
+    }
+    Eight<T> out;
+    out.set(f);
+    T* y = x + row[k] * p.xs[kv].l + head[k] * p.xs[kv].h;
+    if (VEC) out.store(y);
+    else out.store(y, p.dh - d);
+  }
+}
+
+template <class T, int FMT>
+cudaError_t launch_page_rows(const PageRowsParams& p, int B, bool vec, bool write, cudaStream_t st) {
+  const uint32_t rows = static_cast<uint32_t>(p.L) * p.H;
+  const uint32_t each = (kRowThreads >> p.lanes) * (write && sizeof(T) == 4 ? 2 : 4);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((rows + each - 1) / each, B, 2), kRowThreads, 0, st, attr);
+  if (write)
+    return vec ? cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true>, p)
+               : cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, false>, p);
+  return vec ? cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true>, p)
+             : cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, false>, p);
+}
+
+template <class T>
+cudaError_t launch_page_rows_any(const PageRowsParams& p, int B, bool vec, bool write, cudaStream_t st) {
+  switch (p.c.format) {
+    case PSV_PAGE_E4M3: return launch_page_rows<T, PSV_PAGE_E4M3>(p, B, vec, write, st);
+    case PSV_PAGE_I8: return launch_page_rows<T, PSV_PAGE_I8>(p, B, vec, write, st);
+    case PSV_PAGE_BF16:
+      if constexpr (!std::is_same<T, __half>::value) return launch_page_rows<T, PSV_PAGE_BF16>(p, B, vec, write, st);
+      break;
+    default:
+      if constexpr (!std::is_same<T, __nv_bfloat16>::value) return launch_page_rows<T, PSV_PAGE_F16>(p, B, vec, write, st);
+  }
+  return cudaErrorInvalidValue;  // (refused before)
+}
+
+// ---------------------------------------------------------------- checks
+
+// A tensor's reach in bytes, in a type that cannot overflow; false if it is none
+// that an address space holds.
+bool reach_ok(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t width, int size) {
+  const double reach = (static_cast<double>(s[0]) * (n0 - 1) + static_cast<double>(s[1]) * (n1 - 1) +
+                        static_cast<double>(s[2]) * (n2 - 1) + width) * size;
+  return reach < 0x1p56;
+}
+
+int check_page_cache(const psv_page_cache* c) {
+  if (!c) return cache_fail(PSV_EINVAL, "null cache");
+  if (c->format < PSV_PAGE_BF16 || c->format > PSV_PAGE_I8) return cache_fail(PSV_EINVAL, "unknown page format %d", c->format);
+  if (c->B < 1 || c->B > 65535 || c->Hkv < 1) return cache_fail(PSV_EINVAL, "need B of 1 to 65535 and Hkv >= 1");
+  if (c->dh < 1 || c->dh > 256) return cache_fail(PSV_EINVAL, "dh %d: 1 to 256", c->dh);
+  if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1)
+    return cache_fail(PSV_EINVAL, "need n_pages, page_size, max_pages >= 1");
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > (1 << 30))
+    return cache_fail(PSV_EINVAL, "the table covers over 2^30 positions");
+  if (static_cast<int64_t>(c->B) * c->Hkv > (1 << 24)) return cache_fail(PSV_EINVAL, "over 2^24 sequences x heads");
+  if (!stride_ok(c->k_stride, 3) || !stride_ok(c->v_stride, 3) || !stride_ok(&c->table_stride, 1) ||
+      (scaled(c->format) && !stride_ok(c->scale_stride, 3)))
+    return cache_fail(PSV_EINVAL, "strides must lie in [0, 2^40]");
+  const int size = page_esize(c->format);
+  if (!reach_ok(c->k_stride, c->n_pages, c->page_size, c->Hkv, c->dh, size) ||
+      !reach_ok(c->v_stride, c->n_pages, c->page_size, c->Hkv, c->dh, size) ||
+      (scaled(c->format) && !reach_ok(c->scale_stride, c->n_pages, c->page_size, c->Hkv, 1, 4)))
+    return cache_fail(PSV_EINVAL, "the pages reach over 2^56 bytes");
+  if (!c->k_pages || !c->v_pages || !c->table || (scaled(c->format) && (!c->k_scales || !c->v_scales)))
+    return cache_fail(PSV_EINVAL, "null pointer");
+  if ((reinterpret_cast<uintptr_t>(c->k_pages) | reinterpret_cast<uintptr_t>(c->v_pages)) & (size - 1))
+    return cache_fail(PSV_EINVAL, "pages must be aligned to their type");
+  if (!on4({c->table, scaled(c->format) ? c->k_scales : nullptr, scaled(c->format) ? c->v_scales : nullptr}))
+    return cache_fail(PSV_EINVAL, "tables and scales must be aligned to 4 bytes");
+  return PSV_OK;
+}
+
+PageCacheDev page_cache_dev(const psv_page_cache* c) {
+  PageCacheDev d{};
+  d.format = c->format, d.n_pages = c->n_pages, d.page_size = c->page_size;
+  d.positions = c->max_pages * c->page_size;
+  d.by_page = FastDiv::of(static_cast<uint32_t>(c->page_size));
+  d.ks = strides3(c->k_stride), d.vs = strides3(c->v_stride), d.ss = strides3(c->scale_stride);
+  d.table = c->table, d.table_b = c->table_stride;
+  d.k = c->k_pages, d.v = c->v_pages, d.k_scale = c->k_scales, d.v_scale = c->v_scales;
+  return d;
+}
+
+// The bytes of a cache's parts.
+struct PageAreas {
+  Area k, v, ks, vs, table;
+  explicit PageAreas(const psv_page_cache* c) {
+    const int size = page_esize(c->format);
+    k = tensor_area("k_pages", c->k_pages, c->k_stride, c->n_pages, c->page_size, c->Hkv, c->dh, size);
+    v = tensor_area("v_pages", c->v_pages, c->v_stride, c->n_pages, c->page_size, c->Hkv, c->dh, size);
+    auto scales = [&](const char* name, const void* at) {
+      return scaled(c->format) ? tensor_area(name, at, c->scale_stride, c->n_pages, c->page_size, c->Hkv, 1, 4)
+                               : plain_area(name, nullptr, 0);
+    };
+    ks = scales("k_scales", c->k_scales), vs = scales("v_scales", c->v_scales);
+    const int64_t st[3] = {c->table_stride, 0, 0};
+    table = tensor_area("table", c->table, st, c->B, 1, 1, c->max_pages, 4);
+  }
+};
+
+int page_rows_call(const psv_page_cache* c, const psv_page_rows* r, const void* k, const void* v, bool write,
+                   void* cuda_stream) {
+  if (int e = check_page_cache(c)) return e;
+  if (!r) return cache_fail(PSV_EINVAL, "null rows");
+  const int size = dtype_size(r->dtype);
+  if (!size) return cache_fail(PSV_EINVAL, "unknown dtype %d", r->dtype);
+  if ((c->format == PSV_PAGE_BF16 && r->dtype == PSV_DTYPE_F16) || (c->format == PSV_PAGE_F16 && r->dtype == PSV_DTYPE_BF16))
+    return cache_fail(PSV_EINVAL, "rows of one 16-bit type, pages of the other");
+  if (r->L < 0 || static_cast<int64_t>(r->L) * c->Hkv > (1 << 30))
+    return cache_fail(PSV_EINVAL, "L %d: not negative, L x Hkv at most 2^30", r->L);
+  if (!stride_ok(r->k_stride, 3) || !stride_ok(r->v_stride, 3)) return cache_fail(PSV_EINVAL, "strides must lie in [0, 2^40]");
+  if (r->L == 0) return PSV_OK;
+  if (!reach_ok(r->k_stride, c->B, r->L, c->Hkv, c->dh, size) || !reach_ok(r->v_stride, c->B, r->L, c->Hkv, c->dh, size))
+    return cache_fail(PSV_EINVAL, "the rows reach over 2^56 bytes");
+  if (write) {
+    const int pages[3] = {c->n_pages, c->page_size, c->Hkv};
+    if (!rows_distinct(c->k_stride, pages[0], pages[1], pages[2], c->dh) ||
+        !rows_distinct(c->v_stride, pages[0], pages[1], pages[2], c->dh) ||
+        (scaled(c->format) && !rows_distinct(c->scale_stride, pages[0], pages[1], pages[2], 1)))
+      return cache_fail(PSV_EINVAL, "the pages' rows overlap");
+  } else if (!rows_distinct(r->k_stride, c->B, r->L, c->Hkv, c->dh) || !rows_distinct(r->v_stride, c->B, r->L, c->Hkv, c->dh)) {
+    return cache_fail(PSV_EINVAL, "the rows of k or v overlap");
+  }
+  if (!k || !v) return cache_fail(PSV_EINVAL, "null pointer");
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & (size - 1))
+    return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  if (!on4({r->starts, r->lens})) return cache_fail(PSV_EINVAL, "starts and lengths must be aligned to 4 bytes");
+  const PageAreas a(c);
+  const Area ka = tensor_area("k", k, r->k_stride, c->B, r->L, c->Hkv, c->dh, size);
+  const Area va = tensor_area("v", v, r->v_stride, c->B, r->L, c->Hkv, c->dh, size);
+  const Area starts = plain_area("starts", r->starts, c->B * int64_t{4}), lens = plain_area("lens", r->lens, c->B * int64_t{4});
+  if (int e = write ? check_areas({a.k, a.v, a.ks, a.vs}, {ka, va, a.table, starts, lens})
+                    : check_areas({ka, va}, {a.k, a.v, a.ks, a.vs, a.table, starts, lens}))
+    return e;
+  int dev = 0;
+  if (int e = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return e;
+  if (int e = check_device(dev, k, "k")) return e;
+  if (int e = check_device(dev, c->k_pages, "k_pages")) return e;
+  PageRowsParams p{};
+  p.c = page_cache_dev(c);
+  p.L = r->L, p.H = c->Hkv, p.dh = c->dh;
+  while (8 << p.lanes < c->dh) ++p.lanes;
+  p.by_head = FastDiv::of(static_cast<uint32_t>(c->Hkv));
+  p.xs[0] = strides3(r->k_stride), p.xs[1] = strides3(r->v_stride);
+  p.x[0] = const_cast<void*>(k), p.x[1] = const_cast<void*>(v);
+  p.starts = r->starts, p.lens = r->lens;
+  const int es = page_esize(c->format);
+  auto eights = [&](const void* at, const int64_t* s) {  // eight stored values as one access
+    return (reinterpret_cast<uintptr_t>(at) & (8 * es - 1)) == 0 && (s[0] | s[1] | s[2]) % 8 == 0;
+  };
+  const bool vec = c->dh % 8 == 0 && multiple16(k, r->k_stride, c->B, r->L, c->Hkv, size) &&
+                   multiple16(v, r->v_stride, c->B, r->L, c->Hkv, size) && eights(c->k_pages, c->k_stride) &&
+                   eights(c->v_pages, c->v_stride);
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const cudaError_t e = r->dtype == PSV_DTYPE_F32    ? launch_page_rows_any<float>(p, c->B, vec, write, st)
+                        : r->dtype == PSV_DTYPE_BF16 ? launch_page_rows_any<__nv_bfloat16>(p, c->B, vec, write, st)
+                                                     : launch_page_rows_any<__half>(p, c->B, vec, write, st);
+  return cuda_status(e, write ? "page write launch" : "page read launch");
+}
+
+int check_page_query(const psv_page_cache* c, const psv_page_query* q) {
+  if (int e = check_page_cache(c)) return e;
+  if (!q) return cache_fail(PSV_EINVAL, "null query");
+  if (q->dtype != PSV_DTYPE_BF16 && q->dtype != PSV_DTYPE_F16) return cache_fail(PSV_EINVAL, "dtype %d: bf16 or f16", q->dtype);
+  if ((c->format == PSV_PAGE_BF16 && q->dtype == PSV_DTYPE_F16) || (c->format == PSV_PAGE_F16 && q->dtype == PSV_DTYPE_BF16))
+    return cache_fail(PSV_EINVAL, "queries of one 16-bit type, pages of the other");
+  if (q->Hq < 1 || q->Hq % c->Hkv) return cache_fail(PSV_EINVAL, "Hq (%d) must be a multiple of Hkv (%d)", q->Hq, c->Hkv);
+  if (q->Lq < 0 || q->Lq > (1 << 20)) return cache_fail(PSV_EINVAL, "Lq %d: 0 to 2^20", q->Lq);
+  if (static_cast<int64_t>(c->B) * q->Hq > (1 << 24)) return cache_fail(PSV_EINVAL, "over 2^24 sequences x heads");
+  if (q->window < 0 || q->sinks < 0) return cache_fail(PSV_EINVAL, "window and sinks must not be negative");
+  if (q->sinks && !q->window) return cache_fail(PSV_EINVAL, "sinks need a window");
+  if (!(std::isfinite(q->scale) && q->scale >= 0)) return cache_fail(PSV_EINVAL, "scale must be finite and not negative");
+  if (!(std::isfinite(q->softcap) && q->softcap >= 0)) return cache_fail(PSV_EINVAL, "softcap must be finite and not negative");
+  if (!stride_ok(q->q_stride, 3) || !stride_ok(q->o_stride, 3)) return cache_fail(PSV_EINVAL, "strides must lie in [0, 2^40]");
+  if (q->Lq && (!reach_ok(q->q_stride, c->B, q->Lq, q->Hq, c->dh, 2) || !reach_ok(q->o_stride, c->B, q->Lq, q->Hq, c->dh, 2)))
+    return cache_fail(PSV_EINVAL, "the rows reach over 2^56 bytes");
+  if (!on4({q->q_lens, q->k_lens})) return cache_fail(PSV_EINVAL, "lengths must be aligned to 4 bytes");
+  return PSV_OK;
+}
+
+}  // namespace
+
+PSV_API int psv_page_write(const psv_page_cache* c, const psv_page_rows* r, const void* k, const void* v,
+                           void* cuda_stream) {
+  return page_rows_call(c, r, k, v, true, cuda_stream);
+}
+
+PSV_API int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void* v, void* cuda_stream) {
+  return page_rows_call(c, r, k, v, false, cuda_stream);
+}
+
+PSV_API int psv_page_scratch_bytes(const psv_page_cache* c, const psv_page_query* q, size_t* bytes) {
+  if (int e = check_page_query(c, q)) return e;
+  if (!bytes) return cache_fail(PSV_EINVAL, "null pointer");
+  *bytes = PSV_PAGE_SCRATCH_HEAD;
+  return PSV_OK;
+}
+
+PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q, const void* x, void* o, float* lse,
+                               void* scratch, size_t scratch_bytes, void* cuda_stream) {
+  if (int e = check_page_query(c, q)) return e;
+  if (q->Lq == 0) return PSV_OK;
+  if (!rows_distinct(q->o_stride, c->B, q->Lq, q->Hq, c->dh)) return cache_fail(PSV_EINVAL, "o's rows overlap");
+  if (!x || !o || !scratch) return cache_fail(PSV_EINVAL, "null pointer");
+  if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(o)) & 1) || (reinterpret_cast<uintptr_t>(lse) & 3))
+    return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
+  const size_t need = PSV_PAGE_SCRATCH_HEAD;
+  if (reinterpret_cast<uintptr_t>(scratch) & 255) return cache_fail(PSV_EINVAL, "scratch must be 256-byte aligned");
+  if (scratch_bytes < need) return cache_fail(PSV_EINVAL, "scratch of %zu bytes, %zu needed", scratch_bytes, need);
+  const bool in_place = x == o && same_rows(q->q_stride, q->o_stride, c->B, q->Lq, q->Hq);
+  const PageAreas a(c);
+  if (int e = check_areas(
+          {tensor_area("o", o, q->o_stride, c->B, q->Lq, q->Hq, c->dh, 2),
+           plain_area("lse", lse, static_cast<int64_t>(c->B) * q->Hq * q->Lq * 4), plain_area("scratch", scratch, need)},
+          {in_place ? plain_area("", nullptr, 0) : tensor_area("q", x, q->q_stride, c->B, q->Lq, q->Hq, c->dh, 2), a.k, a.v,
+           a.ks, a.vs, a.table, plain_area("q_lens", q->q_lens, c->B * int64_t{4}),
+           plain_area("k_lens", q->k_lens, c->B * int64_t{4})}))
+    return e;
+  int dev = 0;
+  if (int e = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return e;
+  if (int e = check_device(dev, x, "q")) return e;
+  if (int e = check_device(dev, o, "o")) return e;
+  PageAttnParams p{};
+  p.c = page_cache_dev(c);
+  p.B = c->B, p.Hq = q->Hq, p.Hkv = c->Hkv, p.G = q->Hq / c->Hkv, p.dh = c->dh, p.Lq = q->Lq;
+  p.causal = q->causal != 0, p.window = q->window, p.sinks = q->sinks, p.append = q->append != 0;
+  p.bf16 = q->dtype == PSV_DTYPE_BF16;
+  p.scale = q->scale > 0 ? q->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c->dh)));
+  p.softcap = q->softcap;
+  p.qs = strides3(q->q_stride), p.os = strides3(q->o_stride);
+  p.q = x, p.o = o, p.lse = lse, p.q_lens = q->q_lens, p.k_lens = q->k_lens;
+  return cuda_status(launch_page_attention_general(p, static_cast<cudaStream_t>(cuda_stream)), "page attention launch");
+}

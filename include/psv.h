@@ -541,6 +541,109 @@ typedef struct psv_evict_problem {
 int psv_cache_evict(const psv_evict_problem* p, const void* k, const void* v, const float* mass,
                     void* k_out, void* v_out, float* mass_out, int32_t* idx_out, void* cuda_stream);
 
+/* ---- kernel-level operators of a paged key/value cache ---------------------
+ *
+ * The pages keep the keys and values of the preceding chunks (AREX article,
+ * §难题) and say nothing about how a server of many streams holds them.  These
+ * calls keep the caches of all streams in one pool of pages, in 16 bits or in
+ * 8 with a scale for each token and head: rows are written (and quantised) into
+ * pages, read back as plain tensors, which psv_cache_attention takes for a
+ * chunk's many rows, and looked at by a new token, or a few, in place.
+ *
+ * The conventions of the rolling cache's calls hold, psv_cache_last_error()
+ * among them.  Tables, starts and lengths are read on the device when the kernels
+ * run.  The pages' content is psv_page_write's, or equal to what it would write. */
+
+#define PSV_PAGE_BF16 1 /* values as they are (rounded, from F32 rows)                */
+#define PSV_PAGE_F16  2
+#define PSV_PAGE_E4M3 3 /* 8-bit floats, scale = (largest size of the row) / 448      */
+#define PSV_PAGE_I8   4 /* 8-bit integers of -127 to 127, scale = (largest size) / 127 */
+
+/* The cache.  Position j of sequence b lies in row j mod page_size of page
+ * table[b][j / page_size].  An entry outside [0, n_pages) names no page, and
+ * positions behind max_pages x page_size have none: rows written there are
+ * dropped, they read back as zeros, and attention does not see them.  Sequences
+ * may share pages.
+ * A row (one head's dh values of one key or value) is kept, in 8 bits, as
+ * code = nearest(x * (M / size)), ties to even, and scale = size / M, with size the
+ * largest |x| of the row and M = 448 or 127, in f32 arithmetic; it stands for
+ * code * scale.  A row with size below 2^-100 is kept as zeros with scale 0; one
+ * that holds a NaN or an infinity has the scale NaN and reads back as NaN.
+ * Requirements: 1 <= B <= 65535; n_pages, page_size, max_pages, Hkv >= 1;
+ * max_pages x page_size <= 2^30; B x Hkv <= 2^24; 1 <= dh <= 256; strides in
+ * [0, 2^40]. */
+typedef struct psv_page_cache {
+  int32_t format, B, n_pages, page_size, max_pages, Hkv, dh;
+  int64_t k_stride[3], v_stride[3]; /* page, row, head, in stored values */
+  int64_t scale_stride[3];          /* page, row, head, of k_scales and v_scales */
+  int64_t table_stride;             /* of a sequence (0: shared) */
+  const int32_t* table;             /* [B][max_pages] */
+  void *k_pages, *v_pages;          /* [n_pages][page_size][Hkv][dh] in any order of the indexes */
+  float *k_scales, *v_scales;       /* [n_pages][page_size][Hkv]; NULL for 16-bit pages */
+} psv_page_cache;
+
+/* Rows k, v [B][L][Hkv][dh] of a program: row i of sequence b is position
+ * starts[b] + i.  dtype F32, BF16 or F16 (16-bit pages: their own type or F32);
+ * L >= 0, L x Hkv <= 2^30. */
+typedef struct psv_page_rows {
+  int32_t dtype, L;
+  int64_t k_stride[3], v_stride[3]; /* batch, row, head */
+  const int32_t* starts;            /* [B]; NULL: 0 */
+  const int32_t* lens;              /* [B] rows in use, clamped to [0, L]; NULL: L */
+} psv_page_rows;
+
+/* Writes the rows in use into their pages.  Of two rows that one call writes to one
+ * place either's values may stay, and the other's scale.  Rows of pages must be
+ * distinct; pages and scales that meet an input or one another are refused (k and
+ * v may be packed into one buffer).  Multiples of 8 as dh and strides of pages,
+ * and of 16 bytes as strides of k and v and as all bases, use wide accesses. */
+int psv_page_write(const psv_page_cache* c, const psv_page_rows* r, const void* k, const void* v,
+                   void* cuda_stream);
+
+/* Reads positions back into k and v, rounded once; rows not in use are left as
+ * they were.  k and v meet neither the cache nor one another. */
+int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void* v, void* cuda_stream);
+
+/* Attention of rows over the pages.  q, o [B][Lq][Hq][dh]; query head h reads key
+ * head h / (Hq / Hkv).  With n = k_lens[b] (append: + q_lens[b], where k_lens
+ * counts the keys before this call's rows), row i stands at position
+ * p = n - q_lens[b] + i and sees key j < n if it has a page and
+ *   causal: j <= p;     window > 0: j > p - window, or j < sinks
+ *   s = scale * q.k; softcap > 0: s = softcap * tanh(s / softcap)
+ *   o = softmax(s) v;  lse = log sum exp s  [B][Hq][Lq]
+ * A row that sees nothing gets o = 0 and lse = -infinity; one that sees a NaN score
+ * gets NaN in both.  Rows i >= q_lens[b] of o and lse are left as they were.  o may
+ * be q itself (equal strides).  Keys that no row sees may hold anything, and so may
+ * keys and values that are masked for some rows.
+ * Products take f16 operands (bf16 ones for BF16 pages) and accumulate in f32: 8-bit
+ * codes are exact in f16, queries get a power of two for each row first, a key's
+ * scale is applied to its score and a value's to its weight, in f32.  Scores,
+ * maxima, sums and lse are f32; the weights are rounded to the operand type for
+ * their product with v, the output once.  Results repeat bit for bit for the same
+ * lengths; those of a sequence may differ in their roundings where the lengths
+ * of others change, as the work is shared out among the SMs by all of them.
+ * Requirements: dtype BF16 or F16 (16-bit pages: their own); Hq a multiple of Hkv;
+ * B x Hq <= 2^24; 0 <= Lq <= 2^20; window, sinks >= 0, sinks need a window; scale,
+ * softcap >= 0 finite; o's rows distinct. */
+typedef struct psv_page_query {
+  int32_t dtype, Lq, Hq, causal, window, sinks, append;
+  float scale;                      /* 0: 1 / sqrt(dh) */
+  float softcap;                    /* 0: none */
+  int64_t q_stride[3], o_stride[3]; /* batch, row, head */
+  const int32_t* q_lens;            /* [B], clamped to [0, Lq]; NULL: Lq */
+  const int32_t* k_lens;            /* [B], clamped to [0, max_pages x page_size]; NULL: that (append: 0) */
+} psv_page_query;
+
+/* Workspace of psv_page_attention: 256-byte aligned device memory whose first
+ * PSV_PAGE_SCRATCH_HEAD bytes the caller zeroes once, before its first use.  It may
+ * serve any number of calls (captured ones too, of any problem that it is large
+ * enough for) that do not overlap on the GPU. */
+#define PSV_PAGE_SCRATCH_HEAD 8192
+int psv_page_scratch_bytes(const psv_page_cache* c, const psv_page_query* q, size_t* bytes);
+
+int psv_page_attention(const psv_page_cache* c, const psv_page_query* q, const void* x /* q */, void* o,
+                       float* lse /* may be NULL */, void* scratch, size_t scratch_bytes, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
