@@ -77,4 +77,9 @@ __device__ __forceinline__ int page_length(const PageAttnParams& p, int b, int r
 
 cudaError_t launch_page_attention_general(const PageAttnParams& p, cudaStream_t st);
 
+// For rows and pages of 16-byte pieces and heads of up to 128: the workspace
+// (head included; Lq, G and dh count) and the launch on `sms` SMs.
+size_t page_attn_scratch(const PageAttnParams& p);
+cudaError_t launch_page_attention(const PageAttnParams& p, int sms, cudaStream_t st);
+
 }  // namespace psv

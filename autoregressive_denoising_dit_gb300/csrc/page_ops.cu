@@ -427,6 +427,7 @@ int check_page_query(const psv_page_cache* c, const psv_page_query* q) {
   if (q->Hq < 1 || q->Hq % c->Hkv) return cache_fail(PSV_EINVAL, "Hq (%d) must be a multiple of Hkv (%d)", q->Hq, c->Hkv);
   if (q->Lq < 0 || q->Lq > (1 << 20)) return cache_fail(PSV_EINVAL, "Lq %d: 0 to 2^20", q->Lq);
   if (static_cast<int64_t>(c->B) * q->Hq > (1 << 24)) return cache_fail(PSV_EINVAL, "over 2^24 sequences x heads");
+  if (static_cast<int64_t>(q->Lq) * q->Hq > (1 << 30)) return cache_fail(PSV_EINVAL, "Lq x Hq over 2^30");
   if (q->window < 0 || q->sinks < 0) return cache_fail(PSV_EINVAL, "window and sinks must not be negative");
   if (q->sinks && !q->window) return cache_fail(PSV_EINVAL, "sinks need a window");
   if (!(std::isfinite(q->scale) && q->scale >= 0)) return cache_fail(PSV_EINVAL, "scale must be finite and not negative");
@@ -436,6 +437,26 @@ int check_page_query(const psv_page_cache* c, const psv_page_query* q) {
     return cache_fail(PSV_EINVAL, "the rows reach over 2^56 bytes");
   if (!on4({q->q_lens, q->k_lens})) return cache_fail(PSV_EINVAL, "lengths must be aligned to 4 bytes");
   return PSV_OK;
+}
+
+PageAttnParams page_attn_params(const psv_page_cache* c, const psv_page_query* q) {
+  PageAttnParams p{};
+  p.c = page_cache_dev(c);
+  p.B = c->B, p.Hq = q->Hq, p.Hkv = c->Hkv, p.G = q->Hq / c->Hkv, p.dh = c->dh, p.Lq = q->Lq;
+  p.causal = q->causal != 0, p.window = q->window, p.sinks = q->sinks, p.append = q->append != 0;
+  p.bf16 = q->dtype == PSV_DTYPE_BF16;
+  p.scale = q->scale > 0 ? q->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c->dh)));
+  p.softcap = q->softcap;
+  p.qs = strides3(q->q_stride), p.os = strides3(q->o_stride);
+  p.q_lens = q->q_lens, p.k_lens = q->k_lens;
+  return p;
+}
+
+// Whether heads are made of 16-byte pieces in the pages (and 16-bit rows).
+bool page_attn_pieces(const psv_page_cache* c) { return c->dh <= 128 && c->dh * page_esize(c->format) % 16 == 0; }
+
+size_t page_scratch(const psv_page_cache* c, const PageAttnParams& p) {
+  return page_attn_pieces(c) ? page_attn_scratch(p) : PSV_PAGE_SCRATCH_HEAD;
 }
 
 }  // namespace
@@ -452,7 +473,7 @@ PSV_API int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void*
 PSV_API int psv_page_scratch_bytes(const psv_page_cache* c, const psv_page_query* q, size_t* bytes) {
   if (int e = check_page_query(c, q)) return e;
   if (!bytes) return cache_fail(PSV_EINVAL, "null pointer");
-  *bytes = PSV_PAGE_SCRATCH_HEAD;
+  *bytes = page_scratch(c, page_attn_params(c, q));
   return PSV_OK;
 }
 
@@ -464,7 +485,8 @@ PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q,
   if (!x || !o || !scratch) return cache_fail(PSV_EINVAL, "null pointer");
   if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(o)) & 1) || (reinterpret_cast<uintptr_t>(lse) & 3))
     return cache_fail(PSV_EINVAL, "pointers must be aligned to their type");
-  const size_t need = PSV_PAGE_SCRATCH_HEAD;
+  PageAttnParams p = page_attn_params(c, q);
+  const size_t need = page_scratch(c, p);
   if (reinterpret_cast<uintptr_t>(scratch) & 255) return cache_fail(PSV_EINVAL, "scratch must be 256-byte aligned");
   if (scratch_bytes < need) return cache_fail(PSV_EINVAL, "scratch of %zu bytes, %zu needed", scratch_bytes, need);
   const bool in_place = x == o && same_rows(q->q_stride, q->o_stride, c->B, q->Lq, q->Hq);
@@ -480,14 +502,19 @@ PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q,
   if (int e = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return e;
   if (int e = check_device(dev, x, "q")) return e;
   if (int e = check_device(dev, o, "o")) return e;
-  PageAttnParams p{};
-  p.c = page_cache_dev(c);
-  p.B = c->B, p.Hq = q->Hq, p.Hkv = c->Hkv, p.G = q->Hq / c->Hkv, p.dh = c->dh, p.Lq = q->Lq;
-  p.causal = q->causal != 0, p.window = q->window, p.sinks = q->sinks, p.append = q->append != 0;
-  p.bf16 = q->dtype == PSV_DTYPE_BF16;
-  p.scale = q->scale > 0 ? q->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c->dh)));
-  p.softcap = q->softcap;
-  p.qs = strides3(q->q_stride), p.os = strides3(q->o_stride);
-  p.q = x, p.o = o, p.lse = lse, p.q_lens = q->q_lens, p.k_lens = q->k_lens;
-  return cuda_status(launch_page_attention_general(p, static_cast<cudaStream_t>(cuda_stream)), "page attention launch");
+  p.q = x, p.o = o, p.lse = lse;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const int es = page_esize(c->format);
+  if (page_attn_pieces(c) && multiple16(x, q->q_stride, c->B, q->Lq, q->Hq, 2) &&
+      multiple16(o, q->o_stride, c->B, q->Lq, q->Hq, 2) &&
+      multiple16(c->k_pages, c->k_stride, c->n_pages, c->page_size, c->Hkv, es) &&
+      multiple16(c->v_pages, c->v_stride, c->n_pages, c->page_size, c->Hkv, es)) {
+    int sms = 0;
+    if (int e = cuda_status(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "device")) return e;
+    if (p.softcap > 0) set_cap_form(p.cap, p.scale, p.softcap);
+    p.arrived = static_cast<int*>(scratch);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + PSV_PAGE_SCRATCH_HEAD);
+    return cuda_status(launch_page_attention(p, sms, st), "page attention launch");
+  }
+  return cuda_status(launch_page_attention_general(p, st), "page attention launch");
 }

@@ -623,7 +623,7 @@ int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void
  * lengths; those of a sequence may differ in their roundings where the lengths
  * of others change, as the work is shared out among the SMs by all of them.
  * Requirements: dtype BF16 or F16 (16-bit pages: their own); Hq a multiple of Hkv;
- * B x Hq <= 2^24; 0 <= Lq <= 2^20; window, sinks >= 0, sinks need a window; scale,
+ * B x Hq <= 2^24; 0 <= Lq <= 2^20, Lq x Hq <= 2^30; window, sinks >= 0, sinks need a window; scale,
  * softcap >= 0 finite; o's rows distinct. */
 typedef struct psv_page_query {
   int32_t dtype, Lq, Hq, causal, window, sinks, append;
