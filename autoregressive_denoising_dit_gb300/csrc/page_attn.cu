@@ -1,15 +1,16 @@
 // Attention of a token's rows, or a few tokens', over the pages of a cache.
 //
-// Bound by reading the codes of K and V once.  A CTA reads them straight into the
-// registers that mma.sync takes them from: the contraction over a head's values
-// may run in any order, so that a thread holds 16 bytes in a row of each key (and
-// of its query rows), and the products are transposed, so that keys and values are
-// the operand of 16 rows and 8 query rows fill a product:
+// Bound by reading the codes of K and V once.  A thread brings the very bytes that
+// its products take, by 16-byte asynchronous copies into a ring of its own in shared
+// memory: the contraction over a head's values may run in any order, so that a
+// thread holds 16 bytes in a row of each key (and of its query rows), and the
+// products are transposed, so that keys and values are the operand of 16 rows and 8
+// query rows fill a product:
 //   S^T = K Q^T      a thread holds keys lane / 4 and + 8 of a step of 16
 //   O^T += V^T P^T   a thread holds the keys 2 (lane % 4) + {0, 1, 8, 9}, whose
 //                    bytes of one column are paired by a byte permutation
-// No shared memory, no barrier and no alignment to a page's start stand between
-// the pages and the products; 16 warps an SM keep 4 kB each on their way.
+// No barrier and no alignment to a page's start stand between the pages and the
+// products, and 100 to 200 kB an SM are on their way.
 //
 // Codes become f16 (exactly); queries become f16 with a power of two for each row;
 // a key's scale multiplies its scores.  A value's scale enters its weight as an
@@ -21,6 +22,7 @@
 // Where a cut falls into a group its shares go to the workspace and the last CTA
 // to be done joins them in order.
 #include <algorithm>
+#include <cfloat>
 
 #include "page_kernels.h"
 #include "psv_device.cuh"
@@ -34,7 +36,8 @@ constexpr int kStep = 16;  // keys of a warp's step
 constexpr int kCtasSm = 2;
 constexpr int kMaxCtas = 152 * kCtasSm;  // shares in the workspace
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: weights stay below 2^8 of a stale maximum
+constexpr float kRescale = 256.0f;  // weights above it take up a new maximum
+constexpr float kNone = -FLT_MAX;   // a maximum of nothing: exp2(-inf - kNone) = 0, exp2(kNone - kNone) = 1
 
 template <int DH, int FMT, int NT>
 struct ACfg {
@@ -45,10 +48,16 @@ struct ACfg {
   static constexpr int KS = kScaled ? 4 : 2;  // products (of 16 values) a piece
   static constexpr int VW = DH * ES / 32;   // 4-byte words of a value in a thread
   static constexpr int JSTRIDE = DH + 4;    // floats between a join area's rows
+  static constexpr int K_BYTES = 2 * KP * 512, V_BYTES = 4 * VW * 128;
+  static constexpr int SLOT = K_BYTES + V_BYTES + (kScaled ? 128 : 0);  // a warp's step: K, V, the scales
   // Two CTAs an SM: 128, 168 or 255 registers a thread.
   static constexpr int WARPS = NT == 1 && DH == 64 ? 8 : NT == 1 && kScaled ? 6 : DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int SMEM = WARPS * ROWS * (JSTRIDE + 4) * 4;
+  static constexpr int STAGES = std::min(4, (112 << 10) / (WARPS * SLOT));
+  static constexpr int RING = WARPS * STAGES * SLOT;
+  static constexpr int JOIN = WARPS * ROWS * (JSTRIDE + 4) * 4;  // in the ring's place
+  static constexpr int SMEM = RING > JOIN ? RING : JOIN;
+  static_assert(2 * (SMEM + 1024 + 64) <= 233472, "two CTAs an SM");
 };
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -109,17 +118,20 @@ __device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// Copies of 16 or 8 bytes that do not wait; `bytes` 0 leaves zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ uint2 load8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // What a sequence's steps are: steps [0, head) from key 0 on (the sinks), the
@@ -167,9 +179,10 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   using C = ACfg<DH, FMT, NT>;
   constexpr int ROWS = C::ROWS, kWarps = C::WARPS, kThreads = C::THREADS;
   constexpr bool kBf16Operands = FMT == PSV_PAGE_BF16;
-  extern __shared__ float smem[];
-  float* so = smem;                                    // [kWarps][ROWS][JSTRIDE]
-  float* sm = smem + kWarps * ROWS * C::JSTRIDE;       // [kWarps][ROWS][4]: m', m, l
+  constexpr int kStages = C::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* so = reinterpret_cast<float*>(smem);      // [kWarps][ROWS][JSTRIDE]
+  float* sm = so + kWarps * ROWS * C::JSTRIDE;     // [kWarps][ROWS][4]: m', m, l
   __shared__ int s_last;
   const PageCacheDev& c = p.c;
   const int warp = warp_id(), lane = lane_id(), quad = lane / 4, four = lane % 4;
@@ -258,7 +271,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       for (int i = 0; i < C::KP; ++i)
 #pragma unroll
         for (int x = 0; x < C::KS; ++x) qf[t][i * C::KS + x][0] = raw[i][2 * x], qf[t][i * C::KS + x][1] = raw[i][2 * x + 1];
-      // (row quad's factor to the threads that hold its scores)
+      // (row quad's factor to the threads that hold its scores; the cap takes raw products)
+      if (!(p.softcap > 0)) e *= p.scale * kLog2e;
       up[t][0] = __shfl_sync(0xffffffffu, e, (2 * four) * 4);
       up[t][1] = __shfl_sync(0xffffffffu, e, (2 * four + 1) * 4);
     }
@@ -286,74 +300,92 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][i][e] = 0.0f;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) mo[t][x] = ml[t][x] = -INFINITY, l[t][x] = 0.0f;
+      for (int x = 0; x < 2; ++x) mo[t][x] = ml[t][x] = kNone, l[t][x] = 0.0f;
     }
 
-    const char* k_base = static_cast<const char*>(c.k) + kvh * c.ks.h * C::ES;
-    const char* v_base = static_cast<const char*>(c.v) + kvh * c.vs.h * C::ES;
-    // The step's key lane % 16: its place, none if no row of the tile sees it.
+    // This thread's bytes of row 0 of page 0; pieces behind the head are left out.
+    const char* k_mine = static_cast<const char*>(c.k) + kvh * c.ks.h * C::ES + four * 16;
+    const char* v_mine = static_cast<const char*>(c.v) + kvh * c.vs.h * C::ES + quad * (C::VW == 2 ? 8 : 16);
+    const char* s_mine = reinterpret_cast<const char*>((lane < 16 ? c.k_scale : c.v_scale) + kvh * c.ss.h);
+    const bool aligned = c.page_size % kStep == 0;  // a step lies in one page
     auto key_of = [&](int step) { return step < s.head ? step * kStep : s.from + (step - s.head) * kStep; };
+    // Where a step's key is: the first one, or where it may lie in several pages key lane % 16.
     auto locate = [&](int step) {
-      PageRow at{-1, 0};
-      if (step < step1) {
-        const int j = key_of(step) + (lane & 15);
-        if (j < any_end && (j >= any_first || j < sinks)) at = page_row(c, b, j);
-      }
-      return at;
+      return step < step1 ? page_row(c, b, key_of(step) + (aligned ? 0 : lane & 15)) : PageRow{-1, 0};
     };
-    auto load_k = [&](PageRow at, uint4 (&k)[2][C::KP], float (&ksc)[2], float (&vsc)[2]) {
+    uint32_t found = 0;  // a bit for each step under way: whether the key is there
+    auto issue = [&](int step, int slot, PageRow at) {
+      found = found << 1 | (at.page >= 0);
+      if (step >= step1) return;
+      const int key0 = key_of(step);
+      // Keys that some row of the tile sees are read.
+      const bool every = key0 + kStep <= any_end && (key0 >= any_first || key0 + kStep <= sinks);
+      const uint32_t dst = smem_u32(smem) + (warp * kStages + slot) * C::SLOT;
+      auto wanted = [&](int key) {
+        const int j = key0 + key;
+        return every || (j < any_end && (j >= any_first || j < sinks));
+      };
+      const int page0 = max(at.page, 0);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int page = __shfl_sync(0xffffffffu, at.page, quad + 8 * x), row = __shfl_sync(0xffffffffu, at.row, quad + 8 * x);
-        const char* src = k_base + (page * c.ks.b + row * c.ks.l) * C::ES;
+        const int key = quad + 8 * x;
+        const int page = aligned ? at.page : __shfl_sync(0xffffffffu, at.page, key);
+        const int row = aligned ? at.row + key : __shfl_sync(0xffffffffu, at.row, key);
+        const char* src = k_mine + static_cast<uint64_t>(p.kb) * max(page, 0) + static_cast<uint64_t>(p.kl) * row;
+        const bool want = page >= 0 && wanted(key);
 #pragma unroll
         for (int i = 0; i < C::KP; ++i) {
-          const int piece = (four + 4 * i) * 16;
-          k[x][i] = make_uint4(0, 0, 0, 0);
-          if (page >= 0 && (piece < p.dh * C::ES)) k[x][i] = load16(src + piece);
-        }
-        if (C::kScaled) {
-          ksc[x] = vsc[x] = 0.0f;
-          if (page >= 0) {
-            const int64_t i = page * c.ss.b + row * c.ss.l + kvh * c.ss.h;
-            ksc[x] = c.k_scale[i], vsc[x] = c.v_scale[i];
-          }
+          const bool in = (four + 4 * i) * 16 < p.dh * C::ES;
+          copy16(dst + (x * C::KP + i) * 512 + lane * 16, in ? src + i * 64 : k_mine - four * 16, want && in ? 16 : 0);
         }
       }
-    };
-    auto load_v = [&](PageRow at, uint32_t (&v)[4][C::VW]) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int key = 2 * four + (x & 1) + 8 * (x >> 1);
-        const int page = __shfl_sync(0xffffffffu, at.page, key), row = __shfl_sync(0xffffffffu, at.row, key);
-        const char* src = v_base + (page * c.vs.b + row * c.vs.l) * C::ES;
+        const int page = aligned ? at.page : __shfl_sync(0xffffffffu, at.page, key);
+        const int row = aligned ? at.row + key : __shfl_sync(0xffffffffu, at.row, key);
+        const char* src = v_mine + static_cast<uint64_t>(p.vb) * max(page, 0) + static_cast<uint64_t>(p.vl) * row;
+        const bool want = page >= 0 && wanted(key);
+        const uint32_t to = dst + C::K_BYTES + x * C::VW * 128;
         if constexpr (C::VW == 2) {
-          uint2 y = make_uint2(0, 0);
-          if (page >= 0 && quad * 8 < p.dh * C::ES) y = load8(src + quad * 8);
-          v[x][0] = y.x, v[x][1] = y.y;
+          const bool in = quad * 8 < p.dh * C::ES;
+          copy8(to + lane * 8, in ? src : v_mine - quad * 8, want && in ? 8 : 0);
         } else {
 #pragma unroll
           for (int i = 0; i < C::VW / 4; ++i) {
-            const int piece = (quad + 8 * i) * 16;
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (page >= 0 && piece < p.dh * C::ES) y = load16(src + piece);
-            v[x][4 * i] = y.x, v[x][4 * i + 1] = y.y, v[x][4 * i + 2] = y.z, v[x][4 * i + 3] = y.w;
+            const bool in = (quad + 8 * i) * 16 < p.dh * C::ES;
+            copy16(to + i * 512 + lane * 16, in ? src + i * 128 : v_mine - quad * 16, want && in ? 16 : 0);
           }
         }
       }
+      if constexpr (C::kScaled) {
+        const int row = aligned ? at.row + (lane & 15) : at.row;
+        copy4(dst + C::K_BYTES + C::V_BYTES + lane * 4,
+              s_mine + static_cast<uint64_t>(p.sb) * page0 + static_cast<uint64_t>(p.sl) * row,
+              at.page >= 0 && wanted(lane & 15) ? 4 : 0);
+      }
     };
 
-    uint4 k[2][C::KP];
-    uint32_t v[4][C::VW];
-    float ksc[2], vsc[2];
-    int step = step0 + warp;
-    PageRow at = locate(step), next = locate(step + kWarps);
-    load_k(at, k, ksc, vsc);
+    int step = step0 + warp, slot = 0;
+    {
+      PageRow at[kStages - 1];
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) at[i] = locate(step + i * kWarps);
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) {
+        issue(step + i * kWarps, i, at[i]);
+        copies_commit();
+      }
+    }
+    PageRow next = locate(step + (kStages - 1) * kWarps);
     for (; step < step1; step += kWarps) {
-      load_v(at, v);
-      const PageRow here = at;
-      at = next;
-      next = locate(step + 2 * kWarps);
+      issue(step + (kStages - 1) * kWarps, slot == 0 ? kStages - 1 : slot - 1, next);
+      copies_commit();
+      next = locate(step + kStages * kWarps);
+      copies_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* mine = smem + (warp * kStages + slot) * C::SLOT;
+      slot = slot == kStages - 1 ? 0 : slot + 1;
       // ---- scores
       float sc[NT][4];
 #pragma unroll
@@ -362,8 +394,9 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         for (int e = 0; e < 4; ++e) sc[t][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < C::KP; ++i) {
-        const uint32_t w0[4] = {k[0][i].x, k[0][i].y, k[0][i].z, k[0][i].w};
-        const uint32_t w1[4] = {k[1][i].x, k[1][i].y, k[1][i].z, k[1][i].w};
+        const uint4 k0 = *reinterpret_cast<const uint4*>(mine + i * 512 + lane * 16);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(mine + (C::KP + i) * 512 + lane * 16);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int x = 0; x < C::KS; ++x) {
           uint32_t a[4];
@@ -377,18 +410,19 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           for (int t = 0; t < NT; ++t) mma<FMT>(sc[t], a, qf[t][i * C::KS + x][0], qf[t][i * C::KS + x][1]);
         }
       }
-      const float ks0 = ksc[0], ks1 = ksc[1];
-      float lv[2] = {0.0f, 0.0f};
-      if (C::kScaled) lv[0] = fast_log2(vsc[0]), lv[1] = fast_log2(vsc[1]);
-      load_k(at, k, ksc, vsc);
+      float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
+      if constexpr (C::kScaled) {
+        const float* scales = reinterpret_cast<const float*>(mine + C::K_BYTES + C::V_BYTES);
+        ks[0] = scales[quad], ks[1] = scales[quad + 8];
+        lv[0] = fast_log2(scales[16 + quad]), lv[1] = fast_log2(scales[24 + quad]);
+      }
       // ---- scores and weights' exponents in the log2 domain
       const int key0 = key_of(step);
       float u[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (C::kScaled) sc[t][e] = sc[t][e] * (e < 2 ? ks0 : ks1) * up[t][e & 1];
+        for (int e = 0; e < 4; ++e) sc[t][e] = (C::kScaled ? sc[t][e] * ks[e >> 1] : sc[t][e]) * up[t][e & 1];
       if (p.softcap > 0) {
         float big = 0.0f;
 #pragma unroll
@@ -397,22 +431,16 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(sc[t][e]));
         if (__all_sync(0xffffffffu, big * p.cap.inv <= 1.0f)) cap_within<4 * NT>(&sc[0][0], p.cap);
         else cap_any<4 * NT>(&sc[0][0], p.cap);
-      } else {
-        const float scale2 = p.scale * kLog2e;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[t][e] *= scale2;
       }
       const bool whole = (key0 + kStep <= all_end && (key0 >= all_first || key0 + kStep <= sinks)) &&
-                         __all_sync(0xffffffffu, here.page >= 0);
+                         __all_sync(0xffffffffu, found >> (kStages - 1) & 1);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[t][e] = C::kScaled ? sc[t][e] + lv[e >> 1] : sc[t][e];
       unsigned there = 0xffffu;
       if (!whole) {
-        there = __ballot_sync(0xffffffffu, here.page >= 0);
+        there = __ballot_sync(0xffffffffu, found >> (kStages - 1) & 1);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -422,50 +450,64 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
               sc[t][e] = -INFINITY, u[t][e] = -INFINITY;
           }
       }
-      // ---- a larger maximum is taken up when a score passes the old one by far
-      bool grow = false;
+      // ---- weights; a new maximum is taken up where one passes the old one by far
+      float w[NT][4], y[NT][4];
+      auto weigh = [&]() {
+        float big = 0.0f;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          grow |= sc[t][e] > ml[t][e & 1] + kRescaleThreshold;
-          if (C::kScaled) grow |= u[t][e] > mo[t][e & 1] + kRescaleThreshold;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
+          for (int e = 0; e < 4; ++e) {
+            y[t][e] = fast_exp2(sc[t][e] - ml[t][e & 1]);
+            w[t][e] = C::kScaled ? fast_exp2(u[t][e] - mo[t][e & 1]) : y[t][e];
+            big = fmaxf(big, fmaxf(y[t][e], w[t][e]));
+          }
+        return big;
+      };
+      if (__any_sync(0xffffffffu, weigh() > kRescale)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             float a = fmaxf(sc[t][x], sc[t][2 + x]), d = fmaxf(u[t][x], u[t][2 + x]);
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) {
-              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
-              if (C::kScaled) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, w));
+            for (int i = 4; i < 32; i <<= 1) {
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, i));
+              if (C::kScaled) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, i));
             }
             a = fmaxf(a, ml[t][x]);
             d = C::kScaled ? fmaxf(d, mo[t][x]) : a;
-            l[t][x] *= a == -INFINITY ? 1.0f : fast_exp2(ml[t][x] - a);
-            const float f = d == -INFINITY ? 1.0f : fast_exp2(mo[t][x] - d);
+            l[t][x] *= fast_exp2(ml[t][x] - a);
+            const float f = fast_exp2(mo[t][x] - d);
             ml[t][x] = a, mo[t][x] = d;
 #pragma unroll
             for (int i = 0; i < DH / 16; ++i) o[t][i][x] *= f, o[t][i][2 + x] *= f;
           }
+        weigh();
       }
-      // ---- weights, transposed into the second product's operand
+      // ---- transposed into the second product's operand
       uint32_t pb[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int x = e & 1;
-          const float m0 = ml[t][x] == -INFINITY ? 0.0f : ml[t][x];
-          const float y = fast_exp2(sc[t][e] - m0);
-          l[t][x] += y;
-          w[e] = C::kScaled ? fast_exp2(u[t][e] - (mo[t][x] == -INFINITY ? 0.0f : mo[t][x])) : y;
+        for (int e = 0; e < 4; ++e) l[t][e & 1] += y[t][e];
+        pb[t][0] = movmatrix_t(pack2<kBf16Operands>(w[t][0], w[t][1]));
+        pb[t][1] = movmatrix_t(pack2<kBf16Operands>(w[t][2], w[t][3]));
+      }
+      uint32_t v[4][C::VW];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint8_t* from = mine + C::K_BYTES + x * C::VW * 128;
+        if constexpr (C::VW == 2) {
+          const uint2 z = *reinterpret_cast<const uint2*>(from + lane * 8);
+          v[x][0] = z.x, v[x][1] = z.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::VW / 4; ++i) {
+            const uint4 z = *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16);
+            v[x][4 * i] = z.x, v[x][4 * i + 1] = z.y, v[x][4 * i + 2] = z.z, v[x][4 * i + 3] = z.w;
+          }
         }
-        pb[t][0] = movmatrix_t(pack2<kBf16Operands>(w[0], w[1]));
-        pb[t][1] = movmatrix_t(pack2<kBf16Operands>(w[2], w[3]));
       }
       // ---- O^T += V^T P^T
       if constexpr (!C::kScaled) {
@@ -524,7 +566,9 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       }
     }
 
-    // ---- join the warps
+    // ---- join the warps, in the ring's place
+    copies_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -554,7 +598,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     // Scale, sum and value of a row's shares: finished and written, or left as a share.
     auto write_out = [&](int r, int d, float mm_o, float mm_l, float ll, float4 acc) {
       const int tok = (r0 + r) / p.G, head = kvh * p.G + (r0 + r) % p.G;
-      const float f = ll > 0.0f ? (mm_o == -INFINITY ? 0.0f : fast_exp2(mm_o - mm_l)) / ll : (ll == 0.0f ? 0.0f : ll);
+      const float f = ll > 0.0f ? fast_exp2(mm_o - mm_l) / ll : ll;  // (0 or NaN)
       if (d < p.dh) {
         const uint2 y = p.bf16 ? make_uint2(pack2<true>(acc.x * f, acc.y * f), pack2<true>(acc.z * f, acc.w * f))
                                : make_uint2(pack2<false>(acc.x * f, acc.y * f), pack2<false>(acc.z * f, acc.w * f));
@@ -565,21 +609,20 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     };
     for (int x = threadIdx.x; x < n_rows * (DH / 4); x += kThreads) {
       const int r = x / (DH / 4), d = x % (DH / 4) * 4;
-      float mm_o = -INFINITY, mm_l = -INFINITY;
+      float mm_o = kNone, mm_l = kNone;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         mm_o = fmaxf(mm_o, sm[(w * ROWS + r) * 4]);
         mm_l = fmaxf(mm_l, sm[(w * ROWS + r) * 4 + 1]);
       }
-      const float o0 = mm_o == -INFINITY ? 0.0f : mm_o, l0 = mm_l == -INFINITY ? 0.0f : mm_l;
       float ll = 0.0f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* st = sm + (w * ROWS + r) * 4;
         const float4 y = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * C::JSTRIDE + d);
-        const float f = fast_exp2(st[0] - o0);
-        ll = fmaf(fast_exp2(st[1] - l0), st[2], ll);
+        const float f = fast_exp2(st[0] - mm_o);
+        ll = fmaf(fast_exp2(st[1] - mm_l), st[2], ll);
         acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
         acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
       }
@@ -610,23 +653,22 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         for (int x = threadIdx.x; x < n_rows * (DH / 4); x += kThreads) {
           const int r = x / (DH / 4), d = x % (DH / 4) * 4;
           auto share = [&](int cta) { return p.part + (2 * static_cast<int64_t>(cta) + (cta == c0)) * kPart; };
-          float mm_o = -INFINITY, mm_l = -INFINITY;
+          float mm_o = kNone, mm_l = kNone;
 #pragma unroll 4
           for (int cta = c0; cta <= c1; ++cta) {
             const float* st = share(cta) + ROWS * DH + r * 4;
             mm_o = fmaxf(mm_o, __ldcg(st));
             mm_l = fmaxf(mm_l, __ldcg(st + 1));
           }
-          const float o0 = mm_o == -INFINITY ? 0.0f : mm_o, l0 = mm_l == -INFINITY ? 0.0f : mm_l;
-          float ll = 0.0f;
+              float ll = 0.0f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int cta = c0; cta <= c1; ++cta) {
             const float* at_share = share(cta);
             const float4 st = __ldcg(reinterpret_cast<const float4*>(at_share + ROWS * DH + r * 4));
             const float4 y = __ldcg(reinterpret_cast<const float4*>(at_share + r * DH + d));
-            const float f = fast_exp2(st.x - o0);
-            ll = fmaf(fast_exp2(st.y - l0), st.z, ll);
+            const float f = fast_exp2(st.x - mm_o);
+            ll = fmaf(fast_exp2(st.y - mm_l), st.z, ll);
             acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
             acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
           }

@@ -505,13 +505,17 @@ PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q,
   p.q = x, p.o = o, p.lse = lse;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int es = page_esize(c->format);
-  if (page_attn_pieces(c) && multiple16(x, q->q_stride, c->B, q->Lq, q->Hq, 2) &&
+  auto small = [](const int64_t* st, int size) { return st[0] * size < int64_t{1} << 32 && st[1] * size < int64_t{1} << 32; };
+  if (page_attn_pieces(c) && small(c->k_stride, es) && small(c->v_stride, es) && (es == 2 || small(c->scale_stride, 4)) && multiple16(x, q->q_stride, c->B, q->Lq, q->Hq, 2) &&
       multiple16(o, q->o_stride, c->B, q->Lq, q->Hq, 2) &&
       multiple16(c->k_pages, c->k_stride, c->n_pages, c->page_size, c->Hkv, es) &&
       multiple16(c->v_pages, c->v_stride, c->n_pages, c->page_size, c->Hkv, es)) {
     int sms = 0;
     if (int e = cuda_status(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "device")) return e;
     if (p.softcap > 0) set_cap_form(p.cap, p.scale, p.softcap);
+    p.kb = static_cast<uint32_t>(c->k_stride[0] * es), p.kl = static_cast<uint32_t>(c->k_stride[1] * es);
+    p.vb = static_cast<uint32_t>(c->v_stride[0] * es), p.vl = static_cast<uint32_t>(c->v_stride[1] * es);
+    p.sb = static_cast<uint32_t>(c->scale_stride[0] * 4), p.sl = static_cast<uint32_t>(c->scale_stride[1] * 4);
     p.arrived = static_cast<int*>(scratch);
     p.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + PSV_PAGE_SCRATCH_HEAD);
     return cuda_status(launch_page_attention(p, sms, st), "page attention launch");
