@@ -53,11 +53,12 @@ struct ACfg {
   // Two CTAs an SM: 128, 168 or 255 registers a thread.
   static constexpr int WARPS = NT == 1 && DH == 64 ? 8 : NT == 1 && kScaled ? 6 : DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int STAGES = std::min(4, (112 << 10) / (WARPS * SLOT));
+  static constexpr int JOIN = WARPS * ROWS * (JSTRIDE + 4) * 4;  // the warps' sums at the end of a group
+  static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN) / (WARPS * SLOT));
   static constexpr int RING = WARPS * STAGES * SLOT;
-  static constexpr int JOIN = WARPS * ROWS * (JSTRIDE + 4) * 4;  // in the ring's place
-  static constexpr int SMEM = RING > JOIN ? RING : JOIN;
-  static_assert(2 * (SMEM + 1024 + 64) <= 233472, "two CTAs an SM");
+  static constexpr int SMEM = RING + JOIN;
+  static_assert(2 * (SMEM + 1024 + 256) <= 233472, "two CTAs an SM");
+  static_assert((ROWS * (kMaxCtas + 4) + THREADS * 4) * 4 <= RING, "the join of CTAs, in the ring's place");
 };
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -103,10 +104,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 template <int FMT>
 __device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == PSV_PAGE_E4M3) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffff), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x >> 16), __NV_E4M3);
-    lo = *reinterpret_cast<const uint32_t*>(&a);
-    hi = *reinterpret_cast<const uint32_t*>(&b);
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
   } else {
     // 1024 + (x + 128) is the f16 whose lower byte is x + 128: 1152 less is x.
     const uint32_t u = x ^ 0x80808080u;
@@ -121,6 +124,9 @@ __device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
 // Copies of 16 or 8 bytes that do not wait; `bytes` 0 leaves zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -143,20 +149,26 @@ struct Seq {
 };
 
 template <int ROWS>
-__device__ __forceinline__ Seq sequence(const PageAttnParams& p, int b) {
+__device__ __forceinline__ Seq sequence(const PageAttnParams& p, int rows, int n) {
   Seq s;
-  s.rows = page_rows(p, b);
-  s.n = page_length(p, b, s.rows);
-  s.keys = min(s.n, p.c.positions);
-  const int first = p.window ? max(s.n - s.rows - p.window + 1, 0) : 0;  // of the first row
+  s.rows = rows;
+  s.n = n;
+  s.keys = min(n, p.c.positions);
+  const int first = p.window ? max(n - rows - p.window + 1, 0) : 0;  // of the first row
   const int end = (s.keys + kStep - 1) / kStep;
   s.head = min(p.window ? (min(p.sinks, s.keys) + kStep - 1) / kStep : 0, end);
   const int from = min(max(first / kStep, s.head), end);
   s.from = from * kStep;
   s.steps = max(s.head + end - from, 1);  // (a row without keys is written too)
-  s.tiles = (s.rows * p.G + ROWS - 1) / ROWS;
+  s.tiles = (rows * p.G + ROWS - 1) / ROWS;
   s.total = static_cast<int64_t>(s.steps) * s.tiles * p.Hkv;
   return s;
+}
+
+// a / b for 0 <= a, 0 < b, in 32 bits where they do.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // The line of `all` steps in `ctas` stretches, the first ones a step longer.
@@ -164,47 +176,64 @@ struct Cut {
   int ctas, more;
   int64_t each;
   __device__ __forceinline__ Cut(int64_t all, int n) : ctas(n), more(0), each(0) {
-    if (n) each = all / n, more = static_cast<int>(all - each * n);
+    if (n) each = divide(all, n), more = static_cast<int>(all - each * n);
   }
   __device__ __forceinline__ int64_t begin(int cta) const { return each * cta + min(cta, more); }
   __device__ __forceinline__ int of(int64_t x) const {
     const int64_t longer = (each + 1) * more;
-    return static_cast<int>(x < longer ? x / (each + 1) : more + (x - longer) / each);
+    return static_cast<int>(x < longer ? divide(x, each + 1) : more + divide(x - longer, each));
   }
+};
+
+// A group of which a CTA has a share: its first and last step on the line, and its rows.
+struct Share {
+  int64_t first, last;
+  int b, kvh, r0, rows, used;
 };
 
 template <int DH, int FMT, int NT>
 __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     page_attn_kernel(const __grid_constant__ PageAttnParams p) {
   using C = ACfg<DH, FMT, NT>;
-  constexpr int ROWS = C::ROWS, kWarps = C::WARPS, kThreads = C::THREADS;
+  constexpr int ROWS = C::ROWS, kWarps = C::WARPS, kThreads = C::THREADS, kStages = C::STAGES;
   constexpr bool kBf16Operands = FMT == PSV_PAGE_BF16;
-  constexpr int kStages = C::STAGES;
+  constexpr int kPart = ROWS * (DH + 4);  // floats of a share: O, then m', m, l of each row
   extern __shared__ __align__(128) uint8_t smem[];
-  float* so = reinterpret_cast<float*>(smem);      // [kWarps][ROWS][JSTRIDE]
-  float* sm = so + kWarps * ROWS * C::JSTRIDE;     // [kWarps][ROWS][4]: m', m, l
-  __shared__ int s_last;
+  float* so = reinterpret_cast<float*>(smem + C::RING);  // [kWarps][ROWS][JSTRIDE]
+  float* sm = so + kWarps * ROWS * C::JSTRIDE;           // [kWarps][ROWS][4]: m', m, l
+  __shared__ Share s_share[2];  // of a group that began before this CTA, of one that it begins
+  __shared__ int s_last[2][2];  // whether this CTA is the last of the group's, its first CTA and their number
+  static_assert(kMaxCtas * sizeof(int) <= PSV_PAGE_SCRATCH_HEAD, "counters in the workspace's head");
   const PageCacheDev& c = p.c;
   const int warp = warp_id(), lane = lane_id(), quad = lane / 4, four = lane % 4;
+  if (threadIdx.x < 2) s_share[threadIdx.x].used = 0;
+  if (p.dh < DH) {  // pieces behind the head stay zeros
+    for (int i = threadIdx.x; i < C::RING / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
   pdl_trigger();
   pdl_wait();
 
-  // The line's length, and this CTA's stretch of it.
-  static_assert(kMaxCtas * sizeof(int) <= PSV_PAGE_SCRATCH_HEAD, "counters in the workspace's head");
-  int64_t all = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32)
-    if (b0 + lane < p.B) all += sequence<ROWS>(p, b0 + lane).total;
+  // The line's length, this CTA's stretch [lo, hi) of it, and the sequence that it begins in.
+  auto rows_at = [&](int b) { return b < p.B ? page_rows(p, b) : 0; };
+  int rows_b = rows_at(lane), n_b = lane < p.B ? page_length(p, lane, rows_b) : 0;
+  int64_t all = sequence<ROWS>(p, rows_b, n_b).total;
+  for (int b = lane + 32; b < p.B; b += 32) {
+    const int rows = page_rows(p, b);
+    all += sequence<ROWS>(p, rows, page_length(p, b, rows)).total;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   const Cut cut(all, static_cast<int>(min(static_cast<int64_t>(gridDim.x), (all + kWarps - 1) / kWarps)));
   if (static_cast<int>(blockIdx.x) >= cut.ctas) return;
   int64_t lo = cut.begin(blockIdx.x);
   const int64_t hi = cut.begin(blockIdx.x + 1);
-  // The sequence that it begins in.
   int b = 0;
   int64_t before = 0;  // steps of earlier sequences
+  Seq s;
   for (int b0 = 0;; b0 += 32) {
-    const int64_t mine = b0 + lane < p.B ? sequence<ROWS>(p, b0 + lane).total : 0;
+    if (b0) rows_b = rows_at(b0 + lane), n_b = b0 + lane < p.B ? page_length(p, b0 + lane, rows_b) : 0;
+    const int64_t mine = sequence<ROWS>(p, rows_b, n_b).total;
     int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -216,46 +245,254 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       const int at = __ffs(hit) - 1;
       b = b0 + at;
       before += __shfl_sync(0xffffffffu, sum - mine, at);
+      s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
       break;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
-  Seq s = sequence<ROWS>(p, b);
 
+  const uint32_t ring = smem_u32(smem) + warp * kStages * C::SLOT + lane * 16;
+  const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
+  const int sinks = p.window ? p.sinks : 0;
+  const char *k_mine = nullptr, *v_mine = nullptr, *s_mine = nullptr;
+  int kvh = 0, r0 = 0, n_rows = 0, step0 = 0, step1 = 0, slot = 0;
+  int all_end = 0, any_end = 0, all_first = 0, any_first = 0;
+  uint32_t found = 0;  // a bit for each step under way: whether key lane % 16 is there
+  // Where the keys of the warp's next steps are: in lane 2 i + h the half h of number i
+  // of 16 steps, and of the 16 behind them, or where eight keys may lie in several pages
+  // of the next step key lane % 16.
+  PageRow place{-1, 0}, later{-1, 0};
+  int issued = 0;  // steps of the group that the warp has asked for
+  auto key_of = [&](int step) { return step < s.head ? step * kStep : s.from + (step - s.head) * kStep; };
+  auto look = [&](int number) {  // of the warp's steps
+    const int step = step0 + warp + (number + (eights ? lane / 2 : 0)) * kWarps;
+    return step < step1 ? page_row(c, b, key_of(step) + (eights ? lane % 2 * 8 : lane % 16)) : PageRow{-1, 0};
+  };
+  auto offset = [](uint32_t page_stride, uint32_t row_stride, int page, int row) {
+    return static_cast<uint64_t>(page_stride) * static_cast<uint32_t>(page) +
+           static_cast<uint64_t>(row_stride) * static_cast<uint32_t>(row);
+  };
+  auto issue = [&](int into) {
+    const int step = step0 + warp + issued * kWarps, number = issued++;
+    found <<= 1;
+    if (step >= step1) return;
+    const uint32_t dst = ring + into * C::SLOT;
+    const int key0 = key_of(step);
+    // Keys that some row of the tile sees are read.
+    const bool every = key0 + kStep <= any_end && (key0 >= any_first || key0 + kStep <= sinks);
+    PageRow half[2];
+    if (eights) {
+      if (number % 16 == 0 && number) place = later, later = look(number + 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        half[h].page = __shfl_sync(0xffffffffu, place.page, 2 * (number % 16) + h);
+        half[h].row = __shfl_sync(0xffffffffu, place.row, 2 * (number % 16) + h);
+      }
+    }
+    if (eights && every && half[0].page >= 0 && half[1].page >= 0) {
+      found |= 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const char* k = k_mine + offset(p.kb, p.kl, half[h].page, half[h].row);
+        const char* v = v_mine + offset(p.vb, p.vl, half[h].page, half[h].row);
+#pragma unroll
+        for (int i = 0; i < C::KP; ++i)
+          if ((four + 4 * i) * 16 < p.dh * C::ES) copy16(dst + (h * C::KP + i) * 512, k + i * 64);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t to = dst + C::K_BYTES + (2 * h + x) * C::VW * 128;
+          if constexpr (C::VW == 2) {
+            if (quad * 8 < p.dh * C::ES) copy8(to - lane * 8, v, 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < C::VW / 4; ++i)
+              if ((quad + 8 * i) * 16 < p.dh * C::ES) copy16(to + i * 512, v + i * 128);
+          }
+          v += p.vl;
+        }
+      }
+      if constexpr (C::kScaled) {
+        const bool h = lane & 8;
+        copy4(dst + C::K_BYTES + C::V_BYTES - lane * 12,
+              s_mine + offset(p.sb, p.sl, h ? half[1].page : half[0].page, (h ? half[1].row : half[0].row) + lane % 8), 4);
+      }
+      return;
+    }
+    // Key by key; what is not wanted (keys, pieces behind the head) is zeros.
+    PageRow at = place;
+    if (eights) at = lane & 8 ? half[1] : half[0], at.row += lane % 8;
+    else place = look(issued);
+    const int j = key0 + lane % 16;
+    if (at.page < 0 || j >= any_end || (j < any_first && j >= sinks)) at = PageRow{-1, 0};
+    found |= at.page >= 0;
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+      const int page = __shfl_sync(0xffffffffu, at.page, quad + 8 * x), row = __shfl_sync(0xffffffffu, at.row, quad + 8 * x);
+      const char* src = k_mine + offset(p.kb, p.kl, max(page, 0), row) - offset(0, p.kl, 0, quad);
+#pragma unroll
+      for (int i = 0; i < C::KP; ++i) {
+        const bool in = (four + 4 * i) * 16 < p.dh * C::ES;
+        copy16(dst + (x * C::KP + i) * 512, in ? src + i * 64 : src - four * 16, page >= 0 && in ? 16 : 0);
+      }
+    }
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {
+      const int key = 2 * four + (x & 1) + 8 * (x >> 1);
+      const int page = __shfl_sync(0xffffffffu, at.page, key), row = __shfl_sync(0xffffffffu, at.row, key);
+      const char* src = v_mine + offset(p.vb, p.vl, max(page, 0), row) - offset(0, p.vl, 0, 2 * four);
+      const uint32_t to = dst + C::K_BYTES + x * C::VW * 128;
+      if constexpr (C::VW == 2) {
+        const bool in = quad * 8 < p.dh * C::ES;
+        copy8(to - lane * 8, in ? src : src - quad * 8, page >= 0 && in ? 8 : 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::VW / 4; ++i) {
+          const bool in = (quad + 8 * i) * 16 < p.dh * C::ES;
+          copy16(to + i * 512, in ? src + i * 128 : src - quad * 16, page >= 0 && in ? 16 : 0);
+        }
+      }
+    }
+    if constexpr (C::kScaled)
+      copy4(dst + C::K_BYTES + C::V_BYTES - lane * 12, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);
+  };
+  // A row's finished value and lse.
+  auto write_out = [&](int wb, int wkvh, int row, int d, float mm_o, float mm_l, float ll, float4 acc) {
+    const int tok = p.by_group.div(row), head = wkvh * p.G + row - tok * p.G;
+    const float f = ll > 0.0f ? fast_exp2(mm_o - mm_l) / ll : ll;  // (0 or NaN)
+    if (d < p.dh) {
+      const uint2 y = p.bf16 ? make_uint2(pack2<true>(acc.x * f, acc.y * f), pack2<true>(acc.z * f, acc.w * f))
+                             : make_uint2(pack2<false>(acc.x * f, acc.y * f), pack2<false>(acc.z * f, acc.w * f));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + wb * p.os.b + tok * p.os.l + head * p.os.h + d) = y;
+    }
+    if (d == 0 && p.lse)
+      p.lse[(static_cast<int64_t>(wb) * p.Hq + head) * p.Lq + tok] = ll == 0.0f ? -INFINITY : (mm_l + fast_log2(ll)) * kLn2;
+  };
+
+  float o[NT][DH / 16][4], mo[NT][2], ml[NT][2], l[NT][2];
+  bool joining = false, split = false;  // the group before, whose sums are still the warps'
+  int was_b = 0, was_kvh = 0, was_r0 = 0, was_rows = 0, was_slot = 0;
   while (true) {
-    const int64_t within = lo - before;
-    const int group = static_cast<int>(within / s.steps), step0 = static_cast<int>(within - static_cast<int64_t>(group) * s.steps);
-    const int step1 = static_cast<int>(min(static_cast<int64_t>(s.steps), step0 + (hi - lo)));
-    const int kvh = group / s.tiles, r0 = group % s.tiles * ROWS;
-    const int n_rows = min(s.rows * p.G - r0, ROWS);
+    const bool more = lo < hi;
+    constexpr int kPer = 16 / C::ES;  // values of a piece
+    uint32_t raw[NT][C::KP][kPer / 2];
+    if (more) {
+      // ---- the next group: its first keys and its queries are on their way before the last one is joined
+      while (lo >= before + s.total) {
+        before += s.total;
+        ++b;
+        const int rows = page_rows(p, b);
+        s = sequence<ROWS>(p, rows, page_length(p, b, rows));
+      }
+      const int64_t within = lo - before;
+      const int group = static_cast<int>(divide(within, s.steps));
+      step0 = static_cast<int>(within - static_cast<int64_t>(group) * s.steps);
+      step1 = static_cast<int>(min(static_cast<int64_t>(s.steps), step0 + (hi - lo)));
+      kvh = s.tiles == 1 ? group : group / s.tiles;
+      r0 = (group - kvh * s.tiles) * ROWS;
+      n_rows = min(s.rows * p.G - r0, ROWS);
+      // what all rows see and what any of them sees, by their positions
+      const int at0 = s.n - s.rows + static_cast<int>(p.by_group.div(r0));
+      const int at1 = s.n - s.rows + static_cast<int>(p.by_group.div(r0 + n_rows - 1));
+      all_end = p.causal ? min(at0 + 1, s.keys) : s.keys, any_end = p.causal ? min(at1 + 1, s.keys) : s.keys;
+      all_first = p.window ? at1 - p.window + 1 : 0, any_first = p.window ? at0 - p.window + 1 : 0;
+      // this thread's bytes of a step's first row (its half's, for keys), in page 0
+      k_mine = static_cast<const char*>(c.k) + kvh * c.ks.h * C::ES + offset(0, p.kl, 0, quad) + four * 16;
+      v_mine = static_cast<const char*>(c.v) + kvh * c.vs.h * C::ES + offset(0, p.vl, 0, 2 * four) + quad * (C::VW == 2 ? 8 : 16);
+      s_mine = reinterpret_cast<const char*>((lane < 16 ? c.k_scale : c.v_scale) + kvh * c.ss.h);
+      issued = 0;
+      slot = 0;
+      place = look(0);
+      if (eights) later = look(16);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        // queries: row quad (+ 8) of the tile, values of this thread's pieces
+        const int r = r0 + 8 * t + quad, tok = p.by_group.div(r), head = kvh * p.G + r - tok * p.G;
+        const bool there = 8 * t + quad < n_rows;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.qs.b + tok * p.qs.l + head * p.qs.h;
+#pragma unroll
+        for (int i = 0; i < C::KP; ++i) {
+          const int d = (four + 4 * i) * kPer;
+#pragma unroll
+          for (int x = 0; x < kPer / 8; ++x) {
+            const uint4 y = there && d + 8 * x < p.dh ? *reinterpret_cast<const uint4*>(q + d + 8 * x) : make_uint4(0, 0, 0, 0);
+            raw[t][i][4 * x] = y.x, raw[t][i][4 * x + 1] = y.y, raw[t][i][4 * x + 2] = y.z, raw[t][i][4 * x + 3] = y.w;
+          }
+        }
+      }
+#pragma unroll 1
+      for (int i = 0; i < kStages - 1; ++i) {
+        issue(i);
+        copies_commit();
+      }
+    }
+    if (joining) {
+      // ---- join the warps
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
+          const int r = 8 * t + 2 * four + x;
+          if (r < was_rows) {
+            float* row = so + (warp * ROWS + r) * C::JSTRIDE;
+#pragma unroll
+            for (int i = 0; i < DH / 16; ++i) {
+              // the column pair that this thread's products i belong to
+              const int d = C::kScaled ? quad * (DH / 8) + 2 * i : (quad + 8 * (i / 4)) * 8 + 2 * (i % 4);
+              *reinterpret_cast<float2*>(row + d) = make_float2(o[t][i][x], o[t][i][2 + x]);
+            }
+            if (quad == 0)
+              *reinterpret_cast<float4*>(sm + (warp * ROWS + r) * 4) = make_float4(mo[t][x], ml[t][x], l[t][x], 0.0f);
+          }
+        }
+      __syncthreads();
+      float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + was_slot) * kPart;
+#pragma unroll 1
+      for (int x = threadIdx.x; x < was_rows * (DH / 4); x += kThreads) {
+        const int r = x / (DH / 4), d = x % (DH / 4) * 4;
+        float4 st[kWarps];
+        float mm_o = kNone, mm_l = kNone;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          st[w] = *reinterpret_cast<const float4*>(sm + (w * ROWS + r) * 4);
+          mm_o = fmaxf(mm_o, st[w].x);
+          mm_l = fmaxf(mm_l, st[w].y);
+        }
+        float ll = 0.0f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * C::JSTRIDE + d);
+          const float f = fast_exp2(st[w].x - mm_o);
+          ll = fmaf(fast_exp2(st[w].y - mm_l), st[w].z, ll);
+          acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
+          acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
+        }
+        if (split) {
+          *reinterpret_cast<float4*>(part + r * DH + d) = acc;
+          if (d == 0) *reinterpret_cast<float4*>(part + ROWS * DH + r * 4) = make_float4(mm_o, mm_l, ll, 0.0f);
+        } else {
+          write_out(was_b, was_kvh, was_r0 + r, d, mm_o, mm_l, ll, acc);
+        }
+      }
+      __syncthreads();
+    }
+    if (!more) break;
 
-    // ---- queries: row quad (+ 8) of the tile, values of this thread's pieces
+    // ---- queries as operands: f16 with the row's largest value in [1, 2) where they are bf16 and codes f16
     uint32_t qf[NT][C::KP * C::KS][2];
     float up[NT][2];  // by row of the scores: what its power of two took
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = r0 + 8 * t + quad, tok = r / p.G, head = kvh * p.G + r % p.G;
-      const bool there = 8 * t + quad < n_rows;
-      const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.qs.b + tok * p.qs.l + head * p.qs.h;
-      constexpr int kPer = 16 / C::ES;  // values of a piece
-      uint32_t raw[C::KP][kPer / 2];
-#pragma unroll
-      for (int i = 0; i < C::KP; ++i) {
-        const int d = (four + 4 * i) * kPer;
-#pragma unroll
-        for (int x = 0; x < kPer / 8; ++x) {
-          const uint4 y = there && d + 8 * x < p.dh ? *reinterpret_cast<const uint4*>(q + d + 8 * x) : make_uint4(0, 0, 0, 0);
-          raw[i][4 * x] = y.x, raw[i][4 * x + 1] = y.y, raw[i][4 * x + 2] = y.z, raw[i][4 * x + 3] = y.w;
-        }
-      }
       float e = 1.0f;
       if (C::kScaled && p.bf16) {
-        // to f16, with the row's largest value in [1, 2)
         uint32_t big = 0;
 #pragma unroll
         for (int i = 0; i < C::KP; ++i)
 #pragma unroll
-          for (int x = 0; x < kPer / 2; ++x) big = max(big, max(raw[i][x] << 16 & 0x7fff0000u, raw[i][x] & 0x7fff0000u));
+          for (int x = 0; x < kPer / 2; ++x)
+            big = max(big, max(raw[t][i][x] << 16 & 0x7fff0000u, raw[t][i][x] & 0x7fff0000u));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
         const int ex = big >= 0x7f800000u ? 0 : min(max(static_cast<int>(big >> 23) - 127, -120), 120);
@@ -265,127 +502,36 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         for (int i = 0; i < C::KP; ++i)
 #pragma unroll
           for (int x = 0; x < kPer / 2; ++x)
-            raw[i][x] = pack2<false>(__uint_as_float(raw[i][x] << 16) * down, __uint_as_float(raw[i][x] & 0xffff0000u) * down);
+            raw[t][i][x] = pack2<false>(__uint_as_float(raw[t][i][x] << 16) * down,
+                                        __uint_as_float(raw[t][i][x] & 0xffff0000u) * down);
       }
 #pragma unroll
       for (int i = 0; i < C::KP; ++i)
 #pragma unroll
-        for (int x = 0; x < C::KS; ++x) qf[t][i * C::KS + x][0] = raw[i][2 * x], qf[t][i * C::KS + x][1] = raw[i][2 * x + 1];
+        for (int x = 0; x < C::KS; ++x)
+          qf[t][i * C::KS + x][0] = raw[t][i][2 * x], qf[t][i * C::KS + x][1] = raw[t][i][2 * x + 1];
       // (row quad's factor to the threads that hold its scores; the cap takes raw products)
       if (!(p.softcap > 0)) e *= p.scale * kLog2e;
       up[t][0] = __shfl_sync(0xffffffffu, e, (2 * four) * 4);
       up[t][1] = __shfl_sync(0xffffffffu, e, (2 * four + 1) * 4);
-    }
-    // ---- what this thread's rows of scores, 8 t + 2 four + {0, 1}, see
-    int end[NT][2], first[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = 8 * t + 2 * four + x, at = s.n - s.rows + (r0 + r) / p.G;
-        end[t][x] = r < n_rows ? (p.causal ? min(at + 1, s.keys) : s.keys) : 0;
-        first[t][x] = p.window ? at - p.window + 1 : 0;
-      }
-    const int sinks = p.window ? p.sinks : 0;
-    // by all rows and by any of them
-    const int at0 = s.n - s.rows + r0 / p.G, at1 = s.n - s.rows + (r0 + n_rows - 1) / p.G;
-    const int all_end = p.causal ? min(at0 + 1, s.keys) : s.keys, any_end = p.causal ? min(at1 + 1, s.keys) : s.keys;
-    const int all_first = p.window ? at1 - p.window + 1 : 0, any_first = p.window ? at0 - p.window + 1 : 0;
-
-    float o[NT][DH / 16][4], mo[NT][2], ml[NT][2], l[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int i = 0; i < DH / 16; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][i][e] = 0.0f;
+        for (int x = 0; x < 4; ++x) o[t][i][x] = 0.0f;
 #pragma unroll
       for (int x = 0; x < 2; ++x) mo[t][x] = ml[t][x] = kNone, l[t][x] = 0.0f;
     }
 
-    // This thread's bytes of row 0 of page 0; pieces behind the head are left out.
-    const char* k_mine = static_cast<const char*>(c.k) + kvh * c.ks.h * C::ES + four * 16;
-    const char* v_mine = static_cast<const char*>(c.v) + kvh * c.vs.h * C::ES + quad * (C::VW == 2 ? 8 : 16);
-    const char* s_mine = reinterpret_cast<const char*>((lane < 16 ? c.k_scale : c.v_scale) + kvh * c.ss.h);
-    const bool aligned = c.page_size % kStep == 0;  // a step lies in one page
-    auto key_of = [&](int step) { return step < s.head ? step * kStep : s.from + (step - s.head) * kStep; };
-    // Where a step's key is: the first one, or where it may lie in several pages key lane % 16.
-    auto locate = [&](int step) {
-      return step < step1 ? page_row(c, b, key_of(step) + (aligned ? 0 : lane & 15)) : PageRow{-1, 0};
-    };
-    uint32_t found = 0;  // a bit for each step under way: whether the key is there
-    auto issue = [&](int step, int slot, PageRow at) {
-      found = found << 1 | (at.page >= 0);
-      if (step >= step1) return;
-      const int key0 = key_of(step);
-      // Keys that some row of the tile sees are read.
-      const bool every = key0 + kStep <= any_end && (key0 >= any_first || key0 + kStep <= sinks);
-      const uint32_t dst = smem_u32(smem) + (warp * kStages + slot) * C::SLOT;
-      auto wanted = [&](int key) {
-        const int j = key0 + key;
-        return every || (j < any_end && (j >= any_first || j < sinks));
-      };
-      const int page0 = max(at.page, 0);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int key = quad + 8 * x;
-        const int page = aligned ? at.page : __shfl_sync(0xffffffffu, at.page, key);
-        const int row = aligned ? at.row + key : __shfl_sync(0xffffffffu, at.row, key);
-        const char* src = k_mine + static_cast<uint64_t>(p.kb) * max(page, 0) + static_cast<uint64_t>(p.kl) * row;
-        const bool want = page >= 0 && wanted(key);
-#pragma unroll
-        for (int i = 0; i < C::KP; ++i) {
-          const bool in = (four + 4 * i) * 16 < p.dh * C::ES;
-          copy16(dst + (x * C::KP + i) * 512 + lane * 16, in ? src + i * 64 : k_mine - four * 16, want && in ? 16 : 0);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int key = 2 * four + (x & 1) + 8 * (x >> 1);
-        const int page = aligned ? at.page : __shfl_sync(0xffffffffu, at.page, key);
-        const int row = aligned ? at.row + key : __shfl_sync(0xffffffffu, at.row, key);
-        const char* src = v_mine + static_cast<uint64_t>(p.vb) * max(page, 0) + static_cast<uint64_t>(p.vl) * row;
-        const bool want = page >= 0 && wanted(key);
-        const uint32_t to = dst + C::K_BYTES + x * C::VW * 128;
-        if constexpr (C::VW == 2) {
-          const bool in = quad * 8 < p.dh * C::ES;
-          copy8(to + lane * 8, in ? src : v_mine - quad * 8, want && in ? 8 : 0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < C::VW / 4; ++i) {
-            const bool in = (quad + 8 * i) * 16 < p.dh * C::ES;
-            copy16(to + i * 512 + lane * 16, in ? src + i * 128 : v_mine - quad * 16, want && in ? 16 : 0);
-          }
-        }
-      }
-      if constexpr (C::kScaled) {
-        const int row = aligned ? at.row + (lane & 15) : at.row;
-        copy4(dst + C::K_BYTES + C::V_BYTES + lane * 4,
-              s_mine + static_cast<uint64_t>(p.sb) * page0 + static_cast<uint64_t>(p.sl) * row,
-              at.page >= 0 && wanted(lane & 15) ? 4 : 0);
-      }
-    };
-
-    int step = step0 + warp, slot = 0;
-    {
-      PageRow at[kStages - 1];
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) at[i] = locate(step + i * kWarps);
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) {
-        issue(step + i * kWarps, i, at[i]);
-        copies_commit();
-      }
-    }
-    PageRow next = locate(step + (kStages - 1) * kWarps);
-    for (; step < step1; step += kWarps) {
-      issue(step + (kStages - 1) * kWarps, slot == 0 ? kStages - 1 : slot - 1, next);
+#pragma unroll 1
+    for (int step = step0 + warp; step < step1; step += kWarps) {
+      issue(slot == 0 ? kStages - 1 : slot - 1);
       copies_commit();
-      next = locate(step + kStages * kWarps);
       copies_wait<kStages - 1>();
       __syncwarp();
       const uint8_t* mine = smem + (warp * kStages + slot) * C::SLOT;
       slot = slot == kStages - 1 ? 0 : slot + 1;
+      const unsigned there = __ballot_sync(0xffffffffu, found >> (kStages - 1) & 1);
+      if (!there) continue;
       // ---- scores
       float sc[NT][4];
 #pragma unroll
@@ -432,23 +578,23 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         if (__all_sync(0xffffffffu, big * p.cap.inv <= 1.0f)) cap_within<4 * NT>(&sc[0][0], p.cap);
         else cap_any<4 * NT>(&sc[0][0], p.cap);
       }
-      const bool whole = (key0 + kStep <= all_end && (key0 >= all_first || key0 + kStep <= sinks)) &&
-                         __all_sync(0xffffffffu, found >> (kStages - 1) & 1);
+      const bool whole = (key0 + kStep <= all_end && (key0 >= all_first || key0 + kStep <= sinks)) && there == 0xffffffffu;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[t][e] = C::kScaled ? sc[t][e] + lv[e >> 1] : sc[t][e];
-      unsigned there = 0xffffu;
+      // whether row r of the tile sees the step's key
+      auto sees = [&](int r, int key) {
+        const int at_row = s.n - s.rows + static_cast<int>(p.by_group.div(r0 + r)), j = key0 + key;
+        return r < n_rows && ((there >> key) & 1) && j < (p.causal ? min(at_row + 1, s.keys) : s.keys) &&
+               (!p.window || j > at_row - p.window || j < sinks);
+      };
       if (!whole) {
-        there = __ballot_sync(0xffffffffu, found >> (kStages - 1) & 1);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at_key = quad + 8 * (e >> 1), j = key0 + at_key, x = e & 1;
-            if (!((there >> at_key) & 1) || j >= end[t][x] || (j < first[t][x] && j >= sinks))
-              sc[t][e] = -INFINITY, u[t][e] = -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e)
+            if (!sees(8 * t + 2 * four + (e & 1), quad + 8 * (e >> 1))) sc[t][e] = -INFINITY, u[t][e] = -INFINITY;
       }
       // ---- weights; a new maximum is taken up where one passes the old one by far
       float w[NT][4], y[NT][4];
@@ -527,24 +673,18 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           for (int t = 0; t < NT; ++t)
 #pragma unroll 1
             for (int n = 0; n < 8; ++n) {
-              const int at_row = s.n - s.rows + (r0 + 8 * t + n) / p.G;
-              const int row_end = 8 * t + n < n_rows ? (p.causal ? min(at_row + 1, s.keys) : s.keys) : 0;
-              const int row_first = p.window ? at_row - p.window + 1 : 0;
               uint32_t see[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const int key = 2 * four + (x & 1) + 8 * (x >> 1), j = key0 + key;
-                see[x] = ((there >> key) & 1) && j < row_end && (j >= row_first || j < sinks) ? 0xffffffffu : 0u;
-              }
+              for (int x = 0; x < 4; ++x) see[x] = sees(8 * t + n, 2 * four + (x & 1) + 8 * (x >> 1)) ? 0xffffffffu : 0u;
 #pragma unroll
               for (int i = 0; i < DH / 16; ++i) {
-                const uint32_t y[4] = {v[0][i] & see[0], v[1][i] & see[1], v[2][i] & see[2], v[3][i] & see[3]};
-                const uint32_t a[4] = {__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[0], y[1], 0x7632),
-                                       __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[2], y[3], 0x7632)};
-                float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma<FMT>(z, a, pb[t][0], pb[t][1]);
-                if (n == 2 * four) o[t][i][0] += z[0], o[t][i][2] += z[2];
-                if (n == 2 * four + 1) o[t][i][1] += z[1], o[t][i][3] += z[3];
+                const uint32_t z[4] = {v[0][i] & see[0], v[1][i] & see[1], v[2][i] & see[2], v[3][i] & see[3]};
+                const uint32_t a[4] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[0], z[1], 0x7632),
+                                       __byte_perm(z[2], z[3], 0x5410), __byte_perm(z[2], z[3], 0x7632)};
+                float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma<FMT>(add, a, pb[t][0], pb[t][1]);
+                if (n == 2 * four) o[t][i][0] += add[0], o[t][i][2] += add[2];
+                if (n == 2 * four + 1) o[t][i][1] += add[1], o[t][i][3] += add[3];
               }
             }
           continue;
@@ -566,123 +706,90 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       }
     }
 
-    // ---- join the warps, in the ring's place
-    copies_wait<0>();
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
-        const int r = 8 * t + 2 * four + x;
-        if (r < n_rows) {
-          float* row = so + (warp * ROWS + r) * C::JSTRIDE;
-#pragma unroll
-          for (int i = 0; i < DH / 16; ++i) {
-            // the column pair that this thread's products i belong to
-            const int d = C::kScaled ? quad * (DH / 8) + 2 * i : (quad + 8 * (i / 4)) * 8 + 2 * (i % 4);
-            *reinterpret_cast<float2*>(row + d) = make_float2(o[t][i][x], o[t][i][2 + x]);
-          }
-          if (quad == 0) {
-            float* st = sm + (warp * ROWS + r) * 4;
-            st[0] = mo[t][x], st[1] = ml[t][x], st[2] = l[t][x];
-          }
-        }
-      }
-    __syncthreads();
-    const bool split = step0 > 0 || step1 < s.steps;
-    constexpr int kPart = ROWS * (DH + 4);  // floats of a share: O, then m', m, l of each row
-    // a share that begins its group is a CTA's second, one that goes on with it its first
-    float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (step0 == 0)) * kPart;
-    // Scale, sum and value of a row's shares: finished and written, or left as a share.
-    auto write_out = [&](int r, int d, float mm_o, float mm_l, float ll, float4 acc) {
-      const int tok = (r0 + r) / p.G, head = kvh * p.G + (r0 + r) % p.G;
-      const float f = ll > 0.0f ? fast_exp2(mm_o - mm_l) / ll : ll;  // (0 or NaN)
-      if (d < p.dh) {
-        const uint2 y = p.bf16 ? make_uint2(pack2<true>(acc.x * f, acc.y * f), pack2<true>(acc.z * f, acc.w * f))
-                               : make_uint2(pack2<false>(acc.x * f, acc.y * f), pack2<false>(acc.z * f, acc.w * f));
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + b * p.os.b + tok * p.os.l + head * p.os.h + d) = y;
-      }
-      if (d == 0 && p.lse)
-        p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Lq + tok] = ll == 0.0f ? -INFINITY : (mm_l + fast_log2(ll)) * kLn2;
-    };
-    for (int x = threadIdx.x; x < n_rows * (DH / 4); x += kThreads) {
-      const int r = x / (DH / 4), d = x % (DH / 4) * 4;
-      float mm_o = kNone, mm_l = kNone;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        mm_o = fmaxf(mm_o, sm[(w * ROWS + r) * 4]);
-        mm_l = fmaxf(mm_l, sm[(w * ROWS + r) * 4 + 1]);
-      }
-      float ll = 0.0f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* st = sm + (w * ROWS + r) * 4;
-        const float4 y = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * C::JSTRIDE + d);
-        const float f = fast_exp2(st[0] - mm_o);
-        ll = fmaf(fast_exp2(st[1] - mm_l), st[2], ll);
-        acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
-        acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
-      }
-      if (split) {
-        *reinterpret_cast<float4*>(part + r * DH + d) = acc;
-        if (d == 0) {
-          float* st = part + ROWS * DH + r * 4;
-          st[0] = mm_o, st[1] = mm_l, st[2] = ll;
-        }
-      } else {
-        write_out(r, d, mm_o, mm_l, ll, acc);
-      }
+    // ---- what its join needs
+    joining = true;
+    split = step0 > 0 || step1 < s.steps;
+    was_b = b, was_kvh = kvh, was_r0 = r0, was_rows = n_rows;
+    was_slot = step0 == 0;
+    if (split && threadIdx.x == 0) {
+      const int64_t first = lo - step0;
+      s_share[was_slot] = Share{first, first + s.steps - 1, b, kvh, r0, n_rows, 1};
     }
-    __syncthreads();
-    if (split) {
-      // The CTAs whose stretches hold the group's first and last step.
-      const int64_t g0 = before + static_cast<int64_t>(group) * s.steps, g1 = g0 + s.steps - 1;
-      const int c0 = cut.of(g0), c1 = cut.of(g1);
-      if (threadIdx.x == 0) {
-        __threadfence();
-        const int last = atomicAdd(p.arrived + c0, 1) == c1 - c0;
-        if (last) p.arrived[c0] = 0;
-        __threadfence();
-        s_last = last;
-      }
-      __syncthreads();
-      if (s_last) {
-        for (int x = threadIdx.x; x < n_rows * (DH / 4); x += kThreads) {
-          const int r = x / (DH / 4), d = x % (DH / 4) * 4;
-          auto share = [&](int cta) { return p.part + (2 * static_cast<int64_t>(cta) + (cta == c0)) * kPart; };
-          float mm_o = kNone, mm_l = kNone;
-#pragma unroll 4
-          for (int cta = c0; cta <= c1; ++cta) {
-            const float* st = share(cta) + ROWS * DH + r * 4;
-            mm_o = fmaxf(mm_o, __ldcg(st));
-            mm_l = fmaxf(mm_l, __ldcg(st + 1));
-          }
-              float ll = 0.0f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int cta = c0; cta <= c1; ++cta) {
-            const float* at_share = share(cta);
-            const float4 st = __ldcg(reinterpret_cast<const float4*>(at_share + ROWS * DH + r * 4));
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(at_share + r * DH + d));
-            const float f = fast_exp2(st.x - mm_o);
-            ll = fmaf(fast_exp2(st.y - mm_l), st.z, ll);
-            acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
-            acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
-          }
-          write_out(r, d, mm_o, mm_l, ll, acc);
-        }
-      }
-    }
-    // ---- the next stretch
     lo += step1 - step0;
-    if (lo >= hi) break;
-    while (lo >= before + s.total) {
-      before += s.total;
-      s = sequence<ROWS>(p, ++b);
+  }
+
+  // ---- groups that are shared: the last CTA to be done joins all shares, in order
+  if (threadIdx.x == 0 && (s_share[0].used | s_share[1].used)) {
+    __threadfence();
+    for (int i = 0; i < 2; ++i) {
+      if (!s_share[i].used) continue;
+      const int c0 = cut.of(s_share[i].first), n = cut.of(s_share[i].last) - c0 + 1;
+      const bool last = atomicAdd(p.arrived + c0, 1) == n - 1;
+      if (last) p.arrived[c0] = 0;
+      s_last[i][0] = c0, s_last[i][1] = last ? n : 0;
     }
+    __threadfence();
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!s_share[i].used || !s_last[i][1]) continue;
+    // All at once: a warp a row's statistics, then the values, with as many threads a
+    // column as there are (a round trip to L2 takes 0.5 us and more).
+    const int c0 = s_last[i][0], n_shares = s_last[i][1], rows = s_share[i].rows;
+    auto share = [&](int k) { return p.part + (2 * static_cast<int64_t>(c0 + k) + (k == 0)) * kPart; };
+    float* factor = reinterpret_cast<float*>(smem);  // [rows][n_shares]
+    float* stat = factor + ROWS * kMaxCtas;          // [rows][4]
+    float4* sums = reinterpret_cast<float4*>(stat + ROWS * 4);
+    for (int r = warp; r < rows; r += kWarps) {
+      float mm_o = kNone, mm_l = kNone, ll = 0.0f;
+      for (int k = lane; k < n_shares; k += 32) {
+        const float4 st = __ldcg(reinterpret_cast<const float4*>(share(k) + ROWS * DH + r * 4));
+        factor[r * n_shares + k] = st.x;
+        mm_o = fmaxf(mm_o, st.x);
+        const float m = fmaxf(mm_l, st.y);
+        ll = ll * fast_exp2(mm_l - m) + st.z * fast_exp2(st.y - m);
+        mm_l = m;
+      }
+#pragma unroll
+      for (int k = 16; k; k >>= 1) {
+        mm_o = fmaxf(mm_o, __shfl_xor_sync(0xffffffffu, mm_o, k));
+        const float m1 = __shfl_xor_sync(0xffffffffu, mm_l, k), l1 = __shfl_xor_sync(0xffffffffu, ll, k);
+        const float m = fmaxf(mm_l, m1);
+        ll = __fadd_rn(__fmul_rn(ll, fast_exp2(mm_l - m)), __fmul_rn(l1, fast_exp2(m1 - m)));  // (the same in both lanes)
+        mm_l = m;
+      }
+      for (int k = lane; k < n_shares; k += 32) factor[r * n_shares + k] = fast_exp2(factor[r * n_shares + k] - mm_o);
+      if (lane == 0) stat[r * 4] = mm_o, stat[r * 4 + 1] = mm_l, stat[r * 4 + 2] = ll;
+    }
+    __syncthreads();
+    const int columns = rows * (DH / 4), parts = max(kThreads / columns, 1);
+    for (int x = threadIdx.x; x < columns * parts; x += kThreads) {
+      const int column = x % columns, r = column / (DH / 4), d = column % (DH / 4) * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int k = x / columns; k < n_shares; k += parts) {
+        const float4 z = __ldcg(reinterpret_cast<const float4*>(share(k) + r * DH + d));
+        const float f = factor[r * n_shares + k];
+        acc.x = fmaf(f, z.x, acc.x), acc.y = fmaf(f, z.y, acc.y);
+        acc.z = fmaf(f, z.z, acc.z), acc.w = fmaf(f, z.w, acc.w);
+      }
+      if (parts > 1) sums[x] = acc;
+      else write_out(s_share[i].b, s_share[i].kvh, s_share[i].r0 + r, d, stat[r * 4], stat[r * 4 + 1], stat[r * 4 + 2], acc);
+    }
+    if (parts > 1) {
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < columns) {
+        const int r = threadIdx.x / (DH / 4), d = threadIdx.x % (DH / 4) * 4;
+        float4 acc = sums[threadIdx.x];
+        for (int k = 1; k < parts; ++k) {
+          const float4 z = sums[threadIdx.x + k * columns];
+          acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
+        }
+        write_out(s_share[i].b, s_share[i].kvh, s_share[i].r0 + r, d, stat[r * 4], stat[r * 4 + 1], stat[r * 4 + 2], acc);
+      }
+    }
+    __syncthreads();
   }
 }
 

@@ -55,6 +55,7 @@ struct PageAttnParams {
   int B, Hq, Hkv, G, dh, Lq;
   int causal, window, sinks, append, bf16;
   float scale, softcap;
+  FastDiv by_group;                 // by G
   uint32_t kb, kl, vb, vl, sb, sl;  // page_attn.cu: strides of a page and a row in bytes
   CapForm cap;
   Strides3 qs, os;

@@ -513,6 +513,7 @@ PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q,
     int sms = 0;
     if (int e = cuda_status(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "device")) return e;
     if (p.softcap > 0) set_cap_form(p.cap, p.scale, p.softcap);
+    p.by_group = FastDiv::of(static_cast<uint32_t>(p.G));
     p.kb = static_cast<uint32_t>(c->k_stride[0] * es), p.kl = static_cast<uint32_t>(c->k_stride[1] * es);
     p.vb = static_cast<uint32_t>(c->v_stride[0] * es), p.vl = static_cast<uint32_t>(c->v_stride[1] * es);
     p.sb = static_cast<uint32_t>(c->scale_stride[0] * 4), p.sl = static_cast<uint32_t>(c->scale_stride[1] * 4);
