@@ -1,16 +1,18 @@
 // Attention of a token's rows, or a few tokens', over the pages of a cache.
 //
-// Bound by reading the codes of K and V once.  A thread brings the very bytes that
-// its products take, by 16-byte asynchronous copies into a ring of its own in shared
-// memory: the contraction over a head's values may run in any order, so that a
-// thread holds 16 bytes in a row of each key (and of its query rows), and the
-// products are transposed, so that keys and values are the operand of 16 rows and 8
-// query rows fill a product:
+// Bound by reading the codes of K and V once.  Each warp brings its own steps of 16
+// keys by 16-byte asynchronous copies, whole rows at a time, into a ring of its own in
+// shared memory, and takes the products' operands from there as they are: the
+// contraction over a head's values may run in any order, so that a thread holds 16
+// bytes in a row of each key (and of its query rows), and the products are
+// transposed, so that keys and values are the operand of 16 rows and 8 query rows
+// fill a product:
 //   S^T = K Q^T      a thread holds keys lane / 4 and + 8 of a step of 16
 //   O^T += V^T P^T   a thread holds the keys 2 (lane % 4) + {0, 1, 8, 9}, whose
 //                    bytes of one column are paired by a byte permutation
 // No barrier and no alignment to a page's start stand between the pages and the
-// products, and 100 to 200 kB an SM are on their way.
+// products.  (A copy of a thread's own 16 bytes, half a row of 128 a copy, takes a
+// quarter longer: 64-byte requests to L2.)
 //
 // Codes become f16 (exactly); queries become f16 with a power of two for each row;
 // a key's scale multiplies its scores.  A value's scale enters its weight as an
@@ -48,8 +50,11 @@ struct ACfg {
   static constexpr int KS = kScaled ? 4 : 2;  // products (of 16 values) a piece
   static constexpr int VW = DH * ES / 32;   // 4-byte words of a value in a thread
   static constexpr int JSTRIDE = DH + 4;    // floats between a join area's rows
-  static constexpr int K_BYTES = 2 * KP * 512, V_BYTES = 4 * VW * 128;
-  static constexpr int SLOT = K_BYTES + V_BYTES + (kScaled ? 128 : 0);  // a warp's step: K, V, the scales
+  static constexpr int RB = DH * ES;       // bytes of a row
+  static constexpr int LPR = RB / 16;      // lanes that copy it
+  static constexpr int RPC = 32 / LPR;     // rows of a copy
+  static constexpr int KV = kStep * RB;    // a step's keys, or values
+  static constexpr int SLOT = 2 * KV + (kScaled ? 128 : 0);  // a warp's step: K, V, the scales
   // Two CTAs an SM: 128, 168 or 255 registers a thread.
   static constexpr int WARPS = NT == 1 && DH == 64 ? 8 : NT == 1 && kScaled ? 6 : DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
@@ -58,7 +63,7 @@ struct ACfg {
   static constexpr int RING = WARPS * STAGES * SLOT;
   static constexpr int SMEM = RING + JOIN;
   static_assert(2 * (SMEM + 1024 + 256) <= 233472, "two CTAs an SM");
-  static_assert((ROWS * (kMaxCtas + 4) + THREADS * 4) * 4 <= RING, "the join of CTAs, in the ring's place");
+  static_assert((2 * ROWS * (kMaxCtas + 4) + THREADS * 4) * 4 <= RING, "the join of CTAs, in the ring's place");
 };
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -128,9 +133,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -138,6 +140,15 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where 16-byte piece `piece` of row `row` of a step lies: within 128 bytes pieces
+// change places so that eight lanes that read two adjacent rows' four pieces (keys) or
+// four even or odd rows' two (values) meet in no bank.
+template <int RB>
+__device__ __forceinline__ int placed(int row, int piece) {
+  if constexpr (RB == 64) return row / 2 * 128 + ((row % 2 * 4 + piece) ^ (row / 2 % 4 * 2)) * 16;
+  return row * RB + (piece ^ (((row / 4 ^ row) & 1) * 4 + (row & 2))) * 16;
 }
 
 // What a sequence's steps are: steps [0, head) from key 0 on (the sinks), the
@@ -185,7 +196,8 @@ struct Cut {
   }
 };
 
-// A group of which a CTA has a share: its first and last step on the line, and its rows.
+// A group of which a CTA has a share: its first and last step on the line, and its rows;
+// in the end its first CTA and, as `used`, how many shares there are to be joined.
 struct Share {
   int64_t first, last;
   int b, kvh, r0, rows, used;
@@ -202,7 +214,6 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   float* so = reinterpret_cast<float*>(smem + C::RING);  // [kWarps][ROWS][JSTRIDE]
   float* sm = so + kWarps * ROWS * C::JSTRIDE;           // [kWarps][ROWS][4]: m', m, l
   __shared__ Share s_share[2];  // of a group that began before this CTA, of one that it begins
-  __shared__ int s_last[2][2];  // whether this CTA is the last of the group's, its first CTA and their number
   static_assert(kMaxCtas * sizeof(int) <= PSV_PAGE_SCRATCH_HEAD, "counters in the workspace's head");
   const PageCacheDev& c = p.c;
   const int warp = warp_id(), lane = lane_id(), quad = lane / 4, four = lane % 4;
@@ -251,7 +262,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
 
-  const uint32_t ring = smem_u32(smem) + warp * kStages * C::SLOT + lane * 16;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * C::SLOT;
+  const bool in_head = lane % C::LPR * 16 < p.dh * C::ES;  // the piece that this lane copies
   const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
   const int sinks = p.window ? p.sinks : 0;
   const char *k_mine = nullptr, *v_mine = nullptr, *s_mine = nullptr;
@@ -295,25 +307,18 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       for (int h = 0; h < 2; ++h) {
         const char* k = k_mine + offset(p.kb, p.kl, half[h].page, half[h].row);
         const char* v = v_mine + offset(p.vb, p.vl, half[h].page, half[h].row);
+        if (in_head) {
 #pragma unroll
-        for (int i = 0; i < C::KP; ++i)
-          if ((four + 4 * i) * 16 < p.dh * C::ES) copy16(dst + (h * C::KP + i) * 512, k + i * 64);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t to = dst + C::K_BYTES + (2 * h + x) * C::VW * 128;
-          if constexpr (C::VW == 2) {
-            if (quad * 8 < p.dh * C::ES) copy8(to - lane * 8, v, 8);
-          } else {
-#pragma unroll
-            for (int i = 0; i < C::VW / 4; ++i)
-              if ((quad + 8 * i) * 16 < p.dh * C::ES) copy16(to + i * 512, v + i * 128);
+          for (int i = 0; i < 8 / C::RPC; ++i) {
+            const uint32_t to = dst + placed<C::RB>(8 * h + i * C::RPC + lane / C::LPR, lane % C::LPR);
+            copy16(to, k + static_cast<uint64_t>(p.kl) * (i * C::RPC));
+            copy16(to + C::KV, v + static_cast<uint64_t>(p.vl) * (i * C::RPC));
           }
-          v += p.vl;
         }
       }
       if constexpr (C::kScaled) {
         const bool h = lane & 8;
-        copy4(dst + C::K_BYTES + C::V_BYTES - lane * 12,
+        copy4(dst + 2 * C::KV + lane * 4,
               s_mine + offset(p.sb, p.sl, h ? half[1].page : half[0].page, (h ? half[1].row : half[0].row) + lane % 8), 4);
       }
       return;
@@ -326,34 +331,16 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     if (at.page < 0 || j >= any_end || (j < any_first && j >= sinks)) at = PageRow{-1, 0};
     found |= at.page >= 0;
 #pragma unroll 1
-    for (int x = 0; x < 2; ++x) {
-      const int page = __shfl_sync(0xffffffffu, at.page, quad + 8 * x), row = __shfl_sync(0xffffffffu, at.row, quad + 8 * x);
-      const char* src = k_mine + offset(p.kb, p.kl, max(page, 0), row) - offset(0, p.kl, 0, quad);
-#pragma unroll
-      for (int i = 0; i < C::KP; ++i) {
-        const bool in = (four + 4 * i) * 16 < p.dh * C::ES;
-        copy16(dst + (x * C::KP + i) * 512, in ? src + i * 64 : src - four * 16, page >= 0 && in ? 16 : 0);
-      }
-    }
-#pragma unroll 1
-    for (int x = 0; x < 4; ++x) {
-      const int key = 2 * four + (x & 1) + 8 * (x >> 1);
-      const int page = __shfl_sync(0xffffffffu, at.page, key), row = __shfl_sync(0xffffffffu, at.row, key);
-      const char* src = v_mine + offset(p.vb, p.vl, max(page, 0), row) - offset(0, p.vl, 0, 2 * four);
-      const uint32_t to = dst + C::K_BYTES + x * C::VW * 128;
-      if constexpr (C::VW == 2) {
-        const bool in = quad * 8 < p.dh * C::ES;
-        copy8(to - lane * 8, in ? src : src - quad * 8, page >= 0 && in ? 8 : 0);
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::VW / 4; ++i) {
-          const bool in = (quad + 8 * i) * 16 < p.dh * C::ES;
-          copy16(to + i * 512, in ? src + i * 128 : src - quad * 16, page >= 0 && in ? 16 : 0);
-        }
-      }
+    for (int i = 0; i < kStep / C::RPC; ++i) {
+      const int key = i * C::RPC + lane / C::LPR;
+      const int page = __shfl_sync(0xffffffffu, at.page, key), row = __shfl_sync(0xffffffffu, at.row, key) - lane / C::LPR;
+      const uint32_t to = dst + placed<C::RB>(key, lane % C::LPR);
+      const int bytes = page >= 0 && in_head ? 16 : 0;
+      copy16(to, bytes ? k_mine + offset(p.kb, 0, page, 0) + static_cast<int64_t>(p.kl) * row : static_cast<const char*>(c.k), bytes);
+      copy16(to + C::KV, bytes ? v_mine + offset(p.vb, 0, page, 0) + static_cast<int64_t>(p.vl) * row : static_cast<const char*>(c.v), bytes);
     }
     if constexpr (C::kScaled)
-      copy4(dst + C::K_BYTES + C::V_BYTES - lane * 12, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);
+      copy4(dst + 2 * C::KV + lane * 4, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);
   };
   // A row's finished value and lse.
   auto write_out = [&](int wb, int wkvh, int row, int d, float mm_o, float mm_l, float ll, float4 acc) {
@@ -395,9 +382,9 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       const int at1 = s.n - s.rows + static_cast<int>(p.by_group.div(r0 + n_rows - 1));
       all_end = p.causal ? min(at0 + 1, s.keys) : s.keys, any_end = p.causal ? min(at1 + 1, s.keys) : s.keys;
       all_first = p.window ? at1 - p.window + 1 : 0, any_first = p.window ? at0 - p.window + 1 : 0;
-      // this thread's bytes of a step's first row (its half's, for keys), in page 0
-      k_mine = static_cast<const char*>(c.k) + kvh * c.ks.h * C::ES + offset(0, p.kl, 0, quad) + four * 16;
-      v_mine = static_cast<const char*>(c.v) + kvh * c.vs.h * C::ES + offset(0, p.vl, 0, 2 * four) + quad * (C::VW == 2 ? 8 : 16);
+      // the piece that this lane copies of the first rows of page 0
+      k_mine = static_cast<const char*>(c.k) + kvh * c.ks.h * C::ES + offset(0, p.kl, 0, lane / C::LPR) + lane % C::LPR * 16;
+      v_mine = static_cast<const char*>(c.v) + kvh * c.vs.h * C::ES + offset(0, p.vl, 0, lane / C::LPR) + lane % C::LPR * 16;
       s_mine = reinterpret_cast<const char*>((lane < 16 ? c.k_scale : c.v_scale) + kvh * c.ss.h);
       issued = 0;
       slot = 0;
@@ -540,8 +527,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         for (int e = 0; e < 4; ++e) sc[t][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < C::KP; ++i) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(mine + i * 512 + lane * 16);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(mine + (C::KP + i) * 512 + lane * 16);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(mine + placed<C::RB>(quad, four + 4 * i));
+        const uint4 k1 = *reinterpret_cast<const uint4*>(mine + 8 * C::RB + placed<C::RB>(quad, four + 4 * i));
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int x = 0; x < C::KS; ++x) {
@@ -558,7 +545,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       }
       float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
       if constexpr (C::kScaled) {
-        const float* scales = reinterpret_cast<const float*>(mine + C::K_BYTES + C::V_BYTES);
+        const float* scales = reinterpret_cast<const float*>(mine + 2 * C::KV);
         ks[0] = scales[quad], ks[1] = scales[quad + 8];
         lv[0] = fast_log2(scales[16 + quad]), lv[1] = fast_log2(scales[24 + quad]);
       }
@@ -643,14 +630,15 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       uint32_t v[4][C::VW];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const uint8_t* from = mine + C::K_BYTES + x * C::VW * 128;
+        const uint8_t* from = mine + C::KV + (x >> 1) * 8 * C::RB;
+        const int row = 2 * four + (x & 1);
         if constexpr (C::VW == 2) {
-          const uint2 z = *reinterpret_cast<const uint2*>(from + lane * 8);
+          const uint2 z = *reinterpret_cast<const uint2*>(from + placed<C::RB>(row, quad / 2) + quad % 2 * 8);
           v[x][0] = z.x, v[x][1] = z.y;
         } else {
 #pragma unroll
           for (int i = 0; i < C::VW / 4; ++i) {
-            const uint4 z = *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16);
+            const uint4 z = *reinterpret_cast<const uint4*>(from + placed<C::RB>(row, quad + 8 * i));
             v[x][4 * i] = z.x, v[x][4 * i + 1] = z.y, v[x][4 * i + 2] = z.z, v[x][4 * i + 3] = z.w;
           }
         }
@@ -720,76 +708,107 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 
   // ---- groups that are shared: the last CTA to be done joins all shares, in order
   if (threadIdx.x == 0 && (s_share[0].used | s_share[1].used)) {
+    int c0[2], n[2], at[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (s_share[i].used) c0[i] = cut.of(s_share[i].first), n[i] = cut.of(s_share[i].last) - c0[i] + 1;
     __threadfence();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (s_share[i].used) at[i] = atomicAdd(p.arrived + c0[i], 1);
+#pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!s_share[i].used) continue;
-      const int c0 = cut.of(s_share[i].first), n = cut.of(s_share[i].last) - c0 + 1;
-      const bool last = atomicAdd(p.arrived + c0, 1) == n - 1;
-      if (last) p.arrived[c0] = 0;
-      s_last[i][0] = c0, s_last[i][1] = last ? n : 0;
+      const bool last = at[i] == n[i] - 1;
+      if (last) p.arrived[c0[i]] = 0;
+      s_share[i].first = c0[i], s_share[i].used = last ? n[i] : 0;
     }
     __threadfence();
   }
   __syncthreads();
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    if (!s_share[i].used || !s_last[i][1]) continue;
-    // All at once: a warp a row's statistics, then the values, with as many threads a
-    // column as there are (a round trip to L2 takes 0.5 us and more).
-    const int c0 = s_last[i][0], n_shares = s_last[i][1], rows = s_share[i].rows;
-    auto share = [&](int k) { return p.part + (2 * static_cast<int64_t>(c0 + k) + (k == 0)) * kPart; };
-    float* factor = reinterpret_cast<float*>(smem);  // [rows][n_shares]
-    float* stat = factor + ROWS * kMaxCtas;          // [rows][4]
-    float4* sums = reinterpret_cast<float4*>(stat + ROWS * 4);
-    for (int r = warp; r < rows; r += kWarps) {
-      float mm_o = kNone, mm_l = kNone, ll = 0.0f;
-      for (int k = lane; k < n_shares; k += 32) {
-        const float4 st = __ldcg(reinterpret_cast<const float4*>(share(k) + ROWS * DH + r * 4));
-        factor[r * n_shares + k] = st.x;
-        mm_o = fmaxf(mm_o, st.x);
-        const float m = fmaxf(mm_l, st.y);
-        ll = ll * fast_exp2(mm_l - m) + st.z * fast_exp2(st.y - m);
-        mm_l = m;
-      }
+  // The rows of both groups at once: a warp a row's statistics, then the values, as many
+  // threads a column as there are and 16 reads a thread at a time, the first ones before
+  // the statistics are known (a round trip to L2 takes 0.6 us and more).
+  const int rows0 = s_share[0].used ? s_share[0].rows : 0, rows1 = s_share[1].used ? s_share[1].rows : 0;
+  const int rows = rows0 + rows1;
+  if (rows == 0) return;
+  float* factor = reinterpret_cast<float*>(smem);  // [rows][kMaxCtas]
+  float* stat = factor + 2 * ROWS * kMaxCtas;      // [rows][4]
+  float4* sums = reinterpret_cast<float4*>(stat + 2 * ROWS * 4);
+  auto share = [&](int i, int k) { return p.part + (2 * (s_share[i].first + k) + (k == 0)) * kPart; };
+  constexpr int kReads = 16;
+  const int columns = rows * (DH / 4), parts = max(kThreads / columns, 1);
+  // reads [k0, k0 + kReads) of column and part x
+  auto read = [&](int x, int k0, float4 (&z)[kReads]) {
+    const int column = x % columns, r = column / (DH / 4), i = r >= rows0, n = s_share[i].used;
+    const int at = (i ? r - rows0 : r) * DH + column % (DH / 4) * 4;
 #pragma unroll
-      for (int k = 16; k; k >>= 1) {
-        mm_o = fmaxf(mm_o, __shfl_xor_sync(0xffffffffu, mm_o, k));
-        const float m1 = __shfl_xor_sync(0xffffffffu, mm_l, k), l1 = __shfl_xor_sync(0xffffffffu, ll, k);
-        const float m = fmaxf(mm_l, m1);
-        ll = __fadd_rn(__fmul_rn(ll, fast_exp2(mm_l - m)), __fmul_rn(l1, fast_exp2(m1 - m)));  // (the same in both lanes)
-        mm_l = m;
-      }
-      for (int k = lane; k < n_shares; k += 32) factor[r * n_shares + k] = fast_exp2(factor[r * n_shares + k] - mm_o);
-      if (lane == 0) stat[r * 4] = mm_o, stat[r * 4 + 1] = mm_l, stat[r * 4 + 2] = ll;
+    for (int e = 0; e < kReads; ++e) {
+      const int k = x / columns + (k0 + e) * parts;
+      z[e] = k < n ? __ldcg(reinterpret_cast<const float4*>(share(i, k) + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+  };
+  float4 z[kReads];
+  if (static_cast<int>(threadIdx.x) < columns * parts) read(threadIdx.x, 0, z);
+  for (int r = warp; r < rows; r += kWarps) {
+    const int i = r >= rows0, n = s_share[i].used, at = ROWS * DH + (i ? r - rows0 : r) * 4;
+    float mm_o = kNone, mm_l = kNone, ll = 0.0f;
+    for (int k = lane; k < n; k += 32) {
+      const float4 st = __ldcg(reinterpret_cast<const float4*>(share(i, k) + at));
+      factor[r * kMaxCtas + k] = st.x;
+      mm_o = fmaxf(mm_o, st.x);
+      const float m = fmaxf(mm_l, st.y);
+      ll = ll * fast_exp2(mm_l - m) + st.z * fast_exp2(st.y - m);
+      mm_l = m;
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) {
+      mm_o = fmaxf(mm_o, __shfl_xor_sync(0xffffffffu, mm_o, k));
+      const float m1 = __shfl_xor_sync(0xffffffffu, mm_l, k), l1 = __shfl_xor_sync(0xffffffffu, ll, k);
+      const float m = fmaxf(mm_l, m1);
+      ll = __fadd_rn(__fmul_rn(ll, fast_exp2(mm_l - m)), __fmul_rn(l1, fast_exp2(m1 - m)));  // (the same in both lanes)
+      mm_l = m;
+    }
+    for (int k = lane; k < n; k += 32) factor[r * kMaxCtas + k] = fast_exp2(factor[r * kMaxCtas + k] - mm_o);
+    if (lane == 0) stat[r * 4] = mm_o, stat[r * 4 + 1] = mm_l, stat[r * 4 + 2] = ll;
+  }
+  __syncthreads();
+  auto finish = [&](int column, float4 acc) {
+    const int r = column / (DH / 4), i = r >= rows0;
+    write_out(s_share[i].b, s_share[i].kvh, s_share[i].r0 + (i ? r - rows0 : r), column % (DH / 4) * 4, stat[r * 4],
+              stat[r * 4 + 1], stat[r * 4 + 2], acc);
+  };
+#pragma unroll 1
+  for (int x = threadIdx.x; x < columns * parts; x += kThreads) {
+    const int column = x % columns, r = column / (DH / 4), n = s_share[r >= rows0].used;
+    if (x >= kThreads) read(x, 0, z);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0;;) {
+#pragma unroll
+      for (int e = 0; e < kReads; ++e) {
+        const int k = x / columns + (k0 + e) * parts;
+        const float f = k < n ? factor[r * kMaxCtas + k] : 0.0f;
+        acc.x = fmaf(f, z[e].x, acc.x), acc.y = fmaf(f, z[e].y, acc.y);
+        acc.z = fmaf(f, z[e].z, acc.z), acc.w = fmaf(f, z[e].w, acc.w);
+      }
+      k0 += kReads;
+      if (k0 * parts >= n) break;
+      read(x, k0, z);
+    }
+    if (parts > 1) sums[x] = acc;
+    else finish(column, acc);
+  }
+  if (parts > 1) {
     __syncthreads();
-    const int columns = rows * (DH / 4), parts = max(kThreads / columns, 1);
-    for (int x = threadIdx.x; x < columns * parts; x += kThreads) {
-      const int column = x % columns, r = column / (DH / 4), d = column % (DH / 4) * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int k = x / columns; k < n_shares; k += parts) {
-        const float4 z = __ldcg(reinterpret_cast<const float4*>(share(k) + r * DH + d));
-        const float f = factor[r * n_shares + k];
-        acc.x = fmaf(f, z.x, acc.x), acc.y = fmaf(f, z.y, acc.y);
-        acc.z = fmaf(f, z.z, acc.z), acc.w = fmaf(f, z.w, acc.w);
+    if (static_cast<int>(threadIdx.x) < columns) {
+      float4 acc = sums[threadIdx.x];
+      for (int k = 1; k < parts; ++k) {
+        const float4 y = sums[threadIdx.x + k * columns];
+        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
       }
-      if (parts > 1) sums[x] = acc;
-      else write_out(s_share[i].b, s_share[i].kvh, s_share[i].r0 + r, d, stat[r * 4], stat[r * 4 + 1], stat[r * 4 + 2], acc);
+      finish(threadIdx.x, acc);
     }
-    if (parts > 1) {
-      __syncthreads();
-      if (static_cast<int>(threadIdx.x) < columns) {
-        const int r = threadIdx.x / (DH / 4), d = threadIdx.x % (DH / 4) * 4;
-        float4 acc = sums[threadIdx.x];
-        for (int k = 1; k < parts; ++k) {
-          const float4 z = sums[threadIdx.x + k * columns];
-          acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
-        }
-        write_out(s_share[i].b, s_share[i].kvh, s_share[i].r0 + r, d, stat[r * 4], stat[r * 4 + 1], stat[r * 4 + 2], acc);
-      }
-    }
-    __syncthreads();
   }
 }
 
