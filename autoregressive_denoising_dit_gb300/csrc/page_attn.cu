@@ -49,6 +49,8 @@ struct ACfg {
   static constexpr int KP = DH * ES / 64;   // 16-byte pieces of a key in a thread
   static constexpr int KS = kScaled ? 4 : 2;  // products (of 16 values) a piece
   static constexpr int VW = DH * ES / 32;   // 4-byte words of a value in a thread
+  static constexpr bool QS = NT == 2;       // queries in shared memory: registers for 12 warps an SM
+  static constexpr int Q_BYTES = QS ? NT * KP * KS * 256 + ROWS * 4 : 0;  // operands, a factor a row
   static constexpr int JSTRIDE = DH + 4;    // floats between a join area's rows
   static constexpr int RB = DH * ES;       // bytes of a row
   static constexpr int LPR = RB / 16;      // lanes that copy it
@@ -56,12 +58,12 @@ struct ACfg {
   static constexpr int KV = kStep * RB;    // a step's keys, or values
   static constexpr int SLOT = 2 * KV + (kScaled ? 128 : 0);  // a warp's step: K, V, the scales
   // Two CTAs an SM: 128, 168 or 255 registers a thread.
-  static constexpr int WARPS = NT == 1 && DH == 64 ? 8 : NT == 1 && kScaled ? 6 : DH == 64 ? 6 : 4;
+  static constexpr int WARPS = NT == 1 && DH == 64 ? 8 : (NT == 1 && kScaled) || DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int JOIN = WARPS * ROWS * (JSTRIDE + 4) * 4;  // the warps' sums at the end of a group
-  static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN) / (WARPS * SLOT));
+  static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN - Q_BYTES) / (WARPS * SLOT));
   static constexpr int RING = WARPS * STAGES * SLOT;
-  static constexpr int SMEM = RING + JOIN;
+  static constexpr int SMEM = RING + JOIN + Q_BYTES;
   static_assert(2 * (SMEM + 1024 + 256) <= 233472, "two CTAs an SM");
   static_assert((2 * ROWS * (kMaxCtas + 4) + THREADS * 4) * 4 <= RING, "the join of CTAs, in the ring's place");
 };
@@ -190,6 +192,11 @@ struct Cut {
     if (n) each = divide(all, n), more = static_cast<int>(all - each * n);
   }
   __device__ __forceinline__ int64_t begin(int cta) const { return each * cta + min(cta, more); }
+  // A cut this near to an end of its group is moved there, so that fewer CTAs have
+  // shares of two groups.
+  __device__ __forceinline__ int near(int steps) const {
+    return static_cast<int>(min(each >> 3, static_cast<int64_t>(steps >> 2)));
+  }
   __device__ __forceinline__ int of(int64_t x) const {
     const int64_t longer = (each + 1) * more;
     return static_cast<int>(x < longer ? divide(x, each + 1) : more + divide(x - longer, each));
@@ -213,6 +220,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   extern __shared__ __align__(128) uint8_t smem[];
   float* so = reinterpret_cast<float*>(smem + C::RING);  // [kWarps][ROWS][JSTRIDE]
   float* sm = so + kWarps * ROWS * C::JSTRIDE;           // [kWarps][ROWS][4]: m', m, l
+  uint4* sq = reinterpret_cast<uint4*>(smem + C::RING + C::JOIN);  // QS: [NT][KP * KS / 2][lane]
+  float* sq_up = reinterpret_cast<float*>(sq + NT * C::KP * C::KS * 16);  // [ROWS]
   __shared__ Share s_share[2];  // of a group that began before this CTA, of one that it begins
   static_assert(kMaxCtas * sizeof(int) <= PSV_PAGE_SCRATCH_HEAD, "counters in the workspace's head");
   const PageCacheDev& c = p.c;
@@ -237,29 +246,48 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   const Cut cut(all, static_cast<int>(min(static_cast<int64_t>(gridDim.x), (all + kWarps - 1) / kWarps)));
   if (static_cast<int>(blockIdx.x) >= cut.ctas) return;
-  int64_t lo = cut.begin(blockIdx.x);
-  const int64_t hi = cut.begin(blockIdx.x + 1);
+  int64_t lo = 0, hi = 0;
   int b = 0;
   int64_t before = 0;  // steps of earlier sequences
   Seq s;
-  for (int b0 = 0;; b0 += 32) {
-    if (b0) rows_b = rows_at(b0 + lane), n_b = b0 + lane < p.B ? page_length(p, b0 + lane, rows_b) : 0;
-    const int64_t mine = sequence<ROWS>(p, rows_b, n_b).total;
-    int64_t sum = mine;
+  {
+    int64_t sum0 = 0;
+    bool begun = false;
+    const int64_t lo0 = cut.begin(blockIdx.x), hi0 = cut.begin(blockIdx.x + 1);
+    for (int b0 = 0;; b0 += 32) {
+      if (b0) rows_b = rows_at(b0 + lane), n_b = b0 + lane < p.B ? page_length(p, b0 + lane, rows_b) : 0;
+      const Seq mine = sequence<ROWS>(p, rows_b, n_b);
+      int64_t sum = mine.total;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      // the cut at x, if it lies in one of these sequences: there, or at the end of a group that is near
+      auto moved = [&](int64_t x, int& at) {
+        const unsigned hit = __ballot_sync(0xffffffffu, sum0 + sum > x);
+        at = __ffs(hit) - 1;
+        if (!hit) return x;
+        const int steps = __shfl_sync(0xffffffffu, mine.steps, at);
+        const int64_t within = x - sum0 - __shfl_sync(0xffffffffu, sum - mine.total, at);
+        const int64_t rest = within - divide(within, steps) * steps;
+        return rest < cut.near(steps) ? x - rest : steps - rest < cut.near(steps) ? x + steps - rest : x;
+      };
+      int at;
+      if (!begun) {
+        lo = moved(lo0, at);
+        if (at >= 0) {
+          begun = true;
+          b = b0 + at;
+          before = sum0 + __shfl_sync(0xffffffffu, sum - mine.total, at);
+          s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
+        }
+      }
+      hi = moved(hi0, at);
+      if (at >= 0) break;
+      sum0 += __shfl_sync(0xffffffffu, sum, 31);
+      if (hi0 >= all && sum0 >= all) break;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + sum > lo);
-    if (hit) {
-      const int at = __ffs(hit) - 1;
-      b = b0 + at;
-      before += __shfl_sync(0xffffffffu, sum - mine, at);
-      s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, sum, 31);
   }
 
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::SLOT;
@@ -361,7 +389,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   while (true) {
     const bool more = lo < hi;
     constexpr int kPer = 16 / C::ES;  // values of a piece
-    uint32_t raw[NT][C::KP][kPer / 2];
+    constexpr int NQ = C::QS ? 1 : NT;  // tiles of queries a warp brings: its own, or all
+    uint32_t raw[NQ][C::KP][kPer / 2];
     if (more) {
       // ---- the next group: its first keys and its queries are on their way before the last one is joined
       while (lo >= before + s.total) {
@@ -391,10 +420,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       place = look(0);
       if (eights) later = look(16);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NQ; ++t) {
         // queries: row quad (+ 8) of the tile, values of this thread's pieces
-        const int r = r0 + 8 * t + quad, tok = p.by_group.div(r), head = kvh * p.G + r - tok * p.G;
-        const bool there = 8 * t + quad < n_rows;
+        const int r_tile = 8 * (C::QS ? warp : t) + quad;
+        const bool there = r_tile < n_rows;
+        const int r = r0 + r_tile, tok = p.by_group.div(r), head = kvh * p.G + r - tok * p.G;
         const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.qs.b + tok * p.qs.l + head * p.qs.h;
 #pragma unroll
         for (int i = 0; i < C::KP; ++i) {
@@ -468,10 +498,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     if (!more) break;
 
     // ---- queries as operands: f16 with the row's largest value in [1, 2) where they are bf16 and codes f16
-    uint32_t qf[NT][C::KP * C::KS][2];
+    uint32_t qf[C::QS ? 1 : NT][C::KP * C::KS][2];
     float up[NT][2];  // by row of the scores: what its power of two took
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NQ; ++t) {
+      if (C::QS && warp >= NT) continue;
       float e = 1.0f;
       if (C::kScaled && p.bf16) {
         uint32_t big = 0;
@@ -492,15 +523,27 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
             raw[t][i][x] = pack2<false>(__uint_as_float(raw[t][i][x] << 16) * down,
                                         __uint_as_float(raw[t][i][x] & 0xffff0000u) * down);
       }
-#pragma unroll
-      for (int i = 0; i < C::KP; ++i)
-#pragma unroll
-        for (int x = 0; x < C::KS; ++x)
-          qf[t][i * C::KS + x][0] = raw[t][i][2 * x], qf[t][i * C::KS + x][1] = raw[t][i][2 * x + 1];
-      // (row quad's factor to the threads that hold its scores; the cap takes raw products)
+      // (the cap takes raw products)
       if (!(p.softcap > 0)) e *= p.scale * kLog2e;
-      up[t][0] = __shfl_sync(0xffffffffu, e, (2 * four) * 4);
-      up[t][1] = __shfl_sync(0xffffffffu, e, (2 * four + 1) * 4);
+      if constexpr (C::QS) {
+#pragma unroll
+        for (int i = 0; i < C::KP * C::KS / 2; ++i) {
+          const uint32_t* y = &raw[t][0][0] + 4 * i;
+          sq[(warp * (C::KP * C::KS / 2) + i) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        if (four == 0) sq_up[8 * warp + quad] = e;
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::KP * C::KS; ++i) qf[t][i][0] = (&raw[t][0][0])[2 * i], qf[t][i][1] = (&raw[t][0][0])[2 * i + 1];
+        // (row quad's factor to the threads that hold its scores)
+        up[t][0] = __shfl_sync(0xffffffffu, e, (2 * four) * 4);
+        up[t][1] = __shfl_sync(0xffffffffu, e, (2 * four + 1) * 4);
+      }
+    }
+    if constexpr (C::QS) __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (C::QS) up[t][0] = sq_up[8 * t + 2 * four], up[t][1] = sq_up[8 * t + 2 * four + 1];
 #pragma unroll
       for (int i = 0; i < DH / 16; ++i)
 #pragma unroll
@@ -530,6 +573,19 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         const uint4 k0 = *reinterpret_cast<const uint4*>(mine + placed<C::RB>(quad, four + 4 * i));
         const uint4 k1 = *reinterpret_cast<const uint4*>(mine + 8 * C::RB + placed<C::RB>(quad, four + 4 * i));
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        uint32_t qs[NT][2 * C::KS];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int x = 0; x < C::KS / 2; ++x) {
+            if constexpr (C::QS) {
+              const uint4 y = sq[(t * (C::KP * C::KS / 2) + i * (C::KS / 2) + x) * 32 + lane];
+              qs[t][4 * x] = y.x, qs[t][4 * x + 1] = y.y, qs[t][4 * x + 2] = y.z, qs[t][4 * x + 3] = y.w;
+            } else {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) qs[t][4 * x + h] = qf[t][i * C::KS + 2 * x + h / 2][h % 2];
+            }
+          }
 #pragma unroll
         for (int x = 0; x < C::KS; ++x) {
           uint32_t a[4];
@@ -540,7 +596,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
             a[0] = w0[2 * x], a[1] = w1[2 * x], a[2] = w0[2 * x + 1], a[3] = w1[2 * x + 1];
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma<FMT>(sc[t], a, qf[t][i * C::KS + x][0], qf[t][i * C::KS + x][1]);
+          for (int t = 0; t < NT; ++t) mma<FMT>(sc[t], a, qs[t][2 * x], qs[t][2 * x + 1]);
         }
       }
       float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
@@ -711,7 +767,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     int c0[2], n[2], at[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (s_share[i].used) c0[i] = cut.of(s_share[i].first), n[i] = cut.of(s_share[i].last) - c0[i] + 1;
+      if (s_share[i].used) {
+        const int near = cut.near(static_cast<int>(s_share[i].last - s_share[i].first + 1));
+        c0[i] = cut.of(s_share[i].first + max(near - 1, 0));
+        n[i] = cut.of(s_share[i].last - max(near - 1, 0)) - c0[i] + 1;
+      }
     __threadfence();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
