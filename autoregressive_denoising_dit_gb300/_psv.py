@@ -63,7 +63,6 @@ PSV_PAGE_BF16 = 1
 PSV_PAGE_F16 = 2
 PSV_PAGE_E4M3 = 3
 PSV_PAGE_I8 = 4
-PSV_PAGE_SCRATCH_HEAD = 8192
 
 
 class ModelDesc(ctypes.Structure):

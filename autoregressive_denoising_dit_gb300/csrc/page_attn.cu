@@ -21,8 +21,9 @@
 //
 // The work (16-key steps of every sequence, kv head and tile of query rows) is
 // one line that is cut into equal stretches, one a CTA, whatever the lengths.
-// Where a cut falls into a group its shares go to the workspace and the last CTA
-// to be done joins them in order.
+// Where a cut falls into a group its shares go to the workspace, and a second kernel
+// joins them in order.  (The last of a group's CTAs to be done took 5 to 12 us to
+// notice that and to join them; all SMs take 3, launch included.)
 #include <algorithm>
 #include <cfloat>
 
@@ -31,6 +32,12 @@
 #include "psv_kernels.h"
 
 namespace psv {
+
+// A group that CTA `i` of the grid begins and does not end: its rows (0: there is none)
+// and how many CTAs have shares of it.
+struct alignas(32) Shared {
+  int rows, shares, b, kvh, r0;
+};
 
 namespace {
 
@@ -65,7 +72,6 @@ struct ACfg {
   static constexpr int RING = WARPS * STAGES * SLOT;
   static constexpr int SMEM = RING + JOIN + Q_BYTES;
   static_assert(2 * (SMEM + 1024 + 256) <= 233472, "two CTAs an SM");
-  static_assert((2 * ROWS * (kMaxCtas + 4) + THREADS * 4) * 4 <= RING, "the join of CTAs, in the ring's place");
 };
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -184,31 +190,40 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a / b;
 }
 
-// The line of `all` steps in `ctas` stretches, the first ones a step longer.
+// The line of `all` steps in `ctas` equal stretches.
 struct Cut {
+  int64_t all, each;
   int ctas, more;
-  int64_t each;
-  __device__ __forceinline__ Cut(int64_t all, int n) : ctas(n), more(0), each(0) {
-    if (n) each = divide(all, n), more = static_cast<int>(all - each * n);
+  __device__ __forceinline__ Cut(int64_t a, int n) : all(a), each(0), ctas(n), more(0) {
+    if (n) each = divide(a, n), more = static_cast<int>(a - each * n);
   }
-  __device__ __forceinline__ int64_t begin(int cta) const { return each * cta + min(cta, more); }
+  __device__ __forceinline__ int64_t begin(int cta) const { return each * cta + more * cta / ctas; }
   // A cut this near to an end of its group is moved there, so that fewer CTAs have
   // shares of two groups.
   __device__ __forceinline__ int near(int steps) const {
     return static_cast<int>(min(each >> 3, static_cast<int64_t>(steps >> 2)));
   }
-  __device__ __forceinline__ int of(int64_t x) const {
-    const int64_t longer = (each + 1) * more;
-    return static_cast<int>(x < longer ? divide(x, each + 1) : more + divide(x - longer, each));
-  }
+  __device__ __forceinline__ int of(int64_t x) const { return static_cast<int>(divide((x + 1) * ctas - 1, all)); }
 };
 
-// A group of which a CTA has a share: its first and last step on the line, and its rows;
-// in the end its first CTA and, as `used`, how many shares there are to be joined.
-struct Share {
-  int64_t first, last;
-  int b, kvh, r0, rows, used;
-};
+constexpr size_t kSharedBytes = kMaxCtas * sizeof(Shared);
+
+// Floats of a share: O, then m', m, l of each row.
+constexpr int share_floats(int dh, int rows) { return rows * (dh + 4); }
+
+// A row's finished value (four of it) and lse.
+__device__ __forceinline__ void write_out(const PageAttnParams& p, int b, int kvh, int row, int d, float mm_o, float mm_l,
+                                          float ll, float4 acc) {
+  const int tok = p.by_group.div(row), head = kvh * p.G + row - tok * p.G;
+  const float f = ll > 0.0f ? fast_exp2(mm_o - mm_l) / ll : ll;  // (0 or NaN)
+  if (d < p.dh) {
+    const uint2 y = p.bf16 ? make_uint2(pack2<true>(acc.x * f, acc.y * f), pack2<true>(acc.z * f, acc.w * f))
+                           : make_uint2(pack2<false>(acc.x * f, acc.y * f), pack2<false>(acc.z * f, acc.w * f));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + b * p.os.b + tok * p.os.l + head * p.os.h + d) = y;
+  }
+  if (d == 0 && p.lse)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Lq + tok] = ll == 0.0f ? -INFINITY : (mm_l + fast_log2(ll)) * kLn2;
+}
 
 template <int DH, int FMT, int NT>
 __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
@@ -216,17 +231,14 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   using C = ACfg<DH, FMT, NT>;
   constexpr int ROWS = C::ROWS, kWarps = C::WARPS, kThreads = C::THREADS, kStages = C::STAGES;
   constexpr bool kBf16Operands = FMT == PSV_PAGE_BF16;
-  constexpr int kPart = ROWS * (DH + 4);  // floats of a share: O, then m', m, l of each row
+  constexpr int kPart = share_floats(DH, ROWS);
   extern __shared__ __align__(128) uint8_t smem[];
   float* so = reinterpret_cast<float*>(smem + C::RING);  // [kWarps][ROWS][JSTRIDE]
   float* sm = so + kWarps * ROWS * C::JSTRIDE;           // [kWarps][ROWS][4]: m', m, l
   uint4* sq = reinterpret_cast<uint4*>(smem + C::RING + C::JOIN);  // QS: [NT][KP * KS / 2][lane]
   float* sq_up = reinterpret_cast<float*>(sq + NT * C::KP * C::KS * 16);  // [ROWS]
-  __shared__ Share s_share[2];  // of a group that began before this CTA, of one that it begins
-  static_assert(kMaxCtas * sizeof(int) <= PSV_PAGE_SCRATCH_HEAD, "counters in the workspace's head");
   const PageCacheDev& c = p.c;
   const int warp = warp_id(), lane = lane_id(), quad = lane / 4, four = lane % 4;
-  if (threadIdx.x < 2) s_share[threadIdx.x].used = 0;
   if (p.dh < DH) {  // pieces behind the head stay zeros
     for (int i = threadIdx.x; i < C::RING / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   }
@@ -245,6 +257,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 #pragma unroll
   for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   const Cut cut(all, static_cast<int>(min(static_cast<int64_t>(gridDim.x), (all + kWarps - 1) / kWarps)));
+  if (threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
   if (static_cast<int>(blockIdx.x) >= cut.ctas) return;
   int64_t lo = 0, hi = 0;
   int b = 0;
@@ -370,19 +383,6 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     if constexpr (C::kScaled)
       copy4(dst + 2 * C::KV + lane * 4, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);
   };
-  // A row's finished value and lse.
-  auto write_out = [&](int wb, int wkvh, int row, int d, float mm_o, float mm_l, float ll, float4 acc) {
-    const int tok = p.by_group.div(row), head = wkvh * p.G + row - tok * p.G;
-    const float f = ll > 0.0f ? fast_exp2(mm_o - mm_l) / ll : ll;  // (0 or NaN)
-    if (d < p.dh) {
-      const uint2 y = p.bf16 ? make_uint2(pack2<true>(acc.x * f, acc.y * f), pack2<true>(acc.z * f, acc.w * f))
-                             : make_uint2(pack2<false>(acc.x * f, acc.y * f), pack2<false>(acc.z * f, acc.w * f));
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + wb * p.os.b + tok * p.os.l + head * p.os.h + d) = y;
-    }
-    if (d == 0 && p.lse)
-      p.lse[(static_cast<int64_t>(wb) * p.Hq + head) * p.Lq + tok] = ll == 0.0f ? -INFINITY : (mm_l + fast_log2(ll)) * kLn2;
-  };
-
   float o[NT][DH / 16][4], mo[NT][2], ml[NT][2], l[NT][2];
   bool joining = false, split = false;  // the group before, whose sums are still the warps'
   int was_b = 0, was_kvh = 0, was_r0 = 0, was_rows = 0, was_slot = 0;
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           *reinterpret_cast<float4*>(part + r * DH + d) = acc;
           if (d == 0) *reinterpret_cast<float4*>(part + ROWS * DH + r * 4) = make_float4(mm_o, mm_l, ll, 0.0f);
         } else {
-          write_out(was_b, was_kvh, was_r0 + r, d, mm_o, mm_l, ll, acc);
+          write_out(p, was_b, was_kvh, was_r0 + r, d, mm_o, mm_l, ll, acc);
         }
       }
       __syncthreads();
@@ -755,66 +755,50 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     split = step0 > 0 || step1 < s.steps;
     was_b = b, was_kvh = kvh, was_r0 = r0, was_rows = n_rows;
     was_slot = step0 == 0;
-    if (split && threadIdx.x == 0) {
-      const int64_t first = lo - step0;
-      s_share[was_slot] = Share{first, first + s.steps - 1, b, kvh, r0, n_rows, 1};
+    if (split && was_slot && threadIdx.x == 0) {
+      const int near = max(cut.near(s.steps) - 1, 0);
+      const int shares = cut.of(lo + s.steps - 1 - near) - static_cast<int>(blockIdx.x) + 1;
+      p.shared[blockIdx.x] = Shared{n_rows, shares, b, kvh, r0};
     }
     lo += step1 - step0;
   }
+}
 
-  // ---- groups that are shared: the last CTA to be done joins all shares, in order
-  if (threadIdx.x == 0 && (s_share[0].used | s_share[1].used)) {
-    int c0[2], n[2], at[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (s_share[i].used) {
-        const int near = cut.near(static_cast<int>(s_share[i].last - s_share[i].first + 1));
-        c0[i] = cut.of(s_share[i].first + max(near - 1, 0));
-        n[i] = cut.of(s_share[i].last - max(near - 1, 0)) - c0[i] + 1;
-      }
-    __threadfence();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (s_share[i].used) at[i] = atomicAdd(p.arrived + c0[i], 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (!s_share[i].used) continue;
-      const bool last = at[i] == n[i] - 1;
-      if (last) p.arrived[c0[i]] = 0;
-      s_share[i].first = c0[i], s_share[i].used = last ? n[i] : 0;
-    }
-    __threadfence();
-  }
-  __syncthreads();
-  // The rows of both groups at once: a warp a row's statistics, then the values, as many
-  // threads a column as there are and 16 reads a thread at a time, the first ones before
-  // the statistics are known (a round trip to L2 takes 0.6 us and more).
-  const int rows0 = s_share[0].used ? s_share[0].rows : 0, rows1 = s_share[1].used ? s_share[1].rows : 0;
-  const int rows = rows0 + rows1;
-  if (rows == 0) return;
-  float* factor = reinterpret_cast<float*>(smem);  // [rows][kMaxCtas]
-  float* stat = factor + 2 * ROWS * kMaxCtas;      // [rows][4]
-  float4* sums = reinterpret_cast<float4*>(stat + 2 * ROWS * 4);
-  auto share = [&](int i, int k) { return p.part + (2 * (s_share[i].first + k) + (k == 0)) * kPart; };
-  constexpr int kReads = 16;
-  const int columns = rows * (DH / 4), parts = max(kThreads / columns, 1);
-  // reads [k0, k0 + kReads) of column and part x
-  auto read = [&](int x, int k0, float4 (&z)[kReads]) {
-    const int column = x % columns, r = column / (DH / 4), i = r >= rows0, n = s_share[i].used;
-    const int at = (i ? r - rows0 : r) * DH + column % (DH / 4) * 4;
+constexpr int kJoinThreads = 512;
+
+// Joins the shares of the group that CTA blockIdx.x of the attention began: a row's
+// statistics by a warp, its values by as many threads a column as there are, whose first
+// reads are on their way before the statistics are known.
+template <int DH>
+__global__ void __launch_bounds__(kJoinThreads) page_join_kernel(const __grid_constant__ PageAttnParams p, int row_tile) {
+  constexpr int kReads = 8;
+  __shared__ float factor[16 * kMaxCtas];  // [rows][shares]
+  __shared__ float4 stat[16], sums[kJoinThreads];
+  const int warp = warp_id(), lane = lane_id();
+  pdl_trigger();
+  pdl_wait();
+  const Shared g = p.shared[blockIdx.x];
+  if (g.rows == 0) return;
+  const int64_t floats = share_floats(DH, row_tile);
+  const float* part = p.part + 2 * static_cast<int64_t>(blockIdx.x) * floats;
+  // (a share that begins its group is its CTA's second, one that goes on with it its first)
+  auto share = [&](int k) { return part + (2 * k + (k == 0)) * floats; };
+  const int columns = g.rows * (DH / 4), parts = kJoinThreads / columns, x = threadIdx.x;
+  const int column = x % columns, r_mine = column / (DH / 4), d = column % (DH / 4) * 4;
+  float4 z[kReads];
+  auto read = [&](int k0) {
 #pragma unroll
     for (int e = 0; e < kReads; ++e) {
       const int k = x / columns + (k0 + e) * parts;
-      z[e] = k < n ? __ldcg(reinterpret_cast<const float4*>(share(i, k) + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      z[e] = k < g.shares ? __ldcg(reinterpret_cast<const float4*>(share(k) + r_mine * DH + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
-  float4 z[kReads];
-  if (static_cast<int>(threadIdx.x) < columns * parts) read(threadIdx.x, 0, z);
-  for (int r = warp; r < rows; r += kWarps) {
-    const int i = r >= rows0, n = s_share[i].used, at = ROWS * DH + (i ? r - rows0 : r) * 4;
+  const bool busy = x < columns * parts;
+  if (busy) read(0);
+  for (int r = warp; r < g.rows; r += kJoinThreads / 32) {
     float mm_o = kNone, mm_l = kNone, ll = 0.0f;
-    for (int k = lane; k < n; k += 32) {
-      const float4 st = __ldcg(reinterpret_cast<const float4*>(share(i, k) + at));
+    for (int k = lane; k < g.shares; k += 32) {
+      const float4 st = __ldcg(reinterpret_cast<const float4*>(share(k) + row_tile * DH + r * 4));
       factor[r * kMaxCtas + k] = st.x;
       mm_o = fmaxf(mm_o, st.x);
       const float m = fmaxf(mm_l, st.y);
@@ -829,46 +813,33 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       ll = __fadd_rn(__fmul_rn(ll, fast_exp2(mm_l - m)), __fmul_rn(l1, fast_exp2(m1 - m)));  // (the same in both lanes)
       mm_l = m;
     }
-    for (int k = lane; k < n; k += 32) factor[r * kMaxCtas + k] = fast_exp2(factor[r * kMaxCtas + k] - mm_o);
-    if (lane == 0) stat[r * 4] = mm_o, stat[r * 4 + 1] = mm_l, stat[r * 4 + 2] = ll;
+    for (int k = lane; k < g.shares; k += 32) factor[r * kMaxCtas + k] = fast_exp2(factor[r * kMaxCtas + k] - mm_o);
+    if (lane == 0) stat[r] = make_float4(mm_o, mm_l, ll, 0.0f);
   }
   __syncthreads();
-  auto finish = [&](int column, float4 acc) {
-    const int r = column / (DH / 4), i = r >= rows0;
-    write_out(s_share[i].b, s_share[i].kvh, s_share[i].r0 + (i ? r - rows0 : r), column % (DH / 4) * 4, stat[r * 4],
-              stat[r * 4 + 1], stat[r * 4 + 2], acc);
-  };
-#pragma unroll 1
-  for (int x = threadIdx.x; x < columns * parts; x += kThreads) {
-    const int column = x % columns, r = column / (DH / 4), n = s_share[r >= rows0].used;
-    if (x >= kThreads) read(x, 0, z);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (busy) {
     for (int k0 = 0;;) {
 #pragma unroll
       for (int e = 0; e < kReads; ++e) {
         const int k = x / columns + (k0 + e) * parts;
-        const float f = k < n ? factor[r * kMaxCtas + k] : 0.0f;
+        const float f = k < g.shares ? factor[r_mine * kMaxCtas + k] : 0.0f;
         acc.x = fmaf(f, z[e].x, acc.x), acc.y = fmaf(f, z[e].y, acc.y);
         acc.z = fmaf(f, z[e].z, acc.z), acc.w = fmaf(f, z[e].w, acc.w);
       }
       k0 += kReads;
-      if (k0 * parts >= n) break;
-      read(x, k0, z);
+      if (k0 * parts >= g.shares) break;
+      read(k0);
     }
-    if (parts > 1) sums[x] = acc;
-    else finish(column, acc);
+    sums[x] = acc;
   }
-  if (parts > 1) {
-    __syncthreads();
-    if (static_cast<int>(threadIdx.x) < columns) {
-      float4 acc = sums[threadIdx.x];
-      for (int k = 1; k < parts; ++k) {
-        const float4 y = sums[threadIdx.x + k * columns];
-        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
-      }
-      finish(threadIdx.x, acc);
+  __syncthreads();
+  if (x < columns) {
+    for (int k = 1; k < parts; ++k) {
+      const float4 y = sums[x + k * columns];
+      acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
     }
+    write_out(p, g.b, g.kvh, g.r0 + r_mine, d, stat[r_mine].x, stat[r_mine].y, stat[r_mine].z, acc);
   }
 }
 
@@ -890,7 +861,11 @@ cudaError_t launch(const PageAttnParams& p, int sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, page_attn_kernel<DH, FMT, NT>, p);
+  e = cudaLaunchKernelEx(&cfg, page_attn_kernel<DH, FMT, NT>, p);
+  if (e != cudaSuccess) return e;
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, page_join_kernel<DH>, p, C::ROWS);
 }
 
 template <int DH, int FMT>
@@ -912,8 +887,13 @@ cudaError_t launch_format(const PageAttnParams& p, int sms, cudaStream_t st) {
 
 // At most two shares a CTA.
 size_t page_attn_scratch(const PageAttnParams& p) {
-  return PSV_PAGE_SCRATCH_HEAD +
-         static_cast<size_t>(kMaxCtas) * 2 * (p.Lq * p.G <= 8 ? 8 : 16) * ((p.dh <= 64 ? 64 : 128) + 4) * sizeof(float);
+  const int dh = p.dh <= 64 ? 64 : 128, rows = p.Lq * p.G <= 8 ? 8 : 16;
+  return kSharedBytes + static_cast<size_t>(kMaxCtas) * 2 * share_floats(dh, rows) * sizeof(float);
+}
+
+void page_attn_scratch(PageAttnParams& p, void* scratch) {
+  p.shared = static_cast<Shared*>(scratch);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kSharedBytes);
 }
 
 cudaError_t launch_page_attention(const PageAttnParams& p, int sms, cudaStream_t st) {

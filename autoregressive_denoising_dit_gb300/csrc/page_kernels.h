@@ -49,6 +49,8 @@ __device__ __forceinline__ PageRow page_row(const PageCacheDev& c, int b, int64_
   return PageRow{page < c.n_pages ? page : -1, static_cast<int>(static_cast<uint32_t>(pos) - at * c.by_page.d)};
 }
 
+struct Shared;
+
 // The attention's arguments.
 struct PageAttnParams {
   PageCacheDev c;
@@ -63,8 +65,8 @@ struct PageAttnParams {
   void* o;
   float* lse;  // or null
   const int32_t *q_lens, *k_lens;
-  int* arrived;  // counters of the groups that several CTAs share, zero between calls
-  float* part;   // their shares
+  Shared* shared;  // page_attn.cu: the groups that several CTAs share
+  float* part;            // their shares
 };
 
 __device__ __forceinline__ int page_rows(const PageAttnParams& p, int b) {
@@ -79,9 +81,10 @@ __device__ __forceinline__ int page_length(const PageAttnParams& p, int b, int r
 
 cudaError_t launch_page_attention_general(const PageAttnParams& p, cudaStream_t st);
 
-// For rows and pages of 16-byte pieces and heads of up to 128: the workspace
-// (head included; Lq, G and dh count) and the launch on `sms` SMs.
+// For rows and pages of 16-byte pieces and heads of up to 128: the workspace's size
+// (Lq, G and dh count), its use, and the launch on `sms` SMs.
 size_t page_attn_scratch(const PageAttnParams& p);
+void page_attn_scratch(PageAttnParams& p, void* scratch);
 cudaError_t launch_page_attention(const PageAttnParams& p, int sms, cudaStream_t st);
 
 }  // namespace psv

@@ -427,7 +427,7 @@ int check_page_query(const psv_page_cache* c, const psv_page_query* q) {
   if (q->Hq < 1 || q->Hq % c->Hkv) return cache_fail(PSV_EINVAL, "Hq (%d) must be a multiple of Hkv (%d)", q->Hq, c->Hkv);
   if (q->Lq < 0 || q->Lq > (1 << 20)) return cache_fail(PSV_EINVAL, "Lq %d: 0 to 2^20", q->Lq);
   if (static_cast<int64_t>(c->B) * q->Hq > (1 << 24)) return cache_fail(PSV_EINVAL, "over 2^24 sequences x heads");
-  if (static_cast<int64_t>(q->Lq) * q->Hq > (1 << 30)) return cache_fail(PSV_EINVAL, "Lq x Hq over 2^30");
+  if (static_cast<double>(c->B) * q->Lq * q->Hq > 0x1p30) return cache_fail(PSV_EINVAL, "B x Lq x Hq over 2^30");
   if (q->window < 0 || q->sinks < 0) return cache_fail(PSV_EINVAL, "window and sinks must not be negative");
   if (q->sinks && !q->window) return cache_fail(PSV_EINVAL, "sinks need a window");
   if (!(std::isfinite(q->scale) && q->scale >= 0)) return cache_fail(PSV_EINVAL, "scale must be finite and not negative");
@@ -456,7 +456,7 @@ PageAttnParams page_attn_params(const psv_page_cache* c, const psv_page_query* q
 bool page_attn_pieces(const psv_page_cache* c) { return c->dh <= 128 && c->dh * page_esize(c->format) % 16 == 0; }
 
 size_t page_scratch(const psv_page_cache* c, const PageAttnParams& p) {
-  return page_attn_pieces(c) ? page_attn_scratch(p) : PSV_PAGE_SCRATCH_HEAD;
+  return page_attn_pieces(c) ? page_attn_scratch(p) : 256;
 }
 
 }  // namespace
@@ -517,8 +517,7 @@ PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q,
     p.kb = static_cast<uint32_t>(c->k_stride[0] * es), p.kl = static_cast<uint32_t>(c->k_stride[1] * es);
     p.vb = static_cast<uint32_t>(c->v_stride[0] * es), p.vl = static_cast<uint32_t>(c->v_stride[1] * es);
     p.sb = static_cast<uint32_t>(c->scale_stride[0] * 4), p.sl = static_cast<uint32_t>(c->scale_stride[1] * 4);
-    p.arrived = static_cast<int*>(scratch);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + PSV_PAGE_SCRATCH_HEAD);
+    page_attn_scratch(p, scratch);
     return cuda_status(launch_page_attention(p, sms, st), "page attention launch");
   }
   return cuda_status(launch_page_attention_general(p, st), "page attention launch");

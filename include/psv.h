@@ -623,7 +623,7 @@ int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void
  * lengths; those of a sequence may differ in their roundings where the lengths
  * of others change, as the work is shared out among the SMs by all of them.
  * Requirements: dtype BF16 or F16 (16-bit pages: their own); Hq a multiple of Hkv;
- * B x Hq <= 2^24; 0 <= Lq <= 2^20, Lq x Hq <= 2^30; window, sinks >= 0, sinks need a window; scale,
+ * B x Hq <= 2^24; 0 <= Lq <= 2^20, B x Lq x Hq <= 2^30; window, sinks >= 0, sinks need a window; scale,
  * softcap >= 0 finite; o's rows distinct. */
 typedef struct psv_page_query {
   int32_t dtype, Lq, Hq, causal, window, sinks, append;
@@ -634,11 +634,9 @@ typedef struct psv_page_query {
   const int32_t* k_lens;            /* [B], clamped to [0, max_pages x page_size]; NULL: that (append: 0) */
 } psv_page_query;
 
-/* Workspace of psv_page_attention: 256-byte aligned device memory whose first
- * PSV_PAGE_SCRATCH_HEAD bytes the caller zeroes once, before its first use.  It may
- * serve any number of calls (captured ones too, of any problem that it is large
- * enough for) that do not overlap on the GPU. */
-#define PSV_PAGE_SCRATCH_HEAD 8192
+/* Workspace of psv_page_attention: 256-byte aligned device memory of any content.  It
+ * may serve any number of calls (captured ones too, of any problem that it is large
+ * enough for) that do not overlap on the GPU.  5 MB at most. */
 int psv_page_scratch_bytes(const psv_page_cache* c, const psv_page_query* q, size_t* bytes);
 
 int psv_page_attention(const psv_page_cache* c, const psv_page_query* q, const void* x /* q */, void* o,
