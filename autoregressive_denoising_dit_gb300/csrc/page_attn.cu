@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
 
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -303,7 +303,16 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     }
   }
 
-  const uint32_t ring = smem_u32(smem) + warp * kStages * C::SLOT;
+  // Places within a step (128-byte aligned, so that a change of bits 4 to 6 changes places
+  // of pieces): what this lane copies of rows [0, RPC), its pieces of key lane / 4 and of
+  // value 2 (lane % 4).  Row i RPC + r is copied to (copied ^ flip(i)) + i 512, piece
+  // four + 4 i of the key is at (key_at ^ 64 (i % 2)) + 128 (i / 2), the next row's value at
+  // (value_at ^ 64) + RB (rows of 64 bytes: two to 128, value_at ^ 64).
+  const uint32_t ring = smem_u32(smem), ring0 = warp * kStages * C::SLOT;
+  const uint32_t copied = placed<C::RB>(lane / C::LPR, lane % C::LPR);
+  const uint32_t key_at = placed<C::RB>(quad, four);
+  const uint32_t value_at = C::RB == 64 ? placed<C::RB>(2 * four, quad / 2) + quad % 2 * 8 : placed<C::RB>(2 * four, quad);
+  auto flip = [](int i) -> uint32_t { return C::RB == 256 ? (i / 2 * 4 + i % 2 * 2) * 16 : i * 64; };
   const bool in_head = lane % C::LPR * 16 < p.dh * C::ES;  // the piece that this lane copies
   const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
   const int sinks = p.window ? p.sinks : 0;
@@ -329,7 +338,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     const int step = step0 + warp + issued * kWarps, number = issued++;
     found <<= 1;
     if (step >= step1) return;
-    const uint32_t dst = ring + into * C::SLOT;
+    const uint32_t dst = ring0 + into * C::SLOT;
     const int key0 = key_of(step);
     // Keys that some row of the tile sees are read.
     const bool every = key0 + kStep <= any_end && (key0 >= any_first || key0 + kStep <= sinks);
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         if (in_head) {
 #pragma unroll
           for (int i = 0; i < 8 / C::RPC; ++i) {
-            const uint32_t to = dst + placed<C::RB>(8 * h + i * C::RPC + lane / C::LPR, lane % C::LPR);
+            const uint32_t to = ring + ((dst + copied) ^ flip(i)) + (h * 8 / C::RPC + i) * 512;
             copy16(to, k + static_cast<uint64_t>(p.kl) * (i * C::RPC));
             copy16(to + C::KV, v + static_cast<uint64_t>(p.vl) * (i * C::RPC));
           }
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       }
       if constexpr (C::kScaled) {
         const bool h = lane & 8;
-        copy4(dst + 2 * C::KV + lane * 4,
+        copy4(ring + dst + 2 * C::KV + lane * 4,
               s_mine + offset(p.sb, p.sl, h ? half[1].page : half[0].page, (h ? half[1].row : half[0].row) + lane % 8), 4);
       }
       return;
@@ -375,13 +384,13 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     for (int i = 0; i < kStep / C::RPC; ++i) {
       const int key = i * C::RPC + lane / C::LPR;
       const int page = __shfl_sync(0xffffffffu, at.page, key), row = __shfl_sync(0xffffffffu, at.row, key) - lane / C::LPR;
-      const uint32_t to = dst + placed<C::RB>(key, lane % C::LPR);
+      const uint32_t to = ring + dst + placed<C::RB>(key, lane % C::LPR);
       const int bytes = page >= 0 && in_head ? 16 : 0;
       copy16(to, bytes ? k_mine + offset(p.kb, 0, page, 0) + static_cast<int64_t>(p.kl) * row : static_cast<const char*>(c.k), bytes);
       copy16(to + C::KV, bytes ? v_mine + offset(p.vb, 0, page, 0) + static_cast<int64_t>(p.vl) * row : static_cast<const char*>(c.v), bytes);
     }
     if constexpr (C::kScaled)
-      copy4(dst + 2 * C::KV + lane * 4, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);
+      copy4(ring + dst + 2 * C::KV + lane * 4, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);
   };
   float o[NT][DH / 16][4], mo[NT][2], ml[NT][2], l[NT][2];
   bool joining = false, split = false;  // the group before, whose sums are still the warps'
@@ -558,7 +567,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       copies_commit();
       copies_wait<kStages - 1>();
       __syncwarp();
-      const uint8_t* mine = smem + (warp * kStages + slot) * C::SLOT;
+      const uint32_t mine = ring0 + slot * C::SLOT;
       slot = slot == kStages - 1 ? 0 : slot + 1;
       const unsigned there = __ballot_sync(0xffffffffu, found >> (kStages - 1) & 1);
       if (!there) continue;
@@ -570,8 +579,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         for (int e = 0; e < 4; ++e) sc[t][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < C::KP; ++i) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(mine + placed<C::RB>(quad, four + 4 * i));
-        const uint4 k1 = *reinterpret_cast<const uint4*>(mine + 8 * C::RB + placed<C::RB>(quad, four + 4 * i));
+        const uint8_t* key = smem + ((mine + key_at) ^ (i % 2 * 64)) + i / 2 * 128;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(key), k1 = *reinterpret_cast<const uint4*>(key + 8 * C::RB);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
         uint32_t qs[NT][2 * C::KS];
 #pragma unroll
@@ -601,7 +610,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       }
       float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
       if constexpr (C::kScaled) {
-        const float* scales = reinterpret_cast<const float*>(mine + 2 * C::KV);
+        const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV);
         ks[0] = scales[quad], ks[1] = scales[quad + 8];
         lv[0] = fast_log2(scales[16 + quad]), lv[1] = fast_log2(scales[24 + quad]);
       }
@@ -686,15 +695,14 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       uint32_t v[4][C::VW];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const uint8_t* from = mine + C::KV + (x >> 1) * 8 * C::RB;
-        const int row = 2 * four + (x & 1);
+        const uint8_t* from = smem + ((mine + value_at) ^ (x % 2 * 64)) + (C::RB == 64 ? 0 : x % 2 * C::RB) + C::KV + x / 2 * 8 * C::RB;
         if constexpr (C::VW == 2) {
-          const uint2 z = *reinterpret_cast<const uint2*>(from + placed<C::RB>(row, quad / 2) + quad % 2 * 8);
+          const uint2 z = *reinterpret_cast<const uint2*>(from);
           v[x][0] = z.x, v[x][1] = z.y;
         } else {
 #pragma unroll
           for (int i = 0; i < C::VW / 4; ++i) {
-            const uint4 z = *reinterpret_cast<const uint4*>(from + placed<C::RB>(row, quad + 8 * i));
+            const uint4 z = *reinterpret_cast<const uint4*>(from + i * 128);
             v[x][4 * i] = z.x, v[x][4 * i + 1] = z.y, v[x][4 * i + 2] = z.z, v[x][4 * i + 3] = z.w;
           }
         }
