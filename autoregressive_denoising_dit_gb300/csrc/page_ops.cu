@@ -22,8 +22,9 @@ int page_esize(int format) { return scaled(format) ? 1 : 2; }
 // Rows of sequence b: number i of [0, L) at position starts[b] + i.
 struct PageRowsParams {
   PageCacheDev c;
-  int L, H, dh, lanes;  // lanes of a row (log2): 8 values each
-  FastDiv by_head;
+  int L, H, dh, lanes;  // lanes of a head's row (log2, at least 2): 8 values each
+  int heads;            // of a thread, at most kHeads
+  FastDiv by_groups;    // groups of heads a token
   Strides3 xs[2];
   void* x[2];  // k, v
   const int32_t *starts, *lens;
@@ -38,29 +39,47 @@ struct PageFormat {
   static constexpr int kSize = kScaled ? 1 : 2;
 };
 
-// Two values as they are stored, from the lower half on.
+// Four values as they are stored in 8 bits, two in 16, from the lowest bits on.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(const float* f) {
+  if constexpr (FMT == PSV_PAGE_E4M3) {
+    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3)) |
+           static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3)) << 16;
+  } else {
+    // |f| < 2^22: the lowest byte of f + 1.5 2^23 is the nearest whole number, ties to even
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(__fadd_rn(f[i], 12582912.0f));
+    return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+  }
+}
 template <int FMT>
 __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
   if constexpr (FMT == PSV_PAGE_BF16) return pack_bf16x2(lo, hi);
-  if constexpr (FMT == PSV_PAGE_F16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t u, float* f) {
+  if constexpr (FMT == PSV_PAGE_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> 16 * i), __NV_E4M3);
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      f[2 * i] = y.x, f[2 * i + 1] = y.y;
+    }
+  } else {
+    // 2^23 + (code + 128) is the f32 whose lowest byte is code + 128
+    u ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)) - 8388736.0f;
   }
-  if constexpr (FMT == PSV_PAGE_E4M3) return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-  if constexpr (FMT == PSV_PAGE_I8)
-    return (static_cast<uint32_t>(__float2int_rn(lo)) & 0xff) | (static_cast<uint32_t>(__float2int_rn(hi)) & 0xff) << 8;
 }
 template <int FMT>
 __device__ __forceinline__ float2 decode2(uint32_t u) {
   if constexpr (FMT == PSV_PAGE_BF16)
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  if constexpr (FMT == PSV_PAGE_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
-  if constexpr (FMT == PSV_PAGE_E4M3) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u), __NV_E4M3);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-  }
-  if constexpr (FMT == PSV_PAGE_I8)
-    return make_float2(static_cast<float>(static_cast<int8_t>(u)), static_cast<float>(static_cast<int8_t>(u >> 8)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
 // Eight values of a program's row, as they are in memory.
@@ -92,6 +111,25 @@ struct Eight {
       }
     }
   }
+  // Bits of the largest |x| (NaN is above infinity), 16 of them for 16-bit types.
+  __device__ __forceinline__ uint32_t size() const {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t y[4] = {u[1].x, u[1].y, u[1].z, u[1].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffffffu, y[i] & 0x7fffffffu));
+      return m;
+    } else {
+      const uint32_t a = 0x7fff7fffu, m = __vmaxu2(__vmaxu2(w[0] & a, w[1] & a), __vmaxu2(w[2] & a, w[3] & a));
+      return max(m & 0xffffu, m >> 16);
+    }
+  }
+  static __device__ __forceinline__ float size_value(uint32_t bits) {
+    if constexpr (kFmt == PSV_PAGE_BF16) return __uint_as_float(bits << 16);
+    if constexpr (kFmt == PSV_PAGE_F16) return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    return __uint_as_float(bits);
+  }
   __device__ __forceinline__ void set(const float* f) {
     if constexpr (sizeof(T) == 4) {
       memcpy(u, f, 32);
@@ -114,75 +152,85 @@ struct Eight {
 };
 
 constexpr int kRowThreads = 256;
+constexpr int kHeads = 4;
 
-// A row (a head of a token) belongs to 2^lanes threads of a warp, eight values
-// each, which find its largest size by shuffles; a thread has kR rows on their
-// way.  grid (rows, sequence, key or value).
+// A token's group of heads belongs to 2^lanes threads of a warp, eight values of each
+// head's row, which find the rows' largest sizes by shuffles; the rows' divisions are
+// made by a lane each.  grid (tokens x groups, sequence, key or value).  A thread's
+// first reads do not wait for the lengths: rows not in use are read too.
+// Memory-bound where large: @W@
 template <class T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
-  constexpr int kR = sizeof(T) == 4 ? 2 : 4;
   const int b = blockIdx.y, kv = blockIdx.z;
-  const int step = kRowThreads >> p.lanes, lane = threadIdx.x & ((1 << p.lanes) - 1), d = lane * 8;
-  const uint32_t r0 = blockIdx.x * static_cast<uint32_t>(step * kR) + (threadIdx.x >> p.lanes);
+  const int lane = threadIdx.x & ((1 << p.lanes) - 1), d = lane * 8;
+  const uint32_t r = blockIdx.x * (kRowThreads >> p.lanes) + (threadIdx.x >> p.lanes), i = p.by_groups.div(r);
+  const int h0 = static_cast<int>(r - i * p.by_groups.d) * p.heads, heads = min(p.heads, p.H - h0);
   pdl_trigger();
   pdl_wait();
-  const int n = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
-  const int start = p.starts ? p.starts[b] : 0;
-  const T* x = static_cast<const T*>(p.x[kv]) + b * p.xs[kv].b;
-  Eight<T> in[kR];
-  PageRow at[kR];
-  int head[kR];
+  const Strides3& xs = p.xs[kv];
+  Eight<T> in[kHeads];
+  if (i < static_cast<uint32_t>(p.L) && d < p.dh) {
+    const T* x = static_cast<const T*>(p.x[kv]) + b * xs.b + i * xs.l + h0 * xs.h + d;
 #pragma unroll
-  for (int k = 0; k < kR; ++k) {
-    const uint32_t r = r0 + k * step, i = p.by_head.div(r);
-    head[k] = static_cast<int>(r - i * p.by_head.d);
-    at[k].page = -1;
-    if (i >= static_cast<uint32_t>(n)) continue;
-    if (d < p.dh) {
-      const T* row = x + i * p.xs[kv].l + head[k] * p.xs[kv].h + d;
-      if (VEC) in[k].load(row);
-      else in[k].load(row, p.dh - d);
-    }
-    at[k] = page_row(p.c, b, static_cast<int64_t>(start) + i);
+    for (int k = 0; k < kHeads; ++k, x += xs.h)
+      if (k < heads) {
+        if (VEC) in[k].load(x);
+        else in[k].load(x, p.dh - d);
+      }
   }
+  const int n = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
+  PageRow at{-1, 0};
+  if (i < static_cast<uint32_t>(n)) at = page_row(p.c, b, static_cast<int64_t>(p.starts ? p.starts[b] : 0) + i);
+  float turn[kHeads];
+  if constexpr (F::kScaled) {
+    uint32_t size[kHeads];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) size[k] = k < heads && d < p.dh ? in[k].size() : 0;
+    if constexpr (sizeof(T) == 2) {  // two rows a shuffle
+#pragma unroll
+      for (int k = 0; k < kHeads; k += 2) {
+        uint32_t two = size[k] | size[k + 1] << 16;
+        for (int o = 1 << p.lanes >> 1; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+        size[k] = two & 0xffffu, size[k + 1] = two >> 16;
+      }
+    } else {
+      for (int o = 1 << p.lanes >> 1; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) size[k] = max(size[k], __shfl_xor_sync(0xffffffffu, size[k], o));
+    }
+    // Row lane % 4 is this lane's to divide for.
+    const uint32_t mine = lane & 2 ? (lane & 1 ? size[3] : size[2]) : (lane & 1 ? size[1] : size[0]);
+    const float most = Eight<T>::size_value(mine);
+    const bool finite = __float_as_uint(most) < 0x7f800000u, kept = finite && most >= kTiny;
+    const float my_turn = kept ? __fdiv_rn(F::kMost, most) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) turn[k] = __shfl_sync(0xffffffffu, my_turn, k, 1 << p.lanes);
+    if (lane < heads && at.page >= 0)
+      (kv ? p.c.v_scale : p.c.k_scale)[at.page * p.c.ss.b + at.row * p.c.ss.l + (h0 + lane) * p.c.ss.h] =
+          kept ? __fdiv_rn(most, F::kMost) : finite ? 0.0f : __int_as_float(0x7fc00000);
+  }
+  if (d >= p.dh || at.page < 0) return;
   const Strides3& ps = kv ? p.c.vs : p.c.ks;
-  char* pages = static_cast<char*>(kv ? p.c.v : p.c.k);
+  char* out = static_cast<char*>(kv ? p.c.v : p.c.k) + (at.page * ps.b + at.row * ps.l + h0 * ps.h + d) * F::kSize;
 #pragma unroll
-  for (int k = 0; k < kR; ++k) {
+  for (int k = 0; k < kHeads; ++k, out += ps.h * F::kSize) {
+    if (k >= heads) break;
     float f[8];
-    if (d < p.dh) in[k].get(f);
-    float turn = 1.0f;
-    if constexpr (F::kScaled) {
-      uint32_t size = 0;  // bits of |x|, by which NaN is above infinity
-      if (d < p.dh)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) size = max(size, __float_as_uint(f[j]) & 0x7fffffffu);
-      for (int o = 1 << p.lanes >> 1; o; o >>= 1) size = max(size, __shfl_xor_sync(0xffffffffu, size, o));
-      const float most = __uint_as_float(size);
-      const bool finite = size < 0x7f800000u, zero = most < kTiny;
-      turn = finite && !zero ? __fdiv_rn(F::kMost, most) : 0.0f;
-      if (lane == 0 && at[k].page >= 0)
-        (kv ? p.c.v_scale : p.c.k_scale)[at[k].page * p.c.ss.b + at[k].row * p.c.ss.l + head[k] * p.c.ss.h] =
-            !finite ? __int_as_float(0x7fc00000) : zero ? 0.0f : __fdiv_rn(most, F::kMost);
-    }
-    if (d >= p.dh || at[k].page < 0) continue;
+    in[k].get(f);
     if constexpr (F::kScaled) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = turn > 0.0f ? f[j] * turn : 0.0f;
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = encode2<FMT>(f[2 * j], f[2 * j + 1]);
-    char* out = pages + (at[k].page * ps.b + at[k].row * ps.l + head[k] * ps.h + d) * F::kSize;
-    if constexpr (F::kScaled) {
-      const uint2 y = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      for (int j = 0; j < 8; ++j) f[j] = turn[k] > 0.0f ? f[j] * turn[k] : 0.0f;  // (not 0 * NaN)
+      const uint2 y = make_uint2(encode4<FMT>(f), encode4<FMT>(f + 4));
       if (VEC) *reinterpret_cast<uint2*>(out) = y;
       else
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (d + j < p.dh) out[j] = static_cast<char>((j < 4 ? y.x : y.y) >> 8 * (j % 4));
     } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = encode2<FMT>(f[2 * j], f[2 * j + 1]);
       if (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
       else
 #pragma unroll
@@ -193,85 +241,81 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
 }
 
 // The same threads read rows back; positions without a page read as zeros.
+// @R@
 template <class T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) page_read_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
-  constexpr int kR = 4;
   const int b = blockIdx.y, kv = blockIdx.z;
-  const int step = kRowThreads >> p.lanes, d = (threadIdx.x & ((1 << p.lanes) - 1)) * 8;
-  const uint32_t r0 = blockIdx.x * static_cast<uint32_t>(step * kR) + (threadIdx.x >> p.lanes);
+  const int d = (threadIdx.x & ((1 << p.lanes) - 1)) * 8;
+  const uint32_t r = blockIdx.x * (kRowThreads >> p.lanes) + (threadIdx.x >> p.lanes), i = p.by_groups.div(r);
+  const int h0 = static_cast<int>(r - i * p.by_groups.d) * p.heads, heads = min(p.heads, p.H - h0);
   pdl_trigger();
   pdl_wait();
-  if (d >= p.dh) return;
   const int n = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
-  const int start = p.starts ? p.starts[b] : 0;
-  const Strides3& ps = kv ? p.c.vs : p.c.ks;
-  const char* pages = static_cast<const char*>(kv ? p.c.v : p.c.k);
-  const float* scales = kv ? p.c.v_scale : p.c.k_scale;
-  T* x = static_cast<T*>(p.x[kv]) + b * p.xs[kv].b + d;
-  PageRow at[kR];
-  uint32_t row[kR];
-  int head[kR];
+  if (d >= p.dh || i >= static_cast<uint32_t>(n)) return;
+  const PageRow at = page_row(p.c, b, static_cast<int64_t>(p.starts ? p.starts[b] : 0) + i);
+  uint32_t w[kHeads][4] = {};
+  float s[kHeads] = {};
+  if (at.page >= 0) {
+    const Strides3& ps = kv ? p.c.vs : p.c.ks;
+    const char* in = static_cast<const char*>(kv ? p.c.v : p.c.k) + (at.page * ps.b + at.row * ps.l + h0 * ps.h + d) * F::kSize;
+    const float* scale = (kv ? p.c.v_scale : p.c.k_scale) + (F::kScaled ? at.page * p.c.ss.b + at.row * p.c.ss.l + h0 * p.c.ss.h : 0);
 #pragma unroll
-  for (int k = 0; k < kR; ++k) {
-    const uint32_t r = r0 + k * step;
-    row[k] = p.by_head.div(r);
-    head[k] = static_cast<int>(r - row[k] * p.by_head.d);
-    at[k].page = -1;
-    if (row[k] < static_cast<uint32_t>(n)) at[k] = page_row(p.c, b, static_cast<int64_t>(start) + row[k]);
-  }
-  uint32_t w[kR][4];
-  float s[kR];
+    for (int k = 0; k < kHeads; ++k, in += ps.h * F::kSize) {
+      if (k >= heads) break;
+      if constexpr (F::kScaled) {
+        s[k] = scale[k * p.c.ss.h];
+        if (VEC) {
+          const uint2 y = *reinterpret_cast<const uint2*>(in);
+          w[k][0] = y.x, w[k][1] = y.y;
+        } else {
 #pragma unroll
-  for (int k = 0; k < kR; ++k) {
-    w[k][0] = w[k][1] = w[k][2] = w[k][3] = 0;
-    s[k] = 0.0f;
-    if (at[k].page < 0) continue;
-    const char* in = pages + (at[k].page * ps.b + at[k].row * ps.l + head[k] * ps.h + d) * F::kSize;
-    if constexpr (F::kScaled) {
-      s[k] = scales[at[k].page * p.c.ss.b + at[k].row * p.c.ss.l + head[k] * p.c.ss.h];
-      if (VEC) {
-        const uint2 y = *reinterpret_cast<const uint2*>(in);
-        w[k][0] = y.x, w[k][2] = y.y;
+          for (int j = 0; j < 8; ++j)
+            if (d + j < p.dh) w[k][j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(in[j])) << 8 * (j % 4);
+        }
+      } else if (VEC) {
+        const uint4 y = *reinterpret_cast<const uint4*>(in);
+        w[k][0] = y.x, w[k][1] = y.y, w[k][2] = y.z, w[k][3] = y.w;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (d + j < p.dh) w[k][j / 4 * 2] |= static_cast<uint32_t>(static_cast<uint8_t>(in[j])) << 8 * (j % 4);
+          if (d + j < p.dh)
+            w[k][j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(in)[j]) << 16 * (j % 2);
       }
-    } else if (VEC) {
-      const uint4 y = *reinterpret_cast<const uint4*>(in);
-      w[k][0] = y.x, w[k][1] = y.y, w[k][2] = y.z, w[k][3] = y.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (d + j < p.dh)
-          w[k][j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(in)[j]) << 16 * (j % 2);
     }
   }
+  T* x = static_cast<T*>(p.x[kv]) + b * p.xs[kv].b + i * p.xs[kv].l + h0 * p.xs[kv].h + d;
 #pragma unroll
-  for (int k = 0; k < kR; ++k) {
-    if (row[k] >= static_cast<uint32_t>(n)) continue;
+  for (int k = 0; k < kHeads; ++k, x += p.xs[kv].h) {
+    if (k >= heads) break;
     float f[8];
+    if constexpr (F::kScaled) {
+      decode4<FMT>(w[k][0], f);
+      decode4<FMT>(w[k][1], f + 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 y = decode2<FMT>(F::kScaled ? w[k][j / 2 * 2] >> 16 * (j % 2) & 0xffff : w[k][j]);
-      f[2 * j] = F::kScaled ? y.x * s[k] : y.x;
-      f[2 * j + 1] = F::kScaled ? y.y * s[k] : y.y;
+      for (int j = 0; j < 8; ++j) f[j] *= s[k];
+      if (at.page < 0)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = decode2<FMT>(w[k][j]);
+        f[2 * j] = y.x, f[2 * j + 1] = y.y;
+      }
     }
     Eight<T> out;
     out.set(f);
-    T* y = x + row[k] * p.xs[kv].l + head[k] * p.xs[kv].h;
-    if (VEC) out.store(y);
-    else out.store(y, p.dh - d);
+    if (VEC) out.store(x);
+    else out.store(x, p.dh - d);
   }
 }
 
 template <class T, int FMT>
 cudaError_t launch_page_rows(const PageRowsParams& p, int B, bool vec, bool write, cudaStream_t st) {
-  const uint32_t rows = static_cast<uint32_t>(p.L) * p.H;
-  const uint32_t each = (kRowThreads >> p.lanes) * (write && sizeof(T) == 4 ? 2 : 4);
+  const uint32_t groups = static_cast<uint32_t>(p.L) * p.by_groups.d, each = kRowThreads >> p.lanes;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3((rows + each - 1) / each, B, 2), kRowThreads, 0, st, attr);
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((groups + each - 1) / each, B, 2), kRowThreads, 0, st, attr);
   if (write)
     return vec ? cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true>, p)
                : cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, false>, p);
@@ -399,8 +443,11 @@ int page_rows_call(const psv_page_cache* c, const psv_page_rows* r, const void* 
   PageRowsParams p{};
   p.c = page_cache_dev(c);
   p.L = r->L, p.H = c->Hkv, p.dh = c->dh;
+  p.lanes = 2;
   while (8 << p.lanes < c->dh) ++p.lanes;
-  p.by_head = FastDiv::of(static_cast<uint32_t>(c->Hkv));
+  const int groups = (c->Hkv + kHeads - 1) / kHeads;
+  p.heads = (c->Hkv + groups - 1) / groups;
+  p.by_groups = FastDiv::of(static_cast<uint32_t>(groups));
   p.xs[0] = strides3(r->k_stride), p.xs[1] = strides3(r->v_stride);
   p.x[0] = const_cast<void*>(k), p.x[1] = const_cast<void*>(v);
   p.starts = r->starts, p.lens = r->lens;
