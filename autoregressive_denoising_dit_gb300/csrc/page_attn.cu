@@ -23,7 +23,9 @@
 // one line that is cut into equal stretches, one a CTA, whatever the lengths.
 // Where a cut falls into a group its shares go to the workspace, and a second kernel
 // joins them in order.  (The last of a group's CTAs to be done took 5 to 12 us to
-// notice that and to join them; all SMs take 3, launch included.)
+// notice that and to join them; all SMs take 3, launch included.)  Where the tables
+// cover so little that a cluster of CTAs has two rounds of steps a warp for a group,
+// groups are not cut: a cluster takes whole groups and its CTAs read one another's sums.
 #include <algorithm>
 #include <cfloat>
 
@@ -68,9 +70,10 @@ struct ACfg {
   static constexpr int WARPS = NT == 1 && DH == 64 ? 8 : (NT == 1 && kScaled) || DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int JOIN = WARPS * ROWS * (JSTRIDE + 4) * 4;  // the warps' sums at the end of a group
-  static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN - Q_BYTES) / (WARPS * SLOT));
+  static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN - Q_BYTES - ROWS * (DH + 4) * 4) / (WARPS * SLOT));
   static constexpr int RING = WARPS * STAGES * SLOT;
-  static constexpr int SMEM = RING + JOIN + Q_BYTES;
+  static constexpr int PART = ROWS * (DH + 4) * 4;  // a CTA's sums, which its cluster reads
+  static constexpr int SMEM = RING + JOIN + Q_BYTES + PART;
   static_assert(2 * (SMEM + 1024 + 256) <= 233472, "two CTAs an SM");
 };
 
@@ -92,6 +95,16 @@ template <int FMT>
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if constexpr (FMT == PSV_PAGE_BF16) mma_bf16(c, a, b0, b1);
   else mma_f16(c, a, b0, b1);
+}
+
+// Four floats of another CTA's shared memory.
+__device__ __forceinline__ float4 load_peer(const float* at, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(mapa_shared(at, rank))
+               : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
@@ -225,7 +238,7 @@ __device__ __forceinline__ void write_out(const PageAttnParams& p, int b, int kv
     p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Lq + tok] = ll == 0.0f ? -INFINITY : (mm_l + fast_log2(ll)) * kLn2;
 }
 
-template <int DH, int FMT, int NT>
+template <int DH, int FMT, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     page_attn_kernel(const __grid_constant__ PageAttnParams p) {
   using C = ACfg<DH, FMT, NT>;
@@ -237,6 +250,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   float* sm = so + kWarps * ROWS * C::JSTRIDE;           // [kWarps][ROWS][4]: m', m, l
   uint4* sq = reinterpret_cast<uint4*>(smem + C::RING + C::JOIN);  // QS: [NT][KP * KS / 2][lane]
   float* sq_up = reinterpret_cast<float*>(sq + NT * C::KP * C::KS * 16);  // [ROWS]
+  float* sp = reinterpret_cast<float*>(smem + C::RING + C::JOIN + C::Q_BYTES);  // CLUSTER: a share
   const PageCacheDev& c = p.c;
   const int warp = warp_id(), lane = lane_id(), quad = lane / 4, four = lane % 4;
   if (p.dh < DH) {  // pieces behind the head stay zeros
@@ -246,19 +260,24 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   pdl_trigger();
   pdl_wait();
 
+  // The unit of the line: a step, or in clusters a group.
+  const int peers = CLUSTER ? p.cluster : 1, rank = CLUSTER ? blockIdx.x % peers : 0;
+  const int worker = rank * kWarps + warp, workers = peers * kWarps;
+  auto units = [&](const Seq& x) { return CLUSTER ? static_cast<int64_t>(x.tiles) * p.Hkv : x.total; };
   // The line's length, this CTA's stretch [lo, hi) of it, and the sequence that it begins in.
   auto rows_at = [&](int b) { return b < p.B ? page_rows(p, b) : 0; };
   int rows_b = rows_at(lane), n_b = lane < p.B ? page_length(p, lane, rows_b) : 0;
-  int64_t all = sequence<ROWS>(p, rows_b, n_b).total;
+  int64_t all = units(sequence<ROWS>(p, rows_b, n_b));
   for (int b = lane + 32; b < p.B; b += 32) {
     const int rows = page_rows(p, b);
-    all += sequence<ROWS>(p, rows, page_length(p, b, rows)).total;
+    all += units(sequence<ROWS>(p, rows, page_length(p, b, rows)));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  const Cut cut(all, static_cast<int>(min(static_cast<int64_t>(gridDim.x), (all + kWarps - 1) / kWarps)));
-  if (threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
-  if (static_cast<int>(blockIdx.x) >= cut.ctas) return;
+  const int place_of = blockIdx.x / peers;
+  const Cut cut(all, static_cast<int>(min(static_cast<int64_t>(gridDim.x) / peers, CLUSTER ? all : (all + kWarps - 1) / kWarps)));
+  if (!CLUSTER && threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
+  if (place_of >= cut.ctas) return;
   int64_t lo = 0, hi = 0;
   int b = 0;
   int64_t before = 0;  // steps of earlier sequences
@@ -266,11 +285,12 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   {
     int64_t sum0 = 0;
     bool begun = false;
-    const int64_t lo0 = cut.begin(blockIdx.x), hi0 = cut.begin(blockIdx.x + 1);
+    const int64_t lo0 = cut.begin(place_of), hi0 = cut.begin(place_of + 1);
     for (int b0 = 0;; b0 += 32) {
       if (b0) rows_b = rows_at(b0 + lane), n_b = b0 + lane < p.B ? page_length(p, b0 + lane, rows_b) : 0;
       const Seq mine = sequence<ROWS>(p, rows_b, n_b);
-      int64_t sum = mine.total;
+      const int64_t own = units(mine);
+      int64_t sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
@@ -280,9 +300,9 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       auto moved = [&](int64_t x, int& at) {
         const unsigned hit = __ballot_sync(0xffffffffu, sum0 + sum > x);
         at = __ffs(hit) - 1;
-        if (!hit) return x;
+        if (CLUSTER || !hit) return x;
         const int steps = __shfl_sync(0xffffffffu, mine.steps, at);
-        const int64_t within = x - sum0 - __shfl_sync(0xffffffffu, sum - mine.total, at);
+        const int64_t within = x - sum0 - __shfl_sync(0xffffffffu, sum - own, at);
         const int64_t rest = within - divide(within, steps) * steps;
         return rest < cut.near(steps) ? x - rest : steps - rest < cut.near(steps) ? x + steps - rest : x;
       };
@@ -292,7 +312,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         if (at >= 0) {
           begun = true;
           b = b0 + at;
-          before = sum0 + __shfl_sync(0xffffffffu, sum - mine.total, at);
+          before = sum0 + __shfl_sync(0xffffffffu, sum - own, at);
           s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
         }
       }
@@ -327,7 +347,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   int issued = 0;  // steps of the group that the warp has asked for
   auto key_of = [&](int step) { return step < s.head ? step * kStep : s.from + (step - s.head) * kStep; };
   auto look = [&](int number) {  // of the warp's steps
-    const int step = step0 + warp + (number + (eights ? lane / 2 : 0)) * kWarps;
+    const int step = step0 + worker + (number + (eights ? lane / 2 : 0)) * workers;
     return step < step1 ? page_row(c, b, key_of(step) + (eights ? lane % 2 * 8 : lane % 16)) : PageRow{-1, 0};
   };
   auto offset = [](uint32_t page_stride, uint32_t row_stride, int page, int row) {
@@ -335,7 +355,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
            static_cast<uint64_t>(row_stride) * static_cast<uint32_t>(row);
   };
   auto issue = [&](int into) {
-    const int step = step0 + warp + issued * kWarps, number = issued++;
+    const int step = step0 + worker + issued * workers, number = issued++;
     found <<= 1;
     if (step >= step1) return;
     const uint32_t dst = ring0 + into * C::SLOT;
@@ -402,16 +422,16 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     uint32_t raw[NQ][C::KP][kPer / 2];
     if (more) {
       // ---- the next group: its first keys and its queries are on their way before the last one is joined
-      while (lo >= before + s.total) {
-        before += s.total;
+      while (lo >= before + units(s)) {
+        before += units(s);
         ++b;
         const int rows = page_rows(p, b);
         s = sequence<ROWS>(p, rows, page_length(p, b, rows));
       }
       const int64_t within = lo - before;
-      const int group = static_cast<int>(divide(within, s.steps));
-      step0 = static_cast<int>(within - static_cast<int64_t>(group) * s.steps);
-      step1 = static_cast<int>(min(static_cast<int64_t>(s.steps), step0 + (hi - lo)));
+      const int group = static_cast<int>(CLUSTER ? within : divide(within, s.steps));
+      step0 = CLUSTER ? 0 : static_cast<int>(within - static_cast<int64_t>(group) * s.steps);
+      step1 = CLUSTER ? s.steps : static_cast<int>(min(static_cast<int64_t>(s.steps), step0 + (hi - lo)));
       kvh = s.tiles == 1 ? group : group / s.tiles;
       r0 = (group - kvh * s.tiles) * ROWS;
       n_rows = min(s.rows * p.G - r0, ROWS);
@@ -496,13 +516,36 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
         }
         if (split) {
-          *reinterpret_cast<float4*>(part + r * DH + d) = acc;
-          if (d == 0) *reinterpret_cast<float4*>(part + ROWS * DH + r * 4) = make_float4(mm_o, mm_l, ll, 0.0f);
+          float* to = CLUSTER ? sp : part;
+          *reinterpret_cast<float4*>(to + r * DH + d) = acc;
+          if (d == 0) *reinterpret_cast<float4*>(to + ROWS * DH + r * 4) = make_float4(mm_o, mm_l, ll, 0.0f);
         } else {
           write_out(p, was_b, was_kvh, was_r0 + r, d, mm_o, mm_l, ll, acc);
         }
       }
       __syncthreads();
+      if (CLUSTER && split) {
+        cluster_sync();
+#pragma unroll 1
+        for (int x = rank * kThreads + threadIdx.x; x < was_rows * (DH / 4); x += peers * kThreads) {
+          const int r = x / (DH / 4), d = x % (DH / 4) * 4;
+          float mm_o = kNone, mm_l = kNone, ll = 0.0f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = 0; k < peers; ++k) {
+            const float4 y = load_peer(sp + r * DH + d, k), st = load_peer(sp + ROWS * DH + r * 4, k);
+            const float m = fmaxf(mm_o, st.x), f = fast_exp2(mm_o - m), g = fast_exp2(st.x - m);
+            acc.x = fmaf(g, y.x, acc.x * f), acc.y = fmaf(g, y.y, acc.y * f);
+            acc.z = fmaf(g, y.z, acc.z * f), acc.w = fmaf(g, y.w, acc.w * f);
+            mm_o = m;
+            const float n = fmaxf(mm_l, st.y);
+            ll = fmaf(st.z, fast_exp2(st.y - n), ll * fast_exp2(mm_l - n));
+            mm_l = n;
+          }
+          write_out(p, was_b, was_kvh, was_r0 + r, d, mm_o, mm_l, ll, acc);
+        }
+        cluster_sync();  // (the sums are read; a CTA that ends takes its own along)
+      }
     }
     if (!more) break;
 
@@ -562,7 +605,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     }
 
 #pragma unroll 1
-    for (int step = step0 + warp; step < step1; step += kWarps) {
+    for (int step = step0 + worker; step < step1; step += workers) {
       issue(slot == 0 ? kStages - 1 : slot - 1);
       copies_commit();
       copies_wait<kStages - 1>();
@@ -760,19 +803,20 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 
     // ---- what its join needs
     joining = true;
-    split = step0 > 0 || step1 < s.steps;
+    split = CLUSTER ? peers > 1 : step0 > 0 || step1 < s.steps;
     was_b = b, was_kvh = kvh, was_r0 = r0, was_rows = n_rows;
     was_slot = step0 == 0;
-    if (split && was_slot && threadIdx.x == 0) {
+    if (!CLUSTER && split && was_slot && threadIdx.x == 0) {
       const int near = max(cut.near(s.steps) - 1, 0);
       const int shares = cut.of(lo + s.steps - 1 - near) - static_cast<int>(blockIdx.x) + 1;
       p.shared[blockIdx.x] = Shared{n_rows, shares, b, kvh, r0};
     }
-    lo += step1 - step0;
+    lo += CLUSTER ? 1 : step1 - step0;
   }
 }
 
 constexpr int kJoinThreads = 512;
+constexpr int kRounds = 4;
 
 // Joins the shares of the group that CTA blockIdx.x of the attention began: a row's
 // statistics by a warp, its values by as many threads a column as there are, whose first
@@ -851,34 +895,54 @@ __global__ void __launch_bounds__(kJoinThreads) page_join_kernel(const __grid_co
   }
 }
 
-template <int DH, int FMT, int NT>
+template <int DH, int FMT, int NT, bool CLUSTER>
 cudaError_t launch(const PageAttnParams& p, int sms, cudaStream_t st) {
   using C = ACfg<DH, FMT, NT>;
   static uint64_t set_up = 0;
   cudaError_t e = once_per_device(&set_up, [](int) {
-    return cudaFuncSetAttribute(page_attn_kernel<DH, FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    return cudaFuncSetAttribute(page_attn_kernel<DH, FMT, NT, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
+  const int most = std::min(sms * kCtasSm, kMaxCtas);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(sms * kCtasSm, kMaxCtas)));
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CLUSTER ? p.cluster : 1;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  const int64_t clusters = std::min<int64_t>(most / p.cluster, p.groups);
+  cfg.gridDim = dim3(static_cast<unsigned>(CLUSTER ? clusters * p.cluster : most));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, page_attn_kernel<DH, FMT, NT>, p);
-  if (e != cudaSuccess) return e;
+  cfg.numAttrs = CLUSTER ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, page_attn_kernel<DH, FMT, NT, CLUSTER>, p);
+  if (e != cudaSuccess || CLUSTER) return e;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, page_join_kernel<DH>, p, C::ROWS);
 }
 
+template <int DH, int FMT, int NT>
+cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
+  using C = ACfg<DH, FMT, NT>;
+  // As many CTAs a group as there is room for, at most 8, unless a warp would then have
+  // more than kRounds steps of a group of the greatest length that the tables allow: @C@
+  const int64_t tiles = (static_cast<int64_t>(p.Lq) * p.G + C::ROWS - 1) / C::ROWS;
+  p.groups = p.B * p.Hkv * tiles;
+  const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * kStep)
+                                  : p.c.positions) / kStep + 1;
+  p.cluster = 1;
+  while (p.cluster < 8 && p.groups * p.cluster * 2 <= kMaxCtas && p.cluster * C::WARPS < steps) p.cluster *= 2;
+  const int64_t rounds = (p.groups * p.cluster + kMaxCtas - 1) / kMaxCtas * ((steps + p.cluster * C::WARPS - 1) / (p.cluster * C::WARPS));
+  return rounds <= kRounds ? launch<DH, FMT, NT, true>(p, sms, st) : launch<DH, FMT, NT, false>(p, sms, st);
+}
+
 template <int DH, int FMT>
 cudaError_t launch_rows(const PageAttnParams& p, int sms, cudaStream_t st) {
-  return p.Lq * p.G <= 8 ? launch<DH, FMT, 1>(p, sms, st) : launch<DH, FMT, 2>(p, sms, st);
+  return p.Lq * p.G <= 8 ? launch_tile<DH, FMT, 1>(p, sms, st) : launch_tile<DH, FMT, 2>(p, sms, st);
 }
 
 template <int DH>
