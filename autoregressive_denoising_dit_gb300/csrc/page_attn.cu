@@ -24,8 +24,8 @@
 // Where a cut falls into a group its shares go to the workspace, and a second kernel
 // joins them in order.  (The last of a group's CTAs to be done took 5 to 12 us to
 // notice that and to join them; all SMs take 3, launch included.)  Where the tables
-// cover so little that a cluster of CTAs has two rounds of steps a warp for a group,
-// groups are not cut: a cluster takes whole groups and its CTAs read one another's sums.
+// cover little, groups are not cut: a cluster of CTAs takes whole groups, and its CTAs
+// read one another's sums.
 #include <algorithm>
 #include <cfloat>
 
@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 }
 
 constexpr int kJoinThreads = 512;
-constexpr int kRounds = 4;
+constexpr int kRounds = 12;
 
 // Joins the shares of the group that CTA blockIdx.x of the attention began: a row's
 // statistics by a warp, its values by as many threads a column as there are, whose first
@@ -929,7 +929,10 @@ template <int DH, int FMT, int NT>
 cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   using C = ACfg<DH, FMT, NT>;
   // As many CTAs a group as there is room for, at most 8, unless a warp would then have
-  // more than kRounds steps of a group of the greatest length that the tables allow: @C@
+  // more than kRounds steps at the greatest length that the tables allow.  Whole against
+  // cut groups, 8-bit heads of 128: 12 groups of 1000 keys 7.4 and 12.1 us, 4000 10.8 and
+  // 12.5, 8000 (11 rounds) 14.6 and 14.3; 96 groups of 2000 (11) 16.7 and 20.3, 4000 (21)
+  // 26.1 and 26.8, 7800 44 and 36; 384 of 500 (12) 18.8 and 21.1, 1000 (22) 29.3 and 27.7.
   const int64_t tiles = (static_cast<int64_t>(p.Lq) * p.G + C::ROWS - 1) / C::ROWS;
   p.groups = p.B * p.Hkv * tiles;
   const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * kStep)

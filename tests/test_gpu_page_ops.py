@@ -87,11 +87,15 @@ def numbers(pages, f):
 class Cache:
     """A pool of pages in which everything is NaN (codes 0x7f, scales NaN) but what is written."""
 
-    def __init__(self, P, f, B, Hkv, dh, page, max_pages, spare=3, seed=0, layout="phrd", missing=(), packed=False):
-        self.P, self.f, self.B, self.Hkv, self.dh, self.page, self.max_pages = P, f, B, Hkv, dh, page, max_pages
+    def __init__(self, P, f, B, Hkv, dh, page, max_pages, spare=3, seed=0, layout="phrd", missing=(), packed=False,
+                 width=0):
+        """width: entries of the table, those behind max_pages without a page."""
+        self.P, self.f, self.B, self.Hkv, self.dh, self.page = P, f, B, Hkv, dh, page
+        self.max_pages = max(max_pages, width)
         self.n_pages = B * max_pages + spare
         g = torch.Generator().manual_seed(seed)
         t = torch.randperm(self.n_pages, generator=g)[:B * max_pages].view(B, max_pages).int()
+        t = torch.cat([t, torch.full((B, self.max_pages - max_pages), -7, dtype=torch.int32)], 1)
         for b, i in missing:
             t[b, i] = -1 if (b + i) % 2 else self.n_pages + 5
         self.table = t.cuda()
@@ -284,7 +288,7 @@ def reference(cache, c, q, k, v, lens, rows):
             out.append(None)
             continue
         qq = q[b, :ql].double()
-        m = min(n, cache.max_pages * cache.page)
+        m = min(n, cache.max_pages * cache.page, k.shape[1])  # (there are no pages behind the kept ones)
         kk, vv = (x[b, :m].repeat_interleave(G, 1) for x in (k, v))
         j = torch.arange(m, device="cuda")[None]
         p = (n - ql + torch.arange(ql, device="cuda"))[:, None]
@@ -366,14 +370,17 @@ ATTN = [
 ]
 
 
-def attention_case(P, c, dtype, f, seed=1, layout="phrd", packed=False, spread=1.0):
+def attention_case(P, c, dtype, f, seed=1, layout="phrd", packed=False, spread=1.0, width=0):
     B, Lq, Lk, Hq, Hkv, dh = (c[n] for n in ("B", "Lq", "Lk", "Hq", "Hkv", "dh"))
     g = torch.Generator(device="cuda").manual_seed(seed)
     max_pages = -(-Lk // c["page"])
-    cache = Cache(P, f, B, Hkv, dh, c["page"], max_pages, missing=c.get("missing", ()), layout=layout, packed=packed)
+    cache = Cache(P, f, B, Hkv, dh, c["page"], max_pages, missing=c.get("missing", ()), layout=layout, packed=packed,
+                  width=width)
     lens, rows = c.get("lens", [Lk] * B), c.get("rows", [Lq] * B)
     total = [n + r for n, r in zip(lens, rows)] if c.get("append") else lens
     used = [min(n, max_pages * c["page"]) for n in total]
+    if width and c.get("lens") is None:
+        total = lens = used
     k, v = (torch.randn(B, max(used) or 1, Hkv, dh, device="cuda", generator=g) for _ in range(2))
     # rows of very different size, so that their scales differ
     k, v = (x * torch.exp(spread * torch.randn(x.shape[:2] + (Hkv, 1), device="cuda", generator=g)) for x in (k, v))
@@ -403,9 +410,10 @@ def run_attention(P, c, cache, q, lens, rows, dtype, o=None, scratch=None):
 
 @pytest.mark.parametrize("dtype,f", [("bf16", "e4m3"), ("f16", "e4m3"), ("bf16", "i8"), ("f16", "i8"), ("bf16", "bf16"),
                                      ("f16", "f16")])
+@pytest.mark.parametrize("wide", [False, True])  # tables that cover much more than there is: shared groups are cut
 @pytest.mark.parametrize("case", ATTN, ids=lambda c: f"B{c['B']}q{c['Lq']}k{c['Lk']}H{c['Hq']}-{c['Hkv']}dh{c['dh']}p{c['page']}")
-def test_attention(P, case, dtype, f):
-    cache, q, (k, v), lens, total, rows = attention_case(P, case, dtype, f)
+def test_attention(P, case, dtype, f, wide):
+    cache, q, (k, v), lens, total, rows = attention_case(P, case, dtype, f, width=100000 // case["page"] if wide else 0)
     ref = reference(cache, case, q, k, v, total, rows)
     o, lse = run_attention(P, case, cache, q, lens, rows, dtype)
     check(o, lse, ref, rows, 9.0)
