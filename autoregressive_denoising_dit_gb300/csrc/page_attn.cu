@@ -210,11 +210,18 @@ struct Cut {
   __device__ __forceinline__ Cut(int64_t a, int n) : all(a), each(0), ctas(n), more(0) {
     if (n) each = divide(a, n), more = static_cast<int>(a - each * n);
   }
-  __device__ __forceinline__ int64_t begin(int cta) const { return each * cta + more * cta / ctas; }
+  __device__ __forceinline__ int64_t begin(int cta) const {
+    return each * cta + static_cast<int>(__fdiv_rn(static_cast<float>(more * cta), static_cast<float>(ctas)));  // (exact: < 2^17)
+  }
   // A cut this near to an end of its group is moved there, so that fewer CTAs have
   // shares of two groups.
   __device__ __forceinline__ int near(int steps) const {
     return static_cast<int>(min(each >> 3, static_cast<int64_t>(steps >> 2)));
+  }
+  // By how much, `within` steps into a sequence of groups of `steps`.
+  __device__ __forceinline__ int moved(int64_t within, int steps) const {
+    const int rest = static_cast<int>(within - divide(within, steps) * steps), n = near(steps);
+    return rest < n ? -rest : steps - rest < n ? steps - rest : 0;
   }
   __device__ __forceinline__ int of(int64_t x) const { return static_cast<int>(divide((x + 1) * ctas - 1, all)); }
 };
@@ -236,6 +243,17 @@ __device__ __forceinline__ void write_out(const PageAttnParams& p, int b, int kv
   }
   if (d == 0 && p.lse)
     p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Lq + tok] = ll == 0.0f ? -INFINITY : (mm_l + fast_log2(ll)) * kLn2;
+}
+
+// Takes a share with statistics m', m, l into a sum.
+__device__ __forceinline__ void add_share(float& mm_o, float& mm_l, float& ll, float4& acc, float4 st, float4 y) {
+  const float m = fmaxf(mm_o, st.x), f = fast_exp2(mm_o - m), g = fast_exp2(st.x - m);
+  acc.x = fmaf(g, y.x, acc.x * f), acc.y = fmaf(g, y.y, acc.y * f);
+  acc.z = fmaf(g, y.z, acc.z * f), acc.w = fmaf(g, y.w, acc.w * f);
+  mm_o = m;
+  const float n = fmaxf(mm_l, st.y);
+  ll = fmaf(st.z, fast_exp2(st.y - n), ll * fast_exp2(mm_l - n));
+  mm_l = n;
 }
 
 template <int DH, int FMT, int NT, bool CLUSTER>
@@ -267,27 +285,52 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   // The line's length, this CTA's stretch [lo, hi) of it, and the sequence that it begins in.
   auto rows_at = [&](int b) { return b < p.B ? page_rows(p, b) : 0; };
   int rows_b = rows_at(lane), n_b = lane < p.B ? page_length(p, lane, rows_b) : 0;
-  int64_t all = units(sequence<ROWS>(p, rows_b, n_b));
-  for (int b = lane + 32; b < p.B; b += 32) {
-    const int rows = page_rows(p, b);
-    all += units(sequence<ROWS>(p, rows, page_length(p, b, rows)));
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  const int place_of = blockIdx.x / peers;
-  const Cut cut(all, static_cast<int>(min(static_cast<int64_t>(gridDim.x) / peers, CLUSTER ? all : (all + kWarps - 1) / kWarps)));
-  if (!CLUSTER && threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
-  if (place_of >= cut.ctas) return;
+  const int place_of = blockIdx.x / peers, places = gridDim.x / peers;
   int64_t lo = 0, hi = 0;
   int b = 0;
   int64_t before = 0;  // steps of earlier sequences
   Seq s;
-  {
-    int64_t sum0 = 0;
+  Cut cut(0, 0);
+  if (!CLUSTER && threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
+  if (p.quick) {  // a warp's worth of sequences, 32 bits
+    const Seq mine = sequence<ROWS>(p, rows_b, n_b);
+    const int own = (CLUSTER ? 1 : mine.steps) * mine.tiles * p.Hkv;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    const int all = __shfl_sync(0xffffffffu, sum, 31);
+    cut = Cut(all, min(places, CLUSTER ? all : (all + kWarps - 1) / kWarps));
+    if (place_of >= cut.ctas) return;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const int x = static_cast<int>(cut.begin(place_of + i));
+      const unsigned hit = __ballot_sync(0xffffffffu, sum > x);
+      const int at = max(__ffs(hit) - 1, 0);
+      const int first = __shfl_sync(0xffffffffu, sum - own, at), steps = __shfl_sync(0xffffffffu, mine.steps, at);
+      if (i == 0) {
+        b = at;
+        before = first;
+        s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
+      }
+      lo = hi;
+      hi = CLUSTER || !hit ? x : x + cut.moved(x - first, steps);
+    }
+  } else {
+    int64_t all = units(sequence<ROWS>(p, rows_b, n_b));
+    for (int k = lane + 32; k < p.B; k += 32) {
+      const int rows = page_rows(p, k);
+      all += units(sequence<ROWS>(p, rows, page_length(p, k, rows)));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    cut = Cut(all, static_cast<int>(min(static_cast<int64_t>(places), CLUSTER ? all : (all + kWarps - 1) / kWarps)));
+    if (place_of >= cut.ctas) return;
+    int64_t sum0 = 0, x = cut.begin(place_of);
     bool begun = false;
-    const int64_t lo0 = cut.begin(place_of), hi0 = cut.begin(place_of + 1);
-    for (int b0 = 0;; b0 += 32) {
-      if (b0) rows_b = rows_at(b0 + lane), n_b = b0 + lane < p.B ? page_length(p, b0 + lane, rows_b) : 0;
+    for (int b0 = 0;;) {
       const Seq mine = sequence<ROWS>(p, rows_b, n_b);
       const int64_t own = units(mine);
       int64_t sum = own;
@@ -296,30 +339,28 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += up;
       }
-      // the cut at x, if it lies in one of these sequences: there, or at the end of a group that is near
-      auto moved = [&](int64_t x, int& at) {
-        const unsigned hit = __ballot_sync(0xffffffffu, sum0 + sum > x);
-        at = __ffs(hit) - 1;
-        if (CLUSTER || !hit) return x;
+      // the cut at x lies in one of these sequences, or behind all
+      const unsigned hit = __ballot_sync(0xffffffffu, sum0 + sum > x);
+      if (hit || x >= all) {
+        const int at = max(__ffs(hit) - 1, 0);
+        const int64_t first = sum0 + __shfl_sync(0xffffffffu, sum - own, at);
         const int steps = __shfl_sync(0xffffffffu, mine.steps, at);
-        const int64_t within = x - sum0 - __shfl_sync(0xffffffffu, sum - own, at);
-        const int64_t rest = within - divide(within, steps) * steps;
-        return rest < cut.near(steps) ? x - rest : steps - rest < cut.near(steps) ? x + steps - rest : x;
-      };
-      int at;
-      if (!begun) {
-        lo = moved(lo0, at);
-        if (at >= 0) {
-          begun = true;
-          b = b0 + at;
-          before = sum0 + __shfl_sync(0xffffffffu, sum - own, at);
-          s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
+        const int64_t moved = CLUSTER || !hit ? x : x + cut.moved(x - first, steps);
+        if (begun) {
+          hi = moved;
+          break;
         }
+        begun = true;
+        b = b0 + at;
+        before = first;
+        s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
+        lo = moved;
+        x = cut.begin(place_of + 1);
+        continue;  // (its end may lie in the same sequences)
       }
-      hi = moved(hi0, at);
-      if (at >= 0) break;
       sum0 += __shfl_sync(0xffffffffu, sum, 31);
-      if (hi0 >= all && sum0 >= all) break;
+      b0 += 32;
+      rows_b = rows_at(b0 + lane), n_b = b0 + lane < p.B ? page_length(p, b0 + lane, rows_b) : 0;
     }
   }
 
@@ -532,16 +573,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           float mm_o = kNone, mm_l = kNone, ll = 0.0f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-          for (int k = 0; k < peers; ++k) {
-            const float4 y = load_peer(sp + r * DH + d, k), st = load_peer(sp + ROWS * DH + r * 4, k);
-            const float m = fmaxf(mm_o, st.x), f = fast_exp2(mm_o - m), g = fast_exp2(st.x - m);
-            acc.x = fmaf(g, y.x, acc.x * f), acc.y = fmaf(g, y.y, acc.y * f);
-            acc.z = fmaf(g, y.z, acc.z * f), acc.w = fmaf(g, y.w, acc.w * f);
-            mm_o = m;
-            const float n = fmaxf(mm_l, st.y);
-            ll = fmaf(st.z, fast_exp2(st.y - n), ll * fast_exp2(mm_l - n));
-            mm_l = n;
-          }
+          for (int k = 0; k < peers; ++k)
+            add_share(mm_o, mm_l, ll, acc, load_peer(sp + ROWS * DH + r * 4, k), load_peer(sp + r * DH + d, k));
           write_out(p, was_b, was_kvh, was_r0 + r, d, mm_o, mm_l, ll, acc);
         }
         cluster_sync();  // (the sums are read; a CTA that ends takes its own along)
@@ -815,84 +848,54 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   }
 }
 
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 128;
 constexpr int kRounds = 12;
 
-// Joins the shares of the group that CTA blockIdx.x of the attention began: a row's
-// statistics by a warp, its values by as many threads a column as there are, whose first
-// reads are on their way before the statistics are known.
+// Joins row blockIdx.y of the group that CTA blockIdx.x of the attention began.  A team of
+// lanes, four values each, has every kTeams'th share; statistics and values are read at
+// once, kReads shares at a time (a round trip to L2 takes 0.6 us), and the teams meet in
+// shared memory.  (Small CTAs find room beside the attention's last ones, so that all
+// wait for its end already: with 512 threads a CTA everything takes 1 to 2 us more.)
 template <int DH>
 __global__ void __launch_bounds__(kJoinThreads) page_join_kernel(const __grid_constant__ PageAttnParams p, int row_tile) {
-  constexpr int kReads = 8;
-  __shared__ float factor[16 * kMaxCtas];  // [rows][shares]
-  __shared__ float4 stat[16], sums[kJoinThreads];
-  const int warp = warp_id(), lane = lane_id();
+  constexpr int kReads = 10, kLanes = DH / 4, kTeams = kJoinThreads / kLanes;
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ float4 stats[kTeams];
+  const int team = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4, r = blockIdx.y;
   pdl_trigger();
   pdl_wait();
   const Shared g = p.shared[blockIdx.x];
-  if (g.rows == 0) return;
-  const int64_t floats = share_floats(DH, row_tile);
+  if (r >= g.rows) return;
+  const int floats = share_floats(DH, row_tile);
   const float* part = p.part + 2 * static_cast<int64_t>(blockIdx.x) * floats;
-  // (a share that begins its group is its CTA's second, one that goes on with it its first)
-  auto share = [&](int k) { return part + (2 * k + (k == 0)) * floats; };
-  const int columns = g.rows * (DH / 4), parts = kJoinThreads / columns, x = threadIdx.x;
-  const int column = x % columns, r_mine = column / (DH / 4), d = column % (DH / 4) * 4;
-  float4 z[kReads];
-  auto read = [&](int k0) {
+  float mm_o = kNone, mm_l = kNone, ll = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = team; k0 < g.shares; k0 += kReads * kTeams) {
+    float4 z[kReads], st[kReads];
 #pragma unroll
     for (int e = 0; e < kReads; ++e) {
-      const int k = x / columns + (k0 + e) * parts;
-      z[e] = k < g.shares ? __ldcg(reinterpret_cast<const float4*>(share(k) + r_mine * DH + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  };
-  const bool busy = x < columns * parts;
-  if (busy) read(0);
-  for (int r = warp; r < g.rows; r += kJoinThreads / 32) {
-    float mm_o = kNone, mm_l = kNone, ll = 0.0f;
-    for (int k = lane; k < g.shares; k += 32) {
-      const float4 st = __ldcg(reinterpret_cast<const float4*>(share(k) + row_tile * DH + r * 4));
-      factor[r * kMaxCtas + k] = st.x;
-      mm_o = fmaxf(mm_o, st.x);
-      const float m = fmaxf(mm_l, st.y);
-      ll = ll * fast_exp2(mm_l - m) + st.z * fast_exp2(st.y - m);
-      mm_l = m;
+      const int k = k0 + e * kTeams;
+      if (k >= g.shares) break;
+      // (a share that begins its group is its CTA's second, one that goes on with it its first)
+      const float* share = part + static_cast<int64_t>(2 * k + (k == 0)) * floats;
+      z[e] = __ldcg(reinterpret_cast<const float4*>(share + r * DH + d));
+      st[e] = __ldcg(reinterpret_cast<const float4*>(share + row_tile * DH + r * 4));
     }
 #pragma unroll
-    for (int k = 16; k; k >>= 1) {
-      mm_o = fmaxf(mm_o, __shfl_xor_sync(0xffffffffu, mm_o, k));
-      const float m1 = __shfl_xor_sync(0xffffffffu, mm_l, k), l1 = __shfl_xor_sync(0xffffffffu, ll, k);
-      const float m = fmaxf(mm_l, m1);
-      ll = __fadd_rn(__fmul_rn(ll, fast_exp2(mm_l - m)), __fmul_rn(l1, fast_exp2(m1 - m)));  // (the same in both lanes)
-      mm_l = m;
+    for (int e = 0; e < kReads; ++e) {
+      if (k0 + e * kTeams >= g.shares) break;
+      add_share(mm_o, mm_l, ll, acc, st[e], z[e]);
     }
-    for (int k = lane; k < g.shares; k += 32) factor[r * kMaxCtas + k] = fast_exp2(factor[r * kMaxCtas + k] - mm_o);
-    if (lane == 0) stat[r] = make_float4(mm_o, mm_l, ll, 0.0f);
+  }
+  if (team) {
+    sums[threadIdx.x] = acc;
+    if (d == 0) stats[team] = make_float4(mm_o, mm_l, ll, 0.0f);
   }
   __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (busy) {
-    for (int k0 = 0;;) {
+  if (team) return;
 #pragma unroll
-      for (int e = 0; e < kReads; ++e) {
-        const int k = x / columns + (k0 + e) * parts;
-        const float f = k < g.shares ? factor[r_mine * kMaxCtas + k] : 0.0f;
-        acc.x = fmaf(f, z[e].x, acc.x), acc.y = fmaf(f, z[e].y, acc.y);
-        acc.z = fmaf(f, z[e].z, acc.z), acc.w = fmaf(f, z[e].w, acc.w);
-      }
-      k0 += kReads;
-      if (k0 * parts >= g.shares) break;
-      read(k0);
-    }
-    sums[x] = acc;
-  }
-  __syncthreads();
-  if (x < columns) {
-    for (int k = 1; k < parts; ++k) {
-      const float4 y = sums[x + k * columns];
-      acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
-    }
-    write_out(p, g.b, g.kvh, g.r0 + r_mine, d, stat[r_mine].x, stat[r_mine].y, stat[r_mine].z, acc);
-  }
+  for (int k = 1; k < kTeams; ++k) add_share(mm_o, mm_l, ll, acc, stats[k], sums[threadIdx.x + k * kLanes]);
+  write_out(p, g.b, g.kvh, g.r0 + r, d, mm_o, mm_l, ll, acc);
 }
 
 template <int DH, int FMT, int NT, bool CLUSTER>
@@ -920,6 +923,7 @@ cudaError_t launch(const PageAttnParams& p, int sms, cudaStream_t st) {
   cfg.numAttrs = CLUSTER ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, page_attn_kernel<DH, FMT, NT, CLUSTER>, p);
   if (e != cudaSuccess || CLUSTER) return e;
+  cfg.gridDim.y = static_cast<unsigned>(std::min(p.Lq * p.G, C::ROWS));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, page_join_kernel<DH>, p, C::ROWS);
@@ -937,6 +941,7 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   p.groups = p.B * p.Hkv * tiles;
   const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * kStep)
                                   : p.c.positions) / kStep + 1;
+  p.quick = p.B <= 32 && p.groups * (p.c.positions / kStep + 3) < (int64_t{1} << 31);
   p.cluster = 1;
   while (p.cluster < 8 && p.groups * p.cluster * 2 <= kMaxCtas && p.cluster * C::WARPS < steps) p.cluster *= 2;
   const int64_t rounds = (p.groups * p.cluster + kMaxCtas - 1) / kMaxCtas * ((steps + p.cluster * C::WARPS - 1) / (p.cluster * C::WARPS));
