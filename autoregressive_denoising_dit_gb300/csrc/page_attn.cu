@@ -44,6 +44,7 @@ struct alignas(32) Shared {
 namespace {
 
 constexpr int kStep = 16;  // keys of a warp's step
+constexpr int kStart = 8;  // steps on the line that a group's start counts for
 constexpr int kCtasSm = 2;
 constexpr int kMaxCtas = 152 * kCtasSm;  // shares in the workspace
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -177,7 +178,8 @@ __device__ __forceinline__ int placed(int row, int piece) {
 struct Seq {
   int rows, n, keys;  // query rows, length, keys that may have a page
   int head, from, steps, tiles;
-  int64_t total;  // steps of all its kv heads and row tiles
+  int64_t total;  // on the line, of all its kv heads and row tiles
+  __device__ __forceinline__ int span() const { return steps + kStart; }  // a group's
 };
 
 template <int ROWS>
@@ -193,7 +195,7 @@ __device__ __forceinline__ Seq sequence(const PageAttnParams& p, int rows, int n
   s.from = from * kStep;
   s.steps = max(s.head + end - from, 1);  // (a row without keys is written too)
   s.tiles = (rows * p.G + ROWS - 1) / ROWS;
-  s.total = static_cast<int64_t>(s.steps) * s.tiles * p.Hkv;
+  s.total = static_cast<int64_t>(s.span()) * s.tiles * p.Hkv;
   return s;
 }
 
@@ -203,7 +205,8 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a / b;
 }
 
-// The line of `all` steps in `ctas` equal stretches.
+// The line of all groups (of `span` units: kStart, then a unit a step) in `ctas` equal
+// stretches.
 struct Cut {
   int64_t all, each;
   int ctas, more;
@@ -214,14 +217,14 @@ struct Cut {
     return each * cta + static_cast<int>(__fdiv_rn(static_cast<float>(more * cta), static_cast<float>(ctas)));  // (exact: < 2^17)
   }
   // A cut this near to an end of its group is moved there, so that fewer CTAs have
-  // shares of two groups.
-  __device__ __forceinline__ int near(int steps) const {
-    return static_cast<int>(min(each >> 3, static_cast<int64_t>(steps >> 2)));
+  // shares of two groups, and none has a start alone.
+  __device__ __forceinline__ int near(int span) const {
+    return max(static_cast<int>(min(each >> 3, static_cast<int64_t>(span >> 2))), kStart + 1);
   }
-  // By how much, `within` steps into a sequence of groups of `steps`.
-  __device__ __forceinline__ int moved(int64_t within, int steps) const {
-    const int rest = static_cast<int>(within - divide(within, steps) * steps), n = near(steps);
-    return rest < n ? -rest : steps - rest < n ? steps - rest : 0;
+  // By how much, `within` units into a sequence of groups of `span`.
+  __device__ __forceinline__ int moved(int64_t within, int span) const {
+    const int rest = static_cast<int>(within - divide(within, span) * span), n = near(span);
+    return rest < n ? -rest : span - rest < n ? span - rest : 0;
   }
   __device__ __forceinline__ int of(int64_t x) const { return static_cast<int>(divide((x + 1) * ctas - 1, all)); }
 };
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   if (!CLUSTER && threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
   if (p.quick) {  // a warp's worth of sequences, 32 bits
     const Seq mine = sequence<ROWS>(p, rows_b, n_b);
-    const int own = (CLUSTER ? 1 : mine.steps) * mine.tiles * p.Hkv;
+    const int own = (CLUSTER ? 1 : mine.span()) * mine.tiles * p.Hkv;
     int sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -309,14 +312,14 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       const int x = static_cast<int>(cut.begin(place_of + i));
       const unsigned hit = __ballot_sync(0xffffffffu, sum > x);
       const int at = max(__ffs(hit) - 1, 0);
-      const int first = __shfl_sync(0xffffffffu, sum - own, at), steps = __shfl_sync(0xffffffffu, mine.steps, at);
+      const int first = __shfl_sync(0xffffffffu, sum - own, at), span = __shfl_sync(0xffffffffu, mine.span(), at);
       if (i == 0) {
         b = at;
         before = first;
         s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
       }
       lo = hi;
-      hi = CLUSTER || !hit ? x : x + cut.moved(x - first, steps);
+      hi = CLUSTER || !hit ? x : x + cut.moved(x - first, span);
     }
   } else {
     int64_t all = units(sequence<ROWS>(p, rows_b, n_b));
@@ -344,8 +347,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       if (hit || x >= all) {
         const int at = max(__ffs(hit) - 1, 0);
         const int64_t first = sum0 + __shfl_sync(0xffffffffu, sum - own, at);
-        const int steps = __shfl_sync(0xffffffffu, mine.steps, at);
-        const int64_t moved = CLUSTER || !hit ? x : x + cut.moved(x - first, steps);
+        const int span = __shfl_sync(0xffffffffu, mine.span(), at);
+        const int64_t moved = CLUSTER || !hit ? x : x + cut.moved(x - first, span);
         if (begun) {
           hi = moved;
           break;
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
   const int sinks = p.window ? p.sinks : 0;
   const char *k_mine = nullptr, *v_mine = nullptr, *s_mine = nullptr;
-  int kvh = 0, r0 = 0, n_rows = 0, step0 = 0, step1 = 0, slot = 0;
+  int kvh = 0, r0 = 0, n_rows = 0, step0 = 0, step1 = 0, taken = 0, slot = 0;
   int all_end = 0, any_end = 0, all_first = 0, any_first = 0;
   uint32_t found = 0;  // a bit for each step under way: whether key lane % 16 is there
   // Where the keys of the warp's next steps are: in lane 2 i + h the half h of number i
@@ -470,9 +473,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         s = sequence<ROWS>(p, rows, page_length(p, b, rows));
       }
       const int64_t within = lo - before;
-      const int group = static_cast<int>(CLUSTER ? within : divide(within, s.steps));
-      step0 = CLUSTER ? 0 : static_cast<int>(within - static_cast<int64_t>(group) * s.steps);
-      step1 = CLUSTER ? s.steps : static_cast<int>(min(static_cast<int64_t>(s.steps), step0 + (hi - lo)));
+      const int group = static_cast<int>(CLUSTER ? within : divide(within, s.span()));
+      const int at = CLUSTER ? 0 : static_cast<int>(within - static_cast<int64_t>(group) * s.span());
+      taken = CLUSTER ? 1 : static_cast<int>(min(static_cast<int64_t>(s.span() - at), hi - lo));
+      step0 = max(at - kStart, 0);
+      step1 = CLUSTER ? s.steps : at + taken - kStart;
       kvh = s.tiles == 1 ? group : group / s.tiles;
       r0 = (group - kvh * s.tiles) * ROWS;
       n_rows = min(s.rows * p.G - r0, ROWS);
@@ -840,11 +845,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     was_b = b, was_kvh = kvh, was_r0 = r0, was_rows = n_rows;
     was_slot = step0 == 0;
     if (!CLUSTER && split && was_slot && threadIdx.x == 0) {
-      const int near = max(cut.near(s.steps) - 1, 0);
-      const int shares = cut.of(lo + s.steps - 1 - near) - static_cast<int>(blockIdx.x) + 1;
+      // (the last cut that is not moved to the group's end)
+      const int shares = cut.of(lo + s.span() - cut.near(s.span())) - static_cast<int>(blockIdx.x) + 1;
       p.shared[blockIdx.x] = Shared{n_rows, shares, b, kvh, r0};
     }
-    lo += CLUSTER ? 1 : step1 - step0;
+    lo += taken;
   }
 }
 
@@ -941,7 +946,7 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   p.groups = p.B * p.Hkv * tiles;
   const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * kStep)
                                   : p.c.positions) / kStep + 1;
-  p.quick = p.B <= 32 && p.groups * (p.c.positions / kStep + 3) < (int64_t{1} << 31);
+  p.quick = p.B <= 32 && p.groups * (p.c.positions / kStep + 3 + kStart) < (int64_t{1} << 31);
   p.cluster = 1;
   while (p.cluster < 8 && p.groups * p.cluster * 2 <= kMaxCtas && p.cluster * C::WARPS < steps) p.cluster *= 2;
   const int64_t rounds = (p.groups * p.cluster + kMaxCtas - 1) / kMaxCtas * ((steps + p.cluster * C::WARPS - 1) / (p.cluster * C::WARPS));
