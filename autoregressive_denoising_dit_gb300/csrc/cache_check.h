@@ -160,12 +160,18 @@ inline bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes
 
 inline Strides3 strides3(const int64_t* s) { return Strides3{s[0], s[1], s[2]}; }
 
-inline bool multiple16(const void* ptr, const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int size) {
+// Whether a tensor's base and the strides that are stepped are multiples of `bytes`
+// (a power of two).
+inline bool multiple_of(int bytes, const void* ptr, const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int size) {
   const int64_t n[3] = {n0, n1, n2};
-  if (reinterpret_cast<uintptr_t>(ptr) & 15) return false;
+  if (reinterpret_cast<uintptr_t>(ptr) & (bytes - 1)) return false;
   for (int i = 0; i < 3; ++i)
-    if (n[i] > 1 && (s[i] * size) % 16 != 0) return false;
+    if (n[i] > 1 && (s[i] * size) % bytes != 0) return false;
   return true;
+}
+
+inline bool multiple16(const void* ptr, const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int size) {
+  return multiple_of(16, ptr, s, n0, n1, n2, size);
 }
 
 // A launch that may begin while the kernel before it ends (it waits for that

@@ -148,12 +148,15 @@ __device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-// Copies of 16 or 8 bytes that do not wait; `bytes` 0 leaves zeros.
+// Copies that do not wait; `bytes` 0 leaves zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -378,6 +381,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   const uint32_t value_at = C::RB == 64 ? placed<C::RB>(2 * four, quad / 2) + quad % 2 * 8 : placed<C::RB>(2 * four, quad);
   auto flip = [](int i) -> uint32_t { return C::RB == 256 ? (i / 2 * 4 + i % 2 * 2) * 16 : i * 64; };
   const bool in_head = lane % C::LPR * 16 < p.dh * C::ES;  // the piece that this lane copies
+  const int second = lane % C::LPR * 16 + 8 < p.dh * C::ES ? 8 : 0;  // bytes of its second half
   const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
   const int sinks = p.window ? p.sinks : 0;
   const char *k_mine = nullptr, *v_mine = nullptr, *s_mine = nullptr;
@@ -425,8 +429,16 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 #pragma unroll
           for (int i = 0; i < 8 / C::RPC; ++i) {
             const uint32_t to = ring + ((dst + copied) ^ flip(i)) + (h * 8 / C::RPC + i) * 512;
-            copy16(to, k + static_cast<uint64_t>(p.kl) * (i * C::RPC));
-            copy16(to + C::KV, v + static_cast<uint64_t>(p.vl) * (i * C::RPC));
+            const char *from_k = k + static_cast<uint64_t>(p.kl) * (i * C::RPC), *from_v = v + static_cast<uint64_t>(p.vl) * (i * C::RPC);
+            if (!C::kScaled || !p.halves) {
+              copy16(to, from_k);
+              copy16(to + C::KV, from_v);
+            } else {
+              copy8(to, from_k, 8);
+              copy8(to + 8, from_k + second, second);
+              copy8(to + C::KV, from_v, 8);
+              copy8(to + C::KV + 8, from_v + second, second);
+            }
           }
         }
       }
@@ -450,8 +462,18 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       const int page = __shfl_sync(0xffffffffu, at.page, key), row = __shfl_sync(0xffffffffu, at.row, key) - lane / C::LPR;
       const uint32_t to = ring + dst + placed<C::RB>(key, lane % C::LPR);
       const int bytes = page >= 0 && in_head ? 16 : 0;
-      copy16(to, bytes ? k_mine + offset(p.kb, 0, page, 0) + static_cast<int64_t>(p.kl) * row : static_cast<const char*>(c.k), bytes);
-      copy16(to + C::KV, bytes ? v_mine + offset(p.vb, 0, page, 0) + static_cast<int64_t>(p.vl) * row : static_cast<const char*>(c.v), bytes);
+      const char* from_k = bytes ? k_mine + offset(p.kb, 0, page, 0) + static_cast<int64_t>(p.kl) * row : static_cast<const char*>(c.k);
+      const char* from_v = bytes ? v_mine + offset(p.vb, 0, page, 0) + static_cast<int64_t>(p.vl) * row : static_cast<const char*>(c.v);
+      if (!C::kScaled || !p.halves) {
+        copy16(to, from_k, bytes);
+        copy16(to + C::KV, from_v, bytes);
+      } else {
+        const int more = bytes ? second : 0;
+        copy8(to, from_k, bytes / 2);
+        copy8(to + 8, from_k + more, more);
+        copy8(to + C::KV, from_v, bytes / 2);
+        copy8(to + C::KV + 8, from_v + more, more);
+      }
     }
     if constexpr (C::kScaled)
       copy4(ring + dst + 2 * C::KV + lane * 4, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);

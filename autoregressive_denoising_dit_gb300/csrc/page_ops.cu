@@ -453,7 +453,7 @@ int page_rows_call(const psv_page_cache* c, const psv_page_rows* r, const void* 
   p.starts = r->starts, p.lens = r->lens;
   const int es = page_esize(c->format);
   auto eights = [&](const void* at, const int64_t* s) {  // eight stored values as one access
-    return (reinterpret_cast<uintptr_t>(at) & (8 * es - 1)) == 0 && (s[0] | s[1] | s[2]) % 8 == 0;
+    return multiple_of(8 * es, at, s, c->n_pages, c->page_size, c->Hkv, es);
   };
   const bool vec = c->dh % 8 == 0 && multiple16(k, r->k_stride, c->B, r->L, c->Hkv, size) &&
                    multiple16(v, r->v_stride, c->B, r->L, c->Hkv, size) && eights(c->k_pages, c->k_stride) &&
@@ -490,7 +490,8 @@ PageAttnParams page_attn_params(const psv_page_cache* c, const psv_page_query* q
   PageAttnParams p{};
   p.c = page_cache_dev(c);
   p.B = c->B, p.Hq = q->Hq, p.Hkv = c->Hkv, p.G = q->Hq / c->Hkv, p.dh = c->dh, p.Lq = q->Lq;
-  p.causal = q->causal != 0, p.window = q->window, p.sinks = q->sinks, p.append = q->append != 0;
+  // (a window over every position that rows may stand at is none)
+  p.causal = q->causal != 0, p.window = q->window < (1 << 30) + (1 << 21) ? q->window : (1 << 30) + (1 << 21), p.sinks = q->sinks, p.append = q->append != 0;
   p.bf16 = q->dtype == PSV_DTYPE_BF16;
   p.scale = q->scale > 0 ? q->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c->dh)));
   p.softcap = q->softcap;
@@ -499,8 +500,8 @@ PageAttnParams page_attn_params(const psv_page_cache* c, const psv_page_query* q
   return p;
 }
 
-// Whether heads are made of 16-byte pieces in the pages (and 16-bit rows).
-bool page_attn_pieces(const psv_page_cache* c) { return c->dh <= 128 && c->dh * page_esize(c->format) % 16 == 0; }
+// Whether heads are made of eight values each, for the tensor-core kernel.
+bool page_attn_pieces(const psv_page_cache* c) { return c->dh <= 128 && c->dh % 8 == 0; }
 
 size_t page_scratch(const psv_page_cache* c, const PageAttnParams& p) {
   return page_attn_pieces(c) ? page_attn_scratch(p) : 256;
@@ -555,8 +556,10 @@ PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q,
   auto small = [](const int64_t* st, int size) { return st[0] * size < int64_t{1} << 32 && st[1] * size < int64_t{1} << 32; };
   if (page_attn_pieces(c) && small(c->k_stride, es) && small(c->v_stride, es) && (es == 2 || small(c->scale_stride, 4)) && multiple16(x, q->q_stride, c->B, q->Lq, q->Hq, 2) &&
       multiple16(o, q->o_stride, c->B, q->Lq, q->Hq, 2) &&
-      multiple16(c->k_pages, c->k_stride, c->n_pages, c->page_size, c->Hkv, es) &&
-      multiple16(c->v_pages, c->v_stride, c->n_pages, c->page_size, c->Hkv, es)) {
+      multiple_of(es * 8, c->k_pages, c->k_stride, c->n_pages, c->page_size, c->Hkv, es) &&
+      multiple_of(es * 8, c->v_pages, c->v_stride, c->n_pages, c->page_size, c->Hkv, es)) {
+    p.halves = !(c->dh * es % 16 == 0 && multiple16(c->k_pages, c->k_stride, c->n_pages, c->page_size, c->Hkv, es) &&
+                 multiple16(c->v_pages, c->v_stride, c->n_pages, c->page_size, c->Hkv, es));
     int sms = 0;
     if (int e = cuda_status(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "device")) return e;
     if (p.softcap > 0) set_cap_form(p.cap, p.scale, p.softcap);

@@ -430,3 +430,127 @@ def test_nothing_to_do_and_no_lse(P):
     o = torch.zeros_like(q)
     P.psv_page_attention(cache.desc(), query, at(q), at(o), 0, at(w), w.numel(), stream())
     assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
+@pytest.mark.parametrize("f", ["e4m3", "i8"])
+def test_pages_aligned_to_eight_bytes(P, f, width):
+    """Heads of 128 whose pages begin, and whose rows lie, at odd multiples of eight bytes."""
+    c = dict(B=2, Lq=3, Lk=210, Hq=4, Hkv=2, dh=128, page=16, causal=True, lens=[210, 37])
+    cache, q, (k, v), lens, total, rows = attention_case(P, c, "bf16", f, width=width)
+    ref = reference(cache, c, q, k, v, total, rows)
+    n, h, r, d = cache.k.shape
+    for name in ("k", "v"):
+        wide = torch.full((n * h * r * 136 + 16,), 0x7F, device="cuda", dtype=torch.uint8)[8:8 + n * h * r * 136].view(n, h, r, 136)
+        wide[..., :128] = getattr(cache, name)
+        setattr(cache, name, wide[..., :128])
+    check(*run_attention(P, c, cache, q, lens, rows, "bf16"), ref, rows, 9.0)
+
+
+@pytest.mark.parametrize("dh", [64, 80])
+def test_windows_and_lengths_at_the_ends_of_their_range(P, dh):
+    c = dict(B=2, Lq=4, Lk=100, Hq=2, Hkv=1, dh=dh, page=16, causal=True, window=2**31 - 1, sinks=2**31 - 1, lens=[100, 2])
+    cache, q, (k, v), lens, total, rows = attention_case(P, c, "f16", "i8")
+    ref = reference(cache, dict(c, window=0, sinks=0), q, k, v, total, rows)
+    check(*run_attention(P, c, cache, q, lens, rows, "f16"), ref, rows, 9.0)
+    # lengths beyond what there is are cut to it; negative ones are nothing
+    o, lse = run_attention(P, dict(c, window=0, sinks=0, rows=[2**31 - 1, -5]), cache, q, [2**31 - 1, 50], [2**31 - 1, -5], "f16")
+    full = cache.max_pages * 16
+    assert (o[1] == 9.0).all() and (lse[1] == 9.0).all()
+    pos = torch.arange(full, device="cuda")
+    e = cache.table[0].long()[pos // 16]
+    cache.ks[e, :, pos % 16] = torch.nan_to_num(cache.ks[e, :, pos % 16], 0)  # rows behind the written ones: zeros
+    cache.vs[e, :, pos % 16] = torch.nan_to_num(cache.vs[e, :, pos % 16], 0)
+    o, lse = run_attention(P, dict(c, window=0, sinks=0, rows=[9, -5]), cache, q, [2**31 - 1, 50], [9, -5], "f16")
+    pad = torch.zeros(2, full - 100, 1, dh, device="cuda", dtype=torch.float64)
+    ref = reference(cache, dict(c, window=0, sinks=0), q, torch.cat([k, pad], 1), torch.cat([v, pad], 1), [full, 50], [4, 0])
+    check(o, lse, ref, [4, 0], 9.0)
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+sys.path.insert(0, {tests!r})
+import torch
+from test_gpu_page_edges import Decoder
+from autoregressive_denoising_dit_gb300 import _psv as P
+d = Decoder(P, f={f!r}, Hq={Hq}, dh={dh}, max_pages={max_pages})
+d.feed(torch.Generator(device="cuda").manual_seed(1))
+x = torch.zeros(3, 4, 2, {dh}, device="cuda", dtype=torch.bfloat16)
+r = P.page_rows(P.PSV_DTYPE_BF16, x.shape)
+y = torch.zeros_like(x)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    d.step()
+    P.psv_page_read(d.desc, r, x.data_ptr(), y.data_ptr(), torch.cuda.current_stream().cuda_stream)
+d.before.zero_()
+d.feed(torch.Generator(device="cuda").manual_seed(1))
+g.replay()
+torch.cuda.synchronize()
+o, lse, kx = d.o.clone(), d.lse.clone(), x.clone()
+d.before.zero_()
+d.feed(torch.Generator(device="cuda").manual_seed(1))
+d.step()
+torch.cuda.synchronize()
+assert torch.equal(o, d.o) and torch.equal(lse, d.lse) and float(o.abs().sum()) > 0 and float(kx[:, 0].abs().sum()) > 0
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("kw", [dict(f="e4m3", Hq=8, dh=128, max_pages=12), dict(f="i8", Hq=24, dh=64, max_pages=3000),
+                                dict(f="bf16", Hq=2, dh=128, max_pages=3000), dict(f="e4m3", Hq=4, dh=20, max_pages=12)],
+                         ids=lambda k: f"{k['f']}-{k['Hq']}-{k['dh']}-{k['max_pages']}")
+def test_a_process_may_begin_with_a_capture(kw):
+    """The first calls of a process, before any kernel is loaded, go into a graph."""
+    import os
+    import subprocess
+    import sys
+
+    tests = os.path.dirname(os.path.abspath(__file__))
+    src = FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests, **kw)
+    r = subprocess.run([sys.executable, "-c", src], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-1000:] + r.stderr[-3000:]
+
+
+def test_calls_from_four_threads(P):
+    """Calls at the same time, each thread with its own stream, workspace and outputs; errors stay with their thread."""
+    import threading
+
+    kinds = [dict(f="e4m3"), dict(f="i8", Hq=24, max_pages=300), dict(f="bf16", max_pages=300), dict(f="e4m3", dh=64, Hq=2)]
+    bad = []
+    lens = ints([20, 70, 150])
+
+    def made(kw):
+        d = Decoder(P, **kw)
+        x = torch.randn(3, 150, 2, d.k.shape[3], device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+        P.psv_page_write(d.desc, P.page_rows(P.PSV_DTYPE_BF16, x.shape, lens=at(lens)), at(x), at(x), stream())
+        d.before.copy_(lens)
+        d.feed(torch.Generator(device="cuda").manual_seed(3))
+        return d
+
+    want, got = [made(kw) for kw in kinds], [made(kw) for kw in kinds]
+    for d in want:
+        for _ in range(25):
+            d.step()
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for k in range(25):
+                    got[i].step()
+                    if k % 5 == i:
+                        with pytest.raises(P.PSVError, match=f"scratch of {i} bytes"):
+                            P.psv_page_attention(got[i].desc, got[i].query, at(got[i].q), at(got[i].o), 0, at(got[i].scratch), i, stream())
+                torch.cuda.current_stream().synchronize()
+            assert torch.equal(got[i].o, want[i].o) and torch.equal(got[i].lse, want[i].lse)
+        except BaseException as e:  # noqa: BLE001 (handed to the test's thread)
+            bad.append((i, e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad

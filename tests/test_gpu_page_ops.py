@@ -350,8 +350,13 @@ ATTN = [
     dict(B=2, Lq=1, Lk=777, Hq=3, Hkv=3, dh=80, page=24),
     dict(B=2, Lq=2, Lk=555, Hq=4, Hkv=2, dh=32, page=7, causal=True),
     dict(B=2, Lq=1, Lk=130, Hq=4, Hkv=2, dh=128, page=1),
-    dict(B=2, Lq=3, Lk=230, Hq=4, Hkv=2, dh=40, page=30, causal=True),           # general kernel (8-bit pages)
+    dict(B=2, Lq=3, Lk=230, Hq=4, Hkv=2, dh=40, page=30, causal=True),           # rows of 8-byte pieces
+    dict(B=2, Lq=1, Lk=630, Hq=12, Hkv=2, dh=72, page=64),
+    dict(B=1, Lq=3, Lk=410, Hq=8, Hkv=2, dh=120, page=16, causal=True, window=300, missing=[(0, 13)]),
+    dict(B=1, Lq=1, Lk=130, Hq=2, Hkv=2, dh=8, page=64),
+    dict(B=2, Lq=2, Lk=90, Hq=2, Hkv=2, dh=24, page=9, causal=True),
     dict(B=1, Lq=2, Lk=150, Hq=2, Hkv=1, dh=21, page=64, causal=True),           # general kernel
+    dict(B=1, Lq=1, Lk=100, Hq=2, Hkv=1, dh=100, page=32, window=40, sinks=5, missing=[(0, 2)], cap=3.0),  # general kernel
     dict(B=1, Lq=1, Lk=200, Hq=2, Hkv=1, dh=256, page=64),
     dict(B=2, Lq=1, Lk=900, Hq=4, Hkv=2, dh=128, page=64, causal=True, window=200, sinks=20),
     dict(B=2, Lq=5, Lk=900, Hq=2, Hkv=2, dh=128, page=48, causal=True, window=33, sinks=3, lens=[900, 20]),
