@@ -289,8 +289,6 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   const int worker = rank * kWarps + warp, workers = peers * kWarps;
   auto units = [&](const Seq& x) { return CLUSTER ? static_cast<int64_t>(x.tiles) * p.Hkv : x.total; };
   // The line's length, this CTA's stretch [lo, hi) of it, and the sequence that it begins in.
-  auto rows_at = [&](int b) { return b < p.B ? page_rows(p, b) : 0; };
-  int rows_b = rows_at(lane), n_b = lane < p.B ? page_length(p, lane, rows_b) : 0;
   const int place_of = blockIdx.x / peers, places = gridDim.x / peers;
   int64_t lo = 0, hi = 0;
   int b = 0;
@@ -298,9 +296,24 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   Seq s;
   Cut cut(0, 0);
   if (!CLUSTER && threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
-  if (p.quick) {  // a warp's worth of sequences, 32 bits
-    const Seq mine = sequence<ROWS>(p, rows_b, n_b);
-    const int own = (CLUSTER ? 1 : mine.span()) * mine.tiles * p.Hkv;
+  auto sequence_at = [&](int k) {
+    const int rows = page_rows(p, k);
+    return sequence<ROWS>(p, rows, page_length(p, k, rows));
+  };
+  if (p.quick) {  // up to eight sequences a lane, 32 bits
+    const int each = (p.B + 31) / 32;
+    auto units32 = [&](const Seq& x) { return (CLUSTER ? 1 : x.span()) * x.tiles * p.Hkv; };
+    int own = 0, rows_b = 0, n_b = 0;
+    if (lane * each < p.B) {
+      rows_b = page_rows(p, lane * each);
+      n_b = page_length(p, lane * each, rows_b);
+      own = units32(sequence<ROWS>(p, rows_b, n_b));
+    }
+    if (each > 1) {
+#pragma unroll 1
+      for (int k = lane * each + 1; k < min((lane + 1) * each, p.B); ++k) own += units32(sequence_at(k));
+      __syncwarp();
+    }
     int sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -314,22 +327,27 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     for (int i = 0; i < 2; ++i) {
       const int x = static_cast<int>(cut.begin(place_of + i));
       const unsigned hit = __ballot_sync(0xffffffffu, sum > x);
-      const int at = max(__ffs(hit) - 1, 0);
-      const int first = __shfl_sync(0xffffffffu, sum - own, at), span = __shfl_sync(0xffffffffu, mine.span(), at);
-      if (i == 0) {
-        b = at;
-        before = first;
-        s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
-      }
       lo = hi;
-      hi = CLUSTER || !hit ? x : x + cut.moved(x - first, span);
+      hi = x;
+      if (!hit) break;  // (behind all)
+      const int at = __ffs(hit) - 1;
+      int k = at * each, first = __shfl_sync(0xffffffffu, sum - own, at);
+      Seq y;
+      if (each == 1) {
+        y = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
+      } else {
+        y = sequence_at(k);
+        while (first + units32(y) <= x) {
+          first += units32(y);
+          y = sequence_at(++k);
+        }
+      }
+      if (!CLUSTER) hi = x + cut.moved(x - first, y.span());
+      if (i == 0) b = k, before = first, s = y;
     }
   } else {
-    int64_t all = units(sequence<ROWS>(p, rows_b, n_b));
-    for (int k = lane + 32; k < p.B; k += 32) {
-      const int rows = page_rows(p, k);
-      all += units(sequence<ROWS>(p, rows, page_length(p, k, rows)));
-    }
+    int64_t all = 0;
+    for (int k = lane; k < p.B; k += 32) all += units(sequence_at(k));
 #pragma unroll
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     cut = Cut(all, static_cast<int>(min(static_cast<int64_t>(places), CLUSTER ? all : (all + kWarps - 1) / kWarps)));
@@ -337,8 +355,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     int64_t sum0 = 0, x = cut.begin(place_of);
     bool begun = false;
     for (int b0 = 0;;) {
-      const Seq mine = sequence<ROWS>(p, rows_b, n_b);
-      const int64_t own = units(mine);
+      int64_t own = 0;
+      if (b0 + lane < p.B) own = units(sequence_at(b0 + lane));
       int64_t sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -350,8 +368,12 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       if (hit || x >= all) {
         const int at = max(__ffs(hit) - 1, 0);
         const int64_t first = sum0 + __shfl_sync(0xffffffffu, sum - own, at);
-        const int span = __shfl_sync(0xffffffffu, mine.span(), at);
-        const int64_t moved = CLUSTER || !hit ? x : x + cut.moved(x - first, span);
+        Seq y;
+        int64_t moved = x;
+        if (hit) {
+          y = sequence_at(b0 + at);
+          if (!CLUSTER) moved += cut.moved(x - first, y.span());
+        }
         if (begun) {
           hi = moved;
           break;
@@ -359,14 +381,13 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         begun = true;
         b = b0 + at;
         before = first;
-        s = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
+        s = y;
         lo = moved;
         x = cut.begin(place_of + 1);
         continue;  // (its end may lie in the same sequences)
       }
       sum0 += __shfl_sync(0xffffffffu, sum, 31);
       b0 += 32;
-      rows_b = rows_at(b0 + lane), n_b = b0 + lane < p.B ? page_length(p, b0 + lane, rows_b) : 0;
     }
   }
 
@@ -381,7 +402,6 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   const uint32_t value_at = C::RB == 64 ? placed<C::RB>(2 * four, quad / 2) + quad % 2 * 8 : placed<C::RB>(2 * four, quad);
   auto flip = [](int i) -> uint32_t { return C::RB == 256 ? (i / 2 * 4 + i % 2 * 2) * 16 : i * 64; };
   const bool in_head = lane % C::LPR * 16 < p.dh * C::ES;  // the piece that this lane copies
-  const int second = lane % C::LPR * 16 + 8 < p.dh * C::ES ? 8 : 0;  // bytes of its second half
   const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
   const int sinks = p.window ? p.sinks : 0;
   const char *k_mine = nullptr, *v_mine = nullptr, *s_mine = nullptr;
@@ -419,7 +439,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         half[h].row = __shfl_sync(0xffffffffu, place.row, 2 * (number % 16) + h);
       }
     }
-    if (eights && every && half[0].page >= 0 && half[1].page >= 0) {
+    if (eights && every && !p.halves && half[0].page >= 0 && half[1].page >= 0) {
       found |= 1;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -429,16 +449,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 #pragma unroll
           for (int i = 0; i < 8 / C::RPC; ++i) {
             const uint32_t to = ring + ((dst + copied) ^ flip(i)) + (h * 8 / C::RPC + i) * 512;
-            const char *from_k = k + static_cast<uint64_t>(p.kl) * (i * C::RPC), *from_v = v + static_cast<uint64_t>(p.vl) * (i * C::RPC);
-            if (!C::kScaled || !p.halves) {
-              copy16(to, from_k);
-              copy16(to + C::KV, from_v);
-            } else {
-              copy8(to, from_k, 8);
-              copy8(to + 8, from_k + second, second);
-              copy8(to + C::KV, from_v, 8);
-              copy8(to + C::KV + 8, from_v + second, second);
-            }
+            copy16(to, k + static_cast<uint64_t>(p.kl) * (i * C::RPC));
+            copy16(to + C::KV, v + static_cast<uint64_t>(p.vl) * (i * C::RPC));
           }
         }
       }
@@ -468,7 +480,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         copy16(to, from_k, bytes);
         copy16(to + C::KV, from_v, bytes);
       } else {
-        const int more = bytes ? second : 0;
+        const int more = bytes && lane % C::LPR * 16 + 8 < p.dh ? 8 : 0;  // bytes of the second half
         copy8(to, from_k, bytes / 2);
         copy8(to + 8, from_k + more, more);
         copy8(to + C::KV, from_v, bytes / 2);
@@ -490,9 +502,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       // ---- the next group: its first keys and its queries are on their way before the last one is joined
       while (lo >= before + units(s)) {
         before += units(s);
-        ++b;
-        const int rows = page_rows(p, b);
-        s = sequence<ROWS>(p, rows, page_length(p, b, rows));
+        s = sequence_at(++b);
       }
       const int64_t within = lo - before;
       const int group = static_cast<int>(CLUSTER ? within : divide(within, s.span()));
@@ -968,7 +978,7 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   p.groups = p.B * p.Hkv * tiles;
   const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * kStep)
                                   : p.c.positions) / kStep + 1;
-  p.quick = p.B <= 32 && p.groups * (p.c.positions / kStep + 3 + kStart) < (int64_t{1} << 31);
+  p.quick = p.B <= 256 && p.groups * (p.c.positions / kStep + 3 + kStart) < (int64_t{1} << 31);
   p.cluster = 1;
   while (p.cluster < 8 && p.groups * p.cluster * 2 <= kMaxCtas && p.cluster * C::WARPS < steps) p.cluster *= 2;
   const int64_t rounds = (p.groups * p.cluster + kMaxCtas - 1) / kMaxCtas * ((steps + p.cluster * C::WARPS - 1) / (p.cluster * C::WARPS));
