@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     const int rows = page_rows(p, k);
     return sequence<ROWS>(p, rows, page_length(p, k, rows));
   };
-  if (p.quick) {  // up to eight sequences a lane, 32 bits
+  if (p.quick) {  // up to 32 sequences a lane, 32 bits
     const int each = (p.B + 31) / 32;
     auto units32 = [&](const Seq& x) { return (CLUSTER ? 1 : x.span()) * x.tiles * p.Hkv; };
     int own = 0, rows_b = 0, n_b = 0;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       own = units32(sequence<ROWS>(p, rows_b, n_b));
     }
     if (each > 1) {
-#pragma unroll 1
+#pragma unroll 4
       for (int k = lane * each + 1; k < min((lane + 1) * each, p.B); ++k) own += units32(sequence_at(k));
       __syncwarp();
     }
@@ -336,11 +336,23 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       if (each == 1) {
         y = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
       } else {
-        y = sequence_at(k);
-        while (first + units32(y) <= x) {
-          first += units32(y);
-          y = sequence_at(++k);
+        // lane by lane the sequences of lane `at`
+        int rows = 0, n = 0, mine = 0;
+        if (lane < each && k + lane < p.B) {
+          rows = page_rows(p, k + lane);
+          n = page_length(p, k + lane, rows);
+          mine = units32(sequence<ROWS>(p, rows, n));
         }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += up;
+        }
+        const int in = __ffs(__ballot_sync(0xffffffffu, first + upto > x)) - 1;
+        first += __shfl_sync(0xffffffffu, upto - mine, in);
+        k += in;
+        y = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows, in), __shfl_sync(0xffffffffu, n, in));
       }
       if (!CLUSTER) hi = x + cut.moved(x - first, y.span());
       if (i == 0) b = k, before = first, s = y;
@@ -978,7 +990,7 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   p.groups = p.B * p.Hkv * tiles;
   const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * kStep)
                                   : p.c.positions) / kStep + 1;
-  p.quick = p.B <= 256 && p.groups * (p.c.positions / kStep + 3 + kStart) < (int64_t{1} << 31);
+  p.quick = p.B <= 1024 && p.groups * (p.c.positions / kStep + 3 + kStart) < (int64_t{1} << 31);
   p.cluster = 1;
   while (p.cluster < 8 && p.groups * p.cluster * 2 <= kMaxCtas && p.cluster * C::WARPS < steps) p.cluster *= 2;
   const int64_t rounds = (p.groups * p.cluster + kMaxCtas - 1) / kMaxCtas * ((steps + p.cluster * C::WARPS - 1) / (p.cluster * C::WARPS));

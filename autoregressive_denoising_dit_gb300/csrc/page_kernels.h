@@ -67,7 +67,7 @@ struct PageAttnParams {
   float* lse;  // or null
   const int32_t *q_lens, *k_lens;
   int cluster;            // page_attn.cu: CTAs that share a group without cutting it
-  int quick;              // at most 256 sequences and 2^31 steps
+  int quick;              // at most 1024 sequences and 2^31 steps
   int64_t groups;         // kv heads and tiles of rows of all sequences, at most
   Shared* shared;  // page_attn.cu: the groups that several CTAs share
   float* part;            // their shares

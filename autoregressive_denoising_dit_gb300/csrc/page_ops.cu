@@ -23,8 +23,8 @@ int page_esize(int format) { return scaled(format) ? 1 : 2; }
 struct PageRowsParams {
   PageCacheDev c;
   int L, H, dh, lanes;  // lanes of a head's row (log2, at least 2): 8 values each
-  int heads;            // of a thread, at most kHeads
-  FastDiv by_groups;    // groups of heads a token
+  int heads, tokens;    // of a thread, at most kRows rows in all
+  FastDiv by_groups;    // groups of heads a token (one where there are several tokens)
   Strides3 xs[2];
   void* x[2];  // k, v
   const int32_t *starts, *lens;
@@ -152,44 +152,77 @@ struct Eight {
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kHeads = 4;
+constexpr int kRows = 4;
 
-// A token's group of heads belongs to 2^lanes threads of a warp, eight values of each
-// head's row, which find the rows' largest sizes by shuffles; the rows' divisions are
-// made by a lane each.  grid (tokens x groups, sequence, key or value).  A thread's
-// first reads do not wait for the lengths: rows not in use are read too.
-// Memory-bound where large: @W@
-template <class T, int FMT, bool VEC>
+// A row (a head of a token) belongs to 2^lanes threads of a warp, eight values each; a
+// thread has up to four heads of a token, or (MANY) where there are one or two heads of
+// four or two tokens `step` apart.
+template <bool MANY>
+struct RowMap {
+  uint32_t i, step;  // first token
+  int h0, heads, lane;
+  __device__ __forceinline__ explicit RowMap(const PageRowsParams& p) {
+    const uint32_t each = kRowThreads >> p.lanes;
+    lane = threadIdx.x & ((1 << p.lanes) - 1);
+    if constexpr (MANY) {
+      i = blockIdx.x * each * p.tokens + (threadIdx.x >> p.lanes), step = each;
+      h0 = 0, heads = p.H;
+    } else {
+      const uint32_t r = blockIdx.x * each + (threadIdx.x >> p.lanes);
+      i = p.by_groups.div(r), step = 0;
+      h0 = static_cast<int>(r - i * p.by_groups.d) * p.heads;
+      heads = min(p.heads, p.H - h0);
+    }
+  }
+  // Token and head of the thread's row k (k < heads x tokens).
+  __device__ __forceinline__ uint32_t token(int k) const { return MANY ? i + (heads == 1 ? k : k / 2) * step : i; }
+  __device__ __forceinline__ int head(int k) const { return !MANY ? k : heads == 1 ? 0 : k % 2; }
+};
+
+// Rows find their largest size by shuffles, and their divisions are made by a lane each.
+// grid (tokens x groups of heads, sequence, key or value).  The first reads do not wait
+// for the lengths: rows not in use are read too.
+// Memory-bound where large: 12480 rows x 40 heads of 128 in f32 to 8 bits 91 us (7.1 TB/s),
+// in bf16 65 us (5.9); four sequences of 1560 rows x 12 heads in bf16 13 us.
+template <class T, int FMT, bool VEC, bool MANY>
 __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
   const int b = blockIdx.y, kv = blockIdx.z;
-  const int lane = threadIdx.x & ((1 << p.lanes) - 1), d = lane * 8;
-  const uint32_t r = blockIdx.x * (kRowThreads >> p.lanes) + (threadIdx.x >> p.lanes), i = p.by_groups.div(r);
-  const int h0 = static_cast<int>(r - i * p.by_groups.d) * p.heads, heads = min(p.heads, p.H - h0);
+  const RowMap<MANY> m(p);
+  const int lane = m.lane, d = lane * 8, rows = MANY ? m.heads * p.tokens : m.heads;
   pdl_trigger();
   pdl_wait();
   const Strides3& xs = p.xs[kv];
-  Eight<T> in[kHeads];
-  if (i < static_cast<uint32_t>(p.L) && d < p.dh) {
-    const T* x = static_cast<const T*>(p.x[kv]) + b * xs.b + i * xs.l + h0 * xs.h + d;
+  Eight<T> in[kRows];
+  const T* x = static_cast<const T*>(p.x[kv]) + b * xs.b + m.h0 * xs.h + d;
+  if (!MANY) x += m.i * xs.l;
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k, x += xs.h)
-      if (k < heads) {
-        if (VEC) in[k].load(x);
-        else in[k].load(x, p.dh - d);
-      }
-  }
+  for (int k = 0; k < kRows; ++k, x += MANY ? 0 : xs.h)
+    if (k < rows && m.token(k) < static_cast<uint32_t>(p.L) && d < p.dh) {
+      const T* from = MANY ? x + m.token(k) * xs.l + m.head(k) * xs.h : x;
+      if (VEC) in[k].load(from);
+      else in[k].load(from, p.dh - d);
+    }
   const int n = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
-  PageRow at{-1, 0};
-  if (i < static_cast<uint32_t>(n)) at = page_row(p.c, b, static_cast<int64_t>(p.starts ? p.starts[b] : 0) + i);
-  float turn[kHeads];
-  if constexpr (F::kScaled) {
-    uint32_t size[kHeads];
+  const int start = p.starts ? p.starts[b] : 0;
+  PageRow at[kRows];
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k) size[k] = k < heads && d < p.dh ? in[k].size() : 0;
+  for (int k = 0; k < kRows; ++k) {
+    if (k && (!MANY || m.token(k) == m.token(k - 1))) {
+      at[k] = at[k - 1];
+      continue;
+    }
+    at[k] = PageRow{-1, 0};
+    if (k < rows && m.token(k) < static_cast<uint32_t>(n)) at[k] = page_row(p.c, b, static_cast<int64_t>(start) + m.token(k));
+  }
+  float turn[kRows];
+  if constexpr (F::kScaled) {
+    uint32_t size[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) size[k] = k < rows && m.token(k) < static_cast<uint32_t>(p.L) && d < p.dh ? in[k].size() : 0;
     if constexpr (sizeof(T) == 2) {  // two rows a shuffle
 #pragma unroll
-      for (int k = 0; k < kHeads; k += 2) {
+      for (int k = 0; k < kRows; k += 2) {
         uint32_t two = size[k] | size[k + 1] << 16;
         for (int o = 1 << p.lanes >> 1; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
         size[k] = two & 0xffffu, size[k + 1] = two >> 16;
@@ -197,25 +230,29 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
     } else {
       for (int o = 1 << p.lanes >> 1; o; o >>= 1)
 #pragma unroll
-        for (int k = 0; k < kHeads; ++k) size[k] = max(size[k], __shfl_xor_sync(0xffffffffu, size[k], o));
+        for (int k = 0; k < kRows; ++k) size[k] = max(size[k], __shfl_xor_sync(0xffffffffu, size[k], o));
     }
     // Row lane % 4 is this lane's to divide for.
-    const uint32_t mine = lane & 2 ? (lane & 1 ? size[3] : size[2]) : (lane & 1 ? size[1] : size[0]);
-    const float most = Eight<T>::size_value(mine);
+    const int mine = lane % 4;
+    const float most = Eight<T>::size_value(mine & 2 ? (mine & 1 ? size[3] : size[2]) : (mine & 1 ? size[1] : size[0]));
+    const PageRow to = mine & 2 ? (mine & 1 ? at[3] : at[2]) : (mine & 1 ? at[1] : at[0]);
     const bool finite = __float_as_uint(most) < 0x7f800000u, kept = finite && most >= kTiny;
     const float my_turn = kept ? __fdiv_rn(F::kMost, most) : 0.0f;
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k) turn[k] = __shfl_sync(0xffffffffu, my_turn, k, 1 << p.lanes);
-    if (lane < heads && at.page >= 0)
-      (kv ? p.c.v_scale : p.c.k_scale)[at.page * p.c.ss.b + at.row * p.c.ss.l + (h0 + lane) * p.c.ss.h] =
+    for (int k = 0; k < kRows; ++k) turn[k] = __shfl_sync(0xffffffffu, my_turn, k, 1 << p.lanes);
+    if (lane < rows && lane < kRows && to.page >= 0)
+      (kv ? p.c.v_scale : p.c.k_scale)[to.page * p.c.ss.b + to.row * p.c.ss.l + (m.h0 + m.head(mine)) * p.c.ss.h] =
           kept ? __fdiv_rn(most, F::kMost) : finite ? 0.0f : __int_as_float(0x7fc00000);
   }
-  if (d >= p.dh || at.page < 0) return;
+  if (d >= p.dh || (!MANY && at[0].page < 0)) return;
   const Strides3& ps = kv ? p.c.vs : p.c.ks;
-  char* out = static_cast<char*>(kv ? p.c.v : p.c.k) + (at.page * ps.b + at.row * ps.l + h0 * ps.h + d) * F::kSize;
+  char* pages = static_cast<char*>(kv ? p.c.v : p.c.k) + (m.h0 * ps.h + d) * F::kSize;
+  if (!MANY) pages += (at[0].page * ps.b + at[0].row * ps.l) * F::kSize;
 #pragma unroll
-  for (int k = 0; k < kHeads; ++k, out += ps.h * F::kSize) {
-    if (k >= heads) break;
+  for (int k = 0; k < kRows; ++k, pages += MANY ? 0 : ps.h * F::kSize) {
+    if (k >= rows) break;
+    if (MANY && at[k].page < 0) continue;
+    char* out = MANY ? pages + (at[k].page * ps.b + at[k].row * ps.l + m.head(k) * ps.h) * F::kSize : pages;
     float f[8];
     in[k].get(f);
     if constexpr (F::kScaled) {
@@ -240,63 +277,77 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
   }
 }
 
-// The same threads read rows back; positions without a page read as zeros.
-// @R@
-template <class T, int FMT, bool VEC>
+// The same threads read rows back; positions without a page read as zeros.  Memory-bound:
+// eight sequences of 4836 rows x 40 heads of 128 from 8 bits 178 us (6.8 TB/s).
+template <class T, int FMT, bool VEC, bool MANY>
 __global__ void __launch_bounds__(kRowThreads) page_read_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
   const int b = blockIdx.y, kv = blockIdx.z;
-  const int d = (threadIdx.x & ((1 << p.lanes) - 1)) * 8;
-  const uint32_t r = blockIdx.x * (kRowThreads >> p.lanes) + (threadIdx.x >> p.lanes), i = p.by_groups.div(r);
-  const int h0 = static_cast<int>(r - i * p.by_groups.d) * p.heads, heads = min(p.heads, p.H - h0);
+  const RowMap<MANY> m(p);
+  const int d = m.lane * 8, rows = MANY ? m.heads * p.tokens : m.heads;
   pdl_trigger();
   pdl_wait();
   const int n = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
-  if (d >= p.dh || i >= static_cast<uint32_t>(n)) return;
-  const PageRow at = page_row(p.c, b, static_cast<int64_t>(p.starts ? p.starts[b] : 0) + i);
-  uint32_t w[kHeads][4] = {};
-  float s[kHeads] = {};
-  if (at.page >= 0) {
-    const Strides3& ps = kv ? p.c.vs : p.c.ks;
-    const char* in = static_cast<const char*>(kv ? p.c.v : p.c.k) + (at.page * ps.b + at.row * ps.l + h0 * ps.h + d) * F::kSize;
-    const float* scale = (kv ? p.c.v_scale : p.c.k_scale) + (F::kScaled ? at.page * p.c.ss.b + at.row * p.c.ss.l + h0 * p.c.ss.h : 0);
+  if (d >= p.dh || m.i >= static_cast<uint32_t>(n)) return;
+  const int start = p.starts ? p.starts[b] : 0;
+  PageRow at[kRows];
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k, in += ps.h * F::kSize) {
-      if (k >= heads) break;
-      if constexpr (F::kScaled) {
-        s[k] = scale[k * p.c.ss.h];
-        if (VEC) {
-          const uint2 y = *reinterpret_cast<const uint2*>(in);
-          w[k][0] = y.x, w[k][1] = y.y;
-        } else {
+  for (int k = 0; k < (MANY ? kRows : 1); ++k) {
+    if (k && m.token(k) == m.token(k - 1)) {
+      at[k] = at[k - 1];
+      continue;
+    }
+    at[k] = PageRow{-1, 0};
+    if (k < rows && m.token(k) < static_cast<uint32_t>(n)) at[k] = page_row(p.c, b, static_cast<int64_t>(start) + m.token(k));
+  }
+  const Strides3& ps = kv ? p.c.vs : p.c.ks;
+  const char* pages = static_cast<const char*>(kv ? p.c.v : p.c.k) + (m.h0 * ps.h + d) * F::kSize;
+  const float* scales = (kv ? p.c.v_scale : p.c.k_scale) + (F::kScaled ? m.h0 * p.c.ss.h : 0);
+  uint32_t w[kRows][4] = {};
+  float s[kRows] = {};
+  if (!MANY && at[0].page >= 0) {
+    pages += (at[0].page * ps.b + at[0].row * ps.l) * F::kSize;
+    if (F::kScaled) scales += at[0].page * p.c.ss.b + at[0].row * p.c.ss.l;
+  }
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (d + j < p.dh) w[k][j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(in[j])) << 8 * (j % 4);
-        }
-      } else if (VEC) {
-        const uint4 y = *reinterpret_cast<const uint4*>(in);
-        w[k][0] = y.x, w[k][1] = y.y, w[k][2] = y.z, w[k][3] = y.w;
+  for (int k = 0; k < kRows; ++k, pages += MANY ? 0 : ps.h * F::kSize) {
+    if (k >= rows || (!MANY && at[0].page < 0)) break;
+    if (MANY && at[k].page < 0) continue;
+    const char* in = MANY ? pages + (at[k].page * ps.b + at[k].row * ps.l + m.head(k) * ps.h) * F::kSize : pages;
+    if constexpr (F::kScaled) {
+      s[k] = MANY ? scales[at[k].page * p.c.ss.b + at[k].row * p.c.ss.l + m.head(k) * p.c.ss.h] : scales[k * p.c.ss.h];
+      if (VEC) {
+        const uint2 y = *reinterpret_cast<const uint2*>(in);
+        w[k][0] = y.x, w[k][1] = y.y;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (d + j < p.dh)
-            w[k][j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(in)[j]) << 16 * (j % 2);
+          if (d + j < p.dh) w[k][j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(in[j])) << 8 * (j % 4);
       }
+    } else if (VEC) {
+      const uint4 y = *reinterpret_cast<const uint4*>(in);
+      w[k][0] = y.x, w[k][1] = y.y, w[k][2] = y.z, w[k][3] = y.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (d + j < p.dh)
+          w[k][j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(in)[j]) << 16 * (j % 2);
     }
   }
-  T* x = static_cast<T*>(p.x[kv]) + b * p.xs[kv].b + i * p.xs[kv].l + h0 * p.xs[kv].h + d;
+  T* x = static_cast<T*>(p.x[kv]) + b * p.xs[kv].b + m.h0 * p.xs[kv].h + d;
+  if (!MANY) x += m.i * p.xs[kv].l;
 #pragma unroll
-  for (int k = 0; k < kHeads; ++k, x += p.xs[kv].h) {
-    if (k >= heads) break;
+  for (int k = 0; k < kRows; ++k, x += MANY ? 0 : p.xs[kv].h) {
+    if (k >= rows || (MANY && m.token(k) >= static_cast<uint32_t>(n))) break;
     float f[8];
     if constexpr (F::kScaled) {
       decode4<FMT>(w[k][0], f);
       decode4<FMT>(w[k][1], f + 4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= s[k];
-      if (at.page < 0)
+      if (at[MANY ? k : 0].page < 0)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+        for (int j = 0; j < 8; ++j) f[j] = 0.0f;  // (not the codes' -128 * 0)
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -306,21 +357,26 @@ __global__ void __launch_bounds__(kRowThreads) page_read_kernel(const __grid_con
     }
     Eight<T> out;
     out.set(f);
-    if (VEC) out.store(x);
-    else out.store(x, p.dh - d);
+    T* to = MANY ? x + m.token(k) * p.xs[kv].l + m.head(k) * p.xs[kv].h : x;
+    if (VEC) out.store(to);
+    else out.store(to, p.dh - d);
   }
 }
 
 template <class T, int FMT>
 cudaError_t launch_page_rows(const PageRowsParams& p, int B, bool vec, bool write, cudaStream_t st) {
-  const uint32_t groups = static_cast<uint32_t>(p.L) * p.by_groups.d, each = kRowThreads >> p.lanes;
+  const uint32_t groups = static_cast<uint32_t>(p.L) * p.by_groups.d, each = (kRowThreads >> p.lanes) * p.tokens;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = pdl_config(dim3((groups + each - 1) / each, B, 2), kRowThreads, 0, st, attr);
-  if (write)
-    return vec ? cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true>, p)
-               : cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, false>, p);
-  return vec ? cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true>, p)
-             : cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, false>, p);
+  const bool many = p.tokens > 1;
+  if (write) {
+    if (!vec) return cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, false, false>, p);
+    return many ? cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true, true>, p)
+                : cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true, false>, p);
+  }
+  if (!vec) return cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, false, false>, p);
+  return many ? cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true, true>, p)
+              : cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true, false>, p);
 }
 
 template <class T>
@@ -445,7 +501,7 @@ int page_rows_call(const psv_page_cache* c, const psv_page_rows* r, const void* 
   p.L = r->L, p.H = c->Hkv, p.dh = c->dh;
   p.lanes = 2;
   while (8 << p.lanes < c->dh) ++p.lanes;
-  const int groups = (c->Hkv + kHeads - 1) / kHeads;
+  const int groups = (c->Hkv + kRows - 1) / kRows;
   p.heads = (c->Hkv + groups - 1) / groups;
   p.by_groups = FastDiv::of(static_cast<uint32_t>(groups));
   p.xs[0] = strides3(r->k_stride), p.xs[1] = strides3(r->v_stride);
@@ -458,6 +514,7 @@ int page_rows_call(const psv_page_cache* c, const psv_page_rows* r, const void* 
   const bool vec = c->dh % 8 == 0 && multiple16(k, r->k_stride, c->B, r->L, c->Hkv, size) &&
                    multiple16(v, r->v_stride, c->B, r->L, c->Hkv, size) && eights(c->k_pages, c->k_stride) &&
                    eights(c->v_pages, c->v_stride);
+  p.tokens = !vec ? 1 : c->Hkv == 1 ? 4 : c->Hkv == 2 ? 2 : 1;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = r->dtype == PSV_DTYPE_F32    ? launch_page_rows_any<float>(p, c->B, vec, write, st)
                         : r->dtype == PSV_DTYPE_BF16 ? launch_page_rows_any<__nv_bfloat16>(p, c->B, vec, write, st)
