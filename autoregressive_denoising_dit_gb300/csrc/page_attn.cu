@@ -59,7 +59,7 @@ struct ACfg {
   static constexpr int KP = DH * ES / 64;   // 16-byte pieces of a key in a thread
   static constexpr int KS = kScaled ? 4 : 2;  // products (of 16 values) a piece
   static constexpr int VW = DH * ES / 32;   // 4-byte words of a value in a thread
-  static constexpr bool QS = NT == 2;       // queries in shared memory: registers for 12 warps an SM
+  static constexpr bool QS = NT == 2 || DH == 256;  // queries in shared memory, for want of registers
   static constexpr int Q_BYTES = QS ? NT * KP * KS * 256 + ROWS * 4 : 0;  // operands, a factor a row
   static constexpr int JSTRIDE = DH + 4;    // floats between a join area's rows
   static constexpr int RB = DH * ES;       // bytes of a row
@@ -68,11 +68,12 @@ struct ACfg {
   static constexpr int KV = kStep * RB;    // a step's keys, or values
   static constexpr int SLOT = 2 * KV + (kScaled ? 128 : 0);  // a warp's step: K, V, the scales
   // Two CTAs an SM: 128, 168 or 255 registers a thread.
-  static constexpr int WARPS = NT == 1 && DH == 64 ? 8 : (NT == 1 && kScaled) || DH == 64 ? 6 : 4;
+  static constexpr int WARPS = DH == 256 ? (kScaled ? 3 : 2) : NT == 1 && DH == 64 ? 8 : (NT == 1 && kScaled) || DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int JOIN = WARPS * ROWS * (JSTRIDE + 4) * 4;  // the warps' sums at the end of a group
   static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN - Q_BYTES - ROWS * (DH + 4) * 4) / (WARPS * SLOT));
   static constexpr int RING = WARPS * STAGES * SLOT;
+  static_assert(STAGES >= 2 && WARPS >= NT, "a step ahead, a warp a tile of queries");
   static constexpr int PART = ROWS * (DH + 4) * 4;  // a CTA's sums, which its cluster reads
   static constexpr int SMEM = RING + JOIN + Q_BYTES + PART;
   static_assert(2 * (SMEM + 1024 + 256) <= 233472, "two CTAs an SM");
@@ -412,7 +413,9 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   const uint32_t copied = placed<C::RB>(lane / C::LPR, lane % C::LPR);
   const uint32_t key_at = placed<C::RB>(quad, four);
   const uint32_t value_at = C::RB == 64 ? placed<C::RB>(2 * four, quad / 2) + quad % 2 * 8 : placed<C::RB>(2 * four, quad);
-  auto flip = [](int i) -> uint32_t { return C::RB == 256 ? (i / 2 * 4 + i % 2 * 2) * 16 : i * 64; };
+  auto flip = [](int i) -> uint32_t {
+    return C::RB == 512 ? ((i / 4 ^ i) % 2 * 4 + i / 2 % 2 * 2) * 16 : C::RB == 256 ? (i / 2 * 4 + i % 2 * 2) * 16 : i * 64;
+  };
   const bool in_head = lane % C::LPR * 16 < p.dh * C::ES;  // the piece that this lane copies
   const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
   const int sinks = p.window ? p.sinks : 0;
@@ -575,7 +578,9 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
 #pragma unroll
             for (int i = 0; i < DH / 16; ++i) {
               // the column pair that this thread's products i belong to
-              const int d = C::kScaled ? quad * (DH / 8) + 2 * i : (quad + 8 * (i / 4)) * 8 + 2 * (i % 4);
+              const int d = C::VW == 2    ? quad * 8 + 2 * i
+                            : C::kScaled ? (quad + 8 * (i / 8)) * 16 + 2 * (i % 8)
+                                         : (quad + 8 * (i / 4)) * 8 + 2 * (i % 4);
               *reinterpret_cast<float2*>(row + d) = make_float2(o[t][i][x], o[t][i][2 + x]);
             }
             if (quad == 0)
@@ -999,7 +1004,10 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
 
 template <int DH, int FMT>
 cudaError_t launch_rows(const PageAttnParams& p, int sms, cudaStream_t st) {
-  return p.Lq * p.G <= 8 ? launch_tile<DH, FMT, 1>(p, sms, st) : launch_tile<DH, FMT, 2>(p, sms, st);
+  if constexpr (DH < 256) {  // (the sums of 16 rows of 256 values do not fit the registers)
+    if (p.Lq * p.G > 8) return launch_tile<DH, FMT, 2>(p, sms, st);
+  }
+  return launch_tile<DH, FMT, 1>(p, sms, st);
 }
 
 template <int DH>
@@ -1016,7 +1024,7 @@ cudaError_t launch_format(const PageAttnParams& p, int sms, cudaStream_t st) {
 
 // At most two shares a CTA.
 size_t page_attn_scratch(const PageAttnParams& p) {
-  const int dh = p.dh <= 64 ? 64 : 128, rows = p.Lq * p.G <= 8 ? 8 : 16;
+  const int dh = p.dh <= 64 ? 64 : p.dh <= 128 ? 128 : 256, rows = p.Lq * p.G <= 8 || dh == 256 ? 8 : 16;
   return kSharedBytes + static_cast<size_t>(kMaxCtas) * 2 * share_floats(dh, rows) * sizeof(float);
 }
 
@@ -1026,7 +1034,7 @@ void page_attn_scratch(PageAttnParams& p, void* scratch) {
 }
 
 cudaError_t launch_page_attention(const PageAttnParams& p, int sms, cudaStream_t st) {
-  return p.dh <= 64 ? launch_format<64>(p, sms, st) : launch_format<128>(p, sms, st);
+  return p.dh <= 64 ? launch_format<64>(p, sms, st) : p.dh <= 128 ? launch_format<128>(p, sms, st) : launch_format<256>(p, sms, st);
 }
 
 }  // namespace psv

@@ -85,8 +85,7 @@ __device__ __forceinline__ int page_length(const PageAttnParams& p, int b, int r
 
 cudaError_t launch_page_attention_general(const PageAttnParams& p, cudaStream_t st);
 
-// For rows of 16-byte pieces, pages of 16-byte (or 8-bit ones of 8-byte) pieces and heads
-// of up to 128: the workspace's size
+// For rows of 16-byte pieces and pages of 16-byte (or 8-bit ones of 8-byte) pieces: the workspace's size
 // (Lq, G and dh count), its use, and the launch on `sms` SMs.
 size_t page_attn_scratch(const PageAttnParams& p);
 void page_attn_scratch(PageAttnParams& p, void* scratch);

@@ -558,7 +558,7 @@ PageAttnParams page_attn_params(const psv_page_cache* c, const psv_page_query* q
 }
 
 // Whether heads are made of eight values each, for the tensor-core kernel.
-bool page_attn_pieces(const psv_page_cache* c) { return c->dh <= 128 && c->dh % 8 == 0; }
+bool page_attn_pieces(const psv_page_cache* c) { return c->dh % 8 == 0; }
 
 size_t page_scratch(const psv_page_cache* c, const PageAttnParams& p) {
   return page_attn_pieces(c) ? page_attn_scratch(p) : 256;

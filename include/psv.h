@@ -625,10 +625,10 @@ int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void
  * Requirements: dtype BF16 or F16 (16-bit pages: their own); Hq a multiple of Hkv;
  * B x Hq <= 2^24; 0 <= Lq <= 2^20, B x Lq x Hq <= 2^30; window, sinks >= 0, sinks
  * need a window; scale, softcap >= 0 finite; o's rows distinct.
- * The tensor-core kernel takes dh <= 128, dh % 8 == 0, bases and strides of q and o in
+ * The tensor-core kernel takes dh % 8 == 0, bases and strides of q and o in
  * multiples of 16 bytes, of pages in multiples of eight values, strides of pages, rows
  * and scales below 4 GB; every other problem runs on a slower general kernel.  It is
- * made for few rows: it reads the pages once for every 16 rows a kv head, Lq x Hq / Hkv.
+ * made for few rows: it reads the pages once for every 16 rows a kv head, Lq x Hq / Hkv (8, where dh > 128).
  * (A chunk's many rows: psv_page_read, then psv_cache_attention.)  Pages of a multiple
  * of eight rows are read fastest.  max_pages is what the host knows of the lengths:
  * where it is small, calls need no second kernel. */

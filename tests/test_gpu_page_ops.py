@@ -358,6 +358,9 @@ ATTN = [
     dict(B=1, Lq=2, Lk=150, Hq=2, Hkv=1, dh=21, page=64, causal=True),           # general kernel
     dict(B=1, Lq=1, Lk=100, Hq=2, Hkv=1, dh=100, page=32, window=40, sinks=5, missing=[(0, 2)], cap=3.0),  # general kernel
     dict(B=1, Lq=1, Lk=200, Hq=2, Hkv=1, dh=256, page=64),
+    dict(B=2, Lq=3, Lk=700, Hq=8, Hkv=2, dh=256, page=24, causal=True, lens=[700, 60], rows=[3, 2]),
+    dict(B=2, Lq=1, Lk=530, Hq=4, Hkv=4, dh=200, page=16, window=300, sinks=20),
+    dict(B=1, Lq=5, Lk=260, Hq=4, Hkv=1, dh=136, page=7, causal=True, missing=[(0, 3)]),
     dict(B=2, Lq=1, Lk=900, Hq=4, Hkv=2, dh=128, page=64, causal=True, window=200, sinks=20),
     dict(B=2, Lq=5, Lk=900, Hq=2, Hkv=2, dh=128, page=48, causal=True, window=33, sinks=3, lens=[900, 20]),
     dict(B=1, Lq=9, Lk=400, Hq=4, Hkv=2, dh=64, page=64, window=5, lens=[400]),  # not causal
