@@ -43,13 +43,13 @@ struct alignas(32) Shared {
 
 namespace {
 
-constexpr int kStep = 16;  // keys of a warp's step
-constexpr int kStart = 8;  // steps on the line that a group's start counts for
 constexpr int kCtasSm = 2;
 constexpr int kMaxCtas = 152 * kCtasSm;  // shares in the workspace
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 256.0f;  // weights above it take up a new maximum
 constexpr float kNone = -FLT_MAX;   // a maximum of nothing: exp2(-inf - kNone) = 0, exp2(kNone - kNone) = 1
+
+constexpr bool STEP2(int dh, bool scaled, int nt) { return scaled && (dh == 64 || (dh == 128 && nt == 2)); }
 
 template <int DH, int FMT, int NT>
 struct ACfg {
@@ -65,12 +65,15 @@ struct ACfg {
   static constexpr int RB = DH * ES;       // bytes of a row
   static constexpr int LPR = RB / 16;      // lanes that copy it
   static constexpr int RPC = 32 / LPR;     // rows of a copy
-  static constexpr int KV = kStep * RB;    // a step's keys, or values
-  static constexpr int SLOT = 2 * KV + (kScaled ? 128 : 0);  // a warp's step: K, V, the scales
+  // Keys of a warp's step: 16 a product, twice as many where that costs no step ahead.
+  static constexpr int SUBS = STEP2(DH, kScaled, NT) ? 2 : 1, STEP = 16 * SUBS;
+  static constexpr int START = 8 / SUBS;   // steps on the line that a group's start counts for
+  static constexpr int KV = STEP * RB;     // a step's keys, or values
+  static constexpr int SLOT = 2 * KV + (kScaled ? STEP * 8 : 0);  // a warp's step: K, V, the scales
   // Two CTAs an SM: 128, 168 or 255 registers a thread.
   static constexpr int WARPS = DH == 256 ? (kScaled ? 3 : 2) : NT == 1 && DH == 64 ? 8 : (NT == 1 && kScaled) || DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int JOIN = WARPS * ROWS * (JSTRIDE + 4) * 4;  // the warps' sums at the end of a group
+  static constexpr int JOIN = WARPS * 8 * (JSTRIDE + 4) * 4;  // the warps' sums at the end of a group, a tile at a time
   static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN - Q_BYTES - ROWS * (DH + 4) * 4) / (WARPS * SLOT));
   static constexpr int RING = WARPS * STAGES * SLOT;
   static_assert(STAGES >= 2 && WARPS >= NT, "a step ahead, a warp a tile of queries");
@@ -183,11 +186,12 @@ struct Seq {
   int rows, n, keys;  // query rows, length, keys that may have a page
   int head, from, steps, tiles;
   int64_t total;  // on the line, of all its kv heads and row tiles
-  __device__ __forceinline__ int span() const { return steps + kStart; }  // a group's
+  int span;       // a group's
 };
 
-template <int ROWS>
+template <class C>
 __device__ __forceinline__ Seq sequence(const PageAttnParams& p, int rows, int n) {
+  constexpr int kStep = C::STEP;
   Seq s;
   s.rows = rows;
   s.n = n;
@@ -198,8 +202,9 @@ __device__ __forceinline__ Seq sequence(const PageAttnParams& p, int rows, int n
   const int from = min(max(first / kStep, s.head), end);
   s.from = from * kStep;
   s.steps = max(s.head + end - from, 1);  // (a row without keys is written too)
-  s.tiles = (rows * p.G + ROWS - 1) / ROWS;
-  s.total = static_cast<int64_t>(s.span()) * s.tiles * p.Hkv;
+  s.span = s.steps + C::START;
+  s.tiles = (rows * p.G + C::ROWS - 1) / C::ROWS;
+  s.total = static_cast<int64_t>(s.span) * s.tiles * p.Hkv;
   return s;
 }
 
@@ -209,12 +214,12 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a / b;
 }
 
-// The line of all groups (of `span` units: kStart, then a unit a step) in `ctas` equal
+// The line of all groups (of `span` units: `start` of them, then a unit a step) in `ctas` equal
 // stretches.
 struct Cut {
   int64_t all, each;
-  int ctas, more;
-  __device__ __forceinline__ Cut(int64_t a, int n) : all(a), each(0), ctas(n), more(0) {
+  int ctas, more, start;
+  __device__ __forceinline__ Cut(int64_t a, int n, int s) : all(a), each(0), ctas(n), more(0), start(s) {
     if (n) each = divide(a, n), more = static_cast<int>(a - each * n);
   }
   __device__ __forceinline__ int64_t begin(int cta) const {
@@ -223,7 +228,7 @@ struct Cut {
   // A cut this near to an end of its group is moved there, so that fewer CTAs have
   // shares of two groups, and none has a start alone.
   __device__ __forceinline__ int near(int span) const {
-    return max(static_cast<int>(min(each >> 3, static_cast<int64_t>(span >> 2))), kStart + 1);
+    return max(static_cast<int>(min(each >> 3, static_cast<int64_t>(span >> 2))), start + 1);
   }
   // By how much, `within` units into a sequence of groups of `span`.
   __device__ __forceinline__ int moved(int64_t within, int span) const {
@@ -268,11 +273,12 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     page_attn_kernel(const __grid_constant__ PageAttnParams p) {
   using C = ACfg<DH, FMT, NT>;
   constexpr int ROWS = C::ROWS, kWarps = C::WARPS, kThreads = C::THREADS, kStages = C::STAGES;
+  constexpr int SUBS = C::SUBS, kStep = C::STEP, kHalves = kStep / 8, kAhead = 32 / kHalves;
   constexpr bool kBf16Operands = FMT == PSV_PAGE_BF16;
   constexpr int kPart = share_floats(DH, ROWS);
   extern __shared__ __align__(128) uint8_t smem[];
-  float* so = reinterpret_cast<float*>(smem + C::RING);  // [kWarps][ROWS][JSTRIDE]
-  float* sm = so + kWarps * ROWS * C::JSTRIDE;           // [kWarps][ROWS][4]: m', m, l
+  float* so = reinterpret_cast<float*>(smem + C::RING);  // [kWarps][8][JSTRIDE]
+  float* sm = so + kWarps * 8 * C::JSTRIDE;              // [kWarps][8][4]: m', m, l
   uint4* sq = reinterpret_cast<uint4*>(smem + C::RING + C::JOIN);  // QS: [NT][KP * KS / 2][lane]
   float* sq_up = reinterpret_cast<float*>(sq + NT * C::KP * C::KS * 16);  // [ROWS]
   float* sp = reinterpret_cast<float*>(smem + C::RING + C::JOIN + C::Q_BYTES);  // CLUSTER: a share
@@ -295,20 +301,20 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   int b = 0;
   int64_t before = 0;  // steps of earlier sequences
   Seq s;
-  Cut cut(0, 0);
+  Cut cut(0, 0, C::START);
   if (!CLUSTER && threadIdx.x == 0) p.shared[blockIdx.x].rows = 0;
   auto sequence_at = [&](int k) {
     const int rows = page_rows(p, k);
-    return sequence<ROWS>(p, rows, page_length(p, k, rows));
+    return sequence<C>(p, rows, page_length(p, k, rows));
   };
   if (p.quick) {  // up to 32 sequences a lane, 32 bits
     const int each = (p.B + 31) / 32;
-    auto units32 = [&](const Seq& x) { return (CLUSTER ? 1 : x.span()) * x.tiles * p.Hkv; };
+    auto units32 = [&](const Seq& x) { return (CLUSTER ? 1 : x.span) * x.tiles * p.Hkv; };
     int own = 0, rows_b = 0, n_b = 0;
     if (lane * each < p.B) {
       rows_b = page_rows(p, lane * each);
       n_b = page_length(p, lane * each, rows_b);
-      own = units32(sequence<ROWS>(p, rows_b, n_b));
+      own = units32(sequence<C>(p, rows_b, n_b));
     }
     if (each > 1) {
 #pragma unroll 4
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       if (lane >= o) sum += up;
     }
     const int all = __shfl_sync(0xffffffffu, sum, 31);
-    cut = Cut(all, min(places, CLUSTER ? all : (all + kWarps - 1) / kWarps));
+    cut = Cut(all, min(places, CLUSTER ? all : (all + kWarps - 1) / kWarps), C::START);
     if (place_of >= cut.ctas) return;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
@@ -335,14 +341,14 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       int k = at * each, first = __shfl_sync(0xffffffffu, sum - own, at);
       Seq y;
       if (each == 1) {
-        y = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
+        y = sequence<C>(p, __shfl_sync(0xffffffffu, rows_b, at), __shfl_sync(0xffffffffu, n_b, at));
       } else {
         // lane by lane the sequences of lane `at`
         int rows = 0, n = 0, mine = 0;
         if (lane < each && k + lane < p.B) {
           rows = page_rows(p, k + lane);
           n = page_length(p, k + lane, rows);
-          mine = units32(sequence<ROWS>(p, rows, n));
+          mine = units32(sequence<C>(p, rows, n));
         }
         int upto = mine;
 #pragma unroll
@@ -353,9 +359,9 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         const int in = __ffs(__ballot_sync(0xffffffffu, first + upto > x)) - 1;
         first += __shfl_sync(0xffffffffu, upto - mine, in);
         k += in;
-        y = sequence<ROWS>(p, __shfl_sync(0xffffffffu, rows, in), __shfl_sync(0xffffffffu, n, in));
+        y = sequence<C>(p, __shfl_sync(0xffffffffu, rows, in), __shfl_sync(0xffffffffu, n, in));
       }
-      if (!CLUSTER) hi = x + cut.moved(x - first, y.span());
+      if (!CLUSTER) hi = x + cut.moved(x - first, y.span);
       if (i == 0) b = k, before = first, s = y;
     }
   } else {
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     for (int k = lane; k < p.B; k += 32) all += units(sequence_at(k));
 #pragma unroll
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    cut = Cut(all, static_cast<int>(min(static_cast<int64_t>(places), CLUSTER ? all : (all + kWarps - 1) / kWarps)));
+    cut = Cut(all, static_cast<int>(min(static_cast<int64_t>(places), CLUSTER ? all : (all + kWarps - 1) / kWarps)), C::START);
     if (place_of >= cut.ctas) return;
     int64_t sum0 = 0, x = cut.begin(place_of);
     bool begun = false;
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         int64_t moved = x;
         if (hit) {
           y = sequence_at(b0 + at);
-          if (!CLUSTER) moved += cut.moved(x - first, y.span());
+          if (!CLUSTER) moved += cut.moved(x - first, y.span);
         }
         if (begun) {
           hi = moved;
@@ -419,19 +425,19 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
   const bool in_head = lane % C::LPR * 16 < p.dh * C::ES;  // the piece that this lane copies
   const bool eights = c.page_size % 8 == 0;  // eight keys lie in one page
   const int sinks = p.window ? p.sinks : 0;
-  const char *k_mine = nullptr, *v_mine = nullptr, *s_mine = nullptr;
+  const char *k_mine = nullptr, *v_mine = nullptr, *s_mine[SUBS];  // (scales: of keys and values by lane, or one after the other)
   int kvh = 0, r0 = 0, n_rows = 0, step0 = 0, step1 = 0, taken = 0, slot = 0;
   int all_end = 0, any_end = 0, all_first = 0, any_first = 0;
   uint32_t found = 0;  // a bit for each step under way: whether key lane % 16 is there
-  // Where the keys of the warp's next steps are: in lane 2 i + h the half h of number i
-  // of 16 steps, and of the 16 behind them, or where eight keys may lie in several pages
-  // of the next step key lane % 16.
+  // Where the keys of the warp's next steps are: in lane kHalves i + h the eight keys h of
+  // number i of kAhead steps, and of those behind them, or where eight keys may lie in
+  // several pages of the next step key lane % kStep.
   PageRow place{-1, 0}, later{-1, 0};
   int issued = 0;  // steps of the group that the warp has asked for
   auto key_of = [&](int step) { return step < s.head ? step * kStep : s.from + (step - s.head) * kStep; };
   auto look = [&](int number) {  // of the warp's steps
-    const int step = step0 + worker + (number + (eights ? lane / 2 : 0)) * workers;
-    return step < step1 ? page_row(c, b, key_of(step) + (eights ? lane % 2 * 8 : lane % 16)) : PageRow{-1, 0};
+    const int step = step0 + worker + (number + (eights ? lane / kHalves : 0)) * workers;
+    return step < step1 ? page_row(c, b, key_of(step) + (eights ? lane % kHalves * 8 : lane % kStep)) : PageRow{-1, 0};
   };
   auto offset = [](uint32_t page_stride, uint32_t row_stride, int page, int row) {
     return static_cast<uint64_t>(page_stride) * static_cast<uint32_t>(page) +
@@ -445,21 +451,26 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     const int key0 = key_of(step);
     // Keys that some row of the tile sees are read.
     const bool every = key0 + kStep <= any_end && (key0 >= any_first || key0 + kStep <= sinks);
-    PageRow half[2];
+    PageRow at = place;  // of key lane % kStep
+    int pages[kHalves], rows[kHalves], least = 0;
     if (eights) {
-      if (number % 16 == 0 && number) place = later, later = look(number + 16);
+      const int first = number % kAhead * kHalves;
+      if (first == 0 && number) place = later, later = look(number + kAhead);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        half[h].page = __shfl_sync(0xffffffffu, place.page, 2 * (number % 16) + h);
-        half[h].row = __shfl_sync(0xffffffffu, place.row, 2 * (number % 16) + h);
+      for (int h = 0; h < kHalves; ++h) {
+        pages[h] = __shfl_sync(0xffffffffu, place.page, first + h);
+        rows[h] = __shfl_sync(0xffffffffu, place.row, first + h);
+        least = min(least, pages[h]);
       }
+      at.page = __shfl_sync(0xffffffffu, place.page, first + lane % kStep / 8);
+      at.row = __shfl_sync(0xffffffffu, place.row, first + lane % kStep / 8) + lane % 8;
     }
-    if (eights && every && !p.halves && half[0].page >= 0 && half[1].page >= 0) {
+    if (eights && every && !p.halves && least >= 0) {
       found |= 1;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const char* k = k_mine + offset(p.kb, p.kl, half[h].page, half[h].row);
-        const char* v = v_mine + offset(p.vb, p.vl, half[h].page, half[h].row);
+      for (int h = 0; h < kHalves; ++h) {
+        const char* k = k_mine + offset(p.kb, p.kl, pages[h], rows[h]);
+        const char* v = v_mine + offset(p.vb, p.vl, pages[h], rows[h]);
         if (in_head) {
 #pragma unroll
           for (int i = 0; i < 8 / C::RPC; ++i) {
@@ -470,17 +481,15 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         }
       }
       if constexpr (C::kScaled) {
-        const bool h = lane & 8;
-        copy4(ring + dst + 2 * C::KV + lane * 4,
-              s_mine + offset(p.sb, p.sl, h ? half[1].page : half[0].page, (h ? half[1].row : half[0].row) + lane % 8), 4);
+        const uint64_t from = offset(p.sb, p.sl, at.page, at.row);
+#pragma unroll
+        for (int x = 0; x < SUBS; ++x) copy4(ring + dst + 2 * C::KV + x * 128 + lane * 4, s_mine[x] + from, 4);
       }
       return;
     }
     // Key by key; what is not wanted (keys, pieces behind the head) is zeros.
-    PageRow at = place;
-    if (eights) at = lane & 8 ? half[1] : half[0], at.row += lane % 8;
-    else place = look(issued);
-    const int j = key0 + lane % 16;
+    if (!eights) place = look(issued);
+    const int j = key0 + lane % kStep;
     if (at.page < 0 || j >= any_end || (j < any_first && j >= sinks)) at = PageRow{-1, 0};
     found |= at.page >= 0;
 #pragma unroll 1
@@ -502,8 +511,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         copy8(to + C::KV + 8, from_v + more, more);
       }
     }
-    if constexpr (C::kScaled)
-      copy4(ring + dst + 2 * C::KV + lane * 4, s_mine + offset(p.sb, p.sl, max(at.page, 0), at.row), at.page >= 0 ? 4 : 0);
+    if constexpr (C::kScaled) {
+      const uint64_t from = offset(p.sb, p.sl, max(at.page, 0), at.row);
+#pragma unroll
+      for (int x = 0; x < SUBS; ++x) copy4(ring + dst + 2 * C::KV + x * 128 + lane * 4, s_mine[x] + from, at.page >= 0 ? 4 : 0);
+    }
   };
   float o[NT][DH / 16][4], mo[NT][2], ml[NT][2], l[NT][2];
   bool joining = false, split = false;  // the group before, whose sums are still the warps'
@@ -520,11 +532,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         s = sequence_at(++b);
       }
       const int64_t within = lo - before;
-      const int group = static_cast<int>(CLUSTER ? within : divide(within, s.span()));
-      const int at = CLUSTER ? 0 : static_cast<int>(within - static_cast<int64_t>(group) * s.span());
-      taken = CLUSTER ? 1 : static_cast<int>(min(static_cast<int64_t>(s.span() - at), hi - lo));
-      step0 = max(at - kStart, 0);
-      step1 = CLUSTER ? s.steps : at + taken - kStart;
+      const int group = static_cast<int>(CLUSTER ? within : divide(within, s.span));
+      const int at = CLUSTER ? 0 : static_cast<int>(within - static_cast<int64_t>(group) * s.span);
+      taken = CLUSTER ? 1 : static_cast<int>(min(static_cast<int64_t>(s.span - at), hi - lo));
+      step0 = max(at - C::START, 0);
+      step1 = CLUSTER ? s.steps : at + taken - C::START;
       kvh = s.tiles == 1 ? group : group / s.tiles;
       r0 = (group - kvh * s.tiles) * ROWS;
       n_rows = min(s.rows * p.G - r0, ROWS);
@@ -536,11 +548,13 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       // the piece that this lane copies of the first rows of page 0
       k_mine = static_cast<const char*>(c.k) + kvh * c.ks.h * C::ES + offset(0, p.kl, 0, lane / C::LPR) + lane % C::LPR * 16;
       v_mine = static_cast<const char*>(c.v) + kvh * c.vs.h * C::ES + offset(0, p.vl, 0, lane / C::LPR) + lane % C::LPR * 16;
-      s_mine = reinterpret_cast<const char*>((lane < 16 ? c.k_scale : c.v_scale) + kvh * c.ss.h);
+#pragma unroll
+      for (int x = 0; x < SUBS; ++x)
+        s_mine[x] = reinterpret_cast<const char*>(((SUBS == 1 ? lane < 16 : x == 0) ? c.k_scale : c.v_scale) + kvh * c.ss.h);
       issued = 0;
       slot = 0;
       place = look(0);
-      if (eights) later = look(16);
+      if (eights) later = look(kAhead);
 #pragma unroll
       for (int t = 0; t < NQ; ++t) {
         // queries: row quad (+ 8) of the tile, values of this thread's pieces
@@ -566,15 +580,17 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     }
     if (joining) {
       // ---- join the warps
+      float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + was_slot) * kPart;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        if (8 * t >= was_rows) break;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
-          const int r = 8 * t + 2 * four + x;
-          if (r < was_rows) {
-            float* row = so + (warp * ROWS + r) * C::JSTRIDE;
+          const int r = 2 * four + x;
+          if (8 * t + r < was_rows) {
+            float* row = so + (warp * 8 + r) * C::JSTRIDE;
 #pragma unroll
             for (int i = 0; i < DH / 16; ++i) {
               // the column pair that this thread's products i belong to
@@ -584,41 +600,41 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
               *reinterpret_cast<float2*>(row + d) = make_float2(o[t][i][x], o[t][i][2 + x]);
             }
             if (quad == 0)
-              *reinterpret_cast<float4*>(sm + (warp * ROWS + r) * 4) = make_float4(mo[t][x], ml[t][x], l[t][x], 0.0f);
+              *reinterpret_cast<float4*>(sm + (warp * 8 + r) * 4) = make_float4(mo[t][x], ml[t][x], l[t][x], 0.0f);
           }
         }
-      __syncthreads();
-      float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + was_slot) * kPart;
+        __syncthreads();
 #pragma unroll 1
-      for (int x = threadIdx.x; x < was_rows * (DH / 4); x += kThreads) {
-        const int r = x / (DH / 4), d = x % (DH / 4) * 4;
-        float4 st[kWarps];
-        float mm_o = kNone, mm_l = kNone;
+        for (int x = threadIdx.x; x < min(was_rows - 8 * t, 8) * (DH / 4); x += kThreads) {
+          const int r = x / (DH / 4), d = x % (DH / 4) * 4, row = 8 * t + r;
+          float4 st[kWarps];
+          float mm_o = kNone, mm_l = kNone;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          st[w] = *reinterpret_cast<const float4*>(sm + (w * ROWS + r) * 4);
-          mm_o = fmaxf(mm_o, st[w].x);
-          mm_l = fmaxf(mm_l, st[w].y);
-        }
-        float ll = 0.0f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int w = 0; w < kWarps; ++w) {
+            st[w] = *reinterpret_cast<const float4*>(sm + (w * 8 + r) * 4);
+            mm_o = fmaxf(mm_o, st[w].x);
+            mm_l = fmaxf(mm_l, st[w].y);
+          }
+          float ll = 0.0f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4 y = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * C::JSTRIDE + d);
-          const float f = fast_exp2(st[w].x - mm_o);
-          ll = fmaf(fast_exp2(st[w].y - mm_l), st[w].z, ll);
-          acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
-          acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
+          for (int w = 0; w < kWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(so + (w * 8 + r) * C::JSTRIDE + d);
+            const float f = fast_exp2(st[w].x - mm_o);
+            ll = fmaf(fast_exp2(st[w].y - mm_l), st[w].z, ll);
+            acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
+            acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
+          }
+          if (split) {
+            float* to = CLUSTER ? sp : part;
+            *reinterpret_cast<float4*>(to + row * DH + d) = acc;
+            if (d == 0) *reinterpret_cast<float4*>(to + ROWS * DH + row * 4) = make_float4(mm_o, mm_l, ll, 0.0f);
+          } else {
+            write_out(p, was_b, was_kvh, was_r0 + row, d, mm_o, mm_l, ll, acc);
+          }
         }
-        if (split) {
-          float* to = CLUSTER ? sp : part;
-          *reinterpret_cast<float4*>(to + r * DH + d) = acc;
-          if (d == 0) *reinterpret_cast<float4*>(to + ROWS * DH + r * 4) = make_float4(mm_o, mm_l, ll, 0.0f);
-        } else {
-          write_out(p, was_b, was_kvh, was_r0 + r, d, mm_o, mm_l, ll, acc);
-        }
+        __syncthreads();
       }
-      __syncthreads();
       if (CLUSTER && split) {
         cluster_sync();
 #pragma unroll 1
@@ -702,16 +718,15 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       const unsigned there = __ballot_sync(0xffffffffu, found >> (kStages - 1) & 1);
       if (!there) continue;
       // ---- scores
-      float sc[NT][4];
+      float sc[SUBS][NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int h = 0; h < SUBS; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[t][e] = 0.0f;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[h][t][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < C::KP; ++i) {
-        const uint8_t* key = smem + ((mine + key_at) ^ (i % 2 * 64)) + i / 2 * 128;
-        const uint4 k0 = *reinterpret_cast<const uint4*>(key), k1 = *reinterpret_cast<const uint4*>(key + 8 * C::RB);
-        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
         uint32_t qs[NT][2 * C::KS];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -722,49 +737,67 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
               qs[t][4 * x] = y.x, qs[t][4 * x + 1] = y.y, qs[t][4 * x + 2] = y.z, qs[t][4 * x + 3] = y.w;
             } else {
 #pragma unroll
-              for (int h = 0; h < 4; ++h) qs[t][4 * x + h] = qf[t][i * C::KS + 2 * x + h / 2][h % 2];
+              for (int z = 0; z < 4; ++z) qs[t][4 * x + z] = qf[t][i * C::KS + 2 * x + z / 2][z % 2];
             }
           }
 #pragma unroll
-        for (int x = 0; x < C::KS; ++x) {
-          uint32_t a[4];
-          if constexpr (C::kScaled) {
-            widen<FMT>(w0[x], a[0], a[2]);
-            widen<FMT>(w1[x], a[1], a[3]);
-          } else {
-            a[0] = w0[2 * x], a[1] = w1[2 * x], a[2] = w0[2 * x + 1], a[3] = w1[2 * x + 1];
-          }
+        for (int h = 0; h < SUBS; ++h) {
+          const uint8_t* key = smem + ((mine + key_at) ^ (i % 2 * 64)) + i / 2 * 128 + h * 16 * C::RB;
+          const uint4 k0 = *reinterpret_cast<const uint4*>(key), k1 = *reinterpret_cast<const uint4*>(key + 8 * C::RB);
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma<FMT>(sc[t], a, qs[t][2 * x], qs[t][2 * x + 1]);
+          for (int x = 0; x < C::KS; ++x) {
+            uint32_t a[4];
+            if constexpr (C::kScaled) {
+              widen<FMT>(w0[x], a[0], a[2]);
+              widen<FMT>(w1[x], a[1], a[3]);
+            } else {
+              a[0] = w0[2 * x], a[1] = w1[2 * x], a[2] = w0[2 * x + 1], a[3] = w1[2 * x + 1];
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma<FMT>(sc[h][t], a, qs[t][2 * x], qs[t][2 * x + 1]);
+          }
         }
-      }
-      float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
-      if constexpr (C::kScaled) {
-        const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV);
-        ks[0] = scales[quad], ks[1] = scales[quad + 8];
-        lv[0] = fast_log2(scales[16 + quad]), lv[1] = fast_log2(scales[24 + quad]);
       }
       // ---- scores and weights' exponents in the log2 domain
       const int key0 = key_of(step);
-      float u[NT][4];
+      float u[SUBS][NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[t][e] = (C::kScaled ? sc[t][e] * ks[e >> 1] : sc[t][e]) * up[t][e & 1];
-      if (p.softcap > 0) {
-        float big = 0.0f;
+      for (int h = 0; h < SUBS; ++h) {
+        float ks[2] = {1.0f, 1.0f};
+        if constexpr (C::kScaled) {
+          const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV) + 16 * h;
+          ks[0] = scales[quad], ks[1] = scales[quad + 8];
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(sc[t][e]));
-        if (__all_sync(0xffffffffu, big * p.cap.inv <= 1.0f)) cap_within<4 * NT>(&sc[0][0], p.cap);
-        else cap_any<4 * NT>(&sc[0][0], p.cap);
+          for (int e = 0; e < 4; ++e) sc[h][t][e] = (C::kScaled ? sc[h][t][e] * ks[e >> 1] : sc[h][t][e]) * up[t][e & 1];
+      }
+      if (p.softcap > 0) {
+        float big = 0.0f;
+#pragma unroll
+        for (int h = 0; h < SUBS; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(sc[h][t][e]));
+        if (__all_sync(0xffffffffu, big * p.cap.inv <= 1.0f)) cap_within<4 * NT * SUBS>(&sc[0][0][0], p.cap);
+        else cap_any<4 * NT * SUBS>(&sc[0][0][0], p.cap);
+      }
+#pragma unroll
+      for (int h = 0; h < SUBS; ++h) {
+        float lv[2] = {0.0f, 0.0f};
+        if constexpr (C::kScaled) {
+          const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV) + kStep + 16 * h;
+          lv[0] = fast_log2(scales[quad]), lv[1] = fast_log2(scales[quad + 8]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[h][t][e] = C::kScaled ? sc[h][t][e] + lv[e >> 1] : sc[h][t][e];
       }
       const bool whole = (key0 + kStep <= all_end && (key0 >= all_first || key0 + kStep <= sinks)) && there == 0xffffffffu;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[t][e] = C::kScaled ? sc[t][e] + lv[e >> 1] : sc[t][e];
       // whether row r of the tile sees the step's key
       auto sees = [&](int r, int key) {
         const int at_row = s.n - s.rows + static_cast<int>(p.by_group.div(r0 + r)), j = key0 + key;
@@ -773,23 +806,27 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       };
       if (!whole) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int h = 0; h < SUBS; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!sees(8 * t + 2 * four + (e & 1), quad + 8 * (e >> 1))) sc[t][e] = -INFINITY, u[t][e] = -INFINITY;
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!sees(8 * t + 2 * four + (e & 1), 16 * h + quad + 8 * (e >> 1))) sc[h][t][e] = -INFINITY, u[h][t][e] = -INFINITY;
       }
       // ---- weights; a new maximum is taken up where one passes the old one by far
-      float w[NT][4], y[NT][4];
+      float w[SUBS][NT][4], y[SUBS][NT][4];
       auto weigh = [&]() {
         float big = 0.0f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int h = 0; h < SUBS; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[t][e] = fast_exp2(sc[t][e] - ml[t][e & 1]);
-            w[t][e] = C::kScaled ? fast_exp2(u[t][e] - mo[t][e & 1]) : y[t][e];
-            big = fmaxf(big, fmaxf(y[t][e], w[t][e]));
-          }
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[h][t][e] = fast_exp2(sc[h][t][e] - ml[t][e & 1]);
+              w[h][t][e] = C::kScaled ? fast_exp2(u[h][t][e] - mo[t][e & 1]) : y[h][t][e];
+              big = fmaxf(big, fmaxf(y[h][t][e], w[h][t][e]));
+            }
         return big;
       };
       if (__any_sync(0xffffffffu, weigh() > kRescale)) {
@@ -797,7 +834,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float a = fmaxf(sc[t][x], sc[t][2 + x]), d = fmaxf(u[t][x], u[t][2 + x]);
+            float a = fmaxf(sc[0][t][x], sc[0][t][2 + x]), d = fmaxf(u[0][t][x], u[0][t][2 + x]);
+            if (SUBS > 1) {
+              a = fmaxf(a, fmaxf(sc[SUBS - 1][t][x], sc[SUBS - 1][t][2 + x]));
+              d = fmaxf(d, fmaxf(u[SUBS - 1][t][x], u[SUBS - 1][t][2 + x]));
+            }
 #pragma unroll
             for (int i = 4; i < 32; i <<= 1) {
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, i));
@@ -813,78 +854,83 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           }
         weigh();
       }
-      // ---- transposed into the second product's operand
-      uint32_t pb[NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int h = 0; h < SUBS; ++h) {
+        // ---- transposed into the second product's operand
+        uint32_t pb[NT][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) l[t][e & 1] += y[t][e];
-        pb[t][0] = movmatrix_t(pack2<kBf16Operands>(w[t][0], w[t][1]));
-        pb[t][1] = movmatrix_t(pack2<kBf16Operands>(w[t][2], w[t][3]));
-      }
-      uint32_t v[4][C::VW];
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint8_t* from = smem + ((mine + value_at) ^ (x % 2 * 64)) + (C::RB == 64 ? 0 : x % 2 * C::RB) + C::KV + x / 2 * 8 * C::RB;
-        if constexpr (C::VW == 2) {
-          const uint2 z = *reinterpret_cast<const uint2*>(from);
-          v[x][0] = z.x, v[x][1] = z.y;
-        } else {
+          for (int e = 0; e < 4; ++e) l[t][e & 1] += y[h][t][e];
+          pb[t][0] = movmatrix_t(pack2<kBf16Operands>(w[h][t][0], w[h][t][1]));
+          pb[t][1] = movmatrix_t(pack2<kBf16Operands>(w[h][t][2], w[h][t][3]));
+        }
+        uint32_t v[4][C::VW];
 #pragma unroll
-          for (int i = 0; i < C::VW / 4; ++i) {
-            const uint4 z = *reinterpret_cast<const uint4*>(from + i * 128);
-            v[x][4 * i] = z.x, v[x][4 * i + 1] = z.y, v[x][4 * i + 2] = z.z, v[x][4 * i + 3] = z.w;
+        for (int x = 0; x < 4; ++x) {
+          const uint8_t* from = smem + ((mine + value_at) ^ (x % 2 * 64)) + (C::RB == 64 ? 0 : x % 2 * C::RB) + C::KV +
+                                (x / 2 * 8 + 16 * h) * C::RB;
+          if constexpr (C::VW == 2) {
+            const uint2 z = *reinterpret_cast<const uint2*>(from);
+            v[x][0] = z.x, v[x][1] = z.y;
+          } else {
+#pragma unroll
+            for (int i = 0; i < C::VW / 4; ++i) {
+              const uint4 z = *reinterpret_cast<const uint4*>(from + i * 128);
+              v[x][4 * i] = z.x, v[x][4 * i + 1] = z.y, v[x][4 * i + 2] = z.z, v[x][4 * i + 3] = z.w;
+            }
           }
         }
-      }
-      // ---- O^T += V^T P^T
-      if constexpr (!C::kScaled) {
-        // A value that is not finite, where some row does not see its key: its weight
-        // there is 0, but 0 * NaN is not.  Row by row, with the values that it sees.
-        bool odd = false;
-        if (!whole) {
-          constexpr uint32_t kExp = FMT == PSV_PAGE_BF16 ? 0x7f80u : 0x7c00u;
+        // ---- O^T += V^T P^T
+        if constexpr (!C::kScaled) {
+          // A value that is not finite, where some row does not see its key: its weight
+          // there is 0, but 0 * NaN is not.  Row by row, with the values that it sees.
+          bool odd = false;
+          if (!whole) {
+            constexpr uint32_t kExp = FMT == PSV_PAGE_BF16 ? 0x7f80u : 0x7c00u;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int i = 0; i < C::VW; ++i)
-              odd |= (v[x][i] & kExp) == kExp || (v[x][i] >> 16 & kExp) == kExp;
-        }
-        if (__any_sync(0xffffffffu, odd)) {
+              for (int i = 0; i < C::VW; ++i)
+                odd |= (v[x][i] & kExp) == kExp || (v[x][i] >> 16 & kExp) == kExp;
+          }
+          if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll 1
-            for (int n = 0; n < 8; ++n) {
-              uint32_t see[4];
+              for (int n = 0; n < 8; ++n) {
+                uint32_t see[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) see[x] = sees(8 * t + n, 2 * four + (x & 1) + 8 * (x >> 1)) ? 0xffffffffu : 0u;
+                for (int x = 0; x < 4; ++x)
+                  see[x] = sees(8 * t + n, 16 * h + 2 * four + (x & 1) + 8 * (x >> 1)) ? 0xffffffffu : 0u;
 #pragma unroll
-              for (int i = 0; i < DH / 16; ++i) {
-                const uint32_t z[4] = {v[0][i] & see[0], v[1][i] & see[1], v[2][i] & see[2], v[3][i] & see[3]};
-                const uint32_t a[4] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[0], z[1], 0x7632),
-                                       __byte_perm(z[2], z[3], 0x5410), __byte_perm(z[2], z[3], 0x7632)};
-                float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma<FMT>(add, a, pb[t][0], pb[t][1]);
-                if (n == 2 * four) o[t][i][0] += add[0], o[t][i][2] += add[2];
-                if (n == 2 * four + 1) o[t][i][1] += add[1], o[t][i][3] += add[3];
+                for (int i = 0; i < DH / 16; ++i) {
+                  const uint32_t z[4] = {v[0][i] & see[0], v[1][i] & see[1], v[2][i] & see[2], v[3][i] & see[3]};
+                  const uint32_t a[4] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[0], z[1], 0x7632),
+                                         __byte_perm(z[2], z[3], 0x5410), __byte_perm(z[2], z[3], 0x7632)};
+                  float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma<FMT>(add, a, pb[t][0], pb[t][1]);
+                  if (n == 2 * four) o[t][i][0] += add[0], o[t][i][2] += add[2];
+                  if (n == 2 * four + 1) o[t][i][1] += add[1], o[t][i][3] += add[3];
+                }
               }
-            }
-          continue;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < DH / 16; ++i) {
-        uint32_t a[4];
-        if constexpr (C::kScaled) {
-          const uint32_t sel = i % 2 ? 0x7362 : 0x5140;
-          widen<FMT>(__byte_perm(v[0][i / 2], v[1][i / 2], sel), a[0], a[1]);
-          widen<FMT>(__byte_perm(v[2][i / 2], v[3][i / 2], sel), a[2], a[3]);
-        } else {
-          a[0] = __byte_perm(v[0][i], v[1][i], 0x5410), a[1] = __byte_perm(v[0][i], v[1][i], 0x7632);
-          a[2] = __byte_perm(v[2][i], v[3][i], 0x5410), a[3] = __byte_perm(v[2][i], v[3][i], 0x7632);
+            continue;
+          }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma<FMT>(o[t][i], a, pb[t][0], pb[t][1]);
+        for (int i = 0; i < DH / 16; ++i) {
+          uint32_t a[4];
+          if constexpr (C::kScaled) {
+            const uint32_t sel = i % 2 ? 0x7362 : 0x5140;
+            widen<FMT>(__byte_perm(v[0][i / 2], v[1][i / 2], sel), a[0], a[1]);
+            widen<FMT>(__byte_perm(v[2][i / 2], v[3][i / 2], sel), a[2], a[3]);
+          } else {
+            a[0] = __byte_perm(v[0][i], v[1][i], 0x5410), a[1] = __byte_perm(v[0][i], v[1][i], 0x7632);
+            a[2] = __byte_perm(v[2][i], v[3][i], 0x5410), a[3] = __byte_perm(v[2][i], v[3][i], 0x7632);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma<FMT>(o[t][i], a, pb[t][0], pb[t][1]);
+        }
       }
     }
 
@@ -895,7 +941,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     was_slot = step0 == 0;
     if (!CLUSTER && split && was_slot && threadIdx.x == 0) {
       // (the last cut that is not moved to the group's end)
-      const int shares = cut.of(lo + s.span() - cut.near(s.span())) - static_cast<int>(blockIdx.x) + 1;
+      const int shares = cut.of(lo + s.span - cut.near(s.span)) - static_cast<int>(blockIdx.x) + 1;
       p.shared[blockIdx.x] = Shared{n_rows, shares, b, kvh, r0};
     }
     lo += taken;
@@ -993,13 +1039,13 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   // 26.1 and 26.8, 7800 44 and 36; 384 of 500 (12) 18.8 and 21.1, 1000 (22) 29.3 and 27.7.
   const int64_t tiles = (static_cast<int64_t>(p.Lq) * p.G + C::ROWS - 1) / C::ROWS;
   p.groups = p.B * p.Hkv * tiles;
-  const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * kStep)
-                                  : p.c.positions) / kStep + 1;
-  p.quick = p.B <= 1024 && p.groups * (p.c.positions / kStep + 3 + kStart) < (int64_t{1} << 31);
+  const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.Lq + p.sinks + 2 * C::STEP)
+                                  : p.c.positions) / C::STEP + 1;
+  p.quick = p.B <= 1024 && p.groups * (p.c.positions / C::STEP + 3 + C::START) < (int64_t{1} << 31);
   p.cluster = 1;
   while (p.cluster < 8 && p.groups * p.cluster * 2 <= kMaxCtas && p.cluster * C::WARPS < steps) p.cluster *= 2;
   const int64_t rounds = (p.groups * p.cluster + kMaxCtas - 1) / kMaxCtas * ((steps + p.cluster * C::WARPS - 1) / (p.cluster * C::WARPS));
-  return rounds <= kRounds ? launch<DH, FMT, NT, true>(p, sms, st) : launch<DH, FMT, NT, false>(p, sms, st);
+  return rounds * C::SUBS <= kRounds ? launch<DH, FMT, NT, true>(p, sms, st) : launch<DH, FMT, NT, false>(p, sms, st);
 }
 
 template <int DH, int FMT>
