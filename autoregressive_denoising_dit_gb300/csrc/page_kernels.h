@@ -49,7 +49,15 @@ __device__ __forceinline__ PageRow page_row(const PageCacheDev& c, int b, int64_
   return PageRow{page < c.n_pages ? page : -1, static_cast<int>(static_cast<uint32_t>(pos) - at * c.by_page.d)};
 }
 
-struct Shared;
+// A group (a sequence's kv head and tile of query rows) that CTA `i` of the attention's grid
+// begins and does not end: its rows (0: there is none) and how many CTAs have shares of it.
+struct alignas(32) PageShared {
+  int rows, shares, b, kvh, r0;
+};
+constexpr int kCtasSm = 2;
+constexpr int kMaxCtas = 152 * kCtasSm;  // shares in the workspace
+// Floats of a share: O, then m', m, l of each row.
+constexpr int share_floats(int dh, int rows) { return rows * (dh + 4); }
 
 // The attention's arguments.
 struct PageAttnParams {
@@ -69,7 +77,7 @@ struct PageAttnParams {
   int cluster;            // page_attn.cu: CTAs that share a group without cutting it
   int quick;              // at most 1024 sequences and 2^31 steps
   int64_t groups;         // kv heads and tiles of rows of all sequences, at most
-  Shared* shared;  // page_attn.cu: the groups that several CTAs share
+  PageShared* shared;  // page_attn.cu: the groups that several CTAs share
   float* part;            // their shares
 };
 
@@ -90,5 +98,8 @@ cudaError_t launch_page_attention_general(const PageAttnParams& p, cudaStream_t 
 size_t page_attn_scratch(const PageAttnParams& p);
 void page_attn_scratch(PageAttnParams& p, void* scratch);
 cudaError_t launch_page_attention(const PageAttnParams& p, int sms, cudaStream_t st);
+// Of heads of up to DH, in a translation unit for each width and size of values.
+template <int DH, int FMT>
+cudaError_t launch_page_rows(const PageAttnParams& p, int sms, cudaStream_t st);
 
 }  // namespace psv

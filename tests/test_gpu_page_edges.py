@@ -554,3 +554,47 @@ def test_calls_from_four_threads(P):
     for t in threads:
         t.join()
     assert not bad, bad
+
+
+@pytest.mark.parametrize("dh,Lq", [(128, 4), (64, 7), (256, 2)])
+@pytest.mark.parametrize("f", ["bf16", "f16", "e4m3"])
+def test_many_copies_of_a_sequence(P, f, dh, Lq):
+    """700 copies (a warp has each): all the same, as the definition has it, infinite values that some rows see too."""
+    dtype = "f16" if f == "f16" else "bf16"
+    c = dict(B=1, Lq=Lq, Lk=60, Hq=4, Hkv=2, dh=dh, page=16, causal=True)
+    cache, q, (k, v), lens, total, rows = attention_case(P, c, dtype, f)
+    hit = torch.zeros(Lq, 4, dh, dtype=torch.bool, device="cuda")
+    if f in DT:  # the last row's own value
+        e, r = int(cache.table[0, 59 // 16]), 59 % 16
+        cache.v[e, 0, r, 7], cache.v[e, 1, r, 9] = INF, float("nan")
+        v[0, 59, 0, 7] = v[0, 59, 1, 9] = 0
+        hit[-1, :2, 7] = hit[-1, 2:, 9] = True
+    want_o, tol, want_lse, ltol = reference(cache, c, q, k, v, total, rows)[0]
+    d = cache.desc()
+    d.B, d.table_stride = 700, 0
+    cache.desc = lambda: d
+    o, lse = run_attention(P, dict(c, B=700), cache, q.expand(700, -1, -1, -1).contiguous(), lens * 700, rows * 700, dtype)
+    assert torch.equal(torch.nan_to_num(o.float(), 3e4, 2e4), torch.nan_to_num(o[:1].float(), 3e4, 2e4).expand_as(o)) and torch.equal(lse, lse[:1].expand_as(lse))
+    assert ((o[0].double() - want_o).abs() <= tol)[~hit].all() and not torch.isfinite(o[0][hit].float()).any()
+    assert ((lse[0].T.double() - want_lse).abs() <= ltol).all()
+
+
+def test_a_captured_step_of_many_sequences(P):
+    eager, graphed = (Decoder(P, B=300, Hq=4, Hkv=2, max_pages=3) for _ in range(2))
+    start = ints([b % 22 for b in range(300)])
+    gens = [torch.Generator(device="cuda").manual_seed(7) for _ in range(2)]
+    x = torch.randn(300, 22, 2, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    for d in (eager, graphed):
+        P.psv_page_write(d.desc, P.page_rows(P.PSV_DTYPE_BF16, x.shape, lens=at(start)), at(x), at(x), stream())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed.step()
+    for d in (eager, graphed):
+        d.before.copy_(start)
+    for _ in range(30):  # some pass the ends of their tables
+        eager.feed(gens[0])
+        eager.step()
+        graphed.feed(gens[1])
+        graph.replay()
+        assert torch.equal(eager.o, graphed.o) and torch.equal(eager.lse, graphed.lse)

@@ -373,6 +373,13 @@ ATTN = [
     dict(B=2, Lq=4, Lk=128, Hq=2, Hkv=2, dh=128, page=64, causal=True, append=True, lens=[126, 60], rows=[4, 1]),  # over the table
     dict(B=70, Lq=1, Lk=200, Hq=2, Hkv=1, dh=64, page=16, lens=[(b * 37) % 201 for b in range(70)]),
     dict(B=2, Lq=20, Lk=600, Hq=3, Hkv=1, dh=128, page=64, causal=True, rows=[20, 7]),
+    # many short sequences: a warp has a group by itself
+    dict(B=300, Lq=1, Lk=50, Hq=8, Hkv=4, dh=128, page=16, lens=[(b * 7) % 51 for b in range(300)]),
+    dict(B=200, Lq=3, Lk=40, Hq=24, Hkv=6, dh=128, page=8, causal=True, lens=[40 - b % 40 for b in range(200)], rows=[b % 4 for b in range(200)]),
+    dict(B=260, Lq=2, Lk=70, Hq=10, Hkv=5, dh=64, page=24, causal=True, window=20, sinks=3, missing=[(b, b % 3) for b in range(0, 260, 7)]),
+    dict(B=250, Lq=1, Lk=37, Hq=6, Hkv=6, dh=72, page=7, cap=4.0),
+    dict(B=300, Lq=5, Lk=33, Hq=8, Hkv=4, dh=64, page=16, causal=True),
+    dict(B=300, Lq=1, Lk=33, Hq=8, Hkv=4, dh=200, page=16, lens=[b % 34 for b in range(300)]),
     dict(B=1, Lq=1, Lk=20000, Hq=4, Hkv=1, dh=128, page=64),
     dict(B=1, Lq=4, Lk=9000, Hq=16, Hkv=4, dh=64, page=32, causal=True),
 ]
