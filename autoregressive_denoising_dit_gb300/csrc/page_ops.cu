@@ -183,7 +183,7 @@ struct RowMap {
 // grid (tokens x groups of heads, sequence, key or value).  The first reads do not wait
 // for the lengths: rows not in use are read too.
 // Memory-bound where large: 12480 rows x 40 heads of 128 in f32 to 8 bits 91 us (7.1 TB/s),
-// in bf16 65 us (5.9); four sequences of 1560 rows x 12 heads in bf16 13 us.
+// in bf16 67 us (5.8); four sequences of 1560 rows x 12 heads in bf16 13 us.
 template <class T, int FMT, bool VEC, bool MANY>
 __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
 }
 
 // The same threads read rows back; positions without a page read as zeros.  Memory-bound:
-// eight sequences of 4836 rows x 40 heads of 128 from 8 bits 178 us (6.8 TB/s).
+// eight sequences of 4836 rows x 40 heads of 128 from 8 bits 177 us (6.8 TB/s).
 template <class T, int FMT, bool VEC, bool MANY>
 __global__ void __launch_bounds__(kRowThreads) page_read_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
