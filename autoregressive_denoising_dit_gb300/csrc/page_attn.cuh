@@ -54,7 +54,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 256.0f;  // weights above it take up a new maximum
 constexpr float kNone = -FLT_MAX;   // a maximum of nothing: exp2(-inf - kNone) = 0, exp2(kNone - kNone) = 1
 
-constexpr bool STEP2(int dh, bool scaled, int nt) { return scaled && (dh == 64 || (dh == 128 && nt == 2)); }
+constexpr bool two_products(int dh, bool scaled, int nt) { return scaled && (dh == 64 || (dh == 128 && nt == 2)); }
 
 template <int DH, int FMT, int NT>
 struct ACfg {
@@ -64,28 +64,30 @@ struct ACfg {
   static constexpr int KP = DH * ES / 64;   // 16-byte pieces of a key in a thread
   static constexpr int KS = kScaled ? 4 : 2;  // products (of 16 values) a piece
   static constexpr int VW = DH * ES / 32;   // 4-byte words of a value in a thread
-  static constexpr bool QS = NT == 2 || DH == 256;  // queries in shared memory, for want of registers
+  static constexpr bool QS = NT >= 2 || DH == 256;  // queries in shared memory, for want of registers
   static constexpr int Q_BYTES = QS ? NT * KP * KS * 256 + ROWS * 4 : 0;  // operands, a factor a row
   static constexpr int JSTRIDE = DH + 4;    // floats between a join area's rows
   static constexpr int RB = DH * ES;       // bytes of a row
   static constexpr int LPR = RB / 16;      // lanes that copy it
   static constexpr int RPC = 32 / LPR;     // rows of a copy
   // Keys of a warp's step: 16 a product, twice as many where that costs no step ahead.
-  static constexpr int SUBS = STEP2(DH, kScaled, NT) ? 2 : 1, STEP = 16 * SUBS;
+  static constexpr int SUBS = two_products(DH, kScaled, NT) ? 2 : 1, STEP = 16 * SUBS;
   static constexpr int START = 8 / SUBS;   // steps on the line that a group's start counts for
   static constexpr int KV = STEP * RB;     // a step's keys, or values
   static constexpr int SLOT = 2 * KV + (kScaled ? STEP * 8 : 0);  // a warp's step: K, V, the scales
-  // Two CTAs an SM: 128, 168 or 255 registers a thread.
-  static constexpr int WARPS = DH == 256 ? (kScaled ? 3 : 2) : NT == 1 && DH == 64 && !kScaled ? 8 : (NT == 1 && kScaled) || DH == 64 ? 6 : 4;
+  // Two CTAs an SM (128, 168 or 255 registers a thread), or one of four tiles, whose shares
+  // are twice as large.
+  static constexpr int CTAS = NT == 4 ? 1 : 2, MAX_CTAS = kSms * CTAS;
+  static constexpr int WARPS = NT == 4 ? 8 : DH == 256 ? (kScaled ? 3 : 2) : NT == 1 && DH == 64 && !kScaled ? 8 : (NT == 1 && kScaled) || DH == 64 ? 6 : 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int JOIN = WARPS * 8 * (JSTRIDE + 4) * 4;  // the warps' sums at the end of a group, a tile at a time
-  static constexpr int STAGES = std::min(4, ((112 << 10) - JOIN - Q_BYTES - ROWS * (DH + 4) * 4) / (WARPS * SLOT));
+  static constexpr int STAGES = std::min(4, ((224 << 10) / CTAS - JOIN - Q_BYTES - ROWS * (DH + 4) * 4) / (WARPS * SLOT));
   static constexpr int RING = WARPS * STAGES * SLOT;
   static_assert(STAGES >= 2 && WARPS >= NT, "a step ahead, a warp a tile of queries");
   static constexpr int PART = ROWS * (DH + 4) * 4;  // a CTA's sums, which its cluster reads
   static constexpr int SMEM = RING + JOIN + Q_BYTES + PART;
-  static_assert(2 * (SMEM + 1024 + 256) <= 233472, "two CTAs an SM");
-  static_assert(WARPS * Q_BYTES <= JOIN, "a warp's own queries, in the join's place");
+  static_assert(CTAS * (SMEM + 1024 + 256) <= 233472, "an SM's shared memory");
+  static_assert(NT == 4 || WARPS * Q_BYTES <= JOIN, "a warp's own queries, in the join's place");
 };
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -229,7 +231,7 @@ struct Cut {
     if (n) each = divide(a, n), more = static_cast<int>(a - each * n);
   }
   __device__ __forceinline__ int64_t begin(int cta) const {
-    return each * cta + static_cast<int>(__fdiv_rn(static_cast<float>(more * cta), static_cast<float>(ctas)));  // (exact: < 2^17)
+    return each * cta + static_cast<int>(__fdiv_rn(static_cast<float>(more * cta), static_cast<float>(ctas)));  // (exact: < 2^23)
   }
   // A cut this near to an end of its group is moved there, so that fewer CTAs have
   // shares of two groups, and none has a start alone.
@@ -275,7 +277,7 @@ __device__ __forceinline__ void add_share(float& mm_o, float& mm_l, float& ll, f
 }
 
 template <int DH, int FMT, int NT, int MODE>
-__global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
+__global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>::CTAS)
     page_attn_kernel(const __grid_constant__ PageAttnParams p) {
   using C = ACfg<DH, FMT, NT>;
   constexpr bool CLUSTER = MODE == kClusters, WARP = MODE == kAlone, WHOLE = MODE != kCut;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
           const int r = 8 * t + 2 * four + x;
           if (r >= was_rows) continue;
-          const float ll = l[t][x], f = finish(mo[t][x], ml[t][x], ll);
+          const float ll = l[t][x], f = finish(C::kScaled ? mo[t][x] : ml[t][x], ml[t][x], ll);
           const int tok = p.by_group.div(was_r0 + r), head = was_kvh * p.G + was_r0 + r - tok * p.G;
           uint16_t* out = static_cast<uint16_t*>(p.o) + was_b * p.os.b + tok * p.os.l + head * p.os.h;
 #pragma unroll
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
               *reinterpret_cast<float2*>(row + d) = make_float2(o[t][i][x], o[t][i][2 + x]);
             }
             if (quad == 0)
-              *reinterpret_cast<float4*>(sm + (warp * 8 + r) * 4) = make_float4(mo[t][x], ml[t][x], l[t][x], 0.0f);
+              *reinterpret_cast<float4*>(sm + (warp * 8 + r) * 4) = make_float4(C::kScaled ? mo[t][x] : ml[t][x], ml[t][x], l[t][x], 0.0f);
           }
         }
         __syncthreads();
@@ -737,7 +739,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
     else if constexpr (C::QS) __syncwarp();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (C::QS) up[t][0] = sq_up[8 * t + 2 * four], up[t][1] = sq_up[8 * t + 2 * four + 1];
+      if (C::QS && NT < 4) up[t][0] = sq_up[8 * t + 2 * four], up[t][1] = sq_up[8 * t + 2 * four + 1];
 #pragma unroll
       for (int i = 0; i < DH / 16; ++i)
 #pragma unroll
@@ -800,7 +802,6 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
       }
       // ---- scores and weights' exponents in the log2 domain
       const int key0 = key_of(step);
-      float u[SUBS][NT][4];
 #pragma unroll
       for (int h = 0; h < SUBS; ++h) {
         float ks[2] = {1.0f, 1.0f};
@@ -809,9 +810,11 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
           ks[0] = scales[quad], ks[1] = scales[quad + 8];
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+          if (NT == 4) up[t][0] = sq_up[8 * t + 2 * four], up[t][1] = sq_up[8 * t + 2 * four + 1];
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[h][t][e] = (C::kScaled ? sc[h][t][e] * ks[e >> 1] : sc[h][t][e]) * up[t][e & 1];
+        }
       }
       if (p.softcap > 0) {
         float big = 0.0f;
@@ -824,18 +827,6 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         if (__all_sync(0xffffffffu, big * p.cap.inv <= 1.0f)) cap_within<4 * NT * SUBS>(&sc[0][0][0], p.cap);
         else cap_any<4 * NT * SUBS>(&sc[0][0][0], p.cap);
       }
-#pragma unroll
-      for (int h = 0; h < SUBS; ++h) {
-        float lv[2] = {0.0f, 0.0f};
-        if constexpr (C::kScaled) {
-          const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV) + kStep + 16 * h;
-          lv[0] = fast_log2(scales[quad]), lv[1] = fast_log2(scales[quad + 8]);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) u[h][t][e] = C::kScaled ? sc[h][t][e] + lv[e >> 1] : sc[h][t][e];
-      }
       const bool whole = (key0 + kStep <= all_end && (key0 >= all_first || key0 + kStep <= sinks)) && there == 0xffffffffu;
       // whether row r of the tile sees the step's key
       auto sees = [&](int r, int key) {
@@ -843,67 +834,95 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
         return r < n_rows && ((there >> key) & 1) && j < (p.causal ? min(at_row + 1, s.keys) : s.keys) &&
                (!p.window || j > at_row - p.window || j < sinks);
       };
-      if (!whole) {
+      // ---- weights, two tiles at a time, and the second product's operand
+      uint32_t pb[SUBS][NT][2];
+      constexpr int kPair = NT < 2 ? NT : 2;
 #pragma unroll
-        for (int h = 0; h < SUBS; ++h)
+      for (int t0 = 0; t0 < NT; t0 += kPair) {
+        if (t0 && 8 * t0 >= n_rows) {  // (no rows there)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+          for (int h = 0; h < SUBS; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!sees(8 * t + 2 * four + (e & 1), 16 * h + quad + 8 * (e >> 1))) sc[h][t][e] = -INFINITY, u[h][t][e] = -INFINITY;
-      }
-      // ---- weights; a new maximum is taken up where one passes the old one by far
-      float w[SUBS][NT][4], y[SUBS][NT][4];
-      auto weigh = [&]() {
-        float big = 0.0f;
+            for (int t = t0; t < t0 + kPair; ++t) pb[h][t][0] = pb[h][t][1] = 0;
+          continue;
+        }
+        float u[SUBS][kPair][4];
 #pragma unroll
-        for (int h = 0; h < SUBS; ++h)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[h][t][e] = fast_exp2(sc[h][t][e] - ml[t][e & 1]);
-              w[h][t][e] = C::kScaled ? fast_exp2(u[h][t][e] - mo[t][e & 1]) : y[h][t][e];
-              big = fmaxf(big, fmaxf(y[h][t][e], w[h][t][e]));
-            }
-        return big;
-      };
-      if (__any_sync(0xffffffffu, weigh() > kRescale)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float a = fmaxf(sc[0][t][x], sc[0][t][2 + x]), d = fmaxf(u[0][t][x], u[0][t][2 + x]);
-            if (SUBS > 1) {
-              a = fmaxf(a, fmaxf(sc[SUBS - 1][t][x], sc[SUBS - 1][t][2 + x]));
-              d = fmaxf(d, fmaxf(u[SUBS - 1][t][x], u[SUBS - 1][t][2 + x]));
-            }
-#pragma unroll
-            for (int i = 4; i < 32; i <<= 1) {
-              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, i));
-              if (C::kScaled) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, i));
-            }
-            a = fmaxf(a, ml[t][x]);
-            d = C::kScaled ? fmaxf(d, mo[t][x]) : a;
-            l[t][x] *= fast_exp2(ml[t][x] - a);
-            const float f = fast_exp2(mo[t][x] - d);
-            ml[t][x] = a, mo[t][x] = d;
-#pragma unroll
-            for (int i = 0; i < DH / 16; ++i) o[t][i][x] *= f, o[t][i][2 + x] *= f;
+        for (int h = 0; h < SUBS; ++h) {
+          float lv[2] = {0.0f, 0.0f};
+          if constexpr (C::kScaled) {
+            const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV) + kStep + 16 * h;
+            lv[0] = fast_log2(scales[quad]), lv[1] = fast_log2(scales[quad + 8]);
           }
-        weigh();
+#pragma unroll
+          for (int t = 0; t < kPair; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[h][t][e] = C::kScaled ? sc[h][t0 + t][e] + lv[e >> 1] : sc[h][t0 + t][e];
+        }
+        if (!whole) {
+#pragma unroll
+          for (int h = 0; h < SUBS; ++h)
+#pragma unroll
+            for (int t = 0; t < kPair; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!sees(8 * (t0 + t) + 2 * four + (e & 1), 16 * h + quad + 8 * (e >> 1)))
+                  sc[h][t0 + t][e] = -INFINITY, u[h][t][e] = -INFINITY;
+        }
+        // a new maximum is taken up where one passes the old one by far
+        float w[SUBS][kPair][4], y[SUBS][kPair][4];
+        auto weigh = [&]() {
+          float big = 0.0f;
+#pragma unroll
+          for (int h = 0; h < SUBS; ++h)
+#pragma unroll
+            for (int t = 0; t < kPair; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[h][t][e] = fast_exp2(sc[h][t0 + t][e] - ml[t0 + t][e & 1]);
+                w[h][t][e] = C::kScaled ? fast_exp2(u[h][t][e] - mo[t0 + t][e & 1]) : y[h][t][e];
+                big = fmaxf(big, fmaxf(y[h][t][e], w[h][t][e]));
+              }
+          return big;
+        };
+        if (__any_sync(0xffffffffu, weigh() > kRescale)) {
+#pragma unroll
+          for (int t = 0; t < kPair; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float a = fmaxf(sc[0][t0 + t][x], sc[0][t0 + t][2 + x]), d = fmaxf(u[0][t][x], u[0][t][2 + x]);
+              if (SUBS > 1) {
+                a = fmaxf(a, fmaxf(sc[SUBS - 1][t0 + t][x], sc[SUBS - 1][t0 + t][2 + x]));
+                d = fmaxf(d, fmaxf(u[SUBS - 1][t][x], u[SUBS - 1][t][2 + x]));
+              }
+#pragma unroll
+              for (int i = 4; i < 32; i <<= 1) {
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, i));
+                if (C::kScaled) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, i));
+              }
+              a = fmaxf(a, ml[t0 + t][x]);
+              if (C::kScaled) d = fmaxf(d, mo[t0 + t][x]);
+              const float g = fast_exp2(ml[t0 + t][x] - a), f = C::kScaled ? fast_exp2(mo[t0 + t][x] - d) : g;
+              l[t0 + t][x] *= g;
+              ml[t0 + t][x] = a;
+              if (C::kScaled) mo[t0 + t][x] = d;
+#pragma unroll
+              for (int i = 0; i < DH / 16; ++i) o[t0 + t][i][x] *= f, o[t0 + t][i][2 + x] *= f;
+            }
+          weigh();
+        }
+#pragma unroll
+        for (int h = 0; h < SUBS; ++h)
+#pragma unroll
+          for (int t = 0; t < kPair; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l[t0 + t][e & 1] += y[h][t][e];
+            pb[h][t0 + t][0] = movmatrix_t(pack2<kBf16Operands>(w[h][t][0], w[h][t][1]));
+            pb[h][t0 + t][1] = movmatrix_t(pack2<kBf16Operands>(w[h][t][2], w[h][t][3]));
+          }
       }
 #pragma unroll
       for (int h = 0; h < SUBS; ++h) {
-        // ---- transposed into the second product's operand
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) l[t][e & 1] += y[h][t][e];
-          pb[t][0] = movmatrix_t(pack2<kBf16Operands>(w[h][t][0], w[h][t][1]));
-          pb[t][1] = movmatrix_t(pack2<kBf16Operands>(w[h][t][2], w[h][t][3]));
-        }
         uint32_t v[4][C::VW];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -948,7 +967,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
                   const uint32_t a[4] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[0], z[1], 0x7632),
                                          __byte_perm(z[2], z[3], 0x5410), __byte_perm(z[2], z[3], 0x7632)};
                   float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma<FMT>(add, a, pb[t][0], pb[t][1]);
+                  mma<FMT>(add, a, pb[h][t][0], pb[h][t][1]);
                   if (n == 2 * four) o[t][i][0] += add[0], o[t][i][2] += add[2];
                   if (n == 2 * four + 1) o[t][i][1] += add[1], o[t][i][3] += add[3];
                 }
@@ -968,7 +987,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, kCtasSm)
             a[2] = __byte_perm(v[2][i], v[3][i], 0x5410), a[3] = __byte_perm(v[2][i], v[3][i], 0x7632);
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma<FMT>(o[t][i], a, pb[t][0], pb[t][1]);
+          for (int t = 0; t < NT; ++t) mma<FMT>(o[t][i], a, pb[h][t][0], pb[h][t][1]);
         }
       }
     }
@@ -1044,7 +1063,7 @@ cudaError_t launch(const PageAttnParams& p, int sms, cudaStream_t st) {
     return cudaFuncSetAttribute(page_attn_kernel<DH, FMT, NT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
-  const int most = std::min(sms * kCtasSm, kMaxCtas);
+  const int most = std::min(sms, kSms) * C::CTAS;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1067,6 +1086,19 @@ cudaError_t launch(const PageAttnParams& p, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, page_join_kernel<DH>, p, C::ROWS);
 }
 
+// Whether 16-bit pages of heads of 128 are read once for 32 rows (2.1 us a step of all an
+// SM's warps, two products of 16 rows each) instead of for 16 (1.4 us, which is what L2
+// gives): where that is less in all, for groups of 4000 keys at least and 12 steps a warp,
+// as these CTAs are an SM's only ones and their warps take no groups alone.  Measured, 8 x
+// 7800 keys of 12 heads, 32 rows 92 and 128 us, 48 156 and 134, 64 164 and 237, 96 226 and
+// 254; 64 groups of 4000 37 and 49, 256 of 1000 59 and 56; 8 of 17600 30 and 28.  (In 8 bits
+// 32 rows take 93 us and 79: steps of 32 keys hide more of the conversions.)
+inline bool four_tiles(const PageAttnParams& p) {
+  const int64_t rows = static_cast<int64_t>(p.Lq) * p.G, two = (rows + 15) / 16, four = (rows + 31) / 32;
+  const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.sinks) : p.c.positions) / 16;
+  return 21 * four < 14 * two && steps >= 240 && p.B * p.Hkv * four * steps >= 12 * 8 * kSms;
+}
+
 template <int DH, int FMT, int NT>
 cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   using C = ACfg<DH, FMT, NT>;
@@ -1078,7 +1110,7 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   p.quick = p.B <= 1024 && p.groups * (p.c.positions / C::STEP + 3 + C::START) < (int64_t{1} << 31);
   // As many CTAs a group as there is room for, at most 8.
   p.cluster = 1;
-  while (p.cluster < 8 && p.groups * p.cluster * 2 <= kMaxCtas && p.cluster * C::WARPS < steps) p.cluster *= 2;
+  while (p.cluster < 8 && p.groups * p.cluster * 2 <= C::MAX_CTAS && p.cluster * C::WARPS < steps) p.cluster *= 2;
   // What the modes would take, in us: rounds of groups, each with its steps (t: all warps'
   // in turn at 44 kB an SM and us) and its start and end.  Measured, 8-bit heads of 128:
   //   clusters against cuts: 12 groups of 1000 keys 7.4 and 12.1 us, 4000 10.8 and 12.5, 8000
@@ -1086,13 +1118,15 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   //   warps alone against cuts: 2048 groups of 250 keys 39 and 46 us, 8000 of 300 119 and 177,
   //   1000 of 300 22 and 40, 8198 of 100 78 and 178
   auto rounds = [](int64_t n, int64_t d) { return static_cast<double>((n + d - 1) / d); };
-  const double t = 2.0 * C::WARPS * C::SLOT / 44e3;
-  const double alone = rounds(p.groups, kMaxCtas * C::WARPS) * (steps * t + 3.3);
+  const double t = 1.0 * C::CTAS * C::WARPS * C::SLOT / 44e3;
+  const double alone = rounds(p.groups, C::MAX_CTAS * C::WARPS) * (steps * t + 3.3);
   // (Clusters of one do worse than this where lengths are uneven: 2048 groups of 235 to 1000
   // keys 91 us, cuts 83; all of 1000 97 and 101.)
-  const double clusters = (p.cluster == 1 ? 1.1 : 1.0) * rounds(p.groups * p.cluster, kMaxCtas) * (rounds(steps, p.cluster * C::WARPS) * t + 5.5);
-  const double cut = static_cast<double>(p.groups) / kMaxCtas * (steps * t / C::WARPS + 5.0) + 11.0;
-  if (alone < std::min(clusters, cut)) return launch<DH, FMT, NT, kAlone>(p, sms, st);
+  const double clusters = (p.cluster == 1 ? 1.1 : 1.0) * rounds(p.groups * p.cluster, C::MAX_CTAS) * (rounds(steps, p.cluster * C::WARPS) * t + 5.5);
+  const double cut = static_cast<double>(p.groups) / C::MAX_CTAS * (steps * t / C::WARPS + 5.0) + 11.0;
+  if constexpr (NT < 4) {  // (four tiles' queries do not fit a warp's registers beside their sums)
+    if (alone < std::min(clusters, cut)) return launch<DH, FMT, NT, kAlone>(p, sms, st);
+  }
   return clusters < cut ? launch<DH, FMT, NT, kClusters>(p, sms, st) : launch<DH, FMT, NT, kCut>(p, sms, st);
 }
 
@@ -1101,6 +1135,9 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
 template <int DH, int FMT>
 cudaError_t launch_page_rows(const PageAttnParams& p, int sms, cudaStream_t st) {
   if constexpr (DH < 256) {  // (the sums of 16 rows of 256 values do not fit the registers)
+    if constexpr (DH == 128 && (FMT == PSV_PAGE_BF16 || FMT == PSV_PAGE_F16)) {
+      if (four_tiles(p)) return launch_tile<DH, FMT, 4>(p, sms, st);
+    }
     if (p.Lq * p.G > 8) return launch_tile<DH, FMT, 2>(p, sms, st);
   }
   return launch_tile<DH, FMT, 1>(p, sms, st);

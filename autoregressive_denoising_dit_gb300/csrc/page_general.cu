@@ -1,6 +1,6 @@
 // Attention of any number of rows over a paged cache for every layout, head
 // width and alignment the call accepts: plain loads, one warp per row, 32-bit
-// arithmetic throughout.  page_attn.cu takes the aligned problems; this one is
+// arithmetic throughout.  page_attn.cuh takes the aligned problems; this one is
 // bound by its uncoalesced loads, which it repeats for every row (a fallback for
 // odd layouts, not tuned): two tokens over 2000 keys of 12 heads of 100 750 us, of 256
 // in the other kernel 13.

@@ -54,8 +54,8 @@ __device__ __forceinline__ PageRow page_row(const PageCacheDev& c, int b, int64_
 struct alignas(32) PageShared {
   int rows, shares, b, kvh, r0;
 };
-constexpr int kCtasSm = 2;
-constexpr int kMaxCtas = 152 * kCtasSm;  // shares in the workspace
+constexpr int kSms = 152;
+constexpr int kMaxCtas = 2 * kSms;  // shares in the workspace (of 32 rows: half as many)
 // Floats of a share: O, then m', m, l of each row.
 constexpr int share_floats(int dh, int rows) { return rows * (dh + 4); }
 
@@ -66,18 +66,18 @@ struct PageAttnParams {
   int causal, window, sinks, append, bf16;
   float scale, softcap;
   FastDiv by_group;                 // by G
-  int halves;                       // page_attn.cu: 8-bit rows are aligned to 8 bytes only
-  uint32_t kb, kl, vb, vl, sb, sl;  // page_attn.cu: strides of a page and a row in bytes
+  int halves;                       // page_attn.cuh: 8-bit rows are aligned to 8 bytes only
+  uint32_t kb, kl, vb, vl, sb, sl;  // page_attn.cuh: strides of a page and a row in bytes
   CapForm cap;
   Strides3 qs, os;
   const void* q;
   void* o;
   float* lse;  // or null
   const int32_t *q_lens, *k_lens;
-  int cluster;            // page_attn.cu: CTAs that share a group without cutting it
+  int cluster;            // page_attn.cuh: CTAs that share a group without cutting it
   int quick;              // at most 1024 sequences and 2^31 steps
   int64_t groups;         // kv heads and tiles of rows of all sequences, at most
-  PageShared* shared;  // page_attn.cu: the groups that several CTAs share
+  PageShared* shared;     // page_attn.cuh: the groups that several CTAs share
   float* part;            // their shares
 };
 

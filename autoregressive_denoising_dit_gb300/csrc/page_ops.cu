@@ -548,7 +548,9 @@ PageAttnParams page_attn_params(const psv_page_cache* c, const psv_page_query* q
   p.c = page_cache_dev(c);
   p.B = c->B, p.Hq = q->Hq, p.Hkv = c->Hkv, p.G = q->Hq / c->Hkv, p.dh = c->dh, p.Lq = q->Lq;
   // (a window over every position that rows may stand at is none)
-  p.causal = q->causal != 0, p.window = q->window < (1 << 30) + (1 << 21) ? q->window : (1 << 30) + (1 << 21), p.sinks = q->sinks, p.append = q->append != 0;
+  const int most = (1 << 30) + (1 << 21);
+  p.causal = q->causal != 0, p.append = q->append != 0;
+  p.window = q->window < most ? q->window : most, p.sinks = q->sinks;
   p.bf16 = q->dtype == PSV_DTYPE_BF16;
   p.scale = q->scale > 0 ? q->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c->dh)));
   p.softcap = q->softcap;
@@ -611,7 +613,8 @@ PSV_API int psv_page_attention(const psv_page_cache* c, const psv_page_query* q,
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int es = page_esize(c->format);
   auto small = [](const int64_t* st, int size) { return st[0] * size < int64_t{1} << 32 && st[1] * size < int64_t{1} << 32; };
-  if (page_attn_pieces(c) && small(c->k_stride, es) && small(c->v_stride, es) && (es == 2 || small(c->scale_stride, 4)) && multiple16(x, q->q_stride, c->B, q->Lq, q->Hq, 2) &&
+  if (page_attn_pieces(c) && small(c->k_stride, es) && small(c->v_stride, es) &&
+      (es == 2 || small(c->scale_stride, 4)) && multiple16(x, q->q_stride, c->B, q->Lq, q->Hq, 2) &&
       multiple16(o, q->o_stride, c->B, q->Lq, q->Hq, 2) &&
       multiple_of(es * 8, c->k_pages, c->k_stride, c->n_pages, c->page_size, c->Hkv, es) &&
       multiple_of(es * 8, c->v_pages, c->v_stride, c->n_pages, c->page_size, c->Hkv, es)) {

@@ -598,3 +598,39 @@ def test_a_captured_step_of_many_sequences(P):
         graphed.feed(gens[1])
         graph.replay()
         assert torch.equal(eager.o, graphed.o) and torch.equal(eager.lse, graphed.lse)
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
+@pytest.mark.parametrize("f", ["bf16", "f16"])
+@pytest.mark.parametrize("Lq", [24, 37])
+def test_an_infinite_value_and_many_rows(P, f, width, Lq):
+    c = dict(B=1, Lq=Lq, Lk=90, Hq=4, Hkv=4, dh=128, page=16, causal=True)
+    cache, q, (k, v), lens, total, rows = attention_case(P, c, f, f, width=width)
+    e, r = int(cache.table[0, 84 // 16]), 84 % 16
+    cache.v[e, 0, r, 7] = INF
+    cache.v[e, 1, r, 9] = float("nan")
+    v2 = v.clone()
+    v2[0, 84, 0, 7] = v2[0, 84, 1, 9] = 0
+    o, lse = run_attention(P, c, cache, q, lens, rows, f)
+    want_o, tol, want_lse, ltol = reference(cache, c, q, k, v2, total, rows)[0]
+    first = 84 - (90 - Lq)
+    assert (o[0, first:, 0, 7] == INF).all() and torch.isnan(o[0, first:, 1, 9].float()).all()
+    hit = torch.zeros(o.shape[1:], dtype=torch.bool, device="cuda")
+    hit[first:, 0, 7] = hit[first:, 1, 9] = True
+    assert ((o[0].double() - want_o).abs() <= tol)[~hit].all()
+    assert ((lse[0].T.double() - want_lse).abs() <= ltol).all()
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
+@pytest.mark.parametrize("f", ["e4m3", "i8"])
+def test_scales_of_any_size_and_many_rows(P, f, width):
+    c = dict(B=2, Lq=7, Lk=333, Hq=6, Hkv=2, dh=64, page=64, causal=True, lens=[333, 100], rows=[7, 6])
+    cache, q, _, lens, total, rows = attention_case(P, c, "f16", f, width=width)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k, v = (torch.randn(2, 333, 2, 64, device="cuda", generator=g) for _ in range(2))
+    v = v * torch.exp2(torch.randint(-60, 0, (2, 333, 2, 1), device="cuda", generator=g).float())
+    k = k * torch.exp2(torch.randint(-40, 1, (2, 333, 2, 1), device="cuda", generator=g).float())
+    v[:, ::7], k[:, ::11] = 0, 0
+    k, v = cache.fill(k.double(), v.double(), lens)
+    o, lse = run_attention(P, c, cache, q, lens, rows, "f16")
+    check(o, lse, reference(cache, c, q, k, v, total, rows), rows, 9.0)

@@ -434,3 +434,30 @@ def test_attention(P, case, dtype, f, wide):
     check(o, lse, ref, rows, 9.0)
     o2, lse2 = run_attention(P, case, cache, q, lens, rows, dtype)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)  # repeats bit for bit
+
+
+# Over 16 rows a kv head: four tiles of eight at a time, some of them without rows.
+MANY_ROWS = [
+    dict(B=2, Lq=1, Lk=700, Hq=34, Hkv=2, dh=128, page=64, lens=[700, 90]),                       # 17 rows
+    dict(B=2, Lq=3, Lk=700, Hq=16, Hkv=2, dh=128, page=64, causal=True, lens=[700, 2], rows=[3, 1]),
+    dict(B=1, Lq=4, Lk=3000, Hq=64, Hkv=8, dh=128, page=24, causal=True),
+    dict(B=2, Lq=33, Lk=500, Hq=1, Hkv=1, dh=128, page=7, causal=True, window=60, sinks=3, rows=[33, 17], missing=[(0, 2), (1, 40)]),
+    dict(B=2, Lq=5, Lk=400, Hq=16, Hkv=2, dh=64, page=64, causal=True, cap=5.0),                  # 40 rows
+    dict(B=3, Lq=6, Lk=260, Hq=8, Hkv=1, dh=64, page=16, causal=True, lens=[260, 5, 100], rows=[6, 6, 0]),
+    dict(B=2, Lq=25, Lk=330, Hq=2, Hkv=1, dh=32, page=40, causal=True, window=300),
+    dict(B=2, Lq=2, Lk=640, Hq=20, Hkv=2, dh=72, page=64, missing=[(0, 0), (1, 9)]),
+    dict(B=2, Lq=1, Lk=90, Hq=31, Hkv=1, dh=104, page=9, scale=1.5),
+    dict(B=70, Lq=4, Lk=200, Hq=20, Hkv=4, dh=128, page=16, causal=True, lens=[(b * 37) % 201 for b in range(70)], rows=[b % 5 for b in range(70)]),
+    dict(B=310, Lq=3, Lk=50, Hq=14, Hkv=2, dh=128, page=8, causal=True, append=True, lens=[b % 48 for b in range(310)]),
+    dict(B=1, Lq=3, Lk=20000, Hq=6, Hkv=1, dh=128, page=64, causal=True),
+    dict(B=2, Lq=4, Lk=16000, Hq=64, Hkv=8, dh=128, page=64, causal=True, lens=[15000, 70], cap=20.0),
+    dict(B=2, Lq=9, Lk=4100, Hq=64, Hkv=8, dh=128, page=64, causal=True, lens=[4100, 9], rows=[9, 5], window=4000, sinks=30),  # 72 rows
+]
+
+
+@pytest.mark.parametrize("dtype,f", [("bf16", "e4m3"), ("f16", "e4m3"), ("bf16", "i8"), ("f16", "i8"), ("bf16", "bf16"),
+                                     ("f16", "f16")])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("case", MANY_ROWS, ids=lambda c: f"B{c['B']}q{c['Lq']}k{c['Lk']}H{c['Hq']}-{c['Hkv']}dh{c['dh']}p{c['page']}")
+def test_attention_of_many_rows(P, case, dtype, f, wide):
+    test_attention(P, case, dtype, f, wide)
