@@ -82,6 +82,15 @@ __device__ __forceinline__ float2 decode2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// The larger of two pairs' sizes (with some sign; NaN where either is one).
+template <int FMT>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if constexpr (FMT == PSV_PAGE_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
 // Eight values of a program's row, as they are in memory.
 template <class T>
 struct Eight {
@@ -121,8 +130,8 @@ struct Eight {
       for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffffffu, y[i] & 0x7fffffffu));
       return m;
     } else {
-      const uint32_t a = 0x7fff7fffu, m = __vmaxu2(__vmaxu2(w[0] & a, w[1] & a), __vmaxu2(w[2] & a, w[3] & a));
-      return max(m & 0xffffu, m >> 16);
+      const uint32_t m = larger2<kFmt>(larger2<kFmt>(w[0], w[1]), larger2<kFmt>(w[2], w[3]));
+      return max(m & 0x7fffu, m >> 16 & 0x7fffu);
     }
   }
   static __device__ __forceinline__ float size_value(uint32_t bits) {
@@ -257,8 +266,9 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
     in[k].get(f);
     if constexpr (F::kScaled) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = turn[k] > 0.0f ? f[j] * turn[k] : 0.0f;  // (not 0 * NaN)
-      const uint2 y = make_uint2(encode4<FMT>(f), encode4<FMT>(f + 4));
+      for (int j = 0; j < 8; ++j) f[j] *= turn[k];
+      uint2 y = make_uint2(encode4<FMT>(f), encode4<FMT>(f + 4));
+      if (!(turn[k] > 0.0f)) y = make_uint2(0, 0);  // (not the code of 0 * NaN)
       if (VEC) *reinterpret_cast<uint2*>(out) = y;
       else
 #pragma unroll
