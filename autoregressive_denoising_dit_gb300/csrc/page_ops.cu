@@ -23,6 +23,8 @@ int page_esize(int format) { return scaled(format) ? 1 : 2; }
 struct PageRowsParams {
   PageCacheDev c;
   int L, H, dh, lanes;  // lanes of a head's row (log2, at least 2): 8 values each
+  int narrow;           // lanes of a row, not a power of two, where rows lie closer in a warp so; or 0
+  FastDiv by_narrow;
   int heads, tokens;    // of a thread, at most kRows rows in all
   FastDiv by_groups;    // groups of heads a token (one where there are several tokens)
   Strides3 xs[2];
@@ -163,41 +165,56 @@ struct Eight {
 constexpr int kRowThreads = 256;
 constexpr int kRows = 4;
 
-// A row (a head of a token) belongs to 2^lanes threads of a warp, eight values each; a
-// thread has up to four heads of a token, or (MANY) where there are one or two heads of
-// four or two tokens `step` apart.
-template <bool MANY>
+// Whose rows a thread has: up to four heads of a token (kHeads), or where there are one or two
+// heads of four or two tokens `step` apart (kTokens).  A row (a head of a token) belongs to
+// 2^lanes threads of a warp, eight values each, or (kNarrow) four heads of a token to
+// `narrow` threads: three heads of 80 lie side by side in a warp then, not two (8 x 1560
+// rows of 40 heads in bf16 to 8 bits 59 us and 47; heads of 128 so 72, and 63 by 2^n lanes).
+enum Map { kHeads, kTokens, kNarrow };
+
+template <int MAP>
 struct RowMap {
   uint32_t i, step;  // first token
-  int h0, heads, lane;
+  int h0, heads, lane, first;  // (lane of the row, the row's first one)
   __device__ __forceinline__ explicit RowMap(const PageRowsParams& p) {
-    const uint32_t each = kRowThreads >> p.lanes;
-    lane = threadIdx.x & ((1 << p.lanes) - 1);
-    if constexpr (MANY) {
+    if constexpr (MAP == kTokens) {
+      const uint32_t each = kRowThreads >> p.lanes;
+      lane = threadIdx.x & ((1 << p.lanes) - 1);
       i = blockIdx.x * each * p.tokens + (threadIdx.x >> p.lanes), step = each;
       h0 = 0, heads = p.H;
     } else {
-      const uint32_t r = blockIdx.x * each + (threadIdx.x >> p.lanes);
+      uint32_t r, in_warp = 0, row = 0;
+      if constexpr (MAP == kNarrow) {
+        in_warp = 32 / p.narrow, row = p.by_narrow.div(threadIdx.x % 32);
+        first = static_cast<int>(row) * p.narrow;
+        lane = static_cast<int>(threadIdx.x % 32) - first;
+        r = (blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32) * in_warp + row;
+      } else {
+        lane = threadIdx.x & ((1 << p.lanes) - 1);
+        r = blockIdx.x * (kRowThreads >> p.lanes) + (threadIdx.x >> p.lanes);
+      }
       i = p.by_groups.div(r), step = 0;
       h0 = static_cast<int>(r - i * p.by_groups.d) * p.heads;
       heads = min(p.heads, p.H - h0);
+      if (MAP == kNarrow && row >= in_warp) i = p.L;  // (lanes that are left over)
     }
   }
   // Token and head of the thread's row k (k < heads x tokens).
-  __device__ __forceinline__ uint32_t token(int k) const { return MANY ? i + (heads == 1 ? k : k / 2) * step : i; }
-  __device__ __forceinline__ int head(int k) const { return !MANY ? k : heads == 1 ? 0 : k % 2; }
+  __device__ __forceinline__ uint32_t token(int k) const { return MAP == kTokens ? i + (heads == 1 ? k : k / 2) * step : i; }
+  __device__ __forceinline__ int head(int k) const { return MAP != kTokens ? k : heads == 1 ? 0 : k % 2; }
 };
 
 // Rows find their largest size by shuffles, and their divisions are made by a lane each.
 // grid (tokens x groups of heads, sequence, key or value).  The first reads do not wait
 // for the lengths: rows not in use are read too.
 // Memory-bound where large: 12480 rows x 40 heads of 128 in f32 to 8 bits 91 us (7.1 TB/s),
-// in bf16 67 us (5.8); four sequences of 1560 rows x 12 heads in bf16 13 us.
-template <class T, int FMT, bool VEC, bool MANY>
+// in bf16 63 us (6.2); four sequences of 1560 rows x 12 heads in bf16 13 us.
+template <class T, int FMT, bool VEC, int MAP>
 __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
   const int b = blockIdx.y, kv = blockIdx.z;
-  const RowMap<MANY> m(p);
+  constexpr bool MANY = MAP == kTokens;
+  const RowMap<MAP> m(p);
   const int lane = m.lane, d = lane * 8, rows = MANY ? m.heads * p.tokens : m.heads;
   pdl_trigger();
   pdl_wait();
@@ -229,17 +246,26 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
     uint32_t size[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) size[k] = k < rows && m.token(k) < static_cast<uint32_t>(p.L) && d < p.dh ? in[k].size() : 0;
+    // (after o = 1, 2, 4, .. a lane has the largest of the 2 o of its row from it on, around)
+    auto around = [&](uint32_t x, int o) {
+      return __shfl_sync(0xffffffffu, x, m.first + (lane + o < p.narrow ? lane + o : lane + o - p.narrow));
+    };
     if constexpr (sizeof(T) == 2) {  // two rows a shuffle
 #pragma unroll
       for (int k = 0; k < kRows; k += 2) {
         uint32_t two = size[k] | size[k + 1] << 16;
-        for (int o = 1 << p.lanes >> 1; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+        if constexpr (MAP == kNarrow) {
+          for (int o = 1; o < p.narrow; o *= 2) two = __vmaxu2(two, around(two, o));
+        } else {
+          for (int o = 1 << p.lanes >> 1; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+        }
         size[k] = two & 0xffffu, size[k + 1] = two >> 16;
       }
     } else {
-      for (int o = 1 << p.lanes >> 1; o; o >>= 1)
+      for (int o = MAP == kNarrow ? 1 : 1 << p.lanes >> 1; MAP == kNarrow ? o < p.narrow : o != 0; o = MAP == kNarrow ? o * 2 : o >> 1)
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) size[k] = max(size[k], __shfl_xor_sync(0xffffffffu, size[k], o));
+        for (int k = 0; k < kRows; ++k)
+          size[k] = max(size[k], MAP == kNarrow ? around(size[k], o) : __shfl_xor_sync(0xffffffffu, size[k], o));
     }
     // Row lane % 4 is this lane's to divide for.
     const int mine = lane % 4;
@@ -248,7 +274,7 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
     const bool finite = __float_as_uint(most) < 0x7f800000u, kept = finite && most >= kTiny;
     const float my_turn = kept ? __fdiv_rn(F::kMost, most) : 0.0f;
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) turn[k] = __shfl_sync(0xffffffffu, my_turn, k, 1 << p.lanes);
+    for (int k = 0; k < kRows; ++k) turn[k] = MAP == kNarrow ? __shfl_sync(0xffffffffu, my_turn, m.first + k) : __shfl_sync(0xffffffffu, my_turn, k, 1 << p.lanes);
     if (lane < rows && lane < kRows && to.page >= 0)
       (kv ? p.c.v_scale : p.c.k_scale)[to.page * p.c.ss.b + to.row * p.c.ss.l + (m.h0 + m.head(mine)) * p.c.ss.h] =
           kept ? __fdiv_rn(most, F::kMost) : finite ? 0.0f : __int_as_float(0x7fc00000);
@@ -289,11 +315,12 @@ __global__ void __launch_bounds__(kRowThreads) page_write_kernel(const __grid_co
 
 // The same threads read rows back; positions without a page read as zeros.  Memory-bound:
 // eight sequences of 4836 rows x 40 heads of 128 from 8 bits 177 us (6.8 TB/s).
-template <class T, int FMT, bool VEC, bool MANY>
+template <class T, int FMT, bool VEC, int MAP>
 __global__ void __launch_bounds__(kRowThreads) page_read_kernel(const __grid_constant__ PageRowsParams p) {
   using F = PageFormat<FMT>;
   const int b = blockIdx.y, kv = blockIdx.z;
-  const RowMap<MANY> m(p);
+  constexpr bool MANY = MAP == kTokens;
+  const RowMap<MAP> m(p);
   const int d = m.lane * 8, rows = MANY ? m.heads * p.tokens : m.heads;
   pdl_trigger();
   pdl_wait();
@@ -375,18 +402,20 @@ __global__ void __launch_bounds__(kRowThreads) page_read_kernel(const __grid_con
 
 template <class T, int FMT>
 cudaError_t launch_page_rows(const PageRowsParams& p, int B, bool vec, bool write, cudaStream_t st) {
-  const uint32_t groups = static_cast<uint32_t>(p.L) * p.by_groups.d, each = (kRowThreads >> p.lanes) * p.tokens;
+  const uint32_t groups = static_cast<uint32_t>(p.L) * p.by_groups.d;
+  const uint32_t each = p.narrow ? kRowThreads / 32 * (32 / p.narrow) : (kRowThreads >> p.lanes) * p.tokens;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = pdl_config(dim3((groups + each - 1) / each, B, 2), kRowThreads, 0, st, attr);
-  const bool many = p.tokens > 1;
   if (write) {
-    if (!vec) return cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, false, false>, p);
-    return many ? cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true, true>, p)
-                : cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true, false>, p);
+    if (!vec) return cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, false, kHeads>, p);
+    return p.narrow       ? cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true, kNarrow>, p)
+           : p.tokens > 1 ? cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true, kTokens>, p)
+                          : cudaLaunchKernelEx(&cfg, page_write_kernel<T, FMT, true, kHeads>, p);
   }
-  if (!vec) return cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, false, false>, p);
-  return many ? cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true, true>, p)
-              : cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true, false>, p);
+  if (!vec) return cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, false, kHeads>, p);
+  return p.narrow       ? cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true, kNarrow>, p)
+         : p.tokens > 1 ? cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true, kTokens>, p)
+                        : cudaLaunchKernelEx(&cfg, page_read_kernel<T, FMT, true, kHeads>, p);
 }
 
 template <class T>
@@ -525,6 +554,11 @@ int page_rows_call(const psv_page_cache* c, const psv_page_rows* r, const void* 
                    multiple16(v, r->v_stride, c->B, r->L, c->Hkv, size) && eights(c->k_pages, c->k_stride) &&
                    eights(c->v_pages, c->v_stride);
   p.tokens = !vec ? 1 : c->Hkv == 1 ? 4 : c->Hkv == 2 ? 2 : 1;
+  const int lanes = c->dh / 8;
+  if (vec && p.tokens == 1 && lanes >= 4 && 32 / lanes > 32 >> p.lanes) {
+    p.narrow = lanes;
+    p.by_narrow = FastDiv::of(static_cast<uint32_t>(lanes));
+  }
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = r->dtype == PSV_DTYPE_F32    ? launch_page_rows_any<float>(p, c->B, vec, write, st)
                         : r->dtype == PSV_DTYPE_BF16 ? launch_page_rows_any<__nv_bfloat16>(p, c->B, vec, write, st)

@@ -461,3 +461,19 @@ MANY_ROWS = [
 @pytest.mark.parametrize("case", MANY_ROWS, ids=lambda c: f"B{c['B']}q{c['Lq']}k{c['Lk']}H{c['Hq']}-{c['Hkv']}dh{c['dh']}p{c['page']}")
 def test_attention_of_many_rows(P, case, dtype, f, wide):
     test_attention(P, case, dtype, f, wide)
+
+
+NARROW = [  # rows of 5, 6, 9 and 10 pieces
+    dict(B=2, L=23, Hkv=5, dh=40, page=16, starts=[3, 0], lens=[23, 9]),
+    dict(B=3, L=1, Hkv=12, dh=48, page=64, starts=[0, 63, 64]),
+    dict(B=2, L=61, Hkv=3, dh=72, page=7, starts=[-2, 11], missing=[(0, 1)]),
+    dict(B=1, L=333, Hkv=9, dh=80, page=64, starts=[40], layout="prhd"),
+]
+
+
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("dtype,f", [("bf16", "e4m3"), ("f16", "i8"), ("f32", "e4m3"), ("f32", "i8"), ("bf16", "bf16"),
+                                     ("f32", "f16")])
+@pytest.mark.parametrize("case", NARROW, ids=lambda c: f"B{c['B']}L{c['L']}H{c['Hkv']}dh{c['dh']}p{c['page']}")
+def test_write_and_read_of_narrow_rows(P, case, dtype, f, strided):
+    test_write_and_read(P, case, dtype, f, strided)
