@@ -27,9 +27,9 @@
 // cover little, groups are not cut: a cluster of CTAs takes whole groups, and its CTAs
 // read one another's sums; or, where there are many groups, a warp does by itself.
 //
-// Measured, heads of 128, 8 bits: eight tokens over 5203 to 7800 keys of 12 heads 33.9 us
+// Measured, heads of 128, 8 bits: eight tokens over 5203 to 7800 keys of 12 heads 33.4 us
 // (165 MB; without any products 32), one over 131072 keys of 8 heads, five query heads
-// each, 50 us (277 MB, 5.5 TB/s); 16-bit pages of the former 55 us (320 MB, 5.8 TB/s).
+// each, 49 us (277 MB, 5.6 TB/s); 16-bit pages of the former 55 us (320 MB, 5.8 TB/s).
 // Of a call about 8 us are its start (lengths, tables, first keys: three round trips
 // after the kernel before), the join and the ends of SMs that get less of the memory.
 // Two tiles of rows (9 to 16 a kv head) are bound by the issue of their conversions,
