@@ -619,7 +619,9 @@ int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void
  * codes are exact in f16, queries get a power of two for each row first, a key's
  * scale is applied to its score and a value's to its weight, in f32.  Scores,
  * maxima, sums and lse are f32; the weights are rounded to the operand type for
- * their product with v, the output once.  Results repeat bit for bit for the same
+ * their product with v, the output once.  f16 weights have fixed steps below 2^-21 of a
+ * row's largest (weight times value's scale for 8-bit pages): each is off by at most
+ * 2^-32 of that, n keys together by n 2^-32.  Results repeat bit for bit for the same
  * lengths; those of a sequence may differ in their roundings where the lengths
  * of others change, as the work is shared out among the SMs by all of them.
  * Requirements: dtype BF16 or F16 (16-bit pages: their own); Hq a multiple of Hkv;
