@@ -552,7 +552,8 @@ int psv_cache_evict(const psv_evict_problem* p, const void* k, const void* v, co
  *
  * The conventions of the rolling cache's calls hold, psv_cache_last_error()
  * among them.  Tables, starts and lengths are read on the device when the kernels
- * run.  The pages' content is psv_page_write's, or equal to what it would write. */
+ * run.  What rows of a call read or see of the pages is psv_page_write's, or equal to
+ * what it would write. */
 
 #define PSV_PAGE_BF16 1 /* values as they are (rounded, from F32 rows)                */
 #define PSV_PAGE_F16  2
@@ -614,7 +615,8 @@ int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void
  * A row that sees nothing gets o = 0 and lse = -infinity; one that sees a NaN score
  * gets NaN in both.  Rows i >= q_lens[b] of o and lse are left as they were.  o may
  * be q itself (equal strides).  Keys that no row sees may hold anything, and so may
- * keys and values that are masked for some rows.
+ * keys and values that are masked for some rows, as far as those rows go: codes that are
+ * NaN, scales and values that are not finite reach the rows that see them only.
  * Products take f16 operands (bf16 ones for BF16 pages) and accumulate in f32: 8-bit
  * codes are exact in f16, queries get a power of two for each row first, a key's
  * scale is applied to its score and a value's to its weight, in f32.  Scores,
