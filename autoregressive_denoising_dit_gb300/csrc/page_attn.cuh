@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
           }
         }
       }
+      __syncwarp();  // (all lanes have read the slots that are filled again)
 #pragma unroll 1
       for (int i = 0; i < kStages - 1; ++i) {
         issue(i);
@@ -768,6 +769,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
     [[maybe_unused]] const bool mixed = all_end < any_end || any_first < all_first;  // keys that some rows see and others do not
 #pragma unroll 1
     for (int step = step0 + worker; step < step1; step += workers) {
+      __syncwarp();  // (all lanes have read the step before, whose slot is filled again)
       issue(slot == 0 ? kStages - 1 : slot - 1);
       copies_commit();
       copies_wait<kStages - 1>();
