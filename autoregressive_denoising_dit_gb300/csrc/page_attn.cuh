@@ -14,8 +14,9 @@
 // products.  (A copy of a thread's own 16 bytes, half a row of 128 a copy, takes a
 // quarter longer: 64-byte requests to L2.)
 //
-// Codes become f16 (exactly); queries become f16 with a power of two for each row;
-// a key's scale multiplies its scores.  A value's scale enters its weight as an
+// Codes become f16 (exactly); bf16 queries become f16 with a power of two for each row
+// that brings its largest to [2^14, 2^15), so that values down to 2^-31 of it keep their
+// eight bits; a key's scale (by 2^-14 then) multiplies its scores.  A value's scale enters its weight as an
 // exponent, exp2(s + log2 scale - m'), with a maximum m' of its own, so that
 // weights fit f16 whatever the scales are.
 //
@@ -56,6 +57,7 @@ namespace {
 enum Mode { kCut, kClusters, kAlone };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kUp = 16384.0f;       // what bf16 queries' largest value is brought to, 8-bit pages
 constexpr float kLift = 7.0f;         // a maximum's weight is 2^7 when it is taken up
 constexpr float kRescale = 32768.0f;  // weights above it take up a new maximum
 constexpr float kNone = -FLT_MAX;   // a maximum of nothing: exp2(-inf - kNone) = 0, exp2(kNone - kNone) = 1
@@ -709,14 +711,14 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
     }
     if (!more) break;
 
-    // ---- queries as operands: f16 with the row's largest value in [1, 2) where they are bf16 and codes f16
+    // ---- queries as operands: f16 with the row's largest value in [2^14, 2^15) where they are bf16 and codes f16
     uint32_t qf[C::QS ? 1 : NT][C::KP * C::KS][2];
     float up[NT][2];  // by row of the scores: what its power of two took
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
       if (kOneTile && warp >= NT) continue;
       const int tile = kOneTile ? warp : t;
-      float e = 1.0f;
+      float e = C::kScaled ? kUp : 1.0f;
       if (C::kScaled && p.bf16) {
         uint32_t big = 0;
 #pragma unroll
@@ -726,8 +728,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
             big = max(big, max(raw[t][i][x] << 16 & 0x7fff0000u, raw[t][i][x] & 0x7fff0000u));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const int ex = big >= 0x7f800000u ? 0 : min(max(static_cast<int>(big >> 23) - 127, -120), 120);
-        const float down = __int_as_float((127 - ex) << 23);
+        const int ex = big >= 0x7f800000u ? 0 : min(max(static_cast<int>(big >> 23) - 127, -112), 127);
+        const float down = __int_as_float((127 + 14 - ex) << 23);  // (2^-ex kUp)
         e = __int_as_float((127 + ex) << 23);
 #pragma unroll
         for (int i = 0; i < C::KP; ++i)
@@ -847,7 +849,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
         float ks[2] = {1.0f, 1.0f};
         if constexpr (C::kScaled) {
           const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV) + 16 * h;
-          ks[0] = scales[quad], ks[1] = scales[quad + 8];
+          ks[0] = scales[quad] * (1.0f / kUp), ks[1] = scales[quad + 8] * (1.0f / kUp);  // (f32 holds the same scores as with queries of [1, 2))
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {

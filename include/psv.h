@@ -618,8 +618,9 @@ int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void
  * keys and values that are masked for some rows, as far as those rows go: codes that are
  * NaN, scales and values that are not finite reach the rows that see them only.
  * Products take f16 operands (bf16 ones for BF16 pages) and accumulate in f32: 8-bit
- * codes are exact in f16, queries get a power of two for each row first, a key's
- * scale is applied to its score and a value's to its weight, in f32.  Scores,
+ * codes are exact in f16, bf16 queries get a power of two for each row first (and are
+ * exact down to 2^-31 of the row's largest), a key's scale is applied to its score
+ * and a value's to its weight, in f32.  Scores,
  * maxima, sums and lse are f32; the weights are rounded to the operand type for
  * their product with v, the output once.  f16 weights have fixed steps below 2^-21 of a
  * row's largest (weight times value's scale for 8-bit pages): each is off by at most

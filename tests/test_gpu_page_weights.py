@@ -1,4 +1,5 @@
-"""Weights far below the largest one in the attention over pages, against 64 bits.
+"""Weights and query values far below the largest one in the attention over pages, against
+64 bits.
 
 A few keys have nearly all the weight and nothing in the columns that count, so that the output
 is made of many small weights.  Tolerances, with the largest weight's reference at least 2^7
@@ -89,3 +90,34 @@ def test_small_weights_beside_large_ones(P, case, dtype, f, gap, width):
     err = (got.double() - o[:, None]).abs() / tol[:, None]
     assert (err <= 1).all(), float(err.max())
     assert ((got_lse.double() - lse[..., None]).abs() <= ltol[..., None]).all()
+
+
+@pytest.mark.parametrize("below", [20, 24, 30])
+@pytest.mark.parametrize("f", ["e4m3", "i8", "bf16"])
+@pytest.mark.parametrize("Lq,dh", [(1, 128), (5, 128), (12, 64), (2, 256)])
+def test_small_values_of_a_query_row(P, f, Lq, dh, below):
+    """A query's largest value meets zeros; one 2^-20 to 2^-30 of it makes the score, and keeps
+    its eight bits (1 + 2^-7)."""
+    n = 70
+    cache = Cache(P, f, 1, 1, dh, 16, 5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k = torch.zeros(1, n, 1, dh, device="cuda", dtype=torch.float64)
+    k[0, :, 0, 1] = torch.randint(-8, 9, (n,), device="cuda", generator=g).double()
+    k[0, :, 0, 9] = 16.0  # (met by zeros)
+    v = torch.randn(1, n, 1, dh, device="cuda", generator=g).bfloat16().double()
+    kk, vv = cache.fill(k, v, [n])
+    q = torch.zeros(1, Lq, 1, dh, device="cuda", dtype=torch.bfloat16)
+    q[..., 0], q[..., 1] = 2.0**below, 1.0 + 2.0**-7
+    c = dict(scale=1.0)
+    got, got_lse = run_attention(P, c, cache, q, [n], [Lq], "bf16")
+    s = (1.0 + 2.0**-7) * kk[0, :, 0, 1]
+    es = (dh * 2.0**-23 + 2.0**-21) * s.abs().max()
+    lse = torch.logsumexp(s, 0)
+    assert ((got_lse[0, 0].double() - lse).abs() <= es + 2.0**-20 + 2.0**-22 * lse.abs()).all()
+    p = torch.softmax(s, 0)
+    o, A = p @ vv[0, :, 0], p @ vv[0, :, 0].abs()
+    # (f16 weights: 2^-32 of the largest for each code, at most 448 scales)
+    _, vs = quantised(v, f)
+    tol = ((U["bf16"] if f == "bf16" else U["f16"]) + 2 * es + 2.0**-19) * A + U["bf16"] * o.abs()
+    tol = tol + (0.0 if f == "bf16" else n * 448 * 2.0**-32 * (p * vs[0, :, 0]).max())
+    assert ((got[0, :, 0].double() - o).abs() <= tol).all()
