@@ -649,7 +649,7 @@ typedef struct psv_page_query {
 
 /* Workspace of psv_page_attention: 256-byte aligned device memory of any content.  It
  * may serve any number of calls (captured ones too, of any problem that it is large
- * enough for) that do not overlap on the GPU.  5 MB at most. */
+ * enough for) that do not overlap on the GPU.  5.2 MB (10^6 bytes) at most. */
 int psv_page_scratch_bytes(const psv_page_cache* c, const psv_page_query* q, size_t* bytes);
 
 int psv_page_attention(const psv_page_cache* c, const psv_page_query* q, const void* x /* q */, void* o,
