@@ -20,10 +20,11 @@
 // exponent, exp2(s + log2 scale - m'), with a maximum m' of its own, so that
 // weights fit f16 whatever the scales are.
 //
-// The m and m' that weights are taken relative to are maxima less 7, and a new maximum is
-// taken up where a weight passes 2^15: f16 ends at 2^16, and its fixed half step of 2^-25
-// below 2^-14 is 2^-32 of the largest weight then.  (Many small weights may be all that
+// The m and m' that f16 weights are taken relative to are maxima less 7, and a new maximum
+// is taken up where a weight passes 2^15: f16 ends at 2^16, and its fixed half step of
+// 2^-25 below 2^-14 is 2^-32 of the largest weight then.  (Many small weights may be all that
 // an output is made of: with m the maximum, a key 17.4 below it had no weight but counted in l.)
+// bf16 weights, whose values may be as large as f32's, stay at 2^8 and below.
 //
 // The work (16-key steps of every sequence, kv head and tile of query rows) is
 // one line that is cut into equal stretches, one a CTA, whatever the lengths.
@@ -58,8 +59,10 @@ enum Mode { kCut, kClusters, kAlone };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kUp = 16384.0f;       // what bf16 queries' largest value is brought to, 8-bit pages
-constexpr float kLift = 7.0f;         // a maximum's weight is 2^7 when it is taken up
-constexpr float kRescale = 32768.0f;  // weights above it take up a new maximum
+// What a maximum's weight is when it is taken up (as an exponent), and beyond what weight
+// a new one is.
+__host__ __device__ constexpr float lift(int format) { return format == PSV_PAGE_BF16 ? 0.0f : 7.0f; }
+__host__ __device__ constexpr float rescale(int format) { return format == PSV_PAGE_BF16 ? 256.0f : 32768.0f; }
 constexpr float kNone = -FLT_MAX;   // a maximum of nothing: exp2(-inf - kNone) = 0, exp2(kNone - kNone) = 1
 
 constexpr bool two_products(int dh, bool scaled, int nt) { return scaled && (dh == 64 || (dh == 128 && nt == 2)); }
@@ -260,9 +263,9 @@ struct Cut {
   __device__ __forceinline__ int of(int64_t x) const { return static_cast<int>(divide((x + 1) * ctas - 1, all)); }
 };
 
-// The lse of a row with statistics m, l (l's logarithm is near 0 where few keys count).
-__device__ __forceinline__ float row_lse(float mm_l, float ll) {
-  return ll == 0.0f ? -INFINITY : (mm_l + kLift + fast_log2(ll * 0x1p-7f)) * kLn2;
+// The lse of a row with statistics m, l (without the lift l's logarithm is near 0 where few keys count).
+__device__ __forceinline__ float row_lse(int format, float mm_l, float ll) {
+  return ll == 0.0f ? -INFINITY : (mm_l + lift(format) + fast_log2(ll * (format == PSV_PAGE_BF16 ? 1.0f : 0x1p-7f))) * kLn2;
 }
 
 // What a row's sum of values times weights is multiplied by: it has statistics m', m, l.
@@ -281,7 +284,7 @@ __device__ __forceinline__ void write_out(const PageAttnParams& p, int b, int kv
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + b * p.os.b + tok * p.os.l + head * p.os.h + d) = y;
   }
   if (d == 0 && p.lse)
-    p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Lq + tok] = row_lse(mm_l, ll);
+    p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Lq + tok] = row_lse(p.c.format, mm_l, ll);
 }
 
 // Takes a share with statistics m', m, l into a sum.
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
                                                              : pack2<false>(o[t][i][x] * f, o[t][i][2 + x] * f);
           }
           if (quad == 0 && p.lse)
-            p.lse[(static_cast<int64_t>(was_b) * p.Hq + head) * p.Lq + tok] = row_lse(ml[t][x], ll);
+            p.lse[(static_cast<int64_t>(was_b) * p.Hq + head) * p.Lq + tok] = row_lse(FMT, ml[t][x], ll);
         }
       __syncwarp();
     } else if (joining) {
@@ -927,7 +930,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
               }
           return big;
         };
-        if (__any_sync(0xffffffffu, weigh() > kRescale)) {
+        if (__any_sync(0xffffffffu, weigh() > rescale(FMT))) {
 #pragma unroll
           for (int t = 0; t < kPair; ++t)
 #pragma unroll
@@ -942,8 +945,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, i));
                 if (C::kScaled) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, i));
               }
-              a = fmaxf(a - kLift, ml[t0 + t][x]);
-              if (C::kScaled) d = fmaxf(d - kLift, mo[t0 + t][x]);
+              a = fmaxf(a - lift(FMT), ml[t0 + t][x]);
+              if (C::kScaled) d = fmaxf(d - lift(FMT), mo[t0 + t][x]);
               const float g = fast_exp2(ml[t0 + t][x] - a), f = C::kScaled ? fast_exp2(mo[t0 + t][x] - d) : g;
               l[t0 + t][x] *= g;
               ml[t0 + t][x] = a;

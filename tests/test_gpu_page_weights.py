@@ -121,3 +121,26 @@ def test_small_values_of_a_query_row(P, f, Lq, dh, below):
     tol = ((U["bf16"] if f == "bf16" else U["f16"]) + 2 * es + 2.0**-19) * A + U["bf16"] * o.abs()
     tol = tol + (0.0 if f == "bf16" else n * 448 * 2.0**-32 * (p * vs[0, :, 0]).max())
     assert ((got[0, :, 0].double() - o).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("width", [False, True])
+@pytest.mark.parametrize("Lq,dh", [(1, 128), (6, 64), (2, 256)])
+def test_large_values_in_bf16_pages(P, Lq, dh, width):
+    """Values of 2^118 to 2^119: their sums with weights of at most 2^2 of the first ones stay
+    within f32 (70 x 2^119 x 2^2)."""
+    n = 70
+    cache = Cache(P, "bf16", 1, 2, dh, 16, 5, width=WIDE // 16 if width else 0)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    k = torch.randn(1, n, 2, dh, device="cuda", generator=g).bfloat16().double() * 0.1
+    v = ((1.0 + torch.rand(1, n, 2, dh, device="cuda", generator=g)) * 2.0**118).bfloat16().double()
+    kk, vv = cache.fill(k, v, [n])
+    q = torch.randn(1, Lq, 2, dh, device="cuda", generator=g).bfloat16()
+    got, got_lse = run_attention(P, {}, cache, q, [n], [Lq], "bf16")
+    s = torch.einsum("qhd,jhd->qhj", q[0].double(), kk[0]) * dh**-0.5
+    assert (s.amax(-1) - s.amin(-1)).max() < 2.0 * 0.69  # weights within 2^2 of one another
+    es = (dh * 2.0**-23 * torch.einsum("qhd,jhd->qhj", q[0].double().abs(), kk[0].abs()) * dh**-0.5).amax(-1) + 2.0**-20
+    p = torch.softmax(s, -1)
+    o = torch.einsum("qhj,jhd->qhd", p, vv[0])
+    tol = (2 * U["bf16"] + 2 * es[..., None] + 2.0**-19) * o
+    assert ((got[0].double() - o).abs() <= tol).all()
+    assert ((got_lse[0].T.double() - torch.logsumexp(s, -1)).abs() <= es + 2.0**-20 + 2.0**-20).all()
