@@ -16,7 +16,7 @@
 //
 // Codes become f16 (exactly); bf16 queries become f16 with a power of two for each row
 // that brings its largest to [2^14, 2^15), so that values down to 2^-31 of it keep their
-// eight bits; a key's scale (by 2^-14 then) multiplies its scores.  A value's scale enters its weight as an
+// eight bits; a key's scale multiplies its scores.  A value's scale enters its weight as an
 // exponent, exp2(s + log2 scale - m'), with a maximum m' of its own, so that
 // weights fit f16 whatever the scales are.
 //
@@ -58,7 +58,6 @@ namespace {
 enum Mode { kCut, kClusters, kAlone };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kUp = 16384.0f;       // what bf16 queries' largest value is brought to, 8-bit pages
 // What a maximum's weight is when it is taken up (as an exponent), and beyond what weight
 // a new one is.
 __host__ __device__ constexpr float lift(int format) { return format == PSV_PAGE_BF16 ? 0.0f : 7.0f; }
@@ -721,7 +720,7 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
     for (int t = 0; t < NQ; ++t) {
       if (kOneTile && warp >= NT) continue;
       const int tile = kOneTile ? warp : t;
-      float e = C::kScaled ? kUp : 1.0f;
+      float e = 1.0f;
       if (C::kScaled && p.bf16) {
         uint32_t big = 0;
 #pragma unroll
@@ -732,8 +731,8 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
         const int ex = big >= 0x7f800000u ? 0 : min(max(static_cast<int>(big >> 23) - 127, -112), 127);
-        const float down = __int_as_float((127 + 14 - ex) << 23);  // (2^-ex kUp)
-        e = __int_as_float((127 + ex) << 23);
+        const float down = __int_as_float((127 + 14 - ex) << 23);
+        e = __int_as_float((127 - 14 + ex) << 23);
 #pragma unroll
         for (int i = 0; i < C::KP; ++i)
 #pragma unroll
@@ -783,26 +782,6 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
       slot = slot == kStages - 1 ? 0 : slot + 1;
       const unsigned there = __ballot_sync(0xffffffffu, found >> (kStages - 1) & 1);
       if (!there) continue;
-      if constexpr (FMT == PSV_PAGE_E4M3) {
-        // A value's code that is NaN, where some rows see its key and others do not: its weight
-        // there will be 0, but 0 * NaN is not.  The code becomes a zero and the value's scale
-        // NaN, which reaches the rows that see the key only.  (12 causal rows over 17600 keys
-        // 38.5 us without this and 39.6, single tokens 37.9 and 38.1.)
-        if (__builtin_expect(mixed && (key_of(step) + kStep > all_end || key_of(step) < all_first), 0)) {
-          auto nans = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u) >> 7; };  // 1 a byte
-#pragma unroll 1
-          for (int i = lane; i < C::KV / 16; i += 32) {
-            uint4* code = reinterpret_cast<uint4*>(smem + mine + C::KV) + i;
-            const uint4 z = *code;
-            if (nans(z.x) | nans(z.y) | nans(z.z) | nans(z.w)) {
-              *code = make_uint4(z.x & ~(nans(z.x) * 0xff), z.y & ~(nans(z.y) * 0xff), z.z & ~(nans(z.z) * 0xff),
-                                 z.w & ~(nans(z.w) * 0xff));
-              reinterpret_cast<float*>(smem + mine + 2 * C::KV)[kStep + row_at<C::RB>(i)] = __int_as_float(0x7fc00000);
-            }
-          }
-          __syncwarp();
-        }
-      }
       // ---- scores
       float sc[SUBS][NT][4];
 #pragma unroll
@@ -852,13 +831,13 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
         float ks[2] = {1.0f, 1.0f};
         if constexpr (C::kScaled) {
           const float* scales = reinterpret_cast<const float*>(smem + mine + 2 * C::KV) + 16 * h;
-          ks[0] = scales[quad] * (1.0f / kUp), ks[1] = scales[quad + 8] * (1.0f / kUp);  // (f32 holds the same scores as with queries of [1, 2))
+          ks[0] = scales[quad], ks[1] = scales[quad + 8];
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           if (NT == 4) up[t][0] = sq_up[8 * t + 2 * four], up[t][1] = sq_up[8 * t + 2 * four + 1];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[h][t][e] = (C::kScaled ? sc[h][t][e] * ks[e >> 1] : sc[h][t][e]) * up[t][e & 1];
+          for (int e = 0; e < 4; ++e) sc[h][t][e] *= C::kScaled ? ks[e >> 1] * up[t][e & 1] : up[t][e & 1];
         }
       }
       if (p.softcap > 0) {
@@ -905,6 +884,36 @@ __global__ void __launch_bounds__(ACfg<DH, FMT, NT>::THREADS, ACfg<DH, FMT, NT>:
             for (int e = 0; e < 4; ++e) u[h][t][e] = C::kScaled ? sc[h][t0 + t][e] + lv[e >> 1] : sc[h][t0 + t][e];
         }
         if (!whole) {
+          if (FMT == PSV_PAGE_E4M3 && t0 == 0 && mixed) {
+            // A value's code that is NaN, where some rows see its key and others do not: its
+            // weight there will be 0, but 0 * NaN is not.  The code becomes a zero and the
+            // value's scale NaN, and with it its weight in the rows that see the key.
+            // (12 causal rows over 17600 keys 38.5 us without this and 38.8, single tokens
+            // 38.3 and 38.5; handled before the scores 39.6 and 38.4.)
+            __syncwarp();
+            auto nans = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u) >> 7; };  // 1 a byte
+            float* scales = reinterpret_cast<float*>(smem + mine + 2 * C::KV) + kStep;
+#pragma unroll 1
+            for (int i = lane; i < C::KV / 16; i += 32) {
+              uint4* code = reinterpret_cast<uint4*>(smem + mine + C::KV) + i;
+              const uint4 z = *code;
+              if (nans(z.x) | nans(z.y) | nans(z.z) | nans(z.w)) {
+                *code = make_uint4(z.x & ~(nans(z.x) * 0xff), z.y & ~(nans(z.y) * 0xff), z.z & ~(nans(z.z) * 0xff),
+                                   z.w & ~(nans(z.w) * 0xff));
+                scales[row_at<C::RB>(i)] = __int_as_float(0x7fc00000);
+              }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < SUBS; ++h)
+#pragma unroll
+              for (int t = 0; t < kPair; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float x = scales[16 * h + quad + 8 * (e >> 1)];
+                  if (x != x) u[h][t][e] = x;
+                }
+          }
 #pragma unroll
           for (int h = 0; h < SUBS; ++h)
 #pragma unroll
