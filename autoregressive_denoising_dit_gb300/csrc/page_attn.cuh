@@ -34,13 +34,15 @@
 // cover little, groups are not cut: a cluster of CTAs takes whole groups, and its CTAs
 // read one another's sums; or, where there are many groups, a warp does by itself.
 //
-// Measured, heads of 128, 8 bits: eight tokens over 5203 to 7800 keys of 12 heads 33.4 us
+// Measured, heads of 128, 8 bits: eight tokens over 5203 to 7800 keys of 12 heads 34 us
 // (165 MB; without any products 32), one over 131072 keys of 8 heads, five query heads
-// each, 49 us (277 MB, 5.6 TB/s); 16-bit pages of the former 55 us (320 MB, 5.8 TB/s).
+// each, 50 us (277 MB, 5.5 TB/s); 16-bit pages of the former 56 us (320 MB, 5.7 TB/s).
 // Of a call about 8 us are its start (lengths, tables, first keys: three round trips
 // after the kernel before), the join and the ends of SMs that get less of the memory.
 // Two tiles of rows (9 to 16 a kv head) are bound by the chains of conversions, products
-// and softmax of two warps a scheduler (1.9 instructions a cycle, no pipe over 35 %): 4 x 17600 keys of 8 heads, 12 rows, 42 us (149 MB).
+// and softmax of two warps a scheduler: 4 x 17600 keys of 8 heads, 12 rows, 42 us (149 MB).
+// No pipe is over 25 %, 1.4 instructions issue a cycle and SM; waits of fixed length are
+// the commonest stall, instructions that have to be fetched the next.
 #pragma once
 
 #include <algorithm>
@@ -1144,9 +1146,10 @@ cudaError_t launch(const PageAttnParams& p, int sms, cudaStream_t st) {
 // SM's warps, two products of 16 rows each) instead of for 16 (1.4 us, which is what L2
 // gives): where that is less in all, for groups of 4000 keys at least and 12 steps a warp,
 // as these CTAs are an SM's only ones and their warps take no groups alone.  Measured, 8 x
-// 7800 keys of 12 heads, 32 rows 92 and 128 us, 48 156 and 134, 64 164 and 237, 96 226 and
+// 7800 keys of 12 heads, 32 rows 94 and 128 us, 48 156 and 133, 64 166 and 237, 96 228 and
 // 254; 64 groups of 4000 37 and 49, 256 of 1000 59 and 56; 8 of 17600 30 and 28.  (In 8 bits
-// 32 rows take 93 us and 79: steps of 32 keys hide more of the conversions.)
+// 32 rows take 93 us and 81: steps of 32 keys hide more of the conversions.)  The compiler
+// spills 176 to 296 bytes a thread here, at 255 registers.
 inline bool four_tiles(const PageAttnParams& p) {
   const int64_t rows = static_cast<int64_t>(p.Lq) * p.G, two = (rows + 15) / 16, four = (rows + 31) / 32;
   const int64_t steps = (p.window ? std::min<int64_t>(p.c.positions, static_cast<int64_t>(p.window) + p.sinks) : p.c.positions) / 16;
@@ -1166,7 +1169,8 @@ cudaError_t launch_tile(PageAttnParams p, int sms, cudaStream_t st) {
   p.cluster = 1;
   while (p.cluster < 8 && p.groups * p.cluster * 2 <= C::MAX_CTAS && p.cluster * C::WARPS < steps) p.cluster *= 2;
   // What the modes would take, in us: rounds of groups, each with its steps (t: all warps'
-  // in turn at 44 kB an SM and us) and its start and end.  Measured, 8-bit heads of 128:
+  // in turn at 44 kB an SM and us) and its start and end.  Fitted on 8-bit heads of 128 and
+  // taken as it is for other widths, formats and tiles.  Measured there:
   //   clusters against cuts: 12 groups of 1000 keys 7.4 and 12.1 us, 4000 10.8 and 12.5, 8000
   //   14.6 and 14.3; 96 of 2000 16.7 and 20.3, 7800 44 and 36; 384 of 500 18.8 and 21.1
   //   warps alone against cuts: 2048 groups of 250 keys 39 and 46 us, 8000 of 300 119 and 177,

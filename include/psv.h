@@ -632,7 +632,8 @@ int psv_page_read(const psv_page_cache* c, const psv_page_rows* r, void* k, void
  * need a window; scale, softcap >= 0 finite; o's rows distinct.
  * The tensor-core kernel takes dh % 8 == 0, bases and strides of q and o in
  * multiples of 16 bytes, of pages in multiples of eight values, strides of pages, rows
- * and scales below 4 GB; every other problem runs on a slower general kernel.  It is
+ * and scales below 4 GB; every other problem runs on a general kernel, tens to
+ * thousands of times slower (pad the rows of other widths to a multiple of 8).  It is
  * made for few rows: it reads the pages once for every 16 rows a kv head, Lq x Hq / Hkv (8, where dh > 128;
  * 32 of long caches in 16 bits, heads of 72 to 128).
  * (A chunk's many rows: psv_page_read, then psv_cache_attention.)  Pages of a multiple
